@@ -109,6 +109,8 @@ def load_library() -> ctypes.CDLL:
     lib.prism_fwd_noalloc.restype = ctypes.c_int
     lib.prism_noalloc_scratch_bytes.argtypes = []
     lib.prism_noalloc_scratch_bytes.restype = sz
+    from .layer import declare
+    declare(lib)
     lib.prism_status_string.argtypes = [ctypes.c_int]
     lib.prism_status_string.restype = ctypes.c_char_p
     lib.prism_version.argtypes = []
@@ -646,3 +648,15 @@ def fwd_delta_pred(q, k, v, g, beta, W_p, W_k, W_b, conv_w, L: int, chunk: int =
     if st != 0:
         raise PrismError(f"prism_fwd_delta_pred failed: {status_string(st)}")
     return o, S
+
+
+# ---- the state space layer (layer.py needs torch, which the functions above import on first use) ----
+_LAYER = ("conv_fwd", "conv_bwd", "conv_step", "ssm_fwd", "ssm_bwd", "ssm_step", "norm_fwd", "norm_bwd")
+
+
+def __getattr__(name):
+    if name not in _LAYER:
+        raise AttributeError(f"module {__name__!r} has no attribute {name!r}")
+    from . import layer
+    globals().update({n: getattr(layer, n) for n in _LAYER})
+    return globals()[name]

@@ -1,0 +1,57 @@
+// conv.hip - launches of the causal convolution (prism_conv.h)
+#include "prism_conv.h"
+
+namespace prism {
+namespace host {
+namespace {
+
+prism_status launched() { return hipGetLastError() == hipSuccess ? PRISM_OK : PRISM_ERR_HIP; }
+
+template <class T, int V>
+dim3 strip_grid(const ConvArgs& a) {
+  const int cols = (a.D + V - 1) / V;
+  return dim3((cols + 63) / 64, (a.nstrip + 3) / 4, a.B * a.H);
+}
+
+template <class T, int K>
+prism_status fwd(bool wide, const ConvArgs& a, hipStream_t s) {
+  constexpr int V = 16 / sizeof(T);
+  if (wide) conv::fwd_kernel<T, K, V><<<strip_grid<T, V>(a), 256, 0, s>>>(a);
+  else conv::fwd_kernel<T, K, 1><<<strip_grid<T, 1>(a), 256, 0, s>>>(a);
+  if (a.conv_out != nullptr) conv::tail_kernel<T, K><<<dim3((a.D + 255) / 256, a.B * a.H), 256, 0, s>>>(a);
+  return launched();
+}
+
+template <class T, int K>
+prism_status bwd(bool wide, const ConvArgs& a, hipStream_t s) {
+  constexpr int V = 16 / sizeof(T);
+  if (wide) conv::bwd_kernel<T, K, V><<<strip_grid<T, V>(a), 256, 0, s>>>(a);
+  else conv::bwd_kernel<T, K, 1><<<strip_grid<T, 1>(a), 256, 0, s>>>(a);
+  conv::wsum_kernel<K><<<dim3((a.D + 63) / 64, K + 1, a.H), 256, 0, s>>>(a);
+  return launched();
+}
+
+template <class T, int K>
+prism_status step(const ConvArgs& a, hipStream_t s) {
+  const size_t n = (size_t)a.B * a.H * a.D;
+  conv::step_kernel<T, K><<<dim3((unsigned)((n + 255) / 256)), 256, 0, s>>>(a);
+  return launched();
+}
+
+}  // namespace
+
+prism_status launch_conv_fwd(prism_dtype dt, int K, bool wide, const ConvArgs& a, hipStream_t s) {
+  if (dt == PRISM_BF16) return K == 2 ? fwd<bf16_t, 2>(wide, a, s) : K == 3 ? fwd<bf16_t, 3>(wide, a, s) : fwd<bf16_t, 4>(wide, a, s);
+  return K == 2 ? fwd<float, 2>(wide, a, s) : K == 3 ? fwd<float, 3>(wide, a, s) : fwd<float, 4>(wide, a, s);
+}
+prism_status launch_conv_bwd(prism_dtype dt, int K, bool wide, const ConvArgs& a, hipStream_t s) {
+  if (dt == PRISM_BF16) return K == 2 ? bwd<bf16_t, 2>(wide, a, s) : K == 3 ? bwd<bf16_t, 3>(wide, a, s) : bwd<bf16_t, 4>(wide, a, s);
+  return K == 2 ? bwd<float, 2>(wide, a, s) : K == 3 ? bwd<float, 3>(wide, a, s) : bwd<float, 4>(wide, a, s);
+}
+prism_status launch_conv_step(prism_dtype dt, int K, const ConvArgs& a, hipStream_t s) {
+  if (dt == PRISM_BF16) return K == 2 ? step<bf16_t, 2>(a, s) : K == 3 ? step<bf16_t, 3>(a, s) : step<bf16_t, 4>(a, s);
+  return K == 2 ? step<float, 2>(a, s) : K == 3 ? step<float, 3>(a, s) : step<float, 4>(a, s);
+}
+
+}  // namespace host
+}  // namespace prism

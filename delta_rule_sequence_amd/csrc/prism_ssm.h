@@ -1,0 +1,626 @@
+// prism_ssm.h - the selective state space scan in float32 arithmetic (gfx950): forward, backward and
+// the single-token step, for bfloat16 and float32 tensors.
+//
+//   d_t = softplus(dt_t + bias),  l_t = d_t A,  S_t = e^{l_t} S_{t-1} + d_t B_t x_t^T,  y_t = S_t^T C_t + D x_t
+//
+// Chunked form, 64 tokens per chunk, with c_t the running sum of l inside the chunk and H the state entering it:
+//   y_t  = e^{c_t} H^T C_t + sum_{s<=t} M_ts x_s + D x_t,    M_ts = (C_t . B_s) e^{c_t - c_s} d_s
+//   H'   = e^{c_63} H + sum_s e^{c_63 - c_s} d_s B_s x_s^T
+// A sequence is cut into segments of chunks that run side by side: a first pass forms each
+// segment's end state from zero, a scan over the segments gives the states that enter them.
+// c is summed in float64 and held as base-2 exponents in two floats, so that e^{c_t - c_s} keeps
+// float32 accuracy after long decays.
+#pragma once
+#include "prism_ssm_args.h"
+#include "prism_tile.h"
+
+namespace prism {
+namespace ssm {
+
+constexpr int Q = 64;  // tokens per chunk
+
+// Per-token scalars of one chunk in LDS.
+struct Scal {
+  float ch[Q], cl[Q];  // running log2 decay, high and low part
+  float d[Q];          // step
+  float eo[Q];         // decay from the chunk's start through token t
+  float w[Q];          // decay from token t to the chunk's end
+  float sig[Q];        // derivative of the step with respect to dt
+  float dec;           // decay over the chunk
+};
+
+__device__ __forceinline__ int seq_len(const SsmArgs& a, int b) {
+  if (a.lens == nullptr) return a.T;
+  const int n = a.lens[b];
+  return n < 0 ? 0 : (n > a.T ? a.T : n);
+}
+
+__device__ __forceinline__ double wave_scan(double v, int lane) {
+#pragma unroll
+  for (int o = 1; o < 64; o <<= 1) {
+    const double u = __shfl_up(v, o, 64);
+    if (lane >= o) v += u;
+  }
+  return v;
+}
+
+__device__ __forceinline__ float softplus_f(float z) { return z > 20.f ? z : log1pf(expf(z)); }
+
+constexpr double kLog2e = 1.4426950408889634;
+
+// One wave: the chunk's scalars from its 64 steps; tokens at or past len have a step of 0
+// (decay 1, nothing written).  Returns the chunk's log2 decay on every lane.
+__device__ __forceinline__ double chunk_scalars(const SsmArgs& a, int b, int h, int t0, int len, Scal& s) {
+  const int lane = lane_id(), t = t0 + lane;
+  float d = 0.f, sig = 0.f;
+  if (t < len) {
+    const float z = a.dt[b * a.ts.b + h * a.ts.h + t * a.ts.t] + (a.dt_bias != nullptr ? a.dt_bias[h] : 0.f);
+    d = a.softplus ? softplus_f(z) : z;
+    sig = a.softplus ? 1.f / (1.f + expf(-z)) : 1.f;
+  }
+  const double l2 = t < len ? (double)d * (double)a.A[h] * kLog2e : 0.0;
+  const double c = wave_scan(l2, lane);
+  const double tot = __shfl(c, 63, 64);
+  const float hi = (float)c;
+  s.ch[lane] = hi;
+  s.cl[lane] = (float)(c - (double)hi);
+  s.d[lane] = d;
+  s.sig[lane] = sig;
+  s.eo[lane] = exp2f((float)c);
+  s.w[lane] = exp2f((float)(tot - c));
+  if (lane == 0) s.dec = exp2f((float)tot);
+  return tot;
+}
+
+// Rows t0 .. t0 + 63 of a strided [T, W] tensor as float32 in LDS (row stride LD); rows at or past len are 0.
+template <class T, int W, int LD>
+__device__ __forceinline__ void load_rows(float* dst, const void* base, long long off, long long st, int t0, int len,
+                                          int nthreads) {
+  constexpr int V = 16 / sizeof(T);
+  typedef T vec __attribute__((ext_vector_type(V)));
+  const T* p = reinterpret_cast<const T*>(base) + off;
+  for (int i = threadIdx.x; i < Q * W / V; i += nthreads) {
+    const int r = i / (W / V), c = i % (W / V) * V;
+    float* o = dst + r * LD + c;
+    if (t0 + r < len) {
+      const vec v = *reinterpret_cast<const vec*>(p + (long long)(t0 + r) * st + c);
+#pragma unroll
+      for (int k = 0; k < V; ++k) o[k] = (float)v[k];
+    } else {
+#pragma unroll
+      for (int k = 0; k < V; ++k) o[k] = 0.f;
+    }
+  }
+}
+
+// Operand fragments of the 16x16x4 float32 MFMA over 16 k values: element r of lane (g, i) is k = 4 g + r.
+__device__ __forceinline__ f32x4 frag_k(const float* p, int ld, int row0, int k0) {  // index = row, k contiguous
+  const int l = lane_id();
+  return *reinterpret_cast<const f32x4*>(p + (row0 + (l & 15)) * ld + k0 + 4 * (l >> 4));
+}
+__device__ __forceinline__ f32x4 frag_t(const float* p, int ld, int k0, int col0) {  // k = row, index = column
+  const int l = lane_id();
+  const float* q = p + (k0 + 4 * (l >> 4)) * ld + col0 + (l & 15);
+  f32x4 f;
+#pragma unroll
+  for (int r = 0; r < 4; ++r) f[r] = q[r * ld];
+  return f;
+}
+__device__ __forceinline__ f32x4 scale4(const f32x4& f, const float* s, int k0) {  // times s[k]
+  const int g = lane_id() >> 4;
+  f32x4 o;
+#pragma unroll
+  for (int r = 0; r < 4; ++r) o[r] = f[r] * s[k0 + 4 * g + r];
+  return o;
+}
+// acc[row = index of a][col = index of b] += sum over 16 k
+__device__ __forceinline__ void mm4(f32x4& acc, const f32x4& a, const f32x4& b) {
+#pragma unroll
+  for (int r = 0; r < 4; ++r) acc = mfma(a[r], b[r], acc);
+}
+
+// A state tile in the workspace: tile (pt, nt) of a transposed state H^T [PW][N] as 64 lanes x 4 floats, lane (g, i)
+// holding rows p = 16 pt + 4 g + r, column n = 16 nt + i.
+template <int N>
+__device__ __forceinline__ size_t tile_at(int pt, int nt) {
+  return ((size_t)pt * (N / 16) + nt) * 256 + 4 * lane_id();
+}
+// Offset of element (n, p) in that layout.
+template <int N>
+__device__ __forceinline__ size_t elem_at(int n, int p) {
+  return ((size_t)(p >> 4) * (N / 16) + (n >> 4)) * 256 + ((p >> 2) & 3) * 64 + (n & 15) * 4 + (p & 3);
+}
+
+// States of a segment from zero (or, with SAVE, from the entering state, storing the state at every chunk border).
+// Grid (nseg, B * HV, directions); NW = PW / 16 waves, each owning 16 columns.
+//   direction 0: H' = dec H + (w d B)^T x over the chunks in order;   saved: the state entering each chunk
+//   direction 1: R' = dec R + (eo C)^T dy in reverse order;           saved: the adjoint leaving each chunk
+template <class T, int N, int PW, bool SAVE>
+__global__ __launch_bounds__(PW * 4) void state_kernel(SsmArgs a) {
+  constexpr int NTH = PW * 4, LDN = N + 4, LDP = PW + 4, NT = N / 16;
+  __shared__ float sA[Q * LDN];
+  __shared__ float sV[Q * LDP];
+  __shared__ float sWt[Q];
+  __shared__ Scal sc;
+  const int seg = blockIdx.x, bh = blockIdx.y, rev = blockIdx.z;
+  const int HV = a.H * a.nsl, b = bh / HV, hv = bh % HV, h = hv / a.nsl, p0 = hv % a.nsl * PW, grp = h / (a.H / a.G);
+  const int len = seq_len(a, b), pt = wave_id(), tid = threadIdx.x;
+  const int c0 = seg * a.seg_chunks, c1 = min(c0 + a.seg_chunks, a.nch);
+  const size_t slot = ((size_t)rev * gridDim.y + bh) * a.nseg + seg;
+  f32x4 acc[NT];
+#pragma unroll
+  for (int n = 0; n < NT; ++n)
+    acc[n] = SAVE ? *reinterpret_cast<const f32x4*>(a.seg + slot * (N * PW) + tile_at<N>(pt, n)) : zero4();
+  double log_dec = 0.0;
+  for (int k = 0; k < c1 - c0; ++k) {
+    const int ch = rev ? c1 - 1 - k : c0 + k, t0 = ch * Q;
+    if constexpr (SAVE) {
+      float* st = a.st + (((size_t)rev * gridDim.y + bh) * a.nch + ch) * (N * PW);
+#pragma unroll
+      for (int n = 0; n < NT; ++n) *reinterpret_cast<f32x4*>(st + tile_at<N>(pt, n)) = acc[n];
+    }
+    if (t0 >= len) continue;
+    __syncthreads();
+    if (rev) {
+      load_rows<T, N, LDN>(sA, a.cm, b * a.cs.b + grp * a.cs.h, a.cs.t, t0, len, NTH);
+      load_rows<T, PW, LDP>(sV, a.dy, b * a.dys.b + h * a.dys.h + p0, a.dys.t, t0, len, NTH);
+    } else {
+      load_rows<T, N, LDN>(sA, a.bm, b * a.bs.b + grp * a.bs.h, a.bs.t, t0, len, NTH);
+      load_rows<T, PW, LDP>(sV, a.x, b * a.xs.b + h * a.xs.h + p0, a.xs.t, t0, len, NTH);
+    }
+    if (tid < 64) {
+      log_dec += chunk_scalars(a, b, h, t0, len, sc);
+      sWt[tid] = rev ? sc.eo[tid] : sc.w[tid] * sc.d[tid];
+    }
+    __syncthreads();
+    const float dec = sc.dec;
+#pragma unroll
+    for (int n = 0; n < NT; ++n) acc[n] *= dec;
+#pragma unroll
+    for (int k0 = 0; k0 < Q; k0 += 16) {
+      const f32x4 fv = scale4(frag_t(sV, LDP, k0, 16 * pt), sWt, k0);
+#pragma unroll
+      for (int n = 0; n < NT; ++n) mm4(acc[n], fv, frag_t(sA, LDN, k0, 16 * n));
+    }
+  }
+  if constexpr (!SAVE) {
+#pragma unroll
+    for (int n = 0; n < NT; ++n) *reinterpret_cast<f32x4*>(a.seg + slot * (N * PW) + tile_at<N>(pt, n)) = acc[n];
+    if (rev == 0 && tid == 0) a.seg_dec[(size_t)bh * a.nseg + seg] = exp2f((float)log_dec);
+  }
+}
+
+// The states entering each segment, in place of the segments' own end states: forward from S0, and
+// (direction 1) the adjoints arriving at each segment's end, backward from dS_final.  Grid
+// (N * PW / 256, B * HV, directions), one state element per thread.
+template <int N, int PW>
+__global__ __launch_bounds__(256) void seg_scan_kernel(SsmArgs a, int has_end) {
+  const int e = blockIdx.x * 256 + threadIdx.x, bh = blockIdx.y, rev = blockIdx.z;
+  const int HV = a.H * a.nsl, b = bh / HV, hv = bh % HV, h = hv / a.nsl, p0 = hv % a.nsl * PW;
+  // element (n, p) of position e (see elem_at)
+  const int tile = e >> 8, p = (tile / (N / 16)) * 16 + ((e >> 6) & 3) * 4 + (e & 3), n = (tile % (N / 16)) * 16 + ((e >> 2) & 15);
+  const float* init = rev ? a.dS : a.S0;
+  float v = init != nullptr ? init[((size_t)(b * a.H + h) * N + n) * a.P + p0 + p] : 0.f;
+  float* q = a.seg + ((size_t)rev * gridDim.y + bh) * a.nseg * (N * PW) + e;
+  for (int k = 0; k < a.nseg; ++k) {
+    const int s = rev ? a.nseg - 1 - k : k;
+    const float own = has_end ? q[(size_t)s * (N * PW)] : 0.f;
+    q[(size_t)s * (N * PW)] = v;
+    if (has_end) v = a.seg_dec[(size_t)bh * a.nseg + s] * v + own;
+  }
+}
+
+// The scan of a segment from its entering state (seg when nseg > 1, else S0): outputs, and the final state
+// from the last segment.  Grid (nseg, B * HV).
+template <class T, int N, int PW>
+__global__ __launch_bounds__(PW * 4) void sweep_kernel(SsmArgs a) {
+  constexpr int NTH = PW * 4, NW = PW / 16, LDN = N + 4, LDP = PW + 4, LDQ = Q + 4, NT = N / 16;
+  typedef T out4 __attribute__((ext_vector_type(4)));
+  __shared__ float sB[Q * LDN];
+  __shared__ float sC[Q * LDN];
+  __shared__ float sX[Q * LDP];
+  __shared__ float sM[Q * LDQ];
+  __shared__ Scal sc;
+  const int seg = blockIdx.x, bh = blockIdx.y;
+  const int HV = a.H * a.nsl, b = bh / HV, hv = bh % HV, h = hv / a.nsl, p0 = hv % a.nsl * PW, grp = h / (a.H / a.G);
+  const int len = seq_len(a, b), pt = wave_id(), tid = threadIdx.x, l = lane_id(), g = l >> 4, i = l & 15;
+  const int c0 = seg * a.seg_chunks, c1 = min(c0 + a.seg_chunks, a.nch);
+  const float Dh = a.D != nullptr ? a.D[h] : 0.f;
+  const size_t gstate = ((size_t)(b * a.H + h) * N) * a.P + p0 + 16 * pt;
+  // state tiles: rows n = 16 nt + 4 g + r, column p = 16 pt + i
+  f32x4 hs[NT];
+#pragma unroll
+  for (int n = 0; n < NT; ++n)
+#pragma unroll
+    for (int r = 0; r < 4; ++r) {
+      const int row = 16 * n + 4 * g + r;
+      if (a.nseg > 1) hs[n][r] = a.seg[((size_t)bh * a.nseg + seg) * (N * PW) + elem_at<N>(row, 16 * pt + i)];
+      else hs[n][r] = a.S0 != nullptr ? a.S0[gstate + (size_t)row * a.P + i] : 0.f;
+    }
+  for (int ch = c0; ch < c1; ++ch) {
+    const int t0 = ch * Q;
+    if (t0 >= len) break;
+    __syncthreads();
+    load_rows<T, N, LDN>(sB, a.bm, b * a.bs.b + grp * a.bs.h, a.bs.t, t0, len, NTH);
+    load_rows<T, N, LDN>(sC, a.cm, b * a.cs.b + grp * a.cs.h, a.cs.t, t0, len, NTH);
+    load_rows<T, PW, LDP>(sX, a.x, b * a.xs.b + h * a.xs.h + p0, a.xs.t, t0, len, NTH);
+    if (tid < 64) chunk_scalars(a, b, h, t0, len, sc);
+    __syncthreads();
+    // M, tile (ts, tt): rows s, columns t
+    for (int idx = wave_id(); idx < 10; idx += NW) {
+      int tt = 0, ts = idx;
+      while (ts > tt) ts -= ++tt;
+      f32x4 acc = zero4();
+#pragma unroll
+      for (int n = 0; n < NT; ++n) mm4(acc, frag_k(sB, LDN, 16 * ts, 16 * n), frag_k(sC, LDN, 16 * tt, 16 * n));
+      const int t = 16 * tt + i;
+      f32x4 m;
+#pragma unroll
+      for (int r = 0; r < 4; ++r) {
+        const int s = 16 * ts + 4 * g + r;
+        m[r] = s <= t ? acc[r] * exp2f((sc.ch[t] - sc.ch[s]) + (sc.cl[t] - sc.cl[s])) * sc.d[s] : 0.f;
+      }
+      *reinterpret_cast<f32x4*>(sM + t * LDQ + 16 * ts + 4 * g) = m;
+    }
+    __syncthreads();
+#pragma unroll
+    for (int tt = 0; tt < Q / 16; ++tt) {
+      const int t = 16 * tt + i;
+      f32x4 acc = zero4();
+#pragma unroll
+      for (int n = 0; n < NT; ++n) mm4(acc, hs[n], frag_k(sC, LDN, 16 * tt, 16 * n));
+      acc *= sc.eo[t];
+#pragma unroll
+      for (int ts = 0; ts <= tt; ++ts) mm4(acc, frag_t(sX, LDP, 16 * ts, 16 * pt), frag_k(sM, LDQ, 16 * tt, 16 * ts));
+      const f32x4 xv = *reinterpret_cast<const f32x4*>(sX + t * LDP + 16 * pt + 4 * g);
+      if (t0 + t < len) {
+        out4 o;
+#pragma unroll
+        for (int r = 0; r < 4; ++r) o[r] = (T)(acc[r] + Dh * xv[r]);
+        T* y = reinterpret_cast<T*>(a.y) + b * a.ys.b + h * a.ys.h + (long long)(t0 + t) * a.ys.t + p0 + 16 * pt + 4 * g;
+        *reinterpret_cast<out4*>(y) = o;
+      }
+    }
+    const float dec = sc.dec;
+#pragma unroll
+    for (int n = 0; n < NT; ++n) hs[n] *= dec;
+#pragma unroll
+    for (int k0 = 0; k0 < Q; k0 += 16) {
+      const f32x4 fx = scale4(scale4(frag_t(sX, LDP, k0, 16 * pt), sc.w, k0), sc.d, k0);
+#pragma unroll
+      for (int n = 0; n < NT; ++n) mm4(hs[n], frag_t(sB, LDN, k0, 16 * n), fx);
+    }
+  }
+  if (seg == a.nseg - 1) {
+#pragma unroll
+    for (int n = 0; n < NT; ++n)
+#pragma unroll
+      for (int r = 0; r < 4; ++r) a.S_final[gstate + (size_t)(16 * n + 4 * g + r) * a.P + i] = hs[n][r];
+  }
+}
+
+__device__ __forceinline__ float sum_groups(float v) {  // over the four 16-lane groups
+  v += __shfl_xor(v, 16, 64);
+  return v + __shfl_xor(v, 32, 64);
+}
+__device__ __forceinline__ float sum_lanes16(float v) {  // over the 16 lanes of a group
+#pragma unroll
+  for (int o = 1; o < 16; o <<= 1) v += __shfl_xor(v, o, 64);
+  return v;
+}
+
+// Gradients of one chunk for one group (grid (nch, nsplit, B * G)): the workgroup walks its share of the group's
+// virtual heads, so that dB and dC are summed over heads in registers.  With H the state entering the chunk and R the
+// adjoint of the state leaving it (state_kernel), dM = dy x^T, E_ts = e^{c_t - c_s}:
+//   dx_s = sum_t M_ts dy_t + w_s d_s R^T B_s + D dy_s
+//   dC_t = sum_s (dM E)_ts d_s B_s + eo_t H dy_t,       dB_s = d_s (sum_t (dM E)_ts C_t + w_s R x_s)
+//   dd_s = sum_t q_ts + J_s + A dl_s,   q = (C B^T) E dM,   J_s = w_s B_s . (R x_s)
+//   dl_t = sum_{s<t<=t'} q_t's d_s + sum_{t'>=t} I_t' + sum_{s<t} d_s J_s + e^{c_63} <H, R>,   I_t = eo_t C_t . (H dy_t)
+// Four waves, wave w owning tokens 16 w .. 16 w + 15 as columns t of the score tiles and as rows of dx, dB and dC.
+template <class T, int N, int PW>
+__global__ __launch_bounds__(256) void grad_kernel(SsmArgs a) {
+  constexpr int LDN = N + 4, LDP = PW + 4, LDQ = Q + 4, NT = N / 16, PT = PW / 16;
+  typedef T out4 __attribute__((ext_vector_type(4)));
+  __shared__ float sB[Q * LDN];
+  __shared__ float sC[Q * LDN];
+  __shared__ float sX[Q * LDP];
+  __shared__ float sY[Q * LDP];  // dy
+  __shared__ float sM[Q * LDQ];  // M[t][s]
+  __shared__ Scal sc;
+  __shared__ float sRow[Q], sI[Q], sJ[Q], sDiag[Q], sCol[4][Q], sK[4], sDD[4];
+  const int ch = blockIdx.x, bg = blockIdx.z, b = bg / a.G, grp = bg % a.G, t0 = ch * Q;
+  const int w = wave_id(), tid = threadIdx.x, l = lane_id(), g = l >> 4, i = l & 15;
+  const int HV = a.H * a.nsl, per_group = HV / a.G;
+  const int v0 = blockIdx.y * a.per_split, v1 = min(v0 + a.per_split, per_group);
+  load_rows<T, N, LDN>(sB, a.bm, b * a.bs.b + grp * a.bs.h, a.bs.t, t0, a.T, 256);
+  load_rows<T, N, LDN>(sC, a.cm, b * a.cs.b + grp * a.cs.h, a.cs.t, t0, a.T, 256);
+  __syncthreads();
+  const int tok = 16 * w + i;  // this lane's token
+  f32x4 gm[4], dg[4], dc[NT], db[NT];
+#pragma unroll
+  for (int ts = 0; ts < 4; ++ts) {
+    gm[ts] = zero4();
+    dg[ts] = zero4();
+    if (ts <= w)
+#pragma unroll
+      for (int n = 0; n < NT; ++n) mm4(gm[ts], frag_k(sB, LDN, 16 * ts, 16 * n), frag_k(sC, LDN, 16 * w, 16 * n));
+  }
+#pragma unroll
+  for (int n = 0; n < NT; ++n) dc[n] = db[n] = zero4();
+  for (int v = v0; v < v1; ++v) {
+    const int hv = grp * per_group + v, h = hv / a.nsl, slice = hv % a.nsl, p0 = slice * PW;
+    const size_t bh = (size_t)b * HV + hv;
+    const float* H = a.st + (bh * a.nch + ch) * (N * PW);
+    const float* R = a.st + (((size_t)a.B * HV + bh) * a.nch + ch) * (N * PW);
+    __syncthreads();
+    load_rows<T, PW, LDP>(sX, a.x, b * a.xs.b + h * a.xs.h + p0, a.xs.t, t0, a.T, 256);
+    load_rows<T, PW, LDP>(sY, a.dy, b * a.dys.b + h * a.dys.h + p0, a.dys.t, t0, a.T, 256);
+    if (tid < 64) chunk_scalars(a, b, h, t0, a.T, sc);
+    __syncthreads();
+    float row = 0.f;
+#pragma unroll
+    for (int ts = 0; ts < 4; ++ts) {
+      f32x4 col = zero4();
+      if (ts <= w) {
+        f32x4 dm = zero4(), m;
+#pragma unroll
+        for (int p = 0; p < PT; ++p) mm4(dm, frag_k(sX, LDP, 16 * ts, 16 * p), frag_k(sY, LDP, 16 * w, 16 * p));
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+          const int s = 16 * ts + 4 * g + r;
+          const float e = s <= tok ? exp2f((sc.ch[tok] - sc.ch[s]) + (sc.cl[tok] - sc.cl[s])) : 0.f;
+          m[r] = s <= tok ? gm[ts][r] * e * sc.d[s] : 0.f;
+          dg[ts][r] += s <= tok ? dm[r] * e * sc.d[s] : 0.f;
+          const float q = s <= tok ? gm[ts][r] * e * dm[r] : 0.f;
+          if (s < tok) {
+            row += q * sc.d[s];
+            col[r] = q;
+          }
+          if (s == tok) sDiag[s] = q;
+        }
+        *reinterpret_cast<f32x4*>(sM + tok * LDQ + 16 * ts + 4 * g) = m;
+      }
+#pragma unroll
+      for (int r = 0; r < 4; ++r) {
+        const float c = sum_lanes16(col[r]);
+        if (i == 0) sCol[w][16 * ts + 4 * g + r] = c;
+      }
+    }
+    row = sum_groups(row);
+    if (g == 0) sRow[tok] = row;
+    // products with the states: rows n, columns token
+    float I = 0.f, J = 0.f, K = 0.f;
+    const float eo = sc.eo[tok], ww = sc.w[tok], dd = sc.d[tok];
+#pragma unroll
+    for (int n = 0; n < NT; ++n) {
+      f32x4 uc = zero4(), ub = zero4();
+#pragma unroll
+      for (int p = 0; p < PT; ++p) {
+        const f32x4 fh = *reinterpret_cast<const f32x4*>(H + tile_at<N>(p, n));
+        const f32x4 fr = *reinterpret_cast<const f32x4*>(R + tile_at<N>(p, n));
+        mm4(uc, fh, frag_k(sY, LDP, 16 * w, 16 * p));
+        mm4(ub, fr, frag_k(sX, LDP, 16 * w, 16 * p));
+        if ((p * NT + n) % 4 == w)
+#pragma unroll
+          for (int r = 0; r < 4; ++r) K += fh[r] * fr[r];
+      }
+      const f32x4 fc = *reinterpret_cast<const f32x4*>(sC + tok * LDN + 16 * n + 4 * g);
+      const f32x4 fb = *reinterpret_cast<const f32x4*>(sB + tok * LDN + 16 * n + 4 * g);
+#pragma unroll
+      for (int r = 0; r < 4; ++r) {
+        uc[r] *= eo;
+        ub[r] *= ww;
+        I += fc[r] * uc[r];
+        J += fb[r] * ub[r];
+        dc[n][r] += uc[r];
+        db[n][r] += dd * ub[r];
+      }
+    }
+    I = sum_groups(I);
+    J = sum_groups(J);
+    K = sum_groups(sum_lanes16(K));
+    if (g == 0) {
+      sI[tok] = I;
+      sJ[tok] = J;
+    }
+    if (l == 0) sK[w] = K;
+    __syncthreads();
+    // dx: rows p, columns s (this lane's token)
+    const float Dh = a.D != nullptr ? a.D[h] : 0.f;
+    float xd = 0.f;
+#pragma unroll
+    for (int p = 0; p < PT; ++p) {
+      f32x4 acc = zero4();
+#pragma unroll
+      for (int n = 0; n < NT; ++n) {
+        f32x4 fr;  // index p, k = n
+#pragma unroll
+        for (int r = 0; r < 4; ++r) fr[r] = R[elem_at<N>(16 * n + 4 * g + r, 16 * p + i)];
+        mm4(acc, fr, frag_k(sB, LDN, 16 * w, 16 * n));
+      }
+      acc *= ww * dd;
+#pragma unroll
+      for (int tt = 0; tt < 4; ++tt)
+        if (tt >= w) mm4(acc, frag_t(sY, LDP, 16 * tt, 16 * p), frag_t(sM, LDQ, 16 * tt, 16 * w));
+      const f32x4 yv = *reinterpret_cast<const f32x4*>(sY + tok * LDP + 16 * p + 4 * g);
+      const f32x4 xv = *reinterpret_cast<const f32x4*>(sX + tok * LDP + 16 * p + 4 * g);
+      out4 o;
+#pragma unroll
+      for (int r = 0; r < 4; ++r) {
+        o[r] = (T)(acc[r] + Dh * yv[r]);
+        xd += xv[r] * yv[r];
+      }
+      if (t0 + tok < a.T) {
+        T* q = reinterpret_cast<T*>(a.dx) + b * a.dxs.b + h * a.dxs.h + (long long)(t0 + tok) * a.dxs.t + p0 + 16 * p + 4 * g;
+        *reinterpret_cast<out4*>(q) = o;
+      }
+    }
+    xd = sum_groups(sum_lanes16(xd));
+    if (l == 0) sDD[w] = xd;
+    __syncthreads();
+    if (tid < 64) {
+      const int t = tid;
+      float qoff = 0.f;
+#pragma unroll
+      for (int k = 0; k < 4; ++k) qoff += (t >> 4) <= k ? sCol[k][t] : 0.f;
+      const float d = sc.d[t], J0 = sJ[t], Ah = a.A[h];
+      const double jd = (double)d * J0;
+      const double f = (double)sRow[t] - (double)d * qoff + sI[t];
+      const double fs = wave_scan(f, t), ftot = __shfl(fs, 63, 64);  // suffix sum from t: ftot - fs + f
+      const double js = wave_scan(jd, t);                            // prefix sum before t: js - jd
+      const float kk = sc.dec * ((sK[0] + sK[1]) + (sK[2] + sK[3]));
+      const float dl = (float)((ftot - fs + f) + (js - jd) + kk);
+      const float ddt = (qoff + sDiag[t] + J0 + Ah * dl) * sc.sig[t];
+      const bool in = t0 + t < a.T;
+      if (in) {
+        const size_t at = ((size_t)b * a.H + h) * a.T + t0 + t;
+        if (a.nsl == 1) a.ddt[at] = ddt;
+        else a.part_ddt[(size_t)slice * a.B * a.H * a.T + at] = ddt;
+      }
+      double sa = in ? (double)dl * d : 0.0, sb = in ? (double)ddt : 0.0;
+#pragma unroll
+      for (int o = 1; o < 64; o <<= 1) {
+        sa += __shfl_xor(sa, o, 64);
+        sb += __shfl_xor(sb, o, 64);
+      }
+      if (t == 0) {
+        const size_t at = bh * a.nch + ch, n = (size_t)a.B * HV * a.nch;
+        a.part_sum[at] = (float)sa;
+        a.part_sum[n + at] = (sDD[0] + sDD[1]) + (sDD[2] + sDD[3]);
+        a.part_sum[2 * n + at] = (float)sb;
+      }
+    }
+  }
+  // the summed score gradients times B and C
+  __syncthreads();
+#pragma unroll
+  for (int ts = 0; ts < 4; ++ts)
+    if (ts <= w) *reinterpret_cast<f32x4*>(sM + tok * LDQ + 16 * ts + 4 * g) = dg[ts];
+  __syncthreads();
+#pragma unroll
+  for (int n = 0; n < NT; ++n) {
+#pragma unroll
+    for (int ts = 0; ts < 4; ++ts) {
+      if (ts <= w) mm4(dc[n], frag_t(sB, LDN, 16 * ts, 16 * n), dg[ts]);
+      if (ts >= w) mm4(db[n], frag_t(sC, LDN, 16 * ts, 16 * n), frag_t(sM, LDQ, 16 * ts, 16 * w));
+    }
+    if (t0 + tok < a.T) {
+      const int c = 16 * n + 4 * g;
+      if (a.nsplit == 1) {
+        out4 ob, oc;
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+          ob[r] = (T)db[n][r];
+          oc[r] = (T)dc[n][r];
+        }
+        *reinterpret_cast<out4*>(reinterpret_cast<T*>(a.dbm) + b * a.dbs.b + grp * a.dbs.h + (long long)(t0 + tok) * a.dbs.t + c) = ob;
+        *reinterpret_cast<out4*>(reinterpret_cast<T*>(a.dcm) + b * a.dcs.b + grp * a.dcs.h + (long long)(t0 + tok) * a.dcs.t + c) = oc;
+      } else {
+        const size_t at = (((size_t)blockIdx.y * a.B * a.G + bg) * a.T + t0 + tok) * N + c;
+        *reinterpret_cast<f32x4*>(a.part_b + at) = db[n];
+        *reinterpret_cast<f32x4*>(a.part_c + at) = dc[n];
+      }
+    }
+  }
+}
+
+// dB, dC from the splits' shares, in split order.  One group of 4 values per thread.
+template <class T, int N>
+__global__ __launch_bounds__(256) void split_sum_kernel(SsmArgs a) {
+  typedef T out4 __attribute__((ext_vector_type(4)));
+  const size_t rows = (size_t)a.B * a.G * a.T, i = (size_t)blockIdx.x * 256 + threadIdx.x;
+  const size_t row = i / (N / 4);
+  if (row >= rows) return;
+  const int c = (int)(i % (N / 4)) * 4;
+  const size_t bg = row / a.T, t = row % a.T, b = bg / a.G, grp = bg % a.G;
+  f32x4 sb = zero4(), scv = zero4();
+  for (int k = 0; k < a.nsplit; ++k) {
+    sb += *reinterpret_cast<const f32x4*>(a.part_b + ((size_t)k * rows + row) * N + c);
+    scv += *reinterpret_cast<const f32x4*>(a.part_c + ((size_t)k * rows + row) * N + c);
+  }
+  out4 ob, oc;
+#pragma unroll
+  for (int r = 0; r < 4; ++r) {
+    ob[r] = (T)sb[r];
+    oc[r] = (T)scv[r];
+  }
+  *reinterpret_cast<out4*>(reinterpret_cast<T*>(a.dbm) + b * a.dbs.b + grp * a.dbs.h + (long long)t * a.dbs.t + c) = ob;
+  *reinterpret_cast<out4*>(reinterpret_cast<T*>(a.dcm) + b * a.dcs.b + grp * a.dcs.h + (long long)t * a.dcs.t + c) = oc;
+}
+
+// ddt from the slices' shares (nsl > 1).
+template <class T>
+__global__ __launch_bounds__(256) void ddt_sum_kernel(SsmArgs a) {
+  const size_t n = (size_t)a.B * a.H * a.T, i = (size_t)blockIdx.x * 256 + threadIdx.x;
+  if (i >= n) return;
+  float s = 0.f;
+  for (int k = 0; k < a.nsl; ++k) s += a.part_ddt[k * n + i];
+  a.ddt[i] = s;
+}
+
+// dA, dD, ddt_bias of one head (grid (H, 3)) from the chunks' shares, in float64 and a fixed order.
+template <class T>
+__global__ __launch_bounds__(256) void head_sum_kernel(SsmArgs a) {
+  const int h = blockIdx.x, which = blockIdx.y, HV = a.H * a.nsl;
+  float* out = which == 0 ? a.dA : which == 1 ? a.dD : a.ddt_bias;
+  if (out == nullptr) return;
+  const size_t per = (size_t)a.nsl * a.nch, n = (size_t)a.B * HV * a.nch;
+  double s = 0.0;
+  for (size_t k = threadIdx.x; k < a.B * per; k += 256)
+    s += (double)a.part_sum[which * n + (k / per * HV + (size_t)h * a.nsl) * a.nch + k % per];
+  __shared__ double part[256];
+  part[threadIdx.x] = s;
+  __syncthreads();
+  for (int o = 128; o > 0; o >>= 1) {
+    if ((int)threadIdx.x < o) part[threadIdx.x] += part[threadIdx.x + o];
+    __syncthreads();
+  }
+  if (threadIdx.x == 0) out[h] = (float)part[0];
+}
+
+// One token: S' = e^{d A} S + d B x^T in place, y = S'^T C + D x.  Bound by reading and writing S.  One workgroup per
+// (b, h): P / 4 threads across the columns (16-byte state accesses), 256 / (P / 4) groups of rows whose shares of y
+// are summed in LDS.
+template <class T, int N, int P>
+__global__ __launch_bounds__(256) void step_kernel(SsmStepArgs a) {
+  constexpr int TC = P / 4, RG = 256 / TC, RPT = N >= RG ? N / RG : 1;
+  __shared__ float sY[RG][P];
+  const int b = blockIdx.x / a.H, h = blockIdx.x % a.H, grp = h / (a.H / a.G);
+  const int c = (threadIdx.x % TC) * 4, rg = threadIdx.x / TC;
+  const T* x = reinterpret_cast<const T*>(a.x) + b * a.xs.b + h * a.xs.h;
+  const T* Bm = reinterpret_cast<const T*>(a.bm) + b * a.bs.b + grp * a.bs.h;
+  const T* Cm = reinterpret_cast<const T*>(a.cm) + b * a.cs.b + grp * a.cs.h;
+  const float z = a.dt[b * a.ts.b + h * a.ts.h] + (a.dt_bias != nullptr ? a.dt_bias[h] : 0.f);
+  const float d = a.softplus ? softplus_f(z) : z;
+  const float dec = expf(d * a.A[h]);
+  float* S = a.S + (size_t)blockIdx.x * N * P + c;
+  f32x4 xv, acc = zero4();
+#pragma unroll
+  for (int k = 0; k < 4; ++k) xv[k] = d * (float)x[c + k];
+  f32x4 s[RPT];
+#pragma unroll
+  for (int k = 0; k < RPT; ++k) {
+    const int n = rg + k * RG;
+    if (n < N) s[k] = *reinterpret_cast<const f32x4*>(S + (size_t)n * P);
+  }
+#pragma unroll
+  for (int k = 0; k < RPT; ++k) {
+    const int n = rg + k * RG;
+    if (n < N) {
+      const f32x4 u = s[k] * dec + xv * (float)Bm[n];
+      *reinterpret_cast<f32x4*>(S + (size_t)n * P) = u;
+      acc += u * (float)Cm[n];
+    }
+  }
+  *reinterpret_cast<f32x4*>(&sY[rg][c]) = acc;
+  __syncthreads();
+  if (threadIdx.x < P) {
+    float y = a.D != nullptr ? a.D[h] * (float)x[threadIdx.x] : 0.f;
+#pragma unroll
+    for (int k = 0; k < RG; ++k) y += sY[k][threadIdx.x];
+    reinterpret_cast<T*>(a.y)[(size_t)blockIdx.x * P + threadIdx.x] = (T)y;
+  }
+}
+
+}  // namespace ssm
+}  // namespace prism

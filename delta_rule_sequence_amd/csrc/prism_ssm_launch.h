@@ -1,0 +1,63 @@
+// prism_ssm_launch.h - launches of the state space scan for one tensor type and state width N (one
+// translation unit each, ssm_<type>_n<N>.hip).
+#pragma once
+#include "prism_ssm.h"
+
+namespace prism {
+namespace host {
+
+inline prism_status launched() { return hipGetLastError() == hipSuccess ? PRISM_OK : PRISM_ERR_HIP; }
+
+template <class T, int N, int PW>
+prism_status ssm_fwd_pw(const SsmArgs& a, hipStream_t stream) {
+  const int bh = a.B * a.H * a.nsl;
+  if (a.nseg > 1) {
+    ssm::state_kernel<T, N, PW, false><<<dim3(a.nseg, bh, 1), PW * 4, 0, stream>>>(a);
+    ssm::seg_scan_kernel<N, PW><<<dim3(N * PW / 256, bh, 1), 256, 0, stream>>>(a, 1);
+  }
+  ssm::sweep_kernel<T, N, PW><<<dim3(a.nseg, bh), PW * 4, 0, stream>>>(a);
+  return launched();
+}
+
+template <class T, int N, int PW>
+prism_status ssm_bwd_pw(const SsmArgs& a, hipStream_t stream) {
+  const int bh = a.B * a.H * a.nsl;
+  if (a.nseg > 1) ssm::state_kernel<T, N, PW, false><<<dim3(a.nseg, bh, 2), PW * 4, 0, stream>>>(a);
+  ssm::seg_scan_kernel<N, PW><<<dim3(N * PW / 256, bh, 2), 256, 0, stream>>>(a, a.nseg > 1);
+  ssm::state_kernel<T, N, PW, true><<<dim3(a.nseg, bh, 2), PW * 4, 0, stream>>>(a);
+  ssm::grad_kernel<T, N, PW><<<dim3(a.nch, a.nsplit, a.B * a.G), 256, 0, stream>>>(a);
+  if (a.nsplit > 1) {
+    const size_t n = (size_t)a.B * a.G * a.T * (N / 4);
+    ssm::split_sum_kernel<T, N><<<dim3((unsigned)((n + 255) / 256)), 256, 0, stream>>>(a);
+  }
+  if (a.nsl > 1) {
+    const size_t n = (size_t)a.B * a.H * a.T;
+    ssm::ddt_sum_kernel<T><<<dim3((unsigned)((n + 255) / 256)), 256, 0, stream>>>(a);
+  }
+  ssm::head_sum_kernel<T><<<dim3(a.H, 3), 256, 0, stream>>>(a);
+  return launched();
+}
+
+template <class T, int N, int P>
+prism_status ssm_step_p(int B, const SsmStepArgs& a, hipStream_t stream) {
+  ssm::step_kernel<T, N, P><<<dim3((unsigned)((size_t)B * a.H)), 256, 0, stream>>>(a);
+  return launched();
+}
+
+// The entry points of one (type, N): PW in {16, 32, 64}, P in {16, 32, 64, 128}.
+#define PRISM_SSM_UNIT(NAME, T, N)                                                                  \
+  prism_status NAME##_fwd(int pw, const SsmArgs& a, hipStream_t s) {                                \
+    return pw == 16 ? ssm_fwd_pw<T, N, 16>(a, s) : pw == 32 ? ssm_fwd_pw<T, N, 32>(a, s)            \
+                                                            : ssm_fwd_pw<T, N, 64>(a, s);           \
+  }                                                                                                 \
+  prism_status NAME##_bwd(int pw, const SsmArgs& a, hipStream_t s) {                                \
+    return pw == 16 ? ssm_bwd_pw<T, N, 16>(a, s) : pw == 32 ? ssm_bwd_pw<T, N, 32>(a, s)            \
+                                                            : ssm_bwd_pw<T, N, 64>(a, s);           \
+  }                                                                                                 \
+  prism_status NAME##_step(int p, int B, const SsmStepArgs& a, hipStream_t s) {                     \
+    return p == 16 ? ssm_step_p<T, N, 16>(B, a, s) : p == 32 ? ssm_step_p<T, N, 32>(B, a, s)        \
+         : p == 64 ? ssm_step_p<T, N, 64>(B, a, s) : ssm_step_p<T, N, 128>(B, a, s);                \
+  }
+
+}  // namespace host
+}  // namespace prism

@@ -1,0 +1,5 @@
+// ssm_bf16_n16.hip - the state space scan with N = 16 on bf16 tensors
+#include "prism_ssm_launch.h"
+namespace prism { namespace host {
+PRISM_SSM_UNIT(ssm_bf16_n16, bf16_t, 16)
+} }

@@ -438,6 +438,139 @@ prism_status prism_fwd_noalloc(const void* q, const void* k, const void* v,
                                int B, int H, int T, int dk, int dv, int L, int chunk, prism_dtype dt,
                                void* o, float* S_final, hipStream_t stream);
 
+/* ---- The state space layer: causal convolution, selective scan, root-mean-square norm -----
+ *
+ * The recurrence family's member without the delta rule's erase: one scalar decay per head
+ * and token, and write / read vectors that the heads of a group share.  A layer runs
+ * prism_conv_fwd on its projected rows, prism_ssm_fwd on the result and prism_norm_fwd on the
+ * scan's output (or between layers); generation runs prism_conv_step, prism_ssm_step and
+ * prism_norm_fwd.  prism_norm_fwd takes the output o of prism_fwd as well (rows of dv).
+ *
+ * Row strides: the tensors below that come with a `const prism_strides*` are logically
+ * [B, H, T, width] (B batches, H heads or groups, T tokens) with a unit stride in the last
+ * axis and the given element strides of the other three; NULL = dense in that order, as
+ * everywhere above.  So heads of a token-major projection output [B, T, channels] are read
+ * and written in place.  Strides must be positive where their axis is longer than 1; rows of
+ * an output must not overlap.  Ownership, streams and errors as prism_fwd; the stream must
+ * belong to the current device.  Non-finite inputs reach the outputs they enter, except
+ * rows past a sequence's length, which are never read. */
+typedef struct {
+  long long b, h, t;
+} prism_strides;
+
+/* Depthwise causal convolution over the tokens, width K in {2, 3, 4}:
+ *   pre_t = bias[h, :] + sum_{j<K} conv_w[h, j, :] * x_{t-K+1+j},   y_t = silu ? pre_t sigmoid(pre_t) : pre_t
+ *   x       [B, H, T, D] dtype dt, strided;   conv_w [H, K, D] float32;   bias [H, D] float32 or NULL (zero)
+ *   conv_in [B, H, K-1, D] dtype dt: the rows before the first token, oldest first; NULL = zero
+ *   lens    [B] int32 or NULL (= T): tokens of each sequence of a padded batch, clamped to
+ *           0 .. T; y rows past them are left as they were
+ *   y       [B, H, T, D] dtype dt, strided (output)
+ *   conv_out[B, H, K-1, D] dtype dt (output): the last K-1 rows of [conv_in; x up to the length];
+ *           NULL = not written.  May be the same buffer as conv_in.
+ * Any D >= 1; a channel count that is not a multiple of 16 bytes, or a row that does not
+ * start on a 16-byte boundary, takes a narrower path.  Sums in float32. */
+prism_status prism_conv_fwd(const void* x, const prism_strides* x_strides, const float* conv_w, const float* bias,
+                            const void* conv_in, const int* lens, int B, int H, int T, int D, int K, int silu,
+                            prism_dtype dt, void* y, const prism_strides* y_strides, void* conv_out,
+                            hipStream_t stream);
+
+/* Gradients of sum <dy, y> for prism_conv_fwd with conv_in = NULL and lens = NULL:
+ *   dx [B, H, T, D] dtype dt, strided;  dconv_w [H, K, D] and dbias [H, D] float32, summed over
+ *   batches and tokens in a fixed order (dbias may be NULL).  Workspace:
+ *   prism_conv_bwd_workspace_bytes (0 for invalid arguments). */
+size_t prism_conv_bwd_workspace_bytes(int B, int H, int T, int D, int K, prism_dtype dt);
+prism_status prism_conv_bwd(const void* x, const prism_strides* x_strides, const float* conv_w, const float* bias,
+                            const void* dy, const prism_strides* dy_strides,
+                            int B, int H, int T, int D, int K, int silu, prism_dtype dt,
+                            void* dx, const prism_strides* dx_strides, float* dconv_w, float* dbias,
+                            void* workspace, size_t workspace_bytes, hipStream_t stream);
+
+/* One token of the convolution: x, y [B, H, D] (x strided; t of x_strides is not read);
+ * conv_state [B, H, K-1, D] dtype dt, in / out: the previous rows, oldest first. */
+prism_status prism_conv_step(const void* x, const prism_strides* x_strides, const float* conv_w, const float* bias,
+                             int B, int H, int D, int K, int silu, prism_dtype dt, void* conv_state, void* y,
+                             hipStream_t stream);
+
+/* Selective state space scan.  Head h reads group h / (H / G) of Bm and Cm; S_t is N x P:
+ *   d_t = softplus ? log(1 + exp(dt_t + dt_bias_h)) : dt_t + dt_bias_h
+ *   S_t = exp(d_t A_h) S_{t-1} + d_t Bm_t x_t^T,       y_t = S_t^T Cm_t + D_h x_t
+ *   x  [B, H, T, P] dtype ty, strided;   Bm, Cm [B, G, T, N] dtype ty, strided
+ *   dt [B, H, T] float32, strided with a row width of 1;   A [H] float32 (<= 0 for a decay)
+ *   dt_bias, D [H] float32 or NULL (zero)
+ *   S0 [B, H, N, P] float32 or NULL (zero): the state before the first token (the S_final layout
+ *      of prism_fwd with dk = N, dv = P)
+ *   lens [B] int32 or NULL (= T), clamped to 0 .. T: y rows past a length are left as they were
+ *   y  [B, H, T, P] dtype ty, strided (output)
+ *   S_final [B, H, N, P] float32 (output): the state after the last token (S0 for a length of
+ *      0).  May be the same buffer as S0.
+ * Supported: N, P in {16, 32, 64, 128}; H a multiple of G; B * H * P / min(P, 64) <= 65535; rows
+ * of x, Bm, Cm and y that start on 16-byte boundaries (else PRISM_ERR_UNSUPPORTED).
+ * Precision: decays and states in float32 from log decays summed in float64.  With PRISM_BF16
+ * the products run on bfloat16 operands; what enters the state is split into bfloat16 parts
+ * that keep its float32 digits, the score matrix and the state's readout are rounded once.
+ * Workspace: prism_ssm_fwd_workspace_bytes (0 for invalid or unsupported arguments). */
+size_t prism_ssm_fwd_workspace_bytes(int B, int H, int G, int T, int N, int P, prism_dtype ty);
+prism_status prism_ssm_fwd(const void* x, const prism_strides* x_strides, const void* Bm,
+                           const prism_strides* b_strides, const void* Cm, const prism_strides* c_strides,
+                           const float* dt, const prism_strides* dt_strides, const float* dt_bias, const float* A,
+                           const float* D, const float* S0, const int* lens,
+                           int B, int H, int G, int T, int N, int P, int softplus, prism_dtype ty,
+                           void* y, const prism_strides* y_strides, float* S_final,
+                           void* workspace, size_t workspace_bytes, hipStream_t stream);
+
+/* Gradients of sum <dy, y> + <dS_final, S_final> for prism_ssm_fwd with S0 = NULL, lens = NULL:
+ *   dy [B, H, T, P] dtype ty, strided;   dS_final [B, H, N, P] float32 or NULL (zero)
+ *   dx [B, H, T, P], dBm, dCm [B, G, T, N] dtype ty, strided (dBm, dCm: summed over the group's heads
+ *   in float32);  ddt [B, H, T] float32, dense;  dA [H], and dD, ddt_bias [H] (NULL = not wanted),
+ *   float32, summed over batches and tokens.  Every sum has a fixed order.
+ * Supported and precision as prism_ssm_fwd.  Workspace: prism_ssm_bwd_workspace_bytes. */
+size_t prism_ssm_bwd_workspace_bytes(int B, int H, int G, int T, int N, int P, prism_dtype ty);
+prism_status prism_ssm_bwd(const void* x, const prism_strides* x_strides, const void* Bm,
+                           const prism_strides* b_strides, const void* Cm, const prism_strides* c_strides,
+                           const float* dt, const prism_strides* dt_strides, const float* dt_bias, const float* A,
+                           const float* D, const void* dy, const prism_strides* dy_strides, const float* dS_final,
+                           int B, int H, int G, int T, int N, int P, int softplus, prism_dtype ty,
+                           void* dx, const prism_strides* dx_strides, void* dBm, const prism_strides* db_strides,
+                           void* dCm, const prism_strides* dc_strides, float* ddt, float* dA, float* dD,
+                           float* ddt_bias, void* workspace, size_t workspace_bytes, hipStream_t stream);
+
+/* One token of the scan, the state S [B, H, N, P] float32 updated in place: x [B, H, P], Bm, Cm
+ * [B, G, N] (strided; t is not read), dt [B, H] float32 (strided), y [B, H, P] dense. */
+prism_status prism_ssm_step(const void* x, const prism_strides* x_strides, const void* Bm,
+                            const prism_strides* b_strides, const void* Cm, const prism_strides* c_strides,
+                            const float* dt, const prism_strides* dt_strides, const float* dt_bias, const float* A,
+                            const float* D, int B, int H, int G, int N, int P, int softplus, prism_dtype ty,
+                            float* S, void* y, hipStream_t stream);
+
+/* Root-mean-square norm of rows of D values, with the residual's addition before it, an output
+ * gate and an 8-bit output:
+ *   h = x + residual,   y = h / sqrt(mean(h^2) + eps) * weight * gate sigmoid(gate)
+ *   x, gate [rows, D] dtype dt with row strides x_stride and gate_stride (elements, >= D);
+ *   residual [rows, D] dtype dt, dense;  residual and gate may be NULL (left out);  weight [D]
+ *   float32 or NULL (ones)
+ *   y      [rows, D] dense: dtype dt, or with scales != NULL OCP e4m3 bytes
+ *   scales [rows, ceil(D / 128)] float32: y = byte value * scale, scale = (the largest |y| of the 128
+ *          values) / 448, or 1 where all are 0.  A block with a non-finite y has a scale of
+ *          infinity or NaN and bytes of NaN.
+ *   h_out  [rows, D] dtype dt, dense, or NULL: h rounded (the norm uses it unrounded).  May be the
+ *          same buffer as residual, or as a dense x.
+ * Any D >= 1 and rows >= 1 (unaligned rows take a narrower path).  Statistics in float32. */
+prism_status prism_norm_fwd(const void* x, long long x_stride, const void* residual, const float* weight,
+                            const void* gate, long long gate_stride, int rows, int D, float eps, prism_dtype dt,
+                            void* y, float* scales, void* h_out, hipStream_t stream);
+
+/* Gradients of sum <dy, y> + <dh_in, h> for prism_norm_fwd in dtype dt:
+ *   h [rows, D] (row stride h_stride): the row that was normalised;  dy [rows, D] dense;
+ *   dh_in [rows, D] dense or NULL: the gradient that reaches h from the residual stream
+ *   dh [rows, D] dtype dt, dense (the gradient of x and of residual alike; may be dh_in's buffer);
+ *   dgate [rows, D] dtype dt, dense (required with gate);  dweight [D] float32, summed over the
+ *   rows in a fixed order (NULL = not wanted).  Workspace: prism_norm_bwd_workspace_bytes. */
+size_t prism_norm_bwd_workspace_bytes(int rows, int D, prism_dtype dt);
+prism_status prism_norm_bwd(const void* h, long long h_stride, const float* weight, const void* gate,
+                            long long gate_stride, const void* dy, const void* dh_in, int rows, int D, float eps,
+                            prism_dtype dt, void* dh, void* dgate, float* dweight,
+                            void* workspace, size_t workspace_bytes, hipStream_t stream);
+
 /* A static, human-readable name of a status code. */
 const char* prism_status_string(prism_status s);
 

@@ -7,27 +7,36 @@ namespace {
 
 prism_status launched() { return hipGetLastError() == hipSuccess ? PRISM_OK : PRISM_ERR_HIP; }
 
-template <class T, int V>
-dim3 strip_grid(const ConvArgs& a) {
+// V channels per thread.
+dim3 strip_grid(const ConvArgs& a, int V) {
   const int cols = (a.D + V - 1) / V;
   return dim3((cols + 63) / 64, (a.nstrip + 3) / 4, a.B * a.H);
 }
 
+template <class T, int K, bool SILU>
+void fwd_act(bool wide, const ConvArgs& a, hipStream_t s) {
+  constexpr int V = 16 / sizeof(T);
+  if (wide) conv::fwd_kernel<T, K, V, 8, SILU><<<strip_grid(a, V), 256, 0, s>>>(a);
+  else conv::fwd_kernel<T, K, 1, 8, SILU><<<strip_grid(a, 1), 256, 0, s>>>(a);
+}
 template <class T, int K>
 prism_status fwd(bool wide, const ConvArgs& a, hipStream_t s) {
-  constexpr int V = 16 / sizeof(T);
-  if (wide) conv::fwd_kernel<T, K, V><<<strip_grid<T, V>(a), 256, 0, s>>>(a);
-  else conv::fwd_kernel<T, K, 1><<<strip_grid<T, 1>(a), 256, 0, s>>>(a);
-  if (a.conv_out != nullptr) conv::tail_kernel<T, K><<<dim3((a.D + 255) / 256, a.B * a.H), 256, 0, s>>>(a);
+  if (a.silu) fwd_act<T, K, true>(wide, a, s);
+  else fwd_act<T, K, false>(wide, a, s);
   return launched();
 }
 
+template <class T, int K, bool SILU>
+void bwd_act(bool wide, const ConvArgs& a, hipStream_t s) {
+  constexpr int V = 4;
+  if (wide) conv::bwd_kernel<T, K, V, 4, SILU><<<strip_grid(a, V), 256, 0, s>>>(a);
+  else conv::bwd_kernel<T, K, 1, 4, SILU><<<strip_grid(a, 1), 256, 0, s>>>(a);
+}
 template <class T, int K>
 prism_status bwd(bool wide, const ConvArgs& a, hipStream_t s) {
-  constexpr int V = 16 / sizeof(T);
-  if (wide) conv::bwd_kernel<T, K, V><<<strip_grid<T, V>(a), 256, 0, s>>>(a);
-  else conv::bwd_kernel<T, K, 1><<<strip_grid<T, 1>(a), 256, 0, s>>>(a);
-  conv::wsum_kernel<K><<<dim3((a.D + 63) / 64, K + 1, a.H), 256, 0, s>>>(a);
+  if (a.silu) bwd_act<T, K, true>(wide, a, s);
+  else bwd_act<T, K, false>(wide, a, s);
+  conv::wsum_kernel<K><<<dim3((a.D + 31) / 32, K + 1, a.H), 1024, 0, s>>>(a);
   return launched();
 }
 

@@ -170,13 +170,13 @@ prism_status conv_check(int B, int H, int T, int D, int K, prism_dtype dt) {
   return PRISM_OK;
 }
 
-// Tokens per thread: long strips read their K - 1 border rows (and, backward, keep their shares of dw) once for
+// Tokens per thread: long strips read their K - 1 border rows (and, backward, leave their shares of dw) once for
 // more tokens, short ones fill the device when there are few channels.
 int conv_strip(int B, int H, int T, int D, prism_dtype dt, bool bwd) {
-  const size_t cols = (size_t)B * H * (((size_t)D * elem(dt) + 15) / 16);
-  int strip = bwd ? 128 : 32;
-  while (strip > 8 && cols * (((size_t)T + strip - 1) / strip) < 4 * 64 * kCUs) strip /= 2;
-  // strips map to grid.y
+  const size_t per = bwd ? 4 : 16 / elem(dt), cols = (size_t)B * H * (((size_t)D + per - 1) / per);
+  int strip = bwd ? 64 : 32;
+  while (strip > 8 && cols * (((size_t)T + strip - 1) / strip) < (bwd ? 8 : 16) * 64 * kCUs) strip /= 2;
+  // workgroups of four strips map to grid.y
   while (((size_t)T + strip - 1) / strip / 4 + 1 > 65535) strip *= 2;
   return strip;
 }
@@ -302,7 +302,7 @@ size_t prism_conv_bwd_workspace_bytes(int B, int H, int T, int D, int K, prism_d
   if (conv_check(B, H, T, D, K, dt) != PRISM_OK) return 0;
   const int strip = conv_strip(B, H, T, D, dt, true);
   Layout ly;
-  ly.add((size_t)B * (((size_t)T + strip - 1) / strip) * H * (K + 1), (size_t)D * 4);
+  ly.add((size_t)B * (((size_t)T + 4 * strip - 1) / (4 * strip)) * H * (K + 1), (size_t)D * 4);  // one share per four strips
   return ly.ok() ? ly.total : 0;
 }
 
@@ -352,6 +352,13 @@ static prism_status norm_check(int rows, int D, long long xs, const void* gate, 
   return PRISM_OK;
 }
 
+// Whether rows of D values at p (NULL: not there) can be kept in registers in 16-byte pieces: whole pieces, aligned, up
+// to 1024 of them (16 KB).
+static bool row16(int D, const void* p, long long stride, prism_dtype dt) {
+  const size_t e = elem(dt);
+  return D * e % 16 == 0 && D * e <= 16384 && (p == nullptr || (aligned16(p) && stride * e % 16 == 0));
+}
+
 prism_status prism_norm_fwd(const void* x, long long x_stride, const void* residual, const float* weight,
                             const void* gate, long long gate_stride, int rows, int D, float eps, prism_dtype dt,
                             void* y, float* scales, void* h_out, hipStream_t stream) {
@@ -361,11 +368,13 @@ prism_status prism_norm_fwd(const void* x, long long x_stride, const void* resid
   NormArgs a = {};
   a.x = x, a.xs = x_stride, a.residual = residual, a.w = weight, a.gate = gate, a.gs = gate_stride;
   a.rows = rows, a.D = D, a.eps = eps, a.y = y, a.scales = scales, a.h = h_out;
-  return host::launch_norm_fwd(dt, false, a, stream);
+  const bool one_read = row16(D, x, x_stride, dt) && row16(D, residual, D, dt) && row16(D, gate, gate_stride, dt) &&
+                        row16(D, y, D, dt) && row16(D, h_out, D, dt);
+  return host::launch_norm_fwd(dt, one_read, a, stream);
 }
 
 // Workgroups of the backward: each sums its rows' share of dweight before the shares are joined.
-static int norm_blocks(int rows) { return (int)std::min<size_t>(rows, 2 * kCUs); }
+static int norm_blocks(int rows) { return (int)std::min<size_t>(rows, 4 * kCUs); }
 
 size_t prism_norm_bwd_workspace_bytes(int rows, int D, prism_dtype dt) {
   if (norm_check(rows, D, D, nullptr, 0, 0.f, dt) != PRISM_OK) return 0;
@@ -388,7 +397,9 @@ prism_status prism_norm_bwd(const void* h, long long h_stride, const float* weig
   a.x = h, a.xs = h_stride, a.w = weight, a.gate = gate, a.gs = gate_stride, a.dy = dy, a.dh_in = dh_in;
   a.rows = rows, a.D = D, a.eps = eps, a.h = dh, a.dgate = dgate;
   a.part = reinterpret_cast<float*>(workspace), a.nblk = norm_blocks(rows), a.dw = dweight;
-  return host::launch_norm_bwd(dt, false, a, stream);
+  const bool one_read = row16(D, h, h_stride, dt) && row16(D, gate, gate_stride, dt) && row16(D, dy, D, dt) &&
+                        row16(D, dh_in, D, dt) && row16(D, dh, D, dt) && row16(D, dgate, D, dt);
+  return host::launch_norm_bwd(dt, one_read, a, stream);
 }
 
 }  // extern "C"

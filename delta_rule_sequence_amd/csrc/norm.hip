@@ -7,22 +7,47 @@ namespace {
 
 prism_status launched() { return hipGetLastError() == hipSuccess ? PRISM_OK : PRISM_ERR_HIP; }
 
+template <class T, int TPR, int NV>
+void fwd_row(const NormArgs& a, hipStream_t s) {
+  constexpr int RPB = 256 / TPR;
+  norm::fwd_row_kernel<T, TPR, NV><<<dim3((a.rows + RPB - 1) / RPB), 256, 0, s>>>(a);
+}
+template <class T, int TPR, int NV>
+void bwd_row(const NormArgs& a, hipStream_t s) {
+  if (a.gate != nullptr) norm::bwd_row_kernel<T, TPR, NV, true><<<dim3(a.nblk), 256, 0, s>>>(a);
+  else norm::bwd_row_kernel<T, TPR, NV, false><<<dim3(a.nblk), 256, 0, s>>>(a);
+}
+
+// Lanes and pieces of a row of n 16-byte pieces: a part of a wave up to 32 pieces, a wave up to 256, else the workgroup.
+#define PRISM_NORM_ROWS(F, n)                                                                          \
+  ((n) <= 8 ? F<T, 8, 1>(a, s) : (n) <= 16 ? F<T, 16, 1>(a, s) : (n) <= 32 ? F<T, 32, 1>(a, s)         \
+   : (n) <= 64 ? F<T, 64, 1>(a, s) : (n) <= 128 ? F<T, 64, 2>(a, s) : (n) <= 192 ? F<T, 64, 3>(a, s)   \
+   : (n) <= 256 ? F<T, 64, 4>(a, s) : (n) <= 512 ? F<T, 256, 2>(a, s) : (n) <= 768 ? F<T, 256, 3>(a, s) \
+   : F<T, 256, 4>(a, s))
+
 template <class T>
-prism_status bwd(const NormArgs& a, hipStream_t s) {
-  norm::bwd_kernel<T><<<dim3(a.nblk), 256, 0, s>>>(a);
-  if (a.dw != nullptr) norm::wsum_kernel<<<dim3((a.D + 63) / 64), 256, 0, s>>>(a);
+prism_status fwd(bool rows, const NormArgs& a, hipStream_t s) {
+  const int n = a.D / norm::Piece<T>::V;
+  if (rows) PRISM_NORM_ROWS(fwd_row, n);
+  else norm::fwd_any_kernel<T><<<dim3(a.rows), 256, 0, s>>>(a);
+  return launched();
+}
+template <class T>
+prism_status bwd(bool rows, const NormArgs& a, hipStream_t s) {
+  const int n = a.D / norm::Piece<T>::V;
+  if (rows) PRISM_NORM_ROWS(bwd_row, n);
+  else norm::bwd_any_kernel<T><<<dim3(a.nblk), 256, 0, s>>>(a);
+  if (a.dw != nullptr) norm::wsum_kernel<<<dim3((a.D + 31) / 32), 1024, 0, s>>>(a);
   return launched();
 }
 
 }  // namespace
 
-prism_status launch_norm_fwd(prism_dtype dt, bool, const NormArgs& a, hipStream_t s) {
-  if (dt == PRISM_BF16) norm::fwd_kernel<bf16_t><<<dim3(a.rows), 256, 0, s>>>(a);
-  else norm::fwd_kernel<float><<<dim3(a.rows), 256, 0, s>>>(a);
-  return launched();
+prism_status launch_norm_fwd(prism_dtype dt, bool rows, const NormArgs& a, hipStream_t s) {
+  return dt == PRISM_BF16 ? fwd<bf16_t>(rows, a, s) : fwd<float>(rows, a, s);
 }
-prism_status launch_norm_bwd(prism_dtype dt, bool, const NormArgs& a, hipStream_t s) {
-  return dt == PRISM_BF16 ? bwd<bf16_t>(a, s) : bwd<float>(a, s);
+prism_status launch_norm_bwd(prism_dtype dt, bool rows, const NormArgs& a, hipStream_t s) {
+  return dt == PRISM_BF16 ? bwd<bf16_t>(rows, a, s) : bwd<float>(rows, a, s);
 }
 
 }  // namespace host

@@ -17,12 +17,9 @@ template <class T, int V> struct Vec { typedef T type __attribute__((ext_vector_
 template <class T> struct Vec<T, 1> { typedef T type; };
 
 template <class T, int V>
-__device__ __forceinline__ void load_v(float (&o)[V], const T* p) {
-  const auto v = *reinterpret_cast<const typename Vec<T, V>::type*>(p);
-  if constexpr (V == 1) o[0] = (float)v;
-  else
-#pragma unroll
-    for (int k = 0; k < V; ++k) o[k] = (float)v[k];
+__device__ __forceinline__ float elem(const typename Vec<T, V>::type& v, int k) {
+  if constexpr (V == 1) return (float)v;
+  else return (float)v[k];
 }
 template <class T, int V>
 __device__ __forceinline__ void store_v(T* p, const float (&o)[V]) {
@@ -34,7 +31,36 @@ __device__ __forceinline__ void store_v(T* p, const float (&o)[V]) {
   *reinterpret_cast<typename Vec<T, V>::type*>(p) = v;
 }
 
-__device__ __forceinline__ float sigmoid_f(float z) { return 1.f / (1.f + expf(-z)); }
+// V weights of one channel group in 16-byte loads (any 4-byte alignment).
+template <int V>
+__device__ __forceinline__ void load_w(float (&o)[V], const float* p) {
+  typedef float f4 __attribute__((ext_vector_type(4), aligned(4)));
+  if constexpr (V == 1) {
+    o[0] = *p;
+  } else {
+#pragma unroll
+    for (int k = 0; k < V; k += 4) {
+      const f4 v = *reinterpret_cast<const f4*>(p + k);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) o[k + e] = v[e];
+    }
+  }
+}
+// The filter and bias of channels d .. d + V - 1.
+template <int K, int V>
+__device__ __forceinline__ void load_filter(float (&w)[K][V], float (&bias)[V], const ConvArgs& a, int h, int d) {
+#pragma unroll
+  for (int j = 0; j < K; ++j) load_w<V>(w[j], a.w + ((size_t)h * K + j) * a.D + d);
+  if (a.bias != nullptr) {
+    load_w<V>(bias, a.bias + (size_t)h * a.D + d);
+  } else {
+#pragma unroll
+    for (int k = 0; k < V; ++k) bias[k] = 0.f;
+  }
+}
+
+// From the hardware exponential and reciprocal (1 ulp each).
+__device__ __forceinline__ float sigmoid_f(float z) { return __builtin_amdgcn_rcpf(1.f + __expf(-z)); }
 
 __device__ __forceinline__ int seq_len(const ConvArgs& a, int b) {
   if (a.lens == nullptr) return a.T;
@@ -42,158 +68,175 @@ __device__ __forceinline__ int seq_len(const ConvArgs& a, int b) {
   return n < 0 ? 0 : (n > a.T ? a.T : n);
 }
 
-// Row t of the sequence as floats: before 0 from the history (zero without one).
+// Row t of the sequence: before 0 from the history (zero without one).
 template <class T, int K, int V>
-__device__ __forceinline__ void row(float (&o)[V], const ConvArgs& a, int b, int h, int t, int d) {
-  if (t >= 0) {
-    load_v<T, V>(o, reinterpret_cast<const T*>(a.x) + b * a.xs.b + h * a.xs.h + (long long)t * a.xs.t + d);
-  } else if (a.conv_in != nullptr) {
-    load_v<T, V>(o, reinterpret_cast<const T*>(a.conv_in) + ((size_t)(b * a.H + h) * (K - 1) + t + K - 1) * a.D + d);
-  } else {
-#pragma unroll
-    for (int k = 0; k < V; ++k) o[k] = 0.f;
-  }
+__device__ __forceinline__ typename Vec<T, V>::type row(const ConvArgs& a, int b, int h, int t, int d) {
+  typedef typename Vec<T, V>::type vec;
+  if (t >= 0) return *reinterpret_cast<const vec*>(reinterpret_cast<const T*>(a.x) + b * a.xs.b + h * a.xs.h + (long long)t * a.xs.t + d);
+  if (a.conv_in == nullptr) return vec(0);
+  return *reinterpret_cast<const vec*>(reinterpret_cast<const T*>(a.conv_in) + ((size_t)(b * a.H + h) * (K - 1) + t + K - 1) * a.D + d);
 }
 
-// Grid (channel blocks, strips, B * H).  The workgroup that holds a sequence's last row also writes conv_out.
-template <class T, int K, int V>
+// Grid (channel blocks of 64 threads, strips / 4, B * H).  Rows are loaded U at a time, so that a thread keeps U 16-byte loads in
+// flight.  The first strip's threads also write conv_out: they alone read the history, so it may be the same buffer.
+template <class T, int K, int V, int U, bool SILU>
 __global__ __launch_bounds__(256) void fwd_kernel(ConvArgs a) {
-  const int d = (blockIdx.x * 64 + threadIdx.x % 64) * V, strip = blockIdx.y * 4 + threadIdx.x / 64;
+  typedef typename Vec<T, V>::type vec;
+  const int d = (blockIdx.x * 64 + threadIdx.x % 64) * V;
+  const int strip = blockIdx.y * 4 + __builtin_amdgcn_readfirstlane(threadIdx.x / 64);  // one strip per wave
   const int bh = blockIdx.z, b = bh / a.H, h = bh % a.H;
   if (d >= a.D || strip >= a.nstrip) return;
   const int len = seq_len(a, b), t0 = strip * a.strip, t1 = min(t0 + a.strip, len);
-  float w[K][V], bias[V], x[K][V];
-#pragma unroll
-  for (int j = 0; j < K; ++j)
-#pragma unroll
-    for (int k = 0; k < V; ++k) w[j][k] = a.w[((size_t)h * K + j) * a.D + d + k];
-#pragma unroll
-  for (int k = 0; k < V; ++k) bias[k] = a.bias != nullptr ? a.bias[(size_t)h * a.D + d + k] : 0.f;
   if (t0 < t1) {
+    float w[K][V], bias[V], x[K][V];
+    load_filter<K, V>(w, bias, a, h, d);
 #pragma unroll
-    for (int j = 0; j < K - 1; ++j) row<T, K, V>(x[j + 1], a, b, h, t0 - K + 1 + j, d);
-  }
-  T* y = reinterpret_cast<T*>(a.y) + b * a.ys.b + h * a.ys.h + d;
-  for (int t = t0; t < t1; ++t) {
+    for (int j = 0; j < K - 1; ++j) {
+      const vec v = row<T, K, V>(a, b, h, t0 - K + 1 + j, d);
 #pragma unroll
-    for (int j = 0; j < K - 1; ++j)
-#pragma unroll
-      for (int k = 0; k < V; ++k) x[j][k] = x[j + 1][k];
-    row<T, K, V>(x[K - 1], a, b, h, t, d);
-    float o[V];
-#pragma unroll
-    for (int k = 0; k < V; ++k) {
-      float s = bias[k];
-#pragma unroll
-      for (int j = 0; j < K; ++j) s += w[j][k] * x[j][k];
-      o[k] = a.silu ? s * sigmoid_f(s) : s;
+      for (int k = 0; k < V; ++k) x[j + 1][k] = elem<T, V>(v, k);
     }
-    store_v<T, V>(y + (long long)t * a.ys.t, o);
-  }
-}
-
-// conv_out: rows len - K + 1 .. len - 1 of [conv_in; x].  Each thread reads its channel's rows before it writes,
-// so conv_out may be conv_in.  Grid (channels / 256, B * H).
-template <class T, int K>
-__global__ __launch_bounds__(256) void tail_kernel(ConvArgs a) {
-  const int d = blockIdx.x * 256 + threadIdx.x, bh = blockIdx.y, b = bh / a.H, h = bh % a.H;
-  if (d >= a.D) return;
-  const int len = seq_len(a, b);
-  float v[K - 1][1];
+    const T* xp = reinterpret_cast<const T*>(a.x) + b * a.xs.b + h * a.xs.h + d;
+    T* y = reinterpret_cast<T*>(a.y) + b * a.ys.b + h * a.ys.h + d;
+    for (int t = t0; t < t1; t += U) {
+      vec in[U];
 #pragma unroll
-  for (int j = 0; j < K - 1; ++j) row<T, K, 1>(v[j], a, b, h, len - K + 1 + j, d);
-  T* o = reinterpret_cast<T*>(a.conv_out) + (size_t)bh * (K - 1) * a.D + d;
+      for (int u = 0; u < U; ++u) in[u] = *reinterpret_cast<const vec*>(xp + (long long)min(t + u, t1 - 1) * a.xs.t);
 #pragma unroll
-  for (int j = 0; j < K - 1; ++j) o[(size_t)j * a.D] = (T)v[j][0];
-}
-
-// Grid as fwd_kernel.  A strip's thread forms g for its tokens and the K - 1 after them (their dx reach back), and
-// the strip's shares of dw and dbias.
-template <class T, int K, int V>
-__global__ __launch_bounds__(256) void bwd_kernel(ConvArgs a) {
-  const int d = (blockIdx.x * 64 + threadIdx.x % 64) * V, strip = blockIdx.y * 4 + threadIdx.x / 64;
-  const int bh = blockIdx.z, b = bh / a.H, h = bh % a.H;
-  if (d >= a.D || strip >= a.nstrip) return;
-  const int t0 = strip * a.strip, t1 = min(t0 + a.strip, a.T);
-  float w[K][V], bias[V], x[K][V], g[K][V], dw[K][V], db[V];
-#pragma unroll
-  for (int j = 0; j < K; ++j)
-#pragma unroll
-    for (int k = 0; k < V; ++k) w[j][k] = a.w[((size_t)h * K + j) * a.D + d + k];
-#pragma unroll
-  for (int k = 0; k < V; ++k) {
-    bias[k] = a.bias != nullptr ? a.bias[(size_t)h * a.D + d + k] : 0.f;
-    db[k] = 0.f;
-#pragma unroll
-    for (int j = 0; j < K; ++j) dw[j][k] = g[j][k] = 0.f;
-  }
-#pragma unroll
-  for (int j = 0; j < K - 1; ++j) row<T, K, V>(x[j + 1], a, b, h, t0 - K + 1 + j, d);
-  const T* dy = reinterpret_cast<const T*>(a.dy) + b * a.dys.b + h * a.dys.h + d;
-  T* dx = reinterpret_cast<T*>(a.y) + b * a.ys.b + h * a.ys.h + d;
-  for (int t = t0; t < t1 + K - 1; ++t) {
-    float gy[V];
-#pragma unroll
-    for (int j = 0; j < K - 1; ++j)
-#pragma unroll
-      for (int k = 0; k < V; ++k) {
-        x[j][k] = x[j + 1][k];
-        g[j][k] = g[j + 1][k];
-      }
-    if (t < a.T) {
-      row<T, K, V>(x[K - 1], a, b, h, t, d);
-      load_v<T, V>(gy, dy + (long long)t * a.dys.t);
-#pragma unroll
-      for (int k = 0; k < V; ++k) {
-        float s = bias[k];
-#pragma unroll
-        for (int j = 0; j < K; ++j) s += w[j][k] * x[j][k];
-        const float sg = sigmoid_f(s);
-        g[K - 1][k] = a.silu ? gy[k] * (sg * (1.f + s * (1.f - sg))) : gy[k];
-      }
-      if (t < t1) {
+      for (int u = 0; u < U; ++u) {
+        if (t + u >= t1) break;
+        float o[V];
 #pragma unroll
         for (int k = 0; k < V; ++k) {
-          db[k] += g[K - 1][k];
 #pragma unroll
-          for (int j = 0; j < K; ++j) dw[j][k] += x[j][k] * g[K - 1][k];
+          for (int j = 0; j < K - 1; ++j) x[j][k] = x[j + 1][k];
+          x[K - 1][k] = elem<T, V>(in[u], k);
+          float s = bias[k];
+#pragma unroll
+          for (int j = 0; j < K; ++j) s += w[j][k] * x[j][k];
+          o[k] = SILU ? s * sigmoid_f(s) : s;
         }
+        store_v<T, V>(y + (long long)(t + u) * a.ys.t, o);
       }
-    } else {
-#pragma unroll
-      for (int k = 0; k < V; ++k) g[K - 1][k] = 0.f;
-    }
-    if (t - K + 1 >= t0) {  // g[j] is g_{t-K+1+j}: dx_{t-K+1} = sum_j w_{K-1-j} g[j]
-      float o[V];
-#pragma unroll
-      for (int k = 0; k < V; ++k) {
-        o[k] = 0.f;
-#pragma unroll
-        for (int j = 0; j < K; ++j) o[k] += w[K - 1 - j][k] * g[j][k];
-      }
-      store_v<T, V>(dx + (long long)(t - K + 1) * a.ys.t, o);
     }
   }
-  float* part = a.part + (((size_t)b * a.nstrip + strip) * a.H + h) * (K + 1) * a.D + d;
+  if (strip == 0 && a.conv_out != nullptr) {  // rows len - K + 1 .. len - 1 of [conv_in; x]
+    vec tail[K - 1];
 #pragma unroll
-  for (int j = 0; j < K; ++j) store_v<float, V>(part + (size_t)j * a.D, dw[j]);
-  store_v<float, V>(part + (size_t)K * a.D, db);
+    for (int j = 0; j < K - 1; ++j) tail[j] = row<T, K, V>(a, b, h, len - K + 1 + j, d);
+    T* o = reinterpret_cast<T*>(a.conv_out) + (size_t)bh * (K - 1) * a.D + d;
+#pragma unroll
+    for (int j = 0; j < K - 1; ++j) *reinterpret_cast<vec*>(o + (size_t)j * a.D) = tail[j];
+  }
 }
 
-// dw and dbias: the strips' shares summed in a fixed order.  Grid (channels / 64, (K + 1) rows, H); the four waves take a
-// quarter of the shares each.
+// Grid as fwd_kernel.  A strip's thread forms g for its tokens and the K - 1 after them (their dx reach back), and the
+// strip's shares of dw and dbias, which the workgroup's four strips join in LDS.
+template <class T, int K, int V, int U, bool SILU>
+__global__ __launch_bounds__(256) void bwd_kernel(ConvArgs a) {
+  typedef typename Vec<T, V>::type vec;
+  __shared__ float sum[4][V][64];
+  const int lane = threadIdx.x % 64, q = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);  // one strip per wave
+  const int d = (blockIdx.x * 64 + lane) * V, strip = blockIdx.y * 4 + q;
+  const int bh = blockIdx.z, b = bh / a.H, h = bh % a.H;
+  float dw[K + 1][V];
+#pragma unroll
+  for (int j = 0; j <= K; ++j)
+#pragma unroll
+    for (int k = 0; k < V; ++k) dw[j][k] = 0.f;
+  if (d < a.D && strip < a.nstrip) {
+    const int t0 = strip * a.strip, t1 = min(t0 + a.strip, a.T), te = t1 + K - 1;
+    float w[K][V], bias[V], x[K][V], g[K][V];
+    load_filter<K, V>(w, bias, a, h, d);
+#pragma unroll
+    for (int j = 0; j < K; ++j)
+#pragma unroll
+      for (int k = 0; k < V; ++k) g[j][k] = 0.f;
+#pragma unroll
+    for (int j = 0; j < K - 1; ++j) {
+      const vec v = row<T, K, V>(a, b, h, t0 - K + 1 + j, d);
+#pragma unroll
+      for (int k = 0; k < V; ++k) x[j + 1][k] = elem<T, V>(v, k);
+    }
+    const T* xp = reinterpret_cast<const T*>(a.x) + b * a.xs.b + h * a.xs.h + d;
+    const T* dy = reinterpret_cast<const T*>(a.dy) + b * a.dys.b + h * a.dys.h + d;
+    T* dx = reinterpret_cast<T*>(a.y) + b * a.ys.b + h * a.ys.h + d;
+    for (int t = t0; t < te; t += U) {
+      vec in[U], gy[U];
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        const int tt = min(t + u, a.T - 1);
+        in[u] = *reinterpret_cast<const vec*>(xp + (long long)tt * a.xs.t);
+        gy[u] = *reinterpret_cast<const vec*>(dy + (long long)tt * a.dys.t);
+      }
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        const int tt = t + u;
+        if (tt >= te) break;
+        const bool real = tt < a.T, own = tt < t1;
+        float o[V];
+#pragma unroll
+        for (int k = 0; k < V; ++k) {
+#pragma unroll
+          for (int j = 0; j < K - 1; ++j) {
+            x[j][k] = x[j + 1][k];
+            g[j][k] = g[j + 1][k];
+          }
+          x[K - 1][k] = elem<T, V>(in[u], k);
+          float gk = real ? elem<T, V>(gy[u], k) : 0.f;
+          if constexpr (SILU) {
+            float s = bias[k];
+#pragma unroll
+            for (int j = 0; j < K; ++j) s += w[j][k] * x[j][k];
+            const float sg = sigmoid_f(s);
+            gk = real ? gk * (sg * (1.f + s * (1.f - sg))) : 0.f;
+          }
+          g[K - 1][k] = gk;
+          const float gown = own ? gk : 0.f;
+          dw[K][k] += gown;
+#pragma unroll
+          for (int j = 0; j < K; ++j) dw[j][k] += x[j][k] * gown;
+          // g[j] is g_{tt-K+1+j}: dx_{tt-K+1} = sum_j w_{K-1-j} g[j]
+          o[k] = 0.f;
+#pragma unroll
+          for (int j = 0; j < K; ++j) o[k] += w[K - 1 - j][k] * g[j][k];
+        }
+        if (tt - K + 1 >= t0) store_v<T, V>(dx + (long long)(tt - K + 1) * a.ys.t, o);
+      }
+    }
+  }
+  float* part = a.part + (((size_t)b * gridDim.y + blockIdx.y) * a.H + h) * (K + 1) * a.D;
+#pragma unroll
+  for (int j = 0; j <= K; ++j) {
+    __syncthreads();
+#pragma unroll
+    for (int k = 0; k < V; ++k) sum[q][k][lane] = dw[j][k];
+    __syncthreads();
+    for (int i = threadIdx.x; i < 64 * V; i += 256) {
+      const int col = blockIdx.x * 64 * V + i, k = i % V, ln = i / V;
+      if (col < a.D) part[(size_t)j * a.D + col] = (sum[0][k][ln] + sum[1][k][ln]) + (sum[2][k][ln] + sum[3][k][ln]);
+    }
+  }
+}
+
+// dw and dbias: the workgroups' shares summed in a fixed order.  Grid (channels / 32, (K + 1) rows, H), 32 lanes down the
+// shares of a channel.
 template <int K>
-__global__ __launch_bounds__(256) void wsum_kernel(ConvArgs a) {
-  const int d = blockIdx.x * 64 + threadIdx.x % 64, j = blockIdx.y, h = blockIdx.z, q = threadIdx.x / 64;
-  const int n = a.B * a.nstrip;
-  __shared__ double part[4][64];
+__global__ __launch_bounds__(1024) void wsum_kernel(ConvArgs a) {
+  const int d = blockIdx.x * 32 + threadIdx.x % 32, j = blockIdx.y, h = blockIdx.z, q = threadIdx.x / 32;
+  const int n = a.B * ((a.nstrip + 3) / 4);
+  __shared__ double part[32][33];
   double s = 0.0;
-  if (d < a.D)
-    for (int k = q; k < n; k += 4) s += (double)a.part[(((size_t)k * a.H + h) * (K + 1) + j) * a.D + d];
-  part[q][threadIdx.x % 64] = s;
+  if (d < a.D) {
+#pragma unroll 4
+    for (int k = q; k < n; k += 32) s += (double)a.part[(((size_t)k * a.H + h) * (K + 1) + j) * a.D + d];
+  }
+  part[q][threadIdx.x % 32] = s;
   __syncthreads();
   if (q != 0 || d >= a.D) return;
-  s = (part[0][threadIdx.x] + part[1][threadIdx.x]) + (part[2][threadIdx.x] + part[3][threadIdx.x]);
+  s = 0.0;
+#pragma unroll
+  for (int k = 0; k < 32; ++k) s += part[k][threadIdx.x];
   if (j < K) a.dw[((size_t)h * K + j) * a.D + d] = (float)s;
   else if (a.dbias != nullptr) a.dbias[(size_t)h * a.D + d] = (float)s;
 }

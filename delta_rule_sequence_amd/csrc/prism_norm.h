@@ -33,15 +33,18 @@ __device__ __forceinline__ unsigned wave_max_bits(unsigned v) {
 }
 __device__ __forceinline__ unsigned abs_bits(float v) { return __builtin_bit_cast(unsigned, v) & 0x7fffffffu; }
 
-// The scale of a block from its largest |y| (bits).
-__device__ __forceinline__ float block_scale(unsigned amax) {
-  return amax == 0u ? 1.f : __builtin_bit_cast(float, amax) / kE4m3Max;
-}
-// y / scale rounded to e4m3 (to nearest even, at most 448); NaN for a block whose scale is not finite.
-__device__ __forceinline__ unsigned char to_e4m3(float y, float scale) {
-  if (!(scale < __builtin_inff())) return 0x7f;
-  const float v = fminf(fmaxf(y / scale, -kE4m3Max), kE4m3Max);
-  return (unsigned char)(__builtin_amdgcn_cvt_pk_fp8_f32(v, v, 0, false) & 0xff);
+// Below this a block counts as all zero: 448 / amax would overflow soon after.
+constexpr float kTiny = 0x1p-100f;
+// The scale of a block from its largest |y| (bits), and the factor that takes y to the bytes' range: NaN for a block
+// with a non-finite value, which makes all its bytes NaN.  |y| factor <= 448 (1 + 2^-22) rounds to 448 at most.
+__device__ __forceinline__ float block_scale(unsigned amax, float* factor) {
+  const float m = __builtin_bit_cast(float, amax);
+  if (m < kTiny) {
+    *factor = 0.f;
+    return 1.f;
+  }
+  *factor = m < __builtin_inff() ? kE4m3Max / m : __builtin_nanf("");
+  return m / kE4m3Max;
 }
 
 __device__ __forceinline__ float block_sum(float v, float* part) {  // 256 threads
@@ -52,9 +55,9 @@ __device__ __forceinline__ float block_sum(float v, float* part) {  // 256 threa
   return (part[0] + part[1]) + (part[2] + part[3]);
 }
 
-// One workgroup per row, in 128-value blocks of one wave each.
+// Any row length and alignment: one workgroup per row, read twice, in 128-value blocks of one wave each.
 template <class T>
-__global__ __launch_bounds__(256) void fwd_kernel(NormArgs a) {
+__global__ __launch_bounds__(256) void fwd_any_kernel(NormArgs a) {
   __shared__ float part[4];
   const size_t row = blockIdx.x;
   const T* x = reinterpret_cast<const T*>(a.x) + row * a.xs;
@@ -82,24 +85,25 @@ __global__ __launch_bounds__(256) void fwd_kernel(NormArgs a) {
       }
       m = max(m, abs_bits(y[k]));
     }
-    float scale = 1.f;
+    float factor = 1.f;
     if (a.scales != nullptr) {
-      scale = block_scale(wave_max_bits(m));
+      const float scale = block_scale(wave_max_bits(m), &factor);
       if (lane_id() == 0) a.scales[row * nb + blk] = scale;
     }
 #pragma unroll
     for (int k = 0; k < 2; ++k) {
       const int c = blk * kBlock + k * 64 + lane_id();
       if (c >= a.D) continue;
-      if (a.scales != nullptr) reinterpret_cast<unsigned char*>(a.y)[row * a.D + c] = to_e4m3(y[k], scale);
+      if (a.scales != nullptr) reinterpret_cast<unsigned char*>(a.y)[row * a.D + c] =
+          (unsigned char)(__builtin_amdgcn_cvt_pk_fp8_f32(y[k] * factor, 0.f, 0, false) & 0xff);
       else reinterpret_cast<T*>(a.y)[row * a.D + c] = (T)y[k];
     }
   }
 }
 
-// Workgroup k takes rows k, k + nblk, ...; its shares of dweight stay in part[k].
+// Any row length and alignment: workgroup k takes rows k, k + nblk, ...; its shares of dweight stay in part[k].
 template <class T>
-__global__ __launch_bounds__(256) void bwd_kernel(NormArgs a) {
+__global__ __launch_bounds__(256) void bwd_any_kernel(NormArgs a) {
   __shared__ float part[4];
   float* dw = a.dw != nullptr ? a.part + (size_t)blockIdx.x * a.D : nullptr;
   for (int row = blockIdx.x; row < a.rows; row += a.nblk) {
@@ -134,16 +138,249 @@ __global__ __launch_bounds__(256) void bwd_kernel(NormArgs a) {
   }
 }
 
-// dweight from the workgroups' shares, in float64 and a fixed order.  Grid (columns / 64), four waves.
-__global__ __launch_bounds__(256) void wsum_kernel(NormArgs a) {
-  __shared__ double part[4][64];
-  const int c = blockIdx.x * 64 + threadIdx.x % 64, q = threadIdx.x / 64;
+// ---- aligned rows of up to 16384 bytes -----------------------------------------------------------
+// A row lies in the registers of TPR lanes (a part of a wave, a wave or the workgroup), NV 16-byte pieces per lane, and
+// is read once: statistics by lane exchanges, then the outputs from the same registers.  Piece k of lane j is number
+// k TPR + j of the row, so a 128-value block of the 8-bit output is 128 / V neighbouring lanes.
+template <class T> struct Piece {
+  static constexpr int V = 16 / sizeof(T);
+  typedef T vec __attribute__((ext_vector_type(V)));
+};
+
+template <int W>
+__device__ __forceinline__ float lanes_sum(float v) {
+#pragma unroll
+  for (int o = 1; o < W; o <<= 1) v += __shfl_xor(v, o, 64);
+  return v;
+}
+
+// Sum over a row's lanes; buf (2 x 4 floats, alternating) joins the waves of a 256-lane row.
+template <int TPR>
+__device__ __forceinline__ float row_sum(float v, float* buf) {
+  v = lanes_sum<(TPR < 64 ? TPR : 64)>(v);
+  if constexpr (TPR == 256) {
+    if (lane_id() == 0) buf[wave_id()] = v;
+    __syncthreads();
+    v = (buf[0] + buf[1]) + (buf[2] + buf[3]);
+  }
+  return v;
+}
+
+// silu(z) from the hardware exponential and reciprocal (1 ulp each).
+__device__ __forceinline__ float fast_sigmoid(float z) { return __builtin_amdgcn_rcpf(1.f + __expf(-z)); }
+
+template <class T, int TPR, int NV>
+__global__ __launch_bounds__(256) void fwd_row_kernel(NormArgs a) {
+  constexpr int V = Piece<T>::V, BL = kBlock / V < TPR ? kBlock / V : TPR;  // lanes of a scale block
+  typedef typename Piece<T>::vec vec;
+  __shared__ float buf[4];
+  const int j = threadIdx.x % TPR;
+  const size_t row = (size_t)blockIdx.x * (256 / TPR) + threadIdx.x / TPR;
+  if (row >= (size_t)a.rows) return;  // whole workgroups only where TPR = 256
+  const T* x = reinterpret_cast<const T*>(a.x) + row * a.xs;
+  const T* z = a.gate != nullptr ? reinterpret_cast<const T*>(a.gate) + row * a.gs : nullptr;
+  float h[NV][V];
+  vec zv[NV];
+  float s = 0.f;
+#pragma unroll
+  for (int k = 0; k < NV; ++k) {
+    const int c = (k * TPR + j) * V;
+    const bool in = c < a.D;
+    vec xv = in ? *reinterpret_cast<const vec*>(x + c) : vec(0);
+#pragma unroll
+    for (int e = 0; e < V; ++e) h[k][e] = (float)xv[e];
+    if (z != nullptr) zv[k] = in ? *reinterpret_cast<const vec*>(z + c) : vec(0);
+  }
+  if (a.residual != nullptr) {
+    const T* res = reinterpret_cast<const T*>(a.residual) + row * a.D;
+#pragma unroll
+    for (int k = 0; k < NV; ++k) {
+      const int c = (k * TPR + j) * V;
+      if (c < a.D) {
+        const vec rv = *reinterpret_cast<const vec*>(res + c);
+#pragma unroll
+        for (int e = 0; e < V; ++e) h[k][e] += (float)rv[e];
+      }
+    }
+  }
+#pragma unroll
+  for (int k = 0; k < NV; ++k)
+#pragma unroll
+    for (int e = 0; e < V; ++e) s += h[k][e] * h[k][e];
+  const float r = 1.f / sqrtf(row_sum<TPR>(s, buf) / a.D + a.eps);
+  const int nb = (a.D + kBlock - 1) / kBlock;
+#pragma unroll
+  for (int k = 0; k < NV; ++k) {
+    const int c = (k * TPR + j) * V;
+    const bool in = c < a.D;
+    const size_t at = row * a.D + c;
+    if (a.h != nullptr && in) {
+      vec o;
+#pragma unroll
+      for (int e = 0; e < V; ++e) o[e] = (T)h[k][e];
+      *reinterpret_cast<vec*>(reinterpret_cast<T*>(a.h) + at) = o;
+    }
+    float y[V];
+#pragma unroll
+    for (int e = 0; e < V; ++e) y[e] = h[k][e] * r;
+    if (a.w != nullptr && in) {
+#pragma unroll
+      for (int e = 0; e < V; ++e) y[e] *= a.w[c + e];
+    }
+    if (z != nullptr) {
+#pragma unroll
+      for (int e = 0; e < V; ++e) y[e] *= (float)zv[k][e] * fast_sigmoid((float)zv[k][e]);
+    }
+    if (a.scales == nullptr) {
+      if (in) {
+        vec o;
+#pragma unroll
+        for (int e = 0; e < V; ++e) o[e] = (T)y[e];
+        *reinterpret_cast<vec*>(reinterpret_cast<T*>(a.y) + at) = o;
+      }
+      continue;
+    }
+    unsigned m = 0;
+#pragma unroll
+    for (int e = 0; e < V; ++e) m = max(m, in ? abs_bits(y[e]) : 0u);
+#pragma unroll
+    for (int o = 1; o < BL; o <<= 1) {
+      const unsigned u = __shfl_xor(m, o, 64);
+      m = u > m ? u : m;
+    }
+    float factor;
+    const float scale = block_scale(m, &factor);
+    if (!in) continue;
+    if (j % BL == 0) a.scales[row * nb + c / kBlock] = scale;
+    unsigned q[V / 4];
+#pragma unroll
+    for (int e = 0; e < V; e += 4) {
+      int p = __builtin_amdgcn_cvt_pk_fp8_f32(y[e] * factor, y[e + 1] * factor, 0, false);
+      q[e / 4] = __builtin_amdgcn_cvt_pk_fp8_f32(y[e + 2] * factor, y[e + 3] * factor, p, true);
+    }
+    unsigned char* o = reinterpret_cast<unsigned char*>(a.y) + at;
+    if constexpr (V == 8) *reinterpret_cast<uint2*>(o) = make_uint2(q[0], q[1]);
+    else *reinterpret_cast<unsigned*>(o) = q[0];
+  }
+}
+
+// The same for the backward: the workgroup walks rows (256 / TPR at a time) with its lanes' columns of dweight in
+// registers, joins them over its row slots in LDS and leaves one share per workgroup.
+template <class T, int TPR, int NV, bool GATE>
+__global__ __launch_bounds__(256) void bwd_row_kernel(NormArgs a) {
+  constexpr int V = Piece<T>::V, RPB = 256 / TPR;
+  typedef typename Piece<T>::vec vec;
+  __shared__ float buf[2][8];
+  __shared__ float sdw[RPB > 1 ? RPB * TPR * V : 1];
+  const int j = threadIdx.x % TPR, slot = threadIdx.x / TPR;
+  float dw[NV][V], w[NV][V];
+#pragma unroll
+  for (int k = 0; k < NV; ++k) {
+    const int c = (k * TPR + j) * V;
+    const bool some = a.w != nullptr && c < a.D;
+#pragma unroll
+    for (int e = 0; e < V; ++e) {
+      dw[k][e] = 0.f;
+      w[k][e] = some ? a.w[c + e] : 1.f;
+    }
+  }
+  int flip = 0;
+  for (size_t row = (size_t)blockIdx.x * RPB + slot; row < (size_t)a.rows; row += (size_t)a.nblk * RPB) {
+    const T* h = reinterpret_cast<const T*>(a.x) + row * a.xs;
+    const T* dy = reinterpret_cast<const T*>(a.dy) + row * a.D;
+    const T* z = GATE ? reinterpret_cast<const T*>(a.gate) + row * a.gs : nullptr;
+    const T* din = a.dh_in != nullptr ? reinterpret_cast<const T*>(a.dh_in) + row * a.D : nullptr;
+    vec hv[NV], yv[NV], zv[NV], iv[NV];
+    float s = 0.f, q = 0.f;
+#pragma unroll
+    for (int k = 0; k < NV; ++k) {
+      const int c = (k * TPR + j) * V;
+      const bool in = c < a.D;
+      hv[k] = in ? *reinterpret_cast<const vec*>(h + c) : vec(0);
+      yv[k] = in ? *reinterpret_cast<const vec*>(dy + c) : vec(0);
+      if constexpr (GATE) zv[k] = in ? *reinterpret_cast<const vec*>(z + c) : vec(0);
+      iv[k] = in && din != nullptr ? *reinterpret_cast<const vec*>(din + c) : vec(0);
+    }
+    float u[NV][V], sg[GATE ? NV : 1][V];  // u = dy silu(z)
+#pragma unroll
+    for (int k = 0; k < NV; ++k) {
+#pragma unroll
+      for (int e = 0; e < V; ++e) {
+        const float hh = (float)hv[k][e];
+        u[k][e] = (float)yv[k][e];
+        if constexpr (GATE) {
+          sg[k][e] = fast_sigmoid((float)zv[k][e]);
+          u[k][e] *= (float)zv[k][e] * sg[k][e];
+        }
+        s += hh * hh;
+        q += u[k][e] * w[k][e] * hh;
+      }
+    }
+    s = row_sum<TPR>(s, buf[flip]);
+    q = row_sum<TPR>(q, buf[flip] + 4);
+    flip ^= 1;
+    const float r = 1.f / sqrtf(s / a.D + a.eps), mean = q * r / a.D;
+#pragma unroll
+    for (int k = 0; k < NV; ++k) {
+      const int c = (k * TPR + j) * V;
+      if (c >= a.D) continue;
+      vec o, og;
+#pragma unroll
+      for (int e = 0; e < V; ++e) {
+        const float hat = (float)hv[k][e] * r;
+        dw[k][e] += u[k][e] * hat;
+        o[e] = (T)(r * (u[k][e] * w[k][e] - hat * mean) + (float)iv[k][e]);
+        if constexpr (GATE) {
+          const float zz = (float)zv[k][e];
+          og[e] = (T)((float)yv[k][e] * hat * w[k][e] * (sg[k][e] * (1.f + zz * (1.f - sg[k][e]))));
+        }
+      }
+      *reinterpret_cast<vec*>(reinterpret_cast<T*>(a.h) + row * a.D + c) = o;
+      if constexpr (GATE) *reinterpret_cast<vec*>(reinterpret_cast<T*>(a.dgate) + row * a.D + c) = og;
+    }
+  }
+  if (a.dw == nullptr) return;
+  float* part = a.part + (size_t)blockIdx.x * a.D;
+#pragma unroll
+  for (int k = 0; k < NV; ++k) {
+    const int c = (k * TPR + j) * V;
+    if constexpr (RPB > 1) {
+      __syncthreads();
+#pragma unroll
+      for (int e = 0; e < V; ++e) sdw[(slot * V + e) * TPR + j] = dw[k][e];
+      __syncthreads();
+      for (int i = threadIdx.x; i < TPR * V; i += 256) {  // i = e TPR + lane
+        float t = 0.f;
+#pragma unroll
+        for (int p = 0; p < RPB; ++p) t += sdw[p * V * TPR + i];
+        const int col = (k * TPR + i % TPR) * V + i / TPR;
+        if (col < a.D) part[col] = t;
+      }
+    } else if (c < a.D) {
+#pragma unroll
+      for (int e = 0; e < V; ++e) part[c + e] = dw[k][e];
+    }
+  }
+}
+
+// dweight from the workgroups' shares, in float64 and a fixed order: 32 columns per workgroup, 32 lanes down the shares
+// of each.
+__global__ __launch_bounds__(1024) void wsum_kernel(NormArgs a) {
+  __shared__ double part[32][33];
+  const int c = blockIdx.x * 32 + threadIdx.x % 32, q = threadIdx.x / 32;
   double s = 0.0;
-  if (c < a.D)
-    for (int k = q; k < a.nblk; k += 4) s += (double)a.part[(size_t)k * a.D + c];
-  part[q][threadIdx.x % 64] = s;
+  if (c < a.D) {
+#pragma unroll 8
+    for (int k = q; k < a.nblk; k += 32) s += (double)a.part[(size_t)k * a.D + c];
+  }
+  part[q][threadIdx.x % 32] = s;
   __syncthreads();
-  if (q == 0 && c < a.D) a.dw[c] = (float)((part[0][threadIdx.x] + part[1][threadIdx.x]) + (part[2][threadIdx.x] + part[3][threadIdx.x]));
+  if (q == 0 && c < a.D) {
+    s = 0.0;
+#pragma unroll
+    for (int k = 0; k < 32; ++k) s += part[k][threadIdx.x];
+    a.dw[c] = (float)s;
+  }
 }
 
 }  // namespace norm

@@ -54,7 +54,7 @@ struct ConvArgs {
   void* y;                        // forward: y, backward: dx
   void* conv_out;
   int strip, nstrip;              // tokens per thread, strips of a sequence
-  float* part;                    // backward: [B * nstrip][H][K + 1][D]
+  float* part;                    // backward: [B * ceil(nstrip / 4)][H][K + 1][D]
   float *dw, *dbias;
 };
 

@@ -550,8 +550,8 @@ prism_status prism_ssm_step(const void* x, const prism_strides* x_strides, const
  *   float32 or NULL (ones)
  *   y      [rows, D] dense: dtype dt, or with scales != NULL OCP e4m3 bytes
  *   scales [rows, ceil(D / 128)] float32: y = byte value * scale, scale = (the largest |y| of the 128
- *          values) / 448, or 1 where all are 0.  A block with a non-finite y has a scale of
- *          infinity or NaN and bytes of NaN.
+ *          values) / 448, or 1 and bytes of 0 where all are below 2^-100.  A block with a
+ *          non-finite y has a scale of infinity or NaN and bytes of NaN.
  *   h_out  [rows, D] dtype dt, dense, or NULL: h rounded (the norm uses it unrounded).  May be the
  *          same buffer as residual, or as a dense x.
  * Any D >= 1 and rows >= 1 (unaligned rows take a narrower path).  Statistics in float32. */

@@ -1,7 +1,7 @@
 // prism_ssm_launch.h - launches of the state space scan for one tensor type and state width N (one
 // translation unit each, ssm_<type>_n<N>.hip).
 #pragma once
-#include "prism_ssm.h"
+#include "prism_ssm_bf16.h"
 
 namespace prism {
 namespace host {
@@ -11,21 +11,36 @@ inline prism_status launched() { return hipGetLastError() == hipSuccess ? PRISM_
 template <class T, int N, int PW>
 prism_status ssm_fwd_pw(const SsmArgs& a, hipStream_t stream) {
   const int bh = a.B * a.H * a.nsl;
-  if (a.nseg > 1) {
-    ssm::state_kernel<T, N, PW, false><<<dim3(a.nseg, bh, 1), PW * 4, 0, stream>>>(a);
-    ssm::seg_scan_kernel<N, PW><<<dim3(N * PW / 256, bh, 1), 256, 0, stream>>>(a, 1);
+  if constexpr (std::is_same<T, bf16_t>::value) {
+    if (a.nseg > 1) {
+      ssm::mx::state_kernel<N, PW, false, false><<<dim3(a.nseg, bh, 1), PW * 4, 0, stream>>>(a);
+      ssm::mx::seg_scan_kernel<N, PW, false><<<dim3(N * PW / 256, bh, 1), 256, 0, stream>>>(a, 1);
+    }
+    ssm::mx::sweep_kernel<N, PW><<<dim3(a.nseg, bh), PW * 4, 0, stream>>>(a);
+  } else {
+    if (a.nseg > 1) {
+      ssm::state_kernel<T, N, PW, false><<<dim3(a.nseg, bh, 1), PW * 4, 0, stream>>>(a);
+      ssm::seg_scan_kernel<N, PW><<<dim3(N * PW / 256, bh, 1), 256, 0, stream>>>(a, 1);
+    }
+    ssm::sweep_kernel<T, N, PW><<<dim3(a.nseg, bh), PW * 4, 0, stream>>>(a);
   }
-  ssm::sweep_kernel<T, N, PW><<<dim3(a.nseg, bh), PW * 4, 0, stream>>>(a);
   return launched();
 }
 
 template <class T, int N, int PW>
 prism_status ssm_bwd_pw(const SsmArgs& a, hipStream_t stream) {
   const int bh = a.B * a.H * a.nsl;
-  if (a.nseg > 1) ssm::state_kernel<T, N, PW, false><<<dim3(a.nseg, bh, 2), PW * 4, 0, stream>>>(a);
-  ssm::seg_scan_kernel<N, PW><<<dim3(N * PW / 256, bh, 2), 256, 0, stream>>>(a, a.nseg > 1);
-  ssm::state_kernel<T, N, PW, true><<<dim3(a.nseg, bh, 2), PW * 4, 0, stream>>>(a);
-  ssm::grad_kernel<T, N, PW><<<dim3(a.nch, a.nsplit, a.B * a.G), 256, 0, stream>>>(a);
+  if constexpr (std::is_same<T, bf16_t>::value) {
+    if (a.nseg > 1) ssm::mx::state_kernel<N, PW, true, false><<<dim3(a.nseg, bh, 2), PW * 4, 0, stream>>>(a);
+    ssm::mx::seg_scan_kernel<N, PW, true><<<dim3(N * PW / 256, bh, 2), 256, 0, stream>>>(a, a.nseg > 1);
+    ssm::mx::state_kernel<N, PW, true, true><<<dim3(a.nseg, bh, 2), PW * 4, 0, stream>>>(a);
+    ssm::mx::grad_kernel<N, PW><<<dim3(a.nch, a.nsplit, a.B * a.G), 256, 0, stream>>>(a);
+  } else {
+    if (a.nseg > 1) ssm::state_kernel<T, N, PW, false><<<dim3(a.nseg, bh, 2), PW * 4, 0, stream>>>(a);
+    ssm::seg_scan_kernel<N, PW><<<dim3(N * PW / 256, bh, 2), 256, 0, stream>>>(a, a.nseg > 1);
+    ssm::state_kernel<T, N, PW, true><<<dim3(a.nseg, bh, 2), PW * 4, 0, stream>>>(a);
+    ssm::grad_kernel<T, N, PW><<<dim3(a.nch, a.nsplit, a.B * a.G), 256, 0, stream>>>(a);
+  }
   if (a.nsplit > 1) {
     const size_t n = (size_t)a.B * a.G * a.T * (N / 4);
     ssm::split_sum_kernel<T, N><<<dim3((unsigned)((n + 255) / 256)), 256, 0, stream>>>(a);

@@ -88,7 +88,7 @@ bool make_strides(const prism_strides* given, int B, int H, int T, int width, pr
     if ((B > 1 && out->b <= 0) || (H > 1 && out->h <= 0) || (T > 1 && out->t <= 0)) return false;
     if (B == 1) out->b = 0;
     if (H == 1) out->h = 0;
-    if (T == 1) out->t = 0;
+    if (T == 1) out->t = width;
   }
   const long long lim = LLONG_MAX / 64;
   return out->b <= lim / B && out->h <= lim / H && out->t <= lim / T;
@@ -105,6 +105,13 @@ bool rows_apart(const prism_strides& s, int B, int H, int T, int width) {
     span += a.st * (a.n - 1);
   }
   return true;
+}
+
+// Rows of the scan's tensors: on 16-byte boundaries, not overlapping, and at most 16 MB apart (a chunk's rows are
+// addressed with 32-bit byte offsets).
+bool rows16(const void* p, const prism_strides& s, prism_dtype dt);
+bool scan_rows(const void* p, const prism_strides& s, int width, prism_dtype dt) {
+  return rows16(p, s, dt) && s.t >= width && s.t * (long long)elem(dt) <= (1 << 24);
 }
 
 bool rows16(const void* p, const prism_strides& s, prism_dtype dt) {
@@ -137,7 +144,7 @@ prism_status ssm_plan(int B, int H, int G, int T, int N, int P, prism_dtype ty, 
   const int dirs = bwd ? 2 : 1;
   const bool segs = bwd || pl->nseg > 1;
   pl->seg = ly.add(segs ? dirs * bh * pl->nseg : 0, mat * 4);
-  pl->seg_dec = ly.add(segs ? bh * pl->nseg : 0, 4);
+  pl->seg_dec = ly.add(segs ? dirs * bh * pl->nseg : 0, 4);
   if (bwd) {
     // the gradient pass: a workgroup walks per_split of a group's virtual heads; enough splits for two workgroups per CU
     const size_t per_group = (size_t)pl->HV / G, units = (size_t)pl->nch * B * G;
@@ -206,7 +213,7 @@ prism_status prism_ssm_fwd(const void* x, const prism_strides* x_strides, const 
       !make_strides(c_strides, B, G, T, N, &a.cs) || !make_strides(dt_strides, B, H, T, 1, &a.ts) ||
       !make_strides(y_strides, B, H, T, P, &a.ys) || !rows_apart(a.ys, B, H, T, P))
     return PRISM_ERR_INVALID_ARG;
-  if (!rows16(x, a.xs, ty) || !rows16(Bm, a.bs, ty) || !rows16(Cm, a.cs, ty) || !rows16(y, a.ys, ty))
+  if (!scan_rows(x, a.xs, P, ty) || !scan_rows(Bm, a.bs, N, ty) || !scan_rows(Cm, a.cs, N, ty) || !scan_rows(y, a.ys, P, ty))
     return PRISM_ERR_UNSUPPORTED;
   if (!workspace || workspace_bytes < pl.total) return PRISM_ERR_WORKSPACE;
   if (!aligned16(workspace)) return PRISM_ERR_INVALID_ARG;
@@ -242,8 +249,8 @@ prism_status prism_ssm_bwd(const void* x, const prism_strides* x_strides, const 
       !make_strides(db_strides, B, G, T, N, &a.dbs) || !make_strides(dc_strides, B, G, T, N, &a.dcs) ||
       !rows_apart(a.dxs, B, H, T, P) || !rows_apart(a.dbs, B, G, T, N) || !rows_apart(a.dcs, B, G, T, N))
     return PRISM_ERR_INVALID_ARG;
-  if (!rows16(x, a.xs, ty) || !rows16(Bm, a.bs, ty) || !rows16(Cm, a.cs, ty) || !rows16(dy, a.dys, ty) ||
-      !rows16(dx, a.dxs, ty) || !rows16(dBm, a.dbs, ty) || !rows16(dCm, a.dcs, ty))
+  if (!scan_rows(x, a.xs, P, ty) || !scan_rows(Bm, a.bs, N, ty) || !scan_rows(Cm, a.cs, N, ty) || !scan_rows(dy, a.dys, P, ty) ||
+      !scan_rows(dx, a.dxs, P, ty) || !scan_rows(dBm, a.dbs, N, ty) || !scan_rows(dCm, a.dcs, N, ty))
     return PRISM_ERR_UNSUPPORTED;
   if (!workspace || workspace_bytes < pl.total) return PRISM_ERR_WORKSPACE;
   if (!aligned16(workspace)) return PRISM_ERR_INVALID_ARG;

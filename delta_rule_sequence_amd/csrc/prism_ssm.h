@@ -24,8 +24,7 @@ struct Scal {
   float ch[Q], cl[Q];  // running log2 decay, high and low part
   float d[Q];          // step
   float eo[Q];         // decay from the chunk's start through token t
-  float w[Q];          // decay from token t to the chunk's end
-  float sig[Q];        // derivative of the step with respect to dt
+  float w[Q];          // decay from token t to the chunk's end (or that times the step)
   float dec;           // decay over the chunk
 };
 
@@ -35,12 +34,46 @@ __device__ __forceinline__ int seq_len(const SsmArgs& a, int b) {
   return n < 0 ? 0 : (n > a.T ? a.T : n);
 }
 
-__device__ __forceinline__ double wave_scan(double v, int lane) {
-#pragma unroll
-  for (int o = 1; o < 64; o <<= 1) {
-    const double u = __shfl_up(v, o, 64);
-    if (lane >= o) v += u;
-  }
+// Lane exchanges inside the VALU (DPP and half swaps), without the LDS round trip of a shuffle.
+template <int CTRL, int ROWS>
+__device__ __forceinline__ double dpp_add(double v) {  // v plus its neighbour's value, 0 where there is none
+  const unsigned long long u = __builtin_bit_cast(unsigned long long, v);
+  const unsigned lo = __builtin_amdgcn_update_dpp(0, (int)(unsigned)u, CTRL, ROWS, 0xf, false);
+  const unsigned hi = __builtin_amdgcn_update_dpp(0, (int)(unsigned)(u >> 32), CTRL, ROWS, 0xf, false);
+  return v + __builtin_bit_cast(double, (unsigned long long)hi << 32 | lo);
+}
+// Inclusive prefix sum over the wave: inside rows of 16 lanes, then row ends into the rows after them.
+__device__ __forceinline__ double wave_scan(double v) {
+  v = dpp_add<0x111, 0xf>(v);  // row_shr 1, 2, 4, 8
+  v = dpp_add<0x112, 0xf>(v);
+  v = dpp_add<0x114, 0xf>(v);
+  v = dpp_add<0x118, 0xf>(v);
+  v = dpp_add<0x142, 0xa>(v);  // row_bcast 15
+  return dpp_add<0x143, 0xc>(v);  // row_bcast 31
+}
+__device__ __forceinline__ double last_lane(double v) {
+  const unsigned long long u = __builtin_bit_cast(unsigned long long, v);
+  const unsigned lo = __builtin_amdgcn_readlane((int)(unsigned)u, 63), hi = __builtin_amdgcn_readlane((int)(unsigned)(u >> 32), 63);
+  return __builtin_bit_cast(double, (unsigned long long)hi << 32 | lo);
+}
+template <int CTRL>
+__device__ __forceinline__ float ror_add(float v) {
+  return v + __builtin_bit_cast(float, __builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, v), CTRL, 0xf, 0xf, false));
+}
+__device__ __forceinline__ float sum_lanes16(float v) {  // over the 16 lanes of a group
+  return ror_add<0x121>(ror_add<0x122>(ror_add<0x124>(ror_add<0x128>(v))));
+}
+__device__ __forceinline__ float sum_groups(float v) {  // over the four 16-lane groups
+#ifdef __HIP_DEVICE_COMPILE__  // the host pass does not know the builtins
+  unsigned u = __builtin_bit_cast(unsigned, v);
+  const auto h = __builtin_amdgcn_permlane32_swap(u, u, false, false);
+  const unsigned h0 = h[0], h1 = h[1];
+  v = __builtin_bit_cast(float, h0) + __builtin_bit_cast(float, h1);
+  u = __builtin_bit_cast(unsigned, v);
+  const auto q = __builtin_amdgcn_permlane16_swap(u, u, false, false);
+  const unsigned q0 = q[0], q1 = q[1];
+  v = __builtin_bit_cast(float, q0) + __builtin_bit_cast(float, q1);
+#endif
   return v;
 }
 
@@ -48,28 +81,41 @@ __device__ __forceinline__ float softplus_f(float z) { return z > 20.f ? z : log
 
 constexpr double kLog2e = 1.4426950408889634;
 
-// One wave: the chunk's scalars from its 64 steps; tokens at or past len have a step of 0
-// (decay 1, nothing written).  Returns the chunk's log2 decay on every lane.
-__device__ __forceinline__ double chunk_scalars(const SsmArgs& a, int b, int h, int t0, int len, Scal& s) {
+// Lane t's share of a chunk's scalars: running and total log2 decay, step, and the step's derivative with respect to
+// dt.  Tokens at or past len have a step of 0 (decay 1, nothing written).
+struct Token {
+  double c, tot;
+  float d, dz;
+  __device__ __forceinline__ float from_start() const { return exp2f((float)c); }
+  __device__ __forceinline__ float to_end() const { return exp2f((float)(tot - c)); }
+  __device__ __forceinline__ float all() const { return exp2f((float)tot); }
+};
+__device__ __forceinline__ Token chunk_token(const SsmArgs& a, int b, int h, int t0, int len) {
   const int lane = lane_id(), t = t0 + lane;
-  float d = 0.f, sig = 0.f;
+  Token k;
+  k.d = k.dz = 0.f;
+  double l2 = 0.0;
   if (t < len) {
     const float z = a.dt[b * a.ts.b + h * a.ts.h + t * a.ts.t] + (a.dt_bias != nullptr ? a.dt_bias[h] : 0.f);
-    d = a.softplus ? softplus_f(z) : z;
-    sig = a.softplus ? 1.f / (1.f + expf(-z)) : 1.f;
+    k.d = a.softplus ? softplus_f(z) : z;
+    k.dz = a.softplus ? 1.f / (1.f + expf(-z)) : 1.f;
+    l2 = (double)k.d * (double)a.A[h] * kLog2e;
   }
-  const double l2 = t < len ? (double)d * (double)a.A[h] * kLog2e : 0.0;
-  const double c = wave_scan(l2, lane);
-  const double tot = __shfl(c, 63, 64);
-  const float hi = (float)c;
+  k.c = wave_scan(l2);
+  k.tot = last_lane(k.c);
+  return k;
+}
+// One wave: all of a chunk's scalars (w: to the chunk's end, or with WD that times the step).
+template <bool WD>
+__device__ __forceinline__ void put_scalars(const Token& k, Scal& s) {
+  const int lane = lane_id();
+  const float hi = (float)k.c;
   s.ch[lane] = hi;
-  s.cl[lane] = (float)(c - (double)hi);
-  s.d[lane] = d;
-  s.sig[lane] = sig;
-  s.eo[lane] = exp2f((float)c);
-  s.w[lane] = exp2f((float)(tot - c));
-  if (lane == 0) s.dec = exp2f((float)tot);
-  return tot;
+  s.cl[lane] = (float)(k.c - (double)hi);
+  s.d[lane] = k.d;
+  s.eo[lane] = k.from_start();
+  s.w[lane] = WD ? k.to_end() * k.d : k.to_end();
+  if (lane == 0) s.dec = k.all();
 }
 
 // Rows t0 .. t0 + 63 of a strided [T, W] tensor as float32 in LDS (row stride LD); rows at or past len are 0.
@@ -140,8 +186,7 @@ __global__ __launch_bounds__(PW * 4) void state_kernel(SsmArgs a) {
   constexpr int NTH = PW * 4, LDN = N + 4, LDP = PW + 4, NT = N / 16;
   __shared__ float sA[Q * LDN];
   __shared__ float sV[Q * LDP];
-  __shared__ float sWt[Q];
-  __shared__ Scal sc;
+  __shared__ float sWt[Q], sDec;
   const int seg = blockIdx.x, bh = blockIdx.y, rev = blockIdx.z;
   const int HV = a.H * a.nsl, b = bh / HV, hv = bh % HV, h = hv / a.nsl, p0 = hv % a.nsl * PW, grp = h / (a.H / a.G);
   const int len = seq_len(a, b), pt = wave_id(), tid = threadIdx.x;
@@ -169,11 +214,13 @@ __global__ __launch_bounds__(PW * 4) void state_kernel(SsmArgs a) {
       load_rows<T, PW, LDP>(sV, a.x, b * a.xs.b + h * a.xs.h + p0, a.xs.t, t0, len, NTH);
     }
     if (tid < 64) {
-      log_dec += chunk_scalars(a, b, h, t0, len, sc);
-      sWt[tid] = rev ? sc.eo[tid] : sc.w[tid] * sc.d[tid];
+      const Token tk = chunk_token(a, b, h, t0, len);
+      log_dec += tk.tot;
+      sWt[tid] = rev ? tk.from_start() : tk.to_end() * tk.d;
+      if (tid == 0) sDec = tk.all();
     }
     __syncthreads();
-    const float dec = sc.dec;
+    const float dec = sDec;
 #pragma unroll
     for (int n = 0; n < NT; ++n) acc[n] *= dec;
 #pragma unroll
@@ -202,11 +249,24 @@ __global__ __launch_bounds__(256) void seg_scan_kernel(SsmArgs a, int has_end) {
   const float* init = rev ? a.dS : a.S0;
   float v = init != nullptr ? init[((size_t)(b * a.H + h) * N + n) * a.P + p0 + p] : 0.f;
   float* q = a.seg + ((size_t)rev * gridDim.y + bh) * a.nseg * (N * PW) + e;
-  for (int k = 0; k < a.nseg; ++k) {
-    const int s = rev ? a.nseg - 1 - k : k;
-    const float own = has_end ? q[(size_t)s * (N * PW)] : 0.f;
-    q[(size_t)s * (N * PW)] = v;
-    if (has_end) v = a.seg_dec[(size_t)bh * a.nseg + s] * v + own;
+  const float* dec = a.seg_dec + (size_t)bh * a.nseg;
+  constexpr int U = 16;  // loads in flight
+  for (int k0 = 0; k0 < a.nseg; k0 += U) {
+    float own[U], d[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int k = k0 + u, s = rev ? a.nseg - 1 - k : k;
+      if (k >= a.nseg || !has_end) break;
+      own[u] = q[(size_t)s * (N * PW)];
+      d[u] = dec[s];
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int k = k0 + u, s = rev ? a.nseg - 1 - k : k;
+      if (k >= a.nseg) break;
+      q[(size_t)s * (N * PW)] = v;
+      if (has_end) v = d[u] * v + own[u];
+    }
   }
 }
 
@@ -244,7 +304,7 @@ __global__ __launch_bounds__(PW * 4) void sweep_kernel(SsmArgs a) {
     load_rows<T, N, LDN>(sB, a.bm, b * a.bs.b + grp * a.bs.h, a.bs.t, t0, len, NTH);
     load_rows<T, N, LDN>(sC, a.cm, b * a.cs.b + grp * a.cs.h, a.cs.t, t0, len, NTH);
     load_rows<T, PW, LDP>(sX, a.x, b * a.xs.b + h * a.xs.h + p0, a.xs.t, t0, len, NTH);
-    if (tid < 64) chunk_scalars(a, b, h, t0, len, sc);
+    if (tid < 64) put_scalars<false>(chunk_token(a, b, h, t0, len), sc);
     __syncthreads();
     // M, tile (ts, tt): rows s, columns t
     for (int idx = wave_id(); idx < 10; idx += NW) {
@@ -299,16 +359,6 @@ __global__ __launch_bounds__(PW * 4) void sweep_kernel(SsmArgs a) {
   }
 }
 
-__device__ __forceinline__ float sum_groups(float v) {  // over the four 16-lane groups
-  v += __shfl_xor(v, 16, 64);
-  return v + __shfl_xor(v, 32, 64);
-}
-__device__ __forceinline__ float sum_lanes16(float v) {  // over the 16 lanes of a group
-#pragma unroll
-  for (int o = 1; o < 16; o <<= 1) v += __shfl_xor(v, o, 64);
-  return v;
-}
-
 // Gradients of one chunk for one group (grid (nch, nsplit, B * G)): the workgroup walks its share of the group's
 // virtual heads, so that dB and dC are summed over heads in registers.  With H the state entering the chunk and R the
 // adjoint of the state leaving it (state_kernel), dM = dy x^T, E_ts = e^{c_t - c_s}:
@@ -327,7 +377,7 @@ __global__ __launch_bounds__(256) void grad_kernel(SsmArgs a) {
   __shared__ float sY[Q * LDP];  // dy
   __shared__ float sM[Q * LDQ];  // M[t][s]
   __shared__ Scal sc;
-  __shared__ float sRow[Q], sI[Q], sJ[Q], sDiag[Q], sCol[4][Q], sK[4], sDD[4];
+  __shared__ float sSig[Q], sRow[Q], sI[Q], sJ[Q], sDiag[Q], sCol[4][Q], sK[4], sDD[4];
   const int ch = blockIdx.x, bg = blockIdx.z, b = bg / a.G, grp = bg % a.G, t0 = ch * Q;
   const int w = wave_id(), tid = threadIdx.x, l = lane_id(), g = l >> 4, i = l & 15;
   const int HV = a.H * a.nsl, per_group = HV / a.G;
@@ -355,7 +405,11 @@ __global__ __launch_bounds__(256) void grad_kernel(SsmArgs a) {
     __syncthreads();
     load_rows<T, PW, LDP>(sX, a.x, b * a.xs.b + h * a.xs.h + p0, a.xs.t, t0, a.T, 256);
     load_rows<T, PW, LDP>(sY, a.dy, b * a.dys.b + h * a.dys.h + p0, a.dys.t, t0, a.T, 256);
-    if (tid < 64) chunk_scalars(a, b, h, t0, a.T, sc);
+    if (tid < 64) {
+      const Token tk = chunk_token(a, b, h, t0, a.T);
+      put_scalars<false>(tk, sc);
+      sSig[tid] = tk.dz;
+    }
     __syncthreads();
     float row = 0.f;
 #pragma unroll
@@ -466,23 +520,18 @@ __global__ __launch_bounds__(256) void grad_kernel(SsmArgs a) {
       const float d = sc.d[t], J0 = sJ[t], Ah = a.A[h];
       const double jd = (double)d * J0;
       const double f = (double)sRow[t] - (double)d * qoff + sI[t];
-      const double fs = wave_scan(f, t), ftot = __shfl(fs, 63, 64);  // suffix sum from t: ftot - fs + f
-      const double js = wave_scan(jd, t);                            // prefix sum before t: js - jd
+      const double fs = wave_scan(f), ftot = last_lane(fs);  // suffix sum from t: ftot - fs + f
+      const double js = wave_scan(jd);                       // prefix sum before t: js - jd
       const float kk = sc.dec * ((sK[0] + sK[1]) + (sK[2] + sK[3]));
       const float dl = (float)((ftot - fs + f) + (js - jd) + kk);
-      const float ddt = (qoff + sDiag[t] + J0 + Ah * dl) * sc.sig[t];
+      const float ddt = (qoff + sDiag[t] + J0 + Ah * dl) * sSig[t];
       const bool in = t0 + t < a.T;
       if (in) {
         const size_t at = ((size_t)b * a.H + h) * a.T + t0 + t;
         if (a.nsl == 1) a.ddt[at] = ddt;
         else a.part_ddt[(size_t)slice * a.B * a.H * a.T + at] = ddt;
       }
-      double sa = in ? (double)dl * d : 0.0, sb = in ? (double)ddt : 0.0;
-#pragma unroll
-      for (int o = 1; o < 64; o <<= 1) {
-        sa += __shfl_xor(sa, o, 64);
-        sb += __shfl_xor(sb, o, 64);
-      }
+      const double sa = last_lane(wave_scan(in ? (double)dl * d : 0.0)), sb = last_lane(wave_scan(in ? (double)ddt : 0.0));
       if (t == 0) {
         const size_t at = bh * a.nch + ch, n = (size_t)a.B * HV * a.nch;
         a.part_sum[at] = (float)sa;

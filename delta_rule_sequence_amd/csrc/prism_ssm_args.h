@@ -22,7 +22,7 @@ struct SsmArgs {
   prism_strides ys;
   float* S_final;
   float* seg;                     // [dirs][B * HV][nseg][N * PW]: states at segment borders
-  float* seg_dec;                 // [B * HV][nseg]: decay over each segment
+  float* seg_dec;                 // [dirs][B * HV][nseg]: decay over each segment
   // backward
   float* st;                      // [2][B * HV][nch][N * PW]: state entering / adjoint leaving each chunk
   const float* dS;

@@ -97,151 +97,218 @@ __device__ __forceinline__ bf16x8 round8(const f32x4& a, const f32x4& b) {
   return o;
 }
 
-// Rows t0 .. t0 + 63 of a strided [T, W] tensor on the way from memory to an LDS tile: loaded into registers early, stored
-// when the tile is free.  Rows at or past len are 0.
-template <int W, int NTH>
-struct Stage {
-  static constexpr int NV = Q * W / 8, PER = (NV + NTH - 1) / NTH;
-  bf16x8 v[PER];
-  __device__ __forceinline__ void load(const bf16_t* p, long long st, int t0, int len) {
+// Loads 64 rows of a strided [T, W] tensor into an LDS tile without passing registers, 16 bytes per lane (buffer loads to
+// LDS): a wave's 64 pieces fill 1 KB of the tile in a row, so the permutation of Tile::at is applied to the source
+// pieces.  Rows past the sequence's end lie outside the buffer descriptor and arrive as zeros.  Complete after
+// loads_done() and a barrier.
+template <int W, int NW>
+struct Rows {
+  static constexpr int RPI = 512 / W, STEP = RPI > 16 ? RPI : 16, PERIOD = STEP / RPI;  // rows per load, rows per permutation period
+  static constexpr int NI = Q / RPI, PER = (NI + NW - 1) / NW;                          // loads of a tile, per wave
+  static constexpr int OWN = PER < PERIOD ? PER : PERIOD;                               // a wave's places in a period
+  int off[OWN];
+  int stride;  // bytes
+  __device__ __forceinline__ void init(long long st) {
+    stride = (int)st * 2;
 #pragma unroll
-    for (int k = 0; k < PER; ++k) {
-      const int i = threadIdx.x + k * NTH, t = t0 + i / (W / 8);
-      v[k] = bf16x8(0);
-      if ((NV % NTH == 0 || i < NV) && t < len) v[k] = *reinterpret_cast<const bf16x8*>(p + (long long)t * st + i % (W / 8) * 8);
+    for (int k = 0; k < OWN; ++k) {
+      const int r = (wave_id() * PER + k) % PERIOD * RPI + lane_id() / (W / 8), c = (lane_id() % (W / 8)) ^ Tile<W>::swz(r);
+      off[k] = r * stride + c * 16;
     }
   }
-  __device__ __forceinline__ void store(bf16_t* tile) {
+  // p: row 0 of the tile (wave-uniform); rows: how many exist
+  __device__ __forceinline__ void load(bf16_t* tile, const bf16_t* p, int rows) const {
+#ifdef __HIP_DEVICE_COMPILE__  // the host pass does not know the builtins
+    const int w = __builtin_amdgcn_readfirstlane(wave_id());
+    const int bytes = rows <= 0 ? 0 : (min(rows, Q) - 1) * stride + W * 2;
+    const __amdgpu_buffer_rsrc_t rs = __builtin_amdgcn_make_buffer_rsrc(const_cast<bf16_t*>(p), 0, bytes, 0x00027000);
 #pragma unroll
     for (int k = 0; k < PER; ++k) {
-      const int i = threadIdx.x + k * NTH;
-      if (NV % NTH == 0 || i < NV) *reinterpret_cast<bf16x8*>(tile + Tile<W>::at(i / (W / 8), i % (W / 8) * 8)) = v[k];
+      const int j = w * PER + k;  // wave-uniform
+      if (NI % NW != 0 && j >= NI) break;
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, (__attribute__((address_space(3))) void*)(tile + j * 512), 16,
+                                               off[k % OWN], (j / PERIOD) * STEP * stride, 0, 0);
     }
+#endif
   }
 };
+__device__ __forceinline__ void loads_done() { asm volatile("s_waitcnt vmcnt(0)" ::: "memory"); }
 
 __device__ __forceinline__ float decay(const Scal& s, int t, int r) {  // e^{c_t - c_r}
   return __builtin_amdgcn_exp2f((s.ch[t] - s.ch[r]) + (s.cl[t] - s.cl[r]));
 }
 
-// The decay-weighted rows of V (index = column p0 .., k = token) in three parts: weight wa[k] (times wb[k]).
-template <int W>
-__device__ __forceinline__ void weighted(bf16x8 (&p)[3], const bf16_t* tile, int k0, int p0, const float* wa, const float* wb) {
+// v, or 0 where !on, whatever v is (as bits: the compiler would branch around what leads to v otherwise).
+__device__ __forceinline__ float keep(float v, bool on) { return val(bits(v) & (on ? 0xffffffffu : 0u)); }
+
+// The decay-weighted rows of V (index = column p0 .., k = token k0 ..) in three parts, times wt[k].
+__device__ __forceinline__ void weighted(bf16x8 (&p)[3], const bf16x8& f, int k0, const float* wt) {
   const int g4 = 4 * (lane_id() >> 4);
-  const bf16x8 f = frag_t<W>(tile, k0, p0);
+  const f32x4 a = *reinterpret_cast<const f32x4*>(wt + k0 + g4), b = *reinterpret_cast<const f32x4*>(wt + k0 + 16 + g4);
   float v[8];
 #pragma unroll
   for (int r = 0; r < 4; ++r) {
-    float a = wa[k0 + g4 + r], b = wa[k0 + 16 + g4 + r];
-    if (wb != nullptr) a *= wb[k0 + g4 + r], b *= wb[k0 + 16 + g4 + r];
-    v[r] = (float)f[r] * a;
-    v[4 + r] = (float)f[4 + r] * b;
+    v[r] = (float)f[r] * a[r];
+    v[4 + r] = (float)f[4 + r] * b[r];
   }
   split3(v, p);
 }
 
-// Piece of a saved state: H^T tile (pt, nt) is half of the 8 k = p values of lane (g, n) in block pt / 2, for the products
-// that contract over p.  Two planes (parts) of N * PW bfloat16 each.
+// Piece of a saved state: tile (pt, nt) of H^T, 4 values p = 16 pt + 4 g + r of column n = 16 nt + i per lane, for the
+// products that contract over p.  Two planes (parts) of N * PW bfloat16 each.
 template <int N, int PW>
 __device__ __forceinline__ size_t plane_at(int pt, int nt) {
-  if constexpr (PW == 16) return ((size_t)nt * 64 + lane_id()) * 4;
-  else return (((size_t)nt * (PW / 32) + (pt >> 1)) * 64 + lane_id()) * 8 + (pt & 1) * 4;
+  return ((size_t)nt * (PW / 16) + pt) * 256 + lane_id() * 4;
 }
 
-// States of a segment, as ssm::state_kernel.  SAVE = false (H: rows n, columns p, as the sweep keeps it; or, for the
-// backward, transposed): from zero, the end state to seg.  SAVE = true: from the entering state, saving the state in
-// front of every chunk in two planes.
-template <int N, int PW, bool TRANS, bool SAVE>
-__global__ __launch_bounds__(PW * 4) void state_kernel(SsmArgs a) {
-  constexpr int NTH = PW * 4, NW = PW / 16, NT = N / 16;
-  __shared__ __attribute__((aligned(16))) bf16_t sA[Q * N];
-  __shared__ __attribute__((aligned(16))) bf16_t sV[Q * PW];
-  __shared__ Scal scal[NW];
-  const int seg = blockIdx.x, bh = blockIdx.y, rev = blockIdx.z;
-  const int HV = a.H * a.nsl, b = bh / HV, hv = bh % HV, h = hv / a.nsl, p0 = hv % a.nsl * PW, grp = h / (a.H / a.G);
-  const int len = seq_len(a, b), pt = wave_id(), tid = threadIdx.x;
+// Workgroups of one (batch, group, segment) read the same B and C.  They are numbered next to each other and, since the
+// hardware deals workgroups out to the eight XCDs in turn, every eighth workgroup takes the next number: their rows are
+// then read into one XCD's L2 once.
+__device__ __forceinline__ int xcd_order(int id, int total) {
+  const int q = total / 8, r = total % 8, x = id % 8;
+  return x * q + min(x, r) + id / 8;
+}
+
+// The place of a workgroup of the passes over segments: HP virtual heads of one group from hv0 on, one segment.  Grid
+// (B * HV / HP * segments, directions).
+struct Place {
+  int b, hv0, seg;
+};
+template <int HP>
+__device__ __forceinline__ Place place(const SsmArgs& a, int segs) {
+  const int HV = a.H * a.nsl, pg = HV / a.G / HP;  // workgroups per (batch, group, segment)
+  int id = xcd_order(blockIdx.x, gridDim.x);
+  const int u = id % pg;
+  id /= pg;
+  const int seg = id % segs;
+  id /= segs;
+  return {id / a.G, (id % a.G) * (HV / a.G) + u * HP, seg};
+}
+
+// Column tiles (16 columns) per wave: an operand of B or C read from LDS serves PTW products.
+template <int PW> constexpr int tiles_per_wave() { return PW >= 32 ? 2 : 1; }
+template <int PW> constexpr int waves_per_head() { return PW / 16 / tiles_per_wave<PW>(); }
+
+// States of a segment, as ssm::state_kernel, for HP virtual heads of a group at once (they share the rows of B or C).
+// A wave owns PTW tiles of 16 columns of one head.  SAVE = false: from zero, the end state to seg (H: rows n, columns p, as
+// the sweep keeps it; or, for the backward, transposed); the segment whose end nobody reads is left out.  SAVE = true:
+// from the entering state, saving the state in front of every chunk in two planes.  The next chunk's rows arrive in the
+// second half of the tiles meanwhile.
+template <int N, int PW, int HP, bool TRANS, bool SAVE>
+__global__ __launch_bounds__(waves_per_head<PW>() * HP * 64, 2) void state_kernel(SsmArgs a) {
+  constexpr int PTW = tiles_per_wave<PW>(), NW = waves_per_head<PW>(), NWG = NW * HP, NT = N / 16, NB = 4;  // chunks per batch of weights
+  __shared__ __attribute__((aligned(16))) bf16_t sA[2][Q * N];
+  __shared__ __attribute__((aligned(16))) bf16_t sV[2][HP][Q * PW];
+  __shared__ __attribute__((aligned(16))) float sWt[2][HP][NB][Q];
+  __shared__ float sDec[2][HP][NB];
+  const int rev = blockIdx.y, HV = a.H * a.nsl;
+  const Place pl = place<HP>(a, SAVE ? a.nseg : a.nseg - 1);
+  const int seg = SAVE ? pl.seg : pl.seg + rev, b = pl.b, grp = pl.hv0 / (HV / a.G);
+  const int wv = __builtin_amdgcn_readfirstlane(wave_id()), sub = wv / NW, wh = wv % NW, hv = pl.hv0 + sub, h = hv / a.nsl;
+  const int bh = b * HV + hv, len = seq_len(a, b);
   const int c0 = seg * a.seg_chunks, c1 = min(c0 + a.seg_chunks, a.nch);
-  const size_t slot = ((size_t)rev * gridDim.y + bh) * a.nseg + seg;
-  const bf16_t *pa, *pv;
+  const size_t slot = ((size_t)rev * a.B * HV + bh) * a.nseg + seg;
+  const bf16_t *pa, *pv[HP];
   long long ta, tv;
   if (rev) {
-    pa = (const bf16_t*)a.cm + b * a.cs.b + grp * a.cs.h, ta = a.cs.t;
-    pv = (const bf16_t*)a.dy + b * a.dys.b + h * a.dys.h + p0, tv = a.dys.t;
+    pa = (const bf16_t*)a.cm + b * a.cs.b + grp * a.cs.h, ta = a.cs.t, tv = a.dys.t;
   } else {
-    pa = (const bf16_t*)a.bm + b * a.bs.b + grp * a.bs.h, ta = a.bs.t;
-    pv = (const bf16_t*)a.x + b * a.xs.b + h * a.xs.h + p0, tv = a.xs.t;
+    pa = (const bf16_t*)a.bm + b * a.bs.b + grp * a.bs.h, ta = a.bs.t, tv = a.xs.t;
   }
-  f32x4 acc[NT];
 #pragma unroll
-  for (int n = 0; n < NT; ++n)
-    acc[n] = SAVE ? *reinterpret_cast<const f32x4*>(a.seg + slot * (N * PW) + tile_at<N>(pt, n)) : zero4();
-  // chunks that hold tokens, in walking order
-  const int live = min(c1, (len + Q - 1) / Q) - c0, steps = SAVE ? c1 - c0 : max(live, 0);
-  Stage<N, NTH> la;
-  Stage<PW, NTH> lv;
-  if (steps > 0) {
-    const int t0 = (rev ? c1 - 1 : c0) * Q;
-    la.load(pa, ta, t0, len);
-    lv.load(pv, tv, t0, len);
+  for (int q = 0; q < HP; ++q) {
+    const int v = pl.hv0 + q, off = v % a.nsl * PW;
+    pv[q] = rev ? (const bf16_t*)a.dy + b * a.dys.b + v / a.nsl * a.dys.h + off : (const bf16_t*)a.x + b * a.xs.b + v / a.nsl * a.xs.h + off;
   }
+  f32x4 acc[PTW][NT];
+#pragma unroll
+  for (int p = 0; p < PTW; ++p)
+#pragma unroll
+    for (int n = 0; n < NT; ++n)
+      acc[p][n] = SAVE ? *reinterpret_cast<const f32x4*>(a.seg + slot * (N * PW) + tile_at<N>(wh * PTW + p, n)) : zero4();
+  // chunks that hold tokens, in walking order
+  const int live = min(c1, (len + Q - 1) / Q) - c0, steps = SAVE ? c1 - c0 : max(live, 0), last = SAVE ? c1 - 1 : c0 + steps - 1;
+  Rows<N, NWG> la;
+  Rows<PW, NWG> lv;
+  la.init(ta);
+  lv.init(tv);
+  const auto load = [&](int k) {
+    const int t0 = (rev ? last - k : c0 + k) * Q;
+    la.load(sA[k & 1], pa + (long long)t0 * ta, len - t0);
+#pragma unroll
+    for (int q = 0; q < HP; ++q) lv.load(sV[k & 1][q], pv[q] + (long long)t0 * tv, len - t0);
+  };
+  if (steps > 0) load(0);
   double log_dec = 0.0;
   for (int k = 0; k < steps; ++k) {
-    const int ch = rev ? c1 - 1 - k : c0 + k;
-    __syncthreads();
-    la.store(sA);
-    lv.store(sV);
-    if (k % NW == 0) {  // the next NW chunks' scalars, one wave each
-      const int kk = k + wave_id();
-      if (kk < steps) log_dec += chunk_scalars(a, b, h, (rev ? c1 - 1 - kk : c0 + kk) * Q, len, scal[wave_id()]);
-    }
-    if (k + 1 < steps) {
-      const int t0 = (rev ? ch - 1 : ch + 1) * Q;
-      la.load(pa, ta, t0, len);
-      lv.load(pv, tv, t0, len);
-    }
-    if constexpr (SAVE) {
-      bf16_t* st = reinterpret_cast<bf16_t*>(a.st) + (((size_t)rev * gridDim.y + bh) * a.nch + ch) * (2 * N * PW);
+    const int ch = rev ? last - k : c0 + k, par = (k / NB) & 1;
+    if (k % NB == 0) {  // the next NB chunks' weights, the head's waves in turn; the other half may still be read
 #pragma unroll
-      for (int n = 0; n < NT; ++n) {
-        bf16x4 hi, lo;
-#pragma unroll
-        for (int r = 0; r < 4; ++r) {
-          hi[r] = (bf16_t)acc[n][r];
-          lo[r] = (bf16_t)(acc[n][r] - (float)hi[r]);
+      for (int q = 0; q < NB; q += NW) {
+        const int kk = k + q + wh;
+        if (kk < steps) {
+          const Token tk = chunk_token(a, b, h, (rev ? last - kk : c0 + kk) * Q, len);
+          log_dec += tk.tot;
+          sWt[par][sub][q + wh][lane_id()] = rev ? tk.from_start() : tk.to_end() * tk.d;
+          if (lane_id() == 0) sDec[par][sub][q + wh] = tk.all();
         }
-        *reinterpret_cast<bf16x4*>(st + plane_at<N, PW>(pt, n)) = hi;
-        *reinterpret_cast<bf16x4*>(st + N * PW + plane_at<N, PW>(pt, n)) = lo;
       }
     }
-    __syncthreads();
-    const Scal& sc = scal[k % NW];
-    const float dec = sc.dec;
+    loads_done();
+    __syncthreads();  // this chunk's rows are there, the other half's reads are over
+    if constexpr (SAVE) {
+      bf16_t* st = reinterpret_cast<bf16_t*>(a.st) + (((size_t)rev * a.B * HV + bh) * a.nch + ch) * (2 * N * PW);
 #pragma unroll
-    for (int n = 0; n < NT; ++n) acc[n] *= dec;
+      for (int p = 0; p < PTW; ++p)
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+          bf16x4 hi, lo;
+#pragma unroll
+          for (int r = 0; r < 4; ++r) {
+            hi[r] = (bf16_t)acc[p][n][r];
+            lo[r] = (bf16_t)(acc[p][n][r] - (float)hi[r]);
+          }
+          *reinterpret_cast<bf16x4*>(st + plane_at<N, PW>(wh * PTW + p, n)) = hi;
+          *reinterpret_cast<bf16x4*>(st + N * PW + plane_at<N, PW>(wh * PTW + p, n)) = lo;
+        }
+    }
+    if (k + 1 < steps) load(k + 1);
+    const float dec = sDec[par][sub][k % NB];
+#pragma unroll
+    for (int p = 0; p < PTW; ++p)
+#pragma unroll
+      for (int n = 0; n < NT; ++n) acc[p][n] *= dec;
 #pragma unroll
     for (int k0 = 0; k0 < Q; k0 += 32) {
-      bf16x8 f[3];
-      weighted<PW>(f, sV, k0, 16 * pt, rev ? sc.eo : sc.w, rev ? nullptr : sc.d);
+      bf16x8 f[PTW][3];
 #pragma unroll
-      for (int n = 0; n < NT; ++n) {
-        const bf16x8 fa = frag_t<N>(sA, k0, 16 * n);
+      for (int p = 0; p < PTW; ++p) weighted(f[p], frag_t<PW>(sV[k & 1][sub], k0, 16 * (wh * PTW + p)), k0, sWt[par][sub][k % NB]);
+      bf16x8 fa[NT];
 #pragma unroll
-        for (int q = 2; q >= 0; --q) acc[n] = TRANS ? mfma(f[q], fa, acc[n]) : mfma(fa, f[q], acc[n]);
-      }
+      for (int n = 0; n < NT; ++n) fa[n] = frag_t<N>(sA[k & 1], k0, 16 * n);
+      // parts outermost: neighbouring products go to different accumulators
+#pragma unroll
+      for (int q = 2; q >= 0; --q)
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+          for (int p = 0; p < PTW; ++p) acc[p][n] = TRANS ? mfma(f[p][q], fa[n], acc[p][n]) : mfma(fa[n], f[p][q], acc[p][n]);
     }
   }
   if constexpr (!SAVE) {
 #pragma unroll
-    for (int n = 0; n < NT; ++n) *reinterpret_cast<f32x4*>(a.seg + slot * (N * PW) + tile_at<N>(pt, n)) = acc[n];
-    // the waves' shares of the segment's log decay
-    __shared__ double part[NW];
-    if (lane_id() == 0) part[wave_id()] = log_dec;
-    __syncthreads();
-    if (rev == 0 && tid == 0) {
-      double s = part[0];
+    for (int p = 0; p < PTW; ++p)
 #pragma unroll
-      for (int k = 1; k < NW; ++k) s += part[k];
-      a.seg_dec[(size_t)bh * a.nseg + seg] = exp2f((float)s);
+      for (int n = 0; n < NT; ++n) *reinterpret_cast<f32x4*>(a.seg + slot * (N * PW) + tile_at<N>(wh * PTW + p, n)) = acc[p][n];
+    // the waves' shares of the segment's log decay
+    __shared__ double part[HP][NW];
+    if (lane_id() == 0) part[sub][wh] = log_dec;
+    __syncthreads();
+    if (lane_id() == 0 && wh == 0) {
+      double s = part[sub][0];
+#pragma unroll
+      for (int k = 1; k < NW; ++k) s += part[sub][k];
+      a.seg_dec[((size_t)rev * a.B * HV + bh) * a.nseg + seg] = exp2f((float)s);
     }
   }
 }
@@ -256,377 +323,485 @@ __global__ __launch_bounds__(256) void seg_scan_kernel(SsmArgs a, int has_end) {
   const float* init = rev ? a.dS : a.S0;
   float v = init != nullptr ? init[((size_t)(b * a.H + h) * N + n) * a.P + p0 + p] : 0.f;
   float* q = a.seg + ((size_t)rev * gridDim.y + bh) * a.nseg * (N * PW) + e;
-  for (int k = 0; k < a.nseg; ++k) {
-    const int s = rev ? a.nseg - 1 - k : k;
-    const float own = has_end ? q[(size_t)s * (N * PW)] : 0.f;
-    q[(size_t)s * (N * PW)] = v;
-    if (has_end) v = a.seg_dec[(size_t)bh * a.nseg + s] * v + own;
+  const float* dec = a.seg_dec + ((size_t)rev * gridDim.y + bh) * a.nseg;
+  constexpr int U = 16;  // loads in flight
+  for (int k0 = 0; k0 < a.nseg; k0 += U) {
+    float own[U], d[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int k = k0 + u, s = rev ? a.nseg - 1 - k : k;
+      if (k >= a.nseg - 1 || !has_end) break;  // nothing enters from the last segment's end
+      own[u] = q[(size_t)s * (N * PW)];
+      d[u] = dec[s];
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int k = k0 + u, s = rev ? a.nseg - 1 - k : k;
+      if (k >= a.nseg) break;
+      q[(size_t)s * (N * PW)] = v;
+      if (has_end && k < a.nseg - 1) v = d[u] * v + own[u];
+    }
   }
 }
 
-// Outputs of a segment from its entering state, as ssm::sweep_kernel.  y tiles are formed transposed (rows p, columns t), so
-// that a lane stores 4 neighbouring columns.
-template <int N, int PW>
-__global__ __launch_bounds__(PW * 4) void sweep_kernel(SsmArgs a) {
-  constexpr int NTH = PW * 4, NW = PW / 16, NT = N / 16, KN = kblocks<N>();
+// Outputs of a segment from its entering state, as ssm::sweep_kernel, for HP virtual heads of a group at once.  The heads
+// share B, C and their products: a wave forms C B^T tiles and the scores of all HP heads from them.  y tiles are formed
+// transposed (rows p, columns t), so that a lane stores 4 neighbouring columns; they are stored one chunk later, so that no
+// wave waits for its stores before the next rows.
+template <int N, int PW, int HP>
+__global__ __launch_bounds__(waves_per_head<PW>() * HP * 64, 2) void sweep_kernel(SsmArgs a) {
+  constexpr int PTW = tiles_per_wave<PW>(), NW = waves_per_head<PW>(), NWG = NW * HP, NT = N / 16, KN = kblocks<N>(), TT = Q / 16;
+  constexpr int NB = 2;  // chunks per batch of scalars
   __shared__ __attribute__((aligned(16))) bf16_t sB[Q * N];
   __shared__ __attribute__((aligned(16))) bf16_t sC[Q * N];
-  __shared__ __attribute__((aligned(16))) bf16_t sX[Q * PW];
-  __shared__ __attribute__((aligned(16))) bf16_t sM[Q * Q];
-  __shared__ Scal scal[NW];
-  const int seg = blockIdx.x, bh = blockIdx.y;
-  const int HV = a.H * a.nsl, b = bh / HV, hv = bh % HV, h = hv / a.nsl, p0 = hv % a.nsl * PW, grp = h / (a.H / a.G);
-  const int len = seq_len(a, b), pt = wave_id(), l = lane_id(), g = l >> 4, i = l & 15;
+  __shared__ __attribute__((aligned(16))) bf16_t sX[HP][Q * PW];
+  __shared__ __attribute__((aligned(16))) bf16_t sM[HP][Q * Q];
+  __shared__ Scal scal[HP][NB];
+  const int HV = a.H * a.nsl;
+  const Place pl = place<HP>(a, a.nseg);
+  const int seg = pl.seg, b = pl.b, grp = pl.hv0 / (HV / a.G);
+  const int wv = __builtin_amdgcn_readfirstlane(wave_id()), sub = wv / NW, wh = wv % NW, pt0 = wh * PTW;
+  const int hv = pl.hv0 + sub, h = hv / a.nsl, p0 = hv % a.nsl * PW;
+  const int bh = b * HV + hv, len = seq_len(a, b), l = lane_id(), g = l >> 4, i = l & 15;
   const int c0 = seg * a.seg_chunks, steps = min(min(c0 + a.seg_chunks, a.nch), (len + Q - 1) / Q) - c0;
-  const float Dh = a.D != nullptr ? a.D[h] : 0.f;
-  const size_t gstate = ((size_t)(b * a.H + h) * N) * a.P + p0 + 16 * pt;
+  float Dh[HP];
+#pragma unroll
+  for (int q = 0; q < HP; ++q) Dh[q] = a.D != nullptr ? a.D[(pl.hv0 + q) / a.nsl] : 0.f;
+  const size_t gstate = ((size_t)(b * a.H + h) * N) * a.P + p0 + 16 * pt0;
   const bf16_t* pb = (const bf16_t*)a.bm + b * a.bs.b + grp * a.bs.h;
   const bf16_t* pc = (const bf16_t*)a.cm + b * a.cs.b + grp * a.cs.h;
-  const bf16_t* px = (const bf16_t*)a.x + b * a.xs.b + h * a.xs.h + p0;
-  bf16_t* py = (bf16_t*)a.y + b * a.ys.b + h * a.ys.h + p0 + 16 * pt + 4 * g;
-  Stage<N, NTH> lb, lc;
-  Stage<PW, NTH> lx;
-  if (steps > 0) {
-    lb.load(pb, a.bs.t, c0 * Q, len);
-    lc.load(pc, a.cs.t, c0 * Q, len);
-    lx.load(px, a.xs.t, c0 * Q, len);
-  }
-  // state tiles: rows n = 16 nt + 4 g + r, column p = 16 pt + i
-  f32x4 hs[NT];
+  bf16_t* py = (bf16_t*)a.y + b * a.ys.b + h * a.ys.h + p0 + 16 * pt0 + 4 * g;
+  Rows<N, NWG> lb, lc;
+  Rows<PW, NWG> lx;
+  lb.init(a.bs.t);
+  lc.init(a.cs.t);
+  lx.init(a.xs.t);
+  // state tiles: rows n = 16 nt + 4 g + r, column 16 (pt0 + p) + i
+  f32x4 hs[PTW][NT];
 #pragma unroll
-  for (int n = 0; n < NT; ++n) {
-    if (a.nseg > 1) {
-      hs[n] = *reinterpret_cast<const f32x4*>(a.seg + ((size_t)bh * a.nseg + seg) * (N * PW) + tile_at<N>(pt, n));
-    } else {
+  for (int p = 0; p < PTW; ++p)
 #pragma unroll
-      for (int r = 0; r < 4; ++r)
-        hs[n][r] = a.S0 != nullptr ? a.S0[gstate + (size_t)(16 * n + 4 * g + r) * a.P + i] : 0.f;
+    for (int n = 0; n < NT; ++n) {
+      if (a.nseg > 1) {
+        hs[p][n] = *reinterpret_cast<const f32x4*>(a.seg + ((size_t)bh * a.nseg + seg) * (N * PW) + tile_at<N>(pt0 + p, n));
+      } else {
+#pragma unroll
+        for (int r = 0; r < 4; ++r)
+          hs[p][n][r] = a.S0 != nullptr ? a.S0[gstate + (size_t)(16 * n + 4 * g + r) * a.P + 16 * p + i] : 0.f;
+      }
     }
-  }
   // score tiles above the diagonal that share a k block with one on it
-  for (int k = threadIdx.x; k < 2 * 16 * 16; k += NTH) {
+  for (int k = wh * 64 + l; k < 2 * 16 * 16; k += NW * 64) {
     const int blk = k >> 8, r = (k >> 4) & 15, c = k & 15;
-    sM[Tile<Q>::at(32 * blk + r, 32 * blk + 16 + c)] = (bf16_t)0.f;
+    sM[sub][Tile<Q>::at(32 * blk + r, 32 * blk + 16 + c)] = (bf16_t)0.f;
   }
+  bf16x4 out[PTW][TT];
+  const auto store = [&](int k) {
+    const int t0 = (c0 + k) * Q;
+#pragma unroll
+    for (int tt = 0; tt < TT; ++tt) {
+      const int t = t0 + 16 * tt + i;
+      if (t < len) {
+#pragma unroll
+        for (int p = 0; p < PTW; ++p) *reinterpret_cast<bf16x4*>(py + (long long)t * a.ys.t + 16 * p) = out[p][tt];
+      }
+    }
+  };
   for (int k = 0; k < steps; ++k) {
     const int t0 = (c0 + k) * Q;
-    __syncthreads();
-    lb.store(sB);
-    lc.store(sC);
-    lx.store(sX);
-    if (k % NW == 0 && k + wave_id() < steps) chunk_scalars(a, b, h, (c0 + k + wave_id()) * Q, len, scal[wave_id()]);
-    if (k + 1 < steps) {
-      lb.load(pb, a.bs.t, t0 + Q, len);
-      lc.load(pc, a.cs.t, t0 + Q, len);
-      lx.load(px, a.xs.t, t0 + Q, len);
+    __syncthreads();  // the last chunk's reads are over
+    lb.load(sB, pb + (long long)t0 * a.bs.t, len - t0);
+    lc.load(sC, pc + (long long)t0 * a.cs.t, len - t0);
+#pragma unroll
+    for (int q = 0; q < HP; ++q) {
+      const int v = pl.hv0 + q;
+      lx.load(sX[q], (const bf16_t*)a.x + b * a.xs.b + v / a.nsl * a.xs.h + v % a.nsl * PW + (long long)t0 * a.xs.t, len - t0);
     }
+    if (k % NB == 0) {  // the next NB chunks' scalars, the head's waves in turn
+#pragma unroll
+      for (int q = 0; q < NB; q += NW)
+        if (q + wh < NB && k + q + wh < steps) put_scalars<true>(chunk_token(a, b, h, t0 + (q + wh) * Q, len), scal[sub][q + wh]);
+    }
+    bf16x8 hf[PTW][KN];
+#pragma unroll
+    for (int p = 0; p < PTW; ++p)
+#pragma unroll
+      for (int n = 0; n < KN; ++n) hf[p][n] = round8(hs[p][2 * n], 2 * n + 1 < NT ? hs[p][2 * n + 1 < NT ? 2 * n + 1 : 0] : zero4());
+    loads_done();
     __syncthreads();
-    const Scal& sc = scal[k % NW];
-    // M, tile (ts, tt): rows s, columns t
-    for (int idx = wave_id(); idx < 10; idx += NW) {
-      int tt = 0, ts = idx;
-      while (ts > tt) ts -= ++tt;
-      f32x4 acc = zero4();
+    if (k > 0) store(k - 1);
+    // scores: ten tiles (rows s, columns t) over the waves; a wave without one forms the last tile again.  Here and below
+    // the k block is the outer loop, so that neighbouring products go to different accumulators.
+    constexpr int SL = (10 + NWG - 1) / NWG;
+    int stt[SL], sts[SL];
+    f32x4 sacc[SL];
 #pragma unroll
-      for (int n = 0; n < KN; ++n) acc = mfma(frag_row<N>(sB, 16 * ts, 32 * n), frag_row<N>(sC, 16 * tt, 32 * n), acc);
-      const int t = 16 * tt + i;
-      bf16x4 m;
+    for (int q = 0; q < SL; ++q) {
+      const int idx = min(wv + NWG * q, 9);
+      stt[q] = idx >= 6 ? 3 : idx >= 3 ? 2 : idx >= 1 ? 1 : 0;
+      sts[q] = idx - stt[q] * (stt[q] + 1) / 2;
+      sacc[q] = zero4();
+    }
 #pragma unroll
-      for (int r = 0; r < 4; ++r) {
-        const int s = 16 * ts + 4 * g + r;
-        m[r] = (bf16_t)(s <= t ? acc[r] * (decay(sc, t, s) * sc.d[s]) : 0.f);
+    for (int n = 0; n < KN; ++n)
+#pragma unroll
+      for (int q = 0; q < SL; ++q) sacc[q] = mfma(frag_row<N>(sB, 16 * sts[q], 32 * n), frag_row<N>(sC, 16 * stt[q], 32 * n), sacc[q]);
+#pragma unroll
+    for (int q = 0; q < SL; ++q) {
+      const int t = 16 * stt[q] + i, s0 = 16 * sts[q] + 4 * g;
+#pragma unroll
+      for (int u = 0; u < HP; ++u) {
+        const Scal& sc = scal[u][k % NB];
+        const float cht = sc.ch[t];  // its float32 digits are enough for a score that is rounded to bfloat16
+        const f32x4 chs = *reinterpret_cast<const f32x4*>(sc.ch + s0), ds = *reinterpret_cast<const f32x4*>(sc.d + s0);
+        bf16x4 m;
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+          float v = keep(sacc[q][r] * (__builtin_amdgcn_exp2f(cht - chs[r]) * ds[r]), s0 + r <= t);
+          if (stt[q] == sts[q]) v += s0 + r == t ? Dh[u] : 0.f;  // the skip term: D x_t = D x_s for s = t
+          m[r] = (bf16_t)v;
+        }
+        *reinterpret_cast<bf16x4*>(sM[u] + Tile<Q>::at(t, s0)) = m;
       }
-      *reinterpret_cast<bf16x4*>(sM + Tile<Q>::at(t, 16 * ts + 4 * g)) = m;
     }
-    bf16x8 hf[KN];
-#pragma unroll
-    for (int n = 0; n < KN; ++n) hf[n] = round8(hs[2 * n < NT ? 2 * n : 0], 2 * n + 1 < NT ? hs[2 * n + 1 < NT ? 2 * n + 1 : 0] : zero4());
     __syncthreads();
+    const Scal& sc = scal[sub][k % NB];
+    const bf16_t* tX = sX[sub];
+    f32x4 yt[PTW][TT];
 #pragma unroll
-    for (int tt = 0; tt < Q / 16; ++tt) {
-      const int t = 16 * tt + i;
-      f32x4 acc = zero4();
+    for (int p = 0; p < PTW; ++p)
 #pragma unroll
-      for (int n = 0; n < KN; ++n) acc = mfma(hf[n], frag_o<N>(sC, 16 * tt, 32 * n), acc);
-      acc *= sc.eo[t];
+      for (int tt = 0; tt < TT; ++tt) yt[p][tt] = zero4();
 #pragma unroll
-      for (int kb = 0; kb <= tt / 2; ++kb) acc = mfma(frag_t<PW>(sX, 32 * kb, 16 * pt), frag_o<Q>(sM, 16 * tt, 32 * kb), acc);
-      const bf16x4 xv = *reinterpret_cast<const bf16x4*>(sX + Tile<PW>::at(t, 16 * pt + 4 * g));
-      bf16x4 o;
+    for (int n = 0; n < KN; ++n)
 #pragma unroll
-      for (int r = 0; r < 4; ++r) o[r] = (bf16_t)(acc[r] + Dh * (float)xv[r]);
-      if (t0 + t < len) *reinterpret_cast<bf16x4*>(py + (long long)(t0 + t) * a.ys.t) = o;
+      for (int tt = 0; tt < TT; ++tt) {
+        const bf16x8 fc = frag_o<N>(sC, 16 * tt, 32 * n);
+#pragma unroll
+        for (int p = 0; p < PTW; ++p) yt[p][tt] = mfma(hf[p][n], fc, yt[p][tt]);
+      }
+#pragma unroll
+    for (int tt = 0; tt < TT; ++tt) {
+      const float eo = sc.eo[16 * tt + i];
+#pragma unroll
+      for (int p = 0; p < PTW; ++p) yt[p][tt] *= eo;
     }
     const float dec = sc.dec;
 #pragma unroll
-    for (int n = 0; n < NT; ++n) hs[n] *= dec;
+    for (int p = 0; p < PTW; ++p)
 #pragma unroll
-    for (int k0 = 0; k0 < Q; k0 += 32) {
-      bf16x8 f[3];
-      weighted<PW>(f, sX, k0, 16 * pt, sc.w, sc.d);
+      for (int n = 0; n < NT; ++n) hs[p][n] *= dec;
 #pragma unroll
-      for (int n = 0; n < NT; ++n) {
-        const bf16x8 fb = frag_t<N>(sB, k0, 16 * n);
+    for (int kb = 0; kb < 2; ++kb) {
+      bf16x8 fx[PTW], f[PTW][3];
 #pragma unroll
-        for (int q = 2; q >= 0; --q) hs[n] = mfma(fb, f[q], hs[n]);
+      for (int p = 0; p < PTW; ++p) fx[p] = frag_t<PW>(tX, 32 * kb, 16 * (pt0 + p));
+#pragma unroll
+      for (int tt = 2 * kb; tt < TT; ++tt) {
+        const bf16x8 fm = frag_o<Q>(sM[sub], 16 * tt, 32 * kb);
+#pragma unroll
+        for (int p = 0; p < PTW; ++p) yt[p][tt] = mfma(fx[p], fm, yt[p][tt]);
       }
+#pragma unroll
+      for (int p = 0; p < PTW; ++p) weighted(f[p], fx[p], 32 * kb, sc.w);
+      bf16x8 fb[NT];
+#pragma unroll
+      for (int n = 0; n < NT; ++n) fb[n] = frag_t<N>(sB, 32 * kb, 16 * n);
+#pragma unroll
+      for (int q = 2; q >= 0; --q)
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+          for (int p = 0; p < PTW; ++p) hs[p][n] = mfma(fb[n], f[p][q], hs[p][n]);
     }
+#pragma unroll
+    for (int tt = 0; tt < TT; ++tt)
+#pragma unroll
+      for (int p = 0; p < PTW; ++p)
+#pragma unroll
+        for (int r = 0; r < 4; ++r) out[p][tt][r] = (bf16_t)yt[p][tt][r];
   }
+  if (steps > 0) store(steps - 1);
   if (seg == a.nseg - 1) {
 #pragma unroll
-    for (int n = 0; n < NT; ++n)
+    for (int p = 0; p < PTW; ++p)
 #pragma unroll
-      for (int r = 0; r < 4; ++r) a.S_final[gstate + (size_t)(16 * n + 4 * g + r) * a.P + i] = hs[n][r];
+      for (int n = 0; n < NT; ++n)
+#pragma unroll
+        for (int r = 0; r < 4; ++r) a.S_final[gstate + (size_t)(16 * n + 4 * g + r) * a.P + 16 * p + i] = hs[p][n][r];
   }
 }
 
-// Gradients of one chunk for one group, as ssm::grad_kernel (the same grid, formulas and sums).  The four waves share
-//   * the ten score tiles, three or two each, kept for every head;
+// <p, q> over 8 pairs of bfloat16, added to v in float32.
+__device__ __forceinline__ float dot8(const bf16x8& p, const bf16x8& q, float v) {
+#ifdef __HIP_DEVICE_COMPILE__  // the host pass does not know the builtin
+  v = __builtin_amdgcn_fdot2_f32_bf16(__builtin_shufflevector(p, p, 0, 1), __builtin_shufflevector(q, q, 0, 1), v, false);
+  v = __builtin_amdgcn_fdot2_f32_bf16(__builtin_shufflevector(p, p, 2, 3), __builtin_shufflevector(q, q, 2, 3), v, false);
+  v = __builtin_amdgcn_fdot2_f32_bf16(__builtin_shufflevector(p, p, 4, 5), __builtin_shufflevector(q, q, 4, 5), v, false);
+  v = __builtin_amdgcn_fdot2_f32_bf16(__builtin_shufflevector(p, p, 6, 7), __builtin_shufflevector(q, q, 6, 7), v, false);
+#endif
+  return v;
+}
+
+// Gradients of one chunk for one group, as ssm::grad_kernel (the same grid, formulas and sums).  The eight waves share
+//   * the ten score tiles, two or one each, kept for every head;
 //   * the products with the states by columns n (each wave loads its own part of H and R, from memory to registers);
 //   * dx by columns p, with R's leading part passed on through LDS.
+// Eight waves rather than four: a wave's accumulators and operands then fit its registers (four waves spilled, or ran alone
+// on a SIMD: 183 us where eight take 111, 8 x 12 x 2048 tokens with N = 128, P = 64).
+// The skip term sits on the scores' diagonal (D dy_s = D dy_t for t = s), and dD is the sum of the diagonal of dy x^T.
 template <int N, int PW>
-__global__ __launch_bounds__(256) void grad_kernel(SsmArgs a) {
-  constexpr int NT = N / 16, PT = PW / 16, KN = kblocks<N>(), KP = kblocks<PW>();
-  constexpr int NTW = NT >= 4 ? NT / 4 : 1, SL = NT / NTW, TTW = NT / NTW < 4 ? NT / NTW : 4;  // n tiles per wave, slices, token tiles
+__global__ __launch_bounds__(512, 2) void grad_kernel(SsmArgs a) {
+  constexpr int NT = N / 16, PT = PW / 16, KN = kblocks<N>(), KP = kblocks<PW>(), WV = 8;
+  constexpr int NB = 2;                            // heads per batch of scalars
+  constexpr int SLOTS = 2;                         // score tiles per wave
+  constexpr int TTW = NT * 4 > WV ? NT * 4 / WV : 1;  // token tiles of a wave's column tile n; N = 16 leaves half the waves without
+  constexpr int STW = PT * 4 > WV ? PT * 4 / WV : 1;  // token tiles of a wave's column tile p in dx; P = 16 likewise
   __shared__ __attribute__((aligned(16))) bf16_t sB[Q * N];
   __shared__ __attribute__((aligned(16))) bf16_t sC[Q * N];
   __shared__ __attribute__((aligned(16))) bf16_t sX[Q * PW];
   __shared__ __attribute__((aligned(16))) bf16_t sY[Q * PW];  // dy
   __shared__ __attribute__((aligned(16))) bf16_t sM[Q * Q];   // [t][s]
   __shared__ __attribute__((aligned(16))) bf16_t sR[N < 32 ? 32 * PW : N * PW];  // [n][p]
-  __shared__ Scal scal[4];
-  __shared__ float sRow[10][16], sCol[10][16], sDiag[Q], sI[SL][Q], sJ[SL][Q], sK[4], sDD[4];
+  __shared__ Scal scal[NB];
+  __shared__ float sSig[NB][Q], sRow[10][16], sCol[10][16], sDiag[Q], sXY[Q], sI[NT][Q], sJ[NT][Q], sK[WV];
   const int ch = blockIdx.x, bg = blockIdx.z, b = bg / a.G, grp = bg % a.G, t0 = ch * Q;
-  const int w = wave_id(), tid = threadIdx.x, l = lane_id(), g = l >> 4, i = l & 15;
+  const int w = __builtin_amdgcn_readfirstlane(wave_id()), tid = threadIdx.x, l = lane_id(), g = l >> 4, i = l & 15;
   const int HV = a.H * a.nsl, per_group = HV / a.G;
   const int v0 = blockIdx.y * a.per_split, v1 = min(v0 + a.per_split, per_group);
-  const int slice = w % SL, n0 = slice * NTW, tt0 = w / SL * TTW;  // this wave's part of the products with the states
-  const int pw = w % PT, st0 = w / PT * PT;                        // its part of dx: column tile, token tiles st0 .. st0 + PT - 1
+  const int nt = w % NT, tt0 = w / NT * TTW;   // this wave's part of the products with the states
+  const int pw = w % PT, st0 = w / PT * STW;   // its part of dx
+  const bool has_n = tt0 < 4, has_p = st0 < 4;
   {
-    Stage<N, 256> lb, lc;
-    lb.load((const bf16_t*)a.bm + b * a.bs.b + grp * a.bs.h, a.bs.t, t0, a.T);
-    lc.load((const bf16_t*)a.cm + b * a.cs.b + grp * a.cs.h, a.cs.t, t0, a.T);
-    lb.store(sB);
-    lc.store(sC);
+    Rows<N, WV> lb, lc;
+    lb.init(a.bs.t);
+    lc.init(a.cs.t);
+    lb.load(sB, (const bf16_t*)a.bm + b * a.bs.b + grp * a.bs.h + (long long)t0 * a.bs.t, a.T - t0);
+    lc.load(sC, (const bf16_t*)a.cm + b * a.cs.b + grp * a.cs.h + (long long)t0 * a.cs.t, a.T - t0);
   }
-  for (int k = tid; k < 2 * 16 * 16; k += 256) {  // score tiles above the diagonal inside a k block
+  for (int k = tid; k < 2 * 16 * 16; k += 512) {  // score tiles above the diagonal inside a k block
     const int blk = k >> 8, r = (k >> 4) & 15, c = k & 15;
     sM[Tile<Q>::at(32 * blk + r, 32 * blk + 16 + c)] = (bf16_t)0.f;
   }
   if constexpr (N < 32)
-    for (int k = tid; k < 16 * PW; k += 256) sR[16 * PW + k] = (bf16_t)0.f;  // the empty half of the only k block
-  Stage<PW, 256> lx, ly;
-  const auto load_head = [&](int v) {
-    const int hv = grp * per_group + v, h = hv / a.nsl, p0 = hv % a.nsl * PW;
-    lx.load((const bf16_t*)a.x + b * a.xs.b + h * a.xs.h + p0, a.xs.t, t0, a.T);
-    ly.load((const bf16_t*)a.dy + b * a.dys.b + h * a.dys.h + p0, a.dys.t, t0, a.T);
-  };
-  load_head(v0);
+    for (int k = tid; k < 16 * PW; k += 512) sR[16 * PW + k] = (bf16_t)0.f;  // the empty half of the only k block
+  Rows<PW, WV> lx, ly;
+  lx.init(a.xs.t);
+  ly.init(a.dys.t);
+  loads_done();
   __syncthreads();
-  int stt[3], sts[3];  // this wave's score tiles w, w + 4, w + 8
-  f32x4 gm[3], dg[3], dc[NTW][TTW], db[NTW][TTW];
+  int stt[SLOTS], sts[SLOTS];  // this wave's score tiles w, w + 8
+  f32x4 gm[SLOTS], dg[SLOTS], dc[TTW], db[TTW];
 #pragma unroll
-  for (int k = 0; k < 3; ++k) {
-    int tt = 0, ts = w + 4 * k;
-    while (ts > tt) ts -= ++tt;
-    stt[k] = tt, sts[k] = ts;
+  for (int k = 0; k < SLOTS; ++k) {
+    const int idx = min(w + WV * k, 9);
+    stt[k] = idx >= 6 ? 3 : idx >= 3 ? 2 : idx >= 1 ? 1 : 0;
+    sts[k] = idx - stt[k] * (stt[k] + 1) / 2;
     gm[k] = dg[k] = zero4();
-    if (w + 4 * k < 10)
+    if (w + WV * k < 10)
 #pragma unroll
-      for (int n = 0; n < KN; ++n) gm[k] = mfma(frag_row<N>(sB, 16 * ts, 32 * n), frag_row<N>(sC, 16 * tt, 32 * n), gm[k]);
+      for (int n = 0; n < KN; ++n) gm[k] = mfma(frag_row<N>(sB, 16 * sts[k], 32 * n), frag_row<N>(sC, 16 * stt[k], 32 * n), gm[k]);
   }
 #pragma unroll
-  for (int n = 0; n < NTW; ++n)
-#pragma unroll
-    for (int t = 0; t < TTW; ++t) dc[n][t] = db[n][t] = zero4();
+  for (int t = 0; t < TTW; ++t) dc[t] = db[t] = zero4();
   for (int v = v0; v < v1; ++v) {
-    const int hv = grp * per_group + v, h = hv / a.nsl, sl = hv % a.nsl, p0 = sl * PW;
+    const int hv = grp * per_group + v, h = hv / a.nsl, sl = hv % a.nsl, p0 = sl * PW, hb = (v - v0) % NB;
     const size_t bh = (size_t)b * HV + hv;
     const bf16_t* H = reinterpret_cast<const bf16_t*>(a.st) + (bh * a.nch + ch) * (2 * N * PW);
     const bf16_t* R = reinterpret_cast<const bf16_t*>(a.st) + (((size_t)a.B * HV + bh) * a.nch + ch) * (2 * N * PW);
-    const Scal& sc = scal[(v - v0) & 3];
-    __syncthreads();
-    lx.store(sX);
-    ly.store(sY);
-    if (((v - v0) & 3) == 0 && v + w < v1) chunk_scalars(a, b, (grp * per_group + v + w) / a.nsl, t0, a.T, scal[w]);
+    const Scal& sc = scal[hb];
+    const float Dh = a.D != nullptr ? a.D[h] : 0.f;
+    __syncthreads();  // the last head's reads are over
+    lx.load(sX, (const bf16_t*)a.x + b * a.xs.b + h * a.xs.h + p0 + (long long)t0 * a.xs.t, a.T - t0);
+    ly.load(sY, (const bf16_t*)a.dy + b * a.dys.b + h * a.dys.h + p0 + (long long)t0 * a.dys.t, a.T - t0);
     // this wave's parts of the states: index n, k = p
-    bf16x8 fh[2][NTW][KP], fr[2][NTW][KP];
+    bf16x8 fh[2][KP], fr[2][KP];
+    if (has_n) {
 #pragma unroll
-    for (int q = 0; q < 2; ++q)
-#pragma unroll
-      for (int n = 0; n < NTW; ++n)
+      for (int q = 0; q < 2; ++q)
 #pragma unroll
         for (int p = 0; p < KP; ++p) {
-          const size_t at = q * (N * PW) + plane_at<N, PW>(2 * p, n0 + n);
-          if constexpr (PW == 16) {
-            const bf16x4 zero = {0, 0, 0, 0};
-            fh[q][n][p] = __builtin_shufflevector(*reinterpret_cast<const bf16x4*>(H + at), zero, 0, 1, 2, 3, 4, 5, 6, 7);
-            fr[q][n][p] = __builtin_shufflevector(*reinterpret_cast<const bf16x4*>(R + at), zero, 0, 1, 2, 3, 4, 5, 6, 7);
-          } else {
-            fh[q][n][p] = *reinterpret_cast<const bf16x8*>(H + at);
-            fr[q][n][p] = *reinterpret_cast<const bf16x8*>(R + at);
+          const bf16_t *ph = H + q * (N * PW), *pr = R + q * (N * PW);
+          bf16x4 h1 = {0, 0, 0, 0}, r1 = {0, 0, 0, 0};
+          const bf16x4 h0 = *reinterpret_cast<const bf16x4*>(ph + plane_at<N, PW>(2 * p, nt));
+          const bf16x4 r0 = *reinterpret_cast<const bf16x4*>(pr + plane_at<N, PW>(2 * p, nt));
+          if constexpr (PW >= 32) {
+            h1 = *reinterpret_cast<const bf16x4*>(ph + plane_at<N, PW>(2 * p + 1, nt));
+            r1 = *reinterpret_cast<const bf16x4*>(pr + plane_at<N, PW>(2 * p + 1, nt));
           }
+          fh[q][p] = __builtin_shufflevector(h0, h1, 0, 1, 2, 3, 4, 5, 6, 7);
+          fr[q][p] = __builtin_shufflevector(r0, r1, 0, 1, 2, 3, 4, 5, 6, 7);
         }
-    if (v + 1 < v1) load_head(v + 1);
+    }
+    if (hb == 0 && w < NB && v + w < v1) {
+      const Token tk = chunk_token(a, b, (grp * per_group + v + w) / a.nsl, t0, a.T);
+      put_scalars<false>(tk, scal[w]);
+      sSig[w][l] = tk.dz;
+    }
+    loads_done();
     __syncthreads();
     // scores: rows s, columns t
 #pragma unroll
-    for (int k = 0; k < 3; ++k) {
-      if (w + 4 * k >= 10) break;
-      const int tt = stt[k], ts = sts[k], t = 16 * tt + i;
-      f32x4 dm = zero4(), col = zero4();
+    for (int k = 0; k < SLOTS; ++k) {
+      if (w + WV * k >= 10) break;
+      const int tt = stt[k], ts = sts[k], t = 16 * tt + i, s0 = 16 * ts + 4 * g;
+      f32x4 dm = zero4(), col;
 #pragma unroll
       for (int p = 0; p < KP; ++p) dm = mfma(frag_row<PW>(sX, 16 * ts, 32 * p), frag_row<PW>(sY, 16 * tt, 32 * p), dm);
+      const float cht = sc.ch[t], clt = sc.cl[t];
+      const f32x4 chs = *reinterpret_cast<const f32x4*>(sc.ch + s0), cls = *reinterpret_cast<const f32x4*>(sc.cl + s0);
+      const f32x4 ds = *reinterpret_cast<const f32x4*>(sc.d + s0);
       float row = 0.f;
       bf16x4 m;
 #pragma unroll
       for (int r = 0; r < 4; ++r) {
-        const int s = 16 * ts + 4 * g + r;
-        const bool in = s <= t;
-        const float e = in ? decay(sc, t, s) : 0.f, d = sc.d[s];
-        const float ge = in ? gm[k][r] * e : 0.f, q = in ? ge * dm[r] : 0.f;
-        m[r] = (bf16_t)(in ? ge * d : 0.f);
-        dg[k][r] += in ? dm[r] * (e * d) : 0.f;
-        if (s < t) {
-          row += q * d;
-          col[r] = q;
+        const float e = __builtin_amdgcn_exp2f((cht - chs[r]) + (clt - cls[r])), ed = e * ds[r];
+        const float q = gm[k][r] * e * dm[r];
+        float mm = gm[k][r] * ed, dd = dm[r] * ed, off = q;
+        if (tt == ts) {
+          mm = keep(mm, s0 + r <= t) + (s0 + r == t ? Dh : 0.f);
+          dd = keep(dd, s0 + r <= t);
+          off = keep(q, s0 + r < t);
+          if (s0 + r == t) {
+            sDiag[t] = q;
+            sXY[t] = dm[r];
+          }
         }
-        if (s == t) sDiag[s] = q;
+        m[r] = (bf16_t)mm;
+        dg[k][r] += dd;
+        row += off * ds[r];
+        col[r] = off;
       }
-      *reinterpret_cast<bf16x4*>(sM + Tile<Q>::at(t, 16 * ts + 4 * g)) = m;
+      *reinterpret_cast<bf16x4*>(sM + Tile<Q>::at(t, s0)) = m;
       row = sum_groups(row);
-      if (g == 0) sRow[w + 4 * k][i] = row;
+      if (g == 0) sRow[w + WV * k][i] = row;
 #pragma unroll
-      for (int r = 0; r < 4; ++r) {
-        const float c = sum_lanes16(col[r]);
-        if (i == 0) sCol[w + 4 * k][4 * g + r] = c;
-      }
+      for (int r = 0; r < 4; ++r) col[r] = sum_lanes16(col[r]);
+      if (i == 0) *reinterpret_cast<f32x4*>(&sCol[w + WV * k][4 * g]) = col;
     }
     // products with the states: rows n, columns token
     float K = 0.f;
+    if (has_n) {
+      if (tt0 == 0) {
 #pragma unroll
-    for (int n = 0; n < NTW; ++n)
-#pragma unroll
-      for (int p = 0; p < KP; ++p) {
-#pragma unroll
-        for (int e = 0; e < 8; ++e)
-          if (tt0 == 0) K += ((float)fh[0][n][p][e] + (float)fh[1][n][p][e]) * ((float)fr[0][n][p][e] + (float)fr[1][n][p][e]);
-        // R's leading part as rows n for dx
-        if (tt0 == 0) {
-          const bf16x8 f = fr[0][n][p];
-          const int row = 16 * (n0 + n) + i;
-          *reinterpret_cast<bf16x4*>(sR + Tile<PW>::at(row, 32 * p + 4 * g)) = __builtin_shufflevector(f, f, 0, 1, 2, 3);
+        for (int p = 0; p < KP; ++p) {
+          K = dot8(fh[0][p], fr[0][p], K);
+          K = dot8(fh[0][p], fr[1][p], K);
+          K = dot8(fh[1][p], fr[0][p], K);
+          // R's leading part as rows n for dx
+          const bf16x8 f = fr[0][p];
+          *reinterpret_cast<bf16x4*>(sR + Tile<PW>::at(16 * nt + i, 32 * p + 4 * g)) = __builtin_shufflevector(f, f, 0, 1, 2, 3);
           if constexpr (PW >= 32)
-            *reinterpret_cast<bf16x4*>(sR + Tile<PW>::at(row, 32 * p + 16 + 4 * g)) = __builtin_shufflevector(f, f, 4, 5, 6, 7);
+            *reinterpret_cast<bf16x4*>(sR + Tile<PW>::at(16 * nt + i, 32 * p + 16 + 4 * g)) = __builtin_shufflevector(f, f, 4, 5, 6, 7);
         }
       }
+      f32x4 uc[TTW], ub[TTW];
 #pragma unroll
-    for (int tk = 0; tk < TTW; ++tk) {
-      const int tt = tt0 + tk, t = 16 * tt + i;
-      const float eo = sc.eo[t], ww = sc.w[t], dd = sc.d[t];
-      float I = 0.f, J = 0.f;
-      bf16x8 by[KP], bx[KP];
+      for (int k = 0; k < TTW; ++k) uc[k] = ub[k] = zero4();
 #pragma unroll
-      for (int p = 0; p < KP; ++p) {
-        by[p] = frag_o<PW>(sY, 16 * tt, 32 * p);
-        bx[p] = frag_o<PW>(sX, 16 * tt, 32 * p);
-      }
+      for (int p = 0; p < KP; ++p)
 #pragma unroll
-      for (int n = 0; n < NTW; ++n) {
-        f32x4 uc = zero4(), ub = zero4();
+        for (int k = 0; k < TTW; ++k) {
+          const bf16x8 by = frag_o<PW>(sY, 16 * (tt0 + k), 32 * p), bx = frag_o<PW>(sX, 16 * (tt0 + k), 32 * p);
 #pragma unroll
-        for (int q = 1; q >= 0; --q)
-#pragma unroll
-          for (int p = 0; p < KP; ++p) {
-            uc = mfma(fh[q][n][p], by[p], uc);
-            ub = mfma(fr[q][n][p], bx[p], ub);
+          for (int q = 1; q >= 0; --q) {
+            uc[k] = mfma(fh[q][p], by, uc[k]);
+            ub[k] = mfma(fr[q][p], bx, ub[k]);
           }
-        const bf16x4 fc = *reinterpret_cast<const bf16x4*>(sC + Tile<N>::at(t, 16 * (n0 + n) + 4 * g));
-        const bf16x4 fb = *reinterpret_cast<const bf16x4*>(sB + Tile<N>::at(t, 16 * (n0 + n) + 4 * g));
+        }
+#pragma unroll
+      for (int k = 0; k < TTW; ++k) {
+        const int t = 16 * (tt0 + k) + i;
+        const float eo = sc.eo[t], ww = sc.w[t], wd = ww * sc.d[t];
+        const bf16x4 fc = *reinterpret_cast<const bf16x4*>(sC + Tile<N>::at(t, 16 * nt + 4 * g));
+        const bf16x4 fb = *reinterpret_cast<const bf16x4*>(sB + Tile<N>::at(t, 16 * nt + 4 * g));
+        float I = 0.f, J = 0.f;
 #pragma unroll
         for (int r = 0; r < 4; ++r) {
-          uc[r] *= eo;
-          ub[r] *= ww;
-          I += (float)fc[r] * uc[r];
-          J += (float)fb[r] * ub[r];
-          dc[n][tk][r] += uc[r];
-          db[n][tk][r] += dd * ub[r];
+          I += (float)fc[r] * uc[k][r];
+          J += (float)fb[r] * ub[k][r];
+          dc[k][r] += eo * uc[k][r];
+          db[k][r] += wd * ub[k][r];
+        }
+        I = sum_groups(I);
+        J = sum_groups(J);
+        if (g == 0) {
+          sI[nt][t] = I * eo;
+          sJ[nt][t] = J * ww;
         }
       }
-      I = sum_groups(I);
-      J = sum_groups(J);
-      if (g == 0) {
-        sI[slice][t] = I;
-        sJ[slice][t] = J;
-      }
+      K = sum_groups(sum_lanes16(K));
     }
-    K = sum_groups(sum_lanes16(K));
     if (l == 0) sK[w] = K;
     __syncthreads();
     // dx: rows p, columns s
-    const float Dh = a.D != nullptr ? a.D[h] : 0.f;
-    float xd = 0.f;
+    if (has_p) {
+      f32x4 ax[STW];
 #pragma unroll
-    for (int sk = 0; sk < PT; ++sk) {
-      const int st = st0 + sk, s = 16 * st + i;
-      f32x4 acc = zero4();
+      for (int k = 0; k < STW; ++k) ax[k] = zero4();
 #pragma unroll
-      for (int n = 0; n < KN; ++n) acc = mfma(frag_t<PW>(sR, 32 * n, 16 * pw), frag_o<N>(sB, 16 * st, 32 * n), acc);
-      acc *= sc.w[s] * sc.d[s];
+      for (int n = 0; n < KN; ++n) {
+        const bf16x8 f = frag_t<PW>(sR, 32 * n, 16 * pw);
 #pragma unroll
-      for (int kb = 0; kb < 2; ++kb)
-        if (kb >= st / 2) acc = mfma(frag_t<PW>(sY, 32 * kb, 16 * pw), frag_t<Q>(sM, 32 * kb, 16 * st), acc);
-      const bf16x4 yv = *reinterpret_cast<const bf16x4*>(sY + Tile<PW>::at(s, 16 * pw + 4 * g));
-      const bf16x4 xv = *reinterpret_cast<const bf16x4*>(sX + Tile<PW>::at(s, 16 * pw + 4 * g));
-      bf16x4 o;
-#pragma unroll
-      for (int r = 0; r < 4; ++r) {
-        o[r] = (bf16_t)(acc[r] + Dh * (float)yv[r]);
-        xd += (float)xv[r] * (float)yv[r];
+        for (int k = 0; k < STW; ++k) ax[k] = mfma(f, frag_o<N>(sB, 16 * (st0 + k), 32 * n), ax[k]);
       }
-      if (t0 + s < a.T)
-        *reinterpret_cast<bf16x4*>((bf16_t*)a.dx + b * a.dxs.b + h * a.dxs.h + (long long)(t0 + s) * a.dxs.t + p0 + 16 * pw + 4 * g) = o;
+#pragma unroll
+      for (int k = 0; k < STW; ++k) {
+        const int s = 16 * (st0 + k) + i;
+        ax[k] *= sc.w[s] * sc.d[s];
+      }
+#pragma unroll
+      for (int kb = 0; kb < 2; ++kb) {
+        const bf16x8 f = frag_t<PW>(sY, 32 * kb, 16 * pw);
+#pragma unroll
+        for (int k = 0; k < STW; ++k)
+          if (kb >= (st0 + k) / 2) ax[k] = mfma(f, frag_t<Q>(sM, 32 * kb, 16 * (st0 + k)), ax[k]);
+      }
+#pragma unroll
+      for (int k = 0; k < STW; ++k) {
+        const int s = 16 * (st0 + k) + i;
+        bf16x4 o;
+#pragma unroll
+        for (int r = 0; r < 4; ++r) o[r] = (bf16_t)ax[k][r];
+        if (t0 + s < a.T)
+          *reinterpret_cast<bf16x4*>((bf16_t*)a.dx + b * a.dxs.b + h * a.dxs.h + (long long)(t0 + s) * a.dxs.t + p0 + 16 * pw + 4 * g) = o;
+      }
     }
-    xd = sum_groups(sum_lanes16(xd));
-    if (l == 0) sDD[w] = xd;
-    __syncthreads();
-    if (w == ((v - v0) & 3)) {  // the head's scalars, the waves in turn
+    if (w == ((v - v0) & (WV - 1))) {  // the head's scalars, the waves in turn
       const int t = l, tt = t >> 4;
-      float row = 0.f, qoff = 0.f, I = 0.f, J0 = 0.f, kk = 0.f;
+      float row = 0.f, qoff = 0.f, I = 0.f, J0 = 0.f;
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
         if (k <= tt) row += sRow[tt * (tt + 1) / 2 + k][t & 15];
         if (k >= tt) qoff += sCol[k * (k + 1) / 2 + tt][t & 15];
-        kk += sK[k];
       }
 #pragma unroll
-      for (int k = 0; k < SL; ++k) {
+      for (int k = 0; k < NT; ++k) {
         I += sI[k][t];
         J0 += sJ[k][t];
       }
+      float kk = 0.f;
+#pragma unroll
+      for (int k = 0; k < WV; ++k) kk += sK[k];
       const float d = sc.d[t], Ah = a.A[h];
       const double jd = (double)d * J0;
       const double f = (double)row - (double)d * qoff + I;
-      const double fs = wave_scan(f, t), ftot = __shfl(fs, 63, 64);  // suffix sum from t: ftot - fs + f
-      const double js = wave_scan(jd, t);                            // prefix sum before t: js - jd
+      const double fs = wave_scan(f), ftot = last_lane(fs);  // suffix sum from t: ftot - fs + f
+      const double js = wave_scan(jd);                       // prefix sum before t: js - jd
       const float dl = (float)((ftot - fs + f) + (js - jd) + (double)(sc.dec * kk));
-      const float ddt = (qoff + sDiag[t] + J0 + Ah * dl) * sc.sig[t];
+      const float ddt = (qoff + sDiag[t] + J0 + Ah * dl) * sSig[hb][t];
       const bool in = t0 + t < a.T;
       if (in) {
         const size_t at = ((size_t)b * a.H + h) * a.T + t0 + t;
         if (a.nsl == 1) a.ddt[at] = ddt;
         else a.part_ddt[(size_t)sl * a.B * a.H * a.T + at] = ddt;
       }
-      double sa = in ? (double)dl * d : 0.0, sb = in ? (double)ddt : 0.0;
-#pragma unroll
-      for (int o = 1; o < 64; o <<= 1) {
-        sa += __shfl_xor(sa, o, 64);
-        sb += __shfl_xor(sb, o, 64);
-      }
+      const double sa = last_lane(wave_scan(in ? (double)dl * d : 0.0)), sb = last_lane(wave_scan(in ? (double)ddt : 0.0));
+      const double sd = last_lane(wave_scan((double)sXY[t]));
       if (t == 0) {
         const size_t at = bh * a.nch + ch, n = (size_t)a.B * HV * a.nch;
         a.part_sum[at] = (float)sa;
-        a.part_sum[n + at] = (sDD[0] + sDD[1]) + (sDD[2] + sDD[3]);
+        a.part_sum[n + at] = (float)sd;
         a.part_sum[2 * n + at] = (float)sb;
       }
     }
@@ -634,39 +809,37 @@ __global__ __launch_bounds__(256) void grad_kernel(SsmArgs a) {
   // the summed score gradients times B and C
   __syncthreads();
 #pragma unroll
-  for (int k = 0; k < 3; ++k) {
-    if (w + 4 * k >= 10) break;
+  for (int k = 0; k < SLOTS; ++k) {
+    if (w + WV * k >= 10) break;
     bf16x4 o;
 #pragma unroll
     for (int r = 0; r < 4; ++r) o[r] = (bf16_t)dg[k][r];
     *reinterpret_cast<bf16x4*>(sM + Tile<Q>::at(16 * stt[k] + i, 16 * sts[k] + 4 * g)) = o;
   }
   __syncthreads();
+  if (!has_n) return;
 #pragma unroll
-  for (int n = 0; n < NTW; ++n) {
+  for (int k = 0; k < TTW; ++k) {
+    const int tt = tt0 + k, t = 16 * tt + i, c = 16 * nt + 4 * g;
 #pragma unroll
-    for (int tk = 0; tk < TTW; ++tk) {
-      const int tt = tt0 + tk, t = 16 * tt + i, c = 16 * (n0 + n) + 4 * g;
+    for (int kb = 0; kb < 2; ++kb) {
+      if (kb <= tt / 2) dc[k] = mfma(frag_t<N>(sB, 32 * kb, 16 * nt), frag_o<Q>(sM, 16 * tt, 32 * kb), dc[k]);
+      if (kb >= tt / 2) db[k] = mfma(frag_t<N>(sC, 32 * kb, 16 * nt), frag_t<Q>(sM, 32 * kb, 16 * tt), db[k]);
+    }
+    if (t0 + t >= a.T) continue;
+    if (a.nsplit == 1) {
+      bf16x4 ob, oc;
 #pragma unroll
-      for (int kb = 0; kb < 2; ++kb) {
-        if (kb <= tt / 2) dc[n][tk] = mfma(frag_t<N>(sB, 32 * kb, 16 * (n0 + n)), frag_o<Q>(sM, 16 * tt, 32 * kb), dc[n][tk]);
-        if (kb >= tt / 2) db[n][tk] = mfma(frag_t<N>(sC, 32 * kb, 16 * (n0 + n)), frag_t<Q>(sM, 32 * kb, 16 * tt), db[n][tk]);
+      for (int r = 0; r < 4; ++r) {
+        ob[r] = (bf16_t)db[k][r];
+        oc[r] = (bf16_t)dc[k][r];
       }
-      if (t0 + t >= a.T) continue;
-      if (a.nsplit == 1) {
-        bf16x4 ob, oc;
-#pragma unroll
-        for (int r = 0; r < 4; ++r) {
-          ob[r] = (bf16_t)db[n][tk][r];
-          oc[r] = (bf16_t)dc[n][tk][r];
-        }
-        *reinterpret_cast<bf16x4*>((bf16_t*)a.dbm + b * a.dbs.b + grp * a.dbs.h + (long long)(t0 + t) * a.dbs.t + c) = ob;
-        *reinterpret_cast<bf16x4*>((bf16_t*)a.dcm + b * a.dcs.b + grp * a.dcs.h + (long long)(t0 + t) * a.dcs.t + c) = oc;
-      } else {
-        const size_t at = (((size_t)blockIdx.y * a.B * a.G + bg) * a.T + t0 + t) * N + c;
-        *reinterpret_cast<f32x4*>(a.part_b + at) = db[n][tk];
-        *reinterpret_cast<f32x4*>(a.part_c + at) = dc[n][tk];
-      }
+      *reinterpret_cast<bf16x4*>((bf16_t*)a.dbm + b * a.dbs.b + grp * a.dbs.h + (long long)(t0 + t) * a.dbs.t + c) = ob;
+      *reinterpret_cast<bf16x4*>((bf16_t*)a.dcm + b * a.dcs.b + grp * a.dcs.h + (long long)(t0 + t) * a.dcs.t + c) = oc;
+    } else {
+      const size_t at = (((size_t)blockIdx.y * a.B * a.G + bg) * a.T + t0 + t) * N + c;
+      *reinterpret_cast<f32x4*>(a.part_b + at) = db[k];
+      *reinterpret_cast<f32x4*>(a.part_c + at) = dc[k];
     }
   }
 }

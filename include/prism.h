@@ -504,7 +504,8 @@ prism_status prism_conv_step(const void* x, const prism_strides* x_strides, cons
  *   S_final [B, H, N, P] float32 (output): the state after the last token (S0 for a length of
  *      0).  May be the same buffer as S0.
  * Supported: N, P in {16, 32, 64, 128}; H a multiple of G; B * H * P / min(P, 64) <= 65535; rows
- * of x, Bm, Cm and y that start on 16-byte boundaries (else PRISM_ERR_UNSUPPORTED).
+ * of x, Bm, Cm and y that start on 16-byte boundaries, do not overlap from token to token and are
+ * at most 16 MB apart (else PRISM_ERR_UNSUPPORTED).
  * Precision: decays and states in float32 from log decays summed in float64.  With PRISM_BF16
  * the products run on bfloat16 operands; what enters the state is split into bfloat16 parts
  * that keep its float32 digits, the score matrix and the state's readout are rounded once.

@@ -559,12 +559,12 @@ __global__ __launch_bounds__(512, 2) void grad_kernel(SsmArgs a) {
   constexpr int STW = PT * 4 > WV ? PT * 4 / WV : 1;  // token tiles of a wave's column tile p in dx; P = 16 likewise
   __shared__ __attribute__((aligned(16))) bf16_t sB[Q * N];
   __shared__ __attribute__((aligned(16))) bf16_t sC[Q * N];
-  __shared__ __attribute__((aligned(16))) bf16_t sX[Q * PW];
-  __shared__ __attribute__((aligned(16))) bf16_t sY[Q * PW];  // dy
+  __shared__ __attribute__((aligned(16))) bf16_t sXs[2][Q * PW];
+  __shared__ __attribute__((aligned(16))) bf16_t sYs[2][Q * PW];  // dy
   __shared__ __attribute__((aligned(16))) bf16_t sM[Q * Q];   // [t][s]
   __shared__ __attribute__((aligned(16))) bf16_t sR[N < 32 ? 32 * PW : N * PW];  // [n][p]
-  __shared__ Scal scal[NB];
-  __shared__ float sSig[NB][Q], sRow[10][16], sCol[10][16], sDiag[Q], sXY[Q], sI[NT][Q], sJ[NT][Q], sK[WV];
+  __shared__ Scal scals[2][NB];
+  __shared__ float sSig[2][NB][Q], sRow[10][16], sCol[10][16], sDiag[Q], sXY[Q], sI[NT][Q], sJ[NT][Q], sK[WV];
   const int ch = blockIdx.x, bg = blockIdx.z, b = bg / a.G, grp = bg % a.G, t0 = ch * Q;
   const int w = __builtin_amdgcn_readfirstlane(wave_id()), tid = threadIdx.x, l = lane_id(), g = l >> 4, i = l & 15;
   const int HV = a.H * a.nsl, per_group = HV / a.G;
@@ -588,7 +588,36 @@ __global__ __launch_bounds__(512, 2) void grad_kernel(SsmArgs a) {
   Rows<PW, WV> lx, ly;
   lx.init(a.xs.t);
   ly.init(a.dys.t);
+  const auto load = [&](int v) {
+    const int hv = grp * per_group + v, h = hv / a.nsl, p0 = hv % a.nsl * PW, buf = (v - v0) & 1;
+    lx.load(sXs[buf], (const bf16_t*)a.x + b * a.xs.b + h * a.xs.h + p0 + (long long)t0 * a.xs.t, a.T - t0);
+    ly.load(sYs[buf], (const bf16_t*)a.dy + b * a.dys.b + h * a.dys.h + p0 + (long long)t0 * a.dys.t, a.T - t0);
+  };
+  load(v0);
+  // this wave's parts of the states: index n, k = p.  Loaded a head ahead: in flight over dx and the next head's scores.
+  bf16x8 fh[2][KP], fr[2][KP];
+  const auto load_states = [&](int v) {
+    const size_t bh = (size_t)b * HV + grp * per_group + v;
+    const bf16_t* H = reinterpret_cast<const bf16_t*>(a.st) + (bh * a.nch + ch) * (2 * N * PW);
+    const bf16_t* R = reinterpret_cast<const bf16_t*>(a.st) + (((size_t)a.B * HV + bh) * a.nch + ch) * (2 * N * PW);
+#pragma unroll
+    for (int q = 0; q < 2; ++q)
+#pragma unroll
+      for (int p = 0; p < KP; ++p) {
+        const bf16_t *ph = H + q * (N * PW), *pr = R + q * (N * PW);
+        bf16x4 h1 = {0, 0, 0, 0}, r1 = {0, 0, 0, 0};
+        const bf16x4 h0 = *reinterpret_cast<const bf16x4*>(ph + plane_at<N, PW>(2 * p, nt));
+        const bf16x4 r0 = *reinterpret_cast<const bf16x4*>(pr + plane_at<N, PW>(2 * p, nt));
+        if constexpr (PW >= 32) {
+          h1 = *reinterpret_cast<const bf16x4*>(ph + plane_at<N, PW>(2 * p + 1, nt));
+          r1 = *reinterpret_cast<const bf16x4*>(pr + plane_at<N, PW>(2 * p + 1, nt));
+        }
+        fh[q][p] = __builtin_shufflevector(h0, h1, 0, 1, 2, 3, 4, 5, 6, 7);
+        fr[q][p] = __builtin_shufflevector(r0, r1, 0, 1, 2, 3, 4, 5, 6, 7);
+      }
+  };
   loads_done();
+  load_states(v0);
   __syncthreads();
   int stt[SLOTS], sts[SLOTS];  // this wave's score tiles w, w + 8
   f32x4 gm[SLOTS], dg[SLOTS], dc[TTW], db[TTW];
@@ -607,39 +636,17 @@ __global__ __launch_bounds__(512, 2) void grad_kernel(SsmArgs a) {
   for (int v = v0; v < v1; ++v) {
     const int hv = grp * per_group + v, h = hv / a.nsl, sl = hv % a.nsl, p0 = sl * PW, hb = (v - v0) % NB;
     const size_t bh = (size_t)b * HV + hv;
-    const bf16_t* H = reinterpret_cast<const bf16_t*>(a.st) + (bh * a.nch + ch) * (2 * N * PW);
-    const bf16_t* R = reinterpret_cast<const bf16_t*>(a.st) + (((size_t)a.B * HV + bh) * a.nch + ch) * (2 * N * PW);
-    const Scal& sc = scal[hb];
+    const int par = ((v - v0) / NB) & 1;
+    const Scal& sc = scals[par][hb];
+    const bf16_t *sX = sXs[(v - v0) & 1], *sY = sYs[(v - v0) & 1];
     const float Dh = a.D != nullptr ? a.D[h] : 0.f;
-    __syncthreads();  // the last head's reads are over
-    lx.load(sX, (const bf16_t*)a.x + b * a.xs.b + h * a.xs.h + p0 + (long long)t0 * a.xs.t, a.T - t0);
-    ly.load(sY, (const bf16_t*)a.dy + b * a.dys.b + h * a.dys.h + p0 + (long long)t0 * a.dys.t, a.T - t0);
-    // this wave's parts of the states: index n, k = p
-    bf16x8 fh[2][KP], fr[2][KP];
-    if (has_n) {
-#pragma unroll
-      for (int q = 0; q < 2; ++q)
-#pragma unroll
-        for (int p = 0; p < KP; ++p) {
-          const bf16_t *ph = H + q * (N * PW), *pr = R + q * (N * PW);
-          bf16x4 h1 = {0, 0, 0, 0}, r1 = {0, 0, 0, 0};
-          const bf16x4 h0 = *reinterpret_cast<const bf16x4*>(ph + plane_at<N, PW>(2 * p, nt));
-          const bf16x4 r0 = *reinterpret_cast<const bf16x4*>(pr + plane_at<N, PW>(2 * p, nt));
-          if constexpr (PW >= 32) {
-            h1 = *reinterpret_cast<const bf16x4*>(ph + plane_at<N, PW>(2 * p + 1, nt));
-            r1 = *reinterpret_cast<const bf16x4*>(pr + plane_at<N, PW>(2 * p + 1, nt));
-          }
-          fh[q][p] = __builtin_shufflevector(h0, h1, 0, 1, 2, 3, 4, 5, 6, 7);
-          fr[q][p] = __builtin_shufflevector(r0, r1, 0, 1, 2, 3, 4, 5, 6, 7);
-        }
-    }
-    if (hb == 0 && w < NB && v + w < v1) {
+    if (hb == 0 && w < NB && v + w < v1) {  // the next NB heads' scalars; the other half may still be read
       const Token tk = chunk_token(a, b, (grp * per_group + v + w) / a.nsl, t0, a.T);
-      put_scalars<false>(tk, scal[w]);
-      sSig[w][l] = tk.dz;
+      put_scalars<false>(tk, scals[par][w]);
+      sSig[par][w][l] = tk.dz;
     }
-    loads_done();
-    __syncthreads();
+    __syncthreads();  // every wave has its rows of this head (waited for below), the last head's reads are over
+    if (v + 1 < v1) load(v + 1);
     // scores: rows s, columns t
 #pragma unroll
     for (int k = 0; k < SLOTS; ++k) {
@@ -733,6 +740,9 @@ __global__ __launch_bounds__(512, 2) void grad_kernel(SsmArgs a) {
       K = sum_groups(sum_lanes16(K));
     }
     if (l == 0) sK[w] = K;
+    loads_done();  // the next head's rows
+    // unconditional (the last head's again): behind a branch the compiler would wait for them at the barrier
+    load_states(min(v + 1, v1 - 1));
     __syncthreads();
     // dx: rows p, columns s
     if (has_p) {
@@ -789,7 +799,7 @@ __global__ __launch_bounds__(512, 2) void grad_kernel(SsmArgs a) {
       const double fs = wave_scan(f), ftot = last_lane(fs);  // suffix sum from t: ftot - fs + f
       const double js = wave_scan(jd);                       // prefix sum before t: js - jd
       const float dl = (float)((ftot - fs + f) + (js - jd) + (double)(sc.dec * kk));
-      const float ddt = (qoff + sDiag[t] + J0 + Ah * dl) * sSig[hb][t];
+      const float ddt = (qoff + sDiag[t] + J0 + Ah * dl) * sSig[par][hb][t];
       const bool in = t0 + t < a.T;
       if (in) {
         const size_t at = ((size_t)b * a.H + h) * a.T + t0 + t;

@@ -53,6 +53,7 @@ using namespace prism;
 
 constexpr int kChunk = 64;       // tokens per chunk of the scan (ssm::Q)
 constexpr size_t kCUs = 256;     // compute units of an MI355X
+constexpr int kFold = 8;         // most segments whose entering states their readers form
 
 size_t elem(prism_dtype dt) { return dt == PRISM_BF16 ? 2 : 4; }
 bool known(prism_dtype dt) { return dt == PRISM_F32 || dt == PRISM_BF16; }
@@ -134,11 +135,18 @@ prism_status ssm_plan(int B, int H, int G, int T, int N, int P, prism_dtype ty, 
   if ((size_t)B * (size_t)H * (size_t)pl->nsl > 65535) return PRISM_ERR_UNSUPPORTED;  // (b, virtual head) pairs map to grid.y
   pl->HV = H * pl->nsl;
   pl->nch = (int)(((long long)T + kChunk - 1) / kChunk);
-  // Segments until there are two workgroups per CU: a segment costs a state in the workspace and a second read of
-  // its inputs, so no more than fill the device, and at least two chunks each.
-  const size_t bh = (size_t)B * pl->HV, want = std::max<size_t>(1, 2 * kCUs / bh);
-  pl->seg_chunks = (int)std::max<size_t>(2, (pl->nch + want - 1) / want);
-  pl->nseg = (pl->nch + pl->seg_chunks - 1) / pl->seg_chunks;
+  // Segments until the device is full: each costs a state in the workspace and a second read of its inputs.  Up to
+  // kFold of them the passes form their entering states themselves; the forward then takes twice as many, since its
+  // sweep is bound by the chunks it walks one after another (8 x 24 x 2048 tokens: 137 us with 2 segments, 93 with 5;
+  // 2 x 4 x 16384, where a scan over the segments comes on top: 48 us with 64, 51 with 128; the backward's passes at
+  // 8 x 12 x 2048: 96 us with 5, 105 with 8).
+  const size_t bh = (size_t)B * pl->HV;
+  const auto cut = [&](size_t want) {
+    pl->seg_chunks = (int)std::max<size_t>(2, (pl->nch + want - 1) / want);
+    pl->nseg = (pl->nch + pl->seg_chunks - 1) / pl->seg_chunks;
+  };
+  cut(std::max<size_t>(1, 4 * kCUs / bh));
+  if (bwd || pl->nseg > kFold) cut(std::max<size_t>(1, 2 * kCUs / bh));
   const size_t mat = (size_t)N * pl->PW;
   Layout ly;
   const int dirs = bwd ? 2 : 1;
@@ -220,7 +228,7 @@ prism_status prism_ssm_fwd(const void* x, const prism_strides* x_strides, const 
   if (!aligned16(workspace)) return PRISM_ERR_INVALID_ARG;
   a.x = x, a.bm = Bm, a.cm = Cm, a.dt = dt, a.dt_bias = dt_bias, a.A = A, a.D = D, a.lens = lens, a.S0 = S0;
   a.B = B, a.H = H, a.G = G, a.T = T, a.P = P, a.softplus = softplus != 0;
-  a.nsl = pl.nsl, a.nch = pl.nch, a.seg_chunks = pl.seg_chunks, a.nseg = pl.nseg;
+  a.nsl = pl.nsl, a.nch = pl.nch, a.seg_chunks = pl.seg_chunks, a.nseg = pl.nseg, a.fold = pl.nseg <= kFold;
   a.y = y, a.S_final = S_final;
   a.seg = at<float>(workspace, pl.seg), a.seg_dec = at<float>(workspace, pl.seg_dec);
   return host::launch_ssm_fwd(ty, N, pl.PW, a, stream);
@@ -257,7 +265,7 @@ prism_status prism_ssm_bwd(const void* x, const prism_strides* x_strides, const 
   if (!aligned16(workspace)) return PRISM_ERR_INVALID_ARG;
   a.x = x, a.bm = Bm, a.cm = Cm, a.dy = dy, a.dt = dt, a.dt_bias = dt_bias, a.A = A, a.D = D;
   a.B = B, a.H = H, a.G = G, a.T = T, a.P = P, a.softplus = softplus != 0;
-  a.nsl = pl.nsl, a.nch = pl.nch, a.seg_chunks = pl.seg_chunks, a.nseg = pl.nseg;
+  a.nsl = pl.nsl, a.nch = pl.nch, a.seg_chunks = pl.seg_chunks, a.nseg = pl.nseg, a.fold = pl.nseg <= kFold;
   a.seg = at<float>(workspace, pl.seg), a.seg_dec = at<float>(workspace, pl.seg_dec);
   a.st = at<float>(workspace, pl.st), a.dS = dS_final;
   a.dx = dx, a.dbm = dBm, a.dcm = dCm, a.ddt = ddt, a.dA = dA, a.dD = dD, a.ddt_bias = ddt_bias;

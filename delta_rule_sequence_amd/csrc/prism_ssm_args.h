@@ -17,6 +17,7 @@ struct SsmArgs {
   int B, H, G, T, P, softplus;
   int nsl;                        // slices per head
   int nch, seg_chunks, nseg;      // 64-token chunks, chunks per segment, segments
+  int fold;                       // entering states are formed by their readers (few segments), not by a scan of their own
   const float* S0;
   void* y;
   prism_strides ys;

@@ -161,23 +161,19 @@ __device__ __forceinline__ size_t plane_at(int pt, int nt) {
   return ((size_t)nt * (PW / 16) + pt) * 256 + lane_id() * 4;
 }
 
-// Workgroups of one (batch, group, segment) read the same B and C.  They are numbered next to each other and, since the
-// hardware deals workgroups out to the eight XCDs in turn, every eighth workgroup takes the next number: their rows are
-// then read into one XCD's L2 once.
-__device__ __forceinline__ int xcd_order(int id, int total) {
-  const int q = total / 8, r = total % 8, x = id % 8;
-  return x * q + min(x, r) + id / 8;
-}
-
 // The place of a workgroup of the passes over segments: HP virtual heads of one group from hv0 on, one segment.  Grid
-// (B * HV / HP * segments, directions).
+// (B * HV / HP * segments, directions).  The workgroups of one (batch, group, segment) read the same rows of B and C, so
+// they take neighbouring numbers; the hardware deals workgroups out to the eight XCDs in turn, so each XCD is given a
+// range of numbers of its own, and reads those rows into its L2 once.  (Dealing single units out to the XCDs instead:
+// the state pass of 8 x 12 x 2048 tokens 70 us, this way 61.)
 struct Place {
   int b, hv0, seg;
 };
 template <int HP>
 __device__ __forceinline__ Place place(const SsmArgs& a, int segs) {
   const int HV = a.H * a.nsl, pg = HV / a.G / HP;  // workgroups per (batch, group, segment)
-  int id = xcd_order(blockIdx.x, gridDim.x);
+  const int q = gridDim.x / 8, r = gridDim.x % 8, x = blockIdx.x % 8;
+  int id = x * q + min(x, r) + blockIdx.x / 8;
   const int u = id % pg;
   id /= pg;
   const int seg = id % segs;
@@ -185,18 +181,61 @@ __device__ __forceinline__ Place place(const SsmArgs& a, int segs) {
   return {id / a.G, (id % a.G) * (HV / a.G) + u * HP, seg};
 }
 
-// Column tiles (16 columns) per wave: an operand of B or C read from LDS serves PTW products.
-template <int PW> constexpr int tiles_per_wave() { return PW >= 32 ? 2 : 1; }
-template <int PW> constexpr int waves_per_head() { return PW / 16 / tiles_per_wave<PW>(); }
+// The given first state of virtual head hv of batch b (rev: the adjoint of its last), tiles pt0 .. of 16 columns.
+template <int N, int PTW, bool TRANS>
+__device__ __forceinline__ void first_state(f32x4 (&acc)[PTW][N / 16], const SsmArgs& a, int rev, int b, int hv, int p0) {
+  const int l = lane_id(), g = l >> 4, i = l & 15;
+  const float* init = rev ? a.dS : a.S0;
+  const size_t at = (size_t)(b * a.H + hv / a.nsl) * N * a.P + p0;
+#pragma unroll
+  for (int p = 0; p < PTW; ++p)
+#pragma unroll
+    for (int n = 0; n < N / 16; ++n) {
+      acc[p][n] = zero4();
+      if (init != nullptr) {
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+          const int row = TRANS ? 16 * n + i : 16 * n + 4 * g + r, col = 16 * p + (TRANS ? 4 * g + r : i);
+          acc[p][n][r] = init[at + (size_t)row * a.P + col];
+        }
+      }
+    }
+}
+// The state that enters segment seg (rev: the adjoint that arrives at its end) from the ends of the segments before it: what
+// seg_scan_kernel forms, for few segments.  The end that nobody needs gives its place to the first state, which the sweep
+// thus does not read from S0 (S_final may be the same buffer).
+template <int N, int PW, int PTW, bool TRANS>
+__device__ __forceinline__ void entering(f32x4 (&acc)[PTW][N / 16], const SsmArgs& a, int rev, int b, int bh, int hv, int seg, int pt0) {
+  if (a.nseg == 1) return first_state<N, PTW, TRANS>(acc, a, rev, b, hv, hv % a.nsl * PW + 16 * pt0);
+  const size_t slot = ((size_t)rev * a.B * a.H * a.nsl + bh) * a.nseg;
+  const int spare = rev ? 0 : a.nseg - 1;
+#pragma unroll
+  for (int p = 0; p < PTW; ++p)
+#pragma unroll
+    for (int n = 0; n < N / 16; ++n) acc[p][n] = *reinterpret_cast<const f32x4*>(a.seg + (slot + spare) * (N * PW) + tile_at<N>(pt0 + p, n));
+  for (int k = 0; k < (rev ? a.nseg - 1 - seg : seg); ++k) {
+    const int s = rev ? a.nseg - 1 - k : k;
+    const float dec = a.seg_dec[slot + s];
+#pragma unroll
+    for (int p = 0; p < PTW; ++p)
+#pragma unroll
+      for (int n = 0; n < N / 16; ++n)
+        acc[p][n] = acc[p][n] * dec + *reinterpret_cast<const f32x4*>(a.seg + (slot + s) * (N * PW) + tile_at<N>(pt0 + p, n));
+  }
+}
+
+// PTW: column tiles (16 columns) per wave.  With two, an operand of B or C read from LDS serves two products; with one,
+// a head has twice the waves.
+template <int PW, int PTW> constexpr int waves_per_head() { return PW / 16 / PTW; }
 
 // States of a segment, as ssm::state_kernel, for HP virtual heads of a group at once (they share the rows of B or C).
 // A wave owns PTW tiles of 16 columns of one head.  SAVE = false: from zero, the end state to seg (H: rows n, columns p, as
 // the sweep keeps it; or, for the backward, transposed); the segment whose end nobody reads is left out.  SAVE = true:
 // from the entering state, saving the state in front of every chunk in two planes.  The next chunk's rows arrive in the
 // second half of the tiles meanwhile.
-template <int N, int PW, int HP, bool TRANS, bool SAVE>
-__global__ __launch_bounds__(waves_per_head<PW>() * HP * 64, 2) void state_kernel(SsmArgs a) {
-  constexpr int PTW = tiles_per_wave<PW>(), NW = waves_per_head<PW>(), NWG = NW * HP, NT = N / 16, NB = 4;  // chunks per batch of weights
+template <int N, int PW, int PTW, int HP, bool TRANS, bool SAVE>
+__global__ __launch_bounds__((waves_per_head<PW, PTW>() * HP * 64), 2) void state_kernel(SsmArgs a) {
+  constexpr int NW = waves_per_head<PW, PTW>(), NWG = NW * HP, NT = N / 16, NB = 4;  // chunks per batch of weights
   __shared__ __attribute__((aligned(16))) bf16_t sA[2][Q * N];
   __shared__ __attribute__((aligned(16))) bf16_t sV[2][HP][Q * PW];
   __shared__ __attribute__((aligned(16))) float sWt[2][HP][NB][Q];
@@ -221,11 +260,23 @@ __global__ __launch_bounds__(waves_per_head<PW>() * HP * 64, 2) void state_kerne
     pv[q] = rev ? (const bf16_t*)a.dy + b * a.dys.b + v / a.nsl * a.dys.h + off : (const bf16_t*)a.x + b * a.xs.b + v / a.nsl * a.xs.h + off;
   }
   f32x4 acc[PTW][NT];
+  if (!SAVE && a.fold && seg == (rev ? a.nseg - 1 : 0)) {  // see entering()
+    first_state<N, PTW, TRANS>(acc, a, rev, b, hv, hv % a.nsl * PW + 16 * wh * PTW);
+    float* spare = a.seg + (((size_t)rev * a.B * HV + bh) * a.nseg + (rev ? 0 : a.nseg - 1)) * (N * PW);
 #pragma unroll
-  for (int p = 0; p < PTW; ++p)
+    for (int p = 0; p < PTW; ++p)
 #pragma unroll
-    for (int n = 0; n < NT; ++n)
-      acc[p][n] = SAVE ? *reinterpret_cast<const f32x4*>(a.seg + slot * (N * PW) + tile_at<N>(wh * PTW + p, n)) : zero4();
+      for (int n = 0; n < NT; ++n) *reinterpret_cast<f32x4*>(spare + tile_at<N>(wh * PTW + p, n)) = acc[p][n];
+  }
+  if (SAVE && a.fold) {
+    entering<N, PW, PTW, TRANS>(acc, a, rev, b, bh, hv, seg, wh * PTW);
+  } else {
+#pragma unroll
+    for (int p = 0; p < PTW; ++p)
+#pragma unroll
+      for (int n = 0; n < NT; ++n)
+        acc[p][n] = SAVE ? *reinterpret_cast<const f32x4*>(a.seg + slot * (N * PW) + tile_at<N>(wh * PTW + p, n)) : zero4();
+  }
   // chunks that hold tokens, in walking order
   const int live = min(c1, (len + Q - 1) / Q) - c0, steps = SAVE ? c1 - c0 : max(live, 0), last = SAVE ? c1 - 1 : c0 + steps - 1;
   Rows<N, NWG> la;
@@ -315,7 +366,7 @@ __global__ __launch_bounds__(waves_per_head<PW>() * HP * 64, 2) void state_kerne
 
 // The scan over segments (see ssm::seg_scan_kernel); TRANS: which way the tiles lie.
 template <int N, int PW, bool TRANS>
-__global__ __launch_bounds__(256) void seg_scan_kernel(SsmArgs a, int has_end) {
+__global__ __launch_bounds__(256) void seg_scan_kernel(SsmArgs a) {
   const int e = blockIdx.x * 256 + threadIdx.x, bh = blockIdx.y, rev = blockIdx.z;
   const int HV = a.H * a.nsl, b = bh / HV, hv = bh % HV, h = hv / a.nsl, p0 = hv % a.nsl * PW;
   const int tile = e >> 8, row = ((e >> 6) & 3) * 4 + (e & 3), col = (e >> 2) & 15;  // position inside a 16 x 16 tile
@@ -330,7 +381,7 @@ __global__ __launch_bounds__(256) void seg_scan_kernel(SsmArgs a, int has_end) {
 #pragma unroll
     for (int u = 0; u < U; ++u) {
       const int k = k0 + u, s = rev ? a.nseg - 1 - k : k;
-      if (k >= a.nseg - 1 || !has_end) break;  // nothing enters from the last segment's end
+      if (k >= a.nseg - 1) break;  // nothing enters from the last segment's end
       own[u] = q[(size_t)s * (N * PW)];
       d[u] = dec[s];
     }
@@ -339,7 +390,7 @@ __global__ __launch_bounds__(256) void seg_scan_kernel(SsmArgs a, int has_end) {
       const int k = k0 + u, s = rev ? a.nseg - 1 - k : k;
       if (k >= a.nseg) break;
       q[(size_t)s * (N * PW)] = v;
-      if (has_end && k < a.nseg - 1) v = d[u] * v + own[u];
+      if (k < a.nseg - 1) v = d[u] * v + own[u];
     }
   }
 }
@@ -348,9 +399,9 @@ __global__ __launch_bounds__(256) void seg_scan_kernel(SsmArgs a, int has_end) {
 // share B, C and their products: a wave forms C B^T tiles and the scores of all HP heads from them.  y tiles are formed
 // transposed (rows p, columns t), so that a lane stores 4 neighbouring columns; they are stored one chunk later, so that no
 // wave waits for its stores before the next rows.
-template <int N, int PW, int HP>
-__global__ __launch_bounds__(waves_per_head<PW>() * HP * 64, 2) void sweep_kernel(SsmArgs a) {
-  constexpr int PTW = tiles_per_wave<PW>(), NW = waves_per_head<PW>(), NWG = NW * HP, NT = N / 16, KN = kblocks<N>(), TT = Q / 16;
+template <int N, int PW, int PTW, int HP>
+__global__ __launch_bounds__((waves_per_head<PW, PTW>() * HP * 64), 2) void sweep_kernel(SsmArgs a) {
+  constexpr int NW = waves_per_head<PW, PTW>(), NWG = NW * HP, NT = N / 16, KN = kblocks<N>(), TT = Q / 16;
   constexpr int NB = 2;  // chunks per batch of scalars
   __shared__ __attribute__((aligned(16))) bf16_t sB[Q * N];
   __shared__ __attribute__((aligned(16))) bf16_t sC[Q * N];
@@ -378,18 +429,15 @@ __global__ __launch_bounds__(waves_per_head<PW>() * HP * 64, 2) void sweep_kerne
   lx.init(a.xs.t);
   // state tiles: rows n = 16 nt + 4 g + r, column 16 (pt0 + p) + i
   f32x4 hs[PTW][NT];
+  if (a.fold) {
+    entering<N, PW, PTW, false>(hs, a, 0, b, bh, hv, seg, pt0);
+  } else {
 #pragma unroll
-  for (int p = 0; p < PTW; ++p)
+    for (int p = 0; p < PTW; ++p)
 #pragma unroll
-    for (int n = 0; n < NT; ++n) {
-      if (a.nseg > 1) {
+      for (int n = 0; n < NT; ++n)
         hs[p][n] = *reinterpret_cast<const f32x4*>(a.seg + ((size_t)bh * a.nseg + seg) * (N * PW) + tile_at<N>(pt0 + p, n));
-      } else {
-#pragma unroll
-        for (int r = 0; r < 4; ++r)
-          hs[p][n][r] = a.S0 != nullptr ? a.S0[gstate + (size_t)(16 * n + 4 * g + r) * a.P + 16 * p + i] : 0.f;
-      }
-    }
+  }
   // score tiles above the diagonal that share a k block with one on it
   for (int k = wh * 64 + l; k < 2 * 16 * 16; k += NW * 64) {
     const int blk = k >> 8, r = (k >> 4) & 15, c = k & 15;

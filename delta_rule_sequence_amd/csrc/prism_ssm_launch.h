@@ -9,29 +9,33 @@ namespace host {
 inline prism_status launched() { return hipGetLastError() == hipSuccess ? PRISM_OK : PRISM_ERR_HIP; }
 
 // HP: virtual heads of a group per workgroup (two where their number is even: they share the rows of B and C).
-template <int N, int PW, int HP>
+// PTW: column tiles per wave.
+template <int N, int PW, int PTW, int HP>
 void ssm_fwd_mx(const SsmArgs& a, hipStream_t stream) {
-  const int bh = a.B * a.H * a.nsl, nth = ssm::mx::waves_per_head<PW>() * HP * 64;
+  const int bh = a.B * a.H * a.nsl, nth = ssm::mx::waves_per_head<PW, PTW>() * HP * 64;
   if (a.nseg > 1) {
-    ssm::mx::state_kernel<N, PW, HP, false, false><<<dim3(bh / HP * (a.nseg - 1), 1), nth, 0, stream>>>(a);
-    ssm::mx::seg_scan_kernel<N, PW, false><<<dim3(N * PW / 256, bh, 1), 256, 0, stream>>>(a, 1);
+    ssm::mx::state_kernel<N, PW, PTW, HP, false, false><<<dim3(bh / HP * (a.nseg - 1), 1), nth, 0, stream>>>(a);
+    if (!a.fold) ssm::mx::seg_scan_kernel<N, PW, false><<<dim3(N * PW / 256, bh, 1), 256, 0, stream>>>(a);
   }
-  ssm::mx::sweep_kernel<N, PW, HP><<<dim3(bh / HP * a.nseg), nth, 0, stream>>>(a);
+  ssm::mx::sweep_kernel<N, PW, PTW, HP><<<dim3(bh / HP * a.nseg), nth, 0, stream>>>(a);
 }
-template <int N, int PW, int HP>
+template <int N, int PW, int PTW, int HP>
 void ssm_bwd_states_mx(const SsmArgs& a, hipStream_t stream) {
-  const int bh = a.B * a.H * a.nsl, nth = ssm::mx::waves_per_head<PW>() * HP * 64;
-  if (a.nseg > 1) ssm::mx::state_kernel<N, PW, HP, true, false><<<dim3(bh / HP * (a.nseg - 1), 2), nth, 0, stream>>>(a);
-  ssm::mx::seg_scan_kernel<N, PW, true><<<dim3(N * PW / 256, bh, 2), 256, 0, stream>>>(a, a.nseg > 1);
-  ssm::mx::state_kernel<N, PW, HP, true, true><<<dim3(bh / HP * a.nseg, 2), nth, 0, stream>>>(a);
+  const int bh = a.B * a.H * a.nsl, nth = ssm::mx::waves_per_head<PW, PTW>() * HP * 64;
+  if (a.nseg > 1) {
+    ssm::mx::state_kernel<N, PW, PTW, HP, true, false><<<dim3(bh / HP * (a.nseg - 1), 2), nth, 0, stream>>>(a);
+    if (!a.fold) ssm::mx::seg_scan_kernel<N, PW, true><<<dim3(N * PW / 256, bh, 2), 256, 0, stream>>>(a);
+  }
+  ssm::mx::state_kernel<N, PW, PTW, HP, true, true><<<dim3(bh / HP * a.nseg, 2), nth, 0, stream>>>(a);
 }
 
 template <class T, int N, int PW>
 prism_status ssm_fwd_pw(const SsmArgs& a, hipStream_t stream) {
   const int bh = a.B * a.H * a.nsl;
   if constexpr (std::is_same<T, bf16_t>::value) {
-    if (a.H / a.G * a.nsl % 2 == 0) ssm_fwd_mx<N, PW, 2>(a, stream);
-    else ssm_fwd_mx<N, PW, 1>(a, stream);
+    constexpr int PTW = PW >= 32 ? 2 : 1;
+    if (a.H / a.G * a.nsl % 2 == 0) ssm_fwd_mx<N, PW, PTW, 2>(a, stream);
+    else ssm_fwd_mx<N, PW, PTW, 1>(a, stream);
   } else {
     if (a.nseg > 1) {
       ssm::state_kernel<T, N, PW, false><<<dim3(a.nseg, bh, 1), PW * 4, 0, stream>>>(a);
@@ -46,8 +50,9 @@ template <class T, int N, int PW>
 prism_status ssm_bwd_pw(const SsmArgs& a, hipStream_t stream) {
   const int bh = a.B * a.H * a.nsl;
   if constexpr (std::is_same<T, bf16_t>::value) {
-    if (a.H / a.G * a.nsl % 2 == 0) ssm_bwd_states_mx<N, PW, 2>(a, stream);
-    else ssm_bwd_states_mx<N, PW, 1>(a, stream);
+    constexpr int PTW = PW >= 32 ? 2 : 1;
+    if (a.H / a.G * a.nsl % 2 == 0) ssm_bwd_states_mx<N, PW, PTW, 2>(a, stream);
+    else ssm_bwd_states_mx<N, PW, PTW, 1>(a, stream);
     ssm::mx::grad_kernel<N, PW><<<dim3(a.nch, a.nsplit, a.B * a.G), 512, 0, stream>>>(a);
   } else {
     if (a.nseg > 1) ssm::state_kernel<T, N, PW, false><<<dim3(a.nseg, bh, 2), PW * 4, 0, stream>>>(a);

@@ -159,10 +159,15 @@ __device__ __forceinline__ f32x4 scale4(const f32x4& f, const float* s, int k0) 
   for (int r = 0; r < 4; ++r) o[r] = f[r] * s[k0 + 4 * g + r];
   return o;
 }
-// acc[row = index of a][col = index of b] += sum over 16 k
-__device__ __forceinline__ void mm4(f32x4& acc, const f32x4& a, const f32x4& b) {
+// acc[k][row = index of a[k]][col = index of b[k]] += sum over 16 values, for K tiles at once: the values are the outer loop,
+// so that neighbouring products go to different accumulators (a product waits about eight times its issue for the one
+// before it on the same accumulator).
+template <int K>
+__device__ __forceinline__ void mm4k(f32x4 (&acc)[K], const f32x4 (&a)[K], const f32x4 (&b)[K]) {
 #pragma unroll
-  for (int r = 0; r < 4; ++r) acc = mfma(a[r], b[r], acc);
+  for (int r = 0; r < 4; ++r)
+#pragma unroll
+    for (int k = 0; k < K; ++k) acc[k] = mfma(a[k][r], b[k][r], acc[k]);
 }
 
 // A state tile in the workspace: tile (pt, nt) of a transposed state H^T [PW][N] as 64 lanes x 4 floats, lane (g, i)
@@ -226,47 +231,64 @@ __global__ __launch_bounds__(PW * 4) void state_kernel(SsmArgs a) {
 #pragma unroll
     for (int k0 = 0; k0 < Q; k0 += 16) {
       const f32x4 fv = scale4(frag_t(sV, LDP, k0, 16 * pt), sWt, k0);
+      f32x4 fvs[NT], fa[NT];
 #pragma unroll
-      for (int n = 0; n < NT; ++n) mm4(acc[n], fv, frag_t(sA, LDN, k0, 16 * n));
+      for (int n = 0; n < NT; ++n) {
+        fvs[n] = fv;
+        fa[n] = frag_t(sA, LDN, k0, 16 * n);
+      }
+      mm4k<NT>(acc, fvs, fa);
     }
   }
   if constexpr (!SAVE) {
 #pragma unroll
     for (int n = 0; n < NT; ++n) *reinterpret_cast<f32x4*>(a.seg + slot * (N * PW) + tile_at<N>(pt, n)) = acc[n];
-    if (rev == 0 && tid == 0) a.seg_dec[(size_t)bh * a.nseg + seg] = exp2f((float)log_dec);
+    if (tid == 0) a.seg_dec[slot] = exp2f((float)log_dec);
   }
 }
 
-// The states entering each segment, in place of the segments' own end states: forward from S0, and
-// (direction 1) the adjoints arriving at each segment's end, backward from dS_final.  Grid
-// (N * PW / 256, B * HV, directions), one state element per thread.
-template <int N, int PW>
-__global__ __launch_bounds__(256) void seg_scan_kernel(SsmArgs a, int has_end) {
-  const int e = blockIdx.x * 256 + threadIdx.x, bh = blockIdx.y, rev = blockIdx.z;
+// The states entering each segment, in place of the segments' own end states: forward from S0, and (direction 1) the
+// adjoints arriving at each segment's end, backward from dS_final.  Grid (N * PW / (256 / groups), B * HV, directions): a
+// thread holds up to 16 segments of one state element, `groups` (a power of two) threads share an element and pass on
+// their products of decays and local sums in LDS, so that the loads of all segments are in flight at once.  TRANS: the
+// tiles hold rows p and columns n (else rows n, columns p).
+template <int N, int PW, bool TRANS>
+__global__ __launch_bounds__(256) void seg_scan_kernel(SsmArgs a, int groups) {
+  constexpr int U = 16;
+  __shared__ float sP[256], sV[256];
+  const int el = 256 / groups, grp = threadIdx.x / el, e = blockIdx.x * el + threadIdx.x % el, bh = blockIdx.y, rev = blockIdx.z;
   const int HV = a.H * a.nsl, b = bh / HV, hv = bh % HV, h = hv / a.nsl, p0 = hv % a.nsl * PW;
-  // element (n, p) of position e (see elem_at)
-  const int tile = e >> 8, p = (tile / (N / 16)) * 16 + ((e >> 6) & 3) * 4 + (e & 3), n = (tile % (N / 16)) * 16 + ((e >> 2) & 15);
+  const int tile = e >> 8, row = ((e >> 6) & 3) * 4 + (e & 3), col = (e >> 2) & 15;  // position inside a 16 x 16 tile
+  const int p = tile / (N / 16) * 16 + (TRANS ? row : col), n = tile % (N / 16) * 16 + (TRANS ? col : row);
   const float* init = rev ? a.dS : a.S0;
-  float v = init != nullptr ? init[((size_t)(b * a.H + h) * N + n) * a.P + p0 + p] : 0.f;
-  float* q = a.seg + ((size_t)rev * gridDim.y + bh) * a.nseg * (N * PW) + e;
-  const float* dec = a.seg_dec + (size_t)bh * a.nseg;
-  constexpr int U = 16;  // loads in flight
-  for (int k0 = 0; k0 < a.nseg; k0 += U) {
-    float own[U], d[U];
+  const size_t slot = ((size_t)rev * gridDim.y + bh) * a.nseg;
+  float* q = a.seg + slot * (N * PW) + e;
+  float own[U], d[U], prod = 1.f, sum = 0.f;
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const int k = k0 + u, s = rev ? a.nseg - 1 - k : k;
-      if (k >= a.nseg || !has_end) break;
+  for (int u = 0; u < U; ++u) {
+    const int k = grp * U + u, s = rev ? a.nseg - 1 - k : k;
+    own[u] = 0.f, d[u] = 1.f;
+    if (k < a.nseg - 1) {  // nothing enters from the last segment's end
       own[u] = q[(size_t)s * (N * PW)];
-      d[u] = dec[s];
+      d[u] = a.seg_dec[slot + s];
     }
+  }
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const int k = k0 + u, s = rev ? a.nseg - 1 - k : k;
-      if (k >= a.nseg) break;
-      q[(size_t)s * (N * PW)] = v;
-      if (has_end) v = d[u] * v + own[u];
-    }
+  for (int u = 0; u < U; ++u) {
+    sum = d[u] * sum + own[u];
+    prod *= d[u];
+  }
+  sP[threadIdx.x] = prod;
+  sV[threadIdx.x] = sum;
+  float v = init != nullptr ? init[((size_t)(b * a.H + h) * N + n) * a.P + p0 + p] : 0.f;
+  __syncthreads();
+  for (int k = 0; k < grp; ++k) v = sP[k * el + threadIdx.x % el] * v + sV[k * el + threadIdx.x % el];
+#pragma unroll
+  for (int u = 0; u < U; ++u) {
+    const int k = grp * U + u, s = rev ? a.nseg - 1 - k : k;
+    if (k >= a.nseg) break;
+    q[(size_t)s * (N * PW)] = v;
+    v = d[u] * v + own[u];
   }
 }
 
@@ -306,37 +328,76 @@ __global__ __launch_bounds__(PW * 4) void sweep_kernel(SsmArgs a) {
     load_rows<T, PW, LDP>(sX, a.x, b * a.xs.b + h * a.xs.h + p0, a.xs.t, t0, len, NTH);
     if (tid < 64) put_scalars<false>(chunk_token(a, b, h, t0, len), sc);
     __syncthreads();
-    // M, tile (ts, tt): rows s, columns t
-    for (int idx = wave_id(); idx < 10; idx += NW) {
-      int tt = 0, ts = idx;
-      while (ts > tt) ts -= ++tt;
-      f32x4 acc = zero4();
+    // M: ten tiles (rows s, columns t) over the waves, TG of a wave's at a time; a wave without one forms the last again
+    constexpr int SL = (10 + NW - 1) / NW, TG = SL > 5 ? 5 : SL;
 #pragma unroll
-      for (int n = 0; n < NT; ++n) mm4(acc, frag_k(sB, LDN, 16 * ts, 16 * n), frag_k(sC, LDN, 16 * tt, 16 * n));
-      const int t = 16 * tt + i;
-      f32x4 m;
+    for (int q0 = 0; q0 < SL; q0 += TG) {
+      f32x4 acc[TG];
+      int stt[TG], sts[TG];
 #pragma unroll
-      for (int r = 0; r < 4; ++r) {
-        const int s = 16 * ts + 4 * g + r;
-        m[r] = s <= t ? acc[r] * exp2f((sc.ch[t] - sc.ch[s]) + (sc.cl[t] - sc.cl[s])) * sc.d[s] : 0.f;
+      for (int q = 0; q < TG; ++q) {
+        const int idx = min(pt + NW * (q0 + q), 9);
+        stt[q] = idx >= 6 ? 3 : idx >= 3 ? 2 : idx >= 1 ? 1 : 0;
+        sts[q] = idx - stt[q] * (stt[q] + 1) / 2;
+        acc[q] = zero4();
       }
-      *reinterpret_cast<f32x4*>(sM + t * LDQ + 16 * ts + 4 * g) = m;
+#pragma unroll
+      for (int n = 0; n < NT; ++n) {
+        f32x4 fb[TG], fc[TG];
+#pragma unroll
+        for (int q = 0; q < TG; ++q) {
+          fb[q] = frag_k(sB, LDN, 16 * sts[q], 16 * n);
+          fc[q] = frag_k(sC, LDN, 16 * stt[q], 16 * n);
+        }
+        mm4k<TG>(acc, fb, fc);
+      }
+#pragma unroll
+      for (int q = 0; q < TG; ++q) {
+        const int t = 16 * stt[q] + i;
+        f32x4 m;
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+          const int s = 16 * sts[q] + 4 * g + r;
+          m[r] = s <= t ? acc[q][r] * exp2f((sc.ch[t] - sc.ch[s]) + (sc.cl[t] - sc.cl[s])) * sc.d[s] : 0.f;
+        }
+        *reinterpret_cast<f32x4*>(sM + t * LDQ + 16 * sts[q] + 4 * g) = m;
+      }
     }
     __syncthreads();
+    f32x4 yt[Q / 16];
+#pragma unroll
+    for (int tt = 0; tt < Q / 16; ++tt) yt[tt] = zero4();
+#pragma unroll
+    for (int n = 0; n < NT; ++n) {
+      f32x4 fh[Q / 16], fc[Q / 16];
+#pragma unroll
+      for (int tt = 0; tt < Q / 16; ++tt) {
+        fh[tt] = hs[n];
+        fc[tt] = frag_k(sC, LDN, 16 * tt, 16 * n);
+      }
+      mm4k<Q / 16>(yt, fh, fc);
+    }
+#pragma unroll
+    for (int tt = 0; tt < Q / 16; ++tt) yt[tt] *= sc.eo[16 * tt + i];
+#pragma unroll
+    for (int ts = 0; ts < Q / 16; ++ts) {
+      const f32x4 fx = frag_t(sX, LDP, 16 * ts, 16 * pt);
+      f32x4 fm[Q / 16];
+#pragma unroll
+      for (int tt = ts; tt < Q / 16; ++tt) fm[tt] = frag_k(sM, LDQ, 16 * tt, 16 * ts);
+#pragma unroll
+      for (int r = 0; r < 4; ++r)
+#pragma unroll
+        for (int tt = ts; tt < Q / 16; ++tt) yt[tt] = mfma(fx[r], fm[tt][r], yt[tt]);
+    }
 #pragma unroll
     for (int tt = 0; tt < Q / 16; ++tt) {
       const int t = 16 * tt + i;
-      f32x4 acc = zero4();
-#pragma unroll
-      for (int n = 0; n < NT; ++n) mm4(acc, hs[n], frag_k(sC, LDN, 16 * tt, 16 * n));
-      acc *= sc.eo[t];
-#pragma unroll
-      for (int ts = 0; ts <= tt; ++ts) mm4(acc, frag_t(sX, LDP, 16 * ts, 16 * pt), frag_k(sM, LDQ, 16 * tt, 16 * ts));
       const f32x4 xv = *reinterpret_cast<const f32x4*>(sX + t * LDP + 16 * pt + 4 * g);
       if (t0 + t < len) {
         out4 o;
 #pragma unroll
-        for (int r = 0; r < 4; ++r) o[r] = (T)(acc[r] + Dh * xv[r]);
+        for (int r = 0; r < 4; ++r) o[r] = (T)(yt[tt][r] + Dh * xv[r]);
         T* y = reinterpret_cast<T*>(a.y) + b * a.ys.b + h * a.ys.h + (long long)(t0 + t) * a.ys.t + p0 + 16 * pt + 4 * g;
         *reinterpret_cast<out4*>(y) = o;
       }
@@ -347,8 +408,13 @@ __global__ __launch_bounds__(PW * 4) void sweep_kernel(SsmArgs a) {
 #pragma unroll
     for (int k0 = 0; k0 < Q; k0 += 16) {
       const f32x4 fx = scale4(scale4(frag_t(sX, LDP, k0, 16 * pt), sc.w, k0), sc.d, k0);
+      f32x4 fxs[NT], fb[NT];
 #pragma unroll
-      for (int n = 0; n < NT; ++n) mm4(hs[n], frag_t(sB, LDN, k0, 16 * n), fx);
+      for (int n = 0; n < NT; ++n) {
+        fxs[n] = fx;
+        fb[n] = frag_t(sB, LDN, k0, 16 * n);
+      }
+      mm4k<NT>(hs, fb, fxs);
     }
   }
   if (seg == a.nseg - 1) {
@@ -388,12 +454,16 @@ __global__ __launch_bounds__(256) void grad_kernel(SsmArgs a) {
   const int tok = 16 * w + i;  // this lane's token
   f32x4 gm[4], dg[4], dc[NT], db[NT];
 #pragma unroll
-  for (int ts = 0; ts < 4; ++ts) {
-    gm[ts] = zero4();
-    dg[ts] = zero4();
-    if (ts <= w)
+  for (int ts = 0; ts < 4; ++ts) gm[ts] = dg[ts] = zero4();
 #pragma unroll
-      for (int n = 0; n < NT; ++n) mm4(gm[ts], frag_k(sB, LDN, 16 * ts, 16 * n), frag_k(sC, LDN, 16 * w, 16 * n));
+  for (int n = 0; n < NT; ++n) {
+    f32x4 fb[4], fc[4];
+#pragma unroll
+    for (int ts = 0; ts < 4; ++ts) {
+      fb[ts] = frag_k(sB, LDN, 16 * ts, 16 * n);
+      fc[ts] = frag_k(sC, LDN, 16 * w, 16 * n);
+    }
+    mm4k<4>(gm, fb, fc);  // the tiles after the diagonal are formed too, and not used
   }
 #pragma unroll
   for (int n = 0; n < NT; ++n) dc[n] = db[n] = zero4();
@@ -412,13 +482,25 @@ __global__ __launch_bounds__(256) void grad_kernel(SsmArgs a) {
     }
     __syncthreads();
     float row = 0.f;
+    f32x4 dms[4];
+#pragma unroll
+    for (int ts = 0; ts < 4; ++ts) dms[ts] = zero4();
+#pragma unroll
+    for (int p = 0; p < PT; ++p) {
+      f32x4 fx[4], fy[4];
+#pragma unroll
+      for (int ts = 0; ts < 4; ++ts) {
+        fx[ts] = frag_k(sX, LDP, 16 * ts, 16 * p);
+        fy[ts] = frag_k(sY, LDP, 16 * w, 16 * p);
+      }
+      mm4k<4>(dms, fx, fy);
+    }
 #pragma unroll
     for (int ts = 0; ts < 4; ++ts) {
       f32x4 col = zero4();
       if (ts <= w) {
-        f32x4 dm = zero4(), m;
-#pragma unroll
-        for (int p = 0; p < PT; ++p) mm4(dm, frag_k(sX, LDP, 16 * ts, 16 * p), frag_k(sY, LDP, 16 * w, 16 * p));
+        f32x4 m;
+        const f32x4 dm = dms[ts];
 #pragma unroll
         for (int r = 0; r < 4; ++r) {
           const int s = 16 * ts + 4 * g + r;
@@ -445,29 +527,40 @@ __global__ __launch_bounds__(256) void grad_kernel(SsmArgs a) {
     // products with the states: rows n, columns token
     float I = 0.f, J = 0.f, K = 0.f;
     const float eo = sc.eo[tok], ww = sc.w[tok], dd = sc.d[tok];
+    constexpr int NG = NT >= 2 ? 2 : 1;  // columns tiles at a time: four independent chains of products
 #pragma unroll
-    for (int n = 0; n < NT; ++n) {
-      f32x4 uc = zero4(), ub = zero4();
+    for (int n1 = 0; n1 < NT; n1 += NG) {
+      f32x4 u[2 * NG];
+#pragma unroll
+      for (int k = 0; k < 2 * NG; ++k) u[k] = zero4();
 #pragma unroll
       for (int p = 0; p < PT; ++p) {
-        const f32x4 fh = *reinterpret_cast<const f32x4*>(H + tile_at<N>(p, n));
-        const f32x4 fr = *reinterpret_cast<const f32x4*>(R + tile_at<N>(p, n));
-        mm4(uc, fh, frag_k(sY, LDP, 16 * w, 16 * p));
-        mm4(ub, fr, frag_k(sX, LDP, 16 * w, 16 * p));
-        if ((p * NT + n) % 4 == w)
+        f32x4 f[2 * NG], v2[2 * NG];
 #pragma unroll
-          for (int r = 0; r < 4; ++r) K += fh[r] * fr[r];
+        for (int k = 0; k < NG; ++k) {
+          f[2 * k] = *reinterpret_cast<const f32x4*>(H + tile_at<N>(p, n1 + k));
+          f[2 * k + 1] = *reinterpret_cast<const f32x4*>(R + tile_at<N>(p, n1 + k));
+          v2[2 * k] = frag_k(sY, LDP, 16 * w, 16 * p);
+          v2[2 * k + 1] = frag_k(sX, LDP, 16 * w, 16 * p);
+          if ((p * NT + n1 + k) % 4 == w)
+#pragma unroll
+            for (int r = 0; r < 4; ++r) K += f[2 * k][r] * f[2 * k + 1][r];
+        }
+        mm4k<2 * NG>(u, f, v2);
       }
-      const f32x4 fc = *reinterpret_cast<const f32x4*>(sC + tok * LDN + 16 * n + 4 * g);
-      const f32x4 fb = *reinterpret_cast<const f32x4*>(sB + tok * LDN + 16 * n + 4 * g);
 #pragma unroll
-      for (int r = 0; r < 4; ++r) {
-        uc[r] *= eo;
-        ub[r] *= ww;
-        I += fc[r] * uc[r];
-        J += fb[r] * ub[r];
-        dc[n][r] += uc[r];
-        db[n][r] += dd * ub[r];
+      for (int k = 0; k < NG; ++k) {
+        const int n = n1 + k;
+        const f32x4 fc = *reinterpret_cast<const f32x4*>(sC + tok * LDN + 16 * n + 4 * g);
+        const f32x4 fb = *reinterpret_cast<const f32x4*>(sB + tok * LDN + 16 * n + 4 * g);
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+          const float uc = u[2 * k][r] * eo, ub = u[2 * k + 1][r] * ww;
+          I += fc[r] * uc;
+          J += fb[r] * ub;
+          dc[n][r] += uc;
+          db[n][r] += dd * ub;
+        }
       }
     }
     I = sum_groups(I);
@@ -482,26 +575,43 @@ __global__ __launch_bounds__(256) void grad_kernel(SsmArgs a) {
     // dx: rows p, columns s (this lane's token)
     const float Dh = a.D != nullptr ? a.D[h] : 0.f;
     float xd = 0.f;
+    f32x4 ax[PT];
+#pragma unroll
+    for (int p = 0; p < PT; ++p) ax[p] = zero4();
+#pragma unroll
+    for (int n = 0; n < NT; ++n) {
+      const f32x4 fb = frag_k(sB, LDN, 16 * w, 16 * n);
+      f32x4 fr[PT], fbs[PT];
+#pragma unroll
+      for (int p = 0; p < PT; ++p) {  // index p, k = n
+        fbs[p] = fb;
+#pragma unroll
+        for (int r = 0; r < 4; ++r) fr[p][r] = R[elem_at<N>(16 * n + 4 * g + r, 16 * p + i)];
+      }
+      mm4k<PT>(ax, fr, fbs);
+    }
+#pragma unroll
+    for (int p = 0; p < PT; ++p) ax[p] *= ww * dd;
+#pragma unroll
+    for (int tt = 0; tt < 4; ++tt) {
+      if (tt < w) continue;
+      const f32x4 fm = frag_t(sM, LDQ, 16 * tt, 16 * w);
+      f32x4 fy[PT], fms[PT];
+#pragma unroll
+      for (int p = 0; p < PT; ++p) {
+        fms[p] = fm;
+        fy[p] = frag_t(sY, LDP, 16 * tt, 16 * p);
+      }
+      mm4k<PT>(ax, fy, fms);
+    }
 #pragma unroll
     for (int p = 0; p < PT; ++p) {
-      f32x4 acc = zero4();
-#pragma unroll
-      for (int n = 0; n < NT; ++n) {
-        f32x4 fr;  // index p, k = n
-#pragma unroll
-        for (int r = 0; r < 4; ++r) fr[r] = R[elem_at<N>(16 * n + 4 * g + r, 16 * p + i)];
-        mm4(acc, fr, frag_k(sB, LDN, 16 * w, 16 * n));
-      }
-      acc *= ww * dd;
-#pragma unroll
-      for (int tt = 0; tt < 4; ++tt)
-        if (tt >= w) mm4(acc, frag_t(sY, LDP, 16 * tt, 16 * p), frag_t(sM, LDQ, 16 * tt, 16 * w));
       const f32x4 yv = *reinterpret_cast<const f32x4*>(sY + tok * LDP + 16 * p + 4 * g);
       const f32x4 xv = *reinterpret_cast<const f32x4*>(sX + tok * LDP + 16 * p + 4 * g);
       out4 o;
 #pragma unroll
       for (int r = 0; r < 4; ++r) {
-        o[r] = (T)(acc[r] + Dh * yv[r]);
+        o[r] = (T)(ax[p][r] + Dh * yv[r]);
         xd += xv[r] * yv[r];
       }
       if (t0 + tok < a.T) {
@@ -547,12 +657,28 @@ __global__ __launch_bounds__(256) void grad_kernel(SsmArgs a) {
     if (ts <= w) *reinterpret_cast<f32x4*>(sM + tok * LDQ + 16 * ts + 4 * g) = dg[ts];
   __syncthreads();
 #pragma unroll
-  for (int n = 0; n < NT; ++n) {
+  for (int ts = 0; ts < 4; ++ts) {
+    f32x4 f[NT], v2[NT];
+    if (ts <= w) {
 #pragma unroll
-    for (int ts = 0; ts < 4; ++ts) {
-      if (ts <= w) mm4(dc[n], frag_t(sB, LDN, 16 * ts, 16 * n), dg[ts]);
-      if (ts >= w) mm4(db[n], frag_t(sC, LDN, 16 * ts, 16 * n), frag_t(sM, LDQ, 16 * ts, 16 * w));
+      for (int n = 0; n < NT; ++n) {
+        f[n] = frag_t(sB, LDN, 16 * ts, 16 * n);
+        v2[n] = dg[ts];
+      }
+      mm4k<NT>(dc, f, v2);
     }
+    if (ts >= w) {
+      const f32x4 fm = frag_t(sM, LDQ, 16 * ts, 16 * w);
+#pragma unroll
+      for (int n = 0; n < NT; ++n) {
+        f[n] = frag_t(sC, LDN, 16 * ts, 16 * n);
+        v2[n] = fm;
+      }
+      mm4k<NT>(db, f, v2);
+    }
+  }
+#pragma unroll
+  for (int n = 0; n < NT; ++n) {
     if (t0 + tok < a.T) {
       const int c = 16 * n + 4 * g;
       if (a.nsplit == 1) {

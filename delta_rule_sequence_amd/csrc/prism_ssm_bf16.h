@@ -364,37 +364,6 @@ __global__ __launch_bounds__((waves_per_head<PW, PTW>() * HP * 64), 2) void stat
   }
 }
 
-// The scan over segments (see ssm::seg_scan_kernel); TRANS: which way the tiles lie.
-template <int N, int PW, bool TRANS>
-__global__ __launch_bounds__(256) void seg_scan_kernel(SsmArgs a) {
-  const int e = blockIdx.x * 256 + threadIdx.x, bh = blockIdx.y, rev = blockIdx.z;
-  const int HV = a.H * a.nsl, b = bh / HV, hv = bh % HV, h = hv / a.nsl, p0 = hv % a.nsl * PW;
-  const int tile = e >> 8, row = ((e >> 6) & 3) * 4 + (e & 3), col = (e >> 2) & 15;  // position inside a 16 x 16 tile
-  const int p = tile / (N / 16) * 16 + (TRANS ? row : col), n = tile % (N / 16) * 16 + (TRANS ? col : row);
-  const float* init = rev ? a.dS : a.S0;
-  float v = init != nullptr ? init[((size_t)(b * a.H + h) * N + n) * a.P + p0 + p] : 0.f;
-  float* q = a.seg + ((size_t)rev * gridDim.y + bh) * a.nseg * (N * PW) + e;
-  const float* dec = a.seg_dec + ((size_t)rev * gridDim.y + bh) * a.nseg;
-  constexpr int U = 16;  // loads in flight
-  for (int k0 = 0; k0 < a.nseg; k0 += U) {
-    float own[U], d[U];
-#pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const int k = k0 + u, s = rev ? a.nseg - 1 - k : k;
-      if (k >= a.nseg - 1) break;  // nothing enters from the last segment's end
-      own[u] = q[(size_t)s * (N * PW)];
-      d[u] = dec[s];
-    }
-#pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const int k = k0 + u, s = rev ? a.nseg - 1 - k : k;
-      if (k >= a.nseg) break;
-      q[(size_t)s * (N * PW)] = v;
-      if (k < a.nseg - 1) v = d[u] * v + own[u];
-    }
-  }
-}
-
 // Outputs of a segment from its entering state, as ssm::sweep_kernel, for HP virtual heads of a group at once.  The heads
 // share B, C and their products: a wave forms C B^T tiles and the scores of all HP heads from them.  y tiles are formed
 // transposed (rows p, columns t), so that a lane stores 4 neighbouring columns; they are stored one chunk later, so that no

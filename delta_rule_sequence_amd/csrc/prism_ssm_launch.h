@@ -8,6 +8,14 @@ namespace host {
 
 inline prism_status launched() { return hipGetLastError() == hipSuccess ? PRISM_OK : PRISM_ERR_HIP; }
 
+// The scan over the segments, 16 of them per thread.
+template <int N, int PW, bool TRANS>
+void seg_scan(const SsmArgs& a, int dirs, hipStream_t stream) {
+  int groups = 1;
+  while (groups * 16 < a.nseg) groups *= 2;
+  ssm::seg_scan_kernel<N, PW, TRANS><<<dim3(N * PW / 256 * groups, a.B * a.H * a.nsl, dirs), 256, 0, stream>>>(a, groups);
+}
+
 // HP: virtual heads of a group per workgroup (two where their number is even: they share the rows of B and C).
 // PTW: column tiles per wave.
 template <int N, int PW, int PTW, int HP>
@@ -15,7 +23,7 @@ void ssm_fwd_mx(const SsmArgs& a, hipStream_t stream) {
   const int bh = a.B * a.H * a.nsl, nth = ssm::mx::waves_per_head<PW, PTW>() * HP * 64;
   if (a.nseg > 1) {
     ssm::mx::state_kernel<N, PW, PTW, HP, false, false><<<dim3(bh / HP * (a.nseg - 1), 1), nth, 0, stream>>>(a);
-    if (!a.fold) ssm::mx::seg_scan_kernel<N, PW, false><<<dim3(N * PW / 256, bh, 1), 256, 0, stream>>>(a);
+    if (!a.fold) seg_scan<N, PW, false>(a, 1, stream);
   }
   ssm::mx::sweep_kernel<N, PW, PTW, HP><<<dim3(bh / HP * a.nseg), nth, 0, stream>>>(a);
 }
@@ -24,7 +32,7 @@ void ssm_bwd_states_mx(const SsmArgs& a, hipStream_t stream) {
   const int bh = a.B * a.H * a.nsl, nth = ssm::mx::waves_per_head<PW, PTW>() * HP * 64;
   if (a.nseg > 1) {
     ssm::mx::state_kernel<N, PW, PTW, HP, true, false><<<dim3(bh / HP * (a.nseg - 1), 2), nth, 0, stream>>>(a);
-    if (!a.fold) ssm::mx::seg_scan_kernel<N, PW, true><<<dim3(N * PW / 256, bh, 2), 256, 0, stream>>>(a);
+    if (!a.fold) seg_scan<N, PW, true>(a, 2, stream);
   }
   ssm::mx::state_kernel<N, PW, PTW, HP, true, true><<<dim3(bh / HP * a.nseg, 2), nth, 0, stream>>>(a);
 }
@@ -39,7 +47,7 @@ prism_status ssm_fwd_pw(const SsmArgs& a, hipStream_t stream) {
   } else {
     if (a.nseg > 1) {
       ssm::state_kernel<T, N, PW, false><<<dim3(a.nseg, bh, 1), PW * 4, 0, stream>>>(a);
-      ssm::seg_scan_kernel<N, PW><<<dim3(N * PW / 256, bh, 1), 256, 0, stream>>>(a, 1);
+      seg_scan<N, PW, true>(a, 1, stream);
     }
     ssm::sweep_kernel<T, N, PW><<<dim3(a.nseg, bh), PW * 4, 0, stream>>>(a);
   }
@@ -56,7 +64,7 @@ prism_status ssm_bwd_pw(const SsmArgs& a, hipStream_t stream) {
     ssm::mx::grad_kernel<N, PW><<<dim3(a.nch, a.nsplit, a.B * a.G), 512, 0, stream>>>(a);
   } else {
     if (a.nseg > 1) ssm::state_kernel<T, N, PW, false><<<dim3(a.nseg, bh, 2), PW * 4, 0, stream>>>(a);
-    ssm::seg_scan_kernel<N, PW><<<dim3(N * PW / 256, bh, 2), 256, 0, stream>>>(a, a.nseg > 1);
+    seg_scan<N, PW, true>(a, 2, stream);
     ssm::state_kernel<T, N, PW, true><<<dim3(a.nseg, bh, 2), PW * 4, 0, stream>>>(a);
     ssm::grad_kernel<T, N, PW><<<dim3(a.nch, a.nsplit, a.B * a.G), 256, 0, stream>>>(a);
   }

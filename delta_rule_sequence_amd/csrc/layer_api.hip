@@ -136,10 +136,10 @@ prism_status ssm_plan(int B, int H, int G, int T, int N, int P, prism_dtype ty, 
   pl->HV = H * pl->nsl;
   pl->nch = (int)(((long long)T + kChunk - 1) / kChunk);
   // Segments until the device is full: each costs a state in the workspace and a second read of its inputs.  Up to
-  // kFold of them the passes form their entering states themselves; the forward then takes twice as many, since its
-  // sweep is bound by the chunks it walks one after another (8 x 24 x 2048 tokens: 137 us with 2 segments, 93 with 5;
-  // 2 x 4 x 16384, where a scan over the segments comes on top: 48 us with 64, 51 with 128; the backward's passes at
-  // 8 x 12 x 2048: 96 us with 5, 105 with 8).
+  // kFold of them the passes form their entering states themselves; the forward then takes more, since its sweep is
+  // bound by the chunks it walks one after another (8 x 24 x 2048 tokens: 137 us with 2 segments, 94 with 5, 86 with 6,
+  // 97 with 8; 2 x 4 x 16384, where a scan over the segments comes on top: 43 us with 64, 46 with 128; the backward's
+  // passes at 8 x 12 x 2048: 96 us with 5, 105 with 8).
   // Least chunks of a segment: two for bfloat16; a float32 chunk takes longer than a segment costs (3 x 6 x 509 tokens,
   // N = P = 32: 30 us with two, 18 with one).
   const int least = ty == PRISM_BF16 || pl->nch <= 2 ? 2 : 1;
@@ -148,7 +148,7 @@ prism_status ssm_plan(int B, int H, int G, int T, int N, int P, prism_dtype ty, 
     pl->seg_chunks = std::max(std::min(pl->nch, least), (int)((pl->nch + want - 1) / want));
     pl->nseg = (pl->nch + pl->seg_chunks - 1) / pl->seg_chunks;
   };
-  cut(std::max<size_t>(1, 4 * kCUs / bh));
+  cut(std::max<size_t>(1, 5 * kCUs / bh));
   if (bwd || pl->nseg > kFold) cut(std::max<size_t>(1, 2 * kCUs / bh));
   const size_t mat = (size_t)N * pl->PW;
   Layout ly;

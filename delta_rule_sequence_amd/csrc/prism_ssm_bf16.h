@@ -213,14 +213,26 @@ __device__ __forceinline__ void entering(f32x4 (&acc)[PTW][N / 16], const SsmArg
   for (int p = 0; p < PTW; ++p)
 #pragma unroll
     for (int n = 0; n < N / 16; ++n) acc[p][n] = *reinterpret_cast<const f32x4*>(a.seg + (slot + spare) * (N * PW) + tile_at<N>(pt0 + p, n));
-  for (int k = 0; k < (rev ? a.nseg - 1 - seg : seg); ++k) {
-    const int s = rev ? a.nseg - 1 - k : k;
-    const float dec = a.seg_dec[slot + s];
+  const int count = rev ? a.nseg - 1 - seg : seg;
+  for (int k = 0; k < count; k += 2) {  // two states in flight; past the last one, the last again, unused
+    const int s0 = rev ? a.nseg - 1 - k : k, k1 = min(k + 1, count - 1), s1 = rev ? a.nseg - 1 - k1 : k1;
+    const bool two = k + 1 < count;
+    const float d0 = a.seg_dec[slot + s0], d1 = two ? a.seg_dec[slot + s1] : 1.f;
+    f32x4 u[PTW][N / 16], v[PTW][N / 16];
 #pragma unroll
     for (int p = 0; p < PTW; ++p)
 #pragma unroll
-      for (int n = 0; n < N / 16; ++n)
-        acc[p][n] = acc[p][n] * dec + *reinterpret_cast<const f32x4*>(a.seg + (slot + s) * (N * PW) + tile_at<N>(pt0 + p, n));
+      for (int n = 0; n < N / 16; ++n) {
+        u[p][n] = *reinterpret_cast<const f32x4*>(a.seg + (slot + s0) * (N * PW) + tile_at<N>(pt0 + p, n));
+        v[p][n] = *reinterpret_cast<const f32x4*>(a.seg + (slot + s1) * (N * PW) + tile_at<N>(pt0 + p, n));
+      }
+#pragma unroll
+    for (int p = 0; p < PTW; ++p)
+#pragma unroll
+      for (int n = 0; n < N / 16; ++n) {
+        acc[p][n] = acc[p][n] * d0 + u[p][n];
+        if (two) acc[p][n] = acc[p][n] * d1 + v[p][n];
+      }
   }
 }
 

@@ -4,8 +4,8 @@ Argument marshalling only, as the rest of the binding; the operators are describ
 include/prism.h.  Tensors of shape [B, H, T, width] may have any positive strides with a unit
 stride in the last axis, so that the heads of a token-major projection output are passed as
 views; new outputs take the axis order of the matching input (heads outermost, or tokens).
-Calls run on the device of their tensors, on its current stream unless `stream` (a raw
-stream handle of that device) is given.
+Calls run on the device of their tensors, on its current stream or on the one given as the
+keyword `stream` (a raw stream handle of that device), to which new outputs then belong.
 """
 from __future__ import annotations
 
@@ -126,20 +126,34 @@ def _scratch(workspace, need, dev):
     return workspace
 
 
+def _on_stream(f):
+    """Runs f with the stream of its `stream` argument (a raw handle) as torch's current one, so that what it allocates
+    belongs to that stream."""
+    @functools.wraps(f)
+    def g(*args, stream=None, **kw):
+        if stream is None:
+            return f(*args, **kw)
+        dev = next((t.device for t in (*args, *kw.values()) if isinstance(t, torch.Tensor)), None)
+        if dev is None or dev.type != "cuda":
+            raise PrismError("inputs must be on a GPU")
+        s = torch.cuda.ExternalStream(stream, device=dev) if stream else torch.cuda.default_stream(dev)
+        with torch.cuda.stream(s):
+            return f(*args, **kw)
+    return g
+
+
 @functools.lru_cache(maxsize=None)
 def _function(name):
     return getattr(load_library(), name)
 
 
-def _run(name, dev, stream, *args):
+def _run(name, dev, *args):
     index = dev.index
     if torch.cuda.current_device() != index:          # kernels launch on the current device
         with torch.cuda.device(dev):
-            s = torch.cuda.current_stream(dev).cuda_stream if stream is None else stream
-            st = _function(name)(*args, s)
+            st = _function(name)(*args, torch.cuda.current_stream(dev).cuda_stream)
     else:
-        s = torch._C._cuda_getCurrentRawStream(index) if stream is None else stream
-        st = _function(name)(*args, s)
+        st = _function(name)(*args, torch._C._cuda_getCurrentRawStream(index))
     if st != 0:
         raise PrismError(f"{name} failed: {status_string(st)}")
 
@@ -157,7 +171,8 @@ def _conv_shape(x, conv_w, bias, dim):
     return dev, B, H, D, K, _dense("conv_w", conv_w, (H, K, D), _F32, dev), _dense("bias", bias, (H, D), _F32, dev)
 
 
-def conv_fwd(x, conv_w, bias=None, silu=True, conv_in=None, lens=None, out=None, want_conv=True, stream=None):
+@_on_stream
+def conv_fwd(x, conv_w, bias=None, silu=True, conv_in=None, lens=None, out=None, want_conv=True):
     """y, conv_out = conv_fwd(x, conv_w, bias): the depthwise causal convolution of x [B,H,T,D] with conv_w
     [H,K,D] and bias [H,D] (float32).  conv_in [B,H,K-1,D]: the rows before the first token.  lens [B] int32:
     tokens of each sequence; y rows past them keep what `out` holds (a new y holds nothing defined there).
@@ -168,12 +183,13 @@ def conv_fwd(x, conv_w, bias=None, silu=True, conv_in=None, lens=None, out=None,
     p_in, p_lens = _dense("conv_in", conv_in, (B, H, K - 1, D), x.dtype, dev), _dense("lens", lens, (B,), _I32, dev)
     y = _like(x) if out is None else _tensor("out", out, (B, H, T, D), x.dtype, dev)
     conv_out = torch.empty((B, H, max(K - 1, 0), D), dtype=x.dtype, device=dev) if want_conv else None
-    _run("prism_conv_fwd", dev, stream, x.data_ptr(), _strides(x), pw, pb, p_in, p_lens, B, H, T, D, K, bool(silu), _dtype(x),
+    _run("prism_conv_fwd", dev, x.data_ptr(), _strides(x), pw, pb, p_in, p_lens, B, H, T, D, K, bool(silu), _dtype(x),
          y.data_ptr(), _strides(y), conv_out.data_ptr() if want_conv else None)
     return y, conv_out
 
 
-def conv_bwd(x, conv_w, dy, bias=None, silu=True, out=None, workspace=None, stream=None):
+@_on_stream
+def conv_bwd(x, conv_w, dy, bias=None, silu=True, out=None, workspace=None):
     """Gradients of <dy, y> for conv_fwd(x, conv_w, bias, silu) from a sequence start: a dict of dx (dtype of x; out:
     a tensor to write it to), dconv_w and dbias (float32; dbias only with a bias)."""
     dev, B, H, D, K, pw, pb = _conv_shape(x, conv_w, bias, 4)
@@ -184,19 +200,20 @@ def conv_bwd(x, conv_w, dy, bias=None, silu=True, out=None, workspace=None, stre
     db = torch.empty_like(bias) if bias is not None else None
     code = _dtype(x)
     ws = _scratch(workspace, _need("prism_conv_bwd", B, H, T, D, K, code), dev)
-    _run("prism_conv_bwd", dev, stream, x.data_ptr(), _strides(x), pw, pb, dy.data_ptr(), _strides(dy), B, H, T, D, K, bool(silu),
+    _run("prism_conv_bwd", dev, x.data_ptr(), _strides(x), pw, pb, dy.data_ptr(), _strides(dy), B, H, T, D, K, bool(silu),
          code, dx.data_ptr(), _strides(dx), dw.data_ptr(), None if db is None else db.data_ptr(), ws.data_ptr(), ws.numel())
     return {"dx": dx, "dconv_w": dw} if db is None else {"dx": dx, "dconv_w": dw, "dbias": db}
 
 
-def conv_step(conv_state, x, conv_w, bias=None, silu=True, stream=None):
+@_on_stream
+def conv_step(conv_state, x, conv_w, bias=None, silu=True):
     """y = conv_step(conv_state, x, conv_w, bias): one token x [B,H,D]; conv_state [B,H,K-1,D] is updated in place."""
     dev, B, H, D, K, pw, pb = _conv_shape(x, conv_w, bias, 3)
     if conv_state is None:
         raise PrismError("conv_state is required")
     p_state = _dense("conv_state", conv_state, (B, H, K - 1, D), x.dtype, dev)
     y = torch.empty((B, H, D), dtype=x.dtype, device=dev)
-    _run("prism_conv_step", dev, stream, x.data_ptr(), _strides(x), pw, pb, B, H, D, K, bool(silu), _dtype(x), p_state, y.data_ptr())
+    _run("prism_conv_step", dev, x.data_ptr(), _strides(x), pw, pb, B, H, D, K, bool(silu), _dtype(x), p_state, y.data_ptr())
     return y
 
 
@@ -223,8 +240,8 @@ def _scan_shape(x, Bm, Cm, dt, A, D, dt_bias, token):
     return dev, B, H, G, (1 if token else shape[2]), N, P, args
 
 
-def ssm_fwd(x, Bm, Cm, dt, A, D=None, dt_bias=None, softplus=True, S0=None, lens=None, out=None, workspace=None,
-            stream=None):
+@_on_stream
+def ssm_fwd(x, Bm, Cm, dt, A, D=None, dt_bias=None, softplus=True, S0=None, lens=None, out=None, workspace=None):
     """y, S_final = ssm_fwd(x, Bm, Cm, dt, A, D, dt_bias): the selective state space scan of x [B,H,T,P] with Bm, Cm
     [B,G,T,N] (one dtype, bfloat16 or float32) and dt [B,H,T], A, D, dt_bias [H] (float32).  S0 [B,H,N,P] float32:
     the state before the first token.  lens [B] int32: tokens of each sequence; y rows past them keep what `out`
@@ -235,13 +252,13 @@ def ssm_fwd(x, Bm, Cm, dt, A, D=None, dt_bias=None, softplus=True, S0=None, lens
     S = torch.empty((B, H, N, P), dtype=torch.float32, device=dev)
     code = _dtype(x)
     ws = _scratch(workspace, _need("prism_ssm_fwd", B, H, G, T, N, P, code), dev)
-    _run("prism_ssm_fwd", dev, stream, *args, p_s0, p_lens, B, H, G, T, N, P, bool(softplus), code, y.data_ptr(), _strides(y),
+    _run("prism_ssm_fwd", dev, *args, p_s0, p_lens, B, H, G, T, N, P, bool(softplus), code, y.data_ptr(), _strides(y),
          S.data_ptr(), ws.data_ptr(), ws.numel())
     return y, S
 
 
-def ssm_bwd(x, Bm, Cm, dt, A, dy, D=None, dt_bias=None, softplus=True, dS_final=None, out=None, workspace=None,
-            stream=None):
+@_on_stream
+def ssm_bwd(x, Bm, Cm, dt, A, dy, D=None, dt_bias=None, softplus=True, dS_final=None, out=None, workspace=None):
     """Gradients of <dy, y> + <dS_final, S_final> for ssm_fwd from a zero state: a dict of dx, dB, dC (dtype of x; out:
     three tensors to write them to), ddt, dA (float32) and, where the argument is given, dD and ddt_bias."""
     dev, B, H, G, T, N, P, args = _scan_shape(x, Bm, Cm, dt, A, D, dt_bias, False)
@@ -261,14 +278,15 @@ def ssm_bwd(x, Bm, Cm, dt, A, dy, D=None, dt_bias=None, softplus=True, dS_final=
         g["ddt_bias"] = torch.empty_like(dt_bias)
     code = _dtype(x)
     ws = _scratch(workspace, _need("prism_ssm_bwd", B, H, G, T, N, P, code), dev)
-    _run("prism_ssm_bwd", dev, stream, *args, dy.data_ptr(), _strides(dy), p_ds, B, H, G, T, N, P, bool(softplus), code,
+    _run("prism_ssm_bwd", dev, *args, dy.data_ptr(), _strides(dy), p_ds, B, H, G, T, N, P, bool(softplus), code,
          dx.data_ptr(), _strides(dx), dB.data_ptr(), _strides(dB), dC.data_ptr(), _strides(dC), g["ddt"].data_ptr(),
          g["dA"].data_ptr(), None if D is None else g["dD"].data_ptr(), None if dt_bias is None else g["ddt_bias"].data_ptr(),
          ws.data_ptr(), ws.numel())
     return g
 
 
-def ssm_step(S, x, Bm, Cm, dt, A, D=None, dt_bias=None, softplus=True, stream=None):
+@_on_stream
+def ssm_step(S, x, Bm, Cm, dt, A, D=None, dt_bias=None, softplus=True):
     """y = ssm_step(S, x, Bm, Cm, dt, A, D, dt_bias): one token x [B,H,P], Bm, Cm [B,G,N], dt [B,H]; S [B,H,N,P] float32
     is updated in place."""
     dev, B, H, G, _, N, P, args = _scan_shape(x, Bm, Cm, dt, A, D, dt_bias, True)
@@ -276,7 +294,7 @@ def ssm_step(S, x, Bm, Cm, dt, A, D=None, dt_bias=None, softplus=True, stream=No
         raise PrismError("S is required")
     p_s = _dense("S", S, (B, H, N, P), _F32, dev)
     y = torch.empty((B, H, P), dtype=x.dtype, device=dev)
-    _run("prism_ssm_step", dev, stream, *args, B, H, G, N, P, bool(softplus), _dtype(x), p_s, y.data_ptr())
+    _run("prism_ssm_step", dev, *args, B, H, G, N, P, bool(softplus), _dtype(x), p_s, y.data_ptr())
     return y
 
 
@@ -307,7 +325,8 @@ def _rows(name, t, shape, dtype, dev):
     return D if stride is None else stride
 
 
-def norm_fwd(x, weight=None, residual=None, gate=None, eps=1e-5, bits8=False, stream=None):
+@_on_stream
+def norm_fwd(x, weight=None, residual=None, gate=None, eps=1e-5, bits8=False):
     """Root-mean-square norm over the last axis of x, with h = x + residual before it and y * silu(gate) after: a dict
     of y (the dtype of x, or with bits8 torch.float8_e4m3fn), scales (bits8: float32, one per 128 values of a row,
     y.float() * scale is the value) and h (with residual; the dtype of x).  weight [D] float32; gate like x; both
@@ -329,12 +348,13 @@ def norm_fwd(x, weight=None, residual=None, gate=None, eps=1e-5, bits8=False, st
     if pr is not None:
         r["h"] = h = torch.empty(shape, dtype=x.dtype, device=dev)
         ph = h.data_ptr()
-    _run("prism_norm_fwd", dev, stream, x.data_ptr(), xs, pr, pw, None if gate is None else gate.data_ptr(), gs, rows, D, eps, code,
+    _run("prism_norm_fwd", dev, x.data_ptr(), xs, pr, pw, None if gate is None else gate.data_ptr(), gs, rows, D, eps, code,
          y.data_ptr(), ps, ph)
     return r
 
 
-def norm_bwd(h, weight, dy, gate=None, dh_in=None, eps=1e-5, workspace=None, stream=None):
+@_on_stream
+def norm_bwd(h, weight, dy, gate=None, dh_in=None, eps=1e-5, workspace=None):
     """Gradients of <dy, y> + <dh_in, h> for norm_fwd, with h the row that was normalised: a dict of dh (the gradient of x
     and of residual), dw (float32; with a weight) and dgate (with a gate)."""
     dev = _gpu(h, "h")
@@ -355,6 +375,6 @@ def norm_bwd(h, weight, dy, gate=None, dh_in=None, eps=1e-5, workspace=None, str
     if gate is not None:
         g["dgate"] = dz = torch.empty(shape, dtype=h.dtype, device=dev)
     ws = _scratch(workspace, _need("prism_norm_bwd", rows, D, code), dev)
-    _run("prism_norm_bwd", dev, stream, h.data_ptr(), hs, pw, None if gate is None else gate.data_ptr(), gs, py, pi, rows, D, eps, code,
+    _run("prism_norm_bwd", dev, h.data_ptr(), hs, pw, None if gate is None else gate.data_ptr(), gs, py, pi, rows, D, eps, code,
          dh.data_ptr(), None if dz is None else dz.data_ptr(), None if dw is None else dw.data_ptr(), ws.data_ptr(), ws.numel())
     return g

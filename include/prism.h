@@ -452,8 +452,9 @@ prism_status prism_fwd_noalloc(const void* q, const void* k, const void* v,
  * everywhere above.  So heads of a token-major projection output [B, T, channels] are read
  * and written in place.  Strides must be positive where their axis is longer than 1; rows of
  * an output must not overlap.  Ownership, streams and errors as prism_fwd; the stream must
- * belong to the current device.  Non-finite inputs reach the outputs they enter, except
- * rows past a sequence's length, which are never read. */
+ * belong to the current device.  Non-finite inputs reach the outputs they enter; in the scan
+ * a non-finite row of x (of dy in its backward) may also reach the other tokens of its chunk
+ * of 64.  Rows past a sequence's length never reach anything. */
 typedef struct {
   long long b, h, t;
 } prism_strides;

@@ -1,0 +1,163 @@
+"""Edges of the state space layer's operators on the GPU: long and large tensors (offsets past 32 bits), many segments, odd
+head groups, streams, repeated calls.  Tolerances as in tests/test_layer_gpu.py."""
+import numpy as np
+import pytest
+
+from oracle import layer
+from tests.conftest import gpu_available
+from tests.test_layer_gpu import Rng, close, f64, scan_inputs, sizes
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module")
+def prism():
+    if not gpu_available():
+        pytest.skip("no GPU")
+    import delta_rule_sequence_amd as m
+    m.load_library()
+    return m
+
+
+# (dtype, B, H, G, T, N, P): more than 8 and more than 16 segments (a scan over them), one to eight (none), an odd number of
+# heads per group (one head per workgroup), two slices of 64 columns per head, groups of one head
+LONG = [("bf16", 1, 1, 1, 3000, 16, 16), ("f32", 1, 1, 1, 3000, 16, 16), ("bf16", 1, 1, 1, 8200, 16, 32), ("f32", 1, 2, 2, 2100, 32, 16),
+        ("bf16", 2, 9, 3, 450, 32, 64), ("bf16", 1, 5, 1, 700, 64, 32), ("bf16", 1, 3, 3, 330, 64, 128), ("f32", 1, 3, 1, 200, 128, 128),
+        ("bf16", 40, 8, 1, 130, 16, 64)]
+
+
+@pytest.mark.parametrize("case", LONG, ids=lambda c: "_".join(map(str, c)))
+def test_ssm_segments_and_groups(prism, case):
+    dt, B, H, G, T, N, P = case
+    r, x, Bm, Cm, dt_, A, D, bias = scan_inputs(50, *case, layout="tokens")
+    S0 = r.flt(B, H, N, P)
+    y, S = prism.ssm_fwd(x, Bm, Cm, dt_, A, D, bias, S0=S0)
+    ref, ref_S = layer.ssm(*(f64(t) for t in (x, Bm, Cm, dt_, A, D, bias)), True, f64(S0))
+    size, size_S = sizes(x, Bm, Cm, dt_, A, D, bias, True, S0)
+    close("y", y, ref, size, dt)
+    close("S_final", S, ref_S, size_S, dt, "f32")
+    dy, dS = r.vec(B, H, T, P), r.flt(B, H, N, P)
+    g = prism.ssm_bwd(x, Bm, Cm, dt_, A, dy, D, bias, dS_final=dS)
+    args = [f64(t) for t in (x, Bm, Cm, dt_, A, dy, D, bias)]
+    ref, size = layer.ssm_grad(*args, True, f64(dS)), layer.ssm_grad(*args, True, f64(dS), absolute=True)
+    for k in ("dx", "dB", "dC", "ddt", "dA", "dD", "ddt_bias"):
+        close(k, g[k], ref[k], size[k], dt, None if k in ("dx", "dB", "dC") else "f32")
+
+
+def test_ssm_pieces_are_the_whole(prism):
+    """A sequence in pieces of 1, 63, 64, 65 and 300 tokens, each from the state of the one before: float32, sums in another
+    order only."""
+    import torch
+    B, H, G, N, P = 1, 2, 1, 32, 32
+    T = 1 + 63 + 64 + 65 + 300
+    _, x, Bm, Cm, dt_, A, D, bias = scan_inputs(51, "f32", B, H, G, T, N, P)
+    y, S = prism.ssm_fwd(x, Bm, Cm, dt_, A, D, bias)
+    state, at = None, 0
+    for n in (1, 63, 64, 65, 300):
+        cut = [t[:, :, at:at + n] for t in (x, Bm, Cm, dt_)]
+        part, state = prism.ssm_fwd(*cut, A, D, bias, S0=state)
+        assert torch.allclose(part, y[:, :, at:at + n], rtol=1e-4, atol=1e-4)
+        at += n
+    assert torch.allclose(state, S, rtol=1e-4, atol=1e-4)
+
+
+def test_offsets_past_32_bits(prism):
+    """Rows whose element offsets exceed 2^31 (and byte offsets 2^32), against the same rows in a small tensor."""
+    import torch
+    big = torch.empty(1, 300, 1 << 23, dtype=torch.bfloat16, device="cuda")              # 4.7 GiB, rows 16 MB apart
+    r, x, Bm, Cm, dt_, A, D, bias = scan_inputs(52, "bf16", 1, 1, 1, 300, 64, 64)
+    xv, bv, cv, yv = (big[:, :, k * 64:(k + 1) * 64].unsqueeze(1) for k in (0, 1, 2, 131071))
+    xv.copy_(x), bv.copy_(Bm), cv.copy_(Cm)
+    y, S = prism.ssm_fwd(x, Bm, Cm, dt_, A, D, bias)
+    got, got_S = prism.ssm_fwd(xv, bv, cv, dt_, A, D, bias, out=yv)
+    assert torch.equal(got, y) and torch.equal(got_S, S)
+    g = prism.ssm_bwd(x, Bm, Cm, dt_, A, x, D, bias)
+    outs = tuple(big[:, :, k * 64:(k + 1) * 64].unsqueeze(1) for k in (3, 4, 5))
+    h = prism.ssm_bwd(xv, bv, cv, dt_, A, xv, D, bias, out=outs)
+    assert all(torch.equal(g[k], h[k]) for k in g)
+    w = r.flt(1, 4, 64)
+    assert torch.equal(prism.conv_fwd(xv, w, out=yv)[0], prism.conv_fwd(x, w)[0])
+    assert torch.equal(prism.conv_bwd(xv, w, yv)["dx"], prism.conv_bwd(x, w, yv.contiguous())["dx"])
+    n, m = prism.norm_fwd(xv[:, 0])["y"], prism.norm_fwd(x[:, 0])["y"]
+    assert torch.equal(n, m)
+    with pytest.raises(prism.PrismError):                                                # rows more than 16 MB apart
+        wide = big.view(1, 100, 3 << 23)[:, :, :64].unsqueeze(1)
+        prism.ssm_fwd(wide, wide, wide, dt_[:, :, :100].contiguous(), A)
+    del big, xv, bv, cv, yv, outs
+    rows = torch.zeros((1 << 16) + 3, 1 << 15, dtype=torch.bfloat16, device="cuda")      # 2^31 elements and more
+    rows[-3:] = r.vec(3, 1 << 15)
+    ref = prism.norm_fwd(rows[-3:].contiguous(), bits8=True)
+    got = prism.norm_fwd(rows, bits8=True)
+    assert torch.equal(got["y"][-3:].view(torch.uint8), ref["y"].view(torch.uint8)) and torch.equal(got["scales"][-3:], ref["scales"])
+
+
+def test_non_finite_rows_stay_causal(prism):
+    """An infinity in one token of the convolution, and one in B, C or dt of the scan: earlier tokens are unaffected; and a
+    non-finite x reaches no token before its chunk of 64."""
+    import torch
+    r, x, Bm, Cm, dt_, A, D, bias = scan_inputs(53, "bf16", 1, 2, 1, 200, 32, 32)
+    y, _ = prism.ssm_fwd(x, Bm, Cm, dt_, A, D, bias)
+    for t in (Bm, Cm, dt_):
+        keep = t.clone()
+        t[:, :, 100] = float("inf")
+        got, _ = prism.ssm_fwd(x, Bm, Cm, dt_, A, D, bias)
+        assert torch.equal(got[:, :, :100], y[:, :, :100])
+        t.copy_(keep)
+    x2 = x.clone()
+    x2[:, :, 100] = float("nan")
+    got, _ = prism.ssm_fwd(x2, Bm, Cm, dt_, A, D, bias)
+    assert torch.equal(got[:, :, :64], y[:, :, :64]) and bool(torch.isnan(got[:, :, 128:]).all())
+    w = r.flt(2, 4, 32)
+    c, c2 = prism.conv_fwd(x, w)[0], prism.conv_fwd(x2, w)[0]
+    assert torch.equal(c2[:, :, :100], c[:, :, :100]) and torch.equal(c2[:, :, 104:], c[:, :, 104:])
+    assert bool(torch.isnan(c2[:, :, 100:104]).all())
+
+
+def test_two_streams_and_a_given_one(prism):
+    """Calls on two streams at once, and on a stream given by its handle, with results bit-identical to one after another."""
+    import torch
+    cases = [scan_inputs(s, "bf16", 2, 4, 1, 600, 64, 64)[1:] for s in (54, 55)]
+
+    def both(c, **kw):
+        x, Bm, Cm, dt_, A, D, bias = c
+        y, S = prism.ssm_fwd(x, Bm, Cm, dt_, A, D, bias, **kw)
+        g = prism.ssm_bwd(x, Bm, Cm, dt_, A, y, D, bias, dS_final=S, **kw)
+        n = prism.norm_fwd(y, residual=y, bits8=True, **kw)
+        return [y, S, n["y"].view(torch.uint8), n["scales"]] + [g[k] for k in sorted(g)]
+
+    ref = [both(c) for c in cases]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    got = [None, None]
+    for _ in range(3):
+        for k in (0, 1):
+            with torch.cuda.stream(streams[k]):
+                got[k] = both(cases[k])
+    torch.cuda.synchronize()
+    assert all(torch.equal(p, q) for k in (0, 1) for p, q in zip(got[k], ref[k]))
+    got = both(cases[0], stream=streams[0].cuda_stream)
+    streams[0].synchronize()
+    assert all(torch.equal(p, q) for p, q in zip(got, ref[0]))
+    got = both(cases[0], stream=torch.cuda.default_stream().cuda_stream)
+    torch.cuda.synchronize()
+    assert all(torch.equal(p, q) for p, q in zip(got, ref[0]))
+
+
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+def test_repeated_calls_are_identical(prism, dt):
+    """Every sum has a fixed order: three calls on the same inputs, a used workspace among them, agree bit for bit."""
+    import torch
+    r, x, Bm, Cm, dt_, A, D, bias = scan_inputs(56, dt, 2, 6, 2, 500, 32, 128)
+    w, b = r.flt(6, 4, 128), r.flt(6, 128)
+    lib = prism.load_library()
+    ws = torch.full((lib.prism_ssm_bwd_workspace_bytes(2, 6, 2, 500, 32, 128, 1 if dt == "bf16" else 0),), 0xff, dtype=torch.uint8, device="cuda")
+
+    def run():
+        g = prism.ssm_bwd(x, Bm, Cm, dt_, A, x, D, bias, workspace=ws)
+        c = prism.conv_bwd(x, w, x, b)
+        n = prism.norm_bwd(x, torch.ones(128, device="cuda"), x, gate=x)
+        return [d[k].clone() for d in (g, c, n) for k in sorted(d)]
+
+    first = run()
+    for _ in range(2):
+        assert all(torch.equal(p, q) for p, q in zip(first, run()))

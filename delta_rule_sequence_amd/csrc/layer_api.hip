@@ -192,7 +192,7 @@ prism_status conv_check(int B, int H, int T, int D, int K, prism_dtype dt) {
 // Tokens per thread: long strips read their K - 1 border rows (and, backward, leave their shares of dw) once for
 // more tokens, short ones fill the device when there are few channels.
 int conv_strip(int B, int H, int T, int D, prism_dtype dt, bool bwd) {
-  const size_t per = bwd ? 4 : 16 / elem(dt), cols = (size_t)B * H * (((size_t)D + per - 1) / per);
+  const size_t per = bwd || elem(dt) == 4 ? conv_group<4>(D) : conv_group<8>(D), cols = (size_t)B * H * (((size_t)D + per - 1) / per);
   int strip = bwd ? 64 : 32;
   while (strip > 8 && cols * (((size_t)T + strip - 1) / strip) < (bwd ? 8 : 16) * 64 * kCUs) strip /= 2;
   // workgroups of four strips map to grid.y
@@ -308,13 +308,11 @@ prism_status prism_conv_fwd(const void* x, const prism_strides* x_strides, const
   if (!make_strides(x_strides, B, H, T, D, &a.xs) || !make_strides(y_strides, B, H, T, D, &a.ys) ||
       !rows_apart(a.ys, B, H, T, D))
     return PRISM_ERR_INVALID_ARG;
-  const bool wide = (size_t)D * elem(dt) % 16 == 0 && rows16(x, a.xs, dt) && rows16(y, a.ys, dt) &&
-                    (conv_in == nullptr || aligned16(conv_in));
   a.x = x, a.w = conv_w, a.bias = bias, a.conv_in = conv_in, a.lens = lens, a.y = y, a.conv_out = conv_out;
   a.B = B, a.H = H, a.T = T, a.D = D, a.silu = silu != 0;
   a.strip = conv_strip(B, H, T, D, dt, false);
   a.nstrip = (int)(((long long)T + a.strip - 1) / a.strip);
-  return host::launch_conv_fwd(dt, K, wide, a, stream);
+  return host::launch_conv_fwd(dt, K, a, stream);
 }
 
 size_t prism_conv_bwd_workspace_bytes(int B, int H, int T, int D, int K, prism_dtype dt) {
@@ -341,13 +339,12 @@ prism_status prism_conv_bwd(const void* x, const prism_strides* x_strides, const
   if (need == 0) return PRISM_ERR_INVALID_ARG;
   if (!workspace || workspace_bytes < need) return PRISM_ERR_WORKSPACE;
   if (!aligned16(workspace)) return PRISM_ERR_INVALID_ARG;
-  const bool wide = (size_t)D * elem(dt) % 16 == 0 && rows16(x, a.xs, dt) && rows16(dy, a.dys, dt) && rows16(dx, a.ys, dt);
   a.x = x, a.w = conv_w, a.bias = bias, a.dy = dy, a.y = dx;
   a.B = B, a.H = H, a.T = T, a.D = D, a.silu = silu != 0;
   a.strip = conv_strip(B, H, T, D, dt, true);
   a.nstrip = (int)(((long long)T + a.strip - 1) / a.strip);
   a.part = reinterpret_cast<float*>(workspace), a.dw = dconv_w, a.dbias = dbias;
-  return host::launch_conv_bwd(dt, K, wide, a, stream);
+  return host::launch_conv_bwd(dt, K, a, stream);
 }
 
 prism_status prism_conv_step(const void* x, const prism_strides* x_strides, const float* conv_w, const float* bias,
@@ -371,12 +368,8 @@ static prism_status norm_check(int rows, int D, long long xs, const void* gate, 
   return PRISM_OK;
 }
 
-// Whether rows of D values at p (NULL: not there) can be kept in registers in 16-byte pieces: whole pieces, aligned, up
-// to 1024 of them (16 KB).
-static bool row16(int D, const void* p, long long stride, prism_dtype dt) {
-  const size_t e = elem(dt);
-  return D * e % 16 == 0 && D * e <= 16384 && (p == nullptr || (aligned16(p) && stride * e % 16 == 0));
-}
+// Whether rows fit the registers of a workgroup (1024 pieces of 16 bytes).
+static bool norm_short(int D, prism_dtype dt) { return D * elem(dt) <= 16384; }
 
 prism_status prism_norm_fwd(const void* x, long long x_stride, const void* residual, const float* weight,
                             const void* gate, long long gate_stride, int rows, int D, float eps, prism_dtype dt,
@@ -387,9 +380,7 @@ prism_status prism_norm_fwd(const void* x, long long x_stride, const void* resid
   NormArgs a = {};
   a.x = x, a.xs = x_stride, a.residual = residual, a.w = weight, a.gate = gate, a.gs = gate_stride;
   a.rows = rows, a.D = D, a.eps = eps, a.y = y, a.scales = scales, a.h = h_out;
-  const bool one_read = row16(D, x, x_stride, dt) && row16(D, residual, D, dt) && row16(D, gate, gate_stride, dt) &&
-                        row16(D, y, D, dt) && row16(D, h_out, D, dt);
-  return host::launch_norm_fwd(dt, one_read, a, stream);
+  return host::launch_norm_fwd(dt, norm_short(D, dt), a, stream);
 }
 
 // Workgroups of the backward: each sums its rows' share of dweight before the shares are joined.
@@ -416,9 +407,7 @@ prism_status prism_norm_bwd(const void* h, long long h_stride, const float* weig
   a.x = h, a.xs = h_stride, a.w = weight, a.gate = gate, a.gs = gate_stride, a.dy = dy, a.dh_in = dh_in;
   a.rows = rows, a.D = D, a.eps = eps, a.h = dh, a.dgate = dgate;
   a.part = reinterpret_cast<float*>(workspace), a.nblk = norm_blocks(rows), a.dw = dweight;
-  const bool one_read = row16(D, h, h_stride, dt) && row16(D, gate, gate_stride, dt) && row16(D, dy, D, dt) &&
-                        row16(D, dh_in, D, dt) && row16(D, dh, D, dt) && row16(D, dgate, D, dt);
-  return host::launch_norm_bwd(dt, one_read, a, stream);
+  return host::launch_norm_bwd(dt, norm_short(D, dt), a, stream);
 }
 
 }  // extern "C"

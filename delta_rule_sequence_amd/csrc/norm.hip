@@ -27,16 +27,16 @@ void bwd_row(const NormArgs& a, hipStream_t s) {
 
 template <class T>
 prism_status fwd(bool rows, const NormArgs& a, hipStream_t s) {
-  const int n = a.D / norm::Piece<T>::V;
+  const int n = (a.D + norm::Piece<T>::V - 1) / norm::Piece<T>::V;
   if (rows) PRISM_NORM_ROWS(fwd_row, n);
-  else norm::fwd_any_kernel<T><<<dim3(a.rows), 256, 0, s>>>(a);
+  else norm::fwd_long_kernel<T><<<dim3(a.rows), 256, 0, s>>>(a);
   return launched();
 }
 template <class T>
 prism_status bwd(bool rows, const NormArgs& a, hipStream_t s) {
-  const int n = a.D / norm::Piece<T>::V;
+  const int n = (a.D + norm::Piece<T>::V - 1) / norm::Piece<T>::V;
   if (rows) PRISM_NORM_ROWS(bwd_row, n);
-  else norm::bwd_any_kernel<T><<<dim3(a.nblk), 256, 0, s>>>(a);
+  else norm::bwd_long_kernel<T><<<dim3(a.nblk), 256, 0, s>>>(a);
   if (a.dw != nullptr) norm::wsum_kernel<<<dim3((a.D + 31) / 32), 1024, 0, s>>>(a);
   return launched();
 }

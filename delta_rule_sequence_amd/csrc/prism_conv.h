@@ -3,9 +3,10 @@
 //   pre_t = bias + sum_{j<K} w_j x_{t-K+1+j},   y_t = pre_t or silu(pre_t)        (per channel)
 //   g_t = dy_t (silu'(pre_t) or 1),  dx_t = sum_j w_j g_{t+K-1-j},  dw_j = sum_t x_{t-K+1+j} g_t,  dbias = sum_t g_t
 //
-// Bound by its bytes.  A thread owns V neighbouring channels (16 bytes) and walks a strip of tokens with the K
-// rows of the window in registers, so that a row is read once per strip (K - 1 rows again at its border).
-// Rows or pointers that are not 16-byte aligned run with V = 1.
+// Bound by its bytes.  A thread owns V neighbouring channels and walks a strip of tokens with the K rows of the window
+// in registers, so that a row is read once per strip (K - 1 rows again at its border).  Rows may start anywhere (the
+// accesses need the alignment of an element only); the last thread of a row loads the last V channels and writes those
+// its neighbour has not (the history may be written in place, so no value may come from two threads).
 #pragma once
 #include "prism_ssm_args.h"
 #include "prism_tile.h"
@@ -13,7 +14,7 @@
 namespace prism {
 namespace conv {
 
-template <class T, int V> struct Vec { typedef T type __attribute__((ext_vector_type(V))); };
+template <class T, int V> struct Vec { typedef T type __attribute__((ext_vector_type(V), aligned(sizeof(T)))); };
 template <class T> struct Vec<T, 1> { typedef T type; };
 
 template <class T, int V>
@@ -21,14 +22,27 @@ __device__ __forceinline__ float elem(const typename Vec<T, V>::type& v, int k) 
   if constexpr (V == 1) return (float)v;
   else return (float)v[k];
 }
+// Values from .. V - 1 of the vector.
 template <class T, int V>
-__device__ __forceinline__ void store_v(T* p, const float (&o)[V]) {
+__device__ __forceinline__ void store_v(T* p, const typename Vec<T, V>::type& v, int from) {
+  if constexpr (V == 1) {
+    *p = v;
+  } else if (from == 0) {
+    *reinterpret_cast<typename Vec<T, V>::type*>(p) = v;
+  } else {
+#pragma unroll
+    for (int k = 1; k < V; ++k)
+      if (k >= from) p[k] = v[k];
+  }
+}
+template <class T, int V>
+__device__ __forceinline__ void store_v(T* p, const float (&o)[V], int from) {
   typename Vec<T, V>::type v;
   if constexpr (V == 1) v = (T)o[0];
   else
 #pragma unroll
     for (int k = 0; k < V; ++k) v[k] = (T)o[k];
-  *reinterpret_cast<typename Vec<T, V>::type*>(p) = v;
+  store_v<T, V>(p, v, from);
 }
 
 // V weights of one channel group in 16-byte loads (any 4-byte alignment).
@@ -82,10 +96,10 @@ __device__ __forceinline__ typename Vec<T, V>::type row(const ConvArgs& a, int b
 template <class T, int K, int V, int U, bool SILU>
 __global__ __launch_bounds__(256) void fwd_kernel(ConvArgs a) {
   typedef typename Vec<T, V>::type vec;
-  const int d = (blockIdx.x * 64 + threadIdx.x % 64) * V;
+  const int first = (blockIdx.x * 64 + threadIdx.x % 64) * V, d = min(first, a.D - V);
   const int strip = blockIdx.y * 4 + __builtin_amdgcn_readfirstlane(threadIdx.x / 64);  // one strip per wave
   const int bh = blockIdx.z, b = bh / a.H, h = bh % a.H;
-  if (d >= a.D || strip >= a.nstrip) return;
+  if (first >= a.D || strip >= a.nstrip) return;
   const int len = seq_len(a, b), t0 = strip * a.strip, t1 = min(t0 + a.strip, len);
   if (t0 < t1) {
     float w[K][V], bias[V], x[K][V];
@@ -116,7 +130,7 @@ __global__ __launch_bounds__(256) void fwd_kernel(ConvArgs a) {
           for (int j = 0; j < K; ++j) s += w[j][k] * x[j][k];
           o[k] = SILU ? s * sigmoid_f(s) : s;
         }
-        store_v<T, V>(y + (long long)(t + u) * a.ys.t, o);
+        store_v<T, V>(y + (long long)(t + u) * a.ys.t, o, first - d);
       }
     }
   }
@@ -126,7 +140,7 @@ __global__ __launch_bounds__(256) void fwd_kernel(ConvArgs a) {
     for (int j = 0; j < K - 1; ++j) tail[j] = row<T, K, V>(a, b, h, len - K + 1 + j, d);
     T* o = reinterpret_cast<T*>(a.conv_out) + (size_t)bh * (K - 1) * a.D + d;
 #pragma unroll
-    for (int j = 0; j < K - 1; ++j) *reinterpret_cast<vec*>(o + (size_t)j * a.D) = tail[j];
+    for (int j = 0; j < K - 1; ++j) store_v<T, V>(o + (size_t)j * a.D, tail[j], first - d);
   }
 }
 
@@ -137,14 +151,14 @@ __global__ __launch_bounds__(256) void bwd_kernel(ConvArgs a) {
   typedef typename Vec<T, V>::type vec;
   __shared__ float sum[4][V][64];
   const int lane = threadIdx.x % 64, q = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);  // one strip per wave
-  const int d = (blockIdx.x * 64 + lane) * V, strip = blockIdx.y * 4 + q;
+  const int first = (blockIdx.x * 64 + lane) * V, d = min(first, a.D - V), strip = blockIdx.y * 4 + q;
   const int bh = blockIdx.z, b = bh / a.H, h = bh % a.H;
   float dw[K + 1][V];
 #pragma unroll
   for (int j = 0; j <= K; ++j)
 #pragma unroll
     for (int k = 0; k < V; ++k) dw[j][k] = 0.f;
-  if (d < a.D && strip < a.nstrip) {
+  if (first < a.D && strip < a.nstrip) {
     const int t0 = strip * a.strip, t1 = min(t0 + a.strip, a.T), te = t1 + K - 1;
     float w[K][V], bias[V], x[K][V], g[K][V];
     load_filter<K, V>(w, bias, a, h, d);
@@ -201,7 +215,7 @@ __global__ __launch_bounds__(256) void bwd_kernel(ConvArgs a) {
 #pragma unroll
           for (int j = 0; j < K; ++j) o[k] += w[K - 1 - j][k] * g[j][k];
         }
-        if (tt - K + 1 >= t0) store_v<T, V>(dx + (long long)(tt - K + 1) * a.ys.t, o);
+        if (tt - K + 1 >= t0) store_v<T, V>(dx + (long long)(tt - K + 1) * a.ys.t, o, first - d);
       }
     }
   }
@@ -213,8 +227,9 @@ __global__ __launch_bounds__(256) void bwd_kernel(ConvArgs a) {
     for (int k = 0; k < V; ++k) sum[q][k][lane] = dw[j][k];
     __syncthreads();
     for (int i = threadIdx.x; i < 64 * V; i += 256) {
-      const int col = blockIdx.x * 64 * V + i, k = i % V, ln = i / V;
-      if (col < a.D) part[(size_t)j * a.D + col] = (sum[0][k][ln] + sum[1][k][ln]) + (sum[2][k][ln] + sum[3][k][ln]);
+      const int k = i % V, ln = i / V, at = (blockIdx.x * 64 + ln) * V;
+      const int col = min(at, a.D - V) + k;
+      if (at < a.D && col >= at) part[(size_t)j * a.D + col] = (sum[0][k][ln] + sum[1][k][ln]) + (sum[2][k][ln] + sum[3][k][ln]);
     }
   }
 }

@@ -55,9 +55,9 @@ __device__ __forceinline__ float block_sum(float v, float* part) {  // 256 threa
   return (part[0] + part[1]) + (part[2] + part[3]);
 }
 
-// Any row length and alignment: one workgroup per row, read twice, in 128-value blocks of one wave each.
+// Longer rows: one workgroup per row, read twice, in 128-value blocks of one wave each.
 template <class T>
-__global__ __launch_bounds__(256) void fwd_any_kernel(NormArgs a) {
+__global__ __launch_bounds__(256) void fwd_long_kernel(NormArgs a) {
   __shared__ float part[4];
   const size_t row = blockIdx.x;
   const T* x = reinterpret_cast<const T*>(a.x) + row * a.xs;
@@ -101,9 +101,9 @@ __global__ __launch_bounds__(256) void fwd_any_kernel(NormArgs a) {
   }
 }
 
-// Any row length and alignment: workgroup k takes rows k, k + nblk, ...; its shares of dweight stay in part[k].
+// Longer rows: workgroup k takes rows k, k + nblk, ...; its shares of dweight stay in part[k].
 template <class T>
-__global__ __launch_bounds__(256) void bwd_any_kernel(NormArgs a) {
+__global__ __launch_bounds__(256) void bwd_long_kernel(NormArgs a) {
   __shared__ float part[4];
   float* dw = a.dw != nullptr ? a.part + (size_t)blockIdx.x * a.D : nullptr;
   for (int row = blockIdx.x; row < a.rows; row += a.nblk) {
@@ -138,14 +138,51 @@ __global__ __launch_bounds__(256) void bwd_any_kernel(NormArgs a) {
   }
 }
 
-// ---- aligned rows of up to 16384 bytes -----------------------------------------------------------
+// ---- rows of up to 16384 bytes ------------------------------------------------------------------------
 // A row lies in the registers of TPR lanes (a part of a wave, a wave or the workgroup), NV 16-byte pieces per lane, and
 // is read once: statistics by lane exchanges, then the outputs from the same registers.  Piece k of lane j is number
 // k TPR + j of the row, so a 128-value block of the 8-bit output is 128 / V neighbouring lanes.
+// Rows may start anywhere: 16-byte accesses need no more than the alignment of their elements here.
 template <class T> struct Piece {
   static constexpr int V = 16 / sizeof(T);
-  typedef T vec __attribute__((ext_vector_type(V)));
+  typedef T vec __attribute__((ext_vector_type(V), aligned(sizeof(T))));
 };
+// The piece at p, of which n values belong to the row (the others, and all for n <= 0, are 0 and not touched).
+template <class T>
+__device__ __forceinline__ typename Piece<T>::vec load_piece(const T* p, int n) {
+  if (n >= Piece<T>::V) return *reinterpret_cast<const typename Piece<T>::vec*>(p);
+  typename Piece<T>::vec v = (typename Piece<T>::vec)(0);
+#pragma unroll
+  for (int e = 0; e < Piece<T>::V; ++e)
+    if (e < n) v[e] = p[e];
+  return v;
+}
+template <class T>
+__device__ __forceinline__ void store_piece(T* p, const typename Piece<T>::vec& v, int n) {
+  if (n >= Piece<T>::V) {
+    *reinterpret_cast<typename Piece<T>::vec*>(p) = v;
+    return;
+  }
+#pragma unroll
+  for (int e = 0; e < Piece<T>::V; ++e)
+    if (e < n) p[e] = v[e];
+}
+// V weights from column c on (ones without a weight; 0 past the row).
+template <int V>
+__device__ __forceinline__ void load_weight(float (&w)[V], const float* p, int c, int n) {
+  typedef float f4 __attribute__((ext_vector_type(4), aligned(4)));
+  if (p != nullptr && n >= V) {
+#pragma unroll
+    for (int k = 0; k < V; k += 4) {
+      const f4 v = *reinterpret_cast<const f4*>(p + c + k);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) w[k + e] = v[e];
+    }
+  } else {
+#pragma unroll
+    for (int e = 0; e < V; ++e) w[e] = e < n ? (p != nullptr ? p[c + e] : 1.f) : 0.f;
+  }
+}
 
 template <int W>
 __device__ __forceinline__ float lanes_sum(float v) {
@@ -185,22 +222,19 @@ __global__ __launch_bounds__(256) void fwd_row_kernel(NormArgs a) {
 #pragma unroll
   for (int k = 0; k < NV; ++k) {
     const int c = (k * TPR + j) * V;
-    const bool in = c < a.D;
-    vec xv = in ? *reinterpret_cast<const vec*>(x + c) : vec(0);
+    const vec xv = load_piece(x + c, a.D - c);
 #pragma unroll
     for (int e = 0; e < V; ++e) h[k][e] = (float)xv[e];
-    if (z != nullptr) zv[k] = in ? *reinterpret_cast<const vec*>(z + c) : vec(0);
+    if (z != nullptr) zv[k] = load_piece(z + c, a.D - c);
   }
   if (a.residual != nullptr) {
     const T* res = reinterpret_cast<const T*>(a.residual) + row * a.D;
 #pragma unroll
     for (int k = 0; k < NV; ++k) {
       const int c = (k * TPR + j) * V;
-      if (c < a.D) {
-        const vec rv = *reinterpret_cast<const vec*>(res + c);
+      const vec rv = load_piece(res + c, a.D - c);
 #pragma unroll
-        for (int e = 0; e < V; ++e) h[k][e] += (float)rv[e];
-      }
+      for (int e = 0; e < V; ++e) h[k][e] += (float)rv[e];
     }
   }
 #pragma unroll
@@ -212,37 +246,38 @@ __global__ __launch_bounds__(256) void fwd_row_kernel(NormArgs a) {
 #pragma unroll
   for (int k = 0; k < NV; ++k) {
     const int c = (k * TPR + j) * V;
-    const bool in = c < a.D;
+    const int left = a.D - c;
+    const bool in = left > 0;
     const size_t at = row * a.D + c;
-    if (a.h != nullptr && in) {
+    if (a.h != nullptr) {
       vec o;
 #pragma unroll
       for (int e = 0; e < V; ++e) o[e] = (T)h[k][e];
-      *reinterpret_cast<vec*>(reinterpret_cast<T*>(a.h) + at) = o;
+      store_piece(reinterpret_cast<T*>(a.h) + at, o, left);
     }
     float y[V];
 #pragma unroll
     for (int e = 0; e < V; ++e) y[e] = h[k][e] * r;
-    if (a.w != nullptr && in) {
+    if (a.w != nullptr) {
+      float w[V];
+      load_weight<V>(w, a.w, c, left);
 #pragma unroll
-      for (int e = 0; e < V; ++e) y[e] *= a.w[c + e];
+      for (int e = 0; e < V; ++e) y[e] *= w[e];
     }
     if (z != nullptr) {
 #pragma unroll
       for (int e = 0; e < V; ++e) y[e] *= (float)zv[k][e] * fast_sigmoid((float)zv[k][e]);
     }
     if (a.scales == nullptr) {
-      if (in) {
-        vec o;
+      vec o;
 #pragma unroll
-        for (int e = 0; e < V; ++e) o[e] = (T)y[e];
-        *reinterpret_cast<vec*>(reinterpret_cast<T*>(a.y) + at) = o;
-      }
+      for (int e = 0; e < V; ++e) o[e] = (T)y[e];
+      store_piece(reinterpret_cast<T*>(a.y) + at, o, left);
       continue;
     }
     unsigned m = 0;
 #pragma unroll
-    for (int e = 0; e < V; ++e) m = max(m, in ? abs_bits(y[e]) : 0u);
+    for (int e = 0; e < V; ++e) m = max(m, e < left ? abs_bits(y[e]) : 0u);
 #pragma unroll
     for (int o = 1; o < BL; o <<= 1) {
       const unsigned u = __shfl_xor(m, o, 64);
@@ -259,8 +294,16 @@ __global__ __launch_bounds__(256) void fwd_row_kernel(NormArgs a) {
       q[e / 4] = __builtin_amdgcn_cvt_pk_fp8_f32(y[e + 2] * factor, y[e + 3] * factor, p, true);
     }
     unsigned char* o = reinterpret_cast<unsigned char*>(a.y) + at;
-    if constexpr (V == 8) *reinterpret_cast<uint2*>(o) = make_uint2(q[0], q[1]);
-    else *reinterpret_cast<unsigned*>(o) = q[0];
+    if (left >= V) {
+      typedef unsigned any __attribute__((ext_vector_type(V / 4 > 1 ? V / 4 : 2), aligned(1)));
+      typedef unsigned one __attribute__((aligned(1)));
+      if constexpr (V == 8) *reinterpret_cast<any*>(o) = any{q[0], q[1]};
+      else *reinterpret_cast<one*>(o) = q[0];
+    } else {
+#pragma unroll
+      for (int e = 0; e < V; ++e)
+        if (e < left) o[e] = (unsigned char)(q[e / 4] >> (e % 4 * 8));
+    }
   }
 }
 
@@ -277,12 +320,9 @@ __global__ __launch_bounds__(256) void bwd_row_kernel(NormArgs a) {
 #pragma unroll
   for (int k = 0; k < NV; ++k) {
     const int c = (k * TPR + j) * V;
-    const bool some = a.w != nullptr && c < a.D;
+    load_weight<V>(w[k], a.w, c, a.D - c);
 #pragma unroll
-    for (int e = 0; e < V; ++e) {
-      dw[k][e] = 0.f;
-      w[k][e] = some ? a.w[c + e] : 1.f;
-    }
+    for (int e = 0; e < V; ++e) dw[k][e] = 0.f;
   }
   int flip = 0;
   for (size_t row = (size_t)blockIdx.x * RPB + slot; row < (size_t)a.rows; row += (size_t)a.nblk * RPB) {
@@ -295,11 +335,12 @@ __global__ __launch_bounds__(256) void bwd_row_kernel(NormArgs a) {
 #pragma unroll
     for (int k = 0; k < NV; ++k) {
       const int c = (k * TPR + j) * V;
-      const bool in = c < a.D;
-      hv[k] = in ? *reinterpret_cast<const vec*>(h + c) : vec(0);
-      yv[k] = in ? *reinterpret_cast<const vec*>(dy + c) : vec(0);
-      if constexpr (GATE) zv[k] = in ? *reinterpret_cast<const vec*>(z + c) : vec(0);
-      iv[k] = in && din != nullptr ? *reinterpret_cast<const vec*>(din + c) : vec(0);
+      const int left = a.D - c;
+      hv[k] = load_piece(h + c, left);
+      yv[k] = load_piece(dy + c, left);
+      if constexpr (GATE) zv[k] = load_piece(z + c, left);
+      iv[k] = (vec)(0);
+      if (din != nullptr) iv[k] = load_piece(din + c, left);
     }
     float u[NV][V], sg[GATE ? NV : 1][V];  // u = dy silu(z)
 #pragma unroll
@@ -335,8 +376,8 @@ __global__ __launch_bounds__(256) void bwd_row_kernel(NormArgs a) {
           og[e] = (T)((float)yv[k][e] * hat * w[k][e] * (sg[k][e] * (1.f + zz * (1.f - sg[k][e]))));
         }
       }
-      *reinterpret_cast<vec*>(reinterpret_cast<T*>(a.h) + row * a.D + c) = o;
-      if constexpr (GATE) *reinterpret_cast<vec*>(reinterpret_cast<T*>(a.dgate) + row * a.D + c) = og;
+      store_piece(reinterpret_cast<T*>(a.h) + row * a.D + c, o, a.D - c);
+      if constexpr (GATE) store_piece(reinterpret_cast<T*>(a.dgate) + row * a.D + c, og, a.D - c);
     }
   }
   if (a.dw == nullptr) return;
@@ -358,7 +399,8 @@ __global__ __launch_bounds__(256) void bwd_row_kernel(NormArgs a) {
       }
     } else if (c < a.D) {
 #pragma unroll
-      for (int e = 0; e < V; ++e) part[c + e] = dw[k][e];
+      for (int e = 0; e < V; ++e)
+        if (c + e < a.D) part[c + e] = dw[k][e];
     }
   }
 }

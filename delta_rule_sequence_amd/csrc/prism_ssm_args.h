@@ -45,6 +45,12 @@ struct SsmStepArgs {
   void* y;
 };
 
+// Channels per thread of the convolution: V, or 1 where V would leave more than three quarters of a wave without any.
+// One strip per wave; at 16 x 12000 x 64, V against 1: 44 and 13 us (bf16, V 8), 23 and 17 (f32, V 4), backward 60 and
+// 30, 56 and 33; at 16 x 4800 x 160: 21 and 21, 17 and 20, 31 and 32, 39 and 36; at 400 channels V leads by a tenth or
+// more.
+template <int V> inline int conv_group(int D) { return D > 16 * V ? V : 1; }
+
 struct ConvArgs {
   const void *x, *dy;
   prism_strides xs, ys, dys;
@@ -75,14 +81,14 @@ struct NormArgs {
 };
 
 namespace host {
-// Each enqueues on `stream` and reports launch failures.
+// Each enqueues on `stream` and reports launch failures.  rows: the norm's rows fit a workgroup's registers.
 prism_status launch_ssm_fwd(prism_dtype ty, int N, int PW, const SsmArgs& a, hipStream_t stream);
 prism_status launch_ssm_bwd(prism_dtype ty, int N, int PW, const SsmArgs& a, hipStream_t stream);
 prism_status launch_ssm_step(prism_dtype ty, int N, int P, int B, const SsmStepArgs& a, hipStream_t stream);
-prism_status launch_conv_fwd(prism_dtype dt, int K, bool wide, const ConvArgs& a, hipStream_t stream);
-prism_status launch_conv_bwd(prism_dtype dt, int K, bool wide, const ConvArgs& a, hipStream_t stream);
+prism_status launch_conv_fwd(prism_dtype dt, int K, const ConvArgs& a, hipStream_t stream);
+prism_status launch_conv_bwd(prism_dtype dt, int K, const ConvArgs& a, hipStream_t stream);
 prism_status launch_conv_step(prism_dtype dt, int K, const ConvArgs& a, hipStream_t stream);
-prism_status launch_norm_fwd(prism_dtype dt, bool wide, const NormArgs& a, hipStream_t stream);
-prism_status launch_norm_bwd(prism_dtype dt, bool wide, const NormArgs& a, hipStream_t stream);
+prism_status launch_norm_fwd(prism_dtype dt, bool rows, const NormArgs& a, hipStream_t stream);
+prism_status launch_norm_bwd(prism_dtype dt, bool rows, const NormArgs& a, hipStream_t stream);
 }  // namespace host
 }  // namespace prism

@@ -468,8 +468,7 @@ typedef struct {
  *   y       [B, H, T, D] dtype dt, strided (output)
  *   conv_out[B, H, K-1, D] dtype dt (output): the last K-1 rows of [conv_in; x up to the length];
  *           NULL = not written.  May be the same buffer as conv_in.
- * Any D >= 1; a channel count that is not a multiple of 16 bytes, or a row that does not
- * start on a 16-byte boundary, takes a narrower path.  Sums in float32. */
+ * Any D >= 1 and any strides and alignment of whole elements.  Sums in float32. */
 prism_status prism_conv_fwd(const void* x, const prism_strides* x_strides, const float* conv_w, const float* bias,
                             const void* conv_in, const int* lens, int B, int H, int T, int D, int K, int silu,
                             prism_dtype dt, void* y, const prism_strides* y_strides, void* conv_out,
@@ -556,7 +555,7 @@ prism_status prism_ssm_step(const void* x, const prism_strides* x_strides, const
  *          non-finite y has a scale of infinity or NaN and bytes of NaN.
  *   h_out  [rows, D] dtype dt, dense, or NULL: h rounded (the norm uses it unrounded).  May be the
  *          same buffer as residual, or as a dense x.
- * Any D >= 1 and rows >= 1 (unaligned rows take a narrower path).  Statistics in float32. */
+ * Any D >= 1 and rows >= 1, any alignment of whole elements.  Statistics in float32. */
 prism_status prism_norm_fwd(const void* x, long long x_stride, const void* residual, const float* weight,
                             const void* gate, long long gate_stride, int rows, int D, float eps, prism_dtype dt,
                             void* y, float* scales, void* h_out, hipStream_t stream);

@@ -161,3 +161,79 @@ def test_repeated_calls_are_identical(prism, dt):
     first = run()
     for _ in range(2):
         assert all(torch.equal(p, q) for p, q in zip(first, run()))
+
+
+# More channels than a wave's narrow form takes, not a multiple of a thread's group: (dtype, D)
+WIDE = [("bf16", 129), ("bf16", 137), ("bf16", 1001), ("bf16", 519), ("f32", 65), ("f32", 263), ("bf16", 136), ("f32", 514)]
+
+
+@pytest.mark.parametrize("dt,D", WIDE)
+def test_conv_odd_widths_and_starts(prism, dt, D):
+    """Rows that start at any element, with channels left over from the vector groups; the columns beside them stay."""
+    import torch
+    B, H, T, K = 2, 1, 45, 4
+    r = Rng(60, dt)
+    lens = torch.tensor([45, 2], dtype=torch.int32, device="cuda")
+    for off in (0, 1):
+        x, past = r.vec(B, H, T, D + 3)[..., off:off + D], r.vec(B, H, K - 1, D)
+        w, bias, dy = r.flt(H, K, D), r.flt(H, D), r.vec(B, H, T, D + 2)[..., off:off + D]
+        rows = torch.full((B, H, T, D + 3), 7.0, dtype=x.dtype, device="cuda")
+        y, end = prism.conv_fwd(x, w, bias, conv_in=past, lens=lens, out=rows[..., off:off + D])
+        assert bool((rows[..., :off] == 7.0).all()) and bool((rows[..., off + D:] == 7.0).all()) and bool((y[1, :, 2:] == 7.0).all())
+        elementwise = 2e-5 / (2.0 ** -8 + 2.0 ** -12) if dt == "bf16" else 1.0
+        for b, n in enumerate((45, 2)):
+            ref, ref_end = layer.conv(f64(x[b:b + 1, :, :n]), f64(w), f64(bias), True, f64(past[b:b + 1]))
+            size = 1 + layer.conv(np.abs(f64(x[b:b + 1, :, :n])), np.abs(f64(w)), np.abs(f64(bias)), False, np.abs(f64(past[b:b + 1])))[0]
+            close(f"y[{b}]", y[b:b + 1, :, :n], ref, elementwise * size, dt)
+            np.testing.assert_array_equal(f64(end[b:b + 1]), ref_end)
+        dxr = torch.full((B, H, T, D + 3), 7.0, dtype=x.dtype, device="cuda")
+        g = prism.conv_bwd(x, w, dy, bias, out=dxr[..., off:off + D])
+        assert bool((dxr[..., :off] == 7.0).all()) and bool((dxr[..., off + D:] == 7.0).all())
+        ref = layer.conv_grad(f64(x), f64(w), f64(dy), f64(bias))
+        size = 1 + layer.conv(np.abs(f64(x)), np.abs(f64(w)), np.abs(f64(bias)), False)[0]
+        size = layer.conv_grad(np.abs(f64(x)), np.abs(f64(w)), 1.1 * np.abs(f64(dy)) * size, None, False)
+        for k in ("dx", "dconv_w", "dbias"):
+            close(k, g[k], ref[k], (elementwise if k == "dx" else 2e-5 / 2.0 ** -14 if dt == "bf16" else 1.0) * size[k], dt,
+                  None if k == "dx" else "f32")
+
+
+@pytest.mark.parametrize("dt,D", [("bf16", 519), ("f32", 263), ("bf16", 1024)])
+def test_conv_history_in_place(prism, dt, D):
+    """conv_out in the buffer of conv_in: the same rows and the same history as apart, for lengths below and above the
+    window's."""
+    import ctypes
+    import torch
+    B, H, T, K = 3, 2, 40, 4
+    lib = prism.load_library()
+    r = Rng(61, dt)
+    x, w, past = r.vec(B, H, T, D), r.flt(H, K, D), r.vec(B, H, K - 1, D)
+    lens = torch.tensor([1, 40, 2], dtype=torch.int32, device="cuda")
+    y, end = prism.conv_fwd(x, w, conv_in=past, lens=lens, out=torch.zeros_like(x))
+    y2, state = torch.zeros_like(x), past.clone()
+    p = lambda t: ctypes.c_void_p(t.data_ptr())  # noqa: E731
+    assert lib.prism_conv_fwd(p(x), None, p(w), None, p(state), p(lens), B, H, T, D, K, 1, 1 if dt == "bf16" else 0, p(y2), None,
+                              p(state), torch.cuda.current_stream().cuda_stream) == 0
+    torch.cuda.synchronize()
+    assert torch.equal(y, y2) and torch.equal(end, state)
+
+
+@pytest.mark.parametrize("dt,D", [("bf16", 1013), ("f32", 515), ("bf16", 131), ("bf16", 8191)])
+def test_norm_odd_rows_and_starts(prism, dt, D):
+    """Rows of any length that start at any element: what dense rows give, and the columns beside them are not read."""
+    r = Rng(62, dt)
+    nan = float("nan")
+    wide = [r.vec(7, D + 9) for _ in range(4)]
+    w = 1 + 0.1 * r.flt(D)
+    x, res, z, dy = (t[:, 5:5 + D] for t in wide)
+    dense = [t.contiguous() for t in (x, res, z, dy)]
+    for t in wide:
+        t[:, :5], t[:, 5 + D:] = nan, nan
+    for bits8 in (False, True):
+        a = prism.norm_fwd(x, w, residual=dense[1], gate=z, bits8=bits8)
+        b = prism.norm_fwd(dense[0], w, residual=dense[1], gate=dense[2], bits8=bits8)
+        assert all(a[k].float().equal(b[k].float()) for k in b)
+    a, b = prism.norm_bwd(x, w, dense[3], gate=z), prism.norm_bwd(dense[0], w, dense[3], gate=dense[2])
+    assert all(a[k].equal(b[k]) for k in b)
+    ref = layer.norm(f64(dense[0]), f64(w), None, f64(dense[2]))[0]
+    got = prism.norm_fwd(x, w, gate=z)["y"]
+    close("y", got, ref, (2e-5 / (2.0 ** -8 + 2.0 ** -12) if dt == "bf16" else 1.0) * (np.abs(ref) + 1e-3), dt)

@@ -17,6 +17,10 @@ and prints its own JSON line.
     python bench.py --nl [--workload NAME] [--steps K]
 times the forward with the nonlinear refinement (prism_fwd_nl) and its factor kernel.
 
+    python bench.py --layer [--workload NAME] [--steps K]
+times the state space layer (convolution, scan, gated norm) on the workload's shape: a
+prompt, its gradients and one token.
+
     python bench.py --calibrate-copy MB
 runs a plain device-to-device copy of MB megabytes (for scaling the
 FETCH_SIZE / WRITE_SIZE counters of rocprofv3) and exits.
@@ -555,6 +559,76 @@ def time_nl(w, steps, warmup, x0=None):
             "predicted_gains": pred_out, "steps": steps, "warmup": warmup, "input_sets": 2}
 
 
+def layer_bench(steps, warmup, w):
+    """The state space layer at workload w's shape (H heads of dv columns over states of dk rows, one group of B and C,
+    a window of 4): forward over the prompt, the backward of the same chain, and one token, each a run of its operators
+    on resident inputs, two input sets in turn.  One JSON line: ms per run, tokens/s and the achieved bandwidth on the
+    bytes that each operator has to move."""
+    import torch
+    import delta_rule_sequence_amd as prism
+    B, H, T, N, P, G, K = w.B, w.H, w.T, w.dk, w.dv, 1, 4
+    C, E = H * P + 2 * G * N, 2 if w.dtype == "bf16" else 4
+    gen = torch.Generator(device="cuda").manual_seed(w.seed)
+    vt = torch.bfloat16 if w.dtype == "bf16" else torch.float32
+
+    def randn(*shape, dtype=torch.float32):
+        return torch.randn(*shape, generator=gen, device="cuda").to(dtype)
+
+    cw, cb, weight, D, dt_bias = randn(1, K, C), randn(1, C), 1 + 0.1 * randn(H * P), randn(H), randn(H) - 3
+    A = -torch.rand(H, generator=gen, device="cuda") - 0.5
+    sets = [{"rows": randn(B, 1, T, C, dtype=vt), "z": randn(B, T, H * P, dtype=vt), "dt": randn(B, T, H).transpose(1, 2),
+             "dn": randn(B, T, H * P, dtype=vt)} for _ in range(2)]
+
+    def parts(c):  # heads of x, Bm, Cm in the convolution's rows
+        x, b, cc = c[:, 0].split([H * P, G * N, G * N], -1)
+        return (x.unflatten(-1, (H, P)).transpose(1, 2), b.unflatten(-1, (G, N)).transpose(1, 2),
+                cc.unflatten(-1, (G, N)).transpose(1, 2))
+
+    def forward(s):
+        c, conv = prism.conv_fwd(s["rows"], cw, cb)
+        y = torch.empty(B, T, H, P, dtype=vt, device="cuda")
+        _, S = prism.ssm_fwd(*parts(c), s["dt"], A, D, dt_bias, out=y.transpose(1, 2))
+        return c, y, prism.norm_fwd(y.flatten(2), weight, gate=s["z"])["y"], conv, S
+
+    def backward(s):
+        c, y = s["saved"]
+        n = prism.norm_bwd(y.flatten(2), weight, s["dn"], gate=s["z"])
+        dc = torch.empty_like(c)
+        prism.ssm_bwd(*parts(c), s["dt"], A, n["dh"].unflatten(-1, (H, P)).transpose(1, 2), D, dt_bias, out=parts(dc))
+        return prism.conv_bwd(s["rows"], cw, dc, cb)
+
+    for s in sets:
+        *s["saved"], _, s["conv"], s["S"] = forward(s)
+        s["row"] = s["rows"][:, :, 0].contiguous()
+
+    def token(s):
+        c = prism.conv_step(s["conv"], s["row"], cw, cb)
+        x, b, cc = (t[:, :, 0] for t in parts(c.unsqueeze(2)))
+        y = prism.ssm_step(s["S"], x, b, cc, s["dt"][:, :, 0], A, D, dt_bias)
+        return prism.norm_fwd(y.flatten(1), weight, gate=s["z"][:, 0])["y"]
+
+    rows = B * T
+    work = {  # rows in and out of each operator
+        "forward": (forward, rows, rows * ((2 * C + C + H * P + 3 * H * P) * E + 4 * H) + B * H * N * P * 4),
+        "backward": (backward, rows, rows * ((5 * H * P + 2 * C + H * P + 3 * C) * E + 8 * H)),
+        "token": (token, B, B * ((2 * (K - 1) * C + 2 * C + C + H * P + 3 * H * P) * E + 4 * H + 8 * H * N * P)),
+    }
+    res = {}
+    for name, (fn, tokens, moved) in work.items():
+        for i in range(warmup):
+            fn(sets[i % 2])
+        torch.cuda.synchronize()
+        t0 = time.perf_counter()
+        for i in range(steps):
+            fn(sets[i % 2])
+        torch.cuda.synchronize()
+        ms = (time.perf_counter() - t0) / steps * 1e3
+        res[name] = {"ms_per_step": ms, "tokens_per_s": tokens / ms * 1e3, "bytes": moved, "achieved_GBs": moved / ms / 1e6}
+    print(json.dumps({"metric": "state space layer (convolution, scan, gated norm)", "workload": w.name, "dtype": w.dtype,
+                      "config": {"B": B, "H": H, "G": G, "T": T, "N": N, "P": P, "K": K}, "steps": steps, "warmup": warmup,
+                      "peak_GBs": HBM_PEAK_GBS, **res}), flush=True)
+
+
 def main():
     ap = argparse.ArgumentParser()
     ap.add_argument("--gpus", type=int, default=1)
@@ -575,6 +649,8 @@ def main():
                          "auto (the chunked form where it applies)")
     ap.add_argument("--nl", action="store_true",
                     help="time the nonlinear-refinement forward (prism_fwd_nl) on --workload instead")
+    ap.add_argument("--layer", action="store_true",
+                    help="time the state space layer on --workload's shape instead")
     ap.add_argument("--forward-only", action="store_true",
                     help="the forward's line only: skip the backward, nonlinear, copy and GEMM legs "
                          "(for profiler runs)")
@@ -596,6 +672,10 @@ def main():
         return
     if args.bwd:
         bwd_bench(args.steps, args.warmup, args.workload, cpu=not args.no_cpu_baseline, form=args.bwd_form)
+        return
+    if args.layer:
+        import workloads
+        layer_bench(args.steps, args.warmup, workloads.workload(args.workload))
         return
     if args.nl:
         import workloads

@@ -165,7 +165,8 @@ __device__ __forceinline__ size_t plane_at(int pt, int nt) {
 // (B * HV / HP * segments, directions).  The workgroups of one (batch, group, segment) read the same rows of B and C, so
 // they take neighbouring numbers; the hardware deals workgroups out to the eight XCDs in turn, so each XCD is given a
 // range of numbers of its own, and reads those rows into its L2 once.  (Dealing single units out to the XCDs instead:
-// the state pass of 8 x 12 x 2048 tokens 70 us, this way 61.)
+// the state pass of 8 x 12 x 2048 tokens 70 us, this way 61; a batch's segments on several XCDs, for the balance of ragged
+// batches: 69, since a segment reads the ends of those before it.)
 struct Place {
   int b, hv0, seg;
 };
@@ -376,10 +377,34 @@ __global__ __launch_bounds__((waves_per_head<PW, PTW>() * HP * 64), 2) void stat
   }
 }
 
+// y of row tile tt, rounded: the columns that a lane stores.  One column tile: its own 4.  Two: lanes g, g ^ 1 exchange, and
+// a lane holds 8 neighbouring columns, from 16 (g & 1) + 8 (g >> 1) on.
+template <int TT>
+__device__ __forceinline__ bf16x4 row_piece(const f32x4 (&yt)[1][TT], int tt) {
+  bf16x4 o;
+#pragma unroll
+  for (int r = 0; r < 4; ++r) o[r] = (bf16_t)yt[0][tt][r];
+  return o;
+}
+template <int TT>
+__device__ __forceinline__ bf16x8 row_piece(const f32x4 (&yt)[2][TT], int tt) {
+  unsigned v[4] = {};
+#ifdef __HIP_DEVICE_COMPILE__
+#pragma unroll
+  for (int k = 0; k < 2; ++k) {
+    typedef bf16_t pair __attribute__((ext_vector_type(2)));
+    const pair p = {(bf16_t)yt[0][tt][2 * k], (bf16_t)yt[0][tt][2 * k + 1]}, q = {(bf16_t)yt[1][tt][2 * k], (bf16_t)yt[1][tt][2 * k + 1]};
+    const auto s = __builtin_amdgcn_permlane16_swap(__builtin_bit_cast(unsigned, p), __builtin_bit_cast(unsigned, q), false, false);
+    v[k] = s[0], v[2 + k] = s[1];
+  }
+#endif
+  return __builtin_bit_cast(bf16x8, v);
+}
+
 // Outputs of a segment from its entering state, as ssm::sweep_kernel, for HP virtual heads of a group at once.  The heads
 // share B, C and their products: a wave forms C B^T tiles and the scores of all HP heads from them.  y tiles are formed
-// transposed (rows p, columns t), so that a lane stores 4 neighbouring columns; they are stored one chunk later, so that no
-// wave waits for its stores before the next rows.
+// transposed (rows p, columns t), so that a lane stores 8 neighbouring columns (55 -> 53 us at 8 x 24 x 2048 against 4);
+// they are stored one chunk later, so that no wave waits for its stores before the next rows.
 template <int N, int PW, int PTW, int HP>
 __global__ __launch_bounds__((waves_per_head<PW, PTW>() * HP * 64), 2) void sweep_kernel(SsmArgs a) {
   constexpr int NW = waves_per_head<PW, PTW>(), NWG = NW * HP, NT = N / 16, KN = kblocks<N>(), TT = Q / 16;
@@ -402,7 +427,7 @@ __global__ __launch_bounds__((waves_per_head<PW, PTW>() * HP * 64), 2) void swee
   const size_t gstate = ((size_t)(b * a.H + h) * N) * a.P + p0 + 16 * pt0;
   const bf16_t* pb = (const bf16_t*)a.bm + b * a.bs.b + grp * a.bs.h;
   const bf16_t* pc = (const bf16_t*)a.cm + b * a.cs.b + grp * a.cs.h;
-  bf16_t* py = (bf16_t*)a.y + b * a.ys.b + h * a.ys.h + p0 + 16 * pt0 + 4 * g;
+  bf16_t* py = (bf16_t*)a.y + b * a.ys.b + h * a.ys.h + p0 + 16 * pt0 + (PTW == 2 ? 16 * (g & 1) + 8 * (g >> 1) : 4 * g);
   Rows<N, NWG> lb, lc;
   Rows<PW, NWG> lx;
   lb.init(a.bs.t);
@@ -424,16 +449,14 @@ __global__ __launch_bounds__((waves_per_head<PW, PTW>() * HP * 64), 2) void swee
     const int blk = k >> 8, r = (k >> 4) & 15, c = k & 15;
     sM[sub][Tile<Q>::at(32 * blk + r, 32 * blk + 16 + c)] = (bf16_t)0.f;
   }
-  bf16x4 out[PTW][TT];
+  typedef bf16_t ypiece __attribute__((ext_vector_type(4 * PTW)));
+  ypiece out[TT];
   const auto store = [&](int k) {
     const int t0 = (c0 + k) * Q;
 #pragma unroll
     for (int tt = 0; tt < TT; ++tt) {
       const int t = t0 + 16 * tt + i;
-      if (t < len) {
-#pragma unroll
-        for (int p = 0; p < PTW; ++p) *reinterpret_cast<bf16x4*>(py + (long long)t * a.ys.t + 16 * p) = out[p][tt];
-      }
+      if (t < len) *reinterpret_cast<ypiece*>(py + (long long)t * a.ys.t) = out[tt];
     }
   };
   for (int k = 0; k < steps; ++k) {
@@ -544,11 +567,7 @@ __global__ __launch_bounds__((waves_per_head<PW, PTW>() * HP * 64), 2) void swee
           for (int p = 0; p < PTW; ++p) hs[p][n] = mfma(fb[n], f[p][q], hs[p][n]);
     }
 #pragma unroll
-    for (int tt = 0; tt < TT; ++tt)
-#pragma unroll
-      for (int p = 0; p < PTW; ++p)
-#pragma unroll
-        for (int r = 0; r < 4; ++r) out[p][tt][r] = (bf16_t)yt[p][tt][r];
+    for (int tt = 0; tt < TT; ++tt) out[tt] = row_piece(yt, tt);
   }
   if (steps > 0) store(steps - 1);
   if (seg == a.nseg - 1) {

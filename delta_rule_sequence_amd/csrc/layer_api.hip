@@ -53,6 +53,7 @@ using namespace prism;
 
 constexpr int kChunk = 64;       // tokens per chunk of the scan (ssm::Q)
 constexpr size_t kCUs = 256;     // compute units of an MI355X
+constexpr int kMaxWidth = 1 << 26;  // channels of the convolution and the norm: the launches' 32-bit thread counts
 constexpr int kFold = 8;         // most segments whose entering states their readers form
 
 size_t elem(prism_dtype dt) { return dt == PRISM_BF16 ? 2 : 4; }
@@ -129,7 +130,7 @@ struct SsmPlan {
 prism_status ssm_plan(int B, int H, int G, int T, int N, int P, prism_dtype ty, bool bwd, SsmPlan* pl) {
   if (B <= 0 || H <= 0 || G <= 0 || T <= 0 || N <= 0 || P <= 0) return PRISM_ERR_INVALID_ARG;
   if (!known(ty) || H % G != 0) return PRISM_ERR_INVALID_ARG;
-  if (!width_ok(N) || !width_ok(P)) return PRISM_ERR_UNSUPPORTED;
+  if (!width_ok(N) || !width_ok(P) || T > INT_MAX - 4096) return PRISM_ERR_UNSUPPORTED;
   pl->PW = std::min(P, 64);
   pl->nsl = P / pl->PW;
   if ((size_t)B * (size_t)H * (size_t)pl->nsl > 65535) return PRISM_ERR_UNSUPPORTED;  // (b, virtual head) pairs map to grid.y
@@ -170,7 +171,8 @@ prism_status ssm_plan(int B, int H, int G, int T, int N, int P, prism_dtype ty, 
     pl->part_ddt = ly.add(pl->nsl > 1 ? (size_t)pl->nsl * B * H : 0, (size_t)T * 4);
     pl->part_sum = ly.add(3 * bh, (size_t)pl->nch * 4);
     // the launches cover these with 32-bit grids
-    if (rows * (N / 4) > (size_t)UINT_MAX || (size_t)B * H * T > (size_t)UINT_MAX) return PRISM_ERR_UNSUPPORTED;
+    const size_t most = (size_t)UINT_MAX - 512;
+    if (rows * (N / 4) > most || (size_t)B * H * T > most || (size_t)pl->nch * 512 > most) return PRISM_ERR_UNSUPPORTED;
   }
   if (!ly.ok()) return PRISM_ERR_INVALID_ARG;
   pl->total = std::max<size_t>(ly.total, 256);
@@ -185,7 +187,7 @@ prism_status conv_check(int B, int H, int T, int D, int K, prism_dtype dt) {
   if (K < 2 || K > 4) return PRISM_ERR_UNSUPPORTED;
   if ((size_t)B * (size_t)H > 65535) return PRISM_ERR_UNSUPPORTED;  // (b, h) pairs map to grid.z / grid.y
   if ((size_t)B * H > (size_t)INT_MAX / (size_t)D) return PRISM_ERR_UNSUPPORTED;
-  if (D > INT_MAX - 4096 || T > INT_MAX - 4096) return PRISM_ERR_UNSUPPORTED;
+  if (D > kMaxWidth || T > INT_MAX - 4096) return PRISM_ERR_UNSUPPORTED;
   return PRISM_OK;
 }
 
@@ -308,6 +310,7 @@ prism_status prism_conv_fwd(const void* x, const prism_strides* x_strides, const
   if (!make_strides(x_strides, B, H, T, D, &a.xs) || !make_strides(y_strides, B, H, T, D, &a.ys) ||
       !rows_apart(a.ys, B, H, T, D))
     return PRISM_ERR_INVALID_ARG;
+  if (y == x) return PRISM_ERR_INVALID_ARG;  // a strip reads rows that its neighbour writes
   a.x = x, a.w = conv_w, a.bias = bias, a.conv_in = conv_in, a.lens = lens, a.y = y, a.conv_out = conv_out;
   a.B = B, a.H = H, a.T = T, a.D = D, a.silu = silu != 0;
   a.strip = conv_strip(B, H, T, D, dt, false);
@@ -338,7 +341,7 @@ prism_status prism_conv_bwd(const void* x, const prism_strides* x_strides, const
   const size_t need = prism_conv_bwd_workspace_bytes(B, H, T, D, K, dt);
   if (need == 0) return PRISM_ERR_INVALID_ARG;
   if (!workspace || workspace_bytes < need) return PRISM_ERR_WORKSPACE;
-  if (!aligned16(workspace)) return PRISM_ERR_INVALID_ARG;
+  if (!aligned16(workspace) || dx == x || dx == dy) return PRISM_ERR_INVALID_ARG;
   a.x = x, a.w = conv_w, a.bias = bias, a.dy = dy, a.y = dx;
   a.B = B, a.H = H, a.T = T, a.D = D, a.silu = silu != 0;
   a.strip = conv_strip(B, H, T, D, dt, true);
@@ -364,7 +367,7 @@ static prism_status norm_check(int rows, int D, long long xs, const void* gate, 
   if (rows <= 0 || D <= 0 || !known(dt) || !(eps >= 0.f) || xs < D) return PRISM_ERR_INVALID_ARG;
   if (gate != nullptr && gs < D) return PRISM_ERR_INVALID_ARG;
   if (xs > LLONG_MAX / 8 / rows || gs > LLONG_MAX / 8 / rows) return PRISM_ERR_INVALID_ARG;
-  if (D > INT_MAX - 4096) return PRISM_ERR_UNSUPPORTED;
+  if (D > kMaxWidth) return PRISM_ERR_UNSUPPORTED;
   return PRISM_OK;
 }
 

@@ -7,10 +7,16 @@ namespace {
 
 prism_status launched() { return hipGetLastError() == hipSuccess ? PRISM_OK : PRISM_ERR_HIP; }
 
+// n workgroups over x and y (a dimension holds 2^32 threads).
+dim3 blocks(size_t n) {
+  const size_t x = n < 1 << 20 ? n : 1 << 20;
+  return dim3((unsigned)x, (unsigned)((n + x - 1) / x));
+}
+
 template <class T, int TPR, int NV>
 void fwd_row(const NormArgs& a, hipStream_t s) {
   constexpr int RPB = 256 / TPR;
-  norm::fwd_row_kernel<T, TPR, NV><<<dim3((a.rows + RPB - 1) / RPB), 256, 0, s>>>(a);
+  norm::fwd_row_kernel<T, TPR, NV><<<blocks(((size_t)a.rows + RPB - 1) / RPB), 256, 0, s>>>(a);
 }
 template <class T, int TPR, int NV>
 void bwd_row(const NormArgs& a, hipStream_t s) {
@@ -29,7 +35,7 @@ template <class T>
 prism_status fwd(bool rows, const NormArgs& a, hipStream_t s) {
   const int n = (a.D + norm::Piece<T>::V - 1) / norm::Piece<T>::V;
   if (rows) PRISM_NORM_ROWS(fwd_row, n);
-  else norm::fwd_long_kernel<T><<<dim3(a.rows), 256, 0, s>>>(a);
+  else norm::fwd_long_kernel<T><<<blocks(a.rows), 256, 0, s>>>(a);
   return launched();
 }
 template <class T>

@@ -1,5 +1,5 @@
-// prism_ssm.h - the selective state space scan in float32 arithmetic (gfx950): forward, backward and
-// the single-token step, for bfloat16 and float32 tensors.
+// prism_ssm.h - the selective state space scan in float32 arithmetic (gfx950): forward and backward of float32
+// tensors, and for both types the single-token step, the scan over segments and the sums of the gradients' shares.
 //
 //   d_t = softplus(dt_t + bias),  l_t = d_t A,  S_t = e^{l_t} S_{t-1} + d_t B_t x_t^T,  y_t = S_t^T C_t + D x_t
 //
@@ -10,6 +10,10 @@
 // segment's end state from zero, a scan over the segments gives the states that enter them.
 // c is summed in float64 and held as base-2 exponents in two floats, so that e^{c_t - c_s} keeps
 // float32 accuracy after long decays.
+//
+// Products run on the float32 matrix instructions (153 TFLOP/s in a library product of 8192^3).  Measured: forward of
+// 3 x 6 x 509 tokens, N = P = 32: passes of 7, 3 and 11 us; backward of 2 x 6 x 333: 7, 3, 6, 17, 5 and 4 us.  Small
+// calls: launches and one chunk's chain of products bound them.
 #pragma once
 #include "prism_ssm_args.h"
 #include "prism_tile.h"
@@ -753,7 +757,8 @@ __global__ __launch_bounds__(256) void head_sum_kernel(SsmArgs a) {
   if (threadIdx.x == 0) out[h] = (float)part[0];
 }
 
-// One token: S' = e^{d A} S + d B x^T in place, y = S'^T C + D x.  Bound by reading and writing S.  One workgroup per
+// One token: S' = e^{d A} S + d B x^T in place, y = S'^T C + D x.  Bound by reading and writing S: 83 us for 256 x 24
+// states of 128 x 64, 4.9 TB/s.  One workgroup per
 // (b, h): P / 4 threads across the columns (16-byte state accesses), 256 / (P / 4) groups of rows whose shares of y
 // are summed in LDS.
 template <class T, int N, int P>

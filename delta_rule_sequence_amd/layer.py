@@ -69,6 +69,12 @@ def _tensor(name, t, shape, dtype, dev):
     return t
 
 
+def _sizes(*n):
+    """Sizes as the C interface holds them (ctypes would cut them off)."""
+    if max(n) > 0x7fffffff:
+        raise PrismError(f"a size of {max(n)} is more than 2^31 - 1")
+
+
 def _dense(name, t, shape, dtype, dev):
     """A dense tensor argument's pointer (None: not given)."""
     if t is None:
@@ -167,6 +173,7 @@ def _conv_shape(x, conv_w, bias, dim):
         raise PrismError("conv_w must be a tensor [H, K, D]")
     shape, K = x.shape, conv_w.shape[1]
     B, H, D = shape[0], shape[1], shape[-1]
+    _sizes(K, *shape)
     _tensor("x", x, shape, x.dtype, dev)
     return dev, B, H, D, K, _dense("conv_w", conv_w, (H, K, D), _F32, dev), _dense("bias", bias, (H, D), _F32, dev)
 
@@ -227,6 +234,7 @@ def _scan_shape(x, Bm, Cm, dt, A, D, dt_bias, token):
     shape, (G, N) = x.shape, (Bm.shape[1], Bm.shape[-1])
     B, H, P = shape[0], shape[1], shape[-1]
     bc = (B, G, N) if token else (B, G, shape[2], N)
+    _sizes(G, N, *shape)
     _tensor("x", x, shape, x.dtype, dev)
     _tensor("Bm", Bm, bc, x.dtype, dev)
     _tensor("Cm", Cm, bc, x.dtype, dev)
@@ -336,6 +344,7 @@ def norm_fwd(x, weight=None, residual=None, gate=None, eps=1e-5, bits8=False):
         raise PrismError("x must have at least one axis")
     shape, D = x.shape, x.shape[-1]
     rows = x.numel() // D if D else 0
+    _sizes(rows, D)
     xs = _rows("x", x, shape, x.dtype, dev)
     gs = _rows("gate", gate, shape, x.dtype, dev) if gate is not None else 0
     pw, pr = _dense("weight", weight, (D,), _F32, dev), _dense("residual", residual, shape, x.dtype, dev)
@@ -362,6 +371,7 @@ def norm_bwd(h, weight, dy, gate=None, dh_in=None, eps=1e-5, workspace=None):
         raise PrismError("h must have at least one axis")
     shape, D = h.shape, h.shape[-1]
     rows = h.numel() // D if D else 0
+    _sizes(rows, D)
     hs = _rows("h", h, shape, h.dtype, dev)
     gs = _rows("gate", gate, shape, h.dtype, dev) if gate is not None else 0
     pw, pi = _dense("weight", weight, (D,), _F32, dev), _dense("dh_in", dh_in, shape, h.dtype, dev)

@@ -451,10 +451,11 @@ prism_status prism_fwd_noalloc(const void* q, const void* k, const void* v,
  * axis and the given element strides of the other three; NULL = dense in that order, as
  * everywhere above.  So heads of a token-major projection output [B, T, channels] are read
  * and written in place.  Strides must be positive where their axis is longer than 1; rows of
- * an output must not overlap.  Ownership, streams and errors as prism_fwd; the stream must
- * belong to the current device.  Non-finite inputs reach the outputs they enter; in the scan
- * a non-finite row of x (of dy in its backward) may also reach the other tokens of its chunk
- * of 64.  Rows past a sequence's length never reach anything. */
+ * an output must not overlap, and outputs share no memory with inputs but where it is said.
+ * Ownership, streams and errors as prism_fwd; the stream must belong to the current device.
+ * Non-finite inputs reach the outputs they enter; in the scan a non-finite row of x (of dy in
+ * its backward) may also reach the other tokens of its chunk of 64.  Rows past a sequence's
+ * length never reach anything. */
 typedef struct {
   long long b, h, t;
 } prism_strides;
@@ -468,7 +469,7 @@ typedef struct {
  *   y       [B, H, T, D] dtype dt, strided (output)
  *   conv_out[B, H, K-1, D] dtype dt (output): the last K-1 rows of [conv_in; x up to the length];
  *           NULL = not written.  May be the same buffer as conv_in.
- * Any D >= 1 and any strides and alignment of whole elements.  Sums in float32. */
+ * Any D from 1 to 2^26 and any strides and alignment of whole elements.  Sums in float32. */
 prism_status prism_conv_fwd(const void* x, const prism_strides* x_strides, const float* conv_w, const float* bias,
                             const void* conv_in, const int* lens, int B, int H, int T, int D, int K, int silu,
                             prism_dtype dt, void* y, const prism_strides* y_strides, void* conv_out,
@@ -508,7 +509,8 @@ prism_status prism_conv_step(const void* x, const prism_strides* x_strides, cons
  * at most 16 MB apart (else PRISM_ERR_UNSUPPORTED).
  * Precision: decays and states in float32 from log decays summed in float64.  With PRISM_BF16
  * the products run on bfloat16 operands; what enters the state is split into bfloat16 parts
- * that keep its float32 digits, the score matrix and the state's readout are rounded once.
+ * that keep its float32 digits, the score matrix (with the skip term D on its diagonal) and the
+ * state's readout are rounded once.
  * Workspace: prism_ssm_fwd_workspace_bytes (0 for invalid or unsupported arguments). */
 size_t prism_ssm_fwd_workspace_bytes(int B, int H, int G, int T, int N, int P, prism_dtype ty);
 prism_status prism_ssm_fwd(const void* x, const prism_strides* x_strides, const void* Bm,
@@ -524,7 +526,9 @@ prism_status prism_ssm_fwd(const void* x, const prism_strides* x_strides, const 
  *   dx [B, H, T, P], dBm, dCm [B, G, T, N] dtype ty, strided (dBm, dCm: summed over the group's heads
  *   in float32);  ddt [B, H, T] float32, dense;  dA [H], and dD, ddt_bias [H] (NULL = not wanted),
  *   float32, summed over batches and tokens.  Every sum has a fixed order.
- * Supported and precision as prism_ssm_fwd.  Workspace: prism_ssm_bwd_workspace_bytes. */
+ * Supported and precision as prism_ssm_fwd (rows of dy, dx, dBm and dCm too); with PRISM_BF16 ddt, dA and
+ * ddt_bias come from states of 16 bits and more (about 1e-6 of their size).  Workspace:
+ * prism_ssm_bwd_workspace_bytes. */
 size_t prism_ssm_bwd_workspace_bytes(int B, int H, int G, int T, int N, int P, prism_dtype ty);
 prism_status prism_ssm_bwd(const void* x, const prism_strides* x_strides, const void* Bm,
                            const prism_strides* b_strides, const void* Cm, const prism_strides* c_strides,
@@ -555,7 +559,7 @@ prism_status prism_ssm_step(const void* x, const prism_strides* x_strides, const
  *          non-finite y has a scale of infinity or NaN and bytes of NaN.
  *   h_out  [rows, D] dtype dt, dense, or NULL: h rounded (the norm uses it unrounded).  May be the
  *          same buffer as residual, or as a dense x.
- * Any D >= 1 and rows >= 1, any alignment of whole elements.  Statistics in float32. */
+ * Any D from 1 to 2^26, rows >= 1 and any alignment of whole elements.  Statistics in float32. */
 prism_status prism_norm_fwd(const void* x, long long x_stride, const void* residual, const float* weight,
                             const void* gate, long long gate_stride, int rows, int D, float eps, prism_dtype dt,
                             void* y, float* scales, void* h_out, hipStream_t stream);

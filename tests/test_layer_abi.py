@@ -160,3 +160,20 @@ def test_binding_refuses_cpu_tensors():
               lambda: prism.norm_fwd(x), lambda: prism.norm_bwd(x, None, x), lambda: prism.norm_fwd(None)):
         with pytest.raises(prism.PrismError):
             f()
+
+
+def test_conv_in_place_rows(lib):
+    """A strip reads rows that its neighbour would overwrite."""
+    assert conv_fwd(lib, x=P, y=P) == INVALID
+    assert conv_bwd(lib, x=P, dy=2 * P, dx=P) == INVALID and conv_bwd(lib, x=P, dy=2 * P, dx=2 * P) == INVALID
+
+
+@pytest.mark.parametrize("call", [ssm_fwd, ssm_bwd, conv_fwd, conv_bwd])
+def test_longest_sequence(lib, call):
+    assert call(lib, T=2 ** 31 - 1) == UNSUPPORTED
+
+
+@pytest.mark.parametrize("call", [norm_fwd, norm_bwd, conv_fwd, conv_bwd])
+def test_widest_rows(lib, call):
+    wide = {"xs": 1 << 27} if call is norm_fwd else {"hs": 1 << 27} if call is norm_bwd else {}
+    assert call(lib, D=(1 << 26) + 1, **wide) == UNSUPPORTED

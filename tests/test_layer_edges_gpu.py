@@ -237,3 +237,23 @@ def test_norm_odd_rows_and_starts(prism, dt, D):
     ref = layer.norm(f64(dense[0]), f64(w), None, f64(dense[2]))[0]
     got = prism.norm_fwd(x, w, gate=z)["y"]
     close("y", got, ref, (2e-5 / (2.0 ** -8 + 2.0 ** -12) if dt == "bf16" else 1.0) * (np.abs(ref) + 1e-3), dt)
+
+
+@pytest.mark.parametrize("dt,rows,D", [("bf16", (1 << 25) + 77, 5), ("bf16", (1 << 20) + 3, 8193)])
+def test_norm_many_rows(prism, dt, rows, D):
+    """More workgroups than one axis of the launch holds: every row as in a call of its own."""
+    import torch
+    x = torch.empty(rows, D, dtype=torch.bfloat16, device="cuda").normal_(generator=torch.Generator("cuda").manual_seed(5))
+    y = prism.norm_fwd(x)["y"]
+    for at in (0, rows // 2, (1 << 20) - 100, rows - 200):
+        assert torch.equal(y[at:at + 200], prism.norm_fwd(x[at:at + 200].clone())["y"])
+
+
+def test_sizes_past_the_interface(prism):
+    """More rows than the C interface can be told are refused, not cut off."""
+    import torch
+    x = torch.zeros(1, dtype=torch.bfloat16, device="cuda").expand((1 << 32) + 5, 1)
+    with pytest.raises(prism.PrismError):
+        prism.norm_fwd(x)
+    with pytest.raises(prism.PrismError):
+        prism.conv_fwd(x[None, None], torch.zeros(1, 4, 1, device="cuda"))

@@ -15,21 +15,22 @@ dim3 blocks(size_t n) {
 
 template <class T, int TPR, int NV>
 void fwd_row(const NormArgs& a, hipStream_t s) {
-  constexpr int RPB = 256 / TPR;
-  norm::fwd_row_kernel<T, TPR, NV><<<blocks(((size_t)a.rows + RPB - 1) / RPB), 256, 0, s>>>(a);
+  constexpr int RPB = norm::row_threads(TPR) / TPR;
+  norm::fwd_row_kernel<T, TPR, NV><<<blocks(((size_t)a.rows + RPB - 1) / RPB), norm::row_threads(TPR), 0, s>>>(a);
 }
 template <class T, int TPR, int NV>
 void bwd_row(const NormArgs& a, hipStream_t s) {
-  if (a.gate != nullptr) norm::bwd_row_kernel<T, TPR, NV, true><<<dim3(a.nblk), 256, 0, s>>>(a);
-  else norm::bwd_row_kernel<T, TPR, NV, false><<<dim3(a.nblk), 256, 0, s>>>(a);
+  if (a.gate != nullptr) norm::bwd_row_kernel<T, TPR, NV, true><<<dim3(a.nblk), norm::row_threads(TPR), 0, s>>>(a);
+  else norm::bwd_row_kernel<T, TPR, NV, false><<<dim3(a.nblk), norm::row_threads(TPR), 0, s>>>(a);
 }
 
-// Lanes and pieces of a row of n 16-byte pieces: a part of a wave up to 32 pieces, a wave up to 256, else the workgroup.
+// Lanes and pieces of a row of n 16-byte pieces: a part of a wave up to 32 pieces, a wave up to 256, 256 lanes up to 1024,
+// else 1024.
 #define PRISM_NORM_ROWS(F, n)                                                                          \
   ((n) <= 8 ? F<T, 8, 1>(a, s) : (n) <= 16 ? F<T, 16, 1>(a, s) : (n) <= 32 ? F<T, 32, 1>(a, s)         \
    : (n) <= 64 ? F<T, 64, 1>(a, s) : (n) <= 128 ? F<T, 64, 2>(a, s) : (n) <= 192 ? F<T, 64, 3>(a, s)   \
    : (n) <= 256 ? F<T, 64, 4>(a, s) : (n) <= 512 ? F<T, 256, 2>(a, s) : (n) <= 768 ? F<T, 256, 3>(a, s) \
-   : F<T, 256, 4>(a, s))
+   : (n) <= 1024 ? F<T, 256, 4>(a, s) : F<T, 1024, 2>(a, s))
 
 template <class T>
 prism_status fwd(bool rows, const NormArgs& a, hipStream_t s) {

@@ -4,7 +4,7 @@
 //   with u = dy silu(z):  dw = sum_rows u h r,   dz = dy h r w silu'(z)
 //   dh = r (u w - h r mean(u w h r)) + dh_in
 //
-// Bound by its bytes.  A row of up to 16384 bytes stays in the registers of a group of lanes and is read once.  Measured
+// Bound by its bytes.  A row of up to 32768 bytes stays in the registers of a group of lanes and is read once.  Measured
 // (a copy of 1 GiB makes 5.2 TB/s): 16384 x 1536 bfloat16 with residual, 8-bit output 33 us, 4.9 TB/s; 131072 x 64
 // gated 10.6 us, 4.7; backward of 16384 x 768 with a residual's gradient 20 us and 4 for dw, 4.3 TB/s; rows of odd
 // length, which start anywhere: backward of 4924 x 843, gated, 26 us.
@@ -144,7 +144,7 @@ __global__ __launch_bounds__(256) void bwd_long_kernel(NormArgs a) {
   }
 }
 
-// ---- rows of up to 16384 bytes ------------------------------------------------------------------------
+// ---- rows of up to 32768 bytes ------------------------------------------------------------------------
 // A row lies in the registers of TPR lanes (a part of a wave, a wave or the workgroup), NV 16-byte pieces per lane, and
 // is read once: statistics by lane exchanges, then the outputs from the same registers.  Piece k of lane j is number
 // k TPR + j of the row, so a 128-value block of the 8-bit output is 128 / V neighbouring lanes.
@@ -197,14 +197,18 @@ __device__ __forceinline__ float lanes_sum(float v) {
   return v;
 }
 
-// Sum over a row's lanes; buf (2 x 4 floats, alternating) joins the waves of a 256-lane row.
+// Lanes of a workgroup whose rows have TPR lanes each.
+constexpr int row_threads(int TPR) { return TPR > 256 ? TPR : 256; }
+// Sum over a row's lanes; buf (TPR / 64 floats) joins the waves of a row that fills the workgroup.
 template <int TPR>
 __device__ __forceinline__ float row_sum(float v, float* buf) {
   v = lanes_sum<(TPR < 64 ? TPR : 64)>(v);
-  if constexpr (TPR == 256) {
+  if constexpr (TPR >= 256) {
     if (lane_id() == 0) buf[wave_id()] = v;
     __syncthreads();
-    v = (buf[0] + buf[1]) + (buf[2] + buf[3]);
+    v = 0.f;
+#pragma unroll
+    for (int k = 0; k < TPR / 64; k += 4) v += (buf[k] + buf[k + 1]) + (buf[k + 2] + buf[k + 3]);
   }
   return v;
 }
@@ -213,13 +217,13 @@ __device__ __forceinline__ float row_sum(float v, float* buf) {
 __device__ __forceinline__ float fast_sigmoid(float z) { return __builtin_amdgcn_rcpf(1.f + __expf(-z)); }
 
 template <class T, int TPR, int NV>
-__global__ __launch_bounds__(256) void fwd_row_kernel(NormArgs a) {
+__global__ __launch_bounds__(row_threads(TPR)) void fwd_row_kernel(NormArgs a) {
   constexpr int V = Piece<T>::V, BL = kBlock / V < TPR ? kBlock / V : TPR;  // lanes of a scale block
   typedef typename Piece<T>::vec vec;
-  __shared__ float buf[4];
+  __shared__ float buf[TPR < 256 ? 1 : TPR / 64];
   const int j = threadIdx.x % TPR;
-  const size_t row = block_id() * (256 / TPR) + threadIdx.x / TPR;
-  if (row >= (size_t)a.rows) return;  // whole workgroups only where TPR = 256
+  const size_t row = block_id() * (row_threads(TPR) / TPR) + threadIdx.x / TPR;
+  if (row >= (size_t)a.rows) return;  // whole workgroups only where a row fills one
   const T* x = reinterpret_cast<const T*>(a.x) + row * a.xs;
   const T* z = a.gate != nullptr ? reinterpret_cast<const T*>(a.gate) + row * a.gs : nullptr;
   float h[NV][V];
@@ -316,10 +320,10 @@ __global__ __launch_bounds__(256) void fwd_row_kernel(NormArgs a) {
 // The same for the backward: the workgroup walks rows (256 / TPR at a time) with its lanes' columns of dweight in
 // registers, joins them over its row slots in LDS and leaves one share per workgroup.
 template <class T, int TPR, int NV, bool GATE>
-__global__ __launch_bounds__(256) void bwd_row_kernel(NormArgs a) {
-  constexpr int V = Piece<T>::V, RPB = 256 / TPR;
+__global__ __launch_bounds__(row_threads(TPR)) void bwd_row_kernel(NormArgs a) {
+  constexpr int V = Piece<T>::V, RPB = row_threads(TPR) / TPR;
   typedef typename Piece<T>::vec vec;
-  __shared__ float buf[2][8];
+  __shared__ float buf[2][2][TPR < 256 ? 1 : TPR / 64];  // taken in turn: no wait for the last row's reads
   __shared__ float sdw[RPB > 1 ? RPB * TPR * V : 1];
   const int j = threadIdx.x % TPR, slot = threadIdx.x / TPR;
   float dw[NV][V], w[NV][V];
@@ -363,8 +367,8 @@ __global__ __launch_bounds__(256) void bwd_row_kernel(NormArgs a) {
         q += u[k][e] * w[k][e] * hh;
       }
     }
-    s = row_sum<TPR>(s, buf[flip]);
-    q = row_sum<TPR>(q, buf[flip] + 4);
+    s = row_sum<TPR>(s, buf[flip][0]);
+    q = row_sum<TPR>(q, buf[flip][1]);
     flip ^= 1;
     const float r = 1.f / sqrtf(s / a.D + a.eps), mean = q * r / a.D;
 #pragma unroll

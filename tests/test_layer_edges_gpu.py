@@ -4,6 +4,7 @@ import numpy as np
 import pytest
 
 from oracle import layer
+from tests import test_layer_gpu as base
 from tests.conftest import gpu_available
 from tests.test_layer_gpu import Rng, close, f64, scan_inputs, sizes
 
@@ -257,3 +258,11 @@ def test_sizes_past_the_interface(prism):
         prism.norm_fwd(x)
     with pytest.raises(prism.PrismError):
         prism.conv_fwd(x[None, None], torch.zeros(1, 4, 1, device="cuda"))
+
+
+@pytest.mark.parametrize("dt,rows,D", [("bf16", 3, 8193), ("bf16", 2, 16384), ("bf16", 2, 16385), ("f32", 5, 4097), ("f32", 2, 8192),
+                                       ("f32", 3, 8193), ("bf16", 1100, 8250)])
+@pytest.mark.parametrize("residual,gate,weight", [(True, True, True), (False, False, False)])
+def test_norm_long_rows(prism, dt, rows, D, residual, gate, weight):
+    """On both sides of the lengths that a workgroup of 256, of 1024 lanes holds; more rows than workgroups."""
+    base.test_norm_fwd_bwd(prism, (dt, rows, D), residual, gate, weight)

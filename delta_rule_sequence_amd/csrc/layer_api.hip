@@ -136,11 +136,15 @@ prism_status ssm_plan(int B, int H, int G, int T, int N, int P, prism_dtype ty, 
   if ((size_t)B * (size_t)H * (size_t)pl->nsl > 65535) return PRISM_ERR_UNSUPPORTED;  // (b, virtual head) pairs map to grid.y
   pl->HV = H * pl->nsl;
   pl->nch = (int)(((long long)T + kChunk - 1) / kChunk);
-  // Segments until the device is full: each costs a state in the workspace and a second read of its inputs.  Up to
-  // kFold of them the passes form their entering states themselves; the forward then takes more, since its sweep is
-  // bound by the chunks it walks one after another (8 x 24 x 2048 tokens: 137 us with 2 segments, 94 with 5, 86 with 6,
-  // 97 with 8; 2 x 4 x 16384, where a scan over the segments comes on top: 43 us with 64, 46 with 128; the backward's
-  // passes at 8 x 12 x 2048: 96 us with 5, 105 with 8).
+  // Segments until the device is full: each costs a state in the workspace and a second read of its inputs; up to kFold of
+  // them the passes form their entering states themselves, more take a scan over them.  Forward: two workgroups of two
+  // heads per CU and some more, since a batch may be ragged (8 x 24 x 2048 tokens, N = 128: 127 us with 2 segments, 93 with
+  // 4, 86 with 5, 87 with 6, 91 with 8, but ragged 84 with 5 and 78 with 6; 32 x 8 x 1024: 46 with 4, 54 with 8), no more
+  // than those two per CU where the scan comes on top (8 x 12: 57 with 8, 66 with 11; 2 x 4 x 16384, N = 64: 39 with 64, 35
+  // with 128).  Half as many for float32 with a scan (4 x 8 x 2048, N = 64: 52 with 16, 57 with 32; without one not: 8 x 12 x
+  // 2048, N = 128: 296 with 5, 251 with 8) and for the backward, whose two directions fill the device sooner (8 x 12 x 2048:
+  // 165 with 5, 176 with 8; 2 x 4 x 16384: 99 with 64, 109 with 128) and which takes one rather than two (8 x 24 x 2048: 325
+  // and 339; 32 x 8 x 1024: 132 and 143).
   // Least chunks of a segment: two for bfloat16; a float32 chunk takes longer than a segment costs (3 x 6 x 509 tokens,
   // N = P = 32: 30 us with two, 18 with one).
   const int least = ty == PRISM_BF16 || pl->nch <= 2 ? 2 : 1;
@@ -149,8 +153,14 @@ prism_status ssm_plan(int B, int H, int G, int T, int N, int P, prism_dtype ty, 
     pl->seg_chunks = std::max(std::min(pl->nch, least), (int)((pl->nch + want - 1) / want));
     pl->nseg = (pl->nch + pl->seg_chunks - 1) / pl->seg_chunks;
   };
-  cut(std::max<size_t>(1, 5 * kCUs / bh));
-  if (bwd || pl->nseg > kFold) cut(std::max<size_t>(1, 2 * kCUs / bh));
+  const size_t half = std::max<size_t>(1, 2 * kCUs / bh);
+  if (bwd) {
+    cut(half == 2 ? 1 : half);
+  } else {
+    cut(std::max<size_t>(1, 9 * kCUs / 2 / bh));
+    if (pl->nseg > kFold) cut(4 * kCUs / bh);
+    if (pl->nseg > kFold && ty == PRISM_F32) cut(half);
+  }
   const size_t mat = (size_t)N * pl->PW;
   Layout ly;
   const int dirs = bwd ? 2 : 1;
@@ -158,12 +168,19 @@ prism_status ssm_plan(int B, int H, int G, int T, int N, int P, prism_dtype ty, 
   pl->seg = ly.add(segs ? dirs * bh * pl->nseg : 0, mat * 4);
   pl->seg_dec = ly.add(segs ? dirs * bh * pl->nseg : 0, 4);
   if (bwd) {
-    // the gradient pass: a workgroup walks per_split of a group's virtual heads; enough splits for a workgroup per CU
-    // (two per CU, measured on 8 x 12 x 2048 tokens: 122 us with the sum of their shares where one takes 104)
-    const size_t per_group = (size_t)pl->HV / G, units = (size_t)pl->nch * B * G;
-    size_t ns = std::min(per_group, std::max<size_t>(1, (kCUs + units - 1) / units));
-    pl->per_split = (int)((per_group + ns - 1) / ns);
-    pl->nsplit = (int)((per_group + pl->per_split - 1) / pl->per_split);
+    // The gradient pass: a workgroup walks per_split of a group's virtual heads, and loads and sums outside the heads cost
+    // it about one more.  Splits for the least time over the rounds that the device needs; a CU holds one workgroup, or two
+    // of float32 with small tiles.  (float32, 24 heads of 128 in 4 groups, 2464 tokens, N = 16: 147 us with 2 splits, 117 with
+    // 3, 124 with 4; 2 x 8 of 64, N = 128, 1733 tokens: 130 with 4, 145 with 8;
+    // bfloat16, 3 x 8 of 64, N = 64, 4000 tokens: 96 with 2, 85 with 4.)
+    const unsigned per_group = (unsigned)(pl->HV / G);
+    const size_t units = (size_t)pl->nch * B * G, slots = ty == PRISM_F32 && N + pl->PW <= 96 ? 2 * kCUs : kCUs;
+    size_t least_time = SIZE_MAX;
+    for (unsigned ns = 1; ns <= std::min(per_group, 64u); ++ns) {
+      const unsigned per = (per_group + ns - 1) / ns, n = (per_group + per - 1) / per;
+      const size_t time = (units * n + slots - 1) / slots * (per + 1);
+      if (time < least_time) least_time = time, pl->per_split = (int)per, pl->nsplit = (int)n;
+    }
     const size_t rows = (size_t)B * G * T;
     pl->st = ly.add(2 * bh * pl->nch, mat * 4);
     pl->part_b = ly.add(pl->nsplit > 1 ? pl->nsplit * rows : 0, (size_t)N * 4);

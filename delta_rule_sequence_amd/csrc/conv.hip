@@ -16,8 +16,9 @@ dim3 strip_grid(const ConvArgs& a, int V) {
 template <class T, int K, bool SILU>
 void fwd_act(const ConvArgs& a, hipStream_t s) {
   constexpr int V = 16 / sizeof(T);
-  if (conv_group<V>(a.D) == V) conv::fwd_kernel<T, K, V, 8, SILU><<<strip_grid(a, V), 256, 0, s>>>(a);
-  else conv::fwd_kernel<T, K, 1, 8, SILU><<<strip_grid(a, 1), 256, 0, s>>>(a);
+  if (conv_group<V>(a.D) == 1) conv::fwd_kernel<T, K, 1, 8, SILU, false><<<strip_grid(a, 1), 256, 0, s>>>(a);
+  else if (a.D % V == 0) conv::fwd_kernel<T, K, V, 8, SILU, false><<<strip_grid(a, V), 256, 0, s>>>(a);
+  else conv::fwd_kernel<T, K, V, 8, SILU, true><<<strip_grid(a, V), 256, 0, s>>>(a);
 }
 template <class T, int K>
 prism_status fwd(const ConvArgs& a, hipStream_t s) {
@@ -29,8 +30,9 @@ prism_status fwd(const ConvArgs& a, hipStream_t s) {
 template <class T, int K, bool SILU>
 void bwd_act(const ConvArgs& a, hipStream_t s) {
   constexpr int V = 4;
-  if (conv_group<V>(a.D) == V) conv::bwd_kernel<T, K, V, 4, SILU><<<strip_grid(a, V), 256, 0, s>>>(a);
-  else conv::bwd_kernel<T, K, 1, 4, SILU><<<strip_grid(a, 1), 256, 0, s>>>(a);
+  if (conv_group<V>(a.D) == 1) conv::bwd_kernel<T, K, 1, 4, SILU, false><<<strip_grid(a, 1), 256, 0, s>>>(a);
+  else if (a.D % V == 0) conv::bwd_kernel<T, K, V, 4, SILU, false><<<strip_grid(a, V), 256, 0, s>>>(a);
+  else conv::bwd_kernel<T, K, V, 4, SILU, true><<<strip_grid(a, V), 256, 0, s>>>(a);
 }
 template <class T, int K>
 prism_status bwd(const ConvArgs& a, hipStream_t s) {

@@ -81,9 +81,16 @@ __device__ __forceinline__ float sum_groups(float v) {  // over the four 16-lane
   return v;
 }
 
+// Whether a token of log decay l lets nothing of the state through: its gradient e^l <S, R> is 0 in float32, where the
+// sums that cancel to it would leave their roundings (times a large step, in dA).
+__device__ __forceinline__ bool closed(float l) { return l < -105.f; }
+
 __device__ __forceinline__ float softplus_f(float z) { return z > 20.f ? z : log1pf(expf(z)); }
 
 constexpr double kLog2e = 1.4426950408889634;
+// A token that decays the state by more than 2^-kGone leaves 0 of it in float32; the decay counts as this much, so that a
+// chunk's running sum keeps its digits for the tokens after it.
+constexpr double kGone = 160.0;
 
 // Lane t's share of a chunk's scalars: running and total log2 decay, step, and the step's derivative with respect to
 // dt.  Tokens at or past len have a step of 0 (decay 1, nothing written).
@@ -104,6 +111,7 @@ __device__ __forceinline__ Token chunk_token(const SsmArgs& a, int b, int h, int
     k.d = a.softplus ? softplus_f(z) : z;
     k.dz = a.softplus ? 1.f / (1.f + expf(-z)) : 1.f;
     l2 = (double)k.d * (double)a.A[h] * kLog2e;
+    if (l2 < -kGone) l2 = -kGone;
   }
   k.c = wave_scan(l2);
   k.tot = last_lane(k.c);
@@ -637,7 +645,7 @@ __global__ __launch_bounds__(256) void grad_kernel(SsmArgs a) {
       const double fs = wave_scan(f), ftot = last_lane(fs);  // suffix sum from t: ftot - fs + f
       const double js = wave_scan(jd);                       // prefix sum before t: js - jd
       const float kk = sc.dec * ((sK[0] + sK[1]) + (sK[2] + sK[3]));
-      const float dl = (float)((ftot - fs + f) + (js - jd) + kk);
+      const float dl = closed(d * Ah) ? 0.f : (float)((ftot - fs + f) + (js - jd) + kk);
       const float ddt = (qoff + sDiag[t] + J0 + Ah * dl) * sSig[t];
       const bool in = t0 + t < a.T;
       if (in) {

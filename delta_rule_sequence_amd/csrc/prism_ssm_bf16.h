@@ -140,10 +140,6 @@ struct Rows {
 };
 __device__ __forceinline__ void loads_done() { asm volatile("s_waitcnt vmcnt(0)" ::: "memory"); }
 
-__device__ __forceinline__ float decay(const Scal& s, int t, int r) {  // e^{c_t - c_r}
-  return __builtin_amdgcn_exp2f((s.ch[t] - s.ch[r]) + (s.cl[t] - s.cl[r]));
-}
-
 // v, or 0 where !on, whatever v is (as bits: the compiler would branch around what leads to v otherwise).
 __device__ __forceinline__ float keep(float v, bool on) { return val(bits(v) & (on ? 0xffffffffu : 0u)); }
 
@@ -510,7 +506,9 @@ __global__ __launch_bounds__((waves_per_head<PW, PTW>() * HP * 64), 2) void swee
 #pragma unroll
       for (int u = 0; u < HP; ++u) {
         const Scal& sc = scal[u][k % NB];
-        const float cht = sc.ch[t];  // its float32 digits are enough for a score that is rounded to bfloat16
+        // the high part's digits are enough for a score that is rounded to bfloat16: for decays it lies above -64 kGone,
+        // so the exponent is off by 2^-10 at most
+        const float cht = sc.ch[t];
         const f32x4 chs = *reinterpret_cast<const f32x4*>(sc.ch + s0), ds = *reinterpret_cast<const f32x4*>(sc.d + s0);
         bf16x4 m;
 #pragma unroll
@@ -852,7 +850,7 @@ __global__ __launch_bounds__(512, 2) void grad_kernel(SsmArgs a) {
       const double f = (double)row - (double)d * qoff + I;
       const double fs = wave_scan(f), ftot = last_lane(fs);  // suffix sum from t: ftot - fs + f
       const double js = wave_scan(jd);                       // prefix sum before t: js - jd
-      const float dl = (float)((ftot - fs + f) + (js - jd) + (double)(sc.dec * kk));
+      const float dl = closed(d * Ah) ? 0.f : (float)((ftot - fs + f) + (js - jd) + (double)(sc.dec * kk));
       const float ddt = (qoff + sDiag[t] + J0 + Ah * dl) * sSig[par][hb][t];
       const bool in = t0 + t < a.T;
       if (in) {

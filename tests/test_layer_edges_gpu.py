@@ -266,3 +266,28 @@ def test_sizes_past_the_interface(prism):
 def test_norm_long_rows(prism, dt, rows, D, residual, gate, weight):
     """On both sides of the lengths that a workgroup of 256, of 1024 lanes holds; more rows than workgroups."""
     base.test_norm_fwd_bwd(prism, (dt, rows, D), residual, gate, weight)
+
+
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+@pytest.mark.parametrize("step", [30.0, 3e3, 3e4, 1e6])
+def test_ssm_decay_after_a_reset(prism, dt, step):
+    """A token whose step wipes the state out: the log decays of its chunk pass 1e5, those between the tokens after it are
+    small and keep their digits."""
+    B, H, G, T, N, P = 1, 2, 1, 130, 32, 64
+    r, x, Bm, Cm, dt_, A, D, bias = scan_inputs(63, dt, B, H, G, T, N, P)
+    A.fill_(-16.0)
+    d = dt_.sigmoid() * 0.1
+    d[:, :, 3], d[:, :, 70] = step, step
+    x[:, :, 3], x[:, :, 70] = 0.0, 0.0
+    y, S = prism.ssm_fwd(x, Bm, Cm, d, A, D, softplus=False)
+    args = (x, Bm, Cm, d, A, D, None)
+    ref, ref_S = layer.ssm(*(None if t is None else f64(t) for t in args), False)
+    size, size_S = sizes(*args, False, None)
+    close("y", y, ref, size, dt)
+    close("S_final", S, ref_S, size_S, dt, "f32")
+    dy = r.vec(B, H, T, P)
+    g = prism.ssm_bwd(x, Bm, Cm, d, A, dy, D, softplus=False)
+    args = [None if t is None else f64(t) for t in (x, Bm, Cm, d, A, dy, D, None)]
+    ref, size = layer.ssm_grad(*args, False, None), layer.ssm_grad(*args, False, None, absolute=True)
+    for k in ("dx", "dB", "dC", "ddt", "dA", "dD"):
+        close(k, g[k], ref[k], size[k], dt, None if k in ("dx", "dB", "dC") else "f32")

@@ -188,8 +188,8 @@ prism_status ssm_plan(int B, int H, int G, int T, int N, int P, prism_dtype ty, 
     pl->part_ddt = ly.add(pl->nsl > 1 ? (size_t)pl->nsl * B * H : 0, (size_t)T * 4);
     pl->part_sum = ly.add(3 * bh, (size_t)pl->nch * 4);
     // the launches cover these with 32-bit grids
-    const size_t most = (size_t)UINT_MAX - 512;
-    if (rows * (N / 4) > most || (size_t)B * H * T > most || (size_t)pl->nch * 512 > most) return PRISM_ERR_UNSUPPORTED;
+    const size_t most = (size_t)UINT_MAX - 768 * (size_t)H - 1024;
+    if (rows * (N / 4) + (size_t)B * H * T > most || (size_t)pl->nch * 512 > most) return PRISM_ERR_UNSUPPORTED;
   }
   if (!ly.ok()) return PRISM_ERR_INVALID_ARG;
   pl->total = std::max<size_t>(ly.total, 256);

@@ -12,7 +12,7 @@
 // float32 accuracy after long decays.
 //
 // Products run on the float32 matrix instructions (153 TFLOP/s in a library product of 8192^3).  Measured: forward of
-// 3 x 6 x 509 tokens, N = P = 32: passes of 7, 3 and 11 us; backward of 2 x 6 x 333: 7, 3, 6, 17, 5 and 4 us.  Small
+// 3 x 6 x 509 tokens, N = P = 32: passes of 7, 3 and 11 us; backward of 2 x 6 x 333: 7, 3, 6, 17 and 4 us.  Small
 // calls: launches and one chunk's chain of products bound them.
 #pragma once
 #include "prism_ssm_args.h"
@@ -711,11 +711,41 @@ __global__ __launch_bounds__(256) void grad_kernel(SsmArgs a) {
   }
 }
 
-// dB, dC from the splits' shares, in split order.  One group of 4 values per thread.
+// What is left of the gradients once every chunk has its shares, in one launch: workgroups 0 .. 3 H - 1 form dA, dD, ddt_bias of
+// a head from the chunks' shares (in float64 and a fixed order); the next n_ddt ddt from the slices' shares (nsl > 1); the rest
+// dB, dC from the splits' shares in split order (nsplit > 1), a group of 4 values per thread.
 template <class T, int N>
-__global__ __launch_bounds__(256) void split_sum_kernel(SsmArgs a) {
+__global__ __launch_bounds__(256) void finish_kernel(SsmArgs a, unsigned n_ddt) {
+  __shared__ double part[256];
+  unsigned blk = blockIdx.x;
+  if (blk < 3u * a.H) {
+    const int h = blk / 3, which = blk % 3, HV = a.H * a.nsl;
+    float* out = which == 0 ? a.dA : which == 1 ? a.dD : a.ddt_bias;
+    if (out == nullptr) return;
+    const size_t per = (size_t)a.nsl * a.nch, n = (size_t)a.B * HV * a.nch;
+    double s = 0.0;
+    for (size_t k = threadIdx.x; k < a.B * per; k += 256)
+      s += (double)a.part_sum[which * n + (k / per * HV + (size_t)h * a.nsl) * a.nch + k % per];
+    part[threadIdx.x] = s;
+    __syncthreads();
+    for (int o = 128; o > 0; o >>= 1) {
+      if ((int)threadIdx.x < o) part[threadIdx.x] += part[threadIdx.x + o];
+      __syncthreads();
+    }
+    if (threadIdx.x == 0) out[h] = (float)part[0];
+    return;
+  }
+  blk -= 3u * a.H;
+  if (blk < n_ddt) {
+    const size_t n = (size_t)a.B * a.H * a.T, i = (size_t)blk * 256 + threadIdx.x;
+    if (i >= n) return;
+    float s = 0.f;
+    for (int k = 0; k < a.nsl; ++k) s += a.part_ddt[k * n + i];
+    a.ddt[i] = s;
+    return;
+  }
   typedef T out4 __attribute__((ext_vector_type(4)));
-  const size_t rows = (size_t)a.B * a.G * a.T, i = (size_t)blockIdx.x * 256 + threadIdx.x;
+  const size_t rows = (size_t)a.B * a.G * a.T, i = (size_t)(blk - n_ddt) * 256 + threadIdx.x;
   const size_t row = i / (N / 4);
   if (row >= rows) return;
   const int c = (int)(i % (N / 4)) * 4;
@@ -733,36 +763,6 @@ __global__ __launch_bounds__(256) void split_sum_kernel(SsmArgs a) {
   }
   *reinterpret_cast<out4*>(reinterpret_cast<T*>(a.dbm) + b * a.dbs.b + grp * a.dbs.h + (long long)t * a.dbs.t + c) = ob;
   *reinterpret_cast<out4*>(reinterpret_cast<T*>(a.dcm) + b * a.dcs.b + grp * a.dcs.h + (long long)t * a.dcs.t + c) = oc;
-}
-
-// ddt from the slices' shares (nsl > 1).
-template <class T>
-__global__ __launch_bounds__(256) void ddt_sum_kernel(SsmArgs a) {
-  const size_t n = (size_t)a.B * a.H * a.T, i = (size_t)blockIdx.x * 256 + threadIdx.x;
-  if (i >= n) return;
-  float s = 0.f;
-  for (int k = 0; k < a.nsl; ++k) s += a.part_ddt[k * n + i];
-  a.ddt[i] = s;
-}
-
-// dA, dD, ddt_bias of one head (grid (H, 3)) from the chunks' shares, in float64 and a fixed order.
-template <class T>
-__global__ __launch_bounds__(256) void head_sum_kernel(SsmArgs a) {
-  const int h = blockIdx.x, which = blockIdx.y, HV = a.H * a.nsl;
-  float* out = which == 0 ? a.dA : which == 1 ? a.dD : a.ddt_bias;
-  if (out == nullptr) return;
-  const size_t per = (size_t)a.nsl * a.nch, n = (size_t)a.B * HV * a.nch;
-  double s = 0.0;
-  for (size_t k = threadIdx.x; k < a.B * per; k += 256)
-    s += (double)a.part_sum[which * n + (k / per * HV + (size_t)h * a.nsl) * a.nch + k % per];
-  __shared__ double part[256];
-  part[threadIdx.x] = s;
-  __syncthreads();
-  for (int o = 128; o > 0; o >>= 1) {
-    if ((int)threadIdx.x < o) part[threadIdx.x] += part[threadIdx.x + o];
-    __syncthreads();
-  }
-  if (threadIdx.x == 0) out[h] = (float)part[0];
 }
 
 // One token: S' = e^{d A} S + d B x^T in place, y = S'^T C + D x.  Bound by reading and writing S: 83 us for 256 x 24

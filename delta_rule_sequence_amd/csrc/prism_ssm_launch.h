@@ -68,15 +68,10 @@ prism_status ssm_bwd_pw(const SsmArgs& a, hipStream_t stream) {
     ssm::state_kernel<T, N, PW, true><<<dim3(a.nseg, bh, 2), PW * 4, 0, stream>>>(a);
     ssm::grad_kernel<T, N, PW><<<dim3(a.nch, a.nsplit, a.B * a.G), 256, 0, stream>>>(a);
   }
-  if (a.nsplit > 1) {
-    const size_t n = (size_t)a.B * a.G * a.T * (N / 4);
-    ssm::split_sum_kernel<T, N><<<dim3((unsigned)((n + 255) / 256)), 256, 0, stream>>>(a);
-  }
-  if (a.nsl > 1) {
-    const size_t n = (size_t)a.B * a.H * a.T;
-    ssm::ddt_sum_kernel<T><<<dim3((unsigned)((n + 255) / 256)), 256, 0, stream>>>(a);
-  }
-  ssm::head_sum_kernel<T><<<dim3(a.H, 3), 256, 0, stream>>>(a);
+  const auto blocks = [](size_t n) { return (unsigned)((n + 255) / 256); };
+  const unsigned n_ddt = a.nsl > 1 ? blocks((size_t)a.B * a.H * a.T) : 0;
+  const unsigned n_split = a.nsplit > 1 ? blocks((size_t)a.B * a.G * a.T * (N / 4)) : 0;
+  ssm::finish_kernel<T, N><<<dim3(3 * a.H + n_ddt + n_split), 256, 0, stream>>>(a, n_ddt);
   return launched();
 }
 

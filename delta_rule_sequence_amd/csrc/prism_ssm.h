@@ -220,6 +220,7 @@ __global__ __launch_bounds__(PW * 4) void state_kernel(SsmArgs a) {
       float* st = a.st + (((size_t)rev * gridDim.y + bh) * a.nch + ch) * (N * PW);
 #pragma unroll
       for (int n = 0; n < NT; ++n) *reinterpret_cast<f32x4*>(st + tile_at<N>(pt, n)) = acc[n];
+      if (k + 1 == c1 - c0) break;  // nobody reads the state behind the segment
     }
     if (t0 >= len) continue;
     __syncthreads();
@@ -414,6 +415,7 @@ __global__ __launch_bounds__(PW * 4) void sweep_kernel(SsmArgs a) {
         *reinterpret_cast<out4*>(y) = o;
       }
     }
+    if ((ch + 1 == c1 || t0 + Q >= len) && seg != a.nseg - 1) break;  // nobody reads the state behind the segment
     const float dec = sc.dec;
 #pragma unroll
     for (int n = 0; n < NT; ++n) hs[n] *= dec;

@@ -304,7 +304,9 @@ __global__ __launch_bounds__((waves_per_head<PW, PTW>() * HP * 64), 2) void stat
 #pragma unroll
     for (int q = 0; q < HP; ++q) lv.load(sV[k & 1][q], pv[q] + (long long)t0 * tv, len - t0);
   };
-  if (steps > 0) load(0);
+  // saving, the last chunk only has its state saved
+  const int rows = SAVE ? steps - 1 : steps;
+  if (rows > 0) load(0);
   double log_dec = 0.0;
   for (int k = 0; k < steps; ++k) {
     const int ch = rev ? last - k : c0 + k, par = (k / NB) & 1;
@@ -312,7 +314,7 @@ __global__ __launch_bounds__((waves_per_head<PW, PTW>() * HP * 64), 2) void stat
 #pragma unroll
       for (int q = 0; q < NB; q += NW) {
         const int kk = k + q + wh;
-        if (kk < steps) {
+        if (kk < rows) {
           const Token tk = chunk_token(a, b, h, (rev ? last - kk : c0 + kk) * Q, len);
           log_dec += tk.tot;
           sWt[par][sub][q + wh][lane_id()] = rev ? tk.from_start() : tk.to_end() * tk.d;
@@ -338,7 +340,8 @@ __global__ __launch_bounds__((waves_per_head<PW, PTW>() * HP * 64), 2) void stat
           *reinterpret_cast<bf16x4*>(st + N * PW + plane_at<N, PW>(wh * PTW + p, n)) = lo;
         }
     }
-    if (k + 1 < steps) load(k + 1);
+    if (SAVE && k == rows) break;
+    if (k + 1 < rows) load(k + 1);
     const float dec = sDec[par][sub][k % NB];
 #pragma unroll
     for (int p = 0; p < PTW; ++p)
@@ -542,11 +545,15 @@ __global__ __launch_bounds__((waves_per_head<PW, PTW>() * HP * 64), 2) void swee
 #pragma unroll
       for (int p = 0; p < PTW; ++p) yt[p][tt] *= eo;
     }
-    const float dec = sc.dec;
+    // nobody reads the state behind a segment but the last
+    const bool go_on = k + 1 < steps || seg == a.nseg - 1;
+    if (go_on) {
+      const float dec = sc.dec;
 #pragma unroll
-    for (int p = 0; p < PTW; ++p)
+      for (int p = 0; p < PTW; ++p)
 #pragma unroll
-      for (int n = 0; n < NT; ++n) hs[p][n] *= dec;
+        for (int n = 0; n < NT; ++n) hs[p][n] *= dec;
+    }
 #pragma unroll
     for (int kb = 0; kb < 2; ++kb) {
       bf16x8 fx[PTW], f[PTW][3];
@@ -558,6 +565,7 @@ __global__ __launch_bounds__((waves_per_head<PW, PTW>() * HP * 64), 2) void swee
 #pragma unroll
         for (int p = 0; p < PTW; ++p) yt[p][tt] = mfma(fx[p], fm, yt[p][tt]);
       }
+      if (!go_on) continue;
 #pragma unroll
       for (int p = 0; p < PTW; ++p) weighted(f[p], fx[p], 32 * kb, sc.w);
       bf16x8 fb[NT];

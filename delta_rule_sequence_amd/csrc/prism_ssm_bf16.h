@@ -15,7 +15,7 @@
 // transposing reads both touch all banks evenly.
 //
 // Measured, N = 128, P = 64: forward of 8 x 24 x 2048 ragged tokens 31 us for the segments' ends and 52 for the sweep;
-// backward of 8 x 12 x 2048: 35 us for the ends, 56 saving states, 96 for the gradients.  N = P = 64, 2 x 4 x 16384: 13
+// backward of 8 x 12 x 2048: 35 us for the ends, 56 saving states, 94 for the gradients.  N = P = 64, 2 x 4 x 16384: 13
 // and 18 us, and 8 for the scan over 128 segments.  Two waves per SIMD at most (state tiles, operands and scores take all 256 registers), so the sweep is bound by
 // latency: its matrix unit is busy 11 % of the time, vector instructions 21 %, LDS 18 %.  Saving writes 201 MB at
 // 3.6 TB/s, and the gradients read them again.
@@ -693,6 +693,15 @@ __global__ __launch_bounds__(512, 2) void grad_kernel(SsmArgs a) {
   }
 #pragma unroll
   for (int t = 0; t < TTW; ++t) dc[t] = db[t] = zero4();
+  // the scalars of NB heads from v on, by the last NB waves
+  const auto scalars = [&](int v) {
+    const int k = w - (WV - NB), par = ((v - v0) / NB) & 1;
+    if (k < 0 || v + k >= v1) return;
+    const Token tk = chunk_token(a, b, (grp * per_group + v + k) / a.nsl, t0, a.T);
+    put_scalars<false>(tk, scals[par][k]);
+    sSig[par][k][l] = tk.dz;
+  };
+  scalars(v0);
   for (int v = v0; v < v1; ++v) {
     const int hv = grp * per_group + v, h = hv / a.nsl, sl = hv % a.nsl, p0 = sl * PW, hb = (v - v0) % NB;
     const size_t bh = (size_t)b * HV + hv;
@@ -700,11 +709,6 @@ __global__ __launch_bounds__(512, 2) void grad_kernel(SsmArgs a) {
     const Scal& sc = scals[par][hb];
     const bf16_t *sX = sXs[(v - v0) & 1], *sY = sYs[(v - v0) & 1];
     const float Dh = a.D != nullptr ? a.D[h] : 0.f;
-    if (hb == 0 && w < NB && v + w < v1) {  // the next NB heads' scalars; the other half may still be read
-      const Token tk = chunk_token(a, b, (grp * per_group + v + w) / a.nsl, t0, a.T);
-      put_scalars<false>(tk, scals[par][w]);
-      sSig[par][w][l] = tk.dz;
-    }
     __syncthreads();  // every wave has its rows of this head (waited for below), the last head's reads are over
     if (v + 1 < v1) load(v + 1);
     // scores: rows s, columns t
@@ -837,7 +841,10 @@ __global__ __launch_bounds__(512, 2) void grad_kernel(SsmArgs a) {
           *reinterpret_cast<bf16x4*>((bf16_t*)a.dx + b * a.dxs.b + h * a.dxs.h + (long long)(t0 + s) * a.dxs.t + p0 + 16 * pw + 4 * g) = o;
       }
     }
-    if (w == ((v - v0) & (WV - 1))) {  // the head's scalars, the waves in turn
+    // The later waves have less to do for dx: they form what is left of this head, and the next heads' scalars in the half
+    // that the last heads' reads have left (in front of the first barrier, by the first waves: 98 us where this takes 94).
+    if (hb == NB - 1) scalars(v + 1);
+    if (w == WV / 2 + hb) {
       const int t = l, tt = t >> 4;
       float row = 0.f, qoff = 0.f, I = 0.f, J0 = 0.f;
 #pragma unroll

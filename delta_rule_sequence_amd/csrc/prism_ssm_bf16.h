@@ -16,9 +16,9 @@
 //
 // Measured, N = 128, P = 64: forward of 8 x 24 x 2048 ragged tokens 31 us for the segments' ends and 52 for the sweep;
 // backward of 8 x 12 x 2048: 35 us for the ends, 56 saving states, 94 for the gradients.  N = P = 64, 2 x 4 x 16384: 13
-// and 18 us, and 8 for the scan over 128 segments.  Two waves per SIMD at most (state tiles, operands and scores take all 256 registers), so the sweep is bound by
-// latency: its matrix unit is busy 11 % of the time, vector instructions 21 %, LDS 18 %.  Saving writes 201 MB at
-// 3.6 TB/s, and the gradients read them again.
+// and 18 us, and 8 for the scan over 128 segments.  Two waves per SIMD at most (state tiles, operands and scores take
+// all 256 registers), so the sweep is bound by latency: its matrix unit is busy 11 % of the time, vector instructions
+// 22 %, LDS 18 %.  Saving writes 201 MB at 3.6 TB/s, and the gradients read them again.
 #pragma once
 #include "prism_ssm.h"
 

@@ -7,7 +7,8 @@
 //     so states keep float32 accuracy over any length (three MFMAs in place of one);
 //   * the score matrix M, the state as it is read out into y, the summed score gradients and R in dx are rounded to
 //     bfloat16 once: each is one rounding of 2^-9 on average in a result that is itself rounded to bfloat16;
-//   * ddt and dA are float32 results: H and R enter the products behind them as two parts (16 bits).
+//   * ddt and dA are float32 results: H and R enter the products behind them as three parts, and <H, R> in float32 (two parts:
+//     7 us less at 8 x 12 x 2048, but dA off by up to 1e-5 of its size where its terms cancel).
 //
 // Waves own 16 columns p of the state in MFMA accumulators from chunk to chunk; an accumulator tile is the operand of
 // the readout without passing LDS (rows of a tile pair are the k values of one MFMA, in the order of Mma::koff).
@@ -15,10 +16,10 @@
 // transposing reads both touch all banks evenly.
 //
 // Measured, N = 128, P = 64: forward of 8 x 24 x 2048 ragged tokens 31 us for the segments' ends and 52 for the sweep;
-// backward of 8 x 12 x 2048: 35 us for the ends, 56 saving states, 94 for the gradients.  N = P = 64, 2 x 4 x 16384: 13
+// backward of 8 x 12 x 2048: 35 us for the ends, 52 saving states, 100 for the gradients.  N = P = 64, 2 x 4 x 16384: 13
 // and 18 us, and 8 for the scan over 128 segments.  Two waves per SIMD at most (state tiles, operands and scores take
 // all 256 registers), so the sweep is bound by latency: its matrix unit is busy 11 % of the time, vector instructions
-// 22 %, LDS 18 %.  Saving writes 201 MB at 3.6 TB/s, and the gradients read them again.
+// 22 %, LDS 18 %.  Saving writes 201 MB at 3.9 TB/s, and the gradients read them again.
 #pragma once
 #include "prism_ssm.h"
 
@@ -157,9 +158,9 @@ __device__ __forceinline__ void weighted(bf16x8 (&p)[3], const bf16x8& f, int k0
 }
 
 // Piece of a saved state: tile (pt, nt) of H^T, 4 values p = 16 pt + 4 g + r of column n = 16 nt + i per lane, for the
-// products that contract over p.  Two planes (parts) of N * PW bfloat16 each.
+// products that contract over p.
 template <int N, int PW>
-__device__ __forceinline__ size_t plane_at(int pt, int nt) {
+__device__ __forceinline__ size_t saved_at(int pt, int nt) {
   return ((size_t)nt * (PW / 16) + pt) * 256 + lane_id() * 4;
 }
 
@@ -246,7 +247,7 @@ template <int PW, int PTW> constexpr int waves_per_head() { return PW / 16 / PTW
 // States of a segment, as ssm::state_kernel, for HP virtual heads of a group at once (they share the rows of B or C).
 // A wave owns PTW tiles of 16 columns of one head.  SAVE = false: from zero, the end state to seg (H: rows n, columns p, as
 // the sweep keeps it; or, for the backward, transposed); the segment whose end nobody reads is left out.  SAVE = true:
-// from the entering state, saving the state in front of every chunk in two planes.  The next chunk's rows arrive in the
+// from the entering state, saving the state in front of every chunk.  The next chunk's rows arrive in the
 // second half of the tiles meanwhile.
 template <int N, int PW, int PTW, int HP, bool TRANS, bool SAVE>
 __global__ __launch_bounds__((waves_per_head<PW, PTW>() * HP * 64), 2) void state_kernel(SsmArgs a) {
@@ -325,20 +326,11 @@ __global__ __launch_bounds__((waves_per_head<PW, PTW>() * HP * 64), 2) void stat
     loads_done();
     __syncthreads();  // this chunk's rows are there, the other half's reads are over
     if constexpr (SAVE) {
-      bf16_t* st = reinterpret_cast<bf16_t*>(a.st) + (((size_t)rev * a.B * HV + bh) * a.nch + ch) * (2 * N * PW);
+      float* st = a.st + (((size_t)rev * a.B * HV + bh) * a.nch + ch) * (N * PW);
 #pragma unroll
       for (int p = 0; p < PTW; ++p)
 #pragma unroll
-        for (int n = 0; n < NT; ++n) {
-          bf16x4 hi, lo;
-#pragma unroll
-          for (int r = 0; r < 4; ++r) {
-            hi[r] = (bf16_t)acc[p][n][r];
-            lo[r] = (bf16_t)(acc[p][n][r] - (float)hi[r]);
-          }
-          *reinterpret_cast<bf16x4*>(st + plane_at<N, PW>(wh * PTW + p, n)) = hi;
-          *reinterpret_cast<bf16x4*>(st + N * PW + plane_at<N, PW>(wh * PTW + p, n)) = lo;
-        }
+        for (int n = 0; n < NT; ++n) *reinterpret_cast<f32x4*>(st + saved_at<N, PW>(wh * PTW + p, n)) = acc[p][n];
     }
     if (SAVE && k == rows) break;
     if (k + 1 < rows) load(k + 1);
@@ -592,15 +584,19 @@ __global__ __launch_bounds__((waves_per_head<PW, PTW>() * HP * 64), 2) void swee
   }
 }
 
-// <p, q> over 8 pairs of bfloat16, added to v in float32.
-__device__ __forceinline__ float dot8(const bf16x8& p, const bf16x8& q, float v) {
-#ifdef __HIP_DEVICE_COMPILE__  // the host pass does not know the builtin
-  v = __builtin_amdgcn_fdot2_f32_bf16(__builtin_shufflevector(p, p, 0, 1), __builtin_shufflevector(q, q, 0, 1), v, false);
-  v = __builtin_amdgcn_fdot2_f32_bf16(__builtin_shufflevector(p, p, 2, 3), __builtin_shufflevector(q, q, 2, 3), v, false);
-  v = __builtin_amdgcn_fdot2_f32_bf16(__builtin_shufflevector(p, p, 4, 5), __builtin_shufflevector(q, q, 4, 5), v, false);
-  v = __builtin_amdgcn_fdot2_f32_bf16(__builtin_shufflevector(p, p, 6, 7), __builtin_shufflevector(q, q, 6, 7), v, false);
-#endif
-  return v;
+// 8 values in three parts, each rounded to nearest: together they hold the values' float32 digits.
+__device__ __forceinline__ void round3(const f32x4& a, const f32x4& b, bf16x8 (&p)[3]) {
+  f32x4 c = a, d = b;
+#pragma unroll
+  for (int q = 0; q < 3; ++q) {
+    p[q] = round8(c, d);
+    if (q == 2) break;
+#pragma unroll
+    for (int r = 0; r < 4; ++r) {
+      c[r] -= (float)p[q][r];
+      d[r] -= (float)p[q][4 + r];
+    }
+  }
 }
 
 // Gradients of one chunk for one group, as ssm::grad_kernel (the same grid, formulas and sums).  The eight waves share
@@ -654,27 +650,18 @@ __global__ __launch_bounds__(512, 2) void grad_kernel(SsmArgs a) {
     ly.load(sYs[buf], (const bf16_t*)a.dy + b * a.dys.b + h * a.dys.h + p0 + (long long)t0 * a.dys.t, a.T - t0);
   };
   load(v0);
-  // this wave's parts of the states: index n, k = p.  Loaded a head ahead: in flight over dx and the next head's scores.
-  bf16x8 fh[2][KP], fr[2][KP];
+  // this wave's parts of the states: index n, k = p (zeros in the empty half of P = 16).  Loaded a head ahead: in flight over
+  // dx and the next head's scores.
+  f32x4 hv4[2 * KP], rv4[2 * KP];
   const auto load_states = [&](int v) {
     const size_t bh = (size_t)b * HV + grp * per_group + v;
-    const bf16_t* H = reinterpret_cast<const bf16_t*>(a.st) + (bh * a.nch + ch) * (2 * N * PW);
-    const bf16_t* R = reinterpret_cast<const bf16_t*>(a.st) + (((size_t)a.B * HV + bh) * a.nch + ch) * (2 * N * PW);
+    const float* H = a.st + (bh * a.nch + ch) * (N * PW);
+    const float* R = a.st + (((size_t)a.B * HV + bh) * a.nch + ch) * (N * PW);
 #pragma unroll
-    for (int q = 0; q < 2; ++q)
-#pragma unroll
-      for (int p = 0; p < KP; ++p) {
-        const bf16_t *ph = H + q * (N * PW), *pr = R + q * (N * PW);
-        bf16x4 h1 = {0, 0, 0, 0}, r1 = {0, 0, 0, 0};
-        const bf16x4 h0 = *reinterpret_cast<const bf16x4*>(ph + plane_at<N, PW>(2 * p, nt));
-        const bf16x4 r0 = *reinterpret_cast<const bf16x4*>(pr + plane_at<N, PW>(2 * p, nt));
-        if constexpr (PW >= 32) {
-          h1 = *reinterpret_cast<const bf16x4*>(ph + plane_at<N, PW>(2 * p + 1, nt));
-          r1 = *reinterpret_cast<const bf16x4*>(pr + plane_at<N, PW>(2 * p + 1, nt));
-        }
-        fh[q][p] = __builtin_shufflevector(h0, h1, 0, 1, 2, 3, 4, 5, 6, 7);
-        fr[q][p] = __builtin_shufflevector(r0, r1, 0, 1, 2, 3, 4, 5, 6, 7);
-      }
+    for (int p = 0; p < 2 * KP; ++p) {
+      hv4[p] = p < PT ? *reinterpret_cast<const f32x4*>(H + saved_at<N, PW>(p < PT ? p : 0, nt)) : zero4();
+      rv4[p] = p < PT ? *reinterpret_cast<const f32x4*>(R + saved_at<N, PW>(p < PT ? p : 0, nt)) : zero4();
+    }
   };
   loads_done();
   load_states(v0);
@@ -753,33 +740,32 @@ __global__ __launch_bounds__(512, 2) void grad_kernel(SsmArgs a) {
     // products with the states: rows n, columns token
     float K = 0.f;
     if (has_n) {
-      if (tt0 == 0) {
-#pragma unroll
-        for (int p = 0; p < KP; ++p) {
-          K = dot8(fh[0][p], fr[0][p], K);
-          K = dot8(fh[0][p], fr[1][p], K);
-          K = dot8(fh[1][p], fr[0][p], K);
-          // R's leading part as rows n for dx
-          const bf16x8 f = fr[0][p];
-          *reinterpret_cast<bf16x4*>(sR + Tile<PW>::at(16 * nt + i, 32 * p + 4 * g)) = __builtin_shufflevector(f, f, 0, 1, 2, 3);
-          if constexpr (PW >= 32)
-            *reinterpret_cast<bf16x4*>(sR + Tile<PW>::at(16 * nt + i, 32 * p + 16 + 4 * g)) = __builtin_shufflevector(f, f, 4, 5, 6, 7);
-        }
-      }
       f32x4 uc[TTW], ub[TTW];
 #pragma unroll
       for (int k = 0; k < TTW; ++k) uc[k] = ub[k] = zero4();
 #pragma unroll
-      for (int p = 0; p < KP; ++p)
+      for (int p = 0; p < KP; ++p) {
+        bf16x8 fh[3], fr[3];
+        round3(hv4[2 * p], hv4[2 * p + 1], fh);
+        round3(rv4[2 * p], rv4[2 * p + 1], fr);
+        if (tt0 == 0) {
+#pragma unroll
+          for (int r = 0; r < 4; ++r) K += hv4[2 * p][r] * rv4[2 * p][r] + hv4[2 * p + 1][r] * rv4[2 * p + 1][r];
+          // R's leading part as rows n for dx
+          *reinterpret_cast<bf16x4*>(sR + Tile<PW>::at(16 * nt + i, 32 * p + 4 * g)) = __builtin_shufflevector(fr[0], fr[0], 0, 1, 2, 3);
+          if constexpr (PW >= 32)
+            *reinterpret_cast<bf16x4*>(sR + Tile<PW>::at(16 * nt + i, 32 * p + 16 + 4 * g)) = __builtin_shufflevector(fr[0], fr[0], 4, 5, 6, 7);
+        }
 #pragma unroll
         for (int k = 0; k < TTW; ++k) {
           const bf16x8 by = frag_o<PW>(sY, 16 * (tt0 + k), 32 * p), bx = frag_o<PW>(sX, 16 * (tt0 + k), 32 * p);
 #pragma unroll
-          for (int q = 1; q >= 0; --q) {
-            uc[k] = mfma(fh[q][p], by, uc[k]);
-            ub[k] = mfma(fr[q][p], bx, ub[k]);
+          for (int q = 2; q >= 0; --q) {
+            uc[k] = mfma(fh[q], by, uc[k]);
+            ub[k] = mfma(fr[q], bx, ub[k]);
           }
         }
+      }
 #pragma unroll
       for (int k = 0; k < TTW; ++k) {
         const int t = 16 * (tt0 + k) + i;
@@ -842,7 +828,7 @@ __global__ __launch_bounds__(512, 2) void grad_kernel(SsmArgs a) {
       }
     }
     // The later waves have less to do for dx: they form what is left of this head, and the next heads' scalars in the half
-    // that the last heads' reads have left (in front of the first barrier, by the first waves: 98 us where this takes 94).
+    // that the last heads' reads have left (in front of the first barrier, by the first waves: 4 us more).
     if (hb == NB - 1) scalars(v + 1);
     if (w == WV / 2 + hb) {
       const int t = l, tt = t >> 4;

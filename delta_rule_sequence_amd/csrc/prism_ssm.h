@@ -81,6 +81,22 @@ __device__ __forceinline__ float sum_groups(float v) {  // over the four 16-lane
   return v;
 }
 
+// The same sums in float64, for terms whose row and column sums cancel each other.
+template <int CTRL>
+__device__ __forceinline__ double ror_add(double v) {
+  const unsigned long long u = __builtin_bit_cast(unsigned long long, v);
+  const unsigned lo = __builtin_amdgcn_update_dpp(0, (int)(unsigned)u, CTRL, 0xf, 0xf, false);
+  const unsigned hi = __builtin_amdgcn_update_dpp(0, (int)(unsigned)(u >> 32), CTRL, 0xf, 0xf, false);
+  return v + __builtin_bit_cast(double, (unsigned long long)hi << 32 | lo);
+}
+__device__ __forceinline__ double sum_lanes16(double v) {
+  return ror_add<0x121>(ror_add<0x122>(ror_add<0x124>(ror_add<0x128>(v))));
+}
+__device__ __forceinline__ double sum_groups(double v) {
+  v += __shfl_xor(v, 16, 64);
+  return v + __shfl_xor(v, 32, 64);
+}
+
 // Whether a token of log decay l lets nothing of the state through: its gradient e^l <S, R> is 0 in float32, where the
 // sums that cancel to it would leave their roundings (times a large step, in dA).
 __device__ __forceinline__ bool closed(float l) { return l < -105.f; }
@@ -457,7 +473,8 @@ __global__ __launch_bounds__(256) void grad_kernel(SsmArgs a) {
   __shared__ float sY[Q * LDP];  // dy
   __shared__ float sM[Q * LDQ];  // M[t][s]
   __shared__ Scal sc;
-  __shared__ float sSig[Q], sRow[Q], sI[Q], sJ[Q], sDiag[Q], sCol[4][Q], sK[4], sDD[4];
+  __shared__ float sSig[Q], sI[Q], sJ[Q], sDiag[Q], sCol[4][Q], sK[4], sDD[4];
+  __shared__ double sRow[Q], sColZ[4][Q];  // sums of q_ts d_s, s < t, over s and over t
   const int ch = blockIdx.x, bg = blockIdx.z, b = bg / a.G, grp = bg % a.G, t0 = ch * Q;
   const int w = wave_id(), tid = threadIdx.x, l = lane_id(), g = l >> 4, i = l & 15;
   const int HV = a.H * a.nsl, per_group = HV / a.G;
@@ -495,7 +512,7 @@ __global__ __launch_bounds__(256) void grad_kernel(SsmArgs a) {
       sSig[tid] = tk.dz;
     }
     __syncthreads();
-    float row = 0.f;
+    double row = 0.0;
     f32x4 dms[4];
 #pragma unroll
     for (int ts = 0; ts < 4; ++ts) dms[ts] = zero4();
@@ -511,7 +528,7 @@ __global__ __launch_bounds__(256) void grad_kernel(SsmArgs a) {
     }
 #pragma unroll
     for (int ts = 0; ts < 4; ++ts) {
-      f32x4 col = zero4();
+      f32x4 col = zero4(), colz = zero4();
       if (ts <= w) {
         f32x4 m;
         const f32x4 dm = dms[ts];
@@ -523,8 +540,9 @@ __global__ __launch_bounds__(256) void grad_kernel(SsmArgs a) {
           dg[ts][r] += s <= tok ? dm[r] * e * sc.d[s] : 0.f;
           const float q = s <= tok ? gm[ts][r] * e * dm[r] : 0.f;
           if (s < tok) {
-            row += q * sc.d[s];
             col[r] = q;
+            colz[r] = q * sc.d[s];
+            row += (double)colz[r];
           }
           if (s == tok) sDiag[s] = q;
         }
@@ -532,8 +550,12 @@ __global__ __launch_bounds__(256) void grad_kernel(SsmArgs a) {
       }
 #pragma unroll
       for (int r = 0; r < 4; ++r) {
-        const float c = sum_lanes16(col[r]);
-        if (i == 0) sCol[w][16 * ts + 4 * g + r] = c;
+        const float cz = colz[r], c = sum_lanes16(col[r]);
+        const double z = sum_lanes16((double)cz);
+        if (i == 0) {
+          sCol[w][16 * ts + 4 * g + r] = c;
+          sColZ[w][16 * ts + 4 * g + r] = z;
+        }
       }
     }
     row = sum_groups(row);
@@ -639,11 +661,16 @@ __global__ __launch_bounds__(256) void grad_kernel(SsmArgs a) {
     if (tid < 64) {
       const int t = tid;
       float qoff = 0.f;
+      double zoff = 0.0;
 #pragma unroll
-      for (int k = 0; k < 4; ++k) qoff += (t >> 4) <= k ? sCol[k][t] : 0.f;
+      for (int k = 0; k < 4; ++k) {
+        qoff += (t >> 4) <= k ? sCol[k][t] : 0.f;
+        zoff += (t >> 4) <= k ? sColZ[k][t] : 0.0;
+      }
       const float d = sc.d[t], J0 = sJ[t], Ah = a.A[h];
       const double jd = (double)d * J0;
-      const double f = (double)sRow[t] - (double)d * qoff + sI[t];
+      // rows and columns of the same terms in float64: those between two tokens after t cancel in the suffix sum
+      const double f = sRow[t] - zoff + sI[t];
       const double fs = wave_scan(f), ftot = last_lane(fs);  // suffix sum from t: ftot - fs + f
       const double js = wave_scan(jd);                       // prefix sum before t: js - jd
       const float kk = sc.dec * ((sK[0] + sK[1]) + (sK[2] + sK[3]));

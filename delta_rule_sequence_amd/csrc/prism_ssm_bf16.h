@@ -8,7 +8,8 @@
 //   * the score matrix M, the state as it is read out into y, the summed score gradients and R in dx are rounded to
 //     bfloat16 once: each is one rounding of 2^-9 on average in a result that is itself rounded to bfloat16;
 //   * ddt and dA are float32 results: H and R enter the products behind them as three parts, and <H, R> in float32 (two parts:
-//     7 us less at 8 x 12 x 2048, but dA off by up to 1e-5 of its size where its terms cancel).
+//     7 us less at 8 x 12 x 2048, but ddt off by 1e-6 for 2e-7); the sums of score terms that cancel in dA run in float64 (10
+//     us, for dA off by 4e-6 at most over 40 draws of two heads where float32 sums leave 3e-5).
 //
 // Waves own 16 columns p of the state in MFMA accumulators from chunk to chunk; an accumulator tile is the operand of
 // the readout without passing LDS (rows of a tile pair are the k values of one MFMA, in the order of Mma::koff).
@@ -16,7 +17,7 @@
 // transposing reads both touch all banks evenly.
 //
 // Measured, N = 128, P = 64: forward of 8 x 24 x 2048 ragged tokens 31 us for the segments' ends and 52 for the sweep;
-// backward of 8 x 12 x 2048: 35 us for the ends, 52 saving states, 100 for the gradients.  N = P = 64, 2 x 4 x 16384: 13
+// backward of 8 x 12 x 2048: 35 us for the ends, 52 saving states, 110 for the gradients.  N = P = 64, 2 x 4 x 16384: 13
 // and 18 us, and 8 for the scan over 128 segments.  Two waves per SIMD at most (state tiles, operands and scores take
 // all 256 registers), so the sweep is bound by latency: its matrix unit is busy 11 % of the time, vector instructions
 // 22 %, LDS 18 %.  Saving writes 201 MB at 3.9 TB/s, and the gradients read them again.
@@ -620,7 +621,8 @@ __global__ __launch_bounds__(512, 2) void grad_kernel(SsmArgs a) {
   __shared__ __attribute__((aligned(16))) bf16_t sM[Q * Q];   // [t][s]
   __shared__ __attribute__((aligned(16))) bf16_t sR[N < 32 ? 32 * PW : N * PW];  // [n][p]
   __shared__ Scal scals[2][NB];
-  __shared__ float sSig[2][NB][Q], sRow[10][16], sCol[10][16], sDiag[Q], sXY[Q], sI[NT][Q], sJ[NT][Q], sK[WV];
+  __shared__ double sRow[10][16], sColZ[10][16];  // sums of q_ts d_s, s < t, over s and over t
+  __shared__ float sSig[2][NB][Q], sCol[10][16], sDiag[Q], sXY[Q], sI[NT][Q], sJ[NT][Q], sK[WV];
   const int ch = blockIdx.x, bg = blockIdx.z, b = bg / a.G, grp = bg % a.G, t0 = ch * Q;
   const int w = __builtin_amdgcn_readfirstlane(wave_id()), tid = threadIdx.x, l = lane_id(), g = l >> 4, i = l & 15;
   const int HV = a.H * a.nsl, per_group = HV / a.G;
@@ -709,7 +711,8 @@ __global__ __launch_bounds__(512, 2) void grad_kernel(SsmArgs a) {
       const float cht = sc.ch[t], clt = sc.cl[t];
       const f32x4 chs = *reinterpret_cast<const f32x4*>(sc.ch + s0), cls = *reinterpret_cast<const f32x4*>(sc.cl + s0);
       const f32x4 ds = *reinterpret_cast<const f32x4*>(sc.d + s0);
-      float row = 0.f;
+      double row = 0.0;
+      f32x4 colz;
       bf16x4 m;
 #pragma unroll
       for (int r = 0; r < 4; ++r) {
@@ -727,7 +730,9 @@ __global__ __launch_bounds__(512, 2) void grad_kernel(SsmArgs a) {
         }
         m[r] = (bf16_t)mm;
         dg[k][r] += dd;
-        row += off * ds[r];
+        const float z = off * ds[r];
+        row += (double)z;
+        colz[r] = z;
         col[r] = off;
       }
       *reinterpret_cast<bf16x4*>(sM + Tile<Q>::at(t, s0)) = m;
@@ -736,6 +741,12 @@ __global__ __launch_bounds__(512, 2) void grad_kernel(SsmArgs a) {
 #pragma unroll
       for (int r = 0; r < 4; ++r) col[r] = sum_lanes16(col[r]);
       if (i == 0) *reinterpret_cast<f32x4*>(&sCol[w + WV * k][4 * g]) = col;
+#pragma unroll
+      for (int r = 0; r < 4; ++r) {
+        const float cz = colz[r];
+        const double z = sum_lanes16((double)cz);
+        if (i == 0) sColZ[w + WV * k][4 * g + r] = z;
+      }
     }
     // products with the states: rows n, columns token
     float K = 0.f;
@@ -832,11 +843,12 @@ __global__ __launch_bounds__(512, 2) void grad_kernel(SsmArgs a) {
     if (hb == NB - 1) scalars(v + 1);
     if (w == WV / 2 + hb) {
       const int t = l, tt = t >> 4;
-      float row = 0.f, qoff = 0.f, I = 0.f, J0 = 0.f;
+      float qoff = 0.f, I = 0.f, J0 = 0.f;
+      double row = 0.0, zoff = 0.0;
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
         if (k <= tt) row += sRow[tt * (tt + 1) / 2 + k][t & 15];
-        if (k >= tt) qoff += sCol[k * (k + 1) / 2 + tt][t & 15];
+        if (k >= tt) qoff += sCol[k * (k + 1) / 2 + tt][t & 15], zoff += sColZ[k * (k + 1) / 2 + tt][t & 15];
       }
 #pragma unroll
       for (int k = 0; k < NT; ++k) {
@@ -848,7 +860,8 @@ __global__ __launch_bounds__(512, 2) void grad_kernel(SsmArgs a) {
       for (int k = 0; k < WV; ++k) kk += sK[k];
       const float d = sc.d[t], Ah = a.A[h];
       const double jd = (double)d * J0;
-      const double f = (double)row - (double)d * qoff + I;
+      // rows and columns of the same terms in float64: those between two tokens after t cancel in the suffix sum
+      const double f = row - zoff + I;
       const double fs = wave_scan(f), ftot = last_lane(fs);  // suffix sum from t: ftot - fs + f
       const double js = wave_scan(jd);                       // prefix sum before t: js - jd
       const float dl = closed(d * Ah) ? 0.f : (float)((ftot - fs + f) + (js - jd) + (double)(sc.dec * kk));

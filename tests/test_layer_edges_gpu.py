@@ -291,3 +291,24 @@ def test_ssm_decay_after_a_reset(prism, dt, step):
     ref, size = layer.ssm_grad(*args, False, None), layer.ssm_grad(*args, False, None, absolute=True)
     for k in ("dx", "dB", "dC", "ddt", "dA", "dD"):
         close(k, g[k], ref[k], size[k], dt, None if k in ("dx", "dB", "dC") else "f32")
+
+
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+def test_ssm_decay_gradient_has_independent_errors(prism, dt):
+    """dA sums a term per token that cancels to a hundredth of itself.  A token's ddt is off by a few half steps, 2^-22 of
+    their usual size; if those errors are independent, their sum over the tokens, d_t / A each, stays below 4 of its
+    standard deviations (what a chunk's tokens share would add up 64 times)."""
+    import torch
+    worst = 0.0
+    for seed in range(12):
+        r = Rng(70 + seed, dt)
+        B, H, G, T, N, P = 5, 2, 1, 343, 64, 32
+        x, Bm, Cm, dy = r.vec(B, H, T, P), r.vec(B, G, T, N), r.vec(B, G, T, N), r.vec(B, H, T, P)
+        d, A = torch.exp(0.4 * r.flt(B, H, T)) * 0.05, -r.flt(H, lo=1.0, hi=16.0)
+        g = prism.ssm_bwd(x, Bm, Cm, d, A, dy, softplus=False)
+        ref = layer.ssm_grad(f64(x), f64(Bm), f64(Cm), f64(d), f64(A), f64(dy), None, None, False)
+        usual = np.sqrt((ref["ddt"] ** 2).mean((0, 2)))
+        lim = 4 * 2.0 ** -22 * usual * np.sqrt((f64(d) ** 2).sum((0, 2))) / np.abs(f64(A))
+        worst = max(worst, float(np.max(np.abs(f64(g["dA"]) - ref["dA"]) / lim)))
+    print(f"  dA: worst {worst:.3f} of its tolerance", flush=True)
+    assert worst <= 1.0

@@ -105,7 +105,7 @@ __global__ __launch_bounds__(256) void fwd_kernel(ConvArgs a) {
   const int strip = blockIdx.y * 4 + __builtin_amdgcn_readfirstlane(threadIdx.x / 64);  // one strip per wave
   const int bh = blockIdx.z, b = bh / a.H, h = bh % a.H;
   if (first >= a.D || strip >= a.nstrip) return;
-  const int len = seq_len(a, b), t0 = strip * a.strip, t1 = min(t0 + a.strip, len);
+  const int len = seq_len(a, b), t0 = strip * a.strip, t1 = t0 + min(a.strip, len - t0);  // the last strip may end past 2^31
   if (t0 < t1) {
     float w[K][V], bias[V], x[K][V];
     load_filter<K, V>(w, bias, a, h, d);
@@ -165,7 +165,7 @@ __global__ __launch_bounds__(256) void bwd_kernel(ConvArgs a) {
 #pragma unroll
     for (int k = 0; k < V; ++k) dw[j][k] = 0.f;
   if (first < a.D && strip < a.nstrip) {
-    const int t0 = strip * a.strip, t1 = min(t0 + a.strip, a.T), te = t1 + K - 1;
+    const int t0 = strip * a.strip, t1 = t0 + min(a.strip, a.T - t0), te = t1 + K - 1;
     float w[K][V], bias[V], x[K][V], g[K][V];
     load_filter<K, V>(w, bias, a, h, d);
 #pragma unroll

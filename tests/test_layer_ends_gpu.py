@@ -1,0 +1,45 @@
+"""The ends of the state space layer's ranges on the GPU: the longest sequences, the last token."""
+import pytest
+
+from tests.conftest import gpu_available
+from tests.test_layer_gpu import Rng
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module")
+def prism():
+    if not gpu_available():
+        pytest.skip("no GPU")
+    import delta_rule_sequence_amd as m
+    m.load_library()
+    return m
+
+
+LONGEST = 2 ** 31 - 1 - 4096  # tokens that the convolution accepts
+
+
+def test_conv_longest_sequence(prism):
+    """The last rows of the longest sequence that is accepted, and of one whose last strip of tokens ends at 2^31, are what a
+    call on the end of the sequence gives; the filter's gradient has their share."""
+    import torch
+    K, tail = 4, 40000
+    r = Rng(80, "bf16")
+    for T in (LONGEST, 2 ** 31 - 16384 + 5):
+        x, y = torch.zeros(1, 1, T, 1, dtype=torch.bfloat16, device="cuda"), torch.full((1, 1, T, 1), 7.0, dtype=torch.bfloat16, device="cuda")
+        x[:, :, -tail:] = r.vec(1, 1, tail, 1)
+        w = r.flt(1, K, 1)
+        print(f"  T = {T}, forward", flush=True)
+        _, end = prism.conv_fwd(x, w, out=y)
+        ref, ref_end = prism.conv_fwd(x[:, :, -tail:].clone(), w)
+        assert torch.equal(y[:, :, -tail:], ref) and torch.equal(end, ref_end)
+        dy = torch.zeros_like(x)
+        dy[:, :, -tail + K:] = r.vec(1, 1, tail - K, 1)
+        y.fill_(7.0)
+        print(f"  T = {T}, backward", flush=True)
+        g = prism.conv_bwd(x, w, dy, out=y)
+        small = prism.conv_bwd(x[:, :, -tail:].clone(), w, dy[:, :, -tail:].clone())
+        assert torch.equal(g["dx"][:, :, -tail:], small["dx"]) and bool((g["dx"][:, :, :-tail] == 0).all())
+        # the same products, summed in float32 over strips of other lengths: 2e-5 of the sum of their absolute values
+        size = float((x[:, :, -tail:].float().abs().max() * dy[:, :, -tail:].float().abs()).sum()) * 1.1
+        assert float((g["dconv_w"] - small["dconv_w"]).abs().max()) <= 2e-5 * size

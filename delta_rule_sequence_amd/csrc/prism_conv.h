@@ -212,10 +212,11 @@ __global__ __launch_bounds__(256) void bwd_kernel(ConvArgs a) {
             gk = real ? gk * (sg * (1.f + s * (1.f - sg))) : 0.f;
           }
           g[K - 1][k] = gk;
-          const float gown = own ? gk : 0.f;
-          dw[K][k] += gown;
+          if (own) {  // the whole wave; a product with 0 would carry an infinity of a strip's last rows into other taps
+            dw[K][k] += gk;
 #pragma unroll
-          for (int j = 0; j < K; ++j) dw[j][k] += x[j][k] * gown;
+            for (int j = 0; j < K; ++j) dw[j][k] += x[j][k] * gk;
+          }
           // g[j] is g_{tt-K+1+j}: dx_{tt-K+1} = sum_j w_{K-1-j} g[j]
           o[k] = 0.f;
 #pragma unroll

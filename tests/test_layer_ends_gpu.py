@@ -43,3 +43,22 @@ def test_conv_longest_sequence(prism):
         # the same products, summed in float32 over strips of other lengths: 2e-5 of the sum of their absolute values
         size = float((x[:, :, -tail:].float().abs().max() * dy[:, :, -tail:].float().abs()).sum()) * 1.1
         assert float((g["dconv_w"] - small["dconv_w"]).abs().max()) <= 2e-5 * size
+
+
+@pytest.mark.parametrize("dt,D", [("bf16", 7), ("bf16", 264), ("f32", 5), ("f32", 130)])
+@pytest.mark.parametrize("T", [1, 2, 50, 256])
+def test_conv_infinity_in_the_last_token(prism, dt, D, T):
+    """Of dconv_w, the last token's row enters the last tap only; without silu the gradients of the others and all of
+    dx stay what they are without the infinity."""
+    import torch
+    B, H, K = 2, 1, 4
+    r = Rng(81, dt)
+    x, w, bias, dy = r.vec(B, H, T, D), r.flt(H, K, D), r.flt(H, D), r.vec(B, H, T, D)
+    x[:, :, -1] = 0.0
+    ref = prism.conv_bwd(x, w, dy, bias, silu=False)
+    for v in (float("inf"), float("nan")):
+        x[:, :, -1] = v
+        g = prism.conv_bwd(x, w, dy, bias, silu=False)
+        assert torch.equal(g["dconv_w"][:, :-1], ref["dconv_w"][:, :-1])
+        assert torch.equal(g["dx"], ref["dx"]) and torch.equal(g["dbias"], ref["dbias"])
+        assert not bool(torch.isfinite(g["dconv_w"][:, -1]).any())

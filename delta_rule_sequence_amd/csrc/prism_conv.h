@@ -12,6 +12,7 @@
 // copy of 1 GiB makes 5.2; backward 42 us and 4 for the sum of the shares, 3.8 TB/s: it forms silu' again, about 30 us of vector
 // instructions beside its loads.  One token of 4 x 896: 2.6 us, a launch.
 #pragma once
+#include "prism_silu.h"
 #include "prism_ssm_args.h"
 #include "prism_tile.h"
 
@@ -77,9 +78,6 @@ __device__ __forceinline__ void load_filter(float (&w)[K][V], float (&bias)[V], 
   }
 }
 
-// From the hardware exponential and reciprocal (1 ulp each).
-__device__ __forceinline__ float sigmoid_f(float z) { return __builtin_amdgcn_rcpf(1.f + __expf(-z)); }
-
 __device__ __forceinline__ int seq_len(const ConvArgs& a, int b) {
   if (a.lens == nullptr) return a.T;
   const int n = a.lens[b];
@@ -133,7 +131,7 @@ __global__ __launch_bounds__(256) void fwd_kernel(ConvArgs a) {
           float s = bias[k];
 #pragma unroll
           for (int j = 0; j < K; ++j) s += w[j][k] * x[j][k];
-          o[k] = SILU ? s * sigmoid_f(s) : s;
+          o[k] = SILU ? s * sigmoid<T>(s) : s;
         }
         store_v<T, V>(y + (long long)(t + u) * a.ys.t, o, from);
       }
@@ -208,7 +206,7 @@ __global__ __launch_bounds__(256) void bwd_kernel(ConvArgs a) {
             float s = bias[k];
 #pragma unroll
             for (int j = 0; j < K; ++j) s += w[j][k] * x[j][k];
-            const float sg = sigmoid_f(s);
+            const float sg = sigmoid<T>(s);
             gk = real ? gk * (sg * (1.f + s * (1.f - sg))) : 0.f;
           }
           g[K - 1][k] = gk;
@@ -279,7 +277,7 @@ __global__ __launch_bounds__(256) void step_kernel(ConvArgs a) {
   for (int j = 0; j < K; ++j) s += a.w[((size_t)h * K + j) * a.D + d] * (float)x[j];
 #pragma unroll
   for (int j = 0; j < K - 1; ++j) st[(size_t)j * a.D] = x[j + 1];
-  reinterpret_cast<T*>(a.y)[e] = (T)(a.silu ? s * sigmoid_f(s) : s);
+  reinterpret_cast<T*>(a.y)[e] = (T)(a.silu ? s * sigmoid<T>(s) : s);
 }
 
 }  // namespace conv

@@ -9,6 +9,7 @@
 // gated 10.6 us, 4.7; backward of 16384 x 768 with a residual's gradient 20 us and 4 for dw, 4.3 TB/s; rows of odd
 // length, which start anywhere: backward of 4924 x 843, gated, 26 us.
 #pragma once
+#include "prism_silu.h"
 #include "prism_ssm_args.h"
 #include "prism_tile.h"
 
@@ -17,8 +18,6 @@ namespace norm {
 
 constexpr int kBlock = 128;        // values that share one scale of the 8-bit output
 constexpr float kE4m3Max = 448.f;
-
-__device__ __forceinline__ float sigmoid_f(float z) { return 1.f / (1.f + expf(-z)); }
 
 __device__ __forceinline__ float wave_sum(float v) {
 #pragma unroll
@@ -86,7 +85,7 @@ __global__ __launch_bounds__(256) void fwd_long_kernel(NormArgs a) {
       if (c < a.D) {
         const float h = (float)x[c] + (res != nullptr ? (float)res[c] : 0.f);
         y[k] = h * r * (a.w != nullptr ? a.w[c] : 1.f);
-        if (z != nullptr) y[k] *= (float)z[c] * sigmoid_f((float)z[c]);
+        if (z != nullptr) y[k] *= (float)z[c] * sigmoid<float>((float)z[c]);
         if (a.h != nullptr) reinterpret_cast<T*>(a.h)[row * a.D + c] = (T)h;
       }
       m = max(m, abs_bits(y[k]));
@@ -120,7 +119,7 @@ __global__ __launch_bounds__(256) void bwd_long_kernel(NormArgs a) {
     for (int c = threadIdx.x; c < a.D; c += 256) {
       const float hv = (float)h[c];
       float u = (float)dy[c] * (a.w != nullptr ? a.w[c] : 1.f);
-      if (z != nullptr) u *= (float)z[c] * sigmoid_f((float)z[c]);
+      if (z != nullptr) u *= (float)z[c] * sigmoid<float>((float)z[c]);
       s += hv * hv;
       q += u * hv;
     }
@@ -132,7 +131,7 @@ __global__ __launch_bounds__(256) void bwd_long_kernel(NormArgs a) {
       const float hat = (float)h[c] * r, w = a.w != nullptr ? a.w[c] : 1.f;
       float u = (float)dy[c];
       if (z != nullptr) {
-        const float zv = (float)z[c], sg = sigmoid_f(zv);
+        const float zv = (float)z[c], sg = sigmoid<float>(zv);
         reinterpret_cast<T*>(a.dgate)[at] = (T)(u * hat * w * (sg * (1.f + zv * (1.f - sg))));
         u *= zv * sg;
       }
@@ -213,9 +212,6 @@ __device__ __forceinline__ float row_sum(float v, float* buf) {
   return v;
 }
 
-// silu(z) from the hardware exponential and reciprocal (1 ulp each).
-__device__ __forceinline__ float fast_sigmoid(float z) { return __builtin_amdgcn_rcpf(1.f + __expf(-z)); }
-
 template <class T, int TPR, int NV>
 __global__ __launch_bounds__(row_threads(TPR)) void fwd_row_kernel(NormArgs a) {
   constexpr int V = Piece<T>::V, BL = kBlock / V < TPR ? kBlock / V : TPR;  // lanes of a scale block
@@ -276,7 +272,7 @@ __global__ __launch_bounds__(row_threads(TPR)) void fwd_row_kernel(NormArgs a) {
     }
     if (z != nullptr) {
 #pragma unroll
-      for (int e = 0; e < V; ++e) y[e] *= (float)zv[k][e] * fast_sigmoid((float)zv[k][e]);
+      for (int e = 0; e < V; ++e) y[e] *= (float)zv[k][e] * sigmoid<T>((float)zv[k][e]);
     }
     if (a.scales == nullptr) {
       vec o;
@@ -360,7 +356,7 @@ __global__ __launch_bounds__(row_threads(TPR)) void bwd_row_kernel(NormArgs a) {
         const float hh = (float)hv[k][e];
         u[k][e] = (float)yv[k][e];
         if constexpr (GATE) {
-          sg[k][e] = fast_sigmoid((float)zv[k][e]);
+          sg[k][e] = sigmoid<T>((float)zv[k][e]);
           u[k][e] *= (float)zv[k][e] * sg[k][e];
         }
         s += hh * hh;

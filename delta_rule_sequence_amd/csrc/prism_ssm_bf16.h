@@ -5,8 +5,11 @@
 //   * x, B, C, dy are bfloat16 already: C B^T and dy x^T have exact operands;
 //   * what enters a state (decay-weighted x or dy) is split into three bfloat16 parts that together hold its 24 bits,
 //     so states keep float32 accuracy over any length (three MFMAs in place of one);
-//   * the score matrix M, the state as it is read out into y, the summed score gradients and R in dx are rounded to
-//     bfloat16 once: each is one rounding of 2^-9 on average in a result that is itself rounded to bfloat16;
+//   * the score matrix M and the state as it is read out into y pass as two bfloat16 parts, off by 2^-16 at most, and y is
+//     rounded to bfloat16 once (one part each: y was off by 0.0023 of its size for the 0.0017 of that one rounding; the second
+//     parts cost 8 of 61 us in the sweep of 8 x 24 x 2048 tokens);
+//   * in the backward M, the summed score gradients and R in dx are rounded to bfloat16 once: each is one rounding of 2^-9 on
+//     average in a result that is itself rounded to bfloat16;
 //   * ddt and dA are float32 results: H and R enter the products behind them as three parts, and <H, R> in float32 (two parts:
 //     7 us less at 8 x 12 x 2048, but ddt off by 1e-6 for 2e-7); the sums of score terms that cancel in dA run in float64 (10
 //     us, for dA off by 4e-6 at most over 40 draws of two heads where float32 sums leave 3e-5).
@@ -103,6 +106,23 @@ __device__ __forceinline__ bf16x8 round8(const f32x4& a, const f32x4& b) {
     o[4 + r] = (bf16_t)b[r];
   }
   return o;
+}
+
+// 8 values in K parts, each what the ones before leave, rounded to nearest: two hold 16 bits (off by 2^-16 at most), three
+// the values' float32 digits.
+template <int K>
+__device__ __forceinline__ void parts(const f32x4& a, const f32x4& b, bf16x8 (&p)[K]) {
+  f32x4 c = a, d = b;
+#pragma unroll
+  for (int q = 0; q < K; ++q) {
+    p[q] = round8(c, d);
+    if (q == K - 1) break;
+#pragma unroll
+    for (int r = 0; r < 4; ++r) {
+      c[r] -= (float)p[q][r];
+      d[r] -= (float)p[q][4 + r];
+    }
+  }
 }
 
 // Loads 64 rows of a strided [T, W] tensor into an LDS tile without passing registers, 16 bytes per lane (buffer loads to
@@ -410,7 +430,7 @@ __global__ __launch_bounds__((waves_per_head<PW, PTW>() * HP * 64), 2) void swee
   __shared__ __attribute__((aligned(16))) bf16_t sB[Q * N];
   __shared__ __attribute__((aligned(16))) bf16_t sC[Q * N];
   __shared__ __attribute__((aligned(16))) bf16_t sX[HP][Q * PW];
-  __shared__ __attribute__((aligned(16))) bf16_t sM[HP][Q * Q];
+  __shared__ __attribute__((aligned(16))) bf16_t sM[HP][2][10 * 256];  // two parts of the tiles on and below the diagonal
   __shared__ Scal scal[HP][NB];
   const int HV = a.H * a.nsl;
   const Place pl = place<HP>(a, a.nseg);
@@ -442,11 +462,6 @@ __global__ __launch_bounds__((waves_per_head<PW, PTW>() * HP * 64), 2) void swee
       for (int n = 0; n < NT; ++n)
         hs[p][n] = *reinterpret_cast<const f32x4*>(a.seg + ((size_t)bh * a.nseg + seg) * (N * PW) + tile_at<N>(pt0 + p, n));
   }
-  // score tiles above the diagonal that share a k block with one on it
-  for (int k = wh * 64 + l; k < 2 * 16 * 16; k += NW * 64) {
-    const int blk = k >> 8, r = (k >> 4) & 15, c = k & 15;
-    sM[sub][Tile<Q>::at(32 * blk + r, 32 * blk + 16 + c)] = (bf16_t)0.f;
-  }
   typedef bf16_t ypiece __attribute__((ext_vector_type(4 * PTW)));
   ypiece out[TT];
   const auto store = [&](int k) {
@@ -472,11 +487,6 @@ __global__ __launch_bounds__((waves_per_head<PW, PTW>() * HP * 64), 2) void swee
       for (int q = 0; q < NB; q += NW)
         if (q + wh < NB && k + q + wh < steps) put_scalars<true>(chunk_token(a, b, h, t0 + (q + wh) * Q, len), scal[sub][q + wh]);
     }
-    bf16x8 hf[PTW][KN];
-#pragma unroll
-    for (int p = 0; p < PTW; ++p)
-#pragma unroll
-      for (int n = 0; n < KN; ++n) hf[p][n] = round8(hs[p][2 * n], 2 * n + 1 < NT ? hs[p][2 * n + 1 < NT ? 2 * n + 1 : 0] : zero4());
     loads_done();
     __syncthreads();
     if (k > 0) store(k - 1);
@@ -502,18 +512,22 @@ __global__ __launch_bounds__((waves_per_head<PW, PTW>() * HP * 64), 2) void swee
 #pragma unroll
       for (int u = 0; u < HP; ++u) {
         const Scal& sc = scal[u][k % NB];
-        // the high part's digits are enough for a score that is rounded to bfloat16: for decays it lies above -64 kGone,
-        // so the exponent is off by 2^-10 at most
-        const float cht = sc.ch[t];
-        const f32x4 chs = *reinterpret_cast<const f32x4*>(sc.ch + s0), ds = *reinterpret_cast<const f32x4*>(sc.d + s0);
-        bf16x4 m;
+        const float cht = sc.ch[t], clt = sc.cl[t];
+        const f32x4 chs = *reinterpret_cast<const f32x4*>(sc.ch + s0), cls = *reinterpret_cast<const f32x4*>(sc.cl + s0);
+        const f32x4 ds = *reinterpret_cast<const f32x4*>(sc.d + s0);
+        bf16x4 m[2];
 #pragma unroll
         for (int r = 0; r < 4; ++r) {
-          float v = keep(sacc[q][r] * (__builtin_amdgcn_exp2f(cht - chs[r]) * ds[r]), s0 + r <= t);
+          const float e = __builtin_amdgcn_exp2f((cht - chs[r]) + (clt - cls[r]));
+          float v = keep(sacc[q][r] * (e * ds[r]), s0 + r <= t);
           if (stt[q] == sts[q]) v += s0 + r == t ? Dh[u] : 0.f;  // the skip term: D x_t = D x_s for s = t
-          m[r] = (bf16_t)v;
+          m[0][r] = (bf16_t)v;
+          m[1][r] = (bf16_t)(v - (float)m[0][r]);
         }
-        *reinterpret_cast<bf16x4*>(sM[u] + Tile<Q>::at(t, s0)) = m;
+        // in the order in which the readout's lanes take them: lane (g, i) has row t = i, columns 4 g .. 4 g + 3 of a tile
+        const int tile = stt[q] * (stt[q] + 1) / 2 + sts[q];
+#pragma unroll
+        for (int h2 = 0; h2 < 2; ++h2) *reinterpret_cast<bf16x4*>(&sM[u][h2][tile * 256 + 4 * l]) = m[h2];
       }
     }
     __syncthreads();
@@ -525,13 +539,19 @@ __global__ __launch_bounds__((waves_per_head<PW, PTW>() * HP * 64), 2) void swee
 #pragma unroll
       for (int tt = 0; tt < TT; ++tt) yt[p][tt] = zero4();
 #pragma unroll
-    for (int n = 0; n < KN; ++n)
+    for (int n = 0; n < KN; ++n) {
+      bf16x8 hf[PTW][2], fc[TT];
 #pragma unroll
-      for (int tt = 0; tt < TT; ++tt) {
-        const bf16x8 fc = frag_o<N>(sC, 16 * tt, 32 * n);
+      for (int p = 0; p < PTW; ++p) parts(hs[p][2 * n], 2 * n + 1 < NT ? hs[p][2 * n + 1 < NT ? 2 * n + 1 : 0] : zero4(), hf[p]);
 #pragma unroll
-        for (int p = 0; p < PTW; ++p) yt[p][tt] = mfma(hf[p][n], fc, yt[p][tt]);
-      }
+      for (int tt = 0; tt < TT; ++tt) fc[tt] = frag_o<N>(sC, 16 * tt, 32 * n);
+#pragma unroll
+      for (int q = 1; q >= 0; --q)
+#pragma unroll
+        for (int tt = 0; tt < TT; ++tt)
+#pragma unroll
+          for (int p = 0; p < PTW; ++p) yt[p][tt] = mfma(hf[p][q], fc[tt], yt[p][tt]);
+    }
 #pragma unroll
     for (int tt = 0; tt < TT; ++tt) {
       const float eo = sc.eo[16 * tt + i];
@@ -553,11 +573,17 @@ __global__ __launch_bounds__((waves_per_head<PW, PTW>() * HP * 64), 2) void swee
 #pragma unroll
       for (int p = 0; p < PTW; ++p) fx[p] = frag_t<PW>(tX, 32 * kb, 16 * (pt0 + p));
 #pragma unroll
-      for (int tt = 2 * kb; tt < TT; ++tt) {
-        const bf16x8 fm = frag_o<Q>(sM[sub], 16 * tt, 32 * kb);
+      for (int q = 1; q >= 0; --q)
 #pragma unroll
-        for (int p = 0; p < PTW; ++p) yt[p][tt] = mfma(fx[p], fm, yt[p][tt]);
-      }
+        for (int tt = 2 * kb; tt < TT; ++tt) {
+          const bf16_t* m = &sM[sub][q][(tt * (tt + 1) / 2 + 2 * kb) * 256 + 4 * l];
+          const bf16x4 lo = *reinterpret_cast<const bf16x4*>(m);
+          bf16x4 hi = {0, 0, 0, 0};
+          if (tt > 2 * kb) hi = *reinterpret_cast<const bf16x4*>(m + 256);
+          const bf16x8 fm = __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
+#pragma unroll
+          for (int p = 0; p < PTW; ++p) yt[p][tt] = mfma(fx[p], fm, yt[p][tt]);
+        }
       if (!go_on) continue;
 #pragma unroll
       for (int p = 0; p < PTW; ++p) weighted(f[p], fx[p], 32 * kb, sc.w);
@@ -582,21 +608,6 @@ __global__ __launch_bounds__((waves_per_head<PW, PTW>() * HP * 64), 2) void swee
       for (int n = 0; n < NT; ++n)
 #pragma unroll
         for (int r = 0; r < 4; ++r) a.S_final[gstate + (size_t)(16 * n + 4 * g + r) * a.P + 16 * p + i] = hs[p][n][r];
-  }
-}
-
-// 8 values in three parts, each rounded to nearest: together they hold the values' float32 digits.
-__device__ __forceinline__ void round3(const f32x4& a, const f32x4& b, bf16x8 (&p)[3]) {
-  f32x4 c = a, d = b;
-#pragma unroll
-  for (int q = 0; q < 3; ++q) {
-    p[q] = round8(c, d);
-    if (q == 2) break;
-#pragma unroll
-    for (int r = 0; r < 4; ++r) {
-      c[r] -= (float)p[q][r];
-      d[r] -= (float)p[q][4 + r];
-    }
   }
 }
 
@@ -757,8 +768,8 @@ __global__ __launch_bounds__(512, 2) void grad_kernel(SsmArgs a) {
 #pragma unroll
       for (int p = 0; p < KP; ++p) {
         bf16x8 fh[3], fr[3];
-        round3(hv4[2 * p], hv4[2 * p + 1], fh);
-        round3(rv4[2 * p], rv4[2 * p + 1], fr);
+        parts(hv4[2 * p], hv4[2 * p + 1], fh);
+        parts(rv4[2 * p], rv4[2 * p + 1], fr);
         if (tt0 == 0) {
 #pragma unroll
           for (int r = 0; r < 4; ++r) K += hv4[2 * p][r] * rv4[2 * p][r] + hv4[2 * p + 1][r] * rv4[2 * p + 1][r];

@@ -510,7 +510,7 @@ prism_status prism_conv_step(const void* x, const prism_strides* x_strides, cons
  * Precision: decays and states in float32 from log decays summed in float64.  With PRISM_BF16
  * the products run on bfloat16 operands; what enters the state is split into bfloat16 parts
  * that keep its float32 digits, the score matrix (with the skip term D on its diagonal) and the
- * state's readout are rounded once.
+ * state's readout into two that keep 16 bits, so that y is off by little more than its rounding.
  * Workspace: prism_ssm_fwd_workspace_bytes (0 for invalid or unsupported arguments). */
 size_t prism_ssm_fwd_workspace_bytes(int B, int H, int G, int T, int N, int P, prism_dtype ty);
 prism_status prism_ssm_fwd(const void* x, const prism_strides* x_strides, const void* Bm,

@@ -1,9 +1,17 @@
-"""What the state space layer's operators keep of their digits, on the GPU against definitions in 64 bits."""
+"""What the state space layer's operators keep of their digits, on the GPU against definitions in 64 bits.
+
+Tolerances of bfloat16 scans.  An output in bfloat16 is off by its own rounding, 2^-8 of the value (half a step), and by
+what enters its products rounded: the scores and the state pass as two bfloat16 parts, the second a rounding (2^-8) of what
+the first leaves (2^-8): 2^-16 of a term; with float32 sums as in a scan of float32 tensors (2e-5 of the sum of absolute
+values) b = 2^-16 + 2e-5 of that sum.  A scan that rounds a score once is off by up to 2^-8 of its terms and exceeds this
+wherever they cancel.
+"""
 import numpy as np
 import pytest
 
+from oracle import layer
 from tests.conftest import gpu_available
-from tests.test_layer_gpu import f64
+from tests.test_layer_gpu import f64, scan_inputs, sizes
 
 pytestmark = pytest.mark.gpu
 
@@ -48,3 +56,42 @@ def test_silu_keeps_float32_digits(prism):
         worst[name] = float(np.max(np.abs(a - b) / (k * 2.0 ** -24 * scale)))
     print("  " + ", ".join(f"{k}: worst {v:.3f} of its tolerance" for k, v in worst.items()), flush=True)
     assert max(worst.values()) <= 1.0, worst
+
+
+# ---- scan of bfloat16 tensors -----------------------------------------------------------------------------------------------
+def rounded_once(name, got, ref, size):
+    got = f64(got)
+    lim = 2.0 ** -8 * np.abs(ref) + (2.0 ** -16 + 2e-5) * np.abs(size) + 1e-30
+    worst = float(np.max(np.abs(got - ref) / lim))
+    print(f"  {name}: worst {worst:.3f} of its tolerance", flush=True)
+    assert worst <= 1.0, (name, worst)
+
+
+# every width pair with an even and an odd number of heads per group, one to many segments, lengths off the chunk
+SCAN = [(1, 2, 1, 70, n, p) for n in (16, 32, 64, 128) for p in (16, 32, 64, 128)] + \
+       [(2, 3, 1, 333, 64, 64), (1, 5, 1, 700, 128, 64), (2, 9, 3, 130, 16, 32), (1, 1, 1, 3000, 16, 16), (2, 6, 2, 400, 32, 128), (1, 2, 2, 1, 64, 64)]
+
+
+@pytest.mark.parametrize("case", SCAN, ids=lambda c: "_".join(map(str, c)))
+def test_scan_output_is_rounded_once(prism, case):
+    B, H, G, T, N, P = case
+    r, x, Bm, Cm, dt_, A, D, bias = scan_inputs(82, "bf16", *case, layout="tokens")
+    S0 = r.flt(B, H, N, P)
+    y, _ = prism.ssm_fwd(x, Bm, Cm, dt_, A, D, bias, S0=S0)
+    ref = layer.ssm(*(f64(t) for t in (x, Bm, Cm, dt_, A, D, bias)), True, f64(S0))[0]
+    rounded_once("y", y, ref, sizes(x, Bm, Cm, dt_, A, D, bias, True, S0)[0])
+
+
+@pytest.mark.parametrize("step", [30.0, 1e6])
+def test_scan_is_rounded_once_after_a_reset(prism, step):
+    """A token that wipes the state out puts the log decays of its chunk past 230: the scores behind it keep their digits."""
+    B, H, G, T, N, P = 1, 2, 1, 130, 32, 64
+    r, x, Bm, Cm, dt_, A, D, bias = scan_inputs(84, "bf16", B, H, G, T, N, P)
+    A.fill_(-16.0)
+    d = dt_.sigmoid() * 0.1
+    d[:, :, 3], d[:, :, 70] = step, step
+    x[:, :, 3], x[:, :, 70] = 0.0, 0.0
+    y, _ = prism.ssm_fwd(x, Bm, Cm, d, A, D, softplus=False)
+    args = (x, Bm, Cm, d, A, D, None)
+    ref = layer.ssm(*(None if t is None else f64(t) for t in args), False)[0]
+    rounded_once("y", y, ref, sizes(*args, False, None)[0])

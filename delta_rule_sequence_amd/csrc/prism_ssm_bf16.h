@@ -8,8 +8,7 @@
 //   * the score matrix M and the state as it is read out into y pass as two bfloat16 parts, off by 2^-16 at most, and y is
 //     rounded to bfloat16 once (one part each: y was off by 0.0023 of its size for the 0.0017 of that one rounding; the second
 //     parts cost 8 of 61 us in the sweep of 8 x 24 x 2048 tokens);
-//   * in the backward M, the summed score gradients and R in dx are rounded to bfloat16 once: each is one rounding of 2^-9 on
-//     average in a result that is itself rounded to bfloat16;
+//   * so do M, the summed score gradients and R on their way into dx, dB and dC;
 //   * ddt and dA are float32 results: H and R enter the products behind them as three parts, and <H, R> in float32 (two parts:
 //     7 us less at 8 x 12 x 2048, but ddt off by 1e-6 for 2e-7); the sums of score terms that cancel in dA run in float64 (10
 //     us, for dA off by 4e-6 at most over 40 draws of two heads where float32 sums leave 3e-5).
@@ -50,27 +49,26 @@ template <int W> constexpr int kblocks() { return W < 32 ? 1 : W / 32; }
 // Operand fragments.  frag_n: index = row, k natural (8 g + j; W >= 32).  frag_o: index = row, k in koff order.
 // frag_t: index = column, k = row, koff order (gfx950 transposing LDS reads).
 template <int W>
-__device__ __forceinline__ bf16x8 frag_n(const bf16_t* t, int row0, int k0) {
-  const int l = lane_id();
+__device__ __forceinline__ bf16x8 frag_n(const bf16_t* t, int row0, int k0, int l = lane_id()) {
   return *reinterpret_cast<const bf16x8*>(t + Tile<W>::at(row0 + (l & 15), k0 + 8 * (l >> 4)));
 }
 template <int W>
-__device__ __forceinline__ bf16x8 frag_o(const bf16_t* t, int row0, int k0) {
-  const int l = lane_id(), r = row0 + (l & 15), k = k0 + 4 * (l >> 4);
+__device__ __forceinline__ bf16x8 frag_o(const bf16_t* t, int row0, int k0, int l = lane_id()) {
+  const int r = row0 + (l & 15), k = k0 + 4 * (l >> 4);
   const bf16x4 lo = *reinterpret_cast<const bf16x4*>(t + Tile<W>::at(r, k));
   bf16x4 hi = {0, 0, 0, 0};
   if constexpr (W >= 32) hi = *reinterpret_cast<const bf16x4*>(t + Tile<W>::at(r, k + 16));
   return __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
 }
 template <int W>
-__device__ __forceinline__ bf16x8 frag_row(const bf16_t* t, int row0, int k0) {  // any k order, the same on both sides
-  if constexpr (W >= 32) return frag_n<W>(t, row0, k0);
-  else return frag_o<W>(t, row0, k0);
+__device__ __forceinline__ bf16x8 frag_row(const bf16_t* t, int row0, int k0, int l = lane_id()) {  // any k order, the same on both sides
+  if constexpr (W >= 32) return frag_n<W>(t, row0, k0, l);
+  else return frag_o<W>(t, row0, k0, l);
 }
 template <int W>
-__device__ __forceinline__ bf16x8 frag_t(const bf16_t* t, int k0, int col0) {
+__device__ __forceinline__ bf16x8 frag_t(const bf16_t* t, int k0, int col0, int l = lane_id()) {
   typedef __attribute__((address_space(3))) s16x4_t lds_s16x4;
-  const int l = lane_id(), i = l & 15, r = k0 + 4 * (l >> 4) + (i >> 2), c = col0 + 4 * (i & 3);
+  const int i = l & 15, r = k0 + 4 * (l >> 4) + (i >> 2), c = col0 + 4 * (i & 3);
   const s16x4_t lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)(const_cast<bf16_t*>(t + Tile<W>::at(r, c))));
   const s16x4_t hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)(const_cast<bf16_t*>(t + Tile<W>::at(r + 16, c))));
   return __builtin_bit_cast(bf16x8, __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
@@ -108,21 +106,16 @@ __device__ __forceinline__ bf16x8 round8(const f32x4& a, const f32x4& b) {
   return o;
 }
 
-// 8 values in K parts, each what the ones before leave, rounded to nearest: two hold 16 bits (off by 2^-16 at most), three
+// The leading part of 8 values, rounded to nearest and taken off them: two parts hold 16 bits (off by 2^-16 at most), three
 // the values' float32 digits.
-template <int K>
-__device__ __forceinline__ void parts(const f32x4& a, const f32x4& b, bf16x8 (&p)[K]) {
-  f32x4 c = a, d = b;
+__device__ __forceinline__ bf16x8 take(f32x4& a, f32x4& b) {
+  const bf16x8 o = round8(a, b);
 #pragma unroll
-  for (int q = 0; q < K; ++q) {
-    p[q] = round8(c, d);
-    if (q == K - 1) break;
-#pragma unroll
-    for (int r = 0; r < 4; ++r) {
-      c[r] -= (float)p[q][r];
-      d[r] -= (float)p[q][4 + r];
-    }
+  for (int r = 0; r < 4; ++r) {
+    a[r] -= (float)o[r];
+    b[r] -= (float)o[4 + r];
   }
+  return o;
 }
 
 // Loads 64 rows of a strided [T, W] tensor into an LDS tile without passing registers, 16 bytes per lane (buffer loads to
@@ -161,6 +154,13 @@ struct Rows {
   }
 };
 __device__ __forceinline__ void loads_done() { asm volatile("s_waitcnt vmcnt(0)" ::: "memory"); }
+
+// v, of unknown origin: the compiler then forms the LDS places of a phase when it comes to it, rather than once for all heads
+// in registers that the other phases lack.
+__device__ __forceinline__ int fresh(int v) {
+  asm volatile("" : "+v"(v));
+  return v;
+}
 
 // v, or 0 where !on, whatever v is (as bits: the compiler would branch around what leads to v otherwise).
 __device__ __forceinline__ float keep(float v, bool on) { return val(bits(v) & (on ? 0xffffffffu : 0u)); }
@@ -542,7 +542,11 @@ __global__ __launch_bounds__((waves_per_head<PW, PTW>() * HP * 64), 2) void swee
     for (int n = 0; n < KN; ++n) {
       bf16x8 hf[PTW][2], fc[TT];
 #pragma unroll
-      for (int p = 0; p < PTW; ++p) parts(hs[p][2 * n], 2 * n + 1 < NT ? hs[p][2 * n + 1 < NT ? 2 * n + 1 : 0] : zero4(), hf[p]);
+      for (int p = 0; p < PTW; ++p) {
+        f32x4 h0 = hs[p][2 * n], h1 = 2 * n + 1 < NT ? hs[p][2 * n + 1 < NT ? 2 * n + 1 : 0] : zero4();
+        hf[p][0] = take(h0, h1);
+        hf[p][1] = round8(h0, h1);
+      }
 #pragma unroll
       for (int tt = 0; tt < TT; ++tt) fc[tt] = frag_o<N>(sC, 16 * tt, 32 * n);
 #pragma unroll
@@ -614,9 +618,10 @@ __global__ __launch_bounds__((waves_per_head<PW, PTW>() * HP * 64), 2) void swee
 // Gradients of one chunk for one group, as ssm::grad_kernel (the same grid, formulas and sums).  The eight waves share
 //   * the ten score tiles, two or one each, kept for every head;
 //   * the products with the states by columns n (each wave loads its own part of H and R, from memory to registers);
-//   * dx by columns p, with R's leading part passed on through LDS.
-// Eight waves rather than four: a wave's accumulators and operands then fit its registers (four waves spilled, or ran alone
-// on a SIMD: 183 us where eight take 111, 8 x 12 x 2048 tokens with N = 128, P = 64).
+//   * dx by columns p, with R's first two parts passed on through LDS.
+// Eight waves rather than four: a wave's accumulators and operands then fit its registers (245 of 256 for N = 128, P = 64),
+// since the scores' and dx's places in LDS are formed anew for every head (fresh): kept from head to head they leave 30
+// registers to scratch (8 x 12 x 2048 tokens: the backward 239 us for 190).
 // The skip term sits on the scores' diagonal (D dy_s = D dy_t for t = s), and dD is the sum of the diagonal of dy x^T.
 template <int N, int PW>
 __global__ __launch_bounds__(512, 2) void grad_kernel(SsmArgs a) {
@@ -629,8 +634,8 @@ __global__ __launch_bounds__(512, 2) void grad_kernel(SsmArgs a) {
   __shared__ __attribute__((aligned(16))) bf16_t sC[Q * N];
   __shared__ __attribute__((aligned(16))) bf16_t sXs[2][Q * PW];
   __shared__ __attribute__((aligned(16))) bf16_t sYs[2][Q * PW];  // dy
-  __shared__ __attribute__((aligned(16))) bf16_t sM[Q * Q];   // [t][s]
-  __shared__ __attribute__((aligned(16))) bf16_t sR[N < 32 ? 32 * PW : N * PW];  // [n][p]
+  __shared__ __attribute__((aligned(16))) bf16_t sM[2][Q * Q];   // [t][s], two parts
+  __shared__ __attribute__((aligned(16))) bf16_t sR[2][N < 32 ? 32 * PW : N * PW];  // [n][p], the first two of three parts
   __shared__ Scal scals[2][NB];
   __shared__ double sRow[10][16], sColZ[10][16];  // sums of q_ts d_s, s < t, over s and over t
   __shared__ float sSig[2][NB][Q], sCol[10][16], sDiag[Q], sXY[Q], sI[NT][Q], sJ[NT][Q], sK[WV];
@@ -650,10 +655,10 @@ __global__ __launch_bounds__(512, 2) void grad_kernel(SsmArgs a) {
   }
   for (int k = tid; k < 2 * 16 * 16; k += 512) {  // score tiles above the diagonal inside a k block
     const int blk = k >> 8, r = (k >> 4) & 15, c = k & 15;
-    sM[Tile<Q>::at(32 * blk + r, 32 * blk + 16 + c)] = (bf16_t)0.f;
+    sM[0][Tile<Q>::at(32 * blk + r, 32 * blk + 16 + c)] = sM[1][Tile<Q>::at(32 * blk + r, 32 * blk + 16 + c)] = (bf16_t)0.f;
   }
   if constexpr (N < 32)
-    for (int k = tid; k < 16 * PW; k += 512) sR[16 * PW + k] = (bf16_t)0.f;  // the empty half of the only k block
+    for (int k = tid; k < 16 * PW; k += 512) sR[0][16 * PW + k] = sR[1][16 * PW + k] = (bf16_t)0.f;  // the empty half of the only k block
   Rows<PW, WV> lx, ly;
   lx.init(a.xs.t);
   ly.init(a.dys.t);
@@ -715,16 +720,17 @@ __global__ __launch_bounds__(512, 2) void grad_kernel(SsmArgs a) {
 #pragma unroll
     for (int k = 0; k < SLOTS; ++k) {
       if (w + WV * k >= 10) break;
+      const int lf = fresh(l), g = lf >> 4, i = lf & 15;
       const int tt = stt[k], ts = sts[k], t = 16 * tt + i, s0 = 16 * ts + 4 * g;
       f32x4 dm = zero4(), col;
 #pragma unroll
-      for (int p = 0; p < KP; ++p) dm = mfma(frag_row<PW>(sX, 16 * ts, 32 * p), frag_row<PW>(sY, 16 * tt, 32 * p), dm);
+      for (int p = 0; p < KP; ++p) dm = mfma(frag_row<PW>(sX, 16 * ts, 32 * p, lf), frag_row<PW>(sY, 16 * tt, 32 * p, lf), dm);
       const float cht = sc.ch[t], clt = sc.cl[t];
       const f32x4 chs = *reinterpret_cast<const f32x4*>(sc.ch + s0), cls = *reinterpret_cast<const f32x4*>(sc.cl + s0);
       const f32x4 ds = *reinterpret_cast<const f32x4*>(sc.d + s0);
       double row = 0.0;
-      f32x4 colz;
-      bf16x4 m;
+      f32x4 colf;
+      bf16x4 m[2];
 #pragma unroll
       for (int r = 0; r < 4; ++r) {
         const float e = __builtin_amdgcn_exp2f((cht - chs[r]) + (clt - cls[r])), ed = e * ds[r];
@@ -739,14 +745,16 @@ __global__ __launch_bounds__(512, 2) void grad_kernel(SsmArgs a) {
             sXY[t] = dm[r];
           }
         }
-        m[r] = (bf16_t)mm;
+        m[0][r] = (bf16_t)mm;
+        m[1][r] = (bf16_t)(mm - (float)m[0][r]);
         dg[k][r] += dd;
         const float z = off * ds[r];
         row += (double)z;
-        colz[r] = z;
+        colf[r] = z;
         col[r] = off;
       }
-      *reinterpret_cast<bf16x4*>(sM + Tile<Q>::at(t, s0)) = m;
+#pragma unroll
+      for (int q = 0; q < 2; ++q) *reinterpret_cast<bf16x4*>(sM[q] + Tile<Q>::at(t, s0)) = m[q];
       row = sum_groups(row);
       if (g == 0) sRow[w + WV * k][i] = row;
 #pragma unroll
@@ -754,7 +762,7 @@ __global__ __launch_bounds__(512, 2) void grad_kernel(SsmArgs a) {
       if (i == 0) *reinterpret_cast<f32x4*>(&sCol[w + WV * k][4 * g]) = col;
 #pragma unroll
       for (int r = 0; r < 4; ++r) {
-        const float cz = colz[r];
+        const float cz = colf[r];
         const double z = sum_lanes16((double)cz);
         if (i == 0) sColZ[w + WV * k][4 * g + r] = z;
       }
@@ -767,24 +775,27 @@ __global__ __launch_bounds__(512, 2) void grad_kernel(SsmArgs a) {
       for (int k = 0; k < TTW; ++k) uc[k] = ub[k] = zero4();
 #pragma unroll
       for (int p = 0; p < KP; ++p) {
-        bf16x8 fh[3], fr[3];
-        parts(hv4[2 * p], hv4[2 * p + 1], fh);
-        parts(rv4[2 * p], rv4[2 * p + 1], fr);
+        f32x4 &h0 = hv4[2 * p], &h1 = hv4[2 * p + 1], &r0 = rv4[2 * p], &r1 = rv4[2 * p + 1];
         if (tt0 == 0) {
 #pragma unroll
-          for (int r = 0; r < 4; ++r) K += hv4[2 * p][r] * rv4[2 * p][r] + hv4[2 * p + 1][r] * rv4[2 * p + 1][r];
-          // R's leading part as rows n for dx
-          *reinterpret_cast<bf16x4*>(sR + Tile<PW>::at(16 * nt + i, 32 * p + 4 * g)) = __builtin_shufflevector(fr[0], fr[0], 0, 1, 2, 3);
-          if constexpr (PW >= 32)
-            *reinterpret_cast<bf16x4*>(sR + Tile<PW>::at(16 * nt + i, 32 * p + 16 + 4 * g)) = __builtin_shufflevector(fr[0], fr[0], 4, 5, 6, 7);
+          for (int r = 0; r < 4; ++r) K += h0[r] * r0[r] + h1[r] * r1[r];
         }
+        bf16x8 by[TTW], bx[TTW];
 #pragma unroll
-        for (int k = 0; k < TTW; ++k) {
-          const bf16x8 by = frag_o<PW>(sY, 16 * (tt0 + k), 32 * p), bx = frag_o<PW>(sX, 16 * (tt0 + k), 32 * p);
+        for (int k = 0; k < TTW; ++k) by[k] = frag_o<PW>(sY, 16 * (tt0 + k), 32 * p), bx[k] = frag_o<PW>(sX, 16 * (tt0 + k), 32 * p);
+        // part by part, each taken off the values in place
 #pragma unroll
-          for (int q = 2; q >= 0; --q) {
-            uc[k] = mfma(fh[q], by, uc[k]);
-            ub[k] = mfma(fr[q], bx, ub[k]);
+        for (int q = 0; q < 3; ++q) {
+          const bf16x8 fh = take(h0, h1), fr = take(r0, r1);
+          if (q < 2 && tt0 == 0) {  // R as rows n for dx
+            *reinterpret_cast<bf16x4*>(sR[q] + Tile<PW>::at(16 * nt + i, 32 * p + 4 * g)) = __builtin_shufflevector(fr, fr, 0, 1, 2, 3);
+            if constexpr (PW >= 32)
+              *reinterpret_cast<bf16x4*>(sR[q] + Tile<PW>::at(16 * nt + i, 32 * p + 16 + 4 * g)) = __builtin_shufflevector(fr, fr, 4, 5, 6, 7);
+          }
+#pragma unroll
+          for (int k = 0; k < TTW; ++k) {
+            uc[k] = mfma(fh, by[k], uc[k]);
+            ub[k] = mfma(fr, bx[k], ub[k]);
           }
         }
       }
@@ -818,14 +829,21 @@ __global__ __launch_bounds__(512, 2) void grad_kernel(SsmArgs a) {
     __syncthreads();
     // dx: rows p, columns s
     if (has_p) {
+      const int lf = fresh(l), g = lf >> 4, i = lf & 15;
       f32x4 ax[STW];
 #pragma unroll
       for (int k = 0; k < STW; ++k) ax[k] = zero4();
 #pragma unroll
       for (int n = 0; n < KN; ++n) {
-        const bf16x8 f = frag_t<PW>(sR, 32 * n, 16 * pw);
+        bf16x8 f[2], fb[STW];
 #pragma unroll
-        for (int k = 0; k < STW; ++k) ax[k] = mfma(f, frag_o<N>(sB, 16 * (st0 + k), 32 * n), ax[k]);
+        for (int q = 0; q < 2; ++q) f[q] = frag_t<PW>(sR[q], 32 * n, 16 * pw, lf);
+#pragma unroll
+        for (int k = 0; k < STW; ++k) fb[k] = frag_o<N>(sB, 16 * (st0 + k), 32 * n, lf);
+#pragma unroll
+        for (int q = 0; q < 2; ++q)
+#pragma unroll
+          for (int k = 0; k < STW; ++k) ax[k] = mfma(f[q], fb[k], ax[k]);
       }
 #pragma unroll
       for (int k = 0; k < STW; ++k) {
@@ -834,10 +852,12 @@ __global__ __launch_bounds__(512, 2) void grad_kernel(SsmArgs a) {
       }
 #pragma unroll
       for (int kb = 0; kb < 2; ++kb) {
-        const bf16x8 f = frag_t<PW>(sY, 32 * kb, 16 * pw);
+        const bf16x8 f = frag_t<PW>(sY, 32 * kb, 16 * pw, lf);
 #pragma unroll
-        for (int k = 0; k < STW; ++k)
-          if (kb >= (st0 + k) / 2) ax[k] = mfma(f, frag_t<Q>(sM, 32 * kb, 16 * (st0 + k)), ax[k]);
+        for (int q = 0; q < 2; ++q)
+#pragma unroll
+          for (int k = 0; k < STW; ++k)
+            if (kb >= (st0 + k) / 2) ax[k] = mfma(f, frag_t<Q>(sM[q], 32 * kb, 16 * (st0 + k), lf), ax[k]);
       }
 #pragma unroll
       for (int k = 0; k < STW; ++k) {
@@ -898,10 +918,13 @@ __global__ __launch_bounds__(512, 2) void grad_kernel(SsmArgs a) {
 #pragma unroll
   for (int k = 0; k < SLOTS; ++k) {
     if (w + WV * k >= 10) break;
-    bf16x4 o;
 #pragma unroll
-    for (int r = 0; r < 4; ++r) o[r] = (bf16_t)dg[k][r];
-    *reinterpret_cast<bf16x4*>(sM + Tile<Q>::at(16 * stt[k] + i, 16 * sts[k] + 4 * g)) = o;
+    for (int q = 0; q < 2; ++q) {
+      bf16x4 o;
+#pragma unroll
+      for (int r = 0; r < 4; ++r) o[r] = (bf16_t)dg[k][r], dg[k][r] -= (float)o[r];
+      *reinterpret_cast<bf16x4*>(sM[q] + Tile<Q>::at(16 * stt[k] + i, 16 * sts[k] + 4 * g)) = o;
+    }
   }
   __syncthreads();
   if (!has_n) return;
@@ -910,8 +933,11 @@ __global__ __launch_bounds__(512, 2) void grad_kernel(SsmArgs a) {
     const int tt = tt0 + k, t = 16 * tt + i, c = 16 * nt + 4 * g;
 #pragma unroll
     for (int kb = 0; kb < 2; ++kb) {
-      if (kb <= tt / 2) dc[k] = mfma(frag_t<N>(sB, 32 * kb, 16 * nt), frag_o<Q>(sM, 16 * tt, 32 * kb), dc[k]);
-      if (kb >= tt / 2) db[k] = mfma(frag_t<N>(sC, 32 * kb, 16 * nt), frag_t<Q>(sM, 32 * kb, 16 * tt), db[k]);
+#pragma unroll
+      for (int q = 0; q < 2; ++q) {
+        if (kb <= tt / 2) dc[k] = mfma(frag_t<N>(sB, 32 * kb, 16 * nt), frag_o<Q>(sM[q], 16 * tt, 32 * kb), dc[k]);
+        if (kb >= tt / 2) db[k] = mfma(frag_t<N>(sC, 32 * kb, 16 * nt), frag_t<Q>(sM[q], 32 * kb, 16 * tt), db[k]);
+      }
     }
     if (t0 + t >= a.T) continue;
     if (a.nsplit == 1) {

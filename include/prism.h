@@ -526,8 +526,9 @@ prism_status prism_ssm_fwd(const void* x, const prism_strides* x_strides, const 
  *   dx [B, H, T, P], dBm, dCm [B, G, T, N] dtype ty, strided (dBm, dCm: summed over the group's heads
  *   in float32);  ddt [B, H, T] float32, dense;  dA [H], and dD, ddt_bias [H] (NULL = not wanted),
  *   float32, summed over batches and tokens.  Every sum has a fixed order.
- * Supported and precision as prism_ssm_fwd (rows of dy, dx, dBm and dCm too); with PRISM_BF16 the states
- * behind ddt, dA and ddt_bias keep their float32 digits.  Workspace: prism_ssm_bwd_workspace_bytes. */
+ * Supported and precision as prism_ssm_fwd (rows of dy, dx, dBm and dCm too): with PRISM_BF16 dx, dBm and
+ * dCm are off by little more than their rounding, and the states behind ddt, dA and ddt_bias keep their
+ * float32 digits.  Workspace: prism_ssm_bwd_workspace_bytes. */
 size_t prism_ssm_bwd_workspace_bytes(int B, int H, int G, int T, int N, int P, prism_dtype ty);
 prism_status prism_ssm_bwd(const void* x, const prism_strides* x_strides, const void* Bm,
                            const prism_strides* b_strides, const void* Cm, const prism_strides* c_strides,

@@ -1,10 +1,10 @@
 """What the state space layer's operators keep of their digits, on the GPU against definitions in 64 bits.
 
 Tolerances of bfloat16 scans.  An output in bfloat16 is off by its own rounding, 2^-8 of the value (half a step), and by
-what enters its products rounded: the scores and the state pass as two bfloat16 parts, the second a rounding (2^-8) of what
-the first leaves (2^-8): 2^-16 of a term; with float32 sums as in a scan of float32 tensors (2e-5 of the sum of absolute
-values) b = 2^-16 + 2e-5 of that sum.  A scan that rounds a score once is off by up to 2^-8 of its terms and exceeds this
-wherever they cancel.
+what enters its products rounded: the scores, their gradients, the state and its adjoint pass as two bfloat16 parts, the
+second a rounding (2^-8) of what the first leaves (2^-8): 2^-16 of a term; with float32 sums as in a scan of float32
+tensors (2e-5 of the sum of absolute values) b = 2^-16 + 2e-5 of that sum.  A scan that rounds a score once is off by up to
+2^-8 of its terms and exceeds this wherever they cancel.
 """
 import numpy as np
 import pytest
@@ -80,6 +80,18 @@ def test_scan_output_is_rounded_once(prism, case):
     y, _ = prism.ssm_fwd(x, Bm, Cm, dt_, A, D, bias, S0=S0)
     ref = layer.ssm(*(f64(t) for t in (x, Bm, Cm, dt_, A, D, bias)), True, f64(S0))[0]
     rounded_once("y", y, ref, sizes(x, Bm, Cm, dt_, A, D, bias, True, S0)[0])
+
+
+@pytest.mark.parametrize("case", SCAN, ids=lambda c: "_".join(map(str, c)))
+def test_scan_gradients_are_rounded_once(prism, case):
+    B, H, G, T, N, P = case
+    r, x, Bm, Cm, dt_, A, D, bias = scan_inputs(83, "bf16", *case)
+    dy, dS = r.vec(B, H, T, P), r.flt(B, H, N, P)
+    g = prism.ssm_bwd(x, Bm, Cm, dt_, A, dy, D, bias, dS_final=dS)
+    args = [f64(t) for t in (x, Bm, Cm, dt_, A, dy, D, bias)]
+    ref, size = layer.ssm_grad(*args, True, f64(dS)), layer.ssm_grad(*args, True, f64(dS), absolute=True)
+    for k in ("dx", "dB", "dC"):
+        rounded_once(k, g[k], ref[k], size[k])
 
 
 @pytest.mark.parametrize("step", [30.0, 1e6])

@@ -107,3 +107,22 @@ def test_scan_is_rounded_once_after_a_reset(prism, step):
     args = (x, Bm, Cm, d, A, D, None)
     ref = layer.ssm(*(None if t is None else f64(t) for t in args), False)[0]
     rounded_once("y", y, ref, sizes(*args, False, None)[0])
+
+
+@pytest.mark.parametrize("case", [(2, 4, 1, 500, 128, 64), (1, 3, 1, 1100, 64, 32), (2, 2, 2, 300, 16, 128)], ids=lambda c: "_".join(map(str, c)))
+def test_states_and_step_gradients_keep_float32_digits(prism, case):
+    """S_final and ddt of bfloat16 tensors, root mean square of the error against that of the value.  Their operands pass as three
+    parts (24 bits), so what is left are roundings of 2^-24: the weight and its product (3 half steps), a sum over 64 tokens per
+    chunk and one per chunk.  Independent, a dozen of them make 2^-22; the limit is 2^-21.  Two parts (16 bits) leave
+    1e-5 of S_final and 3e-6 of ddt (the oracle's formulas with operands cut to 16 bits)."""
+    B, H, G, T, N, P = case
+    r, x, Bm, Cm, dt_, A, D, bias = scan_inputs(85, "bf16", *case)
+    _, S = prism.ssm_fwd(x, Bm, Cm, dt_, A, D, bias)
+    dy, dS = r.vec(B, H, T, P), r.flt(B, H, N, P)
+    g = prism.ssm_bwd(x, Bm, Cm, dt_, A, dy, D, bias, dS_final=dS)
+    ref_S = layer.ssm(*(f64(t) for t in (x, Bm, Cm, dt_, A, D, bias)))[1]
+    ref = layer.ssm_grad(*(f64(t) for t in (x, Bm, Cm, dt_, A, dy, D, bias)), True, f64(dS))
+    rms = lambda a: float(np.sqrt((a ** 2).mean()))  # noqa: E731
+    off = {"S_final": rms(f64(S) - ref_S) / rms(ref_S), "ddt": rms(f64(g["ddt"]) - ref["ddt"]) / rms(ref["ddt"])}
+    print("  " + ", ".join(f"{k}: {v:.2e}" for k, v in off.items()), flush=True)
+    assert max(off.values()) <= 2.0 ** -21, off

@@ -315,9 +315,12 @@ __global__ __launch_bounds__(row_threads(TPR)) void fwd_row_kernel(NormArgs a) {
 
 // The same for the backward: the workgroup walks rows (256 / TPR at a time) with its lanes' columns of dweight in
 // registers, joins them over its row slots in LDS and leaves one share per workgroup.
+// Gated bfloat16 rows of 1024 lanes form sigmoid(z) and u again for the outputs: held, with the row in 128 registers per lane,
+// they went to scratch (1000 x 8200: 70 us, formed again 33; 1000 x 16384: 99 and 51; in 512 lanes of 256 registers 80 and 116).
 template <class T, int TPR, int NV, bool GATE>
 __global__ __launch_bounds__(row_threads(TPR)) void bwd_row_kernel(NormArgs a) {
   constexpr int V = Piece<T>::V, RPB = row_threads(TPR) / TPR;
+  constexpr bool AGAIN = GATE && TPR == 1024 && V == 8;
   typedef typename Piece<T>::vec vec;
   __shared__ float buf[2][2][TPR < 256 ? 1 : TPR / 64];  // taken in turn: no wait for the last row's reads
   __shared__ float sdw[RPB > 1 ? RPB * TPR * V : 1];
@@ -349,16 +352,19 @@ __global__ __launch_bounds__(row_threads(TPR)) void bwd_row_kernel(NormArgs a) {
       if (din != nullptr) iv[k] = load_piece(din + c, left);
     }
     float u[NV][V], sg[GATE ? NV : 1][V];  // u = dy silu(z)
+    const auto through_gate = [&](int k, int e) {
+      u[k][e] = (float)yv[k][e];
+      if constexpr (GATE) {
+        sg[k][e] = sigmoid<T>((float)zv[k][e]);
+        u[k][e] *= (float)zv[k][e] * sg[k][e];
+      }
+    };
 #pragma unroll
     for (int k = 0; k < NV; ++k) {
 #pragma unroll
       for (int e = 0; e < V; ++e) {
         const float hh = (float)hv[k][e];
-        u[k][e] = (float)yv[k][e];
-        if constexpr (GATE) {
-          sg[k][e] = sigmoid<T>((float)zv[k][e]);
-          u[k][e] *= (float)zv[k][e] * sg[k][e];
-        }
+        through_gate(k, e);
         s += hh * hh;
         q += u[k][e] * w[k][e] * hh;
       }
@@ -371,10 +377,17 @@ __global__ __launch_bounds__(row_threads(TPR)) void bwd_row_kernel(NormArgs a) {
     for (int k = 0; k < NV; ++k) {
       const int c = (k * TPR + j) * V;
       if (c >= a.D) continue;
+      if constexpr (AGAIN) {  // z of unknown origin, so that the compiler does not hold what it has formed from it
+        typedef unsigned u32x4 __attribute__((ext_vector_type(4)));
+        u32x4 z4 = __builtin_bit_cast(u32x4, zv[k]);
+        asm volatile("" : "+v"(z4));
+        zv[k] = __builtin_bit_cast(vec, z4);
+      }
       vec o, og;
 #pragma unroll
       for (int e = 0; e < V; ++e) {
         const float hat = (float)hv[k][e] * r;
+        if constexpr (AGAIN) through_gate(k, e);
         dw[k][e] += u[k][e] * hat;
         o[e] = (T)(r * (u[k][e] * w[k][e] - hat * mean) + (float)iv[k][e]);
         if constexpr (GATE) {

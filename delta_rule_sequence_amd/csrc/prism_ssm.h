@@ -146,24 +146,16 @@ __device__ __forceinline__ void put_scalars(const Token& k, Scal& s) {
   if (lane == 0) s.dec = k.all();
 }
 
-// Rows t0 .. t0 + 63 of a strided [T, W] tensor as float32 in LDS (row stride LD); rows at or past len are 0.
-template <class T, int W, int LD>
+// Rows t0 .. t0 + 63 of a strided [T, W] tensor in LDS (row stride LD); rows at or past len are 0.
+template <int W, int LD>
 __device__ __forceinline__ void load_rows(float* dst, const void* base, long long off, long long st, int t0, int len,
                                           int nthreads) {
-  constexpr int V = 16 / sizeof(T);
-  typedef T vec __attribute__((ext_vector_type(V)));
-  const T* p = reinterpret_cast<const T*>(base) + off;
-  for (int i = threadIdx.x; i < Q * W / V; i += nthreads) {
-    const int r = i / (W / V), c = i % (W / V) * V;
-    float* o = dst + r * LD + c;
-    if (t0 + r < len) {
-      const vec v = *reinterpret_cast<const vec*>(p + (long long)(t0 + r) * st + c);
-#pragma unroll
-      for (int k = 0; k < V; ++k) o[k] = (float)v[k];
-    } else {
-#pragma unroll
-      for (int k = 0; k < V; ++k) o[k] = 0.f;
-    }
+  const float* p = reinterpret_cast<const float*>(base) + off;
+  for (int i = threadIdx.x; i < Q * W / 4; i += nthreads) {
+    const int r = i / (W / 4), c = i % (W / 4) * 4;
+    f32x4 v = zero4();
+    if (t0 + r < len) v = *reinterpret_cast<const f32x4*>(p + (long long)(t0 + r) * st + c);
+    *reinterpret_cast<f32x4*>(dst + r * LD + c) = v;
   }
 }
 
@@ -214,7 +206,7 @@ __device__ __forceinline__ size_t elem_at(int n, int p) {
 // Grid (nseg, B * HV, directions); NW = PW / 16 waves, each owning 16 columns.
 //   direction 0: H' = dec H + (w d B)^T x over the chunks in order;   saved: the state entering each chunk
 //   direction 1: R' = dec R + (eo C)^T dy in reverse order;           saved: the adjoint leaving each chunk
-template <class T, int N, int PW, bool SAVE>
+template <int N, int PW, bool SAVE>
 __global__ __launch_bounds__(PW * 4) void state_kernel(SsmArgs a) {
   constexpr int NTH = PW * 4, LDN = N + 4, LDP = PW + 4, NT = N / 16;
   __shared__ float sA[Q * LDN];
@@ -241,11 +233,11 @@ __global__ __launch_bounds__(PW * 4) void state_kernel(SsmArgs a) {
     if (t0 >= len) continue;
     __syncthreads();
     if (rev) {
-      load_rows<T, N, LDN>(sA, a.cm, b * a.cs.b + grp * a.cs.h, a.cs.t, t0, len, NTH);
-      load_rows<T, PW, LDP>(sV, a.dy, b * a.dys.b + h * a.dys.h + p0, a.dys.t, t0, len, NTH);
+      load_rows<N, LDN>(sA, a.cm, b * a.cs.b + grp * a.cs.h, a.cs.t, t0, len, NTH);
+      load_rows<PW, LDP>(sV, a.dy, b * a.dys.b + h * a.dys.h + p0, a.dys.t, t0, len, NTH);
     } else {
-      load_rows<T, N, LDN>(sA, a.bm, b * a.bs.b + grp * a.bs.h, a.bs.t, t0, len, NTH);
-      load_rows<T, PW, LDP>(sV, a.x, b * a.xs.b + h * a.xs.h + p0, a.xs.t, t0, len, NTH);
+      load_rows<N, LDN>(sA, a.bm, b * a.bs.b + grp * a.bs.h, a.bs.t, t0, len, NTH);
+      load_rows<PW, LDP>(sV, a.x, b * a.xs.b + h * a.xs.h + p0, a.xs.t, t0, len, NTH);
     }
     if (tid < 64) {
       const Token tk = chunk_token(a, b, h, t0, len);
@@ -323,10 +315,9 @@ __global__ __launch_bounds__(256) void seg_scan_kernel(SsmArgs a, int groups) {
 
 // The scan of a segment from its entering state (seg when nseg > 1, else S0): outputs, and the final state
 // from the last segment.  Grid (nseg, B * HV).
-template <class T, int N, int PW>
+template <int N, int PW>
 __global__ __launch_bounds__(PW * 4) void sweep_kernel(SsmArgs a) {
   constexpr int NTH = PW * 4, NW = PW / 16, LDN = N + 4, LDP = PW + 4, LDQ = Q + 4, NT = N / 16;
-  typedef T out4 __attribute__((ext_vector_type(4)));
   __shared__ float sB[Q * LDN];
   __shared__ float sC[Q * LDN];
   __shared__ float sX[Q * LDP];
@@ -352,9 +343,9 @@ __global__ __launch_bounds__(PW * 4) void sweep_kernel(SsmArgs a) {
     const int t0 = ch * Q;
     if (t0 >= len) break;
     __syncthreads();
-    load_rows<T, N, LDN>(sB, a.bm, b * a.bs.b + grp * a.bs.h, a.bs.t, t0, len, NTH);
-    load_rows<T, N, LDN>(sC, a.cm, b * a.cs.b + grp * a.cs.h, a.cs.t, t0, len, NTH);
-    load_rows<T, PW, LDP>(sX, a.x, b * a.xs.b + h * a.xs.h + p0, a.xs.t, t0, len, NTH);
+    load_rows<N, LDN>(sB, a.bm, b * a.bs.b + grp * a.bs.h, a.bs.t, t0, len, NTH);
+    load_rows<N, LDN>(sC, a.cm, b * a.cs.b + grp * a.cs.h, a.cs.t, t0, len, NTH);
+    load_rows<PW, LDP>(sX, a.x, b * a.xs.b + h * a.xs.h + p0, a.xs.t, t0, len, NTH);
     if (tid < 64) put_scalars<false>(chunk_token(a, b, h, t0, len), sc);
     __syncthreads();
     // M: ten tiles (rows s, columns t) over the waves, TG of a wave's at a time; a wave without one forms the last again
@@ -424,11 +415,11 @@ __global__ __launch_bounds__(PW * 4) void sweep_kernel(SsmArgs a) {
       const int t = 16 * tt + i;
       const f32x4 xv = *reinterpret_cast<const f32x4*>(sX + t * LDP + 16 * pt + 4 * g);
       if (t0 + t < len) {
-        out4 o;
+        f32x4 o;
 #pragma unroll
-        for (int r = 0; r < 4; ++r) o[r] = (T)(yt[tt][r] + Dh * xv[r]);
-        T* y = reinterpret_cast<T*>(a.y) + b * a.ys.b + h * a.ys.h + (long long)(t0 + t) * a.ys.t + p0 + 16 * pt + 4 * g;
-        *reinterpret_cast<out4*>(y) = o;
+        for (int r = 0; r < 4; ++r) o[r] = yt[tt][r] + Dh * xv[r];
+        float* y = reinterpret_cast<float*>(a.y) + b * a.ys.b + h * a.ys.h + (long long)(t0 + t) * a.ys.t + p0 + 16 * pt + 4 * g;
+        *reinterpret_cast<f32x4*>(y) = o;
       }
     }
     if ((ch + 1 == c1 || t0 + Q >= len) && seg != a.nseg - 1) break;  // nobody reads the state behind the segment
@@ -463,10 +454,9 @@ __global__ __launch_bounds__(PW * 4) void sweep_kernel(SsmArgs a) {
 //   dd_s = sum_t q_ts + J_s + A dl_s,   q = (C B^T) E dM,   J_s = w_s B_s . (R x_s)
 //   dl_t = sum_{s<t<=t'} q_t's d_s + sum_{t'>=t} I_t' + sum_{s<t} d_s J_s + e^{c_63} <H, R>,   I_t = eo_t C_t . (H dy_t)
 // Four waves, wave w owning tokens 16 w .. 16 w + 15 as columns t of the score tiles and as rows of dx, dB and dC.
-template <class T, int N, int PW>
+template <int N, int PW>
 __global__ __launch_bounds__(256) void grad_kernel(SsmArgs a) {
   constexpr int LDN = N + 4, LDP = PW + 4, LDQ = Q + 4, NT = N / 16, PT = PW / 16;
-  typedef T out4 __attribute__((ext_vector_type(4)));
   __shared__ float sB[Q * LDN];
   __shared__ float sC[Q * LDN];
   __shared__ float sX[Q * LDP];
@@ -479,8 +469,8 @@ __global__ __launch_bounds__(256) void grad_kernel(SsmArgs a) {
   const int w = wave_id(), tid = threadIdx.x, l = lane_id(), g = l >> 4, i = l & 15;
   const int HV = a.H * a.nsl, per_group = HV / a.G;
   const int v0 = blockIdx.y * a.per_split, v1 = min(v0 + a.per_split, per_group);
-  load_rows<T, N, LDN>(sB, a.bm, b * a.bs.b + grp * a.bs.h, a.bs.t, t0, a.T, 256);
-  load_rows<T, N, LDN>(sC, a.cm, b * a.cs.b + grp * a.cs.h, a.cs.t, t0, a.T, 256);
+  load_rows<N, LDN>(sB, a.bm, b * a.bs.b + grp * a.bs.h, a.bs.t, t0, a.T, 256);
+  load_rows<N, LDN>(sC, a.cm, b * a.cs.b + grp * a.cs.h, a.cs.t, t0, a.T, 256);
   __syncthreads();
   const int tok = 16 * w + i;  // this lane's token
   f32x4 gm[4], dg[4], dc[NT], db[NT];
@@ -504,8 +494,8 @@ __global__ __launch_bounds__(256) void grad_kernel(SsmArgs a) {
     const float* H = a.st + (bh * a.nch + ch) * (N * PW);
     const float* R = a.st + (((size_t)a.B * HV + bh) * a.nch + ch) * (N * PW);
     __syncthreads();
-    load_rows<T, PW, LDP>(sX, a.x, b * a.xs.b + h * a.xs.h + p0, a.xs.t, t0, a.T, 256);
-    load_rows<T, PW, LDP>(sY, a.dy, b * a.dys.b + h * a.dys.h + p0, a.dys.t, t0, a.T, 256);
+    load_rows<PW, LDP>(sX, a.x, b * a.xs.b + h * a.xs.h + p0, a.xs.t, t0, a.T, 256);
+    load_rows<PW, LDP>(sY, a.dy, b * a.dys.b + h * a.dys.h + p0, a.dys.t, t0, a.T, 256);
     if (tid < 64) {
       const Token tk = chunk_token(a, b, h, t0, a.T);
       put_scalars<false>(tk, sc);
@@ -644,15 +634,15 @@ __global__ __launch_bounds__(256) void grad_kernel(SsmArgs a) {
     for (int p = 0; p < PT; ++p) {
       const f32x4 yv = *reinterpret_cast<const f32x4*>(sY + tok * LDP + 16 * p + 4 * g);
       const f32x4 xv = *reinterpret_cast<const f32x4*>(sX + tok * LDP + 16 * p + 4 * g);
-      out4 o;
+      f32x4 o;
 #pragma unroll
       for (int r = 0; r < 4; ++r) {
-        o[r] = (T)(ax[p][r] + Dh * yv[r]);
+        o[r] = ax[p][r] + Dh * yv[r];
         xd += xv[r] * yv[r];
       }
       if (t0 + tok < a.T) {
-        T* q = reinterpret_cast<T*>(a.dx) + b * a.dxs.b + h * a.dxs.h + (long long)(t0 + tok) * a.dxs.t + p0 + 16 * p + 4 * g;
-        *reinterpret_cast<out4*>(q) = o;
+        float* q = reinterpret_cast<float*>(a.dx) + b * a.dxs.b + h * a.dxs.h + (long long)(t0 + tok) * a.dxs.t + p0 + 16 * p + 4 * g;
+        *reinterpret_cast<f32x4*>(q) = o;
       }
     }
     xd = sum_groups(sum_lanes16(xd));
@@ -723,14 +713,8 @@ __global__ __launch_bounds__(256) void grad_kernel(SsmArgs a) {
     if (t0 + tok < a.T) {
       const int c = 16 * n + 4 * g;
       if (a.nsplit == 1) {
-        out4 ob, oc;
-#pragma unroll
-        for (int r = 0; r < 4; ++r) {
-          ob[r] = (T)db[n][r];
-          oc[r] = (T)dc[n][r];
-        }
-        *reinterpret_cast<out4*>(reinterpret_cast<T*>(a.dbm) + b * a.dbs.b + grp * a.dbs.h + (long long)(t0 + tok) * a.dbs.t + c) = ob;
-        *reinterpret_cast<out4*>(reinterpret_cast<T*>(a.dcm) + b * a.dcs.b + grp * a.dcs.h + (long long)(t0 + tok) * a.dcs.t + c) = oc;
+        *reinterpret_cast<f32x4*>(reinterpret_cast<float*>(a.dbm) + b * a.dbs.b + grp * a.dbs.h + (long long)(t0 + tok) * a.dbs.t + c) = db[n];
+        *reinterpret_cast<f32x4*>(reinterpret_cast<float*>(a.dcm) + b * a.dcs.b + grp * a.dcs.h + (long long)(t0 + tok) * a.dcs.t + c) = dc[n];
       } else {
         const size_t at = (((size_t)blockIdx.y * a.B * a.G + bg) * a.T + t0 + tok) * N + c;
         *reinterpret_cast<f32x4*>(a.part_b + at) = db[n];

@@ -46,10 +46,10 @@ prism_status ssm_fwd_pw(const SsmArgs& a, hipStream_t stream) {
     else ssm_fwd_mx<N, PW, PTW, 1>(a, stream);
   } else {
     if (a.nseg > 1) {
-      ssm::state_kernel<T, N, PW, false><<<dim3(a.nseg, bh, 1), PW * 4, 0, stream>>>(a);
+      ssm::state_kernel<N, PW, false><<<dim3(a.nseg, bh, 1), PW * 4, 0, stream>>>(a);
       seg_scan<N, PW, true>(a, 1, stream);
     }
-    ssm::sweep_kernel<T, N, PW><<<dim3(a.nseg, bh), PW * 4, 0, stream>>>(a);
+    ssm::sweep_kernel<N, PW><<<dim3(a.nseg, bh), PW * 4, 0, stream>>>(a);
   }
   return launched();
 }
@@ -63,10 +63,10 @@ prism_status ssm_bwd_pw(const SsmArgs& a, hipStream_t stream) {
     else ssm_bwd_states_mx<N, PW, PTW, 1>(a, stream);
     ssm::mx::grad_kernel<N, PW><<<dim3(a.nch, a.nsplit, a.B * a.G), 512, 0, stream>>>(a);
   } else {
-    if (a.nseg > 1) ssm::state_kernel<T, N, PW, false><<<dim3(a.nseg, bh, 2), PW * 4, 0, stream>>>(a);
+    if (a.nseg > 1) ssm::state_kernel<N, PW, false><<<dim3(a.nseg, bh, 2), PW * 4, 0, stream>>>(a);
     seg_scan<N, PW, true>(a, 2, stream);
-    ssm::state_kernel<T, N, PW, true><<<dim3(a.nseg, bh, 2), PW * 4, 0, stream>>>(a);
-    ssm::grad_kernel<T, N, PW><<<dim3(a.nch, a.nsplit, a.B * a.G), 256, 0, stream>>>(a);
+    ssm::state_kernel<N, PW, true><<<dim3(a.nseg, bh, 2), PW * 4, 0, stream>>>(a);
+    ssm::grad_kernel<N, PW><<<dim3(a.nch, a.nsplit, a.B * a.G), 256, 0, stream>>>(a);
   }
   const auto blocks = [](size_t n) { return (unsigned)((n + 255) / 256); };
   const unsigned n_ddt = a.nsl > 1 ? blocks((size_t)a.B * a.H * a.T) : 0;

@@ -12,6 +12,8 @@
 // copy of 1 GiB makes 5.2; backward 42 us and 4 for the sum of the shares, 3.8 TB/s: it forms silu' again, about 30 us of vector
 // instructions beside its loads.  One token of 4 x 896: 2.6 us, a launch.
 #pragma once
+#include <type_traits>
+
 #include "prism_silu.h"
 #include "prism_ssm_args.h"
 #include "prism_tile.h"
@@ -163,7 +165,7 @@ __global__ __launch_bounds__(256) void bwd_kernel(ConvArgs a) {
 #pragma unroll
     for (int k = 0; k < V; ++k) dw[j][k] = 0.f;
   if (first < a.D && strip < a.nstrip) {
-    const int t0 = strip * a.strip, t1 = t0 + min(a.strip, a.T - t0), te = t1 + K - 1;
+    const int t0 = strip * a.strip, t1 = t0 + min(a.strip, a.T - t0);
     float w[K][V], bias[V], x[K][V], g[K][V];
     load_filter<K, V>(w, bias, a, h, d);
 #pragma unroll
@@ -179,50 +181,64 @@ __global__ __launch_bounds__(256) void bwd_kernel(ConvArgs a) {
     const T* xp = reinterpret_cast<const T*>(a.x) + b * a.xs.b + h * a.xs.h + d;
     const T* dy = reinterpret_cast<const T*>(a.dy) + b * a.dys.b + h * a.dys.h + d;
     T* dx = reinterpret_cast<T*>(a.y) + b * a.ys.b + h * a.ys.h + d;
-    for (int t = t0; t < te; t += U) {
+    // A token of the strip (OWN), or one after it, of which dx only needs g: left out of dw by a product with 0, the rows of the
+    // window would carry an infinity into taps that do not read them.
+    const auto token = [&](const vec& xin, const vec& gin, int tt, auto is_own) {
+      constexpr bool OWN = decltype(is_own)::value;
+      const bool real = OWN || tt < a.T;
+      float o[V];
+#pragma unroll
+      for (int k = 0; k < V; ++k) {
+#pragma unroll
+        for (int j = 0; j < K - 1; ++j) {
+          x[j][k] = x[j + 1][k];
+          g[j][k] = g[j + 1][k];
+        }
+        x[K - 1][k] = elem<T, V>(xin, k);
+        float gk = real ? elem<T, V>(gin, k) : 0.f;
+        if constexpr (SILU) {
+          float s = bias[k];
+#pragma unroll
+          for (int j = 0; j < K; ++j) s += w[j][k] * x[j][k];
+          const float sg = sigmoid<T>(s);
+          gk = real ? gk * (sg * (1.f + s * (1.f - sg))) : 0.f;
+        }
+        g[K - 1][k] = gk;
+        if constexpr (OWN) {
+          dw[K][k] += gk;
+#pragma unroll
+          for (int j = 0; j < K; ++j) dw[j][k] += x[j][k] * gk;
+        }
+        // g[j] is g_{tt-K+1+j}: dx_{tt-K+1} = sum_j w_{K-1-j} g[j]
+        o[k] = 0.f;
+#pragma unroll
+        for (int j = 0; j < K; ++j) o[k] += w[K - 1 - j][k] * g[j][k];
+      }
+      if (tt - K + 1 >= t0) store_v<T, V>(dx + (long long)(tt - K + 1) * a.ys.t, o, from);
+    };
+    for (int t = t0; t < t1; t += U) {
       vec in[U], gy[U];
 #pragma unroll
       for (int u = 0; u < U; ++u) {
-        const int tt = min(t + u, a.T - 1);
+        const int tt = min(t + u, t1 - 1);
         in[u] = *reinterpret_cast<const vec*>(xp + (long long)tt * a.xs.t);
         gy[u] = *reinterpret_cast<const vec*>(dy + (long long)tt * a.dys.t);
       }
 #pragma unroll
       for (int u = 0; u < U; ++u) {
-        const int tt = t + u;
-        if (tt >= te) break;
-        const bool real = tt < a.T, own = tt < t1;
-        float o[V];
-#pragma unroll
-        for (int k = 0; k < V; ++k) {
-#pragma unroll
-          for (int j = 0; j < K - 1; ++j) {
-            x[j][k] = x[j + 1][k];
-            g[j][k] = g[j + 1][k];
-          }
-          x[K - 1][k] = elem<T, V>(in[u], k);
-          float gk = real ? elem<T, V>(gy[u], k) : 0.f;
-          if constexpr (SILU) {
-            float s = bias[k];
-#pragma unroll
-            for (int j = 0; j < K; ++j) s += w[j][k] * x[j][k];
-            const float sg = sigmoid<T>(s);
-            gk = real ? gk * (sg * (1.f + s * (1.f - sg))) : 0.f;
-          }
-          g[K - 1][k] = gk;
-          if (own) {  // the whole wave; a product with 0 would carry an infinity of a strip's last rows into other taps
-            dw[K][k] += gk;
-#pragma unroll
-            for (int j = 0; j < K; ++j) dw[j][k] += x[j][k] * gk;
-          }
-          // g[j] is g_{tt-K+1+j}: dx_{tt-K+1} = sum_j w_{K-1-j} g[j]
-          o[k] = 0.f;
-#pragma unroll
-          for (int j = 0; j < K; ++j) o[k] += w[K - 1 - j][k] * g[j][k];
-        }
-        if (tt - K + 1 >= t0) store_v<T, V>(dx + (long long)(tt - K + 1) * a.ys.t, o, from);
+        if (t + u >= t1) break;
+        token(in[u], gy[u], t + u, std::true_type());
       }
     }
+    vec in[K - 1], gy[K - 1];
+#pragma unroll
+    for (int u = 0; u < K - 1; ++u) {
+      const int tt = min(t1 + u, a.T - 1);
+      in[u] = *reinterpret_cast<const vec*>(xp + (long long)tt * a.xs.t);
+      gy[u] = *reinterpret_cast<const vec*>(dy + (long long)tt * a.dys.t);
+    }
+#pragma unroll
+    for (int u = 0; u < K - 1; ++u) token(in[u], gy[u], t1 + u, std::false_type());
   }
   float* part = a.part + (((size_t)b * gridDim.y + blockIdx.y) * a.H + h) * (K + 1) * a.D;
 #pragma unroll

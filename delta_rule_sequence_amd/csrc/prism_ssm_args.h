@@ -45,11 +45,11 @@ struct SsmStepArgs {
   void* y;
 };
 
-// Channels per thread of the convolution: V, or 1 where V would leave more than three quarters of a wave without any.
-// One strip per wave; at 16 x 12000 x 64, V against 1: 44 and 13 us (bf16, V 8), 23 and 17 (f32, V 4), backward 60 and
-// 30, 56 and 33; at 16 x 4800 x 160: 21 and 21, 17 and 20, 31 and 32, 39 and 36; at 400 channels V leads by a tenth or
-// more.
-template <int V> inline int conv_group(int D) { return D > 16 * V ? V : 1; }
+// Channels per thread of the convolution: V, or 1 where V would leave more than half of a wave without any.  One strip per
+// wave.  16 x 768000 / D x D, V against 1, us: forward bf16 (V 8) 45 and 14 at 64 channels, 20 and 16 at 160, 14.6 and 13.7 at 256,
+// 13.5 and 13.6 at 320, 13.2 and 15.7 at 400; f32 (V 4) 27 and 17 at 64, 18 and 17 at 128, 17 and 19 at 160, 19 and 21 at 400;
+// backward (V 4) bf16 55 and 31, 33 and 28, 30 and 31, 25 and 31; f32 62 and 40, 42 and 38, 41 and 41, 40 and 42.
+template <int V> inline int conv_group(int D) { return D > 32 * V ? V : 1; }
 
 struct ConvArgs {
   const void *x, *dy;

@@ -1,6 +1,7 @@
 """The ends of the state space layer's ranges on the GPU: the longest sequences, the last token."""
 import pytest
 
+from tests import test_layer_edges_gpu as edges
 from tests.conftest import gpu_available
 from tests.test_layer_gpu import Rng
 
@@ -62,3 +63,9 @@ def test_conv_infinity_in_the_last_token(prism, dt, D, T):
         assert torch.equal(g["dconv_w"][:, :-1], ref["dconv_w"][:, :-1])
         assert torch.equal(g["dx"], ref["dx"]) and torch.equal(g["dbias"], ref["dbias"])
         assert not bool(torch.isfinite(g["dconv_w"][:, -1]).any())
+
+
+@pytest.mark.parametrize("dt,D", [("bf16", 256), ("bf16", 257), ("bf16", 264), ("f32", 128), ("f32", 129), ("f32", 132), ("bf16", 132)])
+def test_conv_on_both_sides_of_the_narrow_form(prism, dt, D):
+    """The last width whose lanes take a channel each, and the first ones that take a group, whole and with channels left over."""
+    edges.test_conv_odd_widths_and_starts(prism, dt, D)

@@ -54,7 +54,7 @@ using namespace prism;
 constexpr int kChunk = 64;       // tokens per chunk of the scan (ssm::Q)
 constexpr size_t kCUs = 256;     // compute units of an MI355X
 constexpr int kMaxWidth = 1 << 26;  // channels of the convolution and the norm: the launches' 32-bit thread counts
-constexpr int kFold = 8;         // most segments whose entering states their readers form
+constexpr int kFold = 8;         // most segments whose entering states their readers form (bfloat16)
 
 size_t elem(prism_dtype dt) { return dt == PRISM_BF16 ? 2 : 4; }
 bool known(prism_dtype dt) { return dt == PRISM_F32 || dt == PRISM_BF16; }
@@ -138,15 +138,15 @@ prism_status ssm_plan(int B, int H, int G, int T, int N, int P, prism_dtype ty, 
   pl->nch = (int)(((long long)T + kChunk - 1) / kChunk);
   // Segments until the device is full: each costs a state in the workspace and a second read of its inputs; up to kFold of
   // them the passes form their entering states themselves, more take a scan over them.  Forward: two workgroups of two
-  // heads per CU and some more, since a batch may be ragged (8 x 24 x 2048 tokens, N = 128: 127 us with 2 segments, 93 with
-  // 4, 86 with 5, 87 with 6, 91 with 8, but ragged 84 with 5 and 78 with 6; 32 x 8 x 1024: 46 with 4, 54 with 8), no more
-  // than those two per CU where the scan comes on top (8 x 12: 57 with 8, 66 with 11; 2 x 4 x 16384, N = 64: 39 with 64, 35
-  // with 128).  Half as many for float32 with a scan (4 x 8 x 2048, N = 64: 52 with 16, 57 with 32; without one not: 8 x 12 x
-  // 2048, N = 128: 296 with 5, 251 with 8) and for the backward, whose two directions fill the device sooner (8 x 12 x 2048:
-  // 165 with 5, 176 with 8; 2 x 4 x 16384: 99 with 64, 109 with 128) and which takes one rather than two (8 x 24 x 2048: 325
-  // and 339; 32 x 8 x 1024: 132 and 143).
+  // heads per CU and some more, since a batch may be ragged (8 x 24 x 2048 tokens, N = 128: 148 us with 2 segments, 110 with
+  // 4, 97 with 5, 99 with 6, 104 with 8, but ragged 92 with 5, 86 with 6, 94 with 8; 32 x 8 x 1024: 69 with 4, 84 with 8), no
+  // more than those two per CU where the scan comes on top (8 x 12 x 2048: 62 with 8, 72 with 11; 2 x 4 x 16384, N = 64: 42 with
+  // 64, 39 with 128).  Half as many for float32 where they are more than kFold (4 x 8 x 2048, N = 64: 55 with 16, 59 with 32; else
+  // not: 8 x 12 x 2048, N = 128: 317 with 5, 283 with 8) and for the backward, whose two directions fill the device sooner (8 x 12 x
+  // 2048: 191 with 5, 204 with 8; 2 x 4 x 16384: 110 with 64, 125 with 128) and which takes one rather than two (8 x 24 x 2048:
+  // 338 and 354; 32 x 8 x 1024: 224 and 244).
   // Least chunks of a segment: two for bfloat16; a float32 chunk takes longer than a segment costs (3 x 6 x 509 tokens,
-  // N = P = 32: 30 us with two, 18 with one).
+  // N = P = 32: a call of 29 us with two, 26 with one).
   const int least = ty == PRISM_BF16 || pl->nch <= 2 ? 2 : 1;
   const size_t bh = (size_t)B * pl->HV;
   const auto cut = [&](size_t want) {
@@ -170,9 +170,9 @@ prism_status ssm_plan(int B, int H, int G, int T, int N, int P, prism_dtype ty, 
   if (bwd) {
     // The gradient pass: a workgroup walks per_split of a group's virtual heads, and loads and sums outside the heads cost
     // it about one more.  Splits for the least time over the rounds that the device needs; a CU holds one workgroup, or two
-    // of float32 with small tiles.  (float32, 24 heads of 128 in 4 groups, 2464 tokens, N = 16: 147 us with 2 splits, 117 with
-    // 3, 124 with 4; 2 x 8 of 64, N = 128, 1733 tokens: 130 with 4, 145 with 8;
-    // bfloat16, 3 x 8 of 64, N = 64, 4000 tokens: 96 with 2, 85 with 4.)
+    // of float32 with small tiles.  (float32, 24 heads of 128 in 4 groups, 2464 tokens, N = 16: 157 us with 2 splits, 124 with
+    // 3, 150 with 4; 16 heads of 64 in 2 groups, N = 128, 1733 tokens: 175 with 2, 125 with 4, 141 with 8;
+    // bfloat16, 3 x 8 of 64, N = 64, 4000 tokens: 95 with 1, 103 with 2, 102 with 4.)
     const unsigned per_group = (unsigned)(pl->HV / G);
     const size_t units = (size_t)pl->nch * B * G, slots = ty == PRISM_F32 && N + pl->PW <= 96 ? 2 * kCUs : kCUs;
     size_t least_time = SIZE_MAX;
@@ -405,8 +405,8 @@ prism_status prism_norm_fwd(const void* x, long long x_stride, const void* resid
 }
 
 // Workgroups of the backward: each sums its rows' share of dweight before the shares are joined.  Four rows or more to a
-// workgroup, as long as every CU has one: a share is written and read again (1000 x 8192 bfloat16: 24 us with 256 shares, 40
-// with 1000; gated 32 and 56; 2000 x 3000 float32: 24 with 500, 25 with 1024).
+// workgroup, as long as every CU has one: a share is written and read again (1000 x 8192 bfloat16: 22 us with 256 shares, 39
+// with 1000; gated 29 and 52; 2000 x 3000 float32: 21.1 with 500, 21.4 with 1024, 21.8 with 256).
 static int norm_blocks(int rows, int D, prism_dtype dt) {
   const size_t pieces = ((size_t)D * elem(dt) + 15) / 16;
   const size_t at_once = pieces <= 8 ? 32 : pieces <= 16 ? 16 : pieces <= 32 ? 8 : pieces <= 256 ? 4 : 1;  // rows of a workgroup

@@ -9,8 +9,8 @@
 // its neighbour has not (the history may be written in place, so no value may come from two threads).
 //
 // Measured on 8 x 2048 x 1792 bfloat16, K = 4, silu: forward (ragged lengths) 13 to 15 us, 3.9 to 4.5 TB/s where a
-// copy of 1 GiB makes 5.2; backward 42 us and 4 for the sum of the shares, 3.8 TB/s: it forms silu' again, about 30 us of vector
-// instructions beside its loads.  One token of 4 x 896: 2.6 us, a launch.
+// copy of 1 GiB makes 5.2; backward 42 us and 4 for the sum of the shares, 3.8 TB/s: it forms silu' again, 24 us of vector
+// instructions beside its loads.  One token of 4 x 896: 2.7 us, a launch.
 #pragma once
 #include <type_traits>
 

@@ -12,8 +12,10 @@
 // float32 accuracy after long decays.
 //
 // Products run on the float32 matrix instructions (153 TFLOP/s in a library product of 8192^3).  Measured: forward of
-// 3 x 6 x 509 tokens, N = P = 32: passes of 7, 3 and 11 us; backward of 2 x 6 x 333: 7, 3, 6, 17 and 4 us.  Small
-// calls: launches and one chunk's chain of products bound them.
+// 3 x 6 x 509 tokens, N = P = 32: passes of 7, 3 and 11 us; backward of 2 x 6 x 333: 7, 3, 3, 19 and 4 us: launches and one
+// chunk's chain of products bound small calls.  8 x 12 x 2048, N = 128, P = 64: forward 283 us, backward 720, where their products
+// take 42 and 105 at that rate: the sweep's 104 KB of LDS leave a CU one workgroup of 4 waves, whose rows pass registers
+// between two barriers with nothing else in flight, and every head reads B and C again.
 #pragma once
 #include "prism_ssm_args.h"
 #include "prism_tile.h"

@@ -8,21 +8,24 @@
 //   * the score matrix M and the state as it is read out into y pass as two bfloat16 parts, off by 2^-16 at most, and y is
 //     rounded to bfloat16 once (one part each: y was off by 0.0023 of its size for the 0.0017 of that one rounding; the second
 //     parts cost 8 of 61 us in the sweep of 8 x 24 x 2048 tokens);
-//   * so do M, the summed score gradients and R on their way into dx, dB and dC;
+//   * so do M, the summed score gradients and R on their way into dx, dB and dC (2 us of 190 for the backward of 8 x 12 x 2048);
 //   * ddt and dA are float32 results: H and R enter the products behind them as three parts, and <H, R> in float32 (two parts:
-//     7 us less at 8 x 12 x 2048, but ddt off by 1e-6 for 2e-7); the sums of score terms that cancel in dA run in float64 (10
-//     us, for dA off by 4e-6 at most over 40 draws of two heads where float32 sums leave 3e-5).
+//     5 us less there, but ddt off by 1e-6 for 1e-7); the sums of score terms that cancel in dA run in float64 (3 us there,
+//     for dA off by 4e-6 at most over 40 draws of two heads where float32 sums leave 3e-5).
 //
 // Waves own 16 columns p of the state in MFMA accumulators from chunk to chunk; an accumulator tile is the operand of
 // the readout without passing LDS (rows of a tile pair are the k values of one MFMA, in the order of Mma::koff).
 // Tiles lie in LDS without padding, their 16-byte pieces permuted inside a row (Tile::at) so that row reads and
 // transposing reads both touch all banks evenly.
 //
-// Measured, N = 128, P = 64: forward of 8 x 24 x 2048 ragged tokens 31 us for the segments' ends and 52 for the sweep;
-// backward of 8 x 12 x 2048: 35 us for the ends, 52 saving states, 110 for the gradients.  N = P = 64, 2 x 4 x 16384: 13
-// and 18 us, and 8 for the scan over 128 segments.  Two waves per SIMD at most (state tiles, operands and scores take
-// all 256 registers), so the sweep is bound by latency: its matrix unit is busy 11 % of the time, vector instructions
-// 22 %, LDS 18 %.  Saving writes 201 MB at 3.9 TB/s, and the gradients read them again.
+// Measured, N = 128, P = 64: forward of 8 x 24 x 2048 ragged tokens 30 us for the segments' ends and 60 for the sweep;
+// backward of 8 x 12 x 2048: 35 us for the ends, 52 saving states, 110 to 113 for the gradients.  N = P = 64, 2 x 4 x 16384: 13
+// and 20 us, and 8 for the scan over 128 segments.  Two waves per SIMD at most (state tiles, operands and scores take
+// all 256 registers for N = 128, 194 for N = 64), so a sweep waits for latencies: over all SIMDs its matrix unit is busy 11 %
+// of the time, vector instructions 25 %, LDS 16 %; in a ragged batch the XCD with the longest sequence (see Place) works 1.8
+// times the mean.
+// Saving writes 201 MB at 3.9 TB/s, and the gradients read them again; these issue vector instructions 41 % of the time (the
+// splits into parts, float64 sums, LDS places), with the matrix unit busy 11 %, LDS 25 %, and the waves waiting for 48 %.
 #pragma once
 #include "prism_ssm.h"
 
@@ -190,7 +193,8 @@ __device__ __forceinline__ size_t saved_at(int pt, int nt) {
 // they take neighbouring numbers; the hardware deals workgroups out to the eight XCDs in turn, so each XCD is given a
 // range of numbers of its own, and reads those rows into its L2 once.  (Dealing single units out to the XCDs instead:
 // the state pass of 8 x 12 x 2048 tokens 70 us, this way 61; a batch's segments on several XCDs, for the balance of ragged
-// batches: 69, since a segment reads the ends of those before it.)
+// batches: 69, since a segment reads the ends of those before it.)  A batch of eight thus lies one sequence to an XCD: ragged,
+// the call lasts as long as its longest sequence, 1.8 times the mean for lengths uniform in 0 .. T.
 struct Place {
   int b, hv0, seg;
 };

@@ -453,9 +453,10 @@ prism_status prism_fwd_noalloc(const void* q, const void* k, const void* v,
  * and written in place.  Strides must be positive where their axis is longer than 1; rows of
  * an output must not overlap, and outputs share no memory with inputs but where it is said.
  * Ownership, streams and errors as prism_fwd; the stream must belong to the current device.
- * Non-finite inputs reach the outputs they enter; in the scan a non-finite row of x (of dy in
- * its backward) may also reach the other tokens of its chunk of 64.  Rows past a sequence's
- * length never reach anything. */
+ * Non-finite inputs reach the outputs they enter; in the scan a non-finite row of x, and in its
+ * backward one of any input, may also reach the other tokens of its chunk of 64.  Rows past a
+ * sequence's length never reach anything.  Sequences have up to 2^31 - 4097 tokens; sizes past this and
+ * the bounds below return PRISM_ERR_UNSUPPORTED. */
 typedef struct {
   long long b, h, t;
 } prism_strides;
@@ -469,7 +470,8 @@ typedef struct {
  *   y       [B, H, T, D] dtype dt, strided (output)
  *   conv_out[B, H, K-1, D] dtype dt (output): the last K-1 rows of [conv_in; x up to the length];
  *           NULL = not written.  May be the same buffer as conv_in.
- * Any D from 1 to 2^26 and any strides and alignment of whole elements.  Sums in float32. */
+ * Any D from 1 to 2^26 and any strides and alignment of whole elements; B * H <= 65535 and
+ * B * H * D < 2^31.  Sums in float32. */
 prism_status prism_conv_fwd(const void* x, const prism_strides* x_strides, const float* conv_w, const float* bias,
                             const void* conv_in, const int* lens, int B, int H, int T, int D, int K, int silu,
                             prism_dtype dt, void* y, const prism_strides* y_strides, void* conv_out,
@@ -528,7 +530,8 @@ prism_status prism_ssm_fwd(const void* x, const prism_strides* x_strides, const 
  *   float32, summed over batches and tokens.  Every sum has a fixed order.
  * Supported and precision as prism_ssm_fwd (rows of dy, dx, dBm and dCm too): with PRISM_BF16 dx, dBm and
  * dCm are off by little more than their rounding, and the states behind ddt, dA and ddt_bias keep their
- * float32 digits.  Workspace: prism_ssm_bwd_workspace_bytes. */
+ * float32 digits.  B * T * (G * N / 4 + H) and 8 * (T + 64) stay below 2^32 - 1024 * (H + 1).
+ * Workspace: prism_ssm_bwd_workspace_bytes. */
 size_t prism_ssm_bwd_workspace_bytes(int B, int H, int G, int T, int N, int P, prism_dtype ty);
 prism_status prism_ssm_bwd(const void* x, const prism_strides* x_strides, const void* Bm,
                            const prism_strides* b_strides, const void* Cm, const prism_strides* c_strides,
@@ -540,7 +543,8 @@ prism_status prism_ssm_bwd(const void* x, const prism_strides* x_strides, const 
                            float* ddt_bias, void* workspace, size_t workspace_bytes, hipStream_t stream);
 
 /* One token of the scan, the state S [B, H, N, P] float32 updated in place: x [B, H, P], Bm, Cm
- * [B, G, N] (strided; t is not read), dt [B, H] float32 (strided), y [B, H, P] dense. */
+ * [B, G, N] (strided; t is not read), dt [B, H] float32 (strided), y [B, H, P] dense.  B * H < 2^23; S on a
+ * 16-byte boundary. */
 prism_status prism_ssm_step(const void* x, const prism_strides* x_strides, const void* Bm,
                             const prism_strides* b_strides, const void* Cm, const prism_strides* c_strides,
                             const float* dt, const prism_strides* dt_strides, const float* dt_bias, const float* A,

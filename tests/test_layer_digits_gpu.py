@@ -68,7 +68,7 @@ def rounded_once(name, got, ref, size):
 
 
 # every width pair with an even and an odd number of heads per group, one to many segments, lengths off the chunk
-SCAN = [(1, 2, 1, 70, n, p) for n in (16, 32, 64, 128) for p in (16, 32, 64, 128)] + \
+SCAN = [(1, h, 1, 70, n, p) for h in (2, 3) for n in (16, 32, 64, 128) for p in (16, 32, 64, 128)] + \
        [(2, 3, 1, 333, 64, 64), (1, 5, 1, 700, 128, 64), (2, 9, 3, 130, 16, 32), (1, 1, 1, 3000, 16, 16), (2, 6, 2, 400, 32, 128), (1, 2, 2, 1, 64, 64)]
 
 

@@ -109,8 +109,9 @@ def load_library() -> ctypes.CDLL:
     lib.prism_fwd_noalloc.restype = ctypes.c_int
     lib.prism_noalloc_scratch_bytes.argtypes = []
     lib.prism_noalloc_scratch_bytes.restype = sz
-    from .layer import declare
-    declare(lib)
+    from . import attention, layer
+    layer.declare(lib)
+    attention.declare(lib)
     lib.prism_status_string.argtypes = [ctypes.c_int]
     lib.prism_status_string.restype = ctypes.c_char_p
     lib.prism_version.argtypes = []
@@ -650,13 +651,16 @@ def fwd_delta_pred(q, k, v, g, beta, W_p, W_k, W_b, conv_w, L: int, chunk: int =
     return o, S
 
 
-# ---- the state space layer (layer.py needs torch, which the functions above import on first use) ----
-_LAYER = ("conv_fwd", "conv_bwd", "conv_step", "ssm_fwd", "ssm_bwd", "ssm_step", "norm_fwd", "norm_bwd")
+# ---- the state space and attention layers (their modules need torch, which the functions above import on first use) ----
+_MODULES = {"layer": ("conv_fwd", "conv_bwd", "conv_step", "ssm_fwd", "ssm_bwd", "ssm_step", "norm_fwd", "norm_bwd"),
+            "attention": ("attn_fwd",)}
 
 
 def __getattr__(name):
-    if name not in _LAYER:
-        raise AttributeError(f"module {__name__!r} has no attribute {name!r}")
-    from . import layer
-    globals().update({n: getattr(layer, n) for n in _LAYER})
-    return globals()[name]
+    import importlib
+    for module, names in _MODULES.items():
+        if name in names:
+            m = importlib.import_module("." + module, __name__)
+            globals().update({n: getattr(m, n) for n in names})
+            return globals()[name]
+    raise AttributeError(f"module {__name__!r} has no attribute {name!r}")

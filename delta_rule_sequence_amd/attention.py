@@ -1,0 +1,71 @@
+"""The attention layer: norm and rotation of queries and keys, softmax attention of prompts with its gradients, the
+paged cache and the attention of new tokens over it.
+
+Argument marshalling only, as the rest of the binding; the operators are described in include/prism.h.  Tensors, views,
+streams and devices as in the state space layer's calls (layer.py).
+"""
+from __future__ import annotations
+
+import ctypes
+import math
+
+import torch
+
+from . import PrismError
+from .layer import _F32, _I32, _Strides, _dense, _dtype, _gpu, _like, _on_stream, _run, _sizes, _strides, _tensor
+
+
+def declare(lib) -> None:
+    """Argument types of the layer's functions."""
+    p, i, f, sz = ctypes.c_void_p, ctypes.c_int, ctypes.c_float, ctypes.c_size_t
+    st = ctypes.POINTER(_Strides)
+    prompt = [p, st, p, st, p, st]                              # q, k, v with strides
+    sigs = {
+        "prism_attn_fwd": prompt + [p, p, i] + [i] * 5 + [f, i, i, i, p, st, p, p],
+    }
+    for name, args in sigs.items():
+        getattr(lib, name).argtypes = args
+        getattr(lib, name).restype = i
+
+
+# ---- prompts -----------------------------------------------------------------------------------
+def _prompt(q, k, v, lens, starts, scale, causal, window):
+    dev = _gpu(q, "q")
+    if q.dim() != 4:
+        raise PrismError("q must have 4 axes")
+    if not isinstance(k, torch.Tensor) or k.dim() != 4:
+        raise PrismError("k must be a tensor [B, G, T, D]")
+    B, H, T, D = q.shape
+    G = k.shape[1]
+    _sizes(B, H, G, T, D)
+    _tensor("q", q, q.shape, q.dtype, dev)
+    _tensor("k", k, (B, G, T, D), q.dtype, dev)
+    _tensor("v", v, (B, G, T, D), q.dtype, dev)
+    S = 0
+    if starts is not None:
+        if not isinstance(starts, torch.Tensor) or starts.dim() != 1 or starts.shape[0] < 2:
+            raise PrismError("starts must be a tensor [S + 1]")
+        S = starts.shape[0] - 1
+        _sizes(S)
+    p_lens, p_starts = _dense("lens", lens, (B,), _I32, dev), _dense("starts", starts, (S + 1,), _I32, dev)
+    scale = 1 / math.sqrt(D) if scale is None and D else scale
+    return dev, B, H, G, T, D, (p_lens, p_starts, S, B, H, G, T, D, scale, bool(causal), window, _dtype(q))
+
+
+@_on_stream
+def attn_fwd(q, k, v, scale=None, causal=True, window=0, lens=None, starts=None, out=None):
+    """o, lse = attn_fwd(q, k, v): softmax attention of q [B,H,T,D] over k, v [B,G,T,D], each group of H / G heads sharing
+    a key head; o [B,H,T,D] in q's dtype, lse [B,H,T] float32.  scale: 1 / sqrt(D) if not given.  causal: token i
+    sees tokens up to i; window: the last `window` of them only (0: all).  lens [B] int32: tokens of each sequence; or
+    starts [S + 1] int32 with B = 1: sequence s is tokens starts[s] .. starts[s + 1] - 1.  Rows of no sequence keep what
+    out = (o, lse) holds (new tensors hold nothing defined there)."""
+    dev, B, H, G, T, D, args = _prompt(q, k, v, lens, starts, scale, causal, window)
+    if out is None:
+        o, lse = _like(q), torch.empty((B, H, T), dtype=_F32, device=dev)
+    else:
+        if not isinstance(out, (tuple, list)) or len(out) != 2:
+            raise PrismError("out must be two tensors (o, lse)")
+        o, lse = _tensor("o", out[0], (B, H, T, D), q.dtype, dev), out[1]
+    _run("prism_attn_fwd", dev, q.data_ptr(), _strides(q), k.data_ptr(), _strides(k), v.data_ptr(), _strides(v), *args,
+         o.data_ptr(), _strides(o), _dense("lse", lse, (B, H, T), _F32, dev))
+    return o, lse

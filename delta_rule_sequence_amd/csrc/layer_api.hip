@@ -5,9 +5,9 @@
 
 #include <algorithm>
 #include <climits>
-#include <stdint.h>
 
 #include "prism.h"
+#include "prism_checks.h"
 #include "prism_ssm_args.h"
 
 namespace prism {
@@ -50,76 +50,11 @@ prism_status launch_ssm_step(prism_dtype ty, int N, int P, int B, const SsmStepA
 namespace {
 
 using namespace prism;
+using namespace prism::checks;
 
 constexpr int kChunk = 64;       // tokens per chunk of the scan (ssm::Q)
-constexpr size_t kCUs = 256;     // compute units of an MI355X
 constexpr int kMaxWidth = 1 << 26;  // channels of the convolution and the norm: the launches' 32-bit thread counts
 constexpr int kFold = 8;         // most segments whose entering states their readers form (bfloat16)
-
-size_t elem(prism_dtype dt) { return dt == PRISM_BF16 ? 2 : 4; }
-bool known(prism_dtype dt) { return dt == PRISM_F32 || dt == PRISM_BF16; }
-bool width_ok(int n) { return n == 16 || n == 32 || n == 64 || n == 128; }
-
-// A workspace layout: offsets of 256-byte aligned regions; total stays SIZE_MAX after an overflow.
-struct Layout {
-  size_t total = 0;
-  size_t add(size_t count, size_t size) {
-    const size_t at = total;
-    if (total == SIZE_MAX || (size != 0 && count > (SIZE_MAX / 2 - total) / size)) {
-      total = SIZE_MAX;
-      return 0;
-    }
-    total += (count * size + 255) / 256 * 256;
-    return at;
-  }
-  bool ok() const { return total != SIZE_MAX; }
-};
-
-bool aligned16(const void* p) { return ((uintptr_t)p & 15) == 0; }
-
-// Strides of a [B, H, T, width] tensor: the caller's, or dense ones.  Checks signs and that the largest offset fits
-// in 63 bits.
-bool make_strides(const prism_strides* given, int B, int H, int T, int width, prism_strides* out) {
-  if (given == nullptr) {
-    out->t = width;
-    out->h = (long long)T * width;
-    if (out->h > LLONG_MAX / 8 / H) return false;
-    out->b = out->h * H;
-  } else {
-    *out = *given;
-    if ((B > 1 && out->b <= 0) || (H > 1 && out->h <= 0) || (T > 1 && out->t <= 0)) return false;
-    if (B == 1) out->b = 0;
-    if (H == 1) out->h = 0;
-    if (T == 1) out->t = width;
-  }
-  const long long lim = LLONG_MAX / 64;
-  return out->b <= lim / B && out->h <= lim / H && out->t <= lim / T;
-}
-
-// Whether rows of an output [B, H, T, width] cannot overlap: sorted by stride, each axis steps over the ones below.
-bool rows_apart(const prism_strides& s, int B, int H, int T, int width) {
-  struct Axis { long long st; long long n; } ax[3] = {{s.b, B}, {s.h, H}, {s.t, T}};
-  std::sort(ax, ax + 3, [](const Axis& p, const Axis& q) { return p.st < q.st; });
-  long long span = width;
-  for (const Axis& a : ax) {
-    if (a.n == 1) continue;
-    if (a.st < span) return false;
-    span += a.st * (a.n - 1);
-  }
-  return true;
-}
-
-// Rows of the scan's tensors: on 16-byte boundaries, not overlapping, and at most 16 MB apart (a chunk's rows are
-// addressed with 32-bit byte offsets).
-bool rows16(const void* p, const prism_strides& s, prism_dtype dt);
-bool scan_rows(const void* p, const prism_strides& s, int width, prism_dtype dt) {
-  return rows16(p, s, dt) && s.t >= width && s.t * (long long)elem(dt) <= (1 << 24);
-}
-
-bool rows16(const void* p, const prism_strides& s, prism_dtype dt) {
-  const long long e = (long long)elem(dt);
-  return aligned16(p) && s.b * e % 16 == 0 && s.h * e % 16 == 0 && s.t * e % 16 == 0;
-}
 
 // ---- scan ------------------------------------------------------------------------------------
 struct SsmPlan {
@@ -195,8 +130,6 @@ prism_status ssm_plan(int B, int H, int G, int T, int N, int P, prism_dtype ty, 
   pl->total = std::max<size_t>(ly.total, 256);
   return PRISM_OK;
 }
-
-template <class P> P* at(void* ws, size_t off) { return reinterpret_cast<P*>(reinterpret_cast<char*>(ws) + off); }
 
 // ---- convolution -------------------------------------------------------------------------------
 prism_status conv_check(int B, int H, int T, int D, int K, prism_dtype dt) {

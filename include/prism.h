@@ -580,6 +580,11 @@ prism_status prism_norm_bwd(const void* h, long long h_stride, const float* weig
                             prism_dtype dt, void* dh, void* dgate, float* dweight,
                             void* workspace, size_t workspace_bytes, hipStream_t stream);
 
+prism_status prism_attn_fwd(const void* q, const prism_strides* q_strides, const void* k, const prism_strides* k_strides,
+                            const void* v, const prism_strides* v_strides, const int* lens, const int* starts, int S,
+                            int B, int H, int G, int T, int D, float scale, int causal, int window, prism_dtype dt,
+                            void* o, const prism_strides* o_strides, float* lse, hipStream_t stream);
+
 /* A static, human-readable name of a status code. */
 const char* prism_status_string(prism_status s);
 

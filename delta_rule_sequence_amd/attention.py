@@ -12,7 +12,7 @@ import math
 import torch
 
 from . import PrismError
-from .layer import _F32, _I32, _Strides, _dense, _dtype, _gpu, _like, _on_stream, _run, _sizes, _strides, _tensor
+from .layer import _F32, _I32, _Strides, _dense, _dtype, _gpu, _like, _need, _on_stream, _run, _scratch, _sizes, _strides, _tensor
 
 
 def declare(lib) -> None:
@@ -22,10 +22,14 @@ def declare(lib) -> None:
     prompt = [p, st, p, st, p, st]                              # q, k, v with strides
     sigs = {
         "prism_attn_fwd": prompt + [p, p, i] + [i] * 5 + [f, i, i, i, p, st, p, p],
+        "prism_attn_bwd": prompt + [p, st, p, p, st, p, p, i] + [i] * 5 + [f, i, i, i, p, st, p, st, p, st, p, sz, p],
     }
     for name, args in sigs.items():
         getattr(lib, name).argtypes = args
         getattr(lib, name).restype = i
+    for name, n in (("prism_attn_bwd", 6),):
+        fn = getattr(lib, name + "_workspace_bytes")
+        fn.argtypes, fn.restype = [i] * n, sz
 
 
 # ---- prompts -----------------------------------------------------------------------------------
@@ -69,3 +73,30 @@ def attn_fwd(q, k, v, scale=None, causal=True, window=0, lens=None, starts=None,
     _run("prism_attn_fwd", dev, q.data_ptr(), _strides(q), k.data_ptr(), _strides(k), v.data_ptr(), _strides(v), *args,
          o.data_ptr(), _strides(o), _dense("lse", lse, (B, H, T), _F32, dev))
     return o, lse
+
+
+def _zeros_like(t):
+    return _like(t).zero_()
+
+
+@_on_stream
+def attn_bwd(q, k, v, o, lse, do, scale=None, causal=True, window=0, lens=None, starts=None, out=None, workspace=None):
+    """Gradients of <do, o> for attn_fwd with the same arguments, from its o and lse: a dict of dq, dk, dv in q's dtype
+    (out: three tensors to write them to).  Rows of no sequence keep what `out` holds (new gradients: zero)."""
+    dev, B, H, G, T, D, args = _prompt(q, k, v, lens, starts, scale, causal, window)
+    _tensor("o", o, (B, H, T, D), q.dtype, dev)
+    _tensor("do", do, (B, H, T, D), q.dtype, dev)
+    if lse is None:
+        raise PrismError("lse is required")
+    if out is None:
+        new = _like if lens is None and starts is None else _zeros_like
+        dq, dk, dv = new(q), new(k), new(v)
+    else:
+        if not isinstance(out, (tuple, list)) or len(out) != 3:
+            raise PrismError("out must be three tensors (dq, dk, dv)")
+        dq, dk, dv = (_tensor(n, t, s.shape, q.dtype, dev) for n, t, s in zip(("dq", "dk", "dv"), out, (q, k, v)))
+    ws = _scratch(workspace, _need("prism_attn_bwd", B, H, G, T, D, args[-1]), dev)
+    _run("prism_attn_bwd", dev, q.data_ptr(), _strides(q), k.data_ptr(), _strides(k), v.data_ptr(), _strides(v), o.data_ptr(),
+         _strides(o), _dense("lse", lse, (B, H, T), _F32, dev), do.data_ptr(), _strides(do), *args, dq.data_ptr(), _strides(dq),
+         dk.data_ptr(), _strides(dk), dv.data_ptr(), _strides(dv), ws.data_ptr(), ws.numel())
+    return {"dq": dq, "dk": dk, "dv": dv}

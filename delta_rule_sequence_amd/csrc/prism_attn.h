@@ -8,6 +8,7 @@
 // operand of O^T = V^T P^T without leaving their lane.  Q stays in registers; tiles of K and V go through LDS, read by
 // rows (K) and transposed on the way (V).
 #pragma once
+#include <climits>
 #include <type_traits>
 
 #include "prism_attn_args.h"
@@ -139,9 +140,9 @@ struct Seq {
 
 __device__ __forceinline__ int uniform(int x) { return __builtin_amdgcn_readfirstlane(x); }
 
-// Tile `slot` of all sequences' tiles of `rows` rows, a sequence's last tile first (causal: the longest).  With starts, a
-// wave adds up the tiles of 64 sequences at a time.
-__device__ __forceinline__ Seq find_tile(const AttnArgs& a, int slot, int rows) {
+// Tile `slot` of all sequences' tiles of `rows` rows, a sequence's last tile first if `back`.  With starts, a wave adds up
+// the tiles of 64 sequences at a time.
+__device__ __forceinline__ Seq find_tile(const AttnArgs& a, int slot, int rows, bool back) {
   Seq s;
   s.id = -1;
   if (a.starts == nullptr) {
@@ -150,7 +151,8 @@ __device__ __forceinline__ Seq find_tile(const AttnArgs& a, int slot, int rows) 
     s.first = 0;
     s.n = a.T;
     if (a.lens != nullptr) s.n = min(max(uniform(a.lens[s.b]), 0), a.T);
-    s.tile = per - 1 - (slot - s.b * per);
+    s.tile = slot - s.b * per;
+    if (back) s.tile = per - 1 - s.tile;
     if ((long long)s.tile * rows < s.n) s.id = s.b;
     return s;
   }
@@ -175,7 +177,8 @@ __device__ __forceinline__ Seq find_tile(const AttnArgs& a, int slot, int rows) 
       const int j = __ffsll((unsigned long long)past) - 1;
       s.first = __builtin_amdgcn_readlane(first, j);
       s.n = __builtin_amdgcn_readlane(n, j);
-      s.tile = __builtin_amdgcn_readlane(upto, j) - 1 - left;
+      const int end = __builtin_amdgcn_readlane(upto, j);
+      s.tile = back ? end - 1 - left : left - end + (int)(((unsigned)s.n + rows - 1) / rows);
       s.id = base + j;
       return s;
     }
@@ -210,7 +213,7 @@ __global__ __launch_bounds__(64 * NW, QT * D * (int)sizeof(T) > 256 ? 1 : 2) voi
   // heads of a group lie S G blocks apart (or G): with a multiple of 8 they share an XCD and the keys in its L2
   const int heads = a.H, slot0 = (int)(blockIdx.x / heads), pair = (int)(blockIdx.x - (unsigned)slot0 * heads);
   const int rep = a.H / a.G, head = (pair % a.G) * rep + pair / a.G, group = pair % a.G;
-  const Seq s = find_tile(a, slot0, F::kRows);
+  const Seq s = find_tile(a, slot0, F::kRows, a.causal);
   if (s.id < 0) return;
   const int tid = threadIdx.x, l = lane_id(), h = l >> 5, w = uniform(wave_id());
   const int q0 = s.tile * F::kRows, qw = q0 + w * 32 * QT;            // the block's and the wave's first query

@@ -35,5 +35,6 @@ struct AttnArgs {
 namespace host {
 // Each enqueues on `stream` and reports launch failures.
 prism_status launch_attn_fwd(prism_dtype dt, int D, AttnArgs a, hipStream_t stream);
+prism_status launch_attn_bwd(prism_dtype dt, int D, const AttnArgs& a, hipStream_t stream);
 }  // namespace host
 }  // namespace prism

@@ -585,6 +585,15 @@ prism_status prism_attn_fwd(const void* q, const prism_strides* q_strides, const
                             int B, int H, int G, int T, int D, float scale, int causal, int window, prism_dtype dt,
                             void* o, const prism_strides* o_strides, float* lse, hipStream_t stream);
 
+size_t prism_attn_bwd_workspace_bytes(int B, int H, int G, int T, int D, prism_dtype dt);
+prism_status prism_attn_bwd(const void* q, const prism_strides* q_strides, const void* k, const prism_strides* k_strides,
+                            const void* v, const prism_strides* v_strides, const void* o, const prism_strides* o_strides,
+                            const float* lse, const void* d_o, const prism_strides* do_strides,
+                            const int* lens, const int* starts, int S, int B, int H, int G, int T, int D, float scale,
+                            int causal, int window, prism_dtype dt, void* dq, const prism_strides* dq_strides,
+                            void* dk, const prism_strides* dk_strides, void* dv, const prism_strides* dv_strides,
+                            void* workspace, size_t workspace_bytes, hipStream_t stream);
+
 /* A static, human-readable name of a status code. */
 const char* prism_status_string(prism_status s);
 

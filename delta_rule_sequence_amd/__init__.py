@@ -653,7 +653,7 @@ def fwd_delta_pred(q, k, v, g, beta, W_p, W_k, W_b, conv_w, L: int, chunk: int =
 
 # ---- the state space and attention layers (their modules need torch, which the functions above import on first use) ----
 _MODULES = {"layer": ("conv_fwd", "conv_bwd", "conv_step", "ssm_fwd", "ssm_bwd", "ssm_step", "norm_fwd", "norm_bwd"),
-            "attention": ("attn_fwd", "attn_bwd")}
+            "attention": ("rope_fwd", "rope_bwd", "attn_fwd", "attn_bwd", "cache_write", "attn_paged")}
 
 
 def __getattr__(name):

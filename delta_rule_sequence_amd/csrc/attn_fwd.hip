@@ -14,12 +14,13 @@ namespace {
 
 template <class T, int D, int QT, int NW, int BN, int PARTS>
 prism_status run(AttnArgs a, hipStream_t stream) {
-  using F = attn::FwdTile<T, D, QT, NW, BN, PARTS>;
+  using F = attn::FwdTile<T, D, QT, NW, BN, PARTS, attn::kPrompt>;
+  const auto kernel = attn::fwd_kernel<T, D, QT, NW, BN, PARTS, attn::kPrompt>;
   a.tiles = a.starts != nullptr ? a.T / F::kRows + a.S : a.B * ((a.T + F::kRows - 1) / F::kRows);
-  static const bool ok = hipFuncSetAttribute(reinterpret_cast<const void*>(attn::fwd_kernel<T, D, QT, NW, BN, PARTS>),
-                                             hipFuncAttributeMaxDynamicSharedMemorySize, F::kLds) == hipSuccess;
+  static const bool ok = hipFuncSetAttribute(reinterpret_cast<const void*>(kernel), hipFuncAttributeMaxDynamicSharedMemorySize,
+                                             F::kLds) == hipSuccess;
   if (!ok) return PRISM_ERR_HIP;
-  attn::fwd_kernel<T, D, QT, NW, BN, PARTS><<<dim3(a.tiles * a.H), F::kThreads, F::kLds, stream>>>(a);
+  kernel<<<dim3(a.tiles * a.H), F::kThreads, F::kLds, stream>>>(a);
   return hipGetLastError() == hipSuccess ? PRISM_OK : PRISM_ERR_HIP;
 }
 

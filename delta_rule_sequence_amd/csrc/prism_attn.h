@@ -132,6 +132,20 @@ __device__ __forceinline__ float both_sum(float x) {
   return __builtin_bit_cast(float, (unsigned)r[0]) + __builtin_bit_cast(float, (unsigned)r[1]);
 }
 
+// Rows of an accumulator tile whose columns are rows of the tensor: 4 values at a time.
+template <class T, int D>
+__device__ __forceinline__ void store_columns(char* row, const f32x16 (&acc)[D / 32], float f, int h) {
+#pragma unroll
+  for (int d = 0; d < D / 32; ++d)
+#pragma unroll
+    for (int r = 0; r < 4; ++r) {
+      T y[4];
+#pragma unroll
+      for (int u = 0; u < 4; ++u) y[u] = (T)(acc[d][4 * r + u] * f);
+      __builtin_memcpy(row + (32 * d + 8 * r + 4 * h) * (int)sizeof(T), y, sizeof(y));
+    }
+}
+
 // ---- sequences and their tiles ------------------------------------------------------------------------
 struct Seq {
   int b, first, n;     // batch, first token, tokens
@@ -188,36 +202,153 @@ __device__ __forceinline__ Seq find_tile(const AttnArgs& a, int slot, int rows, 
 }
 
 // ---- forward ------------------------------------------------------------------------------------------
+// Where the keys lie: kPrompt: rows of k and v; kCache: pages of the same type; kCache8: pages of e4m3 bytes with a scale
+// per row.
+enum Keys { kPrompt, kCache, kCache8 };
+
 // NW waves of 32 QT queries; keys in tiles of BN, two of them in LDS: a tile is stored while the one before is
 // computed on, and its successor is already on the way to registers.
-template <class T, int D, int QT, int NW, int BN, int PARTS>
+template <class T, int D, int QT, int NW, int BN, int PARTS, Keys KEYS>
 struct FwdTile {
   using R = Rows<T, D>;
   static constexpr int kThreads = 64 * NW, kRows = 32 * QT * NW;
-  static constexpr int kEach = BN * R::kPieces / kThreads;           // pieces per thread of one tile
+  static constexpr int kPieces = KEYS == kCache8 ? D / 16 : R::kPieces;    // 16-byte pieces of a row in memory
+  static constexpr int kEach = (BN * kPieces + kThreads - 1) / kThreads;   // per thread of one tile
   static constexpr int kTile = BN * R::kStride;
-  static constexpr int kLds = 4 * kTile;
-  static_assert(BN * R::kPieces % kThreads == 0, "whole pieces");
+  static constexpr int kLds = 4 * kTile + (KEYS == kCache8 ? 4 * BN * 4 : 0);
+};
+
+// Eight e4m3 values as bfloat16, exactly.
+__device__ __forceinline__ u32x4 widen8(unsigned lo, unsigned hi) {
+  typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+  u32x4 r;
+  r[0] = __builtin_bit_cast(unsigned, (bf16x2)__builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(lo, 1.f, false));
+  r[1] = __builtin_bit_cast(unsigned, (bf16x2)__builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(lo, 1.f, true));
+  r[2] = __builtin_bit_cast(unsigned, (bf16x2)__builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(hi, 1.f, false));
+  r[3] = __builtin_bit_cast(unsigned, (bf16x2)__builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(hi, 1.f, true));
+  return r;
+}
+
+// A tile's pieces of K and V (and rows' scales) between memory and LDS.
+template <class T, int D, int NT, int BN, Keys KEYS> struct KeyTile {
+  using R = Rows<T, D>;
+  using F = FwdTile<T, D, 1, NT / 64, BN, 1, KEYS>;
+  static constexpr int kPieces = F::kPieces, kEach = F::kEach, kStep = NT / kPieces;   // kStep: rows between a thread's pieces
+  static constexpr bool kPart = BN * kPieces < NT;                                     // not every thread has a piece
+  static_assert(BN * kPieces % NT == 0 || kPart, "whole pieces");
+  u32x4 k[kEach], v[kEach];
+  float scale;
+
+  __device__ __forceinline__ void load_prompt(const char* kp, const char* vp, int kst, int vst, int t, int n, int tid) {
+    const int row = tid / kPieces, at = tid % kPieces * 16;
+    const auto rk = rows_of(kp + (long long)t * BN * kst, min(n, BN), kst, R::kBytes);
+    const auto rv = rows_of(vp + (long long)t * BN * vst, min(n, BN), vst, R::kBytes);
+    if (kPart && row >= BN) return;
+#pragma unroll
+    for (int i = 0; i < kEach; ++i) k[i] = load16(rk, (row + i * kStep) * kst + at);
+#pragma unroll
+    for (int i = 0; i < kEach; ++i) v[i] = load16(rv, (row + i * kStep) * vst + at);
+  }
+  // Rows from j0 on of the sequence's pages; rows from `n` on and those of pages outside the cache are zeros.  id: the
+  // page that holds the whole tile, where pages are that large.
+  __device__ __forceinline__ void load_cache(const AttnArgs& a, const int* table, int id, int group, int j0, int n, int tid) {
+    const int row = tid / kPieces, at = tid % kPieces * 16, page = 1 << a.page_shift;
+    constexpr int kBytes = kPieces * 16;
+    if (page >= BN) {
+      const bool in = (unsigned)id < (unsigned)a.pages;
+      const size_t first = ((size_t)(in ? id : 0) * a.G + group) * page + (j0 & (page - 1));
+      const auto rk = rows_of((const char*)a.cache_k + first * kBytes, in ? min(n - j0, BN) : 0, kBytes, kBytes);
+      const auto rv = rows_of((const char*)a.cache_v + first * kBytes, in ? min(n - j0, BN) : 0, kBytes, kBytes);
+      if (!kPart || row < BN) {
+#pragma unroll
+        for (int i = 0; i < kEach; ++i) k[i] = load16(rk, (row + i * kStep) * kBytes + at);
+#pragma unroll
+        for (int i = 0; i < kEach; ++i) v[i] = load16(rv, (row + i * kStep) * kBytes + at);
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < kEach; ++i) {
+        const int j = j0 + row + i * kStep;
+        k[i] = v[i] = u32x4{0, 0, 0, 0};
+        if ((!kPart || row < BN) && j < n) {
+          const int p = table[j >> a.page_shift];
+          if ((unsigned)p < (unsigned)a.pages) {
+            const size_t r = ((size_t)p * a.G + group) * page + (j & (page - 1));
+            k[i] = *reinterpret_cast<const u32x4*>((const char*)a.cache_k + r * kBytes + at);
+            v[i] = *reinterpret_cast<const u32x4*>((const char*)a.cache_v + r * kBytes + at);
+          }
+        }
+      }
+    }
+    if constexpr (KEYS == kCache8) {                                  // the first BN threads: of K, the next: of V
+      static_assert(2 * BN <= NT, "a scale per thread");
+      const int j = j0 + (tid & (BN - 1));
+      scale = 0.f;
+      if (tid < 2 * BN && j < n) {
+        const int p = page >= BN ? id : table[j >> a.page_shift];
+        if ((unsigned)p < (unsigned)a.pages)
+          scale = (tid < BN ? a.cache_ks : a.cache_vs)[((size_t)p * a.G + group) * page + (j & (page - 1))];
+      }
+    }
+  }
+  __device__ __forceinline__ void store(char* kt, char* vt, float* scales, int tid) const {
+    const int row = tid / kPieces, at = tid % kPieces;
+    if (!kPart || row < BN) {
+#pragma unroll
+      for (int i = 0; i < kEach; ++i) {
+        char* const pk = kt + (row + i * kStep) * R::kStride;
+        char* const pv = vt + (row + i * kStep) * R::kStride;
+        if constexpr (KEYS == kCache8) {
+          *reinterpret_cast<u32x4*>(pk + at * 32) = widen8(k[i][0], k[i][1]);
+          *reinterpret_cast<u32x4*>(pk + at * 32 + 16) = widen8(k[i][2], k[i][3]);
+          *reinterpret_cast<u32x4*>(pv + at * 32) = widen8(v[i][0], v[i][1]);
+          *reinterpret_cast<u32x4*>(pv + at * 32 + 16) = widen8(v[i][2], v[i][3]);
+        } else {
+          *reinterpret_cast<u32x4*>(pk + at * 16) = k[i];
+          *reinterpret_cast<u32x4*>(pv + at * 16) = v[i];
+        }
+      }
+    }
+    if constexpr (KEYS == kCache8)
+      if (tid < 2 * BN) scales[tid] = scale;
+  }
 };
 
 // The running maximum moves only when it grows by more than this (in powers of 2): p stays below 2^8, and o is rescaled
 // a few times per row rather than with every tile.
 constexpr float kSlack = 8.f;
 
-template <class T, int D, int QT, int NW, int BN, int PARTS>
+// Shares of a row's result that the join kernel adds up: o before its division, and the maximum (times scale, in powers
+// of 2) and sum behind all rows' o: part = [splits][B H T][D], then [splits][B H T][2].
+__device__ __forceinline__ size_t share(const AttnArgs& a, int split, const Seq& s, int head, int i) {
+  return (((size_t)split * a.B + s.b) * a.H + head) * a.T + s.first + i;
+}
+__device__ __forceinline__ float* share_stats(const AttnArgs& a, int D, size_t row) {
+  return a.part + (size_t)a.splits * a.B * a.H * a.T * D + 2 * row;
+}
+
+template <class T, int D, int QT, int NW, int BN, int PARTS, Keys KEYS>
 __global__ __launch_bounds__(64 * NW, QT * D * (int)sizeof(T) > 256 ? 1 : 2) void fwd_kernel(AttnArgs a) {
-  using F = FwdTile<T, D, QT, NW, BN, PARTS>;
+  using F = FwdTile<T, D, QT, NW, BN, PARTS, KEYS>;
   using R = Rows<T, D>;
   extern __shared__ __align__(16) char lds[];
   constexpr int NT = BN / 32;
+  const unsigned unit = blockIdx.x / (unsigned)a.splits, split = blockIdx.x - unit * a.splits;
   // heads of a group lie S G blocks apart (or G): with a multiple of 8 they share an XCD and the keys in its L2
-  const int heads = a.H, slot0 = (int)(blockIdx.x / heads), pair = (int)(blockIdx.x - (unsigned)slot0 * heads);
+  const int slot0 = (int)(unit / (unsigned)a.H), pair = (int)(unit - (unsigned)slot0 * a.H);
   const int rep = a.H / a.G, head = (pair % a.G) * rep + pair / a.G, group = pair % a.G;
   const Seq s = find_tile(a, slot0, F::kRows, a.causal);
   if (s.id < 0) return;
   const int tid = threadIdx.x, l = lane_id(), h = l >> 5, w = uniform(wave_id());
   const int q0 = s.tile * F::kRows, qw = q0 + w * 32 * QT;            // the block's and the wave's first query
   const long long e = sizeof(T);
+  // tokens in front of the first query, and keys altogether
+  int past = 0, keys = s.n;
+  if constexpr (KEYS != kPrompt) {
+    const int room = a.max_pages << a.page_shift;
+    past = min(max(uniform(a.past[s.b]), 0), room);
+    keys = min(past + s.n, room);
+  }
 
   // Q: the second operand of S^T = K Q^T
   u32x4 qf[QT][R::kSteps];
@@ -231,27 +362,39 @@ __global__ __launch_bounds__(64 * NW, QT * D * (int)sizeof(T) > 256 ? 1 : 2) voi
       for (int k = 0; k < R::kSteps; ++k) qf[t][k] = load16(r, (32 * t + (l & 31)) * stride + (2 * k + h) * 16);
   }
 
+  // the block's keys jbeg .. jend - 1, and its share of their tiles
   const int qlast = min(q0 + F::kRows, s.n) - 1;
-  const int jend = a.causal ? qlast + 1 : s.n;                        // the block's keys: jbeg .. jend - 1
-  const int jbeg = a.window > 0 ? max(q0 - a.window + 1, 0) : 0;
-  const int t0 = jbeg / BN, t1 = (jend + BN - 1) / BN;
+  const int jend = a.causal ? min(past + qlast + 1, keys) : keys;
+  const int jbeg = a.window > 0 ? max(past + q0 - a.window + 1, 0) : 0;
+  int t0 = jbeg / BN, t1 = max((jend + BN - 1) / BN, t0);
+  if (a.splits > 1) {
+    const int per = (t1 - t0 + a.splits - 1) / a.splits;
+    t0 = min(t0 + (int)split * per, t1);
+    t1 = min(t0 + per, t1);
+  }
 
-  u32x4 sk[F::kEach], sv[F::kEach];
-  const int srow = tid / R::kPieces, spiece = tid % R::kPieces;
-  constexpr int kStep = F::kThreads / R::kPieces;                     // rows between a thread's pieces
   const int kst = (int)(a.ks.t * e), vst = (int)(a.vs.t * e);
-  const char* kp = (const char*)a.k + (s.b * a.ks.b + group * a.ks.h + (long long)s.first * a.ks.t) * e;
-  const char* vp = (const char*)a.v + (s.b * a.vs.b + group * a.vs.h + (long long)s.first * a.vs.t) * e;
+  const char *kp = nullptr, *vp = nullptr;
+  const int* table = nullptr;
+  if constexpr (KEYS == kPrompt) {
+    kp = (const char*)a.k + (s.b * a.ks.b + group * a.ks.h + (long long)s.first * a.ks.t) * e;
+    vp = (const char*)a.v + (s.b * a.vs.b + group * a.vs.h + (long long)s.first * a.vs.t) * e;
+  } else {
+    table = a.table + (size_t)s.b * a.max_pages;
+  }
+  KeyTile<T, D, F::kThreads, BN, KEYS> next;
+  // the page of a tile, asked for one tile ahead
+  const auto page_of = [&](int t) { return KEYS != kPrompt && t < t1 && (1 << a.page_shift) >= BN ? table[t * BN >> a.page_shift] : 0; };
+  int id = page_of(t0);
   const auto load = [&](int t) {
-    const int n = min(BN, s.n - t * BN);
-    const auto rk = rows_of(kp + (long long)t * BN * kst, n, kst, R::kBytes);
-    const auto rv = rows_of(vp + (long long)t * BN * vst, n, vst, R::kBytes);
-#pragma unroll
-    for (int i = 0; i < F::kEach; ++i) sk[i] = load16(rk, (srow + i * kStep) * kst + spiece * 16);
-#pragma unroll
-    for (int i = 0; i < F::kEach; ++i) sv[i] = load16(rv, (srow + i * kStep) * vst + spiece * 16);
+    if constexpr (KEYS == kPrompt) {
+      next.load_prompt(kp, vp, kst, vst, t, keys - t * BN, tid);
+    } else {
+      next.load_cache(a, table, uniform(id), group, t * BN, keys, tid);
+      id = page_of(t + 1);
+    }
   };
-  load(t0);
+  if (t0 < t1) load(t0);
 
   f32x16 o[QT][D / 32];
   float m[QT], sum[QT];
@@ -262,20 +405,17 @@ __global__ __launch_bounds__(64 * NW, QT * D * (int)sizeof(T) > 256 ? 1 : 2) voi
     for (int d = 0; d < D / 32; ++d) o[t][d] = zero16();
   }
   const float c = a.scale * kLog2e;
-  const int rrow = R::by_rows(l), rcol = R::transposed(l), wat = srow * R::kStride + spiece * 16;
+  const int rrow = R::by_rows(l), rcol = R::transposed(l), pw = past + qw;
 
   for (int t = t0; t < t1; ++t) {
     char* kt = lds + (t & 1) * F::kTile;
     char* vt = kt + 2 * F::kTile;
-#pragma unroll
-    for (int i = 0; i < F::kEach; ++i) {
-      *reinterpret_cast<u32x4*>(kt + wat + i * kStep * R::kStride) = sk[i];
-      *reinterpret_cast<u32x4*>(vt + wat + i * kStep * R::kStride) = sv[i];
-    }
+    float* scales = reinterpret_cast<float*>(lds + 4 * F::kTile) + (t & 1) * 2 * BN;
+    next.store(kt, vt, scales, tid);
     __syncthreads();
     if (t + 1 < t1) load(t + 1);
     const int j0 = t * BN;
-    if (a.causal && j0 > qw + 32 * QT - 1) continue;                  // nothing for this wave's queries
+    if (a.causal && j0 > pw + 32 * QT - 1) continue;                  // nothing for this wave's queries
 
     f32x16 x[NT][QT];
 #pragma unroll
@@ -290,13 +430,25 @@ __global__ __launch_bounds__(64 * NW, QT * D * (int)sizeof(T) > 256 ? 1 : 2) voi
 #pragma unroll
         for (int q = 0; q < QT; ++q) mma(x[n][q], f, qf[q][k], T());
       }
+    if constexpr (KEYS == kCache8) {
+#pragma unroll
+      for (int n = 0; n < NT; ++n)
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+          const f32x4 f = *reinterpret_cast<const f32x4*>(scales + 32 * n + 8 * r + 4 * h);
+#pragma unroll
+          for (int q = 0; q < QT; ++q)
+#pragma unroll
+            for (int u = 0; u < 4; ++u) x[n][q][4 * r + u] *= f[u];
+        }
+    }
     // keys that not all of the wave's queries see
-    const bool edge = j0 + BN > s.n || (a.causal && j0 + BN - 1 > qw) || (a.window > 0 && j0 <= qw + 32 * QT - 1 - a.window);
+    const bool edge = j0 + BN > keys || (a.causal && j0 + BN - 1 > pw) || (a.window > 0 && j0 <= pw + 32 * QT - 1 - a.window);
     if (edge) {
 #pragma unroll
       for (int q = 0; q < QT; ++q) {
-        const int i = qw + 32 * q + (l & 31);
-        const int last = (a.causal ? min(i, s.n - 1) : s.n - 1) - j0 - 4 * h;
+        const int i = pw + 32 * q + (l & 31);
+        const int last = (a.causal ? min(i, keys - 1) : keys - 1) - j0 - 4 * h;
         const int first = (a.window > 0 ? i - a.window + 1 : 0) - j0 - 4 * h;
 #pragma unroll
         for (int n = 0; n < NT; ++n)
@@ -328,38 +480,84 @@ __global__ __launch_bounds__(64 * NW, QT * D * (int)sizeof(T) > 256 ? 1 : 2) voi
       const float shift = m[q] == -kInf ? 0.f : m[q] * c;
       float part = 0.f;
 #pragma unroll
-      for (int n = 0; n < NT; ++n) {
+      for (int n = 0; n < NT; ++n)
 #pragma unroll
         for (int r = 0; r < 16; ++r) {
           x[n][q][r] = __builtin_amdgcn_exp2f(fmaf(x[n][q][r], c, -shift));
           part += x[n][q][r];
         }
-        p[n][q].set(x[n][q]);
-      }
       sum[q] += part;
     }
 #pragma unroll
-    for (int n = 0; n < NT; ++n) mul_transposed<D, PARTS, QT>(o, vt + rcol + n * 32 * R::kStride, p[n]);
+    for (int n = 0; n < NT; ++n) {
+      if constexpr (KEYS == kCache8) {
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+          const f32x4 f = *reinterpret_cast<const f32x4*>(scales + BN + 32 * n + 8 * r + 4 * h);
+#pragma unroll
+          for (int q = 0; q < QT; ++q)
+#pragma unroll
+            for (int u = 0; u < 4; ++u) x[n][q][4 * r + u] *= f[u];
+        }
+      }
+#pragma unroll
+      for (int q = 0; q < QT; ++q) p[n][q].set(x[n][q]);
+      mul_transposed<D, PARTS, QT>(o, vt + rcol + n * 32 * R::kStride, p[n]);
+    }
   }
 
 #pragma unroll
   for (int q = 0; q < QT; ++q) {
     const int i = qw + 32 * q + (l & 31);
-    const float total = both_sum(sum[q]), f = total > 0.f || total != total ? 1.f / total : 0.f;
+    const float total = both_sum(sum[q]);
     if (i >= s.n) continue;
-    char* p = (char*)a.o + (s.b * a.os.b + head * a.os.h + (long long)(s.first + i) * a.os.t) * e;
-#pragma unroll
-    for (int d = 0; d < D / 32; ++d)
-#pragma unroll
-      for (int r = 0; r < 4; ++r) {
-        T y[4];
-#pragma unroll
-        for (int u = 0; u < 4; ++u) y[u] = (T)(o[q][d][4 * r + u] * f);
-        __builtin_memcpy(p + (32 * d + 8 * r + 4 * h) * e, y, sizeof(y));
-      }
+    if (a.splits > 1) {
+      const size_t row = share(a, split, s, head, i);
+      if (h == 0) share_stats(a, D, row)[0] = m[q] * c, share_stats(a, D, row)[1] = total;
+      store_columns<float, D>(reinterpret_cast<char*>(a.part + row * D), o[q], 1.f, h);
+      continue;
+    }
+    // a row without keys: zeros, and a logarithm of -infinity
+    store_columns<T, D>((char*)a.o + (s.b * a.os.b + head * a.os.h + (long long)(s.first + i) * a.os.t) * e, o[q],
+                        total == 0.f ? 0.f : 1.f / total, h);
     if (a.lse != nullptr && h == 0)
       a.lse[((long long)s.b * a.H + head) * a.T + s.first + i] = total == 0.f ? -kInf : (m[q] * c + __builtin_amdgcn_logf(total)) * kLn2;
   }
+}
+
+// Joins the shares of the rows: D / 4 lanes per row, rows [B H T] in order.
+template <class T, int D>
+__global__ __launch_bounds__(256) void join_kernel(AttnArgs a) {
+  constexpr int L = D / 4;
+  const size_t rows = (size_t)a.B * a.H * a.T, row = (size_t)blockIdx.x * (256 / L) + threadIdx.x / L;
+  if (row >= rows) return;
+  const int at = threadIdx.x % L * 4;
+  const size_t bh = row / a.T;
+  const int t = (int)(row - bh * a.T), b = (int)(bh / a.H), head = (int)(bh - (size_t)b * a.H);
+  int n = a.T;
+  if (a.lens != nullptr) n = min(max(a.lens[b], 0), a.T);
+  if (t >= n) return;
+  const float* stats = share_stats(a, D, row);
+  float m = -kInf;
+  for (int k = 0; k < a.splits; ++k)
+    if (stats[2 * rows * k + 1] != 0.f) m = fmaxf(m, stats[2 * rows * k]);
+  float sum = 0.f;
+  f32x4 o = zero4();
+  for (int k = 0; k < a.splits; ++k) {
+    const float total = stats[2 * rows * k + 1];
+    if (total == 0.f) continue;
+    // an infinite maximum: what comes of it is NaN, as without shares
+    const float f = __builtin_amdgcn_exp2f(stats[2 * rows * k] - m);
+    sum += f * total;
+    const f32x4 x = *reinterpret_cast<const f32x4*>(a.part + (rows * k + row) * D + at);
+#pragma unroll
+    for (int u = 0; u < 4; ++u) o[u] = fmaf(f, x[u], o[u]);
+  }
+  T y[4];
+#pragma unroll
+  for (int u = 0; u < 4; ++u) y[u] = (T)(sum == 0.f ? 0.f : o[u] / sum);
+  __builtin_memcpy((char*)a.o + (b * a.os.b + head * a.os.h + (long long)t * a.os.t + at) * (long long)sizeof(T), y, sizeof(y));
+  if (a.lse != nullptr && at == 0) a.lse[row] = sum == 0.f ? -kInf : (m + __builtin_amdgcn_logf(sum)) * kLn2;
 }
 
 }  // namespace attn

@@ -24,15 +24,34 @@ struct AttnArgs {
   prism_strides dos, dqs, dks, dvs;
   float* delta;                   // [B][H][T]: <do, o> of each row
   void *dq, *dk, *dv;
-  // paged cache: k, v are [pages][G][page][D], of q's type or e4m3 with a scale per row
-  const float *k_scale, *v_scale; // [pages][G][page]
-  const int *table, *past;        // [B][max_pages], [B]
+  // paged cache: [pages][G][page][D], of q's type or e4m3 with a scale per row
+  void *cache_k, *cache_v;
+  float *cache_ks, *cache_vs;     // [pages][G][page]
+  const int *table, *past;        // [S][max_pages], [S]
   int pages, page_shift, max_pages;
   int splits;                     // key ranges of a sequence, joined afterwards
   float* part;                    // their shares of o, and m, l behind them
 };
 
+// Norm and rotation of the rows of two tensors: x[0] with H heads, x[1] with G.
+struct RopeArgs {
+  const void *x[2], *dy[2];
+  void* y[2];                     // forward: y, backward: dx
+  prism_strides xs[2], dys[2], ys[2];
+  const float *w[2], *freq;
+  float* dw[2];
+  const int* pos;                 // [B][T]; null: the token's index
+  int B, T, D, heads[2], rot, interleaved;
+  float factor, eps;
+  int per, groups;                // heads per lane group, groups of a token
+  float* part;                    // [nblk][2][D]
+  int nblk;
+};
+
 namespace host {
+prism_status launch_cache_write(prism_dtype dt, int D, bool bits8, AttnArgs a, hipStream_t stream);
+prism_status launch_attn_paged(prism_dtype dt, int D, bool bits8, bool few, AttnArgs a, hipStream_t stream);
+prism_status launch_rope(prism_dtype dt, bool bwd, const RopeArgs& a, hipStream_t stream);
 // Each enqueues on `stream` and reports launch failures.
 prism_status launch_attn_fwd(prism_dtype dt, int D, AttnArgs a, hipStream_t stream);
 prism_status launch_attn_bwd(prism_dtype dt, int D, const AttnArgs& a, hipStream_t stream);

@@ -49,20 +49,6 @@ __device__ __forceinline__ float dot(const u32x4& a, const u32x4& b) {
   return s;
 }
 
-// Rows of an accumulator tile whose columns are rows of the tensor: 4 values at a time.
-template <class T, int D>
-__device__ __forceinline__ void store_columns(char* row, const f32x16 (&acc)[D / 32], float f, int h) {
-#pragma unroll
-  for (int d = 0; d < D / 32; ++d)
-#pragma unroll
-    for (int r = 0; r < 4; ++r) {
-      T y[4];
-#pragma unroll
-      for (int u = 0; u < 4; ++u) y[u] = (T)(acc[d][4 * r + u] * f);
-      __builtin_memcpy(row + (32 * d + 8 * r + 4 * h) * (int)sizeof(T), y, sizeof(y));
-    }
-}
-
 template <class T, int D, int NW, int BN> struct BwdTile {
   using R = Rows<T, D>;
   static constexpr int kThreads = 64 * NW, kRows = 32 * NW;

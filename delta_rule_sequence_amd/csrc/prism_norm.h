@@ -9,6 +9,7 @@
 // gated 10.6 us, 4.7; backward of 16384 x 768 with a residual's gradient 20 us and 4 for dw, 4.3 TB/s; rows of odd
 // length, which start anywhere: backward of 4924 x 843, gated, 26 us.
 #pragma once
+#include "prism_e4m3.h"
 #include "prism_silu.h"
 #include "prism_ssm_args.h"
 #include "prism_tile.h"
@@ -17,7 +18,6 @@ namespace prism {
 namespace norm {
 
 constexpr int kBlock = 128;        // values that share one scale of the 8-bit output
-constexpr float kE4m3Max = 448.f;
 
 __device__ __forceinline__ float wave_sum(float v) {
 #pragma unroll
@@ -33,22 +33,6 @@ __device__ __forceinline__ unsigned wave_max_bits(unsigned v) {
   }
   return v;
 }
-__device__ __forceinline__ unsigned abs_bits(float v) { return __builtin_bit_cast(unsigned, v) & 0x7fffffffu; }
-
-// Below this a block counts as all zero: 448 / amax would overflow soon after.
-constexpr float kTiny = 0x1p-100f;
-// The scale of a block from its largest |y| (bits), and the factor that takes y to the bytes' range: NaN for a block
-// with a non-finite value, which makes all its bytes NaN.  |y| factor <= 448 (1 + 2^-22) rounds to 448 at most.
-__device__ __forceinline__ float block_scale(unsigned amax, float* factor) {
-  const float m = __builtin_bit_cast(float, amax);
-  if (m < kTiny) {
-    *factor = 0.f;
-    return 1.f;
-  }
-  *factor = m < __builtin_inff() ? kE4m3Max / m : __builtin_nanf("");
-  return m / kE4m3Max;
-}
-
 __device__ __forceinline__ float block_sum(float v, float* part) {  // 256 threads
   v = wave_sum(v);
   __syncthreads();

@@ -594,6 +594,30 @@ prism_status prism_attn_bwd(const void* q, const prism_strides* q_strides, const
                             void* dk, const prism_strides* dk_strides, void* dv, const prism_strides* dv_strides,
                             void* workspace, size_t workspace_bytes, hipStream_t stream);
 
+prism_status prism_rope_fwd(const void* q, const prism_strides* q_strides, const void* k, const prism_strides* k_strides,
+                            const float* freq, const int* pos, const float* wq, const float* wk,
+                            int B, int H, int G, int T, int D, int rot, int interleaved, float factor, float eps,
+                            prism_dtype dt, void* yq, const prism_strides* yq_strides, void* yk,
+                            const prism_strides* yk_strides, hipStream_t stream);
+size_t prism_rope_bwd_workspace_bytes(int B, int H, int G, int T, int D, int rot, prism_dtype dt);
+prism_status prism_rope_bwd(const void* q, const prism_strides* q_strides, const void* k, const prism_strides* k_strides,
+                            const void* dyq, const prism_strides* dyq_strides, const void* dyk,
+                            const prism_strides* dyk_strides, const float* freq, const int* pos, const float* wq,
+                            const float* wk, int B, int H, int G, int T, int D, int rot, int interleaved, float factor,
+                            float eps, prism_dtype dt, void* dq, const prism_strides* dq_strides, void* dk,
+                            const prism_strides* dk_strides, float* dwq, float* dwk, void* workspace,
+                            size_t workspace_bytes, hipStream_t stream);
+prism_status prism_cache_write(const void* k, const prism_strides* k_strides, const void* v, const prism_strides* v_strides,
+                               const int* table, const int* past, const int* lens, const int* starts, int S,
+                               int B, int G, int T, int D, int pages, int page, int max_pages, prism_dtype dt,
+                               void* cache_k, void* cache_v, float* scale_k, float* scale_v, hipStream_t stream);
+size_t prism_attn_paged_workspace_bytes(int B, int H, int G, int T, int D, int page, int max_pages, prism_dtype dt);
+prism_status prism_attn_paged(const void* q, const prism_strides* q_strides, const void* cache_k, const void* cache_v,
+                              const float* scale_k, const float* scale_v, const int* table, const int* past,
+                              const int* lens, int B, int H, int G, int T, int D, int pages, int page, int max_pages,
+                              float scale, int window, prism_dtype dt, void* o, const prism_strides* o_strides,
+                              void* workspace, size_t workspace_bytes, hipStream_t stream);
+
 /* A static, human-readable name of a status code. */
 const char* prism_status_string(prism_status s);
 

@@ -85,7 +85,7 @@ prism_status prism_attn_fwd(const void* q, const prism_strides* q_strides, const
                             void* o, const prism_strides* o_strides, float* lse, hipStream_t stream) {
   const prism_status st = attn_check(B, H, G, T, D, S, lens, starts, scale, window, dt);
   if (st != PRISM_OK) return st;
-  if (!q || !k || !v || !o) return PRISM_ERR_INVALID_ARG;
+  if (!q || !k || !v || !o || o == k || o == v) return PRISM_ERR_INVALID_ARG;
   if (window > 0 && !causal) return PRISM_ERR_INVALID_ARG;
   AttnArgs a = {};
   if (!make_strides(q_strides, B, H, T, D, &a.qs) || !make_strides(k_strides, B, G, T, D, &a.ks) ||

@@ -314,12 +314,24 @@ template <class T, int D, int NT, int BN, Keys KEYS> struct KeyTile {
   }
 };
 
+// Past this, a product's rounding moves the exponent 2^t by whole steps (and past 2^31 to infinity): scores and maximum are
+// subtracted before they are scaled.  Below, fmaf(s, c, -m c) costs one instruction, and the rounding of m c is the
+// same for all of a row.
+constexpr float kFar = 65536.f;
+
 // The running maximum moves only when it grows by more than this (in powers of 2): p stays below 2^8, and o is rescaled
 // a few times per row rather than with every tile.
 constexpr float kSlack = 8.f;
 
-// Shares of a row's result that the join kernel adds up: o before its division, and the maximum (times scale, in powers
-// of 2) and sum behind all rows' o: part = [splits][B H T][D], then [splits][B H T][2].
+// lse from the maximum score and the sum of a row.
+__device__ __forceinline__ float row_lse(float m, float sum, float scale) {
+  if (sum == 0.f) return -kInf;
+  const float c = scale * kLog2e, log2 = __builtin_amdgcn_logf(sum);
+  return fabsf(m * c) > kFar ? m * scale + log2 * kLn2 : (m * c + log2) * kLn2;
+}
+
+// Shares of a row's result that the join kernel adds up: o before its division, and the maximum score and
+// sum behind all rows' o: part = [splits][B H T][D], then [splits][B H T][2].
 __device__ __forceinline__ size_t share(const AttnArgs& a, int split, const Seq& s, int head, int i) {
   return (((size_t)split * a.B + s.b) * a.H + head) * a.T + s.first + i;
 }
@@ -477,13 +489,21 @@ __global__ __launch_bounds__(64 * NW, QT * D * (int)sizeof(T) > 256 ? 1 : 2) voi
 #pragma unroll
         for (int d = 0; d < D / 32; ++d) o[q][d] *= f;
       }
-      const float shift = m[q] == -kInf ? 0.f : m[q] * c;
+      float shift = m[q] == -kInf ? 0.f : m[q] * c, by = c;
+      if (__any(fabsf(shift) > kFar)) {
+        const float to = m[q] == -kInf ? 0.f : m[q];
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+          for (int r = 0; r < 16; ++r) x[n][q][r] = (x[n][q][r] - to) * c;
+        shift = 0.f, by = 1.f;
+      }
       float part = 0.f;
 #pragma unroll
       for (int n = 0; n < NT; ++n)
 #pragma unroll
         for (int r = 0; r < 16; ++r) {
-          x[n][q][r] = __builtin_amdgcn_exp2f(fmaf(x[n][q][r], c, -shift));
+          x[n][q][r] = __builtin_amdgcn_exp2f(fmaf(x[n][q][r], by, -shift));
           part += x[n][q][r];
         }
       sum[q] += part;
@@ -513,7 +533,7 @@ __global__ __launch_bounds__(64 * NW, QT * D * (int)sizeof(T) > 256 ? 1 : 2) voi
     if (i >= s.n) continue;
     if (a.splits > 1) {
       const size_t row = share(a, split, s, head, i);
-      if (h == 0) share_stats(a, D, row)[0] = m[q] * c, share_stats(a, D, row)[1] = total;
+      if (h == 0) share_stats(a, D, row)[0] = m[q], share_stats(a, D, row)[1] = total;
       store_columns<float, D>(reinterpret_cast<char*>(a.part + row * D), o[q], 1.f, h);
       continue;
     }
@@ -521,7 +541,7 @@ __global__ __launch_bounds__(64 * NW, QT * D * (int)sizeof(T) > 256 ? 1 : 2) voi
     store_columns<T, D>((char*)a.o + (s.b * a.os.b + head * a.os.h + (long long)(s.first + i) * a.os.t) * e, o[q],
                         total == 0.f ? 0.f : 1.f / total, h);
     if (a.lse != nullptr && h == 0)
-      a.lse[((long long)s.b * a.H + head) * a.T + s.first + i] = total == 0.f ? -kInf : (m[q] * c + __builtin_amdgcn_logf(total)) * kLn2;
+      a.lse[((long long)s.b * a.H + head) * a.T + s.first + i] = row_lse(m[q], total, a.scale);
   }
 }
 
@@ -547,7 +567,7 @@ __global__ __launch_bounds__(256) void join_kernel(AttnArgs a) {
     const float total = stats[2 * rows * k + 1];
     if (total == 0.f) continue;
     // an infinite maximum: what comes of it is NaN, as without shares
-    const float f = __builtin_amdgcn_exp2f(stats[2 * rows * k] - m);
+    const float f = __builtin_amdgcn_exp2f((stats[2 * rows * k] - m) * (a.scale * kLog2e));
     sum += f * total;
     const f32x4 x = *reinterpret_cast<const f32x4*>(a.part + (rows * k + row) * D + at);
 #pragma unroll
@@ -557,7 +577,7 @@ __global__ __launch_bounds__(256) void join_kernel(AttnArgs a) {
 #pragma unroll
   for (int u = 0; u < 4; ++u) y[u] = (T)(sum == 0.f ? 0.f : o[u] / sum);
   __builtin_memcpy((char*)a.o + (b * a.os.b + head * a.os.h + (long long)t * a.os.t + at) * (long long)sizeof(T), y, sizeof(y));
-  if (a.lse != nullptr && at == 0) a.lse[row] = sum == 0.f ? -kInf : (m + __builtin_amdgcn_logf(sum)) * kLn2;
+  if (a.lse != nullptr && at == 0) a.lse[row] = row_lse(m, sum, a.scale);
 }
 
 }  // namespace attn

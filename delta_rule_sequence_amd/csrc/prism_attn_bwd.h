@@ -49,11 +49,18 @@ __device__ __forceinline__ float dot(const u32x4& a, const u32x4& b) {
   return s;
 }
 
+// log2 of p from a score and an lse beyond kFar: the score is rounded as lse was, so that equal ones leave 0.
+__device__ __forceinline__ float far_exponent(float x, float scale, float lse) {
+#pragma clang fp contract(off)
+  const float s = x * scale;
+  return (s - lse) * kLog2e;
+}
+
 template <class T, int D, int NW, int BN> struct BwdTile {
   using R = Rows<T, D>;
   static constexpr int kThreads = 64 * NW, kRows = 32 * NW;
   static constexpr int kTile = BN * R::kStride;
-  static constexpr int kLds = 4 * kTile + 4 * BN * 4;                 // two tiles of two tensors; lse and delta of two
+  static constexpr int kLds = 4 * kTile + 2 * 2 * BN * 4;             // two tiles of two tensors; lse and delta of two
 };
 
 // dq and delta: a wave owns 32 queries.
@@ -86,11 +93,11 @@ __global__ __launch_bounds__(64 * NW, D * (int)sizeof(T) > 256 ? 1 : 2) void dq_
     delta = both_sum(delta);
   }
   const long long at = ((long long)s.b * a.H + head) * a.T + s.first + i;
-  float lse = 0.f;
-  if (i < s.n) {
-    lse = a.lse[at] * kLog2e;
-    if (h == 0) a.delta[at] = delta;
-  }
+  const float given = i < s.n ? a.lse[at] : 0.f;
+  if (i < s.n && h == 0) a.delta[at] = delta;
+  // scores and lse beyond kFar are subtracted before they go to powers of 2
+  const bool far = __any(fabsf(given) > kFar && fabsf(given) < kInf);
+  const float c = far ? 1.f : a.scale * kLog2e, lse = far ? 0.f : given * kLog2e;
 
   const int jend = a.causal ? min(q0 + F::kRows, s.n) : s.n;
   const int jbeg = a.window > 0 ? max(q0 - a.window + 1, 0) : 0;
@@ -105,7 +112,6 @@ __global__ __launch_bounds__(64 * NW, D * (int)sizeof(T) > 256 ? 1 : 2) void dq_
   f32x16 dq[1][D / 32];
 #pragma unroll
   for (int d = 0; d < D / 32; ++d) dq[0][d] = zero16();
-  const float c = a.scale * kLog2e;
   const int rrow = R::by_rows(l), rcol = R::transposed(l);
 
   for (int t = t0; t < t1; ++t) {
@@ -130,6 +136,10 @@ __global__ __launch_bounds__(64 * NW, D * (int)sizeof(T) > 256 ? 1 : 2) void dq_
       for (int k = 0; k < R::kSteps; ++k) mma(x, lds16(kt + rrow + n * 32 * R::kStride + k * 32), qf[k], T());
 #pragma unroll
       for (int k = 0; k < R::kSteps; ++k) mma(g, lds16(vt + rrow + n * 32 * R::kStride + k * 32), gf[k], T());
+      if (far) {
+#pragma unroll
+        for (int r = 0; r < 16; ++r) x[r] = far_exponent(x[r], a.scale, given);
+      }
 #pragma unroll
       for (int r = 0; r < 16; ++r) {
         float p = __builtin_amdgcn_exp2f(fmaf(x[r], c, -lse)) * (g[r] - delta);
@@ -184,7 +194,7 @@ __global__ __launch_bounds__(64 * NW, D * (int)sizeof(T) > 128 ? 1 : 2) void dkv
       const int i = i0 + (tid & (BN - 1));
       const long long at = ((long long)s.b * a.H + group * rep + head) * a.T + s.first + i;
       // past the last query p is 0
-      row = i >= s.n ? (tid < BN ? kInf : 0.f) : tid < BN ? a.lse[at] * kLog2e : a.delta[at];
+      row = i >= s.n ? (tid < BN ? kInf : 0.f) : tid < BN ? a.lse[at] : a.delta[at];
     }
   };
   load(0, t0);
@@ -221,12 +231,24 @@ __global__ __launch_bounds__(64 * NW, D * (int)sizeof(T) > 128 ? 1 : 2) void dkv
       const int last = (a.window > 0 ? (int)min((long long)j + a.window - 1, (long long)INT_MAX) : INT_MAX) - i0 - 4 * h;
 #pragma unroll
       for (int r4 = 0; r4 < 4; ++r4) {
-        const f32x4 lse = *reinterpret_cast<const f32x4*>(rt + 32 * n + 8 * r4 + 4 * h);
+        f32x4 lse = *reinterpret_cast<const f32x4*>(rt + 32 * n + 8 * r4 + 4 * h);
+        // scores and lse beyond kFar are subtracted before they go to powers of 2
+        float by = c;
+        bool far = false;
+#pragma unroll
+        for (int u = 0; u < 4; ++u) far |= fabsf(lse[u]) > kFar && fabsf(lse[u]) < kInf;
+        if (__any(far)) {
+#pragma unroll
+          for (int u = 0; u < 4; ++u) x[4 * r4 + u] = far_exponent(x[4 * r4 + u], a.scale, lse[u]), lse[u] = 0.f;
+          by = 1.f;
+        } else {
+          lse *= kLog2e;
+        }
         const f32x4 delta = *reinterpret_cast<const f32x4*>(rt + BN + 32 * n + 8 * r4 + 4 * h);
 #pragma unroll
         for (int u = 0; u < 4; ++u) {
           const int r = 4 * r4 + u;
-          float p = __builtin_amdgcn_exp2f(fmaf(x[r], c, -lse[u]));
+          float p = __builtin_amdgcn_exp2f(fmaf(x[r], by, -lse[u]));
           float ds = p * (g[r] - delta[u]);
           if (edge) {
             const int i = 32 * n + 8 * r4 + u;

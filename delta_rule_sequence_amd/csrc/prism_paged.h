@@ -153,7 +153,12 @@ __global__ __launch_bounds__(256, D * (int)sizeof(T) > 256 ? 1 : 2) void few_ker
 #pragma unroll
       for (int d = 0; d < D / 32; ++d) o[0][d] *= f;
     }
-    const float shift = m == -kInf ? 0.f : m * c;
+    float shift = m == -kInf ? 0.f : m * c, by = c;
+    if (__any(fabsf(shift) > kFar)) {
+#pragma unroll
+      for (int k = 0; k < 16; ++k) x[k] = (x[k] - (m == -kInf ? 0.f : m)) * c;
+      shift = 0.f, by = 1.f;
+    }
 #pragma unroll
     for (int r4 = 0; r4 < 4; ++r4) {
       f32x4 f = {1.f, 1.f, 1.f, 1.f};
@@ -161,7 +166,7 @@ __global__ __launch_bounds__(256, D * (int)sizeof(T) > 256 ? 1 : 2) void few_ker
 #pragma unroll
       for (int u = 0; u < 4; ++u) {
         const int k = 4 * r4 + u;
-        x[k] = __builtin_amdgcn_exp2f(fmaf(x[k], c, -shift));
+        x[k] = __builtin_amdgcn_exp2f(fmaf(x[k], by, -shift));
         sum += x[k];
         if constexpr (KEYS == kCache8) x[k] *= f[u];
       }
@@ -176,7 +181,7 @@ __global__ __launch_bounds__(256, D * (int)sizeof(T) > 256 ? 1 : 2) void few_ker
   const float total = both_sum(sum);
   store_columns<float, D>(kt + (l & 31) * F::kOut, o[0], 1.f, h);
   float* const stats = reinterpret_cast<float*>(kt + 32 * F::kOut);
-  if (h == 0) stats[2 * (l & 31)] = m * c, stats[2 * (l & 31) + 1] = total;
+  if (h == 0) stats[2 * (l & 31)] = m, stats[2 * (l & 31) + 1] = total;
   __syncthreads();
   const int row = tid >> 3, rr = tile * 32 + row, t = rr / rep, hd = group * rep + (rr - t * rep);
   if (t >= s.n) return;
@@ -189,7 +194,7 @@ __global__ __launch_bounds__(256, D * (int)sizeof(T) > 256 ? 1 : 2) void few_ker
 #pragma unroll
   for (int k = 0; k < 4; ++k) {
     const float* st = reinterpret_cast<const float*>(lds + k * F::kWave + 32 * F::kOut) + 2 * row;
-    f[k] = st[1] == 0.f ? 0.f : __builtin_amdgcn_exp2f(st[0] - mj);
+    f[k] = st[1] == 0.f ? 0.f : __builtin_amdgcn_exp2f((st[0] - mj) * c);
     sj += f[k] * st[1];
   }
   const size_t at = share(a, split, s, hd, t);

@@ -14,8 +14,8 @@
 namespace prism {
 namespace rope {
 
-// sin and cos of 2 pi t.  t, formed and reduced in float64 (positions up to 2^31: off by 2^-21 of a turn's 2^-32), leaves
-// an eighth of a turn on both sides of a quarter; there Taylor's series to x^9 and x^10 end below 2^-28.
+// sin and cos of 2 pi t, t formed and reduced in float64: three roundings, 2^-53 of the angle each (2^-31 at an angle of 2^20).
+// What is left is an eighth of a turn on both sides of a quarter; there Taylor's series to x^9 and x^10 end below 2^-28.
 __device__ __forceinline__ void turn(double t, float* sn, float* cs) {
   const double q = __builtin_rint(4.0 * t);
   const float x = (float)((4.0 * t - q) * 1.57079632679489661923);

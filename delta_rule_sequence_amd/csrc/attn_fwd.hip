@@ -5,17 +5,16 @@ namespace prism {
 namespace host {
 namespace {
 
-#ifndef QT_
-#define QT_ 1
-#define NW_ 4
+#ifndef NW_
+#define NW_ 8
 #define BN_ 64
 #define PARTS_ 1
 #endif
 
-template <class T, int D, int QT, int NW, int BN, int PARTS>
+template <class T, int D, int NW, int BN, int PARTS>
 prism_status run(AttnArgs a, hipStream_t stream) {
-  using F = attn::FwdTile<T, D, QT, NW, BN, PARTS, attn::kPrompt>;
-  const auto kernel = attn::fwd_kernel<T, D, QT, NW, BN, PARTS, attn::kPrompt>;
+  using F = attn::FwdTile<T, D, NW, BN, attn::kPrompt>;
+  const auto kernel = attn::fwd_kernel<T, D, NW, BN, PARTS, attn::kPrompt>;
   a.tiles = a.starts != nullptr ? a.T / F::kRows + a.S : a.B * ((a.T + F::kRows - 1) / F::kRows);
   static const bool ok = hipFuncSetAttribute(reinterpret_cast<const void*>(kernel), hipFuncAttributeMaxDynamicSharedMemorySize,
                                              F::kLds) == hipSuccess;
@@ -28,8 +27,8 @@ prism_status run(AttnArgs a, hipStream_t stream) {
 
 prism_status launch_attn_fwd(prism_dtype dt, int D, AttnArgs a, hipStream_t s) {
   if (dt == PRISM_BF16)
-    return D == 32 ? run<bf16_t, 32, QT_, NW_, BN_, PARTS_>(a, s) : D == 64 ? run<bf16_t, 64, QT_, NW_, BN_, PARTS_>(a, s) : run<bf16_t, 128, QT_, NW_, BN_, PARTS_>(a, s);
-  return D == 32 ? run<float, 32, 1, 4, 64, 1>(a, s) : D == 64 ? run<float, 64, 1, 4, 32, 1>(a, s) : run<float, 128, 1, 4, 32, 1>(a, s);
+    return D == 32 ? run<bf16_t, 32, 4, 64, 1>(a, s) : D == 64 ? run<bf16_t, 64, NW_, BN_, PARTS_>(a, s) : run<bf16_t, 128, NW_, BN_, PARTS_>(a, s);
+  return D == 32 ? run<float, 32, 4, 64, 1>(a, s) : D == 64 ? run<float, 64, 4, 32, 1>(a, s) : run<float, 128, 4, 32, 1>(a, s);
 }
 
 }  // namespace host

@@ -18,9 +18,9 @@ template <class T, int D, attn::Keys KEYS>
 prism_status paged(bool few, AttnArgs a, hipStream_t s) {
   using W = attn::FewTile<T, D, KEYS>;
   constexpr int BN = sizeof(T) == 2 || D == 32 ? 64 : 32;
-  using M = attn::FwdTile<T, D, 1, 4, BN, 1, KEYS>;
+  using M = attn::FwdTile<T, D, 4, BN, KEYS>;
   const auto few_rows = attn::few_kernel<T, D, KEYS>;
-  const auto many_rows = attn::fwd_kernel<T, D, 1, 4, BN, 1, KEYS>;
+  const auto many_rows = attn::fwd_kernel<T, D, 4, BN, 1, KEYS>;
   static const bool ok =
       hipFuncSetAttribute(reinterpret_cast<const void*>(few_rows), hipFuncAttributeMaxDynamicSharedMemorySize, W::kLds) == hipSuccess &&
       hipFuncSetAttribute(reinterpret_cast<const void*>(many_rows), hipFuncAttributeMaxDynamicSharedMemorySize, M::kLds) == hipSuccess;

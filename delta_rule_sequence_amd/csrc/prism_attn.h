@@ -206,16 +206,15 @@ __device__ __forceinline__ Seq find_tile(const AttnArgs& a, int slot, int rows, 
 // per row.
 enum Keys { kPrompt, kCache, kCache8 };
 
-// NW waves of 32 QT queries; keys in tiles of BN, two of them in LDS: a tile is stored while the one before is
-// computed on, and its successor is already on the way to registers.
-template <class T, int D, int QT, int NW, int BN, int PARTS, Keys KEYS>
+// NW waves of 32 queries; keys in tiles of BN, three of K and two of V in LDS.  Step t computes on tile t, whose scores
+// begin with those of the step before, stores tile t + 2 of K and t + 1 of V, and asks for the ones behind them.
+template <class T, int D, int NW, int BN, Keys KEYS>
 struct FwdTile {
   using R = Rows<T, D>;
-  static constexpr int kThreads = 64 * NW, kRows = 32 * QT * NW;
-  static constexpr int kPieces = KEYS == kCache8 ? D / 16 : R::kPieces;    // 16-byte pieces of a row in memory
-  static constexpr int kEach = (BN * kPieces + kThreads - 1) / kThreads;   // per thread of one tile
+  static constexpr int kThreads = 64 * NW, kRows = 32 * NW;
   static constexpr int kTile = BN * R::kStride;
-  static constexpr int kLds = 4 * kTile + (KEYS == kCache8 ? 4 * BN * 4 : 0);
+  static constexpr int kScales = KEYS == kCache8 ? 5 * BN * 4 : 0;
+  static constexpr int kLds = 5 * kTile + kScales;
 };
 
 // Eight e4m3 values as bfloat16, exactly.
@@ -229,88 +228,77 @@ __device__ __forceinline__ u32x4 widen8(unsigned lo, unsigned hi) {
   return r;
 }
 
-// A tile's pieces of K and V (and rows' scales) between memory and LDS.
+// A tile's pieces of K or V (and rows' scales) between memory and LDS.
 template <class T, int D, int NT, int BN, Keys KEYS> struct KeyTile {
   using R = Rows<T, D>;
-  using F = FwdTile<T, D, 1, NT / 64, BN, 1, KEYS>;
-  static constexpr int kPieces = F::kPieces, kEach = F::kEach, kStep = NT / kPieces;   // kStep: rows between a thread's pieces
-  static constexpr bool kPart = BN * kPieces < NT;                                     // not every thread has a piece
+  static constexpr int kPieces = KEYS == kCache8 ? D / 16 : R::kPieces;    // 16-byte pieces of a row in memory
+  static constexpr int kEach = (BN * kPieces + NT - 1) / NT;               // per thread
+  static constexpr int kStep = NT / kPieces;                               // rows between a thread's pieces
+  static constexpr bool kPart = BN * kPieces < NT;                         // not every thread has a piece
   static_assert(BN * kPieces % NT == 0 || kPart, "whole pieces");
-  u32x4 k[kEach], v[kEach];
+  static_assert(BN <= NT, "a scale per thread");
+  u32x4 x[kEach];
   float scale;
 
-  __device__ __forceinline__ void load_prompt(const char* kp, const char* vp, int kst, int vst, int t, int n, int tid) {
+  // Rows from p on, n of them in the sequence; what lies behind is zeros.
+  __device__ __forceinline__ void load_prompt(const char* p, int stride, int n, int tid) {
     const int row = tid / kPieces, at = tid % kPieces * 16;
-    const auto rk = rows_of(kp + (long long)t * BN * kst, min(n, BN), kst, R::kBytes);
-    const auto rv = rows_of(vp + (long long)t * BN * vst, min(n, BN), vst, R::kBytes);
+    const auto r = rows_of(p, min(n, BN), stride, R::kBytes);
     if (kPart && row >= BN) return;
 #pragma unroll
-    for (int i = 0; i < kEach; ++i) k[i] = load16(rk, (row + i * kStep) * kst + at);
-#pragma unroll
-    for (int i = 0; i < kEach; ++i) v[i] = load16(rv, (row + i * kStep) * vst + at);
+    for (int i = 0; i < kEach; ++i) x[i] = load16(r, (row + i * kStep) * stride + at);
   }
   // Rows from j0 on of the sequence's pages; rows from `n` on and those of pages outside the cache are zeros.  id: the
   // page that holds the whole tile, where pages are that large.
-  __device__ __forceinline__ void load_cache(const AttnArgs& a, const int* table, int id, int group, int j0, int n, int tid) {
+  __device__ __forceinline__ void load_cache(const AttnArgs& a, const void* cache, const float* scales, const int* table, int id,
+                                             int group, int j0, int n, int tid) {
     const int row = tid / kPieces, at = tid % kPieces * 16, page = 1 << a.page_shift;
     constexpr int kBytes = kPieces * 16;
     if (page >= BN) {
       const bool in = (unsigned)id < (unsigned)a.pages;
       const size_t first = ((size_t)(in ? id : 0) * a.G + group) * page + (j0 & (page - 1));
-      const auto rk = rows_of((const char*)a.cache_k + first * kBytes, in ? min(n - j0, BN) : 0, kBytes, kBytes);
-      const auto rv = rows_of((const char*)a.cache_v + first * kBytes, in ? min(n - j0, BN) : 0, kBytes, kBytes);
+      const auto r = rows_of((const char*)cache + first * kBytes, in ? min(n - j0, BN) : 0, kBytes, kBytes);
       if (!kPart || row < BN) {
 #pragma unroll
-        for (int i = 0; i < kEach; ++i) k[i] = load16(rk, (row + i * kStep) * kBytes + at);
-#pragma unroll
-        for (int i = 0; i < kEach; ++i) v[i] = load16(rv, (row + i * kStep) * kBytes + at);
+        for (int i = 0; i < kEach; ++i) x[i] = load16(r, (row + i * kStep) * kBytes + at);
       }
     } else {
 #pragma unroll
       for (int i = 0; i < kEach; ++i) {
         const int j = j0 + row + i * kStep;
-        k[i] = v[i] = u32x4{0, 0, 0, 0};
+        x[i] = u32x4{0, 0, 0, 0};
         if ((!kPart || row < BN) && j < n) {
           const int p = table[j >> a.page_shift];
-          if ((unsigned)p < (unsigned)a.pages) {
-            const size_t r = ((size_t)p * a.G + group) * page + (j & (page - 1));
-            k[i] = *reinterpret_cast<const u32x4*>((const char*)a.cache_k + r * kBytes + at);
-            v[i] = *reinterpret_cast<const u32x4*>((const char*)a.cache_v + r * kBytes + at);
-          }
+          if ((unsigned)p < (unsigned)a.pages)
+            x[i] = *reinterpret_cast<const u32x4*>((const char*)cache + (((size_t)p * a.G + group) * page + (j & (page - 1))) * kBytes + at);
         }
       }
     }
-    if constexpr (KEYS == kCache8) {                                  // the first BN threads: of K, the next: of V
-      static_assert(2 * BN <= NT, "a scale per thread");
-      const int j = j0 + (tid & (BN - 1));
+    if constexpr (KEYS == kCache8) {
+      const int j = j0 + tid;
       scale = 0.f;
-      if (tid < 2 * BN && j < n) {
+      if (tid < BN && j < n) {
         const int p = page >= BN ? id : table[j >> a.page_shift];
-        if ((unsigned)p < (unsigned)a.pages)
-          scale = (tid < BN ? a.cache_ks : a.cache_vs)[((size_t)p * a.G + group) * page + (j & (page - 1))];
+        if ((unsigned)p < (unsigned)a.pages) scale = scales[((size_t)p * a.G + group) * page + (j & (page - 1))];
       }
     }
   }
-  __device__ __forceinline__ void store(char* kt, char* vt, float* scales, int tid) const {
+  __device__ __forceinline__ void store(char* tile, float* scales, int tid) const {
     const int row = tid / kPieces, at = tid % kPieces;
     if (!kPart || row < BN) {
 #pragma unroll
       for (int i = 0; i < kEach; ++i) {
-        char* const pk = kt + (row + i * kStep) * R::kStride;
-        char* const pv = vt + (row + i * kStep) * R::kStride;
+        char* const p = tile + (row + i * kStep) * R::kStride;
         if constexpr (KEYS == kCache8) {
-          *reinterpret_cast<u32x4*>(pk + at * 32) = widen8(k[i][0], k[i][1]);
-          *reinterpret_cast<u32x4*>(pk + at * 32 + 16) = widen8(k[i][2], k[i][3]);
-          *reinterpret_cast<u32x4*>(pv + at * 32) = widen8(v[i][0], v[i][1]);
-          *reinterpret_cast<u32x4*>(pv + at * 32 + 16) = widen8(v[i][2], v[i][3]);
+          *reinterpret_cast<u32x4*>(p + at * 32) = widen8(x[i][0], x[i][1]);
+          *reinterpret_cast<u32x4*>(p + at * 32 + 16) = widen8(x[i][2], x[i][3]);
         } else {
-          *reinterpret_cast<u32x4*>(pk + at * 16) = k[i];
-          *reinterpret_cast<u32x4*>(pv + at * 16) = v[i];
+          *reinterpret_cast<u32x4*>(p + at * 16) = x[i];
         }
       }
     }
     if constexpr (KEYS == kCache8)
-      if (tid < 2 * BN) scales[tid] = scale;
+      if (tid < BN) scales[tid] = scale;
   }
 };
 
@@ -339,9 +327,9 @@ __device__ __forceinline__ float* share_stats(const AttnArgs& a, int D, size_t r
   return a.part + (size_t)a.splits * a.B * a.H * a.T * D + 2 * row;
 }
 
-template <class T, int D, int QT, int NW, int BN, int PARTS, Keys KEYS>
-__global__ __launch_bounds__(64 * NW, QT * D * (int)sizeof(T) > 256 ? 1 : 2) void fwd_kernel(AttnArgs a) {
-  using F = FwdTile<T, D, QT, NW, BN, PARTS, KEYS>;
+template <class T, int D, int NW, int BN, int PARTS, Keys KEYS>
+__global__ __launch_bounds__(64 * NW, D * (int)sizeof(T) > 256 ? 1 : 2) void fwd_kernel(AttnArgs a) {
+  using F = FwdTile<T, D, NW, BN, KEYS>;
   using R = Rows<T, D>;
   extern __shared__ __align__(16) char lds[];
   constexpr int NT = BN / 32;
@@ -352,7 +340,7 @@ __global__ __launch_bounds__(64 * NW, QT * D * (int)sizeof(T) > 256 ? 1 : 2) voi
   const Seq s = find_tile(a, slot0, F::kRows, a.causal);
   if (s.id < 0) return;
   const int tid = threadIdx.x, l = lane_id(), h = l >> 5, w = uniform(wave_id());
-  const int q0 = s.tile * F::kRows, qw = q0 + w * 32 * QT;            // the block's and the wave's first query
+  const int q0 = s.tile * F::kRows, qw = q0 + w * 32;                 // the block's and the wave's first query
   const long long e = sizeof(T);
   // tokens in front of the first query, and keys altogether
   int past = 0, keys = s.n;
@@ -363,15 +351,13 @@ __global__ __launch_bounds__(64 * NW, QT * D * (int)sizeof(T) > 256 ? 1 : 2) voi
   }
 
   // Q: the second operand of S^T = K Q^T
-  u32x4 qf[QT][R::kSteps];
+  u32x4 qf[R::kSteps];
   {
     const char* p = (const char*)a.q + (s.b * a.qs.b + head * a.qs.h + (long long)(s.first + qw) * a.qs.t) * e;
     const int stride = (int)(a.qs.t * e);
-    const auto r = rows_of(p, min(32 * QT, s.n - qw), stride, R::kBytes);
+    const auto r = rows_of(p, min(32, s.n - qw), stride, R::kBytes);
 #pragma unroll
-    for (int t = 0; t < QT; ++t)
-#pragma unroll
-      for (int k = 0; k < R::kSteps; ++k) qf[t][k] = load16(r, (32 * t + (l & 31)) * stride + (2 * k + h) * 16);
+    for (int k = 0; k < R::kSteps; ++k) qf[k] = load16(r, (l & 31) * stride + (2 * k + h) * 16);
   }
 
   // the block's keys jbeg .. jend - 1, and its share of their tiles
@@ -394,155 +380,149 @@ __global__ __launch_bounds__(64 * NW, QT * D * (int)sizeof(T) > 256 ? 1 : 2) voi
   } else {
     table = a.table + (size_t)s.b * a.max_pages;
   }
-  KeyTile<T, D, F::kThreads, BN, KEYS> next;
+  KeyTile<T, D, F::kThreads, BN, KEYS> nk, nv;
   // the page of a tile, asked for one tile ahead
   const auto page_of = [&](int t) { return KEYS != kPrompt && t < t1 && (1 << a.page_shift) >= BN ? table[t * BN >> a.page_shift] : 0; };
-  int id = page_of(t0);
-  const auto load = [&](int t) {
+  int id = page_of(t0), id_v = 0;
+  const auto load_k = [&](int t) {                                    // in the order of the tiles
     if constexpr (KEYS == kPrompt) {
-      next.load_prompt(kp, vp, kst, vst, t, keys - t * BN, tid);
+      nk.load_prompt(kp + (long long)t * BN * kst, kst, keys - t * BN, tid);
     } else {
-      next.load_cache(a, table, uniform(id), group, t * BN, keys, tid);
+      id_v = uniform(id);
+      nk.load_cache(a, a.cache_k, a.cache_ks, table, id_v, group, t * BN, keys, tid);
       id = page_of(t + 1);
     }
   };
-  if (t0 < t1) load(t0);
+  const auto load_v = [&](int t, int page) {
+    if constexpr (KEYS == kPrompt) nv.load_prompt(vp + (long long)t * BN * vst, vst, keys - t * BN, tid);
+    else nv.load_cache(a, a.cache_v, a.cache_vs, table, page, group, t * BN, keys, tid);
+  };
+  char* const v_tiles = lds + 3 * F::kTile;
+  float* const scales = reinterpret_cast<float*>(lds + 5 * F::kTile);  // three of K, two of V
 
-  f32x16 o[QT][D / 32];
-  float m[QT], sum[QT];
+  f32x16 o[1][D / 32];
+  float m = -kInf, sum = 0.f;
 #pragma unroll
-  for (int t = 0; t < QT; ++t) {
-    m[t] = -kInf, sum[t] = 0.f;
-#pragma unroll
-    for (int d = 0; d < D / 32; ++d) o[t][d] = zero16();
-  }
+  for (int d = 0; d < D / 32; ++d) o[0][d] = zero16();
   const float c = a.scale * kLog2e;
   const int rrow = R::by_rows(l), rcol = R::transposed(l), pw = past + qw;
+  const int i = pw + (l & 31);                                        // this lane's position
+  const int last = a.causal ? min(i, keys - 1) : keys - 1, first = a.window > 0 ? i - a.window + 1 : 0;
+  const int wlast = a.causal ? min(pw + 31, keys - 1) : keys - 1;     // of all of the wave's positions
+  const auto scores = [&](f32x16& x, const char* tile) {
+    x = zero16();
+#pragma unroll
+    for (int k = 0; k < R::kSteps; ++k) mma(x, lds16(tile + rrow + k * 32), qf[k], T());
+  };
 
-  for (int t = t0; t < t1; ++t) {
-    char* kt = lds + (t & 1) * F::kTile;
-    char* vt = kt + 2 * F::kTile;
-    float* scales = reinterpret_cast<float*>(lds + 4 * F::kTile) + (t & 1) * 2 * BN;
-    next.store(kt, vt, scales, tid);
+  f32x16 x[2];                                                        // scores of this 32 keys, and of the next
+  int bk = 0, bv = 0;                                                 // tile t's place in LDS
+  if (t0 < t1) {
+    load_k(t0);
+    const int page0 = id_v;
+    load_v(t0, page0);
+    nk.store(lds, scales, tid);
+    nv.store(v_tiles, scales + 3 * BN, tid);
+    if (t0 + 1 < t1) {
+      load_k(t0 + 1);
+      nk.store(lds + F::kTile, scales + BN, tid);
+      load_v(t0 + 1, id_v);
+    }
+    if (t0 + 2 < t1) load_k(t0 + 2);
     __syncthreads();
-    if (t + 1 < t1) load(t + 1);
-    const int j0 = t * BN;
-    if (a.causal && j0 > pw + 32 * QT - 1) continue;                  // nothing for this wave's queries
-
-    f32x16 x[NT][QT];
-#pragma unroll
-    for (int n = 0; n < NT; ++n)
-#pragma unroll
-      for (int q = 0; q < QT; ++q) x[n][q] = zero16();
-#pragma unroll
-    for (int k = 0; k < R::kSteps; ++k)
-#pragma unroll
-      for (int n = 0; n < NT; ++n) {
-        const u32x4 f = lds16(kt + rrow + n * 32 * R::kStride + k * 32);
-#pragma unroll
-        for (int q = 0; q < QT; ++q) mma(x[n][q], f, qf[q][k], T());
-      }
-    if constexpr (KEYS == kCache8) {
-#pragma unroll
-      for (int n = 0; n < NT; ++n)
-#pragma unroll
-        for (int r = 0; r < 4; ++r) {
-          const f32x4 f = *reinterpret_cast<const f32x4*>(scales + 32 * n + 8 * r + 4 * h);
-#pragma unroll
-          for (int q = 0; q < QT; ++q)
-#pragma unroll
-            for (int u = 0; u < 4; ++u) x[n][q][4 * r + u] *= f[u];
-        }
-    }
-    // keys that not all of the wave's queries see
-    const bool edge = j0 + BN > keys || (a.causal && j0 + BN - 1 > pw) || (a.window > 0 && j0 <= pw + 32 * QT - 1 - a.window);
-    if (edge) {
-#pragma unroll
-      for (int q = 0; q < QT; ++q) {
-        const int i = pw + 32 * q + (l & 31);
-        const int last = (a.causal ? min(i, keys - 1) : keys - 1) - j0 - 4 * h;
-        const int first = (a.window > 0 ? i - a.window + 1 : 0) - j0 - 4 * h;
-#pragma unroll
-        for (int n = 0; n < NT; ++n)
-#pragma unroll
-          for (int r = 0; r < 16; ++r) {
-            const int j = 32 * n + 8 * (r >> 2) + (r & 3);
-            x[n][q][r] = j <= last && j >= first ? x[n][q][r] : -kInf;
-          }
-      }
-    }
-    Operand<T, PARTS> p[NT][QT];
-#pragma unroll
-    for (int q = 0; q < QT; ++q) {
-      float top = -kInf;
-#pragma unroll
-      for (int n = 0; n < NT; ++n)
-#pragma unroll
-        for (int r = 0; r < 16; ++r) top = fmaxf(top, x[n][q][r]);
-      top = both_max(top);
-      const bool grows = top > m[q] && !((top - m[q]) * c <= kSlack);
-      if (__any(grows)) {
-        const float to = grows ? top : m[q];
-        const float f = to == m[q] ? 1.f : __builtin_amdgcn_exp2f((m[q] - to) * c);
-        m[q] = to;
-        sum[q] *= f;
-#pragma unroll
-        for (int d = 0; d < D / 32; ++d) o[q][d] *= f;
-      }
-      float shift = m[q] == -kInf ? 0.f : m[q] * c, by = c;
-      if (__any(fabsf(shift) > kFar)) {
-        const float to = m[q] == -kInf ? 0.f : m[q];
-#pragma unroll
-        for (int n = 0; n < NT; ++n)
-#pragma unroll
-          for (int r = 0; r < 16; ++r) x[n][q][r] = (x[n][q][r] - to) * c;
-        shift = 0.f, by = 1.f;
-      }
-      float part = 0.f;
-#pragma unroll
-      for (int n = 0; n < NT; ++n)
-#pragma unroll
-        for (int r = 0; r < 16; ++r) {
-          x[n][q][r] = __builtin_amdgcn_exp2f(fmaf(x[n][q][r], by, -shift));
-          part += x[n][q][r];
-        }
-      sum[q] += part;
-    }
+    scores(x[0], lds);
+  }
+  for (int t = t0; t < t1; ++t) {
+    if (t > t0) __syncthreads();
+    const int bk1 = bk == 2 ? 0 : bk + 1, bk2 = bk1 == 2 ? 0 : bk1 + 1;
+    if (t + 2 < t1) nk.store(lds + bk2 * F::kTile, scales + bk2 * BN, tid);
+    if (t + 1 < t1) nv.store(v_tiles + (bv ^ 1) * F::kTile, scales + (3 + (bv ^ 1)) * BN, tid);
+    if (t + 2 < t1) load_v(t + 2, id_v);
+    if (t + 3 < t1) load_k(t + 3);
+    const char *kt = lds + bk * F::kTile, *kn = lds + bk1 * F::kTile, *vt = v_tiles + bv * F::kTile;
+    const float *ks = scales + bk * BN, *vs = scales + (3 + bv) * BN;
+    bk = bk1, bv ^= 1;
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
+      const int j0 = t * BN + 32 * n;
+      if (j0 > wlast) break;                                          // nothing for this wave's queries
+      f32x16& y = x[n & 1];
       if constexpr (KEYS == kCache8) {
 #pragma unroll
         for (int r = 0; r < 4; ++r) {
-          const f32x4 f = *reinterpret_cast<const f32x4*>(scales + BN + 32 * n + 8 * r + 4 * h);
+          const f32x4 f = *reinterpret_cast<const f32x4*>(ks + 32 * n + 8 * r + 4 * h);
 #pragma unroll
-          for (int q = 0; q < QT; ++q)
-#pragma unroll
-            for (int u = 0; u < 4; ++u) x[n][q][4 * r + u] *= f[u];
+          for (int u = 0; u < 4; ++u) y[4 * r + u] *= f[u];
         }
       }
+      // keys that not all of the wave's queries see
+      if (j0 + 31 > (a.causal ? min(pw, keys - 1) : keys - 1) || (a.window > 0 && j0 <= pw + 31 - a.window)) {
 #pragma unroll
-      for (int q = 0; q < QT; ++q) p[n][q].set(x[n][q]);
-      mul_transposed<D, PARTS, QT>(o, vt + rcol + n * 32 * R::kStride, p[n]);
+        for (int r = 0; r < 16; ++r) {
+          const int j = 8 * (r >> 2) + (r & 3) + j0 + 4 * h;
+          y[r] = j <= last && j >= first ? y[r] : -kInf;
+        }
+      }
+      float top = -kInf;
+#pragma unroll
+      for (int r = 0; r < 16; ++r) top = fmaxf(top, y[r]);
+      top = both_max(top);
+      const bool grows = top > m && !((top - m) * c <= kSlack);
+      if (__any(grows)) {
+        const float to = grows ? top : m;
+        const float f = to == m ? 1.f : __builtin_amdgcn_exp2f((m - to) * c);
+        m = to;
+        sum *= f;
+#pragma unroll
+        for (int d = 0; d < D / 32; ++d) o[0][d] *= f;
+      }
+      float shift = m == -kInf ? 0.f : m * c, by = c;
+      if (__any(fabsf(shift) > kFar)) {
+        const float to = m == -kInf ? 0.f : m;
+#pragma unroll
+        for (int r = 0; r < 16; ++r) y[r] = (y[r] - to) * c;
+        shift = 0.f, by = 1.f;
+      }
+      // the next keys' scores (behind the last ones: of whatever lies there, unused) beside these keys' exponentials
+      scores(x[(n + 1) & 1], n + 1 < NT ? kt + (n + 1) * 32 * R::kStride : kn);
+      float part = 0.f;
+#pragma unroll
+      for (int r = 0; r < 16; ++r) {
+        y[r] = __builtin_amdgcn_exp2f(fmaf(y[r], by, -shift));
+        part += y[r];
+      }
+      sum += part;
+      if constexpr (KEYS == kCache8) {
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+          const f32x4 f = *reinterpret_cast<const f32x4*>(vs + 32 * n + 8 * r + 4 * h);
+#pragma unroll
+          for (int u = 0; u < 4; ++u) y[4 * r + u] *= f[u];
+        }
+      }
+      Operand<T, PARTS> p[1];
+      p[0].set(y);
+      mul_transposed<D, PARTS, 1>(o, vt + rcol + n * 32 * R::kStride, p);
+    }
+    if constexpr (NT % 2 == 1) {
+      // an odd number of parts: the next scores lie in the other half
+      x[0] = x[1];
     }
   }
 
-#pragma unroll
-  for (int q = 0; q < QT; ++q) {
-    const int i = qw + 32 * q + (l & 31);
-    const float total = both_sum(sum[q]);
-    if (i >= s.n) continue;
-    if (a.splits > 1) {
-      const size_t row = share(a, split, s, head, i);
-      if (h == 0) share_stats(a, D, row)[0] = m[q], share_stats(a, D, row)[1] = total;
-      store_columns<float, D>(reinterpret_cast<char*>(a.part + row * D), o[q], 1.f, h);
-      continue;
-    }
-    // a row without keys: zeros, and a logarithm of -infinity
-    store_columns<T, D>((char*)a.o + (s.b * a.os.b + head * a.os.h + (long long)(s.first + i) * a.os.t) * e, o[q],
-                        total == 0.f ? 0.f : 1.f / total, h);
-    if (a.lse != nullptr && h == 0)
-      a.lse[((long long)s.b * a.H + head) * a.T + s.first + i] = row_lse(m[q], total, a.scale);
+  const int iq = qw + (l & 31);
+  const float total = both_sum(sum);
+  if (iq >= s.n) return;
+  if (a.splits > 1) {
+    const size_t row = share(a, split, s, head, iq);
+    if (h == 0) share_stats(a, D, row)[0] = m, share_stats(a, D, row)[1] = total;
+    store_columns<float, D>(reinterpret_cast<char*>(a.part + row * D), o[0], 1.f, h);
+    return;
   }
+  // a row without keys: zeros, and a logarithm of -infinity
+  store_columns<T, D>((char*)a.o + (s.b * a.os.b + head * a.os.h + (long long)(s.first + iq) * a.os.t) * e, o[0],
+                      total == 0.f ? 0.f : 1.f / total, h);
+  if (a.lse != nullptr && h == 0) a.lse[((long long)s.b * a.H + head) * a.T + s.first + iq] = row_lse(m, total, a.scale);
 }
 
 // Joins the shares of the rows: D / 4 lanes per row, rows [B H T] in order.

@@ -106,11 +106,12 @@ __global__ __launch_bounds__(256, D * (int)sizeof(T) > 256 ? 1 : 2) void few_ker
   char* const kt = lds + w * F::kWave;
   char* const vt = kt + F::kTile;
   float* const scales = reinterpret_cast<float*>(kt + 2 * F::kTile);
-  KeyTile<T, D, 64, 32, KEYS> next;
+  KeyTile<T, D, 64, 32, KEYS> nk, nv;
   const auto page_of = [&](int t) { return t < t1 && a.page_shift >= 5 ? table[t * 32 >> a.page_shift] : 0; };
   int id = page_of(t0 + w);
   const auto load = [&](int t) {
-    next.load_cache(a, table, uniform(id), group, t * 32, keys, l);
+    nk.load_cache(a, a.cache_k, a.cache_ks, table, uniform(id), group, t * 32, keys, l);
+    nv.load_cache(a, a.cache_v, a.cache_vs, table, uniform(id), group, t * 32, keys, l);
     id = page_of(t + 4);
   };
   if (t0 + w < t1) load(t0 + w);
@@ -123,7 +124,8 @@ __global__ __launch_bounds__(256, D * (int)sizeof(T) > 256 ? 1 : 2) void few_ker
   const int rrow = R::by_rows(l), rcol = R::transposed(l);
   const int i = tq < s.n ? past + tq : -1;                             // this lane's position
   for (int t = t0 + w; t < t1; t += 4) {
-    next.store(kt, vt, scales, l);
+    nk.store(kt, scales, l);
+    nv.store(vt, scales + 32, l);
     __builtin_amdgcn_wave_barrier();
     if (t + 4 < t1) load(t + 4);
     f32x16 x = zero16();

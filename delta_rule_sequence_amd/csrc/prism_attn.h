@@ -77,10 +77,17 @@ template <class T, int PARTS> struct Operand {
       if constexpr (PARTS == 2) part[1][i >> 3][i & 7] = (bf16_t)(x[i] - (float)hi);
     }
   }
+  __device__ __forceinline__ void scale(float f) {
+#pragma unroll
+    for (int q = 0; q < PARTS; ++q)
+#pragma unroll
+      for (int i = 0; i < 16; ++i) part[q][i >> 3][i & 7] = (bf16_t)((float)part[q][i >> 3][i & 7] * f);
+  }
 };
 template <int PARTS> struct Operand<float, PARTS> {
   f32x16 x;
   __device__ __forceinline__ void set(const f32x16& v) { x = v; }
+  __device__ __forceinline__ void scale(float f) { x *= f; }
 };
 
 // acc[j][] += (32 rows of D values at `rows`, transposed) * x[j];  at: this lane's place, Rows::transposed.
@@ -206,15 +213,16 @@ __device__ __forceinline__ Seq find_tile(const AttnArgs& a, int slot, int rows, 
 // per row.
 enum Keys { kPrompt, kCache, kCache8 };
 
-// NW waves of 32 queries; keys in tiles of BN, three of K and two of V in LDS.  Step t computes on tile t, whose scores
-// begin with those of the step before, stores tile t + 2 of K and t + 1 of V, and asks for the ones behind them.
+// NW waves of 32 queries; keys in tiles of BN, three of K and three of V in LDS.  Step t computes on tile t, stores
+// tile t + 2 of K and t + 1 of V, and asks for the ones behind them.
 template <class T, int D, int NW, int BN, Keys KEYS>
 struct FwdTile {
   using R = Rows<T, D>;
   static constexpr int kThreads = 64 * NW, kRows = 32 * NW;
   static constexpr int kTile = BN * R::kStride;
-  static constexpr int kScales = KEYS == kCache8 ? 5 * BN * 4 : 0;
-  static constexpr int kLds = 5 * kTile + kScales;
+  static constexpr int kScales = KEYS == kCache8 ? 6 * BN * 4 : 0;
+  static constexpr int kZero = 32 * R::kStride;                        // rows of zeros
+  static constexpr int kLds = 6 * kTile + kZero + kScales;
 };
 
 // Eight e4m3 values as bfloat16, exactly.
@@ -302,9 +310,7 @@ template <class T, int D, int NT, int BN, Keys KEYS> struct KeyTile {
   }
 };
 
-// Past this, a product's rounding moves the exponent 2^t by whole steps (and past 2^31 to infinity): scores and maximum are
-// subtracted before they are scaled.  Below, fmaf(s, c, -m c) costs one instruction, and the rounding of m c is the
-// same for all of a row.
+// Up to this the rounding of m c moves the exponent of a row's p, all alike, by 2^-8 at most (past 2^31: to infinity).
 constexpr float kFar = 65536.f;
 
 // The running maximum moves only when it grows by more than this (in powers of 2): p stays below 2^8, and o is rescaled
@@ -316,6 +322,117 @@ __device__ __forceinline__ float row_lse(float m, float sum, float scale) {
   if (sum == 0.f) return -kInf;
   const float c = scale * kLog2e, log2 = __builtin_amdgcn_logf(sum);
   return fabsf(m * c) > kFar ? m * scale + log2 * kLn2 : (m * c + log2) * kLn2;
+}
+
+// Four neighbouring values of a row of keys or values, times its scale.
+template <class T, Keys KEYS>
+__device__ __forceinline__ f32x4 row4(const char* row, int d, float scale) {
+  f32x4 r;
+  if constexpr (KEYS == kCache8) {
+    const int w = *reinterpret_cast<const int*>(row + d);
+    r[0] = __builtin_amdgcn_cvt_f32_fp8(w, 0), r[1] = __builtin_amdgcn_cvt_f32_fp8(w, 1);
+    r[2] = __builtin_amdgcn_cvt_f32_fp8(w, 2), r[3] = __builtin_amdgcn_cvt_f32_fp8(w, 3);
+#pragma unroll
+    for (int u = 0; u < 4; ++u) r[u] *= scale;
+  } else {
+    T x[4];
+    __builtin_memcpy(x, row + d * (int)sizeof(T), sizeof(x));
+#pragma unroll
+    for (int u = 0; u < 4; ++u) r[u] = (float)x[u];
+  }
+  return r;
+}
+
+// A wave's rows once more, key by key: what a tile does to a row that its keys hide from it (0 times an infinity or a NaN),
+// and scores beyond kFar, call for it.  The scores are those of the tiles, bit for bit: an lse of 10^9 has to meet the same
+// ones in the backward.  The keys: tiles t0, t0 + step, ... < t1 of 32 keys, of n keys altogether, first .. last of them
+// for this lane's row; kp, vp, table as in the kernels.  m, sum and o as the tiles leave them.
+template <class T, int D, Keys KEYS, int STEPS>
+__device__ __forceinline__ void careful_rows(const AttnArgs& a, const u32x4 (&qf)[STEPS], const char* kp, const char* vp, long long kst,
+                                          long long vst, const int* table, int group, int t0, int t1, int step, int n,
+                                          int first, int last, float& m, float& sum, f32x16 (&o)[D / 32]) {
+  const int l = lane_id(), h = l >> 5, page = 1 << a.page_shift;
+  constexpr int kBytes = KEYS == kCache8 ? D : D * (int)sizeof(T);
+  const float c = a.scale * kLog2e;
+  // a row of the cache; -1: of a page outside it
+  const auto row_of = [&](int j) -> long long {
+    const int id = table[j >> a.page_shift];
+    return (unsigned)id < (unsigned)a.pages ? ((long long)id * a.G + group) * page + (j & (page - 1)) : -1;
+  };
+  m = -kInf, sum = 0.f;
+#pragma unroll
+  for (int d = 0; d < D / 32; ++d) o[d] = zero16();
+  for (int t = t0; t < t1; t += step) {
+    f32x16 x = zero16();
+    {
+      const int j = t * 32 + (l & 31);
+      const char* k = j < n ? kp + j * kst : nullptr;
+      float f = 0.f;
+      if constexpr (KEYS != kPrompt) {
+        const long long r = j < n ? row_of(j) : -1;
+        k = r >= 0 ? (const char*)a.cache_k + r * kBytes : nullptr;
+        if constexpr (KEYS == kCache8) f = r >= 0 ? a.cache_ks[r] : 0.f;
+      }
+#pragma unroll
+      for (int i = 0; i < STEPS; ++i) {
+        u32x4 y = {0, 0, 0, 0};
+        if (k != nullptr) {
+          if constexpr (KEYS == kCache8) {
+            unsigned w[2];
+            __builtin_memcpy(w, k + (2 * i + h) * 8, 8);
+            y = widen8(w[0], w[1]);
+          } else {
+            y = *reinterpret_cast<const u32x4*>(k + (2 * i + h) * 16);
+          }
+        }
+        mma(x, y, qf[i], T());
+      }
+      if constexpr (KEYS == kCache8) {
+#pragma unroll
+        for (int r = 0; r < 16; ++r) x[r] *= __shfl(f, 8 * (r >> 2) + 4 * h + (r & 3), 64);
+      }
+    }
+    for (int jj = 0; jj < 32; ++jj) {
+      const int j = t * 32 + jj;
+      const bool in = j >= first && j <= last;
+      if (!__any(in)) continue;
+      float s = 0.f;
+#pragma unroll
+      for (int r = 0; r < 16; ++r) s = r == 4 * (jj >> 3) + (jj & 3) ? x[r] : s;
+      s = __shfl(s, (l & 31) + 32 * (jj >> 2 & 1), 64);
+      const char* v = vp + j * vst;
+      float vs = 1.f;
+      if constexpr (KEYS != kPrompt) {
+        const long long r = row_of(j);
+        v = r >= 0 ? (const char*)a.cache_v + r * kBytes : nullptr;
+        if constexpr (KEYS == kCache8) vs = r >= 0 ? a.cache_vs[r] : 0.f;
+      }
+      if (!in) continue;
+      const float to = fmaxf(m, s), ref = to == -kInf ? 0.f : to;
+      const float f = to == m ? 1.f : __builtin_amdgcn_exp2f((m - ref) * c), p = __builtin_amdgcn_exp2f((s - ref) * c);
+      m = to;
+      sum = fmaf(sum, f, p);
+#pragma unroll
+      for (int d = 0; d < D / 32; ++d)
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+          f32x4 y = zero4();
+          if (v != nullptr) y = row4<T, KEYS>(v, 32 * d + 8 * r + 4 * h, vs);
+#pragma unroll
+          for (int u = 0; u < 4; ++u) o[d][4 * r + u] = o[d][4 * r + u] * f + p * y[u];
+        }
+    }
+  }
+  sum = h == 0 ? sum : 0.f;                                           // both lanes of a row have all of it
+}
+template <int N>
+__device__ __forceinline__ bool finite(const f32x16 (&o)[N]) {
+  bool ok = true;
+#pragma unroll
+  for (int d = 0; d < N; ++d)
+#pragma unroll
+    for (int r = 0; r < 16; ++r) ok &= fabsf(o[d][r]) < kInf;
+  return ok;
 }
 
 // Shares of a row's result that the join kernel adds up: o before its division, and the maximum score and
@@ -398,7 +515,7 @@ __global__ __launch_bounds__(64 * NW, D * (int)sizeof(T) > 256 ? 1 : 2) void fwd
     else nv.load_cache(a, a.cache_v, a.cache_vs, table, page, group, t * BN, keys, tid);
   };
   char* const v_tiles = lds + 3 * F::kTile;
-  float* const scales = reinterpret_cast<float*>(lds + 5 * F::kTile);  // three of K, two of V
+  float* const scales = reinterpret_cast<float*>(lds + 6 * F::kTile + F::kZero);  // three of K, three of V
 
   f32x16 o[1][D / 32];
   float m = -kInf, sum = 0.f;
@@ -415,12 +532,19 @@ __global__ __launch_bounds__(64 * NW, D * (int)sizeof(T) > 256 ? 1 : 2) void fwd
     for (int k = 0; k < R::kSteps; ++k) mma(x, lds16(tile + rrow + k * 32), qf[k], T());
   };
 
-  f32x16 x[2];                                                        // scores of this 32 keys, and of the next
-  int bk = 0, bv = 0;                                                 // tile t's place in LDS
+  // 32 keys after another: while the exponentials of some are formed, the matrix cores form the scores of the next and the
+  // products of the ones before with their values.
+  f32x16 x[2];                                                        // scores of these keys, and of the next
+  Operand<T, PARTS> p[1];                                             // p of the keys before
+  p[0].set(zero16());
+  // and their values: before the first ones and where p is empty, zeros (0 times an infinity would be NaN)
+  char* const zeros = lds + 6 * F::kTile;
+  for (int z = tid * 16; z < F::kZero; z += F::kThreads * 16) *reinterpret_cast<u32x4*>(zeros + z) = u32x4{0, 0, 0, 0};
+  const char* pv = zeros + rcol;
+  int buf = 0;                                                        // tile t's place in LDS
   if (t0 < t1) {
     load_k(t0);
-    const int page0 = id_v;
-    load_v(t0, page0);
+    load_v(t0, id_v);
     nk.store(lds, scales, tid);
     nv.store(v_tiles, scales + 3 * BN, tid);
     if (t0 + 1 < t1) {
@@ -429,23 +553,27 @@ __global__ __launch_bounds__(64 * NW, D * (int)sizeof(T) > 256 ? 1 : 2) void fwd
       load_v(t0 + 1, id_v);
     }
     if (t0 + 2 < t1) load_k(t0 + 2);
-    __syncthreads();
-    scores(x[0], lds);
   }
-  for (int t = t0; t < t1; ++t) {
-    if (t > t0) __syncthreads();
-    const int bk1 = bk == 2 ? 0 : bk + 1, bk2 = bk1 == 2 ? 0 : bk1 + 1;
-    if (t + 2 < t1) nk.store(lds + bk2 * F::kTile, scales + bk2 * BN, tid);
-    if (t + 1 < t1) nv.store(v_tiles + (bv ^ 1) * F::kTile, scales + (3 + (bv ^ 1)) * BN, tid);
+  __syncthreads();
+  if (t0 < t1) scores(x[0], lds);
+  const auto stage = [&](int t, int buf1, int buf2) {
+    if (t + 2 < t1) nk.store(lds + buf2 * F::kTile, scales + buf2 * BN, tid);
+    if (t + 1 < t1) nv.store(v_tiles + buf1 * F::kTile, scales + (3 + buf1) * BN, tid);
     if (t + 2 < t1) load_v(t + 2, id_v);
     if (t + 3 < t1) load_k(t + 3);
-    const char *kt = lds + bk * F::kTile, *kn = lds + bk1 * F::kTile, *vt = v_tiles + bv * F::kTile;
-    const float *ks = scales + bk * BN, *vs = scales + (3 + bv) * BN;
-    bk = bk1, bv ^= 1;
+  };
+  const int tw = min(t1, max(t0, wlast / BN + 1));                    // the wave's own tiles
+  int t = t0;
+  for (; t < tw; ++t) {
+    if (t > t0) __syncthreads();
+    const int buf1 = buf == 2 ? 0 : buf + 1, buf2 = buf1 == 2 ? 0 : buf1 + 1;
+    stage(t, buf1, buf2);
+    const char *kt = lds + buf * F::kTile, *kn = lds + buf1 * F::kTile, *vt = v_tiles + buf * F::kTile;
+    const float *ks = scales + buf * BN, *vs = scales + (3 + buf) * BN;
+    buf = buf1;
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
       const int j0 = t * BN + 32 * n;
-      if (j0 > wlast) break;                                          // nothing for this wave's queries
       f32x16& y = x[n & 1];
       if constexpr (KEYS == kCache8) {
 #pragma unroll
@@ -473,22 +601,19 @@ __global__ __launch_bounds__(64 * NW, D * (int)sizeof(T) > 256 ? 1 : 2) void fwd
         const float f = to == m ? 1.f : __builtin_amdgcn_exp2f((m - to) * c);
         m = to;
         sum *= f;
+        p[0].scale(f);                                                // rounded once more, at 2^-8 of what comes now
 #pragma unroll
         for (int d = 0; d < D / 32; ++d) o[0][d] *= f;
       }
-      float shift = m == -kInf ? 0.f : m * c, by = c;
-      if (__any(fabsf(shift) > kFar)) {
-        const float to = m == -kInf ? 0.f : m;
-#pragma unroll
-        for (int r = 0; r < 16; ++r) y[r] = (y[r] - to) * c;
-        shift = 0.f, by = 1.f;
-      }
-      // the next keys' scores (behind the last ones: of whatever lies there, unused) beside these keys' exponentials
+      const float shift = m == -kInf ? 0.f : m * c;
+      // behind the last keys: scores of whatever lies there, unused
       scores(x[(n + 1) & 1], n + 1 < NT ? kt + (n + 1) * 32 * R::kStride : kn);
+      mul_transposed<D, PARTS, 1>(o, pv, p);
+      pv = vt + rcol + n * 32 * R::kStride;
       float part = 0.f;
 #pragma unroll
       for (int r = 0; r < 16; ++r) {
-        y[r] = __builtin_amdgcn_exp2f(fmaf(y[r], by, -shift));
+        y[r] = __builtin_amdgcn_exp2f(fmaf(y[r], c, -shift));
         part += y[r];
       }
       sum += part;
@@ -500,17 +625,32 @@ __global__ __launch_bounds__(64 * NW, D * (int)sizeof(T) > 256 ? 1 : 2) void fwd
           for (int u = 0; u < 4; ++u) y[4 * r + u] *= f[u];
         }
       }
-      Operand<T, PARTS> p[1];
       p[0].set(y);
-      mul_transposed<D, PARTS, 1>(o, vt + rcol + n * 32 * R::kStride, p);
+#ifdef SGB
+      if constexpr (sizeof(T) == 2) {
+#pragma unroll
+        for (int k = 0; k < R::kSteps + PARTS * D / 16; ++k) {
+          __builtin_amdgcn_sched_group_barrier(0x100, 2, 0);
+          __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+          __builtin_amdgcn_sched_group_barrier(0x002, SGB, 0);
+        }
+      }
+#endif
     }
-    if constexpr (NT % 2 == 1) {
-      // an odd number of parts: the next scores lie in the other half
-      x[0] = x[1];
-    }
+    if constexpr (NT % 2 == 1) x[0] = x[1];
+  }
+  mul_transposed<D, PARTS, 1>(o, pv, p);
+  for (; t < t1; ++t) {                                               // those of the block's other waves
+    if (t > t0) __syncthreads();
+    const int buf1 = buf == 2 ? 0 : buf + 1, buf2 = buf1 == 2 ? 0 : buf1 + 1;
+    stage(t, buf1, buf2);
+    buf = buf1;
+  }
+  const int iq = qw + (l & 31);
+  if (__any(iq < s.n && (!finite(o[0]) || !(fabsf(m * c) <= kFar || m == -kInf)))) {
+    careful_rows<T, D, KEYS>(a, qf, kp, vp, kst, vst, table, group, t0 * NT, t1 * NT, 1, keys, first, iq < s.n ? last : -1, m, sum, o[0]);
   }
 
-  const int iq = qw + (l & 31);
   const float total = both_sum(sum);
   if (iq >= s.n) return;
   if (a.splits > 1) {

@@ -49,7 +49,9 @@ __device__ __forceinline__ float dot(const u32x4& a, const u32x4& b) {
   return s;
 }
 
-// log2 of p from a score and an lse beyond kFar: the score is rounded as lse was, so that equal ones leave 0.
+// Past this, the rounding of lse log2(e) moves p by more than bfloat16's half step.
+constexpr float kFarLse = 65536.f;
+// log2 of p from a score and an lse beyond it: the score is rounded as lse was, so that equal ones leave 0.
 __device__ __forceinline__ float far_exponent(float x, float scale, float lse) {
 #pragma clang fp contract(off)
   const float s = x * scale;
@@ -95,8 +97,8 @@ __global__ __launch_bounds__(64 * NW, D * (int)sizeof(T) > 256 ? 1 : 2) void dq_
   const long long at = ((long long)s.b * a.H + head) * a.T + s.first + i;
   const float given = i < s.n ? a.lse[at] : 0.f;
   if (i < s.n && h == 0) a.delta[at] = delta;
-  // scores and lse beyond kFar are subtracted before they go to powers of 2
-  const bool far = __any(fabsf(given) > kFar && fabsf(given) < kInf);
+  // scores and lse beyond kFarLse are subtracted before they go to powers of 2
+  const bool far = __any(fabsf(given) > kFarLse && fabsf(given) < kInf);
   const float c = far ? 1.f : a.scale * kLog2e, lse = far ? 0.f : given * kLog2e;
 
   const int jend = a.causal ? min(q0 + F::kRows, s.n) : s.n;
@@ -232,11 +234,11 @@ __global__ __launch_bounds__(64 * NW, D * (int)sizeof(T) > 128 ? 1 : 2) void dkv
 #pragma unroll
       for (int r4 = 0; r4 < 4; ++r4) {
         f32x4 lse = *reinterpret_cast<const f32x4*>(rt + 32 * n + 8 * r4 + 4 * h);
-        // scores and lse beyond kFar are subtracted before they go to powers of 2
+        // scores and lse beyond kFarLse are subtracted before they go to powers of 2
         float by = c;
         bool far = false;
 #pragma unroll
-        for (int u = 0; u < 4; ++u) far |= fabsf(lse[u]) > kFar && fabsf(lse[u]) < kInf;
+        for (int u = 0; u < 4; ++u) far |= fabsf(lse[u]) > kFarLse && fabsf(lse[u]) < kInf;
         if (__any(far)) {
 #pragma unroll
           for (int u = 0; u < 4; ++u) x[4 * r4 + u] = far_exponent(x[4 * r4 + u], a.scale, lse[u]), lse[u] = 0.f;

@@ -155,12 +155,7 @@ __global__ __launch_bounds__(256, D * (int)sizeof(T) > 256 ? 1 : 2) void few_ker
 #pragma unroll
       for (int d = 0; d < D / 32; ++d) o[0][d] *= f;
     }
-    float shift = m == -kInf ? 0.f : m * c, by = c;
-    if (__any(fabsf(shift) > kFar)) {
-#pragma unroll
-      for (int k = 0; k < 16; ++k) x[k] = (x[k] - (m == -kInf ? 0.f : m)) * c;
-      shift = 0.f, by = 1.f;
-    }
+    const float shift = m == -kInf ? 0.f : m * c;
 #pragma unroll
     for (int r4 = 0; r4 < 4; ++r4) {
       f32x4 f = {1.f, 1.f, 1.f, 1.f};
@@ -168,7 +163,7 @@ __global__ __launch_bounds__(256, D * (int)sizeof(T) > 256 ? 1 : 2) void few_ker
 #pragma unroll
       for (int u = 0; u < 4; ++u) {
         const int k = 4 * r4 + u;
-        x[k] = __builtin_amdgcn_exp2f(fmaf(x[k], by, -shift));
+        x[k] = __builtin_amdgcn_exp2f(fmaf(x[k], c, -shift));
         sum += x[k];
         if constexpr (KEYS == kCache8) x[k] *= f[u];
       }
@@ -177,6 +172,11 @@ __global__ __launch_bounds__(256, D * (int)sizeof(T) > 256 ? 1 : 2) void few_ker
     p[0].set(x);
     mul_transposed<D, PARTS, 1>(o, vt + rcol, p);
     __builtin_amdgcn_wave_barrier();
+  }
+
+  if (__any(tq < s.n && (!finite(o[0]) || !(fabsf(m * c) <= kFar || m == -kInf)))) {
+    careful_rows<T, D, KEYS>(a, qf, nullptr, nullptr, 0, 0, table, group, t0 + w, t1, 4, keys, a.window > 0 ? i - a.window + 1 : 0,
+                          tq < s.n ? min(i, keys - 1) : -1, m, sum, o[0]);
   }
 
   // the waves' shares through LDS

@@ -262,22 +262,46 @@ def test_one_key_above_all_others(prism, dt, size):
     assert torch.equal(o[0, 0, 5:], v[0, 0, 5].expand(T - 5, D))
 
 
+def by_rows(dt, q, k, v, o, lse=None, window=0, past=0):
+    """Each row against the definition over the keys that it sees, so that non-finite ones reach what they enter only."""
+    for t in range(len(q)):
+        lo, hi = max(0, past + t - window + 1) if window else 0, past + t + 1
+        kk, vv = k[lo:hi], v[lo:hi]
+        if np.isfinite(q[t]).all() and np.isfinite(kk).all() and np.isfinite(vv).all():
+            check_head(f"row {t}", dt, q[t:t + 1], kk, vv, 1 / np.sqrt(q.shape[1]), o[t:t + 1], None if lse is None else lse[t:t + 1], past=hi)
+        elif np.isfinite(q[t]).all() and np.isfinite(kk).all():            # values alone: their columns alone
+            bad = ~np.isfinite(vv).all(0)
+            assert (~np.isfinite(o[t]) == bad).all(), t
+        else:
+            assert np.isnan(o[t]).all(), t
+
+
 @pytest.mark.parametrize("dt", ["bf16", "f32"])
-def test_non_finite_rows_stay_in_their_sequence(prism, dt):
+@pytest.mark.parametrize("window", [0, 20])
+def test_non_finite_rows_reach_what_they_enter(prism, dt, window):
     import torch
     T, D = 200, 64
     r = Rng(15, dt)
     q, k, v = r.vec(2, 2, T, D), r.vec(2, 2, T, D), r.vec(2, 2, T, D)
-    clean = prism.attn_fwd(q, k, v)
+    v[0, 1, 130, 5] = float("inf")
+    v[0, 1, 131, 6] = float("nan")
     k[0, 0, 130] = float("nan")
-    v[0, 1, 130] = float("inf")
+    v[0, 0, 150] = -float("inf")
     q[1, 0, 7] = float("nan")
-    o, lse = prism.attn_fwd(q, k, v)
-    assert torch.equal(o[0, :, :128], clean[0][0, :, :128])            # tokens in front of the row's tile
-    assert torch.isnan(o[0, 0, 130:]).all() and not torch.isfinite(o[0, 1, 130:]).any()
-    assert torch.isnan(o[1, 0, 7]).all() and torch.isnan(lse[1, 0, 7])
-    keep = torch.arange(T, device="cuda") != 7
-    assert torch.equal(o[1, 0, keep], clean[0][1, 0, keep]) and torch.equal(o[1, 1], clean[0][1, 1])
+    v[1, 1, 0] = float("nan")
+    o, lse = prism.attn_fwd(q, k, v, window=window)
+    for b in range(2):
+        for h in range(2):
+            by_rows(dt, *(f64(t[b, h]) for t in (q, k, v, o, lse)), window=window)
+    table, past = i32([[3, 1, 0, 2], [7, 4, 5, 6]]), i32([120, 0])         # the same rows from the cache, and a chunk of them
+    ck, cv = (torch.zeros(8, 2, 64, D, dtype=q.dtype, device="cuda") for _ in range(2))
+    prism.cache_write(ck, cv, k, v, table, i32([0, 0]))
+    for n in (10, 70):
+        c = prism.attn_paged(torch.stack([q[0, :, 120:120 + n], q[1, :, :n]]), ck, cv, table, past, window=window)
+        for b in range(2):
+            for h in range(2):
+                first = [120, 0][b]
+                by_rows(dt, f64(q[b, h, first:first + n]), f64(k[b, h]), f64(v[b, h]), f64(c[b, h]), window=window, past=first)
 
 
 def test_far_strides(prism):

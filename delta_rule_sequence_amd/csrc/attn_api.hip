@@ -99,11 +99,26 @@ prism_status prism_attn_fwd(const void* q, const prism_strides* q_strides, const
   return host::launch_attn_fwd(dt, D, a, stream);
 }
 
-size_t prism_attn_bwd_workspace_bytes(int B, int H, int G, int T, int D, prism_dtype dt) {
-  if (attn_check(B, H, G, T, D, 0, nullptr, nullptr, 1.f, 0, dt) != PRISM_OK) return 0;
+// The pass by keys: a group's heads go to `splits` workgroups where the key tiles alone leave the device empty.
+struct BwdPlan {
+  int splits;
+  size_t part, total;
+};
+static BwdPlan bwd_plan(int B, int H, int G, int T, int D) {
+  BwdPlan pl;
+  const size_t units = (size_t)B * G * (((size_t)T + 127) / 128), rep = (size_t)(H / G);
+  const size_t want = std::min(rep, (2 * kCUs + units - 1) / units), each = (rep + want - 1) / want;
+  pl.splits = (int)((rep + each - 1) / each);
   Layout ly;
   ly.add((size_t)B * H, (size_t)T * 4);
-  return ly.ok() ? ly.total : 0;
+  pl.part = ly.add(pl.splits > 1 ? 2 * (size_t)pl.splits * B * G : 0, (size_t)T * D * 4);
+  pl.total = ly.ok() ? ly.total : 0;
+  return pl;
+}
+
+size_t prism_attn_bwd_workspace_bytes(int B, int H, int G, int T, int D, prism_dtype dt) {
+  if (attn_check(B, H, G, T, D, 0, nullptr, nullptr, 1.f, 0, dt) != PRISM_OK) return 0;
+  return bwd_plan(B, H, G, T, D).total;
 }
 
 prism_status prism_attn_bwd(const void* q, const prism_strides* q_strides, const void* k, const prism_strides* k_strides,
@@ -127,9 +142,9 @@ prism_status prism_attn_bwd(const void* q, const prism_strides* q_strides, const
   if (!scan_rows(q, a.qs, D, dt) || !scan_rows(k, a.ks, D, dt) || !scan_rows(v, a.vs, D, dt) || !scan_rows(o, a.os, D, dt) ||
       !scan_rows(d_o, a.dos, D, dt) || !scan_rows(dq, a.dqs, D, dt) || !scan_rows(dk, a.dks, D, dt) || !scan_rows(dv, a.dvs, D, dt))
     return PRISM_ERR_UNSUPPORTED;
-  const size_t need = prism_attn_bwd_workspace_bytes(B, H, G, T, D, dt);
-  if (need == 0) return PRISM_ERR_INVALID_ARG;
-  if (!workspace || workspace_bytes < need) return PRISM_ERR_WORKSPACE;
+  const BwdPlan pl = bwd_plan(B, H, G, T, D);
+  if (pl.total == 0) return PRISM_ERR_INVALID_ARG;
+  if (!workspace || workspace_bytes < pl.total) return PRISM_ERR_WORKSPACE;
   if (!aligned16(workspace)) return PRISM_ERR_INVALID_ARG;
   // dq is written before the other kernel reads q, k, v and do; dk before other workgroups have read k
   for (const void* in : {q, k, v, o, d_o})
@@ -137,7 +152,8 @@ prism_status prism_attn_bwd(const void* q, const prism_strides* q_strides, const
   a.q = q, a.k = k, a.v = v, a.o = const_cast<void*>(o), a.lse = const_cast<float*>(lse), a.dout = d_o;
   a.lens = lens, a.starts = starts, a.B = B, a.H = H, a.G = G, a.T = T, a.S = S;
   a.causal = causal != 0, a.window = window, a.scale = scale;
-  a.delta = reinterpret_cast<float*>(workspace), a.dq = dq, a.dk = dk, a.dv = dv;
+  a.delta = reinterpret_cast<float*>(workspace), a.part = at<float>(workspace, pl.part), a.splits = pl.splits;
+  a.dq = dq, a.dk = dk, a.dv = dv;
   return host::launch_attn_bwd(dt, D, a, stream);
 }
 

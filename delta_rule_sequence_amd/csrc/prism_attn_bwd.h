@@ -51,18 +51,19 @@ __device__ __forceinline__ float dot(const u32x4& a, const u32x4& b) {
 
 // Past this, the rounding of lse log2(e) moves p by more than bfloat16's half step.
 constexpr float kFarLse = 65536.f;
-// log2 of p from a score and an lse beyond it: the score is rounded as lse was, so that equal ones leave 0.
-__device__ __forceinline__ float far_exponent(float x, float scale, float lse) {
+__device__ __forceinline__ bool is_far(float lse) { return fabsf(lse) > kFarLse && fabsf(lse) < kInf; }
+// p from a score and an lse beyond it: the score is rounded as lse was, so that equal ones leave 0.
+__device__ __forceinline__ float far_p(float x, float scale, float lse) {
 #pragma clang fp contract(off)
   const float s = x * scale;
-  return (s - lse) * kLog2e;
+  return __builtin_amdgcn_exp2f((s - lse) * kLog2e);
 }
 
 template <class T, int D, int NW, int BN> struct BwdTile {
   using R = Rows<T, D>;
   static constexpr int kThreads = 64 * NW, kRows = 32 * NW;
   static constexpr int kTile = BN * R::kStride;
-  static constexpr int kLds = 4 * kTile + 2 * 2 * BN * 4;             // two tiles of two tensors; lse and delta of two
+  static constexpr int kLds = 4 * kTile + 2 * 3 * BN * 4;             // two tiles of two tensors; lse log2(e), delta and lse of two
 };
 
 // dq and delta: a wave owns 32 queries.
@@ -97,9 +98,8 @@ __global__ __launch_bounds__(64 * NW, D * (int)sizeof(T) > 256 ? 1 : 2) void dq_
   const long long at = ((long long)s.b * a.H + head) * a.T + s.first + i;
   const float given = i < s.n ? a.lse[at] : 0.f;
   if (i < s.n && h == 0) a.delta[at] = delta;
-  // scores and lse beyond kFarLse are subtracted before they go to powers of 2
-  const bool far = __any(fabsf(given) > kFarLse && fabsf(given) < kInf);
-  const float c = far ? 1.f : a.scale * kLog2e, lse = far ? 0.f : given * kLog2e;
+  const bool far = __any(is_far(given));
+  const float c = a.scale * kLog2e, lse = given * kLog2e;
 
   const int jend = a.causal ? min(q0 + F::kRows, s.n) : s.n;
   const int jbeg = a.window > 0 ? max(q0 - a.window + 1, 0) : 0;
@@ -138,18 +138,16 @@ __global__ __launch_bounds__(64 * NW, D * (int)sizeof(T) > 256 ? 1 : 2) void dq_
       for (int k = 0; k < R::kSteps; ++k) mma(x, lds16(kt + rrow + n * 32 * R::kStride + k * 32), qf[k], T());
 #pragma unroll
       for (int k = 0; k < R::kSteps; ++k) mma(g, lds16(vt + rrow + n * 32 * R::kStride + k * 32), gf[k], T());
-      if (far) {
+      if (edge || far) {
 #pragma unroll
-        for (int r = 0; r < 16; ++r) x[r] = far_exponent(x[r], a.scale, given);
-      }
-#pragma unroll
-      for (int r = 0; r < 16; ++r) {
-        float p = __builtin_amdgcn_exp2f(fmaf(x[r], c, -lse)) * (g[r] - delta);
-        if (edge) {
+        for (int r = 0; r < 16; ++r) {
           const int j = 32 * n + 8 * (r >> 2) + (r & 3);
-          p = j <= last && j >= first ? p : 0.f;
+          const float p = far ? far_p(x[r], a.scale, given) : __builtin_amdgcn_exp2f(fmaf(x[r], c, -lse));
+          x[r] = j <= last && j >= first ? p * (g[r] - delta) : 0.f;
         }
-        x[r] = p;
+      } else {
+#pragma unroll
+        for (int r = 0; r < 16; ++r) x[r] = __builtin_amdgcn_exp2f(fmaf(x[r], c, -lse)) * (g[r] - delta);
       }
       Operand<T, 1> ds[1];
       ds[0].set(x);
@@ -160,29 +158,34 @@ __global__ __launch_bounds__(64 * NW, D * (int)sizeof(T) > 256 ? 1 : 2) void dq_
     store_columns<T, D>((char*)a.dq + (s.b * a.dqs.b + head * a.dqs.h + (long long)(s.first + i) * a.dqs.t) * e, dq[0], a.scale, h);
 }
 
-// dk and dv: a wave owns 32 keys and takes the queries of the group's heads in turn.
-template <class T, int D, int NW, int BN>
-__global__ __launch_bounds__(64 * NW, D * (int)sizeof(T) > 128 ? 1 : 2) void dkv_kernel(AttnArgs a) {
+// dk and dv: a wave owns 32 keys and takes the queries of the group's heads in turn.  PARTS: which of the two (3: both in one
+// pass; one after the other forms the scores twice, but a wave of wide rows needs more registers for both than it has).
+enum { kDk = 1, kDv = 2 };
+template <class T, int D, int NW, int BN, int PARTS>
+__global__ __launch_bounds__(64 * NW, PARTS == 3 && D * (int)sizeof(T) > 128 ? 1 : 2) void dkv_kernel(AttnArgs a) {
   using F = BwdTile<T, D, NW, BN>;
   using R = Rows<T, D>;
   extern __shared__ __align__(16) char lds[];
   constexpr int NT = BN / 32;
-  const int slot0 = (int)(blockIdx.x / (unsigned)a.G), group = (int)(blockIdx.x - (unsigned)slot0 * a.G);
-  const int rep = a.H / a.G;
+  // the heads of a group go to a.splits workgroups
+  const unsigned unit = blockIdx.x / (unsigned)a.splits, split = blockIdx.x - unit * a.splits;
+  const int slot0 = (int)(unit / (unsigned)a.G), group = (int)(unit - (unsigned)slot0 * a.G);
+  const int rep = a.H / a.G, each = (rep + a.splits - 1) / a.splits, h0 = min((int)split * each, rep), h1 = min(h0 + each, rep);
   const Seq s = find_tile(a, slot0, F::kRows, false);
   if (s.id < 0) return;
   const int tid = threadIdx.x, l = lane_id(), h = l >> 5, w = uniform(wave_id());
   const int j0 = s.tile * F::kRows, jw = j0 + w * 32, j = jw + (l & 31);
   const long long e = sizeof(T);
 
-  u32x4 kf[R::kSteps], vf[R::kSteps];
+  u32x4 kf[R::kSteps], vf[PARTS & kDk ? R::kSteps : 1];
   hold(kf, (const char*)a.k + (s.b * a.ks.b + group * a.ks.h + (long long)(s.first + jw) * a.ks.t) * e, s.n - jw, (int)(a.ks.t * e), l);
-  hold(vf, (const char*)a.v + (s.b * a.vs.b + group * a.vs.h + (long long)(s.first + jw) * a.vs.t) * e, s.n - jw, (int)(a.vs.t * e), l);
+  if constexpr (PARTS & kDk)
+    hold(vf, (const char*)a.v + (s.b * a.vs.b + group * a.vs.h + (long long)(s.first + jw) * a.vs.t) * e, s.n - jw, (int)(a.vs.t * e), l);
 
   // queries ibeg .. iend - 1 of each head, in tiles t0 .. t1 - 1
   const int iend = a.window > 0 ? (int)min((long long)s.n, (long long)min(j0 + F::kRows, s.n) - 1 + a.window) : s.n;
-  const int t0 = (a.causal ? j0 : 0) / BN, t1 = (iend + BN - 1) / BN, per = t1 - t0, steps = per * rep;
-  float* const rows = reinterpret_cast<float*>(lds + 4 * F::kTile);   // [2][lse, delta][BN]
+  const int t0 = (a.causal ? j0 : 0) / BN, t1 = (iend + BN - 1) / BN, steps = (t1 - t0) * (h1 - h0);
+  float* const rows = reinterpret_cast<float*>(lds + 4 * F::kTile);   // [2][lse log2(e), delta, lse][BN]
   Stage<T, D, BN, F::kThreads> sq, sg;
   float row = 0.f;
   const int qst = (int)(a.qs.t * e), gst = (int)(a.dos.t * e);
@@ -199,80 +202,111 @@ __global__ __launch_bounds__(64 * NW, D * (int)sizeof(T) > 128 ? 1 : 2) void dkv
       row = i >= s.n ? (tid < BN ? kInf : 0.f) : tid < BN ? a.lse[at] : a.delta[at];
     }
   };
-  load(0, t0);
+  if (steps > 0) load(h0, t0);
 
-  f32x16 dk[1][D / 32], dv[1][D / 32];
-#pragma unroll
-  for (int d = 0; d < D / 32; ++d) dk[0][d] = zero16(), dv[0][d] = zero16();
+  f32x16 dk[1][PARTS & kDk ? D / 32 : 1], dv[1][PARTS & kDv ? D / 32 : 1];
+  for (auto& x : dk[0]) x = zero16();
+  for (auto& x : dv[0]) x = zero16();
   const float c = a.scale * kLog2e;
   const int rrow = R::by_rows(l), rcol = R::transposed(l);
 
-  int t = t0, head = 0;
+  int t = t0, head = h0;
   for (int step = 0; step < steps; ++step) {
     char* qt = lds + (step & 1) * F::kTile;
     char* gt = qt + 2 * F::kTile;
-    float* rt = rows + (step & 1) * 2 * BN;
+    float* rt = rows + (step & 1) * 3 * BN;
     sq.store(qt, tid);
     sg.store(gt, tid);
-    if (tid < 2 * BN) rt[tid] = row;
+    if (tid < 2 * BN) rt[tid] = tid < BN ? row * kLog2e : row;
+    if (tid < BN) rt[2 * BN + tid] = row;
     __syncthreads();
     const int i0 = t * BN;
     if (++t == t1) t = t0, ++head;
     if (step + 1 < steps) load(head, t);
     if (a.causal && i0 + BN - 1 < jw) continue;
     if (a.window > 0 && i0 > jw + 31 + (long long)a.window - 1) continue;
-    const bool edge = (a.causal && i0 < jw + 31) || (a.window > 0 && i0 + BN - 1 >= jw + (long long)a.window);
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
+      const int i1 = i0 + 32 * n;
       f32x16 x = zero16(), g = zero16();
 #pragma unroll
       for (int k = 0; k < R::kSteps; ++k) mma(x, lds16(qt + rrow + n * 32 * R::kStride + k * 32), kf[k], T());
+      if constexpr (PARTS & kDk) {
 #pragma unroll
-      for (int k = 0; k < R::kSteps; ++k) mma(g, lds16(gt + rrow + n * 32 * R::kStride + k * 32), vf[k], T());
-      const int first = (a.causal ? j : 0) - i0 - 4 * h;
-      const int last = (a.window > 0 ? (int)min((long long)j + a.window - 1, (long long)INT_MAX) : INT_MAX) - i0 - 4 * h;
+        for (int k = 0; k < R::kSteps; ++k) mma(g, lds16(gt + rrow + n * 32 * R::kStride + k * 32), vf[k], T());
+      }
+      const bool edge = (a.causal && i1 < jw + 31) || (a.window > 0 && i1 + 31 >= jw + (long long)a.window);
+      const bool far = __any(is_far(rt[2 * BN + 32 * n + (l & 31)]));
+      if (edge || far) {
+        const int first = (a.causal ? j : 0) - i1 - 4 * h;
+        const int last = (a.window > 0 ? (int)min((long long)j + a.window - 1, (long long)INT_MAX) : INT_MAX) - i1 - 4 * h;
 #pragma unroll
-      for (int r4 = 0; r4 < 4; ++r4) {
-        f32x4 lse = *reinterpret_cast<const f32x4*>(rt + 32 * n + 8 * r4 + 4 * h);
-        // scores and lse beyond kFarLse are subtracted before they go to powers of 2
-        float by = c;
-        bool far = false;
-#pragma unroll
-        for (int u = 0; u < 4; ++u) far |= fabsf(lse[u]) > kFarLse && fabsf(lse[u]) < kInf;
-        if (__any(far)) {
-#pragma unroll
-          for (int u = 0; u < 4; ++u) x[4 * r4 + u] = far_exponent(x[4 * r4 + u], a.scale, lse[u]), lse[u] = 0.f;
-          by = 1.f;
-        } else {
-          lse *= kLog2e;
+        for (int r = 0; r < 16; ++r) {
+          const int i = 8 * (r >> 2) + (r & 3);
+          const float lse = rt[32 * n + i + 4 * h], delta = rt[BN + 32 * n + i + 4 * h];
+          const bool in = i >= first && i <= last;
+          const float p = far ? far_p(x[r], a.scale, rt[2 * BN + 32 * n + i + 4 * h]) : __builtin_amdgcn_exp2f(fmaf(x[r], c, -lse));
+          x[r] = in ? p : 0.f;
+          g[r] = in ? p * (g[r] - delta) : 0.f;
         }
-        const f32x4 delta = *reinterpret_cast<const f32x4*>(rt + BN + 32 * n + 8 * r4 + 4 * h);
+      } else {
 #pragma unroll
-        for (int u = 0; u < 4; ++u) {
-          const int r = 4 * r4 + u;
-          float p = __builtin_amdgcn_exp2f(fmaf(x[r], by, -lse[u]));
-          float ds = p * (g[r] - delta[u]);
-          if (edge) {
-            const int i = 32 * n + 8 * r4 + u;
-            const bool in = i >= first && i <= last;
-            p = in ? p : 0.f;
-            ds = in ? ds : 0.f;
+        for (int r4 = 0; r4 < 4; ++r4) {
+          const f32x4 lse = *reinterpret_cast<const f32x4*>(rt + 32 * n + 8 * r4 + 4 * h);
+          const f32x4 delta = *reinterpret_cast<const f32x4*>(rt + BN + 32 * n + 8 * r4 + 4 * h);
+#pragma unroll
+          for (int u = 0; u < 4; ++u) {
+            const int r = 4 * r4 + u;
+            x[r] = __builtin_amdgcn_exp2f(fmaf(x[r], c, -lse[u]));
+            g[r] = x[r] * (g[r] - delta[u]);
           }
-          x[r] = p;
-          g[r] = ds;
         }
       }
-      Operand<T, 1> p[1], ds[1];
-      p[0].set(x);
-      mul_transposed<D, 1, 1>(dv, gt + rcol + n * 32 * R::kStride, p);
-      ds[0].set(g);
-      mul_transposed<D, 1, 1>(dk, qt + rcol + n * 32 * R::kStride, ds);
+      Operand<T, 1> p[1];
+      if constexpr (PARTS & kDv) {
+        p[0].set(x);
+        mul_transposed<D, 1, 1>(dv, gt + rcol + n * 32 * R::kStride, p);
+      }
+      if constexpr (PARTS & kDk) {
+        p[0].set(g);
+        mul_transposed<D, 1, 1>(dk, qt + rcol + n * 32 * R::kStride, p);
+      }
     }
   }
-  if (j < s.n) {
-    store_columns<T, D>((char*)a.dk + (s.b * a.dks.b + group * a.dks.h + (long long)(s.first + j) * a.dks.t) * e, dk[0], a.scale, h);
-    store_columns<T, D>((char*)a.dv + (s.b * a.dvs.b + group * a.dvs.h + (long long)(s.first + j) * a.dvs.t) * e, dv[0], 1.f, h);
+  if (j >= s.n) return;
+  if (a.splits > 1) {                                                 // [splits][dk, dv][B G T][D], added up by sum_kernel
+    const size_t all = (size_t)a.B * a.G * a.T, at = ((size_t)s.b * a.G + group) * a.T + s.first + j;
+    if constexpr (PARTS & kDk) store_columns<float, D>((char*)(a.part + ((2 * split) * all + at) * D), dk[0], a.scale, h);
+    if constexpr (PARTS & kDv) store_columns<float, D>((char*)(a.part + ((2 * split + 1) * all + at) * D), dv[0], 1.f, h);
+    return;
   }
+  if constexpr (PARTS & kDk)
+    store_columns<T, D>((char*)a.dk + (s.b * a.dks.b + group * a.dks.h + (long long)(s.first + j) * a.dks.t) * e, dk[0], a.scale, h);
+  if constexpr (PARTS & kDv)
+    store_columns<T, D>((char*)a.dv + (s.b * a.dvs.b + group * a.dvs.h + (long long)(s.first + j) * a.dvs.t) * e, dv[0], 1.f, h);
+}
+
+// dk and dv from the shares of the heads: D / 4 lanes per row of one of them, tokens of the sequences only.
+template <class T, int D>
+__global__ __launch_bounds__(256) void sum_kernel(AttnArgs a) {
+  constexpr int L = D / 4;
+  const size_t all = (size_t)a.B * a.G * a.T, row = (size_t)blockIdx.x * (256 / L) + threadIdx.x / L;
+  if (row >= 2 * all) return;
+  const bool of_v = row >= all;
+  const size_t r = of_v ? row - all : row, bg = r / a.T;
+  const int at = threadIdx.x % L * 4, t = (int)(r - bg * a.T), b = (int)(bg / a.G), g = (int)(bg - (size_t)b * a.G);
+  if (a.starts != nullptr) {
+    if (t < a.starts[0] || t >= a.starts[a.S]) return;
+  } else if (a.lens != nullptr && t >= a.lens[b]) {
+    return;
+  }
+  f32x4 y = zero4();
+  for (int k = 0; k < a.splits; ++k) y += *reinterpret_cast<const f32x4*>(a.part + ((2 * k + of_v) * all + r) * D + at);
+  T z[4];
+#pragma unroll
+  for (int u = 0; u < 4; ++u) z[u] = (T)y[u];
+  const prism_strides st = of_v ? a.dvs : a.dks;
+  __builtin_memcpy((char*)(of_v ? a.dv : a.dk) + (b * st.b + g * st.h + (long long)t * st.t + at) * (long long)sizeof(T), z, sizeof(z));
 }
 
 }  // namespace attn

@@ -6,13 +6,14 @@ namespace host {
 namespace {
 
 #ifndef NQ_
-#define NQ_ 4
+#define NQ_ 8
 #define BQ_ 64
-#define NK_ 4
+#define KW_ 4
+#define QW_ 2
 #define BK_ 64
 #endif
 #ifndef ONE_
-#define ONE_ 3
+#define ONE_ 1
 #endif
 
 template <class F>
@@ -21,19 +22,19 @@ bool room(const void* kernel) { return hipFuncSetAttribute(kernel, hipFuncAttrib
 int row_tiles(const AttnArgs& a, int rows) { return a.starts != nullptr ? a.T / rows + a.S : a.B * ((a.T + rows - 1) / rows); }
 
 // PASS: parts of a pass by keys, dk and dv at once (3) or one after the other.
-template <class T, int D, int NQ, int BQ, int NK, int BK, int PASS>
+template <class T, int D, int NQ, int BQ, int KW, int QW, int BK, int PASS>
 prism_status run(const AttnArgs& a, hipStream_t stream) {
   using Q = attn::BwdTile<T, D, NQ, BQ>;
-  using K = attn::BwdTile<T, D, NK, BK>;
+  using K = attn::KeyPass<T, D, KW, QW, BK>;
   constexpr int FIRST = PASS == 3 ? 3 : attn::kDk;
   static const bool ok = room<Q>(reinterpret_cast<const void*>(attn::dq_kernel<T, D, NQ, BQ>)) &&
-                         room<K>(reinterpret_cast<const void*>(attn::dkv_kernel<T, D, NK, BK, FIRST>)) &&
-                         (PASS == 3 || room<K>(reinterpret_cast<const void*>(attn::dkv_kernel<T, D, NK, BK, attn::kDv>)));
+                         room<K>(reinterpret_cast<const void*>(attn::dkv_kernel<T, D, KW, QW, BK, FIRST>)) &&
+                         (PASS == 3 || room<K>(reinterpret_cast<const void*>(attn::dkv_kernel<T, D, KW, QW, BK, attn::kDv>)));
   if (!ok) return PRISM_ERR_HIP;
   attn::dq_kernel<T, D, NQ, BQ><<<dim3(row_tiles(a, Q::kRows) * a.H), Q::kThreads, Q::kLds, stream>>>(a);
-  const dim3 grid(row_tiles(a, K::kRows) * a.G * a.splits);
-  attn::dkv_kernel<T, D, NK, BK, FIRST><<<grid, K::kThreads, K::kLds, stream>>>(a);
-  if constexpr (PASS != 3) attn::dkv_kernel<T, D, NK, BK, attn::kDv><<<grid, K::kThreads, K::kLds, stream>>>(a);
+  const dim3 grid(row_tiles(a, K::kKeys) * a.G * a.splits);
+  attn::dkv_kernel<T, D, KW, QW, BK, FIRST><<<grid, K::kThreads, K::kLds, stream>>>(a);
+  if constexpr (PASS != 3) attn::dkv_kernel<T, D, KW, QW, BK, attn::kDv><<<grid, K::kThreads, K::kLds, stream>>>(a);
   if (a.splits > 1) {
     const size_t rows = 2 * (size_t)a.B * a.G * a.T, per = 256 / (D / 4);
     attn::sum_kernel<T, D><<<dim3((unsigned)((rows + per - 1) / per)), 256, 0, stream>>>(a);
@@ -45,8 +46,8 @@ prism_status run(const AttnArgs& a, hipStream_t stream) {
 
 prism_status launch_attn_bwd(prism_dtype dt, int D, const AttnArgs& a, hipStream_t s) {
   if (dt == PRISM_BF16)
-    return D == 32 ? run<bf16_t, 32, 4, 64, 4, 64, 3>(a, s) : D == 64 ? run<bf16_t, 64, NQ_, BQ_, NK_, BK_, 3>(a, s) : run<bf16_t, 128, NQ_, BQ_, NK_, BK_, ONE_>(a, s);
-  return D == 32 ? run<float, 32, 4, 32, 4, 32, 3>(a, s) : D == 64 ? run<float, 64, 4, 32, 4, 32, 3>(a, s) : run<float, 128, 4, 32, 4, 32, 3>(a, s);
+    return D == 32 ? run<bf16_t, 32, 4, 64, 4, 1, 64, 3>(a, s) : D == 64 ? run<bf16_t, 64, NQ_, BQ_, KW_, QW_, BK_, 3>(a, s) : run<bf16_t, 128, NQ_, BQ_, KW_, QW_, BK_, ONE_>(a, s);
+  return D == 32 ? run<float, 32, 4, 32, 2, 2, 64, 3>(a, s) : D == 64 ? run<float, 64, 4, 32, 2, 2, 64, 3>(a, s) : run<float, 128, 4, 32, 2, 2, 64, 3>(a, s);
 }
 
 }  // namespace host

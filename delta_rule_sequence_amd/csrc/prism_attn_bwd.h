@@ -65,6 +65,12 @@ template <class T, int D, int NW, int BN> struct BwdTile {
   static constexpr int kTile = BN * R::kStride;
   static constexpr int kLds = 4 * kTile + 2 * 3 * BN * 4;             // two tiles of two tensors; lse log2(e), delta and lse of two
 };
+// KW x QW waves: KW of 32 keys each, QW that take a tile's queries by turns.
+template <class T, int D, int KW, int QW, int BN> struct KeyPass : BwdTile<T, D, KW * QW, BN> {
+  static constexpr int kKeys = 32 * KW;
+  static_assert(BN % (32 * QW) == 0, "every wave has queries of a tile");
+  static_assert((QW - 1) * KW * 32 * (D + 4) * 4 <= KeyPass::kLds, "a join fits");
+};
 
 // dq and delta: a wave owns 32 queries.
 template <class T, int D, int NW, int BN>
@@ -161,9 +167,9 @@ __global__ __launch_bounds__(64 * NW, D * (int)sizeof(T) > 256 ? 1 : 2) void dq_
 // dk and dv: a wave owns 32 keys and takes the queries of the group's heads in turn.  PARTS: which of the two (3: both in one
 // pass; one after the other forms the scores twice, but a wave of wide rows needs more registers for both than it has).
 enum { kDk = 1, kDv = 2 };
-template <class T, int D, int NW, int BN, int PARTS>
-__global__ __launch_bounds__(64 * NW, PARTS == 3 && D * (int)sizeof(T) > 128 ? 1 : 2) void dkv_kernel(AttnArgs a) {
-  using F = BwdTile<T, D, NW, BN>;
+template <class T, int D, int KW, int QW, int BN, int PARTS>
+__global__ __launch_bounds__(64 * KW * QW, PARTS == 3 && D * (int)sizeof(T) > 128 ? 1 : 2) void dkv_kernel(AttnArgs a) {
+  using F = KeyPass<T, D, KW, QW, BN>;
   using R = Rows<T, D>;
   extern __shared__ __align__(16) char lds[];
   constexpr int NT = BN / 32;
@@ -171,10 +177,10 @@ __global__ __launch_bounds__(64 * NW, PARTS == 3 && D * (int)sizeof(T) > 128 ? 1
   const unsigned unit = blockIdx.x / (unsigned)a.splits, split = blockIdx.x - unit * a.splits;
   const int slot0 = (int)(unit / (unsigned)a.G), group = (int)(unit - (unsigned)slot0 * a.G);
   const int rep = a.H / a.G, each = (rep + a.splits - 1) / a.splits, h0 = min((int)split * each, rep), h1 = min(h0 + each, rep);
-  const Seq s = find_tile(a, slot0, F::kRows, false);
+  const Seq s = find_tile(a, slot0, F::kKeys, false);
   if (s.id < 0) return;
-  const int tid = threadIdx.x, l = lane_id(), h = l >> 5, w = uniform(wave_id());
-  const int j0 = s.tile * F::kRows, jw = j0 + w * 32, j = jw + (l & 31);
+  const int tid = threadIdx.x, l = lane_id(), h = l >> 5, w = uniform(wave_id()), kw = w % KW, qw = w / KW;
+  const int j0 = s.tile * F::kKeys, jw = j0 + kw * 32, j = jw + (l & 31);
   const long long e = sizeof(T);
 
   u32x4 kf[R::kSteps], vf[PARTS & kDk ? R::kSteps : 1];
@@ -183,7 +189,7 @@ __global__ __launch_bounds__(64 * NW, PARTS == 3 && D * (int)sizeof(T) > 128 ? 1
     hold(vf, (const char*)a.v + (s.b * a.vs.b + group * a.vs.h + (long long)(s.first + jw) * a.vs.t) * e, s.n - jw, (int)(a.vs.t * e), l);
 
   // queries ibeg .. iend - 1 of each head, in tiles t0 .. t1 - 1
-  const int iend = a.window > 0 ? (int)min((long long)s.n, (long long)min(j0 + F::kRows, s.n) - 1 + a.window) : s.n;
+  const int iend = a.window > 0 ? (int)min((long long)s.n, (long long)min(j0 + F::kKeys, s.n) - 1 + a.window) : s.n;
   const int t0 = (a.causal ? j0 : 0) / BN, t1 = (iend + BN - 1) / BN, steps = (t1 - t0) * (h1 - h0);
   float* const rows = reinterpret_cast<float*>(lds + 4 * F::kTile);   // [2][lse log2(e), delta, lse][BN]
   Stage<T, D, BN, F::kThreads> sq, sg;
@@ -223,11 +229,10 @@ __global__ __launch_bounds__(64 * NW, PARTS == 3 && D * (int)sizeof(T) > 128 ? 1
     const int i0 = t * BN;
     if (++t == t1) t = t0, ++head;
     if (step + 1 < steps) load(head, t);
-    if (a.causal && i0 + BN - 1 < jw) continue;
-    if (a.window > 0 && i0 > jw + 31 + (long long)a.window - 1) continue;
 #pragma unroll
-    for (int n = 0; n < NT; ++n) {
-      const int i1 = i0 + 32 * n;
+    for (int m = 0; m < NT / QW; ++m) {
+      const int n = m * QW + qw, i1 = i0 + 32 * n;
+      if ((a.causal && i1 + 31 < jw) || (a.window > 0 && i1 > jw + 31 + (long long)a.window - 1)) continue;
       f32x16 x = zero16(), g = zero16();
 #pragma unroll
       for (int k = 0; k < R::kSteps; ++k) mma(x, lds16(qt + rrow + n * 32 * R::kStride + k * 32), kf[k], T());
@@ -273,7 +278,28 @@ __global__ __launch_bounds__(64 * NW, PARTS == 3 && D * (int)sizeof(T) > 128 ? 1
       }
     }
   }
-  if (j >= s.n) return;
+  // the sums of the waves that share the keys, in their order
+  const auto join = [&](f32x16 (&acc)[D / 32]) {
+    __syncthreads();
+    float* const place = reinterpret_cast<float*>(lds) + ((qw - 1) * KW + kw) * 32 * (D + 4) + (l & 31) * (D + 4);
+    if (qw > 0) store_columns<float, D>(reinterpret_cast<char*>(place), acc, 1.f, h);
+    __syncthreads();
+    if (qw > 0) return;
+    for (int o = 0; o < QW - 1; ++o) {
+      const float* from = reinterpret_cast<const float*>(lds) + (o * KW + kw) * 32 * (D + 4) + (l & 31) * (D + 4);
+#pragma unroll
+      for (int d = 0; d < D / 32; ++d)
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+          const f32x4 y = *reinterpret_cast<const f32x4*>(from + 32 * d + 8 * r + 4 * h);
+#pragma unroll
+          for (int u = 0; u < 4; ++u) acc[d][4 * r + u] += y[u];
+        }
+    }
+  };
+  if constexpr (QW > 1 && (PARTS & kDk)) join(dk[0]);
+  if constexpr (QW > 1 && (PARTS & kDv)) join(dv[0]);
+  if (j >= s.n || qw > 0) return;
   if (a.splits > 1) {                                                 // [splits][dk, dv][B G T][D], added up by sum_kernel
     const size_t all = (size_t)a.B * a.G * a.T, at = ((size_t)s.b * a.G + group) * a.T + s.first + j;
     if constexpr (PARTS & kDk) store_columns<float, D>((char*)(a.part + ((2 * split) * all + at) * D), dk[0], a.scale, h);

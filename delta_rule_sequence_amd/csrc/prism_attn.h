@@ -157,28 +157,39 @@ __device__ __forceinline__ void store_columns(char* row, const f32x16 (&acc)[D /
 struct Seq {
   int b, first, n;     // batch, first token, tokens
   int tile, id;        // row tile within it; the sequence's number (-1: none)
+  int head, group;     // head within its group, group
 };
 
 __device__ __forceinline__ int uniform(int x) { return __builtin_amdgcn_readfirstlane(x); }
 
-// Tile `slot` of all sequences' tiles of `rows` rows, a sequence's last tile first if `back`.  With starts, a wave adds up
+// Unit `unit` of all sequences' tiles of `rows` rows times `rep` heads of G groups; a sequence's last tile first if `back`.
+// The tiles that take longest come first, and blocks that read the same rows of a group lie a multiple of G (where the
+// sequences are batches: of B G) apart: with a multiple of 8 they share an XCD and the rows in its L2.  With starts, a wave adds up
 // the tiles of 64 sequences at a time.
-__device__ __forceinline__ Seq find_tile(const AttnArgs& a, int slot, int rows, bool back) {
+__device__ __forceinline__ Seq find_tile(const AttnArgs& a, unsigned unit, int rows, int rep, bool back) {
   Seq s;
   s.id = -1;
+  const unsigned G = (unsigned)a.G;
   if (a.starts == nullptr) {
-    const int per = (int)(((unsigned)a.T + rows - 1) / rows);
-    s.b = slot / per;
+    const unsigned per = ((unsigned)a.T + rows - 1) / rows, all = (unsigned)a.B * G, tile = unit / (all * rep);
+    unit -= tile * all * rep;
+    s.head = (int)(unit / all);
+    unit -= s.head * all;
+    s.b = (int)(unit / G);
+    s.group = (int)(unit - s.b * G);
     s.first = 0;
     s.n = a.T;
     if (a.lens != nullptr) s.n = min(max(uniform(a.lens[s.b]), 0), a.T);
-    s.tile = slot - s.b * per;
-    if (back) s.tile = per - 1 - s.tile;
+    s.tile = (int)(back ? per - 1 - tile : tile);
     if ((long long)s.tile * rows < s.n) s.id = s.b;
     return s;
   }
+  const unsigned slot = unit / (G * rep);
+  unit -= slot * G * rep;
+  s.head = (int)(unit / G);
+  s.group = (int)(unit - s.head * G);
   s.b = 0;
-  int left = slot;
+  int left = (int)slot;
   for (int base = 0; base < a.S; base += 64) {
     const int i = base + lane_id();
     int first = 0, n = 0;
@@ -451,11 +462,10 @@ __global__ __launch_bounds__(64 * NW, D * (int)sizeof(T) > 256 ? 1 : 2) void fwd
   extern __shared__ __align__(16) char lds[];
   constexpr int NT = BN / 32;
   const unsigned unit = blockIdx.x / (unsigned)a.splits, split = blockIdx.x - unit * a.splits;
-  // heads of a group lie S G blocks apart (or G): with a multiple of 8 they share an XCD and the keys in its L2
-  const int slot0 = (int)(unit / (unsigned)a.H), pair = (int)(unit - (unsigned)slot0 * a.H);
-  const int rep = a.H / a.G, head = (pair % a.G) * rep + pair / a.G, group = pair % a.G;
-  const Seq s = find_tile(a, slot0, F::kRows, a.causal);
+  const int rep = a.H / a.G;
+  const Seq s = find_tile(a, unit, F::kRows, rep, a.causal);
   if (s.id < 0) return;
+  const int group = s.group, head = group * rep + s.head;
   const int tid = threadIdx.x, l = lane_id(), h = l >> 5, w = uniform(wave_id());
   const int q0 = s.tile * F::kRows, qw = q0 + w * 32;                 // the block's and the wave's first query
   const long long e = sizeof(T);

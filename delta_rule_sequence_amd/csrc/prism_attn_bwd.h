@@ -79,10 +79,10 @@ __global__ __launch_bounds__(64 * NW, D * (int)sizeof(T) > 256 ? 1 : 2) void dq_
   using R = Rows<T, D>;
   extern __shared__ __align__(16) char lds[];
   constexpr int NT = BN / 32;
-  const int heads = a.H, slot0 = (int)(blockIdx.x / heads), pair = (int)(blockIdx.x - (unsigned)slot0 * heads);
-  const int rep = a.H / a.G, head = (pair % a.G) * rep + pair / a.G, group = pair % a.G;
-  const Seq s = find_tile(a, slot0, F::kRows, a.causal);
+  const int rep = a.H / a.G;
+  const Seq s = find_tile(a, blockIdx.x, F::kRows, rep, a.causal);
   if (s.id < 0) return;
+  const int group = s.group, head = group * rep + s.head;
   const int tid = threadIdx.x, l = lane_id(), h = l >> 5, w = uniform(wave_id());
   const int q0 = s.tile * F::kRows, qw = q0 + w * 32, i = qw + (l & 31);
   const long long e = sizeof(T);
@@ -175,10 +175,10 @@ __global__ __launch_bounds__(64 * KW * QW, PARTS == 3 && D * (int)sizeof(T) > 12
   constexpr int NT = BN / 32;
   // the heads of a group go to a.splits workgroups
   const unsigned unit = blockIdx.x / (unsigned)a.splits, split = blockIdx.x - unit * a.splits;
-  const int slot0 = (int)(unit / (unsigned)a.G), group = (int)(unit - (unsigned)slot0 * a.G);
   const int rep = a.H / a.G, each = (rep + a.splits - 1) / a.splits, h0 = min((int)split * each, rep), h1 = min(h0 + each, rep);
-  const Seq s = find_tile(a, slot0, F::kKeys, false);
+  const Seq s = find_tile(a, unit, F::kKeys, 1, false);
   if (s.id < 0) return;
+  const int group = s.group;
   const int tid = threadIdx.x, l = lane_id(), h = l >> 5, w = uniform(wave_id()), kw = w % KW, qw = w / KW;
   const int j0 = s.tile * F::kKeys, jw = j0 + kw * 32, j = jw + (l & 31);
   const long long e = sizeof(T);

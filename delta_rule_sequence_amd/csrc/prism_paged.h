@@ -15,16 +15,18 @@ constexpr int kWriteTokens = 16;
 
 template <class T, int D, bool BITS8>
 __global__ __launch_bounds__(256) void cache_write_kernel(AttnArgs a) {
+  const int G = a.G;
   constexpr int V = 16 / (int)sizeof(T), L = D / V;
   typedef T vec __attribute__((ext_vector_type(V)));
-  const Seq s = find_tile(a, (int)blockIdx.x, kWriteTokens, false);
+  a.G = 1;                                                            // tiles of all groups at once
+  const Seq s = find_tile(a, blockIdx.x, kWriteTokens, 1, false);
   if (s.id < 0) return;
   const int t0 = s.tile * kWriteTokens, n = min(kWriteTokens, s.n - t0), at = threadIdx.x % L;
   const long long past = max(a.past[s.id], 0);
   const int* table = a.table + (size_t)s.id * a.max_pages;
   const int page = 1 << a.page_shift;
-  for (int r = threadIdx.x / L; r < n * 2 * a.G; r += 256 / L) {
-    const int g = r % a.G, tk = r / a.G, t = t0 + (tk >> 1);
+  for (int r = threadIdx.x / L; r < n * 2 * G; r += 256 / L) {
+    const int g = r % G, tk = r / G, t = t0 + (tk >> 1);
     const bool key = (tk & 1) == 0;
     const long long p = past + t;
     if (p >> a.page_shift >= a.max_pages) continue;
@@ -32,7 +34,7 @@ __global__ __launch_bounds__(256) void cache_write_kernel(AttnArgs a) {
     if ((unsigned)id >= (unsigned)a.pages) continue;
     const prism_strides st = key ? a.ks : a.vs;
     const vec x = *reinterpret_cast<const vec*>((const T*)(key ? a.k : a.v) + (s.b * st.b + g * st.h + (long long)(s.first + t) * st.t) + at * V);
-    const size_t row = ((size_t)id * a.G + g) * page + (p & (page - 1));
+    const size_t row = ((size_t)id * G + g) * page + (p & (page - 1));
     void* const cache = key ? a.cache_k : a.cache_v;
     if constexpr (!BITS8) {
       *reinterpret_cast<vec*>((T*)cache + row * D + at * V) = x;

@@ -12,6 +12,12 @@ namespace {
 #define QW_ 2
 #define BK_ 64
 #endif
+#ifndef N6_
+#define N6_ 4
+#define K6_ 4
+#define Q6_ 2
+#define B6_ 128
+#endif
 #ifndef ONE_
 #define ONE_ 1
 #endif
@@ -46,7 +52,7 @@ prism_status run(const AttnArgs& a, hipStream_t stream) {
 
 prism_status launch_attn_bwd(prism_dtype dt, int D, const AttnArgs& a, hipStream_t s) {
   if (dt == PRISM_BF16)
-    return D == 32 ? run<bf16_t, 32, 4, 64, 4, 1, 64, 3>(a, s) : D == 64 ? run<bf16_t, 64, NQ_, BQ_, KW_, QW_, BK_, 3>(a, s) : run<bf16_t, 128, NQ_, BQ_, KW_, QW_, BK_, ONE_>(a, s);
+    return D == 32 ? run<bf16_t, 32, 4, 64, 4, 1, 64, 3>(a, s) : D == 64 ? run<bf16_t, 64, N6_, 64, K6_, Q6_, B6_, 3>(a, s) : run<bf16_t, 128, NQ_, BQ_, KW_, QW_, BK_, ONE_>(a, s);
   return D == 32 ? run<float, 32, 4, 32, 2, 2, 64, 3>(a, s) : D == 64 ? run<float, 64, 4, 32, 2, 2, 64, 3>(a, s) : run<float, 128, 4, 32, 2, 2, 64, 3>(a, s);
 }
 

@@ -52,18 +52,23 @@ __device__ __forceinline__ float dot(const u32x4& a, const u32x4& b) {
 // Past this, the rounding of lse log2(e) moves p by more than bfloat16's half step.
 constexpr float kFarLse = 65536.f;
 __device__ __forceinline__ bool is_far(float lse) { return fabsf(lse) > kFarLse && fabsf(lse) < kInf; }
-// p from a score and an lse beyond it: the score is rounded as lse was, so that equal ones leave 0.
-__device__ __forceinline__ float far_p(float x, float scale, float lse) {
+// log2 of p from a score and an lse beyond it: the score is rounded as lse was, so that equal ones leave 0.
+__device__ __forceinline__ float far_exponent(float x, float scale, float lse) {
 #pragma clang fp contract(off)
   const float s = x * scale;
-  return __builtin_amdgcn_exp2f((s - lse) * kLog2e);
+  return (s - lse) * kLog2e;
 }
 
 template <class T, int D, int NW, int BN> struct BwdTile {
   using R = Rows<T, D>;
   static constexpr int kThreads = 64 * NW, kRows = 32 * NW;
   static constexpr int kTile = BN * R::kStride;
-  static constexpr int kLds = 4 * kTile + 2 * 3 * BN * 4;             // two tiles of two tensors; lse log2(e), delta and lse of two
+  // bfloat16: the next rows' two products are formed beside these rows' exponentials, so a tile is in LDS one step ahead.
+  // float32's products take too long to hide anything behind, and its tiles leave no room for a third.
+  static constexpr bool kAhead = sizeof(T) == 2;
+  static constexpr int kTiles = kAhead ? 3 : 2;
+  static constexpr int kRowsAt = 2 * kTiles * kTile;                  // of two tensors; then lse log2(e), delta and lse; zeros
+  static constexpr int kLds = kRowsAt + (kTiles * 3 + 1) * BN * 4;
 };
 // KW x QW waves: KW of 32 keys each, QW that take a tile's queries by turns.
 template <class T, int D, int KW, int QW, int BN> struct KeyPass : BwdTile<T, D, KW * QW, BN> {
@@ -104,8 +109,8 @@ __global__ __launch_bounds__(64 * NW, D * (int)sizeof(T) > 256 ? 1 : 2) void dq_
   const long long at = ((long long)s.b * a.H + head) * a.T + s.first + i;
   const float given = i < s.n ? a.lse[at] : 0.f;
   if (i < s.n && h == 0) a.delta[at] = delta;
-  const bool far = __any(is_far(given));
-  const float c = a.scale * kLog2e, lse = given * kLog2e;
+  const bool far = __any(is_far(given));                              // then the exponents are formed by themselves
+  const float scale = a.scale * kLog2e, c = far ? 1.f : scale, lse = far ? 0.f : given * kLog2e;
 
   const int jend = a.causal ? min(q0 + F::kRows, s.n) : s.n;
   const int jbeg = a.window > 0 ? max(q0 - a.window + 1, 0) : 0;
@@ -114,50 +119,80 @@ __global__ __launch_bounds__(64 * NW, D * (int)sizeof(T) > 256 ? 1 : 2) void dq_
   const int kst = (int)(a.ks.t * e), vst = (int)(a.vs.t * e);
   const char* kp = (const char*)a.k + (s.b * a.ks.b + group * a.ks.h + (long long)s.first * a.ks.t) * e;
   const char* vp = (const char*)a.v + (s.b * a.vs.b + group * a.vs.h + (long long)s.first * a.vs.t) * e;
-  sk.load(kp + (long long)t0 * BN * kst, s.n - t0 * BN, kst, tid);
-  sv.load(vp + (long long)t0 * BN * vst, s.n - t0 * BN, vst, tid);
+  const auto load = [&](int t) {
+    sk.load(kp + (long long)t * BN * kst, s.n - t * BN, kst, tid);
+    sv.load(vp + (long long)t * BN * vst, s.n - t * BN, vst, tid);
+  };
+  char* const v_tiles = lds + F::kTiles * F::kTile;
+  const auto store = [&](int place) {
+    sk.store(lds + place * F::kTile, tid);
+    sv.store(v_tiles + place * F::kTile, tid);
+  };
 
   f32x16 dq[1][D / 32];
 #pragma unroll
   for (int d = 0; d < D / 32; ++d) dq[0][d] = zero16();
   const int rrow = R::by_rows(l), rcol = R::transposed(l);
+  const int last = a.causal ? min(i, s.n - 1) : s.n - 1, first = a.window > 0 ? i - a.window + 1 : 0;
+  const int wlast = a.causal ? min(qw + 31, s.n - 1) : s.n - 1;
+  f32x16 xs[F::kAhead ? 2 : 1], gs[F::kAhead ? 2 : 1];                // s and dp of these 32 keys, and of the next
+  const auto products = [&](f32x16& x, f32x16& g, int at) {
+    x = zero16(), g = zero16();
+#pragma unroll
+    for (int k = 0; k < R::kSteps; ++k) mma(x, lds16(lds + at + rrow + k * 32), qf[k], T());
+#pragma unroll
+    for (int k = 0; k < R::kSteps; ++k) mma(g, lds16(v_tiles + at + rrow + k * 32), gf[k], T());
+  };
 
-  for (int t = t0; t < t1; ++t) {
-    char* kt = lds + (t & 1) * F::kTile;
-    char* vt = kt + 2 * F::kTile;
-    sk.store(kt, tid);
-    sv.store(vt, tid);
-    __syncthreads();
-    const int j0 = t * BN;
-    if (t + 1 < t1) {
-      sk.load(kp + (long long)(t + 1) * BN * kst, s.n - j0 - BN, kst, tid);
-      sv.load(vp + (long long)(t + 1) * BN * vst, s.n - j0 - BN, vst, tid);
+  load(t0);
+  int place = 0;                                                      // tile t's in LDS
+  if constexpr (F::kAhead) {
+    store(0);
+    if (t0 + 1 < t1) {
+      load(t0 + 1);
+      store(1);
     }
-    if (a.causal && j0 > qw + 31) continue;
-    const bool edge = j0 + BN > s.n || (a.causal && j0 + BN - 1 > qw) || (a.window > 0 && j0 <= qw + 31 - a.window);
-    const int last = (a.causal ? min(i, s.n - 1) : s.n - 1) - j0 - 4 * h;
-    const int first = (a.window > 0 ? i - a.window + 1 : 0) - j0 - 4 * h;
+    if (t0 + 2 < t1) load(t0 + 2);
+    __syncthreads();
+    products(xs[0], gs[0], 0);
+  }
+  for (int t = t0; t < t1; ++t) {
+    int next = place + 1 == F::kTiles ? 0 : place + 1;
+    if constexpr (F::kAhead) {
+      if (t > t0) __syncthreads();
+      if (t + 2 < t1) store(next + 1 == F::kTiles ? 0 : next + 1);
+      if (t + 3 < t1) load(t + 3);
+    } else {
+      store(place);
+      __syncthreads();
+      if (t + 1 < t1) load(t + 1);
+    }
+    const int at = place * F::kTile, after = next * F::kTile;
+    place = next;
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
-      f32x16 x = zero16(), g = zero16();
-#pragma unroll
-      for (int k = 0; k < R::kSteps; ++k) mma(x, lds16(kt + rrow + n * 32 * R::kStride + k * 32), qf[k], T());
-#pragma unroll
-      for (int k = 0; k < R::kSteps; ++k) mma(g, lds16(vt + rrow + n * 32 * R::kStride + k * 32), gf[k], T());
+      const int j0 = t * BN + 32 * n;
+      if (j0 > wlast) break;                                          // nothing for this wave's queries
+      f32x16 &x = xs[F::kAhead ? n & 1 : 0], &g = gs[F::kAhead ? n & 1 : 0];
+      if constexpr (!F::kAhead) products(x, g, at + n * 32 * R::kStride);
+      const bool edge = j0 + 31 > (a.causal ? min(qw, s.n - 1) : s.n - 1) || (a.window > 0 && j0 <= qw + 31 - a.window);
       if (edge || far) {
 #pragma unroll
         for (int r = 0; r < 16; ++r) {
-          const int j = 32 * n + 8 * (r >> 2) + (r & 3);
-          const float p = far ? far_p(x[r], a.scale, given) : __builtin_amdgcn_exp2f(fmaf(x[r], c, -lse));
-          x[r] = j <= last && j >= first ? p * (g[r] - delta) : 0.f;
+          const int j = 8 * (r >> 2) + (r & 3) + j0 + 4 * h;
+          const bool in = j <= last && j >= first;
+          if (far) x[r] = is_far(given) ? far_exponent(x[r], a.scale, given) : fmaf(x[r], scale, -given * kLog2e);
+          x[r] = in ? x[r] : -kInf;
+          g[r] = in ? g[r] : 0.f;
         }
-      } else {
-#pragma unroll
-        for (int r = 0; r < 16; ++r) x[r] = __builtin_amdgcn_exp2f(fmaf(x[r], c, -lse)) * (g[r] - delta);
       }
+      if constexpr (F::kAhead)
+        products(xs[(n + 1) & 1], gs[(n + 1) & 1], n + 1 < NT ? at + (n + 1) * 32 * R::kStride : after);
+#pragma unroll
+      for (int r = 0; r < 16; ++r) x[r] = __builtin_amdgcn_exp2f(fmaf(x[r], c, -lse)) * (g[r] - delta);
       Operand<T, 1> ds[1];
       ds[0].set(x);
-      mul_transposed<D, 1, 1>(dq, kt + rcol + n * 32 * R::kStride, ds);
+      mul_transposed<D, 1, 1>(dq, lds + at + rcol + n * 32 * R::kStride, ds);
     }
   }
   if (i < s.n)
@@ -191,92 +226,131 @@ __global__ __launch_bounds__(64 * KW * QW, PARTS == 3 && D * (int)sizeof(T) > 12
   // queries ibeg .. iend - 1 of each head, in tiles t0 .. t1 - 1
   const int iend = a.window > 0 ? (int)min((long long)s.n, (long long)min(j0 + F::kKeys, s.n) - 1 + a.window) : s.n;
   const int t0 = (a.causal ? j0 : 0) / BN, t1 = (iend + BN - 1) / BN, steps = (t1 - t0) * (h1 - h0);
-  float* const rows = reinterpret_cast<float*>(lds + 4 * F::kTile);   // [2][lse log2(e), delta, lse][BN]
+  float* const rows = reinterpret_cast<float*>(lds + F::kRowsAt);     // [kTiles][lse log2(e), delta, lse][BN], zeros [BN]
+  float* const zeros = rows + F::kTiles * 3 * BN;
+  if (tid < BN) zeros[tid] = 0.f;
   Stage<T, D, BN, F::kThreads> sq, sg;
   float row = 0.f;
   const int qst = (int)(a.qs.t * e), gst = (int)(a.dos.t * e);
   const char* qp = (const char*)a.q + (s.b * a.qs.b + (long long)group * rep * a.qs.h + (long long)s.first * a.qs.t) * e;
   const char* gp = (const char*)a.dout + (s.b * a.dos.b + (long long)group * rep * a.dos.h + (long long)s.first * a.dos.t) * e;
-  const auto load = [&](int head, int t) {
-    const int i0 = t * BN;
-    sq.load(qp + (head * a.qs.h * e + (long long)i0 * qst), s.n - i0, qst, tid);
-    sg.load(gp + (head * a.dos.h * e + (long long)i0 * gst), s.n - i0, gst, tid);
+  int lt = t0, lh = h0;                                               // the tile that is loaded next, and its head
+  const auto load = [&]() {
+    const int i0 = lt * BN;
+    sq.load(qp + (lh * a.qs.h * e + (long long)i0 * qst), s.n - i0, qst, tid);
+    sg.load(gp + (lh * a.dos.h * e + (long long)i0 * gst), s.n - i0, gst, tid);
     if (tid < 2 * BN) {
       const int i = i0 + (tid & (BN - 1));
-      const long long at = ((long long)s.b * a.H + group * rep + head) * a.T + s.first + i;
+      const long long at = ((long long)s.b * a.H + group * rep + lh) * a.T + s.first + i;
       // past the last query p is 0
       row = i >= s.n ? (tid < BN ? kInf : 0.f) : tid < BN ? a.lse[at] : a.delta[at];
     }
+    if (++lt == t1) lt = t0, ++lh;
   };
-  if (steps > 0) load(h0, t0);
+  char* const g_tiles = lds + F::kTiles * F::kTile;
+  const auto store = [&](int place) {
+    sq.store(lds + place * F::kTile, tid);
+    sg.store(g_tiles + place * F::kTile, tid);
+    float* const rt = rows + place * 3 * BN;
+    if (tid < 2 * BN) rt[tid] = tid < BN ? row * kLog2e : row;
+    if (tid < BN) rt[2 * BN + tid] = row;
+  };
 
   f32x16 dk[1][PARTS & kDk ? D / 32 : 1], dv[1][PARTS & kDv ? D / 32 : 1];
   for (auto& x : dk[0]) x = zero16();
   for (auto& x : dv[0]) x = zero16();
-  const float c = a.scale * kLog2e;
+  const float scale = a.scale * kLog2e;
   const int rrow = R::by_rows(l), rcol = R::transposed(l);
+  f32x16 xs[F::kAhead ? 2 : 1], gs[F::kAhead ? 2 : 1];                // s and dp of these 32 queries, and of the next
+  const auto products = [&](f32x16& x, f32x16& g, int at) {
+    x = zero16(), g = zero16();
+#pragma unroll
+    for (int k = 0; k < R::kSteps; ++k) mma(x, lds16(lds + at + rrow + k * 32), kf[k], T());
+    if constexpr (PARTS & kDk) {
+#pragma unroll
+      for (int k = 0; k < R::kSteps; ++k) mma(g, lds16(g_tiles + at + rrow + k * 32), vf[k], T());
+    }
+  };
 
-  int t = t0, head = h0;
-  for (int step = 0; step < steps; ++step) {
-    char* qt = lds + (step & 1) * F::kTile;
-    char* gt = qt + 2 * F::kTile;
-    float* rt = rows + (step & 1) * 3 * BN;
-    sq.store(qt, tid);
-    sg.store(gt, tid);
-    if (tid < 2 * BN) rt[tid] = tid < BN ? row * kLog2e : row;
-    if (tid < BN) rt[2 * BN + tid] = row;
+  constexpr int M = NT / QW;                                          // a tile's parts of a wave
+  int place = 0;                                                      // this step's tile in LDS
+  if (steps > 0) load();
+  if constexpr (F::kAhead) {
+    if (steps > 0) store(0);
+    if (steps > 1) {
+      load();
+      store(1);
+    }
+    if (steps > 2) load();
     __syncthreads();
-    const int i0 = t * BN;
-    if (++t == t1) t = t0, ++head;
-    if (step + 1 < steps) load(head, t);
+    products(xs[0], gs[0], qw * 32 * R::kStride);
+  }
+  int t = t0;
+  for (int step = 0; step < steps; ++step) {
+    const int next = place + 1 == F::kTiles ? 0 : place + 1;
+    if constexpr (F::kAhead) {
+      if (step > 0) __syncthreads();
+      if (step + 2 < steps) store(next + 1 == F::kTiles ? 0 : next + 1);
+      if (step + 3 < steps) load();
+    } else {
+      store(place);
+      __syncthreads();
+      if (step + 1 < steps) load();
+    }
+    const int i0 = t * BN, tile = place * F::kTile, after = next * F::kTile;
+    const float* const rt = rows + place * 3 * BN;
+    place = next;
+    if (++t == t1) t = t0;
 #pragma unroll
-    for (int m = 0; m < NT / QW; ++m) {
-      const int n = m * QW + qw, i1 = i0 + 32 * n;
-      if ((a.causal && i1 + 31 < jw) || (a.window > 0 && i1 > jw + 31 + (long long)a.window - 1)) continue;
-      f32x16 x = zero16(), g = zero16();
-#pragma unroll
-      for (int k = 0; k < R::kSteps; ++k) mma(x, lds16(qt + rrow + n * 32 * R::kStride + k * 32), kf[k], T());
-      if constexpr (PARTS & kDk) {
-#pragma unroll
-        for (int k = 0; k < R::kSteps; ++k) mma(g, lds16(gt + rrow + n * 32 * R::kStride + k * 32), vf[k], T());
-      }
+    for (int m = 0; m < M; ++m) {
+      const int n = m * QW + qw, i1 = i0 + 32 * n, at = tile + n * 32 * R::kStride;
+      const int at1 = m + 1 < M ? at + QW * 32 * R::kStride : after + qw * 32 * R::kStride;
+      f32x16 &x = xs[F::kAhead ? m & 1 : 0], &g = gs[F::kAhead ? m & 1 : 0];
+      if constexpr (!F::kAhead)
+        if ((a.causal && i1 + 31 < jw) || (a.window > 0 && i1 > jw + 31 + (long long)a.window - 1)) continue;
+      if constexpr (!F::kAhead) products(x, g, at);
       const bool edge = (a.causal && i1 < jw + 31) || (a.window > 0 && i1 + 31 >= jw + (long long)a.window);
-      const bool far = __any(is_far(rt[2 * BN + 32 * n + (l & 31)]));
+      const bool far = __any(is_far(rt[2 * BN + 32 * n + (l & 31)]));  // then the exponents are formed by themselves
+      const float c = far ? 1.f : scale;
+      const float* const lse2 = far ? zeros : rt;
       if (edge || far) {
         const int first = (a.causal ? j : 0) - i1 - 4 * h;
         const int last = (a.window > 0 ? (int)min((long long)j + a.window - 1, (long long)INT_MAX) : INT_MAX) - i1 - 4 * h;
 #pragma unroll
         for (int r = 0; r < 16; ++r) {
           const int i = 8 * (r >> 2) + (r & 3);
-          const float lse = rt[32 * n + i + 4 * h], delta = rt[BN + 32 * n + i + 4 * h];
           const bool in = i >= first && i <= last;
-          const float p = far ? far_p(x[r], a.scale, rt[2 * BN + 32 * n + i + 4 * h]) : __builtin_amdgcn_exp2f(fmaf(x[r], c, -lse));
-          x[r] = in ? p : 0.f;
-          g[r] = in ? p * (g[r] - delta) : 0.f;
-        }
-      } else {
-#pragma unroll
-        for (int r4 = 0; r4 < 4; ++r4) {
-          const f32x4 lse = *reinterpret_cast<const f32x4*>(rt + 32 * n + 8 * r4 + 4 * h);
-          const f32x4 delta = *reinterpret_cast<const f32x4*>(rt + BN + 32 * n + 8 * r4 + 4 * h);
-#pragma unroll
-          for (int u = 0; u < 4; ++u) {
-            const int r = 4 * r4 + u;
-            x[r] = __builtin_amdgcn_exp2f(fmaf(x[r], c, -lse[u]));
-            g[r] = x[r] * (g[r] - delta[u]);
+          if (far) {
+            const float lse = rt[2 * BN + 32 * n + i + 4 * h];
+            x[r] = is_far(lse) ? far_exponent(x[r], a.scale, lse) : fmaf(x[r], scale, -rt[32 * n + i + 4 * h]);
           }
+          x[r] = in ? x[r] : -kInf;
+          g[r] = in ? g[r] : 0.f;
+        }
+      }
+      if constexpr (F::kAhead) products(xs[(m + 1) & 1], gs[(m + 1) & 1], at1);
+#pragma unroll
+      for (int r4 = 0; r4 < 4; ++r4) {
+        const f32x4 lse = *reinterpret_cast<const f32x4*>(lse2 + 32 * n + 8 * r4 + 4 * h);
+        const f32x4 delta = *reinterpret_cast<const f32x4*>(rt + BN + 32 * n + 8 * r4 + 4 * h);
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+          const int r = 4 * r4 + u;
+          x[r] = __builtin_amdgcn_exp2f(fmaf(x[r], c, -lse[u]));
+          g[r] = x[r] * (g[r] - delta[u]);
         }
       }
       Operand<T, 1> p[1];
       if constexpr (PARTS & kDv) {
         p[0].set(x);
-        mul_transposed<D, 1, 1>(dv, gt + rcol + n * 32 * R::kStride, p);
+        mul_transposed<D, 1, 1>(dv, g_tiles + at + rcol, p);
       }
       if constexpr (PARTS & kDk) {
         p[0].set(g);
-        mul_transposed<D, 1, 1>(dk, qt + rcol + n * 32 * R::kStride, p);
+        mul_transposed<D, 1, 1>(dk, lds + at + rcol, p);
       }
     }
+    if constexpr (F::kAhead && M % 2 == 1) xs[0] = xs[1], gs[0] = gs[1];
   }
   // the sums of the waves that share the keys, in their order
   const auto join = [&](f32x16 (&acc)[D / 32]) {

@@ -24,10 +24,16 @@ ARCH = os.environ.get("PRISM_OFFLOAD_ARCH", "gfx950")
 FLAGS = [f"--offload-arch={ARCH}", "-O3", "-std=c++17", "-fPIC",
          "-I", INCLUDE, "-I", CSRC,
          # packed fp32 VALU ops are kept out of every kernel
-         "-Xclang", "-target-feature", "-Xclang", "-packed-fp32-ops",
-         # the latency-bound kernels (scan, sweep phases) gain from the ILP-first
-         # machine scheduler (measured: scan 19.0 -> 17.1 us at the 16K workload)
-         "-mllvm", "-amdgpu-sched-strategy=max-ilp"]
+         "-Xclang", "-target-feature", "-Xclang", "-packed-fp32-ops"]
+
+# The latency-bound kernels (scan, sweep phases) gain from the ILP-first machine scheduler
+# (measured: scan 19.0 -> 17.1 us at the 16K workload).  The attention kernels lose: their
+# registers are few (backward of 8 x 12 x 2048, 64 wide: 252 us with it, 238 without).
+ILP_FIRST = ["-mllvm", "-amdgpu-sched-strategy=max-ilp"]
+
+
+def flags(source):
+    return FLAGS if os.path.basename(source).startswith("attn_") else FLAGS + ILP_FIRST
 
 
 def hipcc() -> str:
@@ -59,7 +65,7 @@ def build(verbose: bool = False, extra_flags=(), lib_path: str = LIB, obj_dir: s
     sources = sorted(os.path.join(CSRC, f) for f in os.listdir(CSRC) if f.endswith(".hip"))
     os.makedirs(obj_dir, exist_ok=True)
     objs = [os.path.join(obj_dir, os.path.basename(s)[:-4] + ".o") for s in sources]
-    cmds = [[cc, *FLAGS, *extra_flags, "-c", s, "-o", o] for s, o in zip(sources, objs)]
+    cmds = [[cc, *flags(s), *extra_flags, "-c", s, "-o", o] for s, o in zip(sources, objs)]
     with ThreadPoolExecutor(_jobs()) as ex:
         list(ex.map(lambda c: _run(c, verbose), cmds))
     tmp = lib_path + ".tmp"

@@ -26,6 +26,7 @@ prism_status attn_check(int B, int H, int G, int T, int D, int S, const int* len
   if (starts != nullptr ? (S <= 0 || B != 1 || lens != nullptr) : S != 0) return PRISM_ERR_INVALID_ARG;
   if (!attn_width(D) || T > INT_MAX - 4096) return PRISM_ERR_UNSUPPORTED;
   const size_t tiles = starts != nullptr ? (size_t)T / 32 + S : (size_t)B * (((size_t)T + 31) / 32);
+  if (H > 65535 || (long long)T * (H / G) > INT_MAX - 4096) return PRISM_ERR_UNSUPPORTED;  // a group's rows are counted in 31 bits
   return tiles > ((size_t)1 << 23) / H ? PRISM_ERR_UNSUPPORTED : PRISM_OK;
 }
 

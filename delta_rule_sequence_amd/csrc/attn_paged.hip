@@ -15,7 +15,7 @@ prism_status write(const AttnArgs& a, hipStream_t s) {
 }
 
 template <class T, int D, attn::Keys KEYS>
-prism_status paged(bool few, AttnArgs a, hipStream_t s) {
+prism_status paged(bool few, const AttnArgs& a, hipStream_t s) {
   using W = attn::FewTile<T, D, KEYS>;
   constexpr int BN = sizeof(T) == 2 || D == 32 ? 64 : 32;
   using M = attn::FwdTile<T, D, 4, BN, KEYS>;
@@ -25,13 +25,8 @@ prism_status paged(bool few, AttnArgs a, hipStream_t s) {
       hipFuncSetAttribute(reinterpret_cast<const void*>(few_rows), hipFuncAttributeMaxDynamicSharedMemorySize, W::kLds) == hipSuccess &&
       hipFuncSetAttribute(reinterpret_cast<const void*>(many_rows), hipFuncAttributeMaxDynamicSharedMemorySize, M::kLds) == hipSuccess;
   if (!ok) return PRISM_ERR_HIP;
-  if (few) {
-    a.tiles = (a.T * (a.H / a.G) + 31) / 32;
-    few_rows<<<dim3(a.B * a.G * a.tiles * a.splits), 256, W::kLds, s>>>(a);
-  } else {
-    a.tiles = row_tiles(a, M::kRows);
-    many_rows<<<dim3(a.tiles * a.H * a.splits), M::kThreads, M::kLds, s>>>(a);
-  }
+  if (few) few_rows<<<dim3(a.B * a.G * ((a.T * (a.H / a.G) + 31) / 32) * a.splits), 256, W::kLds, s>>>(a);
+  else many_rows<<<dim3(row_tiles(a, M::kRows) * a.H * a.splits), M::kThreads, M::kLds, s>>>(a);
   if (a.splits > 1) {
     const size_t rows = (size_t)a.B * a.H * a.T, per = 256 / (D / 4);
     attn::join_kernel<T, D><<<dim3((unsigned)((rows + per - 1) / per)), 256, 0, s>>>(a);

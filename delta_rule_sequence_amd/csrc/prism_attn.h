@@ -162,16 +162,16 @@ struct Seq {
 
 __device__ __forceinline__ int uniform(int x) { return __builtin_amdgcn_readfirstlane(x); }
 
-// Unit `unit` of all sequences' tiles of `rows` rows times `rep` heads of G groups; a sequence's last tile first if `back`.
+// Unit `unit` of all sequences' tiles of `rows` rows, `each` rows per token, times `rep` heads of G groups; a sequence's last tile first if `back`.
 // The tiles that take longest come first, and blocks that read the same rows of a group lie a multiple of G (where the
 // sequences are batches: of B G) apart: with a multiple of 8 they share an XCD and the rows in its L2.  With starts, a wave adds up
 // the tiles of 64 sequences at a time.
-__device__ __forceinline__ Seq find_tile(const AttnArgs& a, unsigned unit, int rows, int rep, bool back) {
+__device__ __forceinline__ Seq find_tile(const AttnArgs& a, unsigned unit, int rows, int rep, bool back, int each = 1) {
   Seq s;
   s.id = -1;
   const unsigned G = (unsigned)a.G;
   if (a.starts == nullptr) {
-    const unsigned per = ((unsigned)a.T + rows - 1) / rows, all = (unsigned)a.B * G, tile = unit / (all * rep);
+    const unsigned per = ((unsigned)a.T * each + rows - 1) / rows, all = (unsigned)a.B * G, tile = unit / (all * rep);
     unit -= tile * all * rep;
     s.head = (int)(unit / all);
     unit -= s.head * all;
@@ -181,7 +181,7 @@ __device__ __forceinline__ Seq find_tile(const AttnArgs& a, unsigned unit, int r
     s.n = a.T;
     if (a.lens != nullptr) s.n = min(max(uniform(a.lens[s.b]), 0), a.T);
     s.tile = (int)(back ? per - 1 - tile : tile);
-    if ((long long)s.tile * rows < s.n) s.id = s.b;
+    if ((long long)s.tile * rows < (long long)s.n * each) s.id = s.b;
     return s;
   }
   const unsigned slot = unit / (G * rep);
@@ -197,7 +197,7 @@ __device__ __forceinline__ Seq find_tile(const AttnArgs& a, unsigned unit, int r
       first = min(max(a.starts[i], 0), a.T);
       n = max(min(a.starts[i + 1], a.T) - first, 0);
     }
-    const int tiles = (int)(((unsigned)n + rows - 1) / rows);
+    const int tiles = (int)(((unsigned)n * each + rows - 1) / rows);
     int upto = tiles;
 #pragma unroll
     for (int o = 1; o < 64; o <<= 1) {
@@ -210,7 +210,7 @@ __device__ __forceinline__ Seq find_tile(const AttnArgs& a, unsigned unit, int r
       s.first = __builtin_amdgcn_readlane(first, j);
       s.n = __builtin_amdgcn_readlane(n, j);
       const int end = __builtin_amdgcn_readlane(upto, j);
-      s.tile = back ? end - 1 - left : left - end + (int)(((unsigned)s.n + rows - 1) / rows);
+      s.tile = back ? end - 1 - left : left - end + (int)(((unsigned)s.n * each + rows - 1) / rows);
       s.id = base + j;
       return s;
     }
@@ -673,6 +673,191 @@ __global__ __launch_bounds__(64 * NW, D * (int)sizeof(T) > 256 ? 1 : 2) void fwd
   store_columns<T, D>((char*)a.o + (s.b * a.os.b + head * a.os.h + (long long)(s.first + iq) * a.os.t) * e, o[0],
                       total == 0.f ? 0.f : 1.f / total, h);
   if (a.lse != nullptr && h == 0) a.lse[((long long)s.b * a.H + head) * a.T + s.first + iq] = row_lse(m, total, a.scale);
+}
+
+// ---- few rows of queries --------------------------------------------------------------------------------
+// The rows of a group's heads, token by token, lie in tiles of 32 rows, so that keys are read once for all of them.  Four
+// waves take every fourth tile of 32 keys each, in LDS of their own, with a maximum, a sum and an o of their own, and join them
+// at the end.  For single tokens, and for prompts that are too short to fill the device with a workgroup per 128 rows.
+template <class T, int D, Keys KEYS> struct FewTile {
+  using R = Rows<T, D>;
+  static constexpr int kTile = 32 * R::kStride;
+  static constexpr int kWave = 2 * kTile + (KEYS == kCache8 ? 64 * 4 : 0);   // keys, values, scales
+  static constexpr int kOut = (D + 4) * 4;                                    // a row of o on its way to the join
+  static constexpr int kLds = 4 * kWave;
+  static_assert(32 * kOut + 64 * 4 <= kWave, "the join fits");
+};
+
+template <class T, int D, Keys KEYS>
+__global__ __launch_bounds__(256, D * (int)sizeof(T) > 256 ? 1 : 2) void few_kernel(AttnArgs a) {
+  using F = FewTile<T, D, KEYS>;
+  using R = Rows<T, D>;
+  constexpr int PARTS = 2;                                             // bound by bytes or latency: both are free
+  extern __shared__ __align__(16) char lds[];
+  const unsigned unit = blockIdx.x / (unsigned)a.splits, split = blockIdx.x - unit * a.splits;
+  const int rep = a.H / a.G;
+  const Seq s = find_tile(a, unit, 32, 1, a.causal, rep);
+  if (s.id < 0) return;
+  const int group = s.group, tile = s.tile, b = s.b;
+  const int first = tile * 32 / rep, lastq = min((tile * 32 + 31) / rep, s.n - 1);
+  const int tid = threadIdx.x, l = lane_id(), h = l >> 5, w = uniform(wave_id());
+  const int r = tile * 32 + (l & 31), tq = r / rep, head = group * rep + (r - tq * rep);
+  int past = 0, keys = s.n;
+  if constexpr (KEYS != kPrompt) {
+    const int room = a.max_pages << a.page_shift;
+    past = min(max(uniform(a.past[b]), 0), room);
+    keys = min(past + s.n, room);
+  }
+  const int jend = a.causal ? min(past + lastq + 1, keys) : keys, jbeg = a.window > 0 ? max(past + first - a.window + 1, 0) : 0;
+  int t0 = jbeg / 32, t1 = max((jend + 31) / 32, t0);
+  {
+    const int per = (t1 - t0 + a.splits - 1) / a.splits;
+    t0 = min(t0 + (int)split * per, t1);
+    t1 = min(t0 + per, t1);
+  }
+  const long long e = sizeof(T);
+  const int kst = (int)(a.ks.t * e), vst = (int)(a.vs.t * e);
+  const char *kp = nullptr, *vp = nullptr;
+  const int* table = nullptr;
+  if constexpr (KEYS == kPrompt) {
+    kp = (const char*)a.k + (b * a.ks.b + group * a.ks.h + (long long)s.first * a.ks.t) * e;
+    vp = (const char*)a.v + (b * a.vs.b + group * a.vs.h + (long long)s.first * a.vs.t) * e;
+  } else {
+    table = a.table + (size_t)b * a.max_pages;
+  }
+
+  u32x4 qf[R::kSteps];
+#pragma unroll
+  for (int k = 0; k < R::kSteps; ++k) {
+    qf[k] = u32x4{0, 0, 0, 0};
+    if (tq < s.n)
+      qf[k] = *reinterpret_cast<const u32x4*>((const char*)a.q + (b * a.qs.b + head * a.qs.h + (long long)(s.first + tq) * a.qs.t) * e +
+                                              (2 * k + h) * 16);
+  }
+  char* const kt = lds + w * F::kWave;
+  char* const vt = kt + F::kTile;
+  float* const scales = reinterpret_cast<float*>(kt + 2 * F::kTile);
+  KeyTile<T, D, 64, 32, KEYS> nk, nv;
+  const auto page_of = [&](int t) { return KEYS != kPrompt && t < t1 && a.page_shift >= 5 ? table[t * 32 >> a.page_shift] : 0; };
+  int id = page_of(t0 + w);
+  const auto load = [&](int t) {
+    if constexpr (KEYS == kPrompt) {
+      nk.load_prompt(kp + (long long)t * 32 * kst, kst, keys - t * 32, l);
+      nv.load_prompt(vp + (long long)t * 32 * vst, vst, keys - t * 32, l);
+    } else {
+      nk.load_cache(a, a.cache_k, a.cache_ks, table, uniform(id), group, t * 32, keys, l);
+      nv.load_cache(a, a.cache_v, a.cache_vs, table, uniform(id), group, t * 32, keys, l);
+      id = page_of(t + 4);
+    }
+  };
+  if (t0 + w < t1) load(t0 + w);
+
+  f32x16 o[1][D / 32];
+#pragma unroll
+  for (int d = 0; d < D / 32; ++d) o[0][d] = zero16();
+  float m = -kInf, sum = 0.f;
+  const float c = a.scale * kLog2e;
+  const int rrow = R::by_rows(l), rcol = R::transposed(l);
+  const int i = tq < s.n ? past + tq : -1;                             // this lane's position
+  for (int t = t0 + w; t < t1; t += 4) {
+    nk.store(kt, scales, l);
+    nv.store(vt, scales + 32, l);
+    __builtin_amdgcn_wave_barrier();
+    if (t + 4 < t1) load(t + 4);
+    f32x16 x = zero16();
+#pragma unroll
+    for (int k = 0; k < R::kSteps; ++k) mma(x, lds16(kt + rrow + k * 32), qf[k], T());
+    const int last = (a.causal ? min(i, keys - 1) : keys - 1) - t * 32 - 4 * h, from = (a.window > 0 ? i - a.window + 1 : 0) - t * 32 - 4 * h;
+    float top = -kInf;
+#pragma unroll
+    for (int r4 = 0; r4 < 4; ++r4) {
+      f32x4 f = {1.f, 1.f, 1.f, 1.f};
+      if constexpr (KEYS == kCache8) f = *reinterpret_cast<const f32x4*>(scales + 8 * r4 + 4 * h);
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+        const int j = 8 * r4 + u, k = 4 * r4 + u;
+        if constexpr (KEYS == kCache8) x[k] *= f[u];
+        x[k] = j <= last && j >= from ? x[k] : -kInf;
+        top = fmaxf(top, x[k]);
+      }
+    }
+    top = both_max(top);
+    const bool grows = top > m && !((top - m) * c <= kSlack);
+    if (__any(grows)) {
+      const float to = grows ? top : m;
+      const float f = to == m ? 1.f : __builtin_amdgcn_exp2f((m - to) * c);
+      m = to;
+      sum *= f;
+#pragma unroll
+      for (int d = 0; d < D / 32; ++d) o[0][d] *= f;
+    }
+    const float shift = m == -kInf ? 0.f : m * c;
+#pragma unroll
+    for (int r4 = 0; r4 < 4; ++r4) {
+      f32x4 f = {1.f, 1.f, 1.f, 1.f};
+      if constexpr (KEYS == kCache8) f = *reinterpret_cast<const f32x4*>(scales + 32 + 8 * r4 + 4 * h);
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+        const int k = 4 * r4 + u;
+        x[k] = __builtin_amdgcn_exp2f(fmaf(x[k], c, -shift));
+        sum += x[k];
+        if constexpr (KEYS == kCache8) x[k] *= f[u];
+      }
+    }
+    Operand<T, PARTS> p[1];
+    p[0].set(x);
+    mul_transposed<D, PARTS, 1>(o, vt + rcol, p);
+    __builtin_amdgcn_wave_barrier();
+  }
+
+  if (__any(tq < s.n && (!finite(o[0]) || !(fabsf(m * c) <= kFar || m == -kInf)))) {
+    careful_rows<T, D, KEYS>(a, qf, kp, vp, kst, vst, table, group, t0 + w, t1, 4, keys, a.window > 0 ? i - a.window + 1 : 0,
+                          tq >= s.n ? -1 : a.causal ? min(i, keys - 1) : keys - 1, m, sum, o[0]);
+  }
+
+  // the waves' shares through LDS
+  const float total = both_sum(sum);
+  store_columns<float, D>(kt + (l & 31) * F::kOut, o[0], 1.f, h);
+  float* const stats = reinterpret_cast<float*>(kt + 32 * F::kOut);
+  if (h == 0) stats[2 * (l & 31)] = m, stats[2 * (l & 31) + 1] = total;
+  __syncthreads();
+  const int row = tid >> 3, rr = tile * 32 + row, t = rr / rep, hd = group * rep + (rr - t * rep);
+  if (t >= s.n) return;
+  float mj = -kInf, sj = 0.f, f[4];
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    const float* st = reinterpret_cast<const float*>(lds + k * F::kWave + 32 * F::kOut) + 2 * row;
+    if (st[1] != 0.f) mj = fmaxf(mj, st[0]);
+  }
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    const float* st = reinterpret_cast<const float*>(lds + k * F::kWave + 32 * F::kOut) + 2 * row;
+    f[k] = st[1] == 0.f ? 0.f : __builtin_amdgcn_exp2f((st[0] - mj) * c);
+    sj += f[k] * st[1];
+  }
+  const size_t at = share(a, split, s, hd, t);
+  if (a.splits > 1 && (tid & 7) == 0) share_stats(a, D, at)[0] = mj, share_stats(a, D, at)[1] = sj;
+  const float by = a.splits > 1 ? 1.f : sj == 0.f ? 0.f : 1.f / sj;
+  if (a.splits == 1 && a.lse != nullptr && (tid & 7) == 0) a.lse[((long long)b * a.H + hd) * a.T + s.first + t] = row_lse(mj, sj, a.scale);
+#pragma unroll
+  for (int d = 0; d < D / 32; ++d) {
+    const int col = 32 * d + (tid & 7) * 4;
+    f32x4 y = zero4();
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const f32x4 v = *reinterpret_cast<const f32x4*>(lds + k * F::kWave + row * F::kOut + col * 4);
+#pragma unroll
+      for (int u = 0; u < 4; ++u) y[u] = fmaf(f[k], v[u], y[u]);
+    }
+    if (a.splits > 1) {
+      *reinterpret_cast<f32x4*>(a.part + at * D + col) = y;
+    } else {
+      T z[4];
+#pragma unroll
+      for (int u = 0; u < 4; ++u) z[u] = (T)(y[u] * by);
+      __builtin_memcpy((char*)a.o + (b * a.os.b + hd * a.os.h + (long long)(s.first + t) * a.os.t + col) * e, z, sizeof(z));
+    }
+  }
 }
 
 // Joins the shares of the rows: D / 4 lanes per row, rows [B H T] in order.

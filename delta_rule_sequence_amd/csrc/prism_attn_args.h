@@ -16,7 +16,6 @@ struct AttnArgs {
   int B, H, G, T, S;
   int causal, window;             // window 0: none
   float scale;
-  int tiles;                      // row tiles of all sequences, at most
   void* o;
   float* lse;                     // [B][H][T]; may be null in the forward
   // backward
@@ -53,7 +52,7 @@ prism_status launch_cache_write(prism_dtype dt, int D, bool bits8, AttnArgs a, h
 prism_status launch_attn_paged(prism_dtype dt, int D, bool bits8, bool few, AttnArgs a, hipStream_t stream);
 prism_status launch_rope(prism_dtype dt, bool bwd, const RopeArgs& a, hipStream_t stream);
 // Each enqueues on `stream` and reports launch failures.
-prism_status launch_attn_fwd(prism_dtype dt, int D, AttnArgs a, hipStream_t stream);
+prism_status launch_attn_fwd(prism_dtype dt, int D, const AttnArgs& a, hipStream_t stream);
 prism_status launch_attn_bwd(prism_dtype dt, int D, const AttnArgs& a, hipStream_t stream);
 }  // namespace host
 }  // namespace prism

@@ -59,28 +59,27 @@ __device__ __forceinline__ float far_exponent(float x, float scale, float lse) {
   return (s - lse) * kLog2e;
 }
 
-template <class T, int D, int NW, int BN> struct BwdTile {
+template <class T, int D, int NW, int BN, bool AHEAD> struct BwdTile {
   using R = Rows<T, D>;
   static constexpr int kThreads = 64 * NW, kRows = 32 * NW;
   static constexpr int kTile = BN * R::kStride;
-  // bfloat16: the next rows' two products are formed beside these rows' exponentials, so a tile is in LDS one step ahead.
-  // float32's products take too long to hide anything behind, and its tiles leave no room for a third.
-  static constexpr bool kAhead = sizeof(T) == 2;
+  // AHEAD: the next rows' two products are formed beside these rows' exponentials, so a tile is in LDS one step ahead.
+  static constexpr bool kAhead = AHEAD;
   static constexpr int kTiles = kAhead ? 3 : 2;
   static constexpr int kRowsAt = 2 * kTiles * kTile;                  // of two tensors; then lse log2(e), delta and lse; zeros
   static constexpr int kLds = kRowsAt + (kTiles * 3 + 1) * BN * 4;
 };
 // KW x QW waves: KW of 32 keys each, QW that take a tile's queries by turns.
-template <class T, int D, int KW, int QW, int BN> struct KeyPass : BwdTile<T, D, KW * QW, BN> {
+template <class T, int D, int KW, int QW, int BN, bool AHEAD> struct KeyPass : BwdTile<T, D, KW * QW, BN, AHEAD> {
   static constexpr int kKeys = 32 * KW;
   static_assert(BN % (32 * QW) == 0, "every wave has queries of a tile");
   static_assert((QW - 1) * KW * 32 * (D + 4) * 4 <= KeyPass::kLds, "a join fits");
 };
 
 // dq and delta: a wave owns 32 queries.
-template <class T, int D, int NW, int BN>
+template <class T, int D, int NW, int BN, bool AHEAD>
 __global__ __launch_bounds__(64 * NW, D * (int)sizeof(T) > 256 ? 1 : 2) void dq_kernel(AttnArgs a) {
-  using F = BwdTile<T, D, NW, BN>;
+  using F = BwdTile<T, D, NW, BN, AHEAD>;
   using R = Rows<T, D>;
   extern __shared__ __align__(16) char lds[];
   constexpr int NT = BN / 32;
@@ -123,6 +122,7 @@ __global__ __launch_bounds__(64 * NW, D * (int)sizeof(T) > 256 ? 1 : 2) void dq_
     sk.load(kp + (long long)t * BN * kst, s.n - t * BN, kst, tid);
     sv.load(vp + (long long)t * BN * vst, s.n - t * BN, vst, tid);
   };
+  static_assert(!F::kAhead || NT % 2 == 0, "two halves by turns");
   char* const v_tiles = lds + F::kTiles * F::kTile;
   const auto store = [&](int place) {
     sk.store(lds + place * F::kTile, tid);
@@ -202,9 +202,9 @@ __global__ __launch_bounds__(64 * NW, D * (int)sizeof(T) > 256 ? 1 : 2) void dq_
 // dk and dv: a wave owns 32 keys and takes the queries of the group's heads in turn.  PARTS: which of the two (3: both in one
 // pass; one after the other forms the scores twice, but a wave of wide rows needs more registers for both than it has).
 enum { kDk = 1, kDv = 2 };
-template <class T, int D, int KW, int QW, int BN, int PARTS>
+template <class T, int D, int KW, int QW, int BN, int PARTS, bool AHEAD>
 __global__ __launch_bounds__(64 * KW * QW, PARTS == 3 && D * (int)sizeof(T) > 128 ? 1 : 2) void dkv_kernel(AttnArgs a) {
-  using F = KeyPass<T, D, KW, QW, BN>;
+  using F = KeyPass<T, D, KW, QW, BN, AHEAD>;
   using R = Rows<T, D>;
   extern __shared__ __align__(16) char lds[];
   constexpr int NT = BN / 32;

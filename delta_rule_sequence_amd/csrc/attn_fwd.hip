@@ -32,18 +32,19 @@ prism_status few(const AttnArgs& a, hipStream_t stream) {
   return hipGetLastError() == hipSuccess ? PRISM_OK : PRISM_ERR_HIP;
 }
 
-#ifndef FORCE
-#define FORCE -1
-#endif
-// Workgroups of 128 rows, or of 256 for wide heads, where there are enough of them for the device; else tiles of 32 rows whose
-// keys four waves share.
+// Workgroups of 128 rows, or of 256 for wide heads of bfloat16 where there are many; else tiles of 32 rows whose keys four waves
+// share.  Measured at the sides of the borders, us, few rows / many rows: bfloat16 of 64: 1 x 16 x 2048 30 / 37, 1 x 32 x 2048
+// 50 / 40, 4 x 16 x 256 7.4 / 8.8, 4 x 16 x 512 14.7 / 13.1; float32 of 64: 1 x 32 x 2048 171 / 217, 8 x 12 x 2048 486 / 466,
+// 8 x 16 x 512 64 / 65, 32 x 16 x 256 86 / 74; of 128: 1 x 16 x 2048 192 / 303, 1 x 32 x 2048 379 / 337; 128 / 256 rows,
+// bfloat16 of 128: 2 x 32 x 2048 114 / 88, 1 x 32 x 2048 62 / 67.
 template <class T, int D>
 prism_status run(const AttnArgs& a, hipStream_t s) {
   const size_t blocks = row_tiles(a, 128, 1) * a.H;
-  int how = blocks < 256 ? 0 : D == 128 && sizeof(T) == 2 && blocks >= 1024 ? 2 : 1;
-  if (FORCE >= 0) how = FORCE;
-  if (how == 0) return few<T, D>(a, s);
-  if constexpr (D == 128 && sizeof(T) == 2) if (how == 2) return many<T, D, 8, 64>(a, s);
+  const bool f32 = sizeof(T) == 4;
+  const size_t few_most = f32 && D < 128 ? (a.T >= 1024 ? 1024 : 512) : a.T >= (f32 ? 512 : 1024) ? 320 : 192;
+  if (blocks <= few_most) return few<T, D>(a, s);
+  if constexpr (D == 128 && sizeof(T) == 2)
+    if (blocks >= 1024) return many<T, D, 8, 64>(a, s);
   return many<T, D, 4, (sizeof(T) == 4 && D > 32 ? 32 : 64)>(a, s);
 }
 

@@ -69,26 +69,46 @@ template <class T, int D, int NW, int BN, bool AHEAD> struct BwdTile {
   static constexpr int kRowsAt = 2 * kTiles * kTile;                  // of two tensors; then lse log2(e), delta and lse; zeros
   static constexpr int kLds = kRowsAt + (kTiles * 3 + 1) * BN * 4;
 };
-// KW x QW waves: KW of 32 keys each, QW that take a tile's queries by turns.
-template <class T, int D, int KW, int QW, int BN, bool AHEAD> struct KeyPass : BwdTile<T, D, KW * QW, BN, AHEAD> {
-  static constexpr int kKeys = 32 * KW;
-  static_assert(BN % (32 * QW) == 0, "every wave has queries of a tile");
-  static_assert((QW - 1) * KW * 32 * (D + 4) * 4 <= KeyPass::kLds, "a join fits");
+// OW x SW waves: OW own 32 rows each, SW take a tile's rows by turns.
+template <class T, int D, int OW, int SW, int BN, bool AHEAD> struct Pass : BwdTile<T, D, OW * SW, BN, AHEAD> {
+  static constexpr int kOwn = 32 * OW;
+  static_assert(BN % (32 * SW) == 0, "every wave has rows of a tile");
+  static_assert((SW - 1) * OW * 32 * (D + 4) * 4 <= Pass::kLds, "a join fits");
 };
 
-// dq and delta: a wave owns 32 queries.
-template <class T, int D, int NW, int BN, bool AHEAD>
-__global__ __launch_bounds__(64 * NW, D * (int)sizeof(T) > 256 ? 1 : 2) void dq_kernel(AttnArgs a) {
-  using F = BwdTile<T, D, NW, BN, AHEAD>;
+// The sums of the waves that own the same rows, in their order, in the first one's registers.
+template <int D, int OW, int SW>
+__device__ __forceinline__ void join_waves(f32x16 (&acc)[D / 32], char* lds, int ow, int sw) {
+  const int l = lane_id(), h = l >> 5;
+  __syncthreads();
+  float* const rows = reinterpret_cast<float*>(lds) + (l & 31) * (D + 4);
+  if (sw > 0) store_columns<float, D>(reinterpret_cast<char*>(rows + ((sw - 1) * OW + ow) * 32 * (D + 4)), acc, 1.f, h);
+  __syncthreads();
+  if (sw > 0) return;
+  for (int o = 0; o < SW - 1; ++o)
+#pragma unroll
+    for (int d = 0; d < D / 32; ++d)
+#pragma unroll
+      for (int r = 0; r < 4; ++r) {
+        const f32x4 y = *reinterpret_cast<const f32x4*>(rows + (o * OW + ow) * 32 * (D + 4) + 32 * d + 8 * r + 4 * h);
+#pragma unroll
+        for (int u = 0; u < 4; ++u) acc[d][4 * r + u] += y[u];
+      }
+}
+
+// dq and delta: OW waves of 32 queries, SW that take a tile's keys by turns.
+template <class T, int D, int OW, int SW, int BN, bool AHEAD>
+__global__ __launch_bounds__(64 * OW * SW, SW > 1 || D * (int)sizeof(T) > 256 ? 1 : 2) void dq_kernel(AttnArgs a) {
+  using F = Pass<T, D, OW, SW, BN, AHEAD>;
   using R = Rows<T, D>;
   extern __shared__ __align__(16) char lds[];
   constexpr int NT = BN / 32;
   const int rep = a.H / a.G;
-  const Seq s = find_tile(a, blockIdx.x, F::kRows, rep, a.causal);
+  const Seq s = find_tile(a, blockIdx.x, F::kOwn, rep, a.causal);
   if (s.id < 0) return;
   const int group = s.group, head = group * rep + s.head;
-  const int tid = threadIdx.x, l = lane_id(), h = l >> 5, w = uniform(wave_id());
-  const int q0 = s.tile * F::kRows, qw = q0 + w * 32, i = qw + (l & 31);
+  const int tid = threadIdx.x, l = lane_id(), h = l >> 5, w = uniform(wave_id()), ow = w % OW, sw = w / OW;
+  const int q0 = s.tile * F::kOwn, qw = q0 + ow * 32, i = qw + (l & 31);
   const long long e = sizeof(T);
 
   u32x4 qf[R::kSteps], gf[R::kSteps];
@@ -107,11 +127,11 @@ __global__ __launch_bounds__(64 * NW, D * (int)sizeof(T) > 256 ? 1 : 2) void dq_
   }
   const long long at = ((long long)s.b * a.H + head) * a.T + s.first + i;
   const float given = i < s.n ? a.lse[at] : 0.f;
-  if (i < s.n && h == 0) a.delta[at] = delta;
+  if (i < s.n && h == 0 && sw == 0) a.delta[at] = delta;
   const bool far = __any(is_far(given));                              // then the exponents are formed by themselves
   const float scale = a.scale * kLog2e, c = far ? 1.f : scale, lse = far ? 0.f : given * kLog2e;
 
-  const int jend = a.causal ? min(q0 + F::kRows, s.n) : s.n;
+  const int jend = a.causal ? min(q0 + F::kOwn, s.n) : s.n;
   const int jbeg = a.window > 0 ? max(q0 - a.window + 1, 0) : 0;
   const int t0 = jbeg / BN, t1 = (jend + BN - 1) / BN;
   Stage<T, D, BN, F::kThreads> sk, sv;
@@ -122,7 +142,8 @@ __global__ __launch_bounds__(64 * NW, D * (int)sizeof(T) > 256 ? 1 : 2) void dq_
     sk.load(kp + (long long)t * BN * kst, s.n - t * BN, kst, tid);
     sv.load(vp + (long long)t * BN * vst, s.n - t * BN, vst, tid);
   };
-  static_assert(!F::kAhead || NT % 2 == 0, "two halves by turns");
+  constexpr int M = NT / SW;                                          // a tile's parts of a wave
+  static_assert(!F::kAhead || M % 2 == 0, "two halves by turns");
   char* const v_tiles = lds + F::kTiles * F::kTile;
   const auto store = [&](int place) {
     sk.store(lds + place * F::kTile, tid);
@@ -154,7 +175,7 @@ __global__ __launch_bounds__(64 * NW, D * (int)sizeof(T) > 256 ? 1 : 2) void dq_
     }
     if (t0 + 2 < t1) load(t0 + 2);
     __syncthreads();
-    products(xs[0], gs[0], 0);
+    products(xs[0], gs[0], sw * 32 * R::kStride);
   }
   for (int t = t0; t < t1; ++t) {
     int next = place + 1 == F::kTiles ? 0 : place + 1;
@@ -170,11 +191,11 @@ __global__ __launch_bounds__(64 * NW, D * (int)sizeof(T) > 256 ? 1 : 2) void dq_
     const int at = place * F::kTile, after = next * F::kTile;
     place = next;
 #pragma unroll
-    for (int n = 0; n < NT; ++n) {
-      const int j0 = t * BN + 32 * n;
+    for (int m = 0; m < M; ++m) {
+      const int n = m * SW + sw, j0 = t * BN + 32 * n, here = at + n * 32 * R::kStride;
       if (j0 > wlast) break;                                          // nothing for this wave's queries
-      f32x16 &x = xs[F::kAhead ? n & 1 : 0], &g = gs[F::kAhead ? n & 1 : 0];
-      if constexpr (!F::kAhead) products(x, g, at + n * 32 * R::kStride);
+      f32x16 &x = xs[F::kAhead ? m & 1 : 0], &g = gs[F::kAhead ? m & 1 : 0];
+      if constexpr (!F::kAhead) products(x, g, here);
       const bool edge = j0 + 31 > (a.causal ? min(qw, s.n - 1) : s.n - 1) || (a.window > 0 && j0 <= qw + 31 - a.window);
       if (edge || far) {
 #pragma unroll
@@ -187,44 +208,42 @@ __global__ __launch_bounds__(64 * NW, D * (int)sizeof(T) > 256 ? 1 : 2) void dq_
         }
       }
       if constexpr (F::kAhead)
-        products(xs[(n + 1) & 1], gs[(n + 1) & 1], n + 1 < NT ? at + (n + 1) * 32 * R::kStride : after);
+        products(xs[(m + 1) & 1], gs[(m + 1) & 1], m + 1 < M ? here + SW * 32 * R::kStride : after + sw * 32 * R::kStride);
 #pragma unroll
       for (int r = 0; r < 16; ++r) x[r] = __builtin_amdgcn_exp2f(fmaf(x[r], c, -lse)) * (g[r] - delta);
       Operand<T, 1> ds[1];
       ds[0].set(x);
-      mul_transposed<D, 1, 1>(dq, lds + at + rcol + n * 32 * R::kStride, ds);
+      mul_transposed<D, 1, 1>(dq, lds + here + rcol, ds);
     }
   }
-  if (i < s.n)
+  if constexpr (SW > 1) join_waves<D, OW, SW>(dq[0], lds, ow, sw);
+  if (i < s.n && sw == 0)
     store_columns<T, D>((char*)a.dq + (s.b * a.dqs.b + head * a.dqs.h + (long long)(s.first + i) * a.dqs.t) * e, dq[0], a.scale, h);
 }
 
-// dk and dv: a wave owns 32 keys and takes the queries of the group's heads in turn.  PARTS: which of the two (3: both in one
-// pass; one after the other forms the scores twice, but a wave of wide rows needs more registers for both than it has).
-enum { kDk = 1, kDv = 2 };
-template <class T, int D, int KW, int QW, int BN, int PARTS, bool AHEAD>
-__global__ __launch_bounds__(64 * KW * QW, PARTS == 3 && D * (int)sizeof(T) > 128 ? 1 : 2) void dkv_kernel(AttnArgs a) {
-  using F = KeyPass<T, D, KW, QW, BN, AHEAD>;
+// dk and dv: KW waves of 32 keys, QW that take a tile's queries by turns; the heads of the group one after the other.
+template <class T, int D, int KW, int QW, int BN, bool AHEAD>
+__global__ __launch_bounds__(64 * KW * QW, D * (int)sizeof(T) > 128 ? 1 : 2) void dkv_kernel(AttnArgs a) {
+  using F = Pass<T, D, KW, QW, BN, AHEAD>;
   using R = Rows<T, D>;
   extern __shared__ __align__(16) char lds[];
   constexpr int NT = BN / 32;
   // the heads of a group go to a.splits workgroups
   const unsigned unit = blockIdx.x / (unsigned)a.splits, split = blockIdx.x - unit * a.splits;
   const int rep = a.H / a.G, each = (rep + a.splits - 1) / a.splits, h0 = min((int)split * each, rep), h1 = min(h0 + each, rep);
-  const Seq s = find_tile(a, unit, F::kKeys, 1, false);
+  const Seq s = find_tile(a, unit, F::kOwn, 1, false);
   if (s.id < 0) return;
   const int group = s.group;
   const int tid = threadIdx.x, l = lane_id(), h = l >> 5, w = uniform(wave_id()), kw = w % KW, qw = w / KW;
-  const int j0 = s.tile * F::kKeys, jw = j0 + kw * 32, j = jw + (l & 31);
+  const int j0 = s.tile * F::kOwn, jw = j0 + kw * 32, j = jw + (l & 31);
   const long long e = sizeof(T);
 
-  u32x4 kf[R::kSteps], vf[PARTS & kDk ? R::kSteps : 1];
+  u32x4 kf[R::kSteps], vf[R::kSteps];
   hold(kf, (const char*)a.k + (s.b * a.ks.b + group * a.ks.h + (long long)(s.first + jw) * a.ks.t) * e, s.n - jw, (int)(a.ks.t * e), l);
-  if constexpr (PARTS & kDk)
-    hold(vf, (const char*)a.v + (s.b * a.vs.b + group * a.vs.h + (long long)(s.first + jw) * a.vs.t) * e, s.n - jw, (int)(a.vs.t * e), l);
+  hold(vf, (const char*)a.v + (s.b * a.vs.b + group * a.vs.h + (long long)(s.first + jw) * a.vs.t) * e, s.n - jw, (int)(a.vs.t * e), l);
 
   // queries ibeg .. iend - 1 of each head, in tiles t0 .. t1 - 1
-  const int iend = a.window > 0 ? (int)min((long long)s.n, (long long)min(j0 + F::kKeys, s.n) - 1 + a.window) : s.n;
+  const int iend = a.window > 0 ? (int)min((long long)s.n, (long long)min(j0 + F::kOwn, s.n) - 1 + a.window) : s.n;
   const int t0 = (a.causal ? j0 : 0) / BN, t1 = (iend + BN - 1) / BN, steps = (t1 - t0) * (h1 - h0);
   float* const rows = reinterpret_cast<float*>(lds + F::kRowsAt);     // [kTiles][lse log2(e), delta, lse][BN], zeros [BN]
   float* const zeros = rows + F::kTiles * 3 * BN;
@@ -256,9 +275,9 @@ __global__ __launch_bounds__(64 * KW * QW, PARTS == 3 && D * (int)sizeof(T) > 12
     if (tid < BN) rt[2 * BN + tid] = row;
   };
 
-  f32x16 dk[1][PARTS & kDk ? D / 32 : 1], dv[1][PARTS & kDv ? D / 32 : 1];
-  for (auto& x : dk[0]) x = zero16();
-  for (auto& x : dv[0]) x = zero16();
+  f32x16 dk[1][D / 32], dv[1][D / 32];
+#pragma unroll
+  for (int d = 0; d < D / 32; ++d) dk[0][d] = zero16(), dv[0][d] = zero16();
   const float scale = a.scale * kLog2e;
   const int rrow = R::by_rows(l), rcol = R::transposed(l);
   f32x16 xs[F::kAhead ? 2 : 1], gs[F::kAhead ? 2 : 1];                // s and dp of these 32 queries, and of the next
@@ -266,10 +285,8 @@ __global__ __launch_bounds__(64 * KW * QW, PARTS == 3 && D * (int)sizeof(T) > 12
     x = zero16(), g = zero16();
 #pragma unroll
     for (int k = 0; k < R::kSteps; ++k) mma(x, lds16(lds + at + rrow + k * 32), kf[k], T());
-    if constexpr (PARTS & kDk) {
 #pragma unroll
-      for (int k = 0; k < R::kSteps; ++k) mma(g, lds16(g_tiles + at + rrow + k * 32), vf[k], T());
-    }
+    for (int k = 0; k < R::kSteps; ++k) mma(g, lds16(g_tiles + at + rrow + k * 32), vf[k], T());
   };
 
   constexpr int M = NT / QW;                                          // a tile's parts of a wave
@@ -341,49 +358,26 @@ __global__ __launch_bounds__(64 * KW * QW, PARTS == 3 && D * (int)sizeof(T) > 12
         }
       }
       Operand<T, 1> p[1];
-      if constexpr (PARTS & kDv) {
-        p[0].set(x);
-        mul_transposed<D, 1, 1>(dv, g_tiles + at + rcol, p);
-      }
-      if constexpr (PARTS & kDk) {
-        p[0].set(g);
-        mul_transposed<D, 1, 1>(dk, lds + at + rcol, p);
-      }
+      p[0].set(x);
+      mul_transposed<D, 1, 1>(dv, g_tiles + at + rcol, p);
+      p[0].set(g);
+      mul_transposed<D, 1, 1>(dk, lds + at + rcol, p);
     }
     if constexpr (F::kAhead && M % 2 == 1) xs[0] = xs[1], gs[0] = gs[1];
   }
-  // the sums of the waves that share the keys, in their order
-  const auto join = [&](f32x16 (&acc)[D / 32]) {
-    __syncthreads();
-    float* const place = reinterpret_cast<float*>(lds) + ((qw - 1) * KW + kw) * 32 * (D + 4) + (l & 31) * (D + 4);
-    if (qw > 0) store_columns<float, D>(reinterpret_cast<char*>(place), acc, 1.f, h);
-    __syncthreads();
-    if (qw > 0) return;
-    for (int o = 0; o < QW - 1; ++o) {
-      const float* from = reinterpret_cast<const float*>(lds) + (o * KW + kw) * 32 * (D + 4) + (l & 31) * (D + 4);
-#pragma unroll
-      for (int d = 0; d < D / 32; ++d)
-#pragma unroll
-        for (int r = 0; r < 4; ++r) {
-          const f32x4 y = *reinterpret_cast<const f32x4*>(from + 32 * d + 8 * r + 4 * h);
-#pragma unroll
-          for (int u = 0; u < 4; ++u) acc[d][4 * r + u] += y[u];
-        }
-    }
-  };
-  if constexpr (QW > 1 && (PARTS & kDk)) join(dk[0]);
-  if constexpr (QW > 1 && (PARTS & kDv)) join(dv[0]);
+  if constexpr (QW > 1) {
+    join_waves<D, KW, QW>(dk[0], lds, kw, qw);
+    join_waves<D, KW, QW>(dv[0], lds, kw, qw);
+  }
   if (j >= s.n || qw > 0) return;
   if (a.splits > 1) {                                                 // [splits][dk, dv][B G T][D], added up by sum_kernel
     const size_t all = (size_t)a.B * a.G * a.T, at = ((size_t)s.b * a.G + group) * a.T + s.first + j;
-    if constexpr (PARTS & kDk) store_columns<float, D>((char*)(a.part + ((2 * split) * all + at) * D), dk[0], a.scale, h);
-    if constexpr (PARTS & kDv) store_columns<float, D>((char*)(a.part + ((2 * split + 1) * all + at) * D), dv[0], 1.f, h);
+    store_columns<float, D>((char*)(a.part + ((2 * split) * all + at) * D), dk[0], a.scale, h);
+    store_columns<float, D>((char*)(a.part + ((2 * split + 1) * all + at) * D), dv[0], 1.f, h);
     return;
   }
-  if constexpr (PARTS & kDk)
-    store_columns<T, D>((char*)a.dk + (s.b * a.dks.b + group * a.dks.h + (long long)(s.first + j) * a.dks.t) * e, dk[0], a.scale, h);
-  if constexpr (PARTS & kDv)
-    store_columns<T, D>((char*)a.dv + (s.b * a.dvs.b + group * a.dvs.h + (long long)(s.first + j) * a.dvs.t) * e, dv[0], 1.f, h);
+  store_columns<T, D>((char*)a.dk + (s.b * a.dks.b + group * a.dks.h + (long long)(s.first + j) * a.dks.t) * e, dk[0], a.scale, h);
+  store_columns<T, D>((char*)a.dv + (s.b * a.dvs.b + group * a.dvs.h + (long long)(s.first + j) * a.dvs.t) * e, dv[0], 1.f, h);
 }
 
 // dk and dv from the shares of the heads: D / 4 lanes per row of one of them, tokens of the sequences only.

@@ -30,6 +30,10 @@ prism_status attn_check(int B, int H, int G, int T, int D, int S, const int* len
   return tiles > ((size_t)1 << 23) / H ? PRISM_ERR_UNSUPPORTED : PRISM_OK;
 }
 
+#ifndef PERW
+#define PERW 8
+#define NBLK 4
+#endif
 // Norm and rotation: sizes, and the lane groups' share of a token's heads.
 int rope_lanes(int D, int rot) { return D % 8 != 0 || rot % 8 != 0 ? 64 : D <= 32 ? 4 : D <= 64 ? 8 : D <= 128 ? 16 : D <= 256 ? 32 : 64; }
 
@@ -40,11 +44,11 @@ prism_status rope_plan(int B, int H, int G, int T, int D, int rot, float factor,
   const size_t tokens = (size_t)B * T, heads = (size_t)H + G, lanes = rope_lanes(D, rot);
   if (tokens > ((size_t)1 << 31) / lanes / heads) return PRISM_ERR_UNSUPPORTED;
   // heads of a token that share their sines and cosines, as long as every CU keeps 8 waves
-  a->per = (int)std::min(heads, std::max<size_t>(1, tokens * heads * lanes / 64 / (8 * kCUs)));
+  a->per = (int)std::min(heads, std::max<size_t>(1, tokens * heads * lanes / 64 / (PERW * kCUs)));
   a->groups = (int)((heads + a->per - 1) / a->per);
   a->per = (int)((heads + a->groups - 1) / a->groups);
   const size_t slots = 256 / lanes;
-  a->nblk = (int)std::min<size_t>((tokens * a->groups + slots - 1) / slots, 4 * kCUs);
+  a->nblk = (int)std::min<size_t>((tokens * a->groups + slots - 1) / slots, NBLK * kCUs);
   a->B = B, a->T = T, a->D = D, a->heads[0] = H, a->heads[1] = G, a->rot = rot, a->factor = factor, a->eps = eps;
   return PRISM_OK;
 }

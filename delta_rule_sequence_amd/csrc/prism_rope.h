@@ -114,7 +114,31 @@ __device__ __forceinline__ Work work_of(const RopeArgs& a, size_t unit) {
   w.t = (int)(token - (size_t)w.b * a.T);
   return w;
 }
-__device__ __forceinline__ long long row_at(const prism_strides& s, const Work& w, int head) { return w.b * s.b + head * s.h + w.t * s.t; }
+__device__ __forceinline__ long long row_at(const prism_strides& s, const Work& w, int head) { return w.b * s.b + head * s.h + (long long)w.t * s.t; }
+
+// The weights of a lane's channels (ones without).
+template <int V, int NU, class LANE>
+__device__ __forceinline__ void weights(float (&w)[NU][2][V], const float* p, const LANE& ln) {
+#pragma unroll
+  for (int i = 0; i < NU; ++i)
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+#pragma unroll
+      for (int j = 0; j < V; ++j) w[i][k][j] = ln.live[i] && p == nullptr ? 1.f : 0.f;
+      if (ln.live[i] && p != nullptr) __builtin_memcpy(w[i][k], p + ln.at[i][k], sizeof(w[i][k]));
+    }
+}
+template <class T, int V, int NU, class LANE>
+__device__ __forceinline__ void widen(float (&x)[NU][2][V], const Row<T, V, NU>& row, const LANE& ln) {
+#pragma unroll
+  for (int i = 0; i < NU; ++i)
+#pragma unroll
+    for (int k = 0; k < 2; ++k)
+#pragma unroll
+      for (int j = 0; j < V; ++j) x[i][k][j] = ln.live[i] ? (float)row.v[i][k][j] : 0.f;
+}
+
+constexpr int kAtOnce = 4;           // rows of a lane group in flight
 
 template <class T, int V, int L, int NU, bool INTER>
 __global__ __launch_bounds__(256) void fwd_kernel(RopeArgs a) {
@@ -126,110 +150,127 @@ __global__ __launch_bounds__(256) void fwd_kernel(RopeArgs a) {
   Angles<V, NU> an;
   an.set(a, ln, lane, L, a.pos != nullptr ? a.pos[(size_t)wk.b * a.T + wk.t] : wk.t);
   const bool norm = a.w[0] != nullptr;
-  for (int hd = wk.first; hd < wk.last; ++hd) {
-    const int which = hd >= a.heads[0], head = which != 0 ? hd - a.heads[0] : hd;
-    const float* w = which != 0 ? a.w[1] : a.w[0];
-    Row<T, V, NU> row;
-    row.load((const T*)(which != 0 ? a.x[1] : a.x[0]) + row_at(which != 0 ? a.xs[1] : a.xs[0], wk, head), ln);
-    float x[NU][2][V], ss = 0.f;
 #pragma unroll
-    for (int i = 0; i < NU; ++i)
+  for (int q = 0; q < 2; ++q) {
+    const int start = q != 0 ? a.heads[0] : 0, lo = max(wk.first, start) - start, hi = min(wk.last - start, a.heads[q]);
+    if (lo >= hi) continue;
+    float w[NU][2][V];
+    weights<V, NU>(w, a.w[q], ln);
+    const T* const src = (const T*)a.x[q] + row_at(a.xs[q], wk, 0);
+    T* const dst = (T*)a.y[q] + row_at(a.ys[q], wk, 0);
+    for (int head = lo; head < hi; head += kAtOnce) {
+      Row<T, V, NU> row[kAtOnce];
 #pragma unroll
-      for (int k = 0; k < 2; ++k)
+      for (int u = 0; u < kAtOnce; ++u)
+        if (head + u < hi) row[u].load(src + (head + u) * a.xs[q].h, ln);
 #pragma unroll
-        for (int j = 0; j < V; ++j) {
-          x[i][k][j] = ln.live[i] ? (float)row.v[i][k][j] : 0.f;
-          ss = fmaf(x[i][k][j], x[i][k][j], ss);
+      for (int u = 0; u < kAtOnce; ++u) {
+        if (head + u >= hi) break;
+        float x[NU][2][V], ss = 0.f;
+        widen<T, V, NU>(x, row[u], ln);
+        if (norm) {
+#pragma unroll
+          for (int i = 0; i < NU; ++i)
+#pragma unroll
+            for (int k = 0; k < 2; ++k)
+#pragma unroll
+              for (int j = 0; j < V; ++j) ss = fmaf(x[i][k][j], x[i][k][j], ss);
+          const float r = 1.f / sqrtf(group_sum<L>(ss) / a.D + a.eps);
+#pragma unroll
+          for (int i = 0; i < NU; ++i)
+#pragma unroll
+            for (int k = 0; k < 2; ++k)
+#pragma unroll
+              for (int j = 0; j < V; ++j) x[i][k][j] *= r * w[i][k][j];
         }
-    float r = 1.f;
-    if (norm) r = 1.f / sqrtf(group_sum<L>(ss) / a.D + a.eps);
 #pragma unroll
-    for (int i = 0; i < NU; ++i) {
-      if (norm && ln.live[i]) {
-        float wv[2][V];
-        __builtin_memcpy(wv[0], w + ln.at[i][0], sizeof(wv[0]));
-        __builtin_memcpy(wv[1], w + ln.at[i][1], sizeof(wv[1]));
+        for (int i = 0; i < NU; ++i) {
+          if (ln.pairs[i]) rotate<V>(x[i], an.sn[i], an.cs[i], INTER, 1.f);
 #pragma unroll
-        for (int k = 0; k < 2; ++k)
+          for (int k = 0; k < 2; ++k)
 #pragma unroll
-          for (int j = 0; j < V; ++j) x[i][k][j] *= r * wv[k][j];
+            for (int j = 0; j < V; ++j) row[u].v[i][k][j] = (T)x[i][k][j];
+        }
+        row[u].store(dst + (head + u) * a.ys[q].h, ln);
       }
-      if (ln.pairs[i]) rotate<V>(x[i], an.sn[i], an.cs[i], INTER, 1.f);
-#pragma unroll
-      for (int k = 0; k < 2; ++k)
-#pragma unroll
-        for (int j = 0; j < V; ++j) row.v[i][k][j] = (T)x[i][k][j];
     }
-    row.store((T*)(which != 0 ? a.y[1] : a.y[0]) + row_at(which != 0 ? a.ys[1] : a.ys[0], wk, head), ln);
   }
 }
 
 // Workgroup k takes the lane groups' units k, k + nblk, ... (256 / L at a time); its shares of dw stay in part[k].
 template <class T, int V, int L, int NU, bool INTER>
 __global__ __launch_bounds__(256) void bwd_kernel(RopeArgs a) {
-  constexpr int S = 256 / L;
+  constexpr int S = 256 / L, U = 2;
   __shared__ float shares[S][L][NU * 2 * V + 1];
   const int lane = threadIdx.x % L, slot = threadIdx.x / L;
   const size_t units = (size_t)a.B * a.T * a.groups;
   const Lane<V, L, NU> ln(a, lane);
   const bool norm = a.w[0] != nullptr;
-  float dw[2][NU][2][V];
+  float dw[2][NU][2][V], w[2][NU][2][V];
 #pragma unroll
   for (int q = 0; q < 2 * NU * 2 * V; ++q) (&dw[0][0][0][0])[q] = 0.f;
+#pragma unroll
+  for (int q = 0; q < 2; ++q) weights<V, NU>(w[q], a.w[q], ln);
   for (size_t unit = (size_t)blockIdx.x * S + slot; unit < units; unit += (size_t)a.nblk * S) {
     const Work wk = work_of(a, unit);
     Angles<V, NU> an;
     an.set(a, ln, lane, L, a.pos != nullptr ? a.pos[(size_t)wk.b * a.T + wk.t] : wk.t);
-    for (int hd = wk.first; hd < wk.last; ++hd) {
-      const int which = hd >= a.heads[0], head = which != 0 ? hd - a.heads[0] : hd;
-      Row<T, V, NU> gr, xr;
-      gr.load((const T*)(which != 0 ? a.dy[1] : a.dy[0]) + row_at(which != 0 ? a.dys[1] : a.dys[0], wk, head), ln);
-      if (norm) xr.load((const T*)(which != 0 ? a.x[1] : a.x[0]) + row_at(which != 0 ? a.xs[1] : a.xs[0], wk, head), ln);
-      float g[NU][2][V], x[NU][2][V], wv[NU][2][V], ss = 0.f, ux = 0.f;
 #pragma unroll
-      for (int i = 0; i < NU; ++i) {
+    for (int q = 0; q < 2; ++q) {
+      const int start = q != 0 ? a.heads[0] : 0, lo = max(wk.first, start) - start, hi = min(wk.last - start, a.heads[q]);
+      const T* const src = (const T*)a.dy[q] + row_at(a.dys[q], wk, 0);
+      const T* const old = (const T*)a.x[q] + row_at(a.xs[q], wk, 0);
+      T* const dst = (T*)a.y[q] + row_at(a.ys[q], wk, 0);
+      for (int head = lo; head < hi; head += U) {
+        Row<T, V, NU> gr[U], xr[U];
 #pragma unroll
-        for (int k = 0; k < 2; ++k)
+        for (int u = 0; u < U; ++u) {
+          if (head + u >= hi) break;
+          gr[u].load(src + (head + u) * a.dys[q].h, ln);
+          if (norm) xr[u].load(old + (head + u) * a.xs[q].h, ln);
+        }
 #pragma unroll
-          for (int j = 0; j < V; ++j) g[i][k][j] = ln.live[i] ? (float)gr.v[i][k][j] : 0.f;
-        if (ln.pairs[i]) rotate<V>(g[i], an.sn[i], an.cs[i], INTER, -1.f);
-        if (norm) {
-          const float* w = which != 0 ? a.w[1] : a.w[0];
+        for (int u = 0; u < U; ++u) {
+          if (head + u >= hi) break;
+          float g[NU][2][V];
+          widen<T, V, NU>(g, gr[u], ln);
 #pragma unroll
-          for (int k = 0; k < 2; ++k) {
-            if (ln.live[i]) __builtin_memcpy(wv[i][k], w + ln.at[i][k], sizeof(wv[i][k]));
+          for (int i = 0; i < NU; ++i)
+            if (ln.pairs[i]) rotate<V>(g[i], an.sn[i], an.cs[i], INTER, -1.f);
+          if (norm) {
+            float x[NU][2][V], ss = 0.f, ux = 0.f;
+            widen<T, V, NU>(x, xr[u], ln);
 #pragma unroll
-            for (int j = 0; j < V; ++j) {
-              x[i][k][j] = ln.live[i] ? (float)xr.v[i][k][j] : 0.f;
-              if (!ln.live[i]) wv[i][k][j] = 0.f;
-              ss = fmaf(x[i][k][j], x[i][k][j], ss);
-              ux = fmaf(g[i][k][j] * wv[i][k][j], x[i][k][j], ux);
-            }
+            for (int i = 0; i < NU; ++i)
+#pragma unroll
+              for (int k = 0; k < 2; ++k)
+#pragma unroll
+                for (int j = 0; j < V; ++j) {
+                  ss = fmaf(x[i][k][j], x[i][k][j], ss);
+                  ux = fmaf(g[i][k][j] * w[q][i][k][j], x[i][k][j], ux);
+                }
+            const float r = 1.f / sqrtf(group_sum<L>(ss) / a.D + a.eps);
+            const float mean = group_sum<L>(ux) * r / a.D;             // of u xhat
+#pragma unroll
+            for (int i = 0; i < NU; ++i)
+#pragma unroll
+              for (int k = 0; k < 2; ++k)
+#pragma unroll
+                for (int j = 0; j < V; ++j) {
+                  const float hat = x[i][k][j] * r;
+                  dw[q][i][k][j] = fmaf(g[i][k][j], hat, dw[q][i][k][j]);
+                  g[i][k][j] = r * (g[i][k][j] * w[q][i][k][j] - hat * mean);
+                }
           }
+#pragma unroll
+          for (int i = 0; i < NU; ++i)
+#pragma unroll
+            for (int k = 0; k < 2; ++k)
+#pragma unroll
+              for (int j = 0; j < V; ++j) gr[u].v[i][k][j] = (T)g[i][k][j];
+          gr[u].store(dst + (head + u) * a.ys[q].h, ln);
         }
       }
-      if (norm) {
-        const float r = 1.f / sqrtf(group_sum<L>(ss) / a.D + a.eps);
-        const float mean = group_sum<L>(ux) * r / a.D;                 // of u xhat
-#pragma unroll
-        for (int i = 0; i < NU; ++i)
-#pragma unroll
-          for (int k = 0; k < 2; ++k)
-#pragma unroll
-            for (int j = 0; j < V; ++j) {
-              const float hat = x[i][k][j] * r, d = g[i][k][j] * hat;
-              dw[0][i][k][j] += which == 0 ? d : 0.f;
-              dw[1][i][k][j] += which != 0 ? d : 0.f;
-              g[i][k][j] = r * (g[i][k][j] * wv[i][k][j] - hat * mean);
-            }
-      }
-#pragma unroll
-      for (int i = 0; i < NU; ++i)
-#pragma unroll
-        for (int k = 0; k < 2; ++k)
-#pragma unroll
-          for (int j = 0; j < V; ++j) gr.v[i][k][j] = (T)g[i][k][j];
-      gr.store((T*)(which != 0 ? a.y[1] : a.y[0]) + row_at(which != 0 ? a.ys[1] : a.ys[0], wk, head), ln);
     }
   }
   if (!norm || a.part == nullptr) return;

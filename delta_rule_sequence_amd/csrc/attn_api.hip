@@ -30,10 +30,6 @@ prism_status attn_check(int B, int H, int G, int T, int D, int S, const int* len
   return tiles > ((size_t)1 << 23) / H ? PRISM_ERR_UNSUPPORTED : PRISM_OK;
 }
 
-#ifndef PERW
-#define PERW 8
-#define NBLK 4
-#endif
 // Norm and rotation: sizes, and the lane groups' share of a token's heads.
 int rope_lanes(int D, int rot) { return D % 8 != 0 || rot % 8 != 0 ? 64 : D <= 32 ? 4 : D <= 64 ? 8 : D <= 128 ? 16 : D <= 256 ? 32 : 64; }
 
@@ -44,11 +40,11 @@ prism_status rope_plan(int B, int H, int G, int T, int D, int rot, float factor,
   const size_t tokens = (size_t)B * T, heads = (size_t)H + G, lanes = rope_lanes(D, rot);
   if (tokens > ((size_t)1 << 31) / lanes / heads) return PRISM_ERR_UNSUPPORTED;
   // heads of a token that share their sines and cosines, as long as every CU keeps 8 waves
-  a->per = (int)std::min(heads, std::max<size_t>(1, tokens * heads * lanes / 64 / (PERW * kCUs)));
+  a->per = (int)std::min(heads, std::max<size_t>(1, tokens * heads * lanes / 64 / (8 * kCUs)));
   a->groups = (int)((heads + a->per - 1) / a->per);
   a->per = (int)((heads + a->groups - 1) / a->groups);
   const size_t slots = 256 / lanes;
-  a->nblk = (int)std::min<size_t>((tokens * a->groups + slots - 1) / slots, NBLK * kCUs);
+  a->nblk = (int)std::min<size_t>((tokens * a->groups + slots - 1) / slots, 4 * kCUs);
   a->B = B, a->T = T, a->D = D, a->heads[0] = H, a->heads[1] = G, a->rot = rot, a->factor = factor, a->eps = eps;
   return PRISM_OK;
 }
@@ -61,6 +57,12 @@ prism_status cache_check(int G, int D, int pages, int page, int max_pages, int T
   return (long long)max_pages * page + T > INT_MAX - 8192 ? PRISM_ERR_UNSUPPORTED : PRISM_OK;
 }
 
+#ifndef FW
+#define FW 4
+#define FK 256
+#define MWANT 2
+#define FR 64
+#endif
 // Few rows of queries: the rows of a group's heads share the cache's tiles, and its keys are split until the device is full.
 struct PagedPlan {
   bool few;
@@ -70,9 +72,9 @@ struct PagedPlan {
 PagedPlan paged_plan(int B, int H, int G, int T, int D, int page, int max_pages) {
   PagedPlan pl;
   const size_t rows = (size_t)T * (H / G), keys = (size_t)max_pages * page;
-  pl.few = rows <= 64;
+  pl.few = rows <= FR;
   const size_t units = pl.few ? (size_t)B * G * ((rows + 31) / 32) : (size_t)B * H * ((T + 127) / 128);
-  const size_t want = ((pl.few ? 4 : 2) * kCUs + units - 1) / units, most = std::max<size_t>(1, keys / (pl.few ? 256 : 512));
+  const size_t want = ((pl.few ? FW : MWANT) * kCUs + units - 1) / units, most = std::max<size_t>(1, keys / (pl.few ? FK : 512));
   pl.splits = (int)std::min<size_t>(std::min(want, most), 64);
   Layout ly;
   if (pl.splits > 1) ly.add((size_t)pl.splits * B * H * T, (size_t)(D + 2) * 4);

@@ -18,9 +18,13 @@ template <class T, int D, attn::Keys KEYS>
 prism_status paged(bool few, const AttnArgs& a, hipStream_t s) {
   using W = attn::FewTile<T, D, KEYS>;
   constexpr int BN = sizeof(T) == 2 || D == 32 ? 64 : 32;
-  using M = attn::FwdTile<T, D, 4, BN, KEYS>;
+#ifndef MW
+#define MW 4
+#endif
+  constexpr int NW = D == 128 && sizeof(T) == 2 ? MW : 4;
+  using M = attn::FwdTile<T, D, NW, BN, KEYS>;
   const auto few_rows = attn::few_kernel<T, D, KEYS>;
-  const auto many_rows = attn::fwd_kernel<T, D, 4, BN, 1, KEYS>;
+  const auto many_rows = attn::fwd_kernel<T, D, NW, BN, 1, KEYS>;
   static const bool ok =
       hipFuncSetAttribute(reinterpret_cast<const void*>(few_rows), hipFuncAttributeMaxDynamicSharedMemorySize, W::kLds) == hipSuccess &&
       hipFuncSetAttribute(reinterpret_cast<const void*>(many_rows), hipFuncAttributeMaxDynamicSharedMemorySize, M::kLds) == hipSuccess;
@@ -28,8 +32,8 @@ prism_status paged(bool few, const AttnArgs& a, hipStream_t s) {
   if (few) few_rows<<<dim3(a.B * a.G * ((a.T * (a.H / a.G) + 31) / 32) * a.splits), 256, W::kLds, s>>>(a);
   else many_rows<<<dim3(row_tiles(a, M::kRows) * a.H * a.splits), M::kThreads, M::kLds, s>>>(a);
   if (a.splits > 1) {
-    const size_t rows = (size_t)a.B * a.H * a.T, per = 256 / (D / 4);
-    attn::join_kernel<T, D><<<dim3((unsigned)((rows + per - 1) / per)), 256, 0, s>>>(a);
+    const size_t rows = (size_t)a.B * a.H * a.T;
+    attn::join_kernel<T, D><<<dim3((unsigned)((rows + 3) / 4)), 256, 0, s>>>(a);
   }
   return launched();
 }

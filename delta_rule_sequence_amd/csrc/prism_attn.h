@@ -860,39 +860,48 @@ __global__ __launch_bounds__(256, D * (int)sizeof(T) > 256 ? 1 : 2) void few_ker
   }
 }
 
-// Joins the shares of the rows: D / 4 lanes per row, rows [B H T] in order.
+// Joins the shares of the rows, at most 64 of each: a wave per row, whose lanes weigh a share each and then take D / 4 columns of
+// every (256 / D)-th share.
 template <class T, int D>
 __global__ __launch_bounds__(256) void join_kernel(AttnArgs a) {
-  constexpr int L = D / 4;
-  const size_t rows = (size_t)a.B * a.H * a.T, row = (size_t)blockIdx.x * (256 / L) + threadIdx.x / L;
+  constexpr int L = D / 4, N = 64 / L;
+  const size_t rows = (size_t)a.B * a.H * a.T, row = (size_t)blockIdx.x * 4 + wave_id();
   if (row >= rows) return;
-  const int at = threadIdx.x % L * 4;
+  const int l = lane_id();
   const size_t bh = row / a.T;
   const int t = (int)(row - bh * a.T), b = (int)(bh / a.H), head = (int)(bh - (size_t)b * a.H);
-  int n = a.T;
-  if (a.lens != nullptr) n = min(max(a.lens[b], 0), a.T);
-  if (t >= n) return;
-  const float* stats = share_stats(a, D, row);
-  float m = -kInf;
-  for (int k = 0; k < a.splits; ++k)
-    if (stats[2 * rows * k + 1] != 0.f) m = fmaxf(m, stats[2 * rows * k]);
-  float sum = 0.f;
-  f32x4 o = zero4();
-  for (int k = 0; k < a.splits; ++k) {
-    const float total = stats[2 * rows * k + 1];
-    if (total == 0.f) continue;
-    // an infinite maximum: what comes of it is NaN, as without shares
-    const float f = __builtin_amdgcn_exp2f((stats[2 * rows * k] - m) * (a.scale * kLog2e));
-    sum += f * total;
-    const f32x4 x = *reinterpret_cast<const f32x4*>(a.part + (rows * k + row) * D + at);
+  if (a.lens != nullptr && t >= uniform(a.lens[b])) return;
+  const float* const stats = share_stats(a, D, row) + 2 * rows * l;
+  float m = -kInf, total = 0.f;
+  if (l < a.splits) m = stats[0], total = stats[1];
+  if (total == 0.f) m = -kInf;
+  float top = m;
 #pragma unroll
-    for (int u = 0; u < 4; ++u) o[u] = fmaf(f, x[u], o[u]);
+  for (int o = 1; o < 64; o <<= 1) top = fmaxf(top, __shfl_xor(top, o, 64));
+  // an infinite maximum: what comes of it is NaN, as without shares
+  const float f = total == 0.f ? 0.f : __builtin_amdgcn_exp2f((m - top) * (a.scale * kLog2e));
+  float sum = f * total;
+#pragma unroll
+  for (int o = 1; o < 64; o <<= 1) sum += __shfl_xor(sum, o, 64);
+  const int at = l % L * 4;
+  f32x4 o = zero4();
+#pragma unroll 4
+  for (int k = l / L; k < (a.splits + N - 1) / N * N; k += N) {
+    const float w = __shfl(f, k, 64);                                  // 0 past the last share and of empty ones: not read
+    f32x4 x = zero4();
+    if (w != 0.f) x = *reinterpret_cast<const f32x4*>(a.part + (rows * k + row) * D + at);
+#pragma unroll
+    for (int u = 0; u < 4; ++u) o[u] = fmaf(w, x[u], o[u]);
   }
+#pragma unroll
+  for (int d = L; d < 64; d <<= 1)
+#pragma unroll
+    for (int u = 0; u < 4; ++u) o[u] += __shfl_xor(o[u], d, 64);
+  if (l >= L) return;
   T y[4];
 #pragma unroll
   for (int u = 0; u < 4; ++u) y[u] = (T)(sum == 0.f ? 0.f : o[u] / sum);
   __builtin_memcpy((char*)a.o + (b * a.os.b + head * a.os.h + (long long)t * a.os.t + at) * (long long)sizeof(T), y, sizeof(y));
-  if (a.lse != nullptr && at == 0) a.lse[row] = row_lse(m, sum, a.scale);
 }
 
 }  // namespace attn

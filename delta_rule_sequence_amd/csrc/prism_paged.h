@@ -25,35 +25,46 @@ __global__ __launch_bounds__(256) void cache_write_kernel(AttnArgs a) {
   const long long past = max(a.past[s.id], 0);
   const int* table = a.table + (size_t)s.id * a.max_pages;
   const int page = 1 << a.page_shift;
-  for (int r = threadIdx.x / L; r < n * 2 * G; r += 256 / L) {
-    const int g = r % G, tk = r / G, t = t0 + (tk >> 1);
-    const bool key = (tk & 1) == 0;
-    const long long p = past + t;
-    if (p >> a.page_shift >= a.max_pages) continue;
-    const int id = table[p >> a.page_shift];
-    if ((unsigned)id >= (unsigned)a.pages) continue;
-    const prism_strides st = key ? a.ks : a.vs;
-    const vec x = *reinterpret_cast<const vec*>((const T*)(key ? a.k : a.v) + (s.b * st.b + g * st.h + (long long)(s.first + t) * st.t) + at * V);
-    const size_t row = ((size_t)id * G + g) * page + (p & (page - 1));
-    void* const cache = key ? a.cache_k : a.cache_v;
-    if constexpr (!BITS8) {
-      *reinterpret_cast<vec*>((T*)cache + row * D + at * V) = x;
-    } else {
-      unsigned m = 0;
+  constexpr int U = 4;                                                 // rows in flight
+  for (int first = threadIdx.x / L; first < n * 2 * G; first += U * (256 / L)) {
+    vec x[U];
+    long long row[U];                                                  // -1: not written
 #pragma unroll
-      for (int i = 0; i < V; ++i) m = max(m, norm::abs_bits((float)x[i]));
+    for (int u = 0; u < U; ++u) {
+      const int r = first + u * (256 / L), g = r % G, tk = r / G, t = t0 + (tk >> 1);
+      const bool key = (tk & 1) == 0;
+      const long long p = past + t;
+      row[u] = -1;
+      if (r >= n * 2 * G || p >> a.page_shift >= a.max_pages) continue;
+      const int id = table[p >> a.page_shift];
+      const prism_strides st = key ? a.ks : a.vs;
+      x[u] = *reinterpret_cast<const vec*>((const T*)(key ? a.k : a.v) + (s.b * st.b + g * st.h + (long long)(s.first + t) * st.t) + at * V);
+      if ((unsigned)id < (unsigned)a.pages) row[u] = ((long long)id * G + g) * page + (p & (page - 1));
+    }
 #pragma unroll
-      for (int o = 1; o < L; o <<= 1) m = max(m, (unsigned)__shfl_xor((int)m, o, 64));
-      float f;
-      const float scale = norm::block_scale(m, &f);
-      unsigned y[V / 4];
+    for (int u = 0; u < U; ++u) {
+      const bool key = ((first + u * (256 / L)) / G & 1) == 0;
+      if (row[u] < 0) continue;                                        // all lanes of a row alike
+      void* const cache = key ? a.cache_k : a.cache_v;
+      if constexpr (!BITS8) {
+        *reinterpret_cast<vec*>((T*)cache + row[u] * D + at * V) = x[u];
+      } else {
+        unsigned m = 0;
 #pragma unroll
-      for (int i = 0; i < V / 4; ++i) {
-        int w = __builtin_amdgcn_cvt_pk_fp8_f32((float)x[4 * i] * f, (float)x[4 * i + 1] * f, 0, false);
-        y[i] = (unsigned)__builtin_amdgcn_cvt_pk_fp8_f32((float)x[4 * i + 2] * f, (float)x[4 * i + 3] * f, w, true);
+        for (int i = 0; i < V; ++i) m = max(m, norm::abs_bits((float)x[u][i]));
+#pragma unroll
+        for (int o = 1; o < L; o <<= 1) m = max(m, (unsigned)__shfl_xor((int)m, o, 64));
+        float f;
+        const float scale = norm::block_scale(m, &f);
+        unsigned y[V / 4];
+#pragma unroll
+        for (int i = 0; i < V / 4; ++i) {
+          const int w = __builtin_amdgcn_cvt_pk_fp8_f32((float)x[u][4 * i] * f, (float)x[u][4 * i + 1] * f, 0, false);
+          y[i] = (unsigned)__builtin_amdgcn_cvt_pk_fp8_f32((float)x[u][4 * i + 2] * f, (float)x[u][4 * i + 3] * f, w, true);
+        }
+        __builtin_memcpy((char*)cache + row[u] * D + at * V, y, sizeof(y));
+        if (at == 0) (key ? a.cache_ks : a.cache_vs)[row[u]] = scale;
       }
-      __builtin_memcpy((char*)cache + row * D + at * V, y, sizeof(y));
-      if (at == 0) (key ? a.cache_ks : a.cache_vs)[row] = scale;
     }
   }
 }

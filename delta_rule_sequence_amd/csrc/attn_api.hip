@@ -57,25 +57,26 @@ prism_status cache_check(int G, int D, int pages, int page, int max_pages, int T
   return (long long)max_pages * page + T > INT_MAX - 8192 ? PRISM_ERR_UNSUPPORTED : PRISM_OK;
 }
 
-#ifndef FW
-#define FW 4
-#define FK 256
-#define MWANT 2
-#define FR 64
-#endif
-// Few rows of queries: the rows of a group's heads share the cache's tiles, and its keys are split until the device is full.
+// How new tokens read the cache.  Few rows of a group's heads: tiles of 32 rows that share the cache's keys; else 128 rows of a head to a
+// workgroup, 256 of wide heads.  A sequence's keys are split until the device is full, into ranges of 512 keys or more (128 where
+// that leaves CUs without any).  Measured, us: 256 rows (8 x 16 heads x 32 tokens over 4096 of 128) 46 as few, 75 as many, 512 rows
+// (2 x 16 x 128 over 8192) 39 as many with one workgroup per CU, 48 with two (of 64 wide heads two fit a CU: 512 tokens 63
+// with two, 83 with one); 1 x 32 x 512 tokens over 4096: 88 with 128 rows, 62 with 256; single tokens of 13 x 2 over 11610: 38
+// with ranges of 512, 40 of 256; 4 x 8 over 500: 13.5 and 11.2 with 128.
 struct PagedPlan {
-  bool few;
-  int splits;
+  int rows, splits;               // rows of a tile: 32 (few), 128 or 256
   size_t total;
 };
-PagedPlan paged_plan(int B, int H, int G, int T, int D, int page, int max_pages) {
+PagedPlan paged_plan(int B, int H, int G, int T, int D, int page, int max_pages, prism_dtype dt) {
   PagedPlan pl;
   const size_t rows = (size_t)T * (H / G), keys = (size_t)max_pages * page;
-  pl.few = rows <= FR;
-  const size_t units = pl.few ? (size_t)B * G * ((rows + 31) / 32) : (size_t)B * H * ((T + 127) / 128);
-  const size_t want = ((pl.few ? FW : MWANT) * kCUs + units - 1) / units, most = std::max<size_t>(1, keys / (pl.few ? FK : 512));
-  pl.splits = (int)std::min<size_t>(std::min(want, most), 64);
+  const bool wide = D == 128 && dt == PRISM_BF16 && T >= 256;
+  pl.rows = rows <= 256 ? 32 : wide ? 256 : 128;
+  const size_t units = pl.rows == 32 ? (size_t)B * G * ((rows + 31) / 32) : (size_t)B * H * ((T + pl.rows - 1) / pl.rows);
+  const size_t want = ((pl.rows == 32 ? 4 : D == 128 ? 1 : 2) * kCUs + units - 1) / units;
+  size_t range = 512;
+  while (range > 128 && units * (keys / range) < kCUs) range /= 2;
+  pl.splits = (int)std::min<size_t>(std::min(want, std::max<size_t>(1, keys / range)), 64);
   Layout ly;
   if (pl.splits > 1) ly.add((size_t)pl.splits * B * H * T, (size_t)(D + 2) * 4);
   pl.total = ly.ok() ? std::max<size_t>(ly.total, 256) : 0;
@@ -238,7 +239,7 @@ prism_status prism_cache_write(const void* k, const prism_strides* k_strides, co
 size_t prism_attn_paged_workspace_bytes(int B, int H, int G, int T, int D, int page, int max_pages, prism_dtype dt) {
   if (attn_check(B, H, G, T, D, 0, nullptr, nullptr, 1.f, 0, dt) != PRISM_OK) return 0;
   if (cache_check(G, D, 1, page, max_pages, T, false, dt) != PRISM_OK) return 0;
-  return paged_plan(B, H, G, T, D, page, max_pages).total;
+  return paged_plan(B, H, G, T, D, page, max_pages, dt).total;
 }
 
 prism_status prism_attn_paged(const void* q, const prism_strides* q_strides, const void* cache_k, const void* cache_v,
@@ -255,7 +256,7 @@ prism_status prism_attn_paged(const void* q, const prism_strides* q_strides, con
   if (!make_strides(q_strides, B, H, T, D, &a.qs) || !make_strides(o_strides, B, H, T, D, &a.os) || !rows_apart(a.os, B, H, T, D))
     return PRISM_ERR_INVALID_ARG;
   if (!scan_rows(q, a.qs, D, dt) || !scan_rows(o, a.os, D, dt) || !aligned16(cache_k) || !aligned16(cache_v)) return PRISM_ERR_UNSUPPORTED;
-  const PagedPlan pl = paged_plan(B, H, G, T, D, page, max_pages);
+  const PagedPlan pl = paged_plan(B, H, G, T, D, page, max_pages, dt);
   if (pl.total == 0) return PRISM_ERR_INVALID_ARG;
   if (!workspace || workspace_bytes < pl.total) return PRISM_ERR_WORKSPACE;
   if (!aligned16(workspace)) return PRISM_ERR_INVALID_ARG;
@@ -264,7 +265,7 @@ prism_status prism_attn_paged(const void* q, const prism_strides* q_strides, con
   a.cache_ks = const_cast<float*>(scale_k), a.cache_vs = const_cast<float*>(scale_v), a.table = table, a.past = past;
   a.pages = pages, a.page_shift = __builtin_ctz((unsigned)page), a.max_pages = max_pages;
   a.o = o, a.splits = pl.splits, a.part = reinterpret_cast<float*>(workspace);
-  return host::launch_attn_paged(dt, D, scale_k != nullptr, pl.few, a, stream);
+  return host::launch_attn_paged(dt, D, scale_k != nullptr, pl.rows, a, stream);
 }
 
 }  // extern "C"

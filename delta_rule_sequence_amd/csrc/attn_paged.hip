@@ -14,45 +14,59 @@ prism_status write(const AttnArgs& a, hipStream_t s) {
   return launched();
 }
 
+template <class K>
+bool room(K kernel, int bytes) {
+  return hipFuncSetAttribute(reinterpret_cast<const void*>(kernel), hipFuncAttributeMaxDynamicSharedMemorySize, bytes) == hipSuccess;
+}
+
 template <class T, int D, attn::Keys KEYS>
-prism_status paged(bool few, const AttnArgs& a, hipStream_t s) {
-  using W = attn::FewTile<T, D, KEYS>;
-  constexpr int BN = sizeof(T) == 2 || D == 32 ? 64 : 32;
-#ifndef MW
-#define MW 4
-#endif
-  constexpr int NW = D == 128 && sizeof(T) == 2 ? MW : 4;
-  using M = attn::FwdTile<T, D, NW, BN, KEYS>;
-  const auto few_rows = attn::few_kernel<T, D, KEYS>;
-  const auto many_rows = attn::fwd_kernel<T, D, NW, BN, 1, KEYS>;
-  static const bool ok =
-      hipFuncSetAttribute(reinterpret_cast<const void*>(few_rows), hipFuncAttributeMaxDynamicSharedMemorySize, W::kLds) == hipSuccess &&
-      hipFuncSetAttribute(reinterpret_cast<const void*>(many_rows), hipFuncAttributeMaxDynamicSharedMemorySize, M::kLds) == hipSuccess;
+prism_status few(const AttnArgs& a, hipStream_t s) {
+  using F = attn::FewTile<T, D, KEYS>;
+  const auto kernel = attn::few_kernel<T, D, KEYS>;
+  static const bool ok = room(kernel, F::kLds);
   if (!ok) return PRISM_ERR_HIP;
-  if (few) few_rows<<<dim3(a.B * a.G * ((a.T * (a.H / a.G) + 31) / 32) * a.splits), 256, W::kLds, s>>>(a);
-  else many_rows<<<dim3(row_tiles(a, M::kRows) * a.H * a.splits), M::kThreads, M::kLds, s>>>(a);
-  if (a.splits > 1) {
-    const size_t rows = (size_t)a.B * a.H * a.T;
-    attn::join_kernel<T, D><<<dim3((unsigned)((rows + 3) / 4)), 256, 0, s>>>(a);
+  kernel<<<dim3((unsigned)(a.B * a.G * ((a.T * (a.H / a.G) + 31) / 32) * a.splits)), 256, F::kLds, s>>>(a);
+  return launched();
+}
+template <class T, int D, attn::Keys KEYS, int NW>
+prism_status many(const AttnArgs& a, hipStream_t s) {
+  constexpr int BN = sizeof(T) == 2 || D == 32 ? 64 : 32;
+  using F = attn::FwdTile<T, D, NW, BN, KEYS>;
+  const auto kernel = attn::fwd_kernel<T, D, NW, BN, 1, KEYS>;
+  static const bool ok = room(kernel, F::kLds);
+  if (!ok) return PRISM_ERR_HIP;
+  kernel<<<dim3((unsigned)(row_tiles(a, F::kRows) * a.H * a.splits)), F::kThreads, F::kLds, s>>>(a);
+  return launched();
+}
+template <class T, int D, attn::Keys KEYS>
+prism_status paged(int rows, const AttnArgs& a, hipStream_t s) {
+  prism_status st;
+  if (rows == 32) {
+    st = few<T, D, KEYS>(a, s);
+  } else {
+    if constexpr (D == 128 && sizeof(T) == 2) st = rows == 256 ? many<T, D, KEYS, 8>(a, s) : many<T, D, KEYS, 4>(a, s);
+    else st = many<T, D, KEYS, 4>(a, s);
   }
+  if (st != PRISM_OK || a.splits == 1) return st;
+  attn::join_kernel<T, D><<<dim3((unsigned)(((size_t)a.B * a.H * a.T + 3) / 4)), 256, 0, s>>>(a);
   return launched();
 }
 
 }  // namespace
 
-prism_status launch_cache_write(prism_dtype dt, int D, bool bits8, AttnArgs a, hipStream_t s) {
+prism_status launch_cache_write(prism_dtype dt, int D, bool bits8, const AttnArgs& a, hipStream_t s) {
   if (dt == PRISM_F32) return D == 32 ? write<float, 32, false>(a, s) : D == 64 ? write<float, 64, false>(a, s) : write<float, 128, false>(a, s);
   if (bits8) return D == 32 ? write<bf16_t, 32, true>(a, s) : D == 64 ? write<bf16_t, 64, true>(a, s) : write<bf16_t, 128, true>(a, s);
   return D == 32 ? write<bf16_t, 32, false>(a, s) : D == 64 ? write<bf16_t, 64, false>(a, s) : write<bf16_t, 128, false>(a, s);
 }
 
-prism_status launch_attn_paged(prism_dtype dt, int D, bool bits8, bool few, AttnArgs a, hipStream_t s) {
+prism_status launch_attn_paged(prism_dtype dt, int D, bool bits8, int rows, const AttnArgs& a, hipStream_t s) {
   using namespace attn;
   if (dt == PRISM_F32)
-    return D == 32 ? paged<float, 32, kCache>(few, a, s) : D == 64 ? paged<float, 64, kCache>(few, a, s) : paged<float, 128, kCache>(few, a, s);
+    return D == 32 ? paged<float, 32, kCache>(rows, a, s) : D == 64 ? paged<float, 64, kCache>(rows, a, s) : paged<float, 128, kCache>(rows, a, s);
   if (bits8)
-    return D == 32 ? paged<bf16_t, 32, kCache8>(few, a, s) : D == 64 ? paged<bf16_t, 64, kCache8>(few, a, s) : paged<bf16_t, 128, kCache8>(few, a, s);
-  return D == 32 ? paged<bf16_t, 32, kCache>(few, a, s) : D == 64 ? paged<bf16_t, 64, kCache>(few, a, s) : paged<bf16_t, 128, kCache>(few, a, s);
+    return D == 32 ? paged<bf16_t, 32, kCache8>(rows, a, s) : D == 64 ? paged<bf16_t, 64, kCache8>(rows, a, s) : paged<bf16_t, 128, kCache8>(rows, a, s);
+  return D == 32 ? paged<bf16_t, 32, kCache>(rows, a, s) : D == 64 ? paged<bf16_t, 64, kCache>(rows, a, s) : paged<bf16_t, 128, kCache>(rows, a, s);
 }
 
 }  // namespace host

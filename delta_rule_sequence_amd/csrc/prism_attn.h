@@ -23,6 +23,8 @@ typedef unsigned u32x4 __attribute__((ext_vector_type(4)));
 constexpr float kLog2e = 1.44269504088896341f, kLn2 = 0.693147180559945309f;
 constexpr float kInf = __builtin_inff();
 
+__device__ __forceinline__ int uniform(int x) { return __builtin_amdgcn_readfirstlane(x); }
+
 // ---- 32 x 32 tiles ---------------------------------------------------------------------------------
 // An operand's piece: 16 bytes of row l % 32; of the two pieces of a step, lane half h = l / 32 holds the h-th.  An
 // accumulator's register i in lane l is row 8 (i / 4) + 4 h + i % 4, column l % 32.
@@ -160,8 +162,6 @@ struct Seq {
   int head, group;     // head within its group, group
 };
 
-__device__ __forceinline__ int uniform(int x) { return __builtin_amdgcn_readfirstlane(x); }
-
 // Unit `unit` of all sequences' tiles of `rows` rows, `each` rows per token, times `rep` heads of G groups; a sequence's last tile first if `back`.
 // The tiles that take longest come first, and blocks that read the same rows of a group lie a multiple of G (where the
 // sequences are batches: of B G) apart: with a multiple of 8 they share an XCD and the rows in its L2.  With starts, a wave adds up
@@ -247,6 +247,28 @@ __device__ __forceinline__ u32x4 widen8(unsigned lo, unsigned hi) {
   return r;
 }
 
+// The pages of a tile's groups of 16 rows (a page has at least that many), asked for one tile ahead.
+template <int BN> struct Pages {
+  int id[BN / 16];
+  // Tile t; t1: the tiles' end, n: the keys.
+  __device__ __forceinline__ void ask(const AttnArgs& a, const int* table, int t, int t1, int n) {
+#pragma unroll
+    for (int g = 0; g < BN / 16; ++g) id[g] = t < t1 && t * BN + 16 * g < n ? table[(t * BN + 16 * g) >> a.page_shift] : -1;
+  }
+  __device__ __forceinline__ Pages now() const {
+    Pages p;
+#pragma unroll
+    for (int g = 0; g < BN / 16; ++g) p.id[g] = uniform(id[g]);
+    return p;
+  }
+  __device__ __forceinline__ int of(int row) const {
+    int p = id[0];
+#pragma unroll
+    for (int g = 1; g < BN / 16; ++g) p = row >= 16 * g ? id[g] : p;
+    return p;
+  }
+};
+
 // A tile's pieces of K or V (and rows' scales) between memory and LDS.
 template <class T, int D, int NT, int BN, Keys KEYS> struct KeyTile {
   using R = Rows<T, D>;
@@ -267,15 +289,15 @@ template <class T, int D, int NT, int BN, Keys KEYS> struct KeyTile {
 #pragma unroll
     for (int i = 0; i < kEach; ++i) x[i] = load16(r, (row + i * kStep) * stride + at);
   }
-  // Rows from j0 on of the sequence's pages; rows from `n` on and those of pages outside the cache are zeros.  id: the
-  // page that holds the whole tile, where pages are that large.
-  __device__ __forceinline__ void load_cache(const AttnArgs& a, const void* cache, const float* scales, const int* table, int id,
+  // Rows from j0 on of the sequence's pages; rows from `n` on and those of pages outside the cache are zeros.  pages: those of
+  // the tile's groups of 16 rows.
+  __device__ __forceinline__ void load_cache(const AttnArgs& a, const void* cache, const float* scales, const Pages<BN>& pages,
                                              int group, int j0, int n, int tid) {
     const int row = tid / kPieces, at = tid % kPieces * 16, page = 1 << a.page_shift;
     constexpr int kBytes = kPieces * 16;
-    if (page >= BN) {
-      const bool in = (unsigned)id < (unsigned)a.pages;
-      const size_t first = ((size_t)(in ? id : 0) * a.G + group) * page + (j0 & (page - 1));
+    if (page >= BN) {                                                 // one page
+      const bool in = (unsigned)pages.id[0] < (unsigned)a.pages;
+      const size_t first = ((size_t)(in ? pages.id[0] : 0) * a.G + group) * page + (j0 & (page - 1));
       const auto r = rows_of((const char*)cache + first * kBytes, in ? min(n - j0, BN) : 0, kBytes, kBytes);
       if (!kPart || row < BN) {
 #pragma unroll
@@ -284,22 +306,16 @@ template <class T, int D, int NT, int BN, Keys KEYS> struct KeyTile {
     } else {
 #pragma unroll
       for (int i = 0; i < kEach; ++i) {
-        const int j = j0 + row + i * kStep;
+        const int r = row + i * kStep, j = j0 + r, p = pages.of(r);
         x[i] = u32x4{0, 0, 0, 0};
-        if ((!kPart || row < BN) && j < n) {
-          const int p = table[j >> a.page_shift];
-          if ((unsigned)p < (unsigned)a.pages)
-            x[i] = *reinterpret_cast<const u32x4*>((const char*)cache + (((size_t)p * a.G + group) * page + (j & (page - 1))) * kBytes + at);
-        }
+        if ((!kPart || row < BN) && j < n && (unsigned)p < (unsigned)a.pages)
+          x[i] = *reinterpret_cast<const u32x4*>((const char*)cache + (((size_t)p * a.G + group) * page + (j & (page - 1))) * kBytes + at);
       }
     }
     if constexpr (KEYS == kCache8) {
-      const int j = j0 + tid;
+      const int j = j0 + tid, p = pages.of(tid & (BN - 1));
       scale = 0.f;
-      if (tid < BN && j < n) {
-        const int p = page >= BN ? id : table[j >> a.page_shift];
-        if ((unsigned)p < (unsigned)a.pages) scale = scales[((size_t)p * a.G + group) * page + (j & (page - 1))];
-      }
+      if (tid < BN && j < n && (unsigned)p < (unsigned)a.pages) scale = scales[((size_t)p * a.G + group) * page + (j & (page - 1))];
     }
   }
   __device__ __forceinline__ void store(char* tile, float* scales, int tid) const {
@@ -508,21 +524,20 @@ __global__ __launch_bounds__(64 * NW, D * (int)sizeof(T) > 256 ? 1 : 2) void fwd
     table = a.table + (size_t)s.b * a.max_pages;
   }
   KeyTile<T, D, F::kThreads, BN, KEYS> nk, nv;
-  // the page of a tile, asked for one tile ahead
-  const auto page_of = [&](int t) { return KEYS != kPrompt && t < t1 && (1 << a.page_shift) >= BN ? table[t * BN >> a.page_shift] : 0; };
-  int id = page_of(t0), id_v = 0;
+  Pages<BN> coming, of_v;                                             // pages of the tile after the last asked for, and of that one
+  if constexpr (KEYS != kPrompt) coming.ask(a, table, t0, t1, keys);
   const auto load_k = [&](int t) {                                    // in the order of the tiles
     if constexpr (KEYS == kPrompt) {
       nk.load_prompt(kp + (long long)t * BN * kst, kst, keys - t * BN, tid);
     } else {
-      id_v = uniform(id);
-      nk.load_cache(a, a.cache_k, a.cache_ks, table, id_v, group, t * BN, keys, tid);
-      id = page_of(t + 1);
+      of_v = coming.now();
+      nk.load_cache(a, a.cache_k, a.cache_ks, of_v, group, t * BN, keys, tid);
+      coming.ask(a, table, t + 1, t1, keys);
     }
   };
-  const auto load_v = [&](int t, int page) {
+  const auto load_v = [&](int t) {                                    // behind load_k of the same tile
     if constexpr (KEYS == kPrompt) nv.load_prompt(vp + (long long)t * BN * vst, vst, keys - t * BN, tid);
-    else nv.load_cache(a, a.cache_v, a.cache_vs, table, page, group, t * BN, keys, tid);
+    else nv.load_cache(a, a.cache_v, a.cache_vs, of_v, group, t * BN, keys, tid);
   };
   char* const v_tiles = lds + 3 * F::kTile;
   float* const scales = reinterpret_cast<float*>(lds + 6 * F::kTile + F::kZero);  // three of K, three of V
@@ -554,13 +569,13 @@ __global__ __launch_bounds__(64 * NW, D * (int)sizeof(T) > 256 ? 1 : 2) void fwd
   int buf = 0;                                                        // tile t's place in LDS
   if (t0 < t1) {
     load_k(t0);
-    load_v(t0, id_v);
+    load_v(t0);
     nk.store(lds, scales, tid);
     nv.store(v_tiles, scales + 3 * BN, tid);
     if (t0 + 1 < t1) {
       load_k(t0 + 1);
       nk.store(lds + F::kTile, scales + BN, tid);
-      load_v(t0 + 1, id_v);
+      load_v(t0 + 1);
     }
     if (t0 + 2 < t1) load_k(t0 + 2);
   }
@@ -569,7 +584,7 @@ __global__ __launch_bounds__(64 * NW, D * (int)sizeof(T) > 256 ? 1 : 2) void fwd
   const auto stage = [&](int t, int buf1, int buf2) {
     if (t + 2 < t1) nk.store(lds + buf2 * F::kTile, scales + buf2 * BN, tid);
     if (t + 1 < t1) nv.store(v_tiles + buf1 * F::kTile, scales + (3 + buf1) * BN, tid);
-    if (t + 2 < t1) load_v(t + 2, id_v);
+    if (t + 2 < t1) load_v(t + 2);
     if (t + 3 < t1) load_k(t + 3);
   };
   const int tw = min(t1, max(t0, wlast / BN + 1));                    // the wave's own tiles
@@ -738,16 +753,17 @@ __global__ __launch_bounds__(256, D * (int)sizeof(T) > 256 ? 1 : 2) void few_ker
   char* const vt = kt + F::kTile;
   float* const scales = reinterpret_cast<float*>(kt + 2 * F::kTile);
   KeyTile<T, D, 64, 32, KEYS> nk, nv;
-  const auto page_of = [&](int t) { return KEYS != kPrompt && t < t1 && a.page_shift >= 5 ? table[t * 32 >> a.page_shift] : 0; };
-  int id = page_of(t0 + w);
+  Pages<32> coming;
+  if constexpr (KEYS != kPrompt) coming.ask(a, table, t0 + w, t1, keys);
   const auto load = [&](int t) {
     if constexpr (KEYS == kPrompt) {
       nk.load_prompt(kp + (long long)t * 32 * kst, kst, keys - t * 32, l);
       nv.load_prompt(vp + (long long)t * 32 * vst, vst, keys - t * 32, l);
     } else {
-      nk.load_cache(a, a.cache_k, a.cache_ks, table, uniform(id), group, t * 32, keys, l);
-      nv.load_cache(a, a.cache_v, a.cache_vs, table, uniform(id), group, t * 32, keys, l);
-      id = page_of(t + 4);
+      const Pages<32> pages = coming.now();
+      nk.load_cache(a, a.cache_k, a.cache_ks, pages, group, t * 32, keys, l);
+      nv.load_cache(a, a.cache_v, a.cache_vs, pages, group, t * 32, keys, l);
+      coming.ask(a, table, t + 4, t1, keys);
     }
   };
   if (t0 + w < t1) load(t0 + w);

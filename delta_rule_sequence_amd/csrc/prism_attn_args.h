@@ -48,8 +48,8 @@ struct RopeArgs {
 };
 
 namespace host {
-prism_status launch_cache_write(prism_dtype dt, int D, bool bits8, AttnArgs a, hipStream_t stream);
-prism_status launch_attn_paged(prism_dtype dt, int D, bool bits8, bool few, AttnArgs a, hipStream_t stream);
+prism_status launch_cache_write(prism_dtype dt, int D, bool bits8, const AttnArgs& a, hipStream_t stream);
+prism_status launch_attn_paged(prism_dtype dt, int D, bool bits8, int rows, const AttnArgs& a, hipStream_t stream);
 prism_status launch_rope(prism_dtype dt, bool bwd, const RopeArgs& a, hipStream_t stream);
 // Each enqueues on `stream` and reports launch failures.
 prism_status launch_attn_fwd(prism_dtype dt, int D, const AttnArgs& a, hipStream_t stream);

@@ -25,7 +25,7 @@ __global__ __launch_bounds__(256) void cache_write_kernel(AttnArgs a) {
   const long long past = max(a.past[s.id], 0);
   const int* table = a.table + (size_t)s.id * a.max_pages;
   const int page = 1 << a.page_shift;
-  constexpr int U = 4;                                                 // rows in flight
+  constexpr int U = 8;                                                 // rows in flight
   for (int first = threadIdx.x / L; first < n * 2 * G; first += U * (256 / L)) {
     vec x[U];
     long long row[U];                                                  // -1: not written

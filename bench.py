@@ -21,6 +21,10 @@ times the forward with the nonlinear refinement (prism_fwd_nl) and its factor ke
 times the state space layer (convolution, scan, gated norm) on the workload's shape: a
 prompt, its gradients and one token.
 
+    python bench.py --attention [--workload NAME] [--steps K]
+times the attention layer (norm and rotation, softmax attention, paged cache) on the workload's shape: a
+prompt, its gradients and one token over the cache that the prompt left.
+
     python bench.py --calibrate-copy MB
 runs a plain device-to-device copy of MB megabytes (for scaling the
 FETCH_SIZE / WRITE_SIZE counters of rocprofv3) and exits.
@@ -629,6 +633,71 @@ def layer_bench(steps, warmup, w):
                       "peak_GBs": HBM_PEAK_GBS, **res}), flush=True)
 
 
+def attention_bench(steps, warmup, w):
+    """The attention layer at workload w's shape (H heads of dv channels, a key head for every two where H is even): norm
+    and rotation, attention and the cache's write over a prompt, the backward of the first two, and one token over that
+    cache, each a run of its operators on resident inputs, two input sets in turn.  One JSON line: ms per run, tokens/s and
+    the achieved rate on the causal products (bytes for the token)."""
+    import torch
+    import delta_rule_sequence_amd as prism
+    B, H, T, D, page = w.B, w.H, w.T, w.dv, 64
+    G, E = (H // 2 if H % 2 == 0 else H), 2 if w.dtype == "bf16" else 4
+    gen = torch.Generator(device="cuda").manual_seed(w.seed)
+    vt = torch.bfloat16 if w.dtype == "bf16" else torch.float32
+
+    def heads(t):
+        return [x.transpose(1, 2) for x in torch.randn(B, t, H + 2 * G, D, generator=gen, device="cuda").to(vt).split((H, G, G), 2)]
+
+    freq = 10000.0 ** (-torch.arange(D // 2, device="cuda") / (D // 2))
+    wq, wk = torch.ones(D, device="cuda"), torch.ones(D, device="cuda")
+    each = -(-(T + 1) // page)
+    table = torch.randperm(B * each, generator=gen, device="cuda").int().view(B, each)
+    start, last = torch.zeros(B, dtype=torch.int32, device="cuda"), torch.full((B,), T, dtype=torch.int32, device="cuda")
+    sets = []
+    for _ in range(2):
+        s = dict(zip("qkv", heads(T)), cache=[torch.zeros(B * each, G, page, D, dtype=vt, device="cuda") for _ in range(2)])
+        s["token"], s["do"] = heads(1), torch.randn(B, T, H, D, generator=gen, device="cuda").to(vt).transpose(1, 2)
+        sets.append(s)
+
+    def forward(s):
+        q, k = prism.rope_fwd(s["q"], s["k"], freq, wq=wq, wk=wk)
+        o, lse = prism.attn_fwd(q, k, s["v"])
+        prism.cache_write(*s["cache"], k, s["v"], table, start)
+        return q, k, o, lse
+
+    def backward(s):
+        q, k, o, lse = s["saved"]
+        g = prism.attn_bwd(q, k, s["v"], o, lse, s["do"])
+        return prism.rope_bwd(s["q"], s["k"], g["dq"], g["dk"], freq, wq=wq, wk=wk), g["dv"]
+
+    def token(s):
+        q, k, v = s["token"]
+        q, k = prism.rope_fwd(q, k, freq, pos=last.unsqueeze(1), wq=wq, wk=wk)
+        prism.cache_write(*s["cache"], k, v, table, last)
+        return prism.attn_paged(q, *s["cache"], table, last)
+
+    for s in sets:
+        s["saved"] = forward(s)
+    pairs = B * H * T * (T + 1) / 2
+    work = {"forward": (forward, B * T, 4 * pairs * D, None), "backward": (backward, B * T, 10 * pairs * D, None),
+            "token": (token, B, None, 2 * B * G * (T + 1) * D * E)}
+    res = {}
+    for name, (fn, tokens, flops, moved) in work.items():
+        for i in range(warmup):
+            fn(sets[i % 2])
+        torch.cuda.synchronize()
+        t0 = time.perf_counter()
+        for i in range(steps):
+            fn(sets[i % 2])
+        torch.cuda.synchronize()
+        ms = (time.perf_counter() - t0) / steps * 1e3
+        res[name] = {"ms_per_step": ms, "tokens_per_s": tokens / ms * 1e3}
+        res[name].update({"achieved_TFLOPs": flops / ms / 1e9} if flops else {"achieved_GBs": moved / ms / 1e6})
+    print(json.dumps({"metric": "attention layer (norm and rotation, attention, paged cache)", "workload": w.name, "dtype": w.dtype,
+                      "config": {"B": B, "H": H, "G": G, "T": T, "D": D, "page": page}, "steps": steps, "warmup": warmup,
+                      "peak_TFLOPs": MFMA_PEAK_TFLOPS, "peak_GBs": HBM_PEAK_GBS, **res}), flush=True)
+
+
 def main():
     ap = argparse.ArgumentParser()
     ap.add_argument("--gpus", type=int, default=1)
@@ -651,6 +720,8 @@ def main():
                     help="time the nonlinear-refinement forward (prism_fwd_nl) on --workload instead")
     ap.add_argument("--layer", action="store_true",
                     help="time the state space layer on --workload's shape instead")
+    ap.add_argument("--attention", action="store_true",
+                    help="time the attention layer on --workload's shape instead")
     ap.add_argument("--forward-only", action="store_true",
                     help="the forward's line only: skip the backward, nonlinear, copy and GEMM legs "
                          "(for profiler runs)")
@@ -676,6 +747,10 @@ def main():
     if args.layer:
         import workloads
         layer_bench(args.steps, args.warmup, workloads.workload(args.workload))
+        return
+    if args.attention:
+        import workloads
+        attention_bench(args.steps, args.warmup, workloads.workload(args.workload))
         return
     if args.nl:
         import workloads

@@ -249,7 +249,8 @@ __device__ __forceinline__ u32x4 widen8(unsigned lo, unsigned hi) {
 
 // The pages of a tile's groups of 16 rows (a page has at least that many), asked for one tile ahead.
 template <int BN> struct Pages {
-  int id[BN / 16];
+  typedef int Ids __attribute__((ext_vector_type(BN / 16)));
+  Ids id;
   // Tile t; t1: the tiles' end, n: the keys.
   __device__ __forceinline__ void ask(const AttnArgs& a, const int* table, int t, int t1, int n) {
 #pragma unroll

@@ -580,11 +580,74 @@ prism_status prism_norm_bwd(const void* h, long long h_stride, const float* weig
                             prism_dtype dt, void* dh, void* dgate, float* dweight,
                             void* workspace, size_t workspace_bytes, hipStream_t stream);
 
+/* ---- The attention layer: norm and rotation of heads, softmax attention of prompts, paged cache -----
+ *
+ * Hybrid models put softmax attention between the recurrence's layers.  A layer runs prism_rope_fwd on its
+ * projected queries and keys, then prism_attn_fwd on a prompt (training: prism_attn_bwd and
+ * prism_rope_bwd); when it serves, prism_cache_write puts keys and values into a cache of pages and
+ * prism_attn_paged lets new tokens, one or a chunk, attend over it.  H heads of queries share G heads of
+ * keys and values, H / G to each: head h reads group h / (H / G).
+ *
+ * Tensors [B, H, T, D] and [B, G, T, D], their strides (NULL = dense), ownership, streams and errors as in the
+ * state space layer; outputs share no memory with inputs but where it is said.  dt: PRISM_BF16 or PRISM_F32,
+ * one for all of a call's tensors.  Attention takes D in {32, 64, 128} and rows that start on 16-byte boundaries, do
+ * not overlap from token to token and are at most 16 MB apart (else PRISM_ERR_UNSUPPORTED); scale is
+ * positive and finite.  Sizes past T = 2^31 - 4097, H = 65535, T H / G = 2^31 - 4097, or 2^23 tiles of 32 tokens
+ * times H return PRISM_ERR_UNSUPPORTED.
+ *
+ * Sequences.  lens [B] int32 or NULL (= T): tokens of each sequence of a padded batch, clamped to 0 .. T.  Or starts
+ * [S + 1] int32 with B = 1 and lens = NULL: sequence s is the tokens starts[s] .. starts[s + 1] - 1 of the row of T;
+ * starts do not decrease and are clamped to 0 .. T (S = 0 without starts).  Rows of no sequence are neither read nor
+ * written.
+ *
+ * Precision.  Scores, the running maximum and sum of the softmax and all sums are float32, and every sum has a
+ * fixed order.  With PRISM_BF16 the probabilities enter their product with the values as bfloat16, and in the
+ * gradients so do they and the gradients of the scores: each output is off by its own rounding and about one more of its
+ * terms.  (Where few rows leave time, as for single tokens over a cache, they enter as two bfloat16 parts, which keep 16 bits.)
+ * Non-finite inputs: a query's reach its own row of o and lse, a key's or value's the rows that see it; in the
+ * gradients they may also reach tokens within 256 of those.  Scores past 45000 in magnitude, and results that are
+ * not finite, are formed again key by key, which takes longer. */
+
+/* Norm (optional) and rotation of queries and keys, in one pass:
+ *   h = w x / sqrt(mean(x^2) + eps) over a head's D channels where wq and wk [D] float32 are given (both or neither); else h = x
+ *   for pair i < rot / 2 of channels (a, b) and the angle pos * freq[i]:
+ *   y_a = factor (h_a cos - h_b sin),  y_b = factor (h_b cos + h_a sin);  channels from rot on: y = h
+ *   pairs: channels (i, i + rot / 2), or (2 i, 2 i + 1) if interleaved
+ *   freq [rot / 2] float32 (the caller scales them for long contexts, and passes what belongs on cos and sin as factor)
+ *   pos  [B, T] int32 or NULL (the token's index t)
+ *   yq, yk: strided; each may be its input's own buffer with the same strides.
+ * D even, up to 512, rot even, 2 .. D; any alignment of whole elements; B T (H + G) up to 2^25.  Angles in float64. */
+prism_status prism_rope_fwd(const void* q, const prism_strides* q_strides, const void* k, const prism_strides* k_strides,
+                            const float* freq, const int* pos, const float* wq, const float* wk,
+                            int B, int H, int G, int T, int D, int rot, int interleaved, float factor, float eps,
+                            prism_dtype dt, void* yq, const prism_strides* yq_strides, void* yk,
+                            const prism_strides* yk_strides, hipStream_t stream);
+
+/* Gradients of sum <dyq, yq> + <dyk, yk> for prism_rope_fwd (freq and pos are constants):
+ *   dq, dk: strided, dtype dt; each may be its dyq's or dyk's own buffer with the same strides
+ *   dwq, dwk [D] float32 (NULL = not wanted; only with weights), summed over rows and heads in a fixed order.
+ * q and k are read with weights only.  Workspace: prism_rope_bwd_workspace_bytes, needed with dwq or dwk only. */
+size_t prism_rope_bwd_workspace_bytes(int B, int H, int G, int T, int D, int rot, prism_dtype dt);
+prism_status prism_rope_bwd(const void* q, const prism_strides* q_strides, const void* k, const prism_strides* k_strides,
+                            const void* dyq, const prism_strides* dyq_strides, const void* dyk,
+                            const prism_strides* dyk_strides, const float* freq, const int* pos, const float* wq,
+                            const float* wk, int B, int H, int G, int T, int D, int rot, int interleaved, float factor,
+                            float eps, prism_dtype dt, void* dq, const prism_strides* dq_strides, void* dk,
+                            const prism_strides* dk_strides, float* dwq, float* dwk, void* workspace,
+                            size_t workspace_bytes, hipStream_t stream);
+
+/* Softmax attention within sequences:  s_ij = scale <q_i, k_j>,  o_i = sum_j softmax_j(s_ij) v_j,
+ * lse_i = log sum_j exp(s_ij), over the tokens j of i's sequence: all of them, or if causal those with j <= i, and with
+ * window > 0 (causal only) of these the last `window`.
+ *   o   [B, H, T, D] dtype dt, strided;  lse [B, H, T] float32, dense, or NULL (not written). */
 prism_status prism_attn_fwd(const void* q, const prism_strides* q_strides, const void* k, const prism_strides* k_strides,
                             const void* v, const prism_strides* v_strides, const int* lens, const int* starts, int S,
                             int B, int H, int G, int T, int D, float scale, int causal, int window, prism_dtype dt,
                             void* o, const prism_strides* o_strides, float* lse, hipStream_t stream);
 
+/* Gradients of sum <d_o, o> for prism_attn_fwd with the same arguments, from its o and lse:
+ *   dq [B, H, T, D], dk, dv [B, G, T, D] dtype dt, strided (dk, dv: summed over the group's heads in float32).
+ * They share no memory with the inputs.  Workspace: prism_attn_bwd_workspace_bytes. */
 size_t prism_attn_bwd_workspace_bytes(int B, int H, int G, int T, int D, prism_dtype dt);
 prism_status prism_attn_bwd(const void* q, const prism_strides* q_strides, const void* k, const prism_strides* k_strides,
                             const void* v, const prism_strides* v_strides, const void* o, const prism_strides* o_strides,
@@ -594,23 +657,26 @@ prism_status prism_attn_bwd(const void* q, const prism_strides* q_strides, const
                             void* dk, const prism_strides* dk_strides, void* dv, const prism_strides* dv_strides,
                             void* workspace, size_t workspace_bytes, hipStream_t stream);
 
-prism_status prism_rope_fwd(const void* q, const prism_strides* q_strides, const void* k, const prism_strides* k_strides,
-                            const float* freq, const int* pos, const float* wq, const float* wk,
-                            int B, int H, int G, int T, int D, int rot, int interleaved, float factor, float eps,
-                            prism_dtype dt, void* yq, const prism_strides* yq_strides, void* yk,
-                            const prism_strides* yk_strides, hipStream_t stream);
-size_t prism_rope_bwd_workspace_bytes(int B, int H, int G, int T, int D, int rot, prism_dtype dt);
-prism_status prism_rope_bwd(const void* q, const prism_strides* q_strides, const void* k, const prism_strides* k_strides,
-                            const void* dyq, const prism_strides* dyq_strides, const void* dyk,
-                            const prism_strides* dyk_strides, const float* freq, const int* pos, const float* wq,
-                            const float* wk, int B, int H, int G, int T, int D, int rot, int interleaved, float factor,
-                            float eps, prism_dtype dt, void* dq, const prism_strides* dq_strides, void* dk,
-                            const prism_strides* dk_strides, float* dwq, float* dwk, void* workspace,
-                            size_t workspace_bytes, hipStream_t stream);
+/* The paged cache.  cache_k, cache_v [pages, G, page, D]: of dtype dt, or, with scale_k and scale_v [pages, G, page]
+ * float32 (dt = PRISM_BF16 only), OCP e4m3 bytes whose value is byte value * scale.  page: a power of two, 16 .. 1024.
+ * Position p of sequence s lies in row p % page of page table[s, p / page];  table [S, max_pages] int32, past [S] int32:
+ * positions of the sequence in front of this call's tokens (S = B without starts).  max_pages * page + T < 2^31 - 8192.
+ *
+ * prism_cache_write writes rows k, v [B, G, T, D] (strided): token t of sequence s at position past[s] + t.  With 8 bits
+ * scale = (the largest |x| of the row) / 448, or 1 and bytes of 0 where all are below 2^-100; a row with a non-finite
+ * value has a scale of infinity or NaN and bytes of NaN.  Positions past max_pages * page and pages outside
+ * 0 .. pages - 1 are not written; two positions that share a row leave either's. */
 prism_status prism_cache_write(const void* k, const prism_strides* k_strides, const void* v, const prism_strides* v_strides,
                                const int* table, const int* past, const int* lens, const int* starts, int S,
                                int B, int G, int T, int D, int pages, int page, int max_pages, prism_dtype dt,
                                void* cache_k, void* cache_v, float* scale_k, float* scale_v, hipStream_t stream);
+
+/* Attention of new tokens q [B, H, T, D] (strided) over the paged cache, which holds their own keys and values
+ * already: token t < lens[b] (NULL = T) of sequence b has position past[b] + t (past clamped to 0 .. max_pages * page) and
+ * sees the positions up to its own, with window > 0 the last `window` of them.  Pages outside 0 .. pages - 1 read as
+ * zeros; positions past max_pages * page are not there, and a token that sees none has an o of zeros.
+ *   o [B, H, T, D] dtype dt, strided; not q's buffer; rows past a length are left as they were.
+ * Workspace: prism_attn_paged_workspace_bytes. */
 size_t prism_attn_paged_workspace_bytes(int B, int H, int G, int T, int D, int page, int max_pages, prism_dtype dt);
 prism_status prism_attn_paged(const void* q, const prism_strides* q_strides, const void* cache_k, const void* cache_v,
                               const float* scale_k, const float* scale_v, const int* table, const int* past,

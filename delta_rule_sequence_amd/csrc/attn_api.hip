@@ -33,6 +33,13 @@ prism_status attn_check(int B, int H, int G, int T, int D, int S, const int* len
 // Norm and rotation: sizes, and the lane groups' share of a token's heads.
 int rope_lanes(int D, int rot) { return D % 8 != 0 || rot % 8 != 0 ? 64 : D <= 32 ? 4 : D <= 64 ? 8 : D <= 128 ? 16 : D <= 256 ? 32 : 64; }
 
+// An output's rows may be those of its own input, with its strides.
+bool same(const prism_strides& x, const prism_strides& y) { return x.b == y.b && x.h == y.h && x.t == y.t; }
+bool in_place(const void* const* x, const prism_strides* xs, void* const* y, const prism_strides* ys) {
+  if (y[0] == y[1] || y[0] == x[1] || y[1] == x[0]) return false;
+  return (y[0] != x[0] || same(xs[0], ys[0])) && (y[1] != x[1] || same(xs[1], ys[1]));
+}
+
 prism_status rope_plan(int B, int H, int G, int T, int D, int rot, float factor, float eps, prism_dtype dt, RopeArgs* a) {
   if (B <= 0 || H <= 0 || G <= 0 || T <= 0 || D <= 0 || rot <= 0 || rot > D || !known(dt)) return PRISM_ERR_INVALID_ARG;
   if (!(eps >= 0.f) || !std::isfinite(factor)) return PRISM_ERR_INVALID_ARG;
@@ -93,7 +100,7 @@ prism_status prism_attn_fwd(const void* q, const prism_strides* q_strides, const
                             void* o, const prism_strides* o_strides, float* lse, hipStream_t stream) {
   const prism_status st = attn_check(B, H, G, T, D, S, lens, starts, scale, window, dt);
   if (st != PRISM_OK) return st;
-  if (!q || !k || !v || !o || o == k || o == v) return PRISM_ERR_INVALID_ARG;
+  if (!q || !k || !v || !o || o == q || o == k || o == v) return PRISM_ERR_INVALID_ARG;
   if (window > 0 && !causal) return PRISM_ERR_INVALID_ARG;
   AttnArgs a = {};
   if (!make_strides(q_strides, B, H, T, D, &a.qs) || !make_strides(k_strides, B, G, T, D, &a.ks) ||
@@ -157,6 +164,7 @@ prism_status prism_attn_bwd(const void* q, const prism_strides* q_strides, const
   // dq is written before the other kernel reads q, k, v and do; dk before other workgroups have read k
   for (const void* in : {q, k, v, o, d_o})
     if (dq == in || dk == in || dv == in) return PRISM_ERR_INVALID_ARG;
+  if (dq == dk || dq == dv || dk == dv) return PRISM_ERR_INVALID_ARG;
   a.q = q, a.k = k, a.v = v, a.o = const_cast<void*>(o), a.lse = const_cast<float*>(lse), a.dout = d_o;
   a.lens = lens, a.starts = starts, a.B = B, a.H = H, a.G = G, a.T = T, a.S = S;
   a.causal = causal != 0, a.window = window, a.scale = scale;
@@ -180,6 +188,7 @@ prism_status prism_rope_fwd(const void* q, const prism_strides* q_strides, const
     return PRISM_ERR_INVALID_ARG;
   a.x[0] = q, a.x[1] = k, a.y[0] = yq, a.y[1] = yk, a.w[0] = wq, a.w[1] = wk, a.freq = freq, a.pos = pos;
   a.interleaved = interleaved != 0;
+  if (!in_place(a.x, a.xs, a.y, a.ys)) return PRISM_ERR_INVALID_ARG;
   return host::launch_rope(dt, false, a, stream);
 }
 
@@ -216,6 +225,8 @@ prism_status prism_rope_bwd(const void* q, const prism_strides* q_strides, const
   }
   a.x[0] = q, a.x[1] = k, a.dy[0] = dyq, a.dy[1] = dyk, a.y[0] = dq, a.y[1] = dk, a.w[0] = wq, a.w[1] = wk;
   a.dw[0] = dwq, a.dw[1] = dwk, a.freq = freq, a.pos = pos, a.interleaved = interleaved != 0;
+  if (!in_place(a.dy, a.dys, a.y, a.ys)) return PRISM_ERR_INVALID_ARG;
+  if (norm && (dq == q || dq == k || dk == q || dk == k)) return PRISM_ERR_INVALID_ARG;
   return host::launch_rope(dt, true, a, stream);
 }
 
@@ -230,6 +241,7 @@ prism_status prism_cache_write(const void* k, const prism_strides* k_strides, co
   AttnArgs a = {};
   if (!make_strides(k_strides, B, G, T, D, &a.ks) || !make_strides(v_strides, B, G, T, D, &a.vs)) return PRISM_ERR_INVALID_ARG;
   if (!scan_rows(k, a.ks, D, dt) || !scan_rows(v, a.vs, D, dt) || !aligned16(cache_k) || !aligned16(cache_v)) return PRISM_ERR_UNSUPPORTED;
+  if (cache_k == cache_v || (scale_k != nullptr && scale_k == scale_v)) return PRISM_ERR_INVALID_ARG;
   a.k = k, a.v = v, a.lens = lens, a.starts = starts, a.B = B, a.H = G, a.G = G, a.T = T, a.S = S;
   a.cache_k = cache_k, a.cache_v = cache_v, a.cache_ks = scale_k, a.cache_vs = scale_v, a.table = table, a.past = past;
   a.pages = pages, a.page_shift = __builtin_ctz((unsigned)page), a.max_pages = max_pages;

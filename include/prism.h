@@ -615,7 +615,7 @@ prism_status prism_norm_bwd(const void* h, long long h_stride, const float* weig
  *   pairs: channels (i, i + rot / 2), or (2 i, 2 i + 1) if interleaved
  *   freq [rot / 2] float32 (the caller scales them for long contexts, and passes what belongs on cos and sin as factor)
  *   pos  [B, T] int32 or NULL (the token's index t)
- *   yq, yk: strided; each may be its input's own buffer with the same strides.
+ *   yq, yk: strided; each may be its own input's buffer with the same strides (not the other one's).
  * D even, up to 512, rot even, 2 .. D; any alignment of whole elements; B T (H + G) up to 2^25.  Angles in float64. */
 prism_status prism_rope_fwd(const void* q, const prism_strides* q_strides, const void* k, const prism_strides* k_strides,
                             const float* freq, const int* pos, const float* wq, const float* wk,
@@ -624,7 +624,7 @@ prism_status prism_rope_fwd(const void* q, const prism_strides* q_strides, const
                             const prism_strides* yk_strides, hipStream_t stream);
 
 /* Gradients of sum <dyq, yq> + <dyk, yk> for prism_rope_fwd (freq and pos are constants):
- *   dq, dk: strided, dtype dt; each may be its dyq's or dyk's own buffer with the same strides
+ *   dq, dk: strided, dtype dt; each may be its own dyq's or dyk's buffer with the same strides
  *   dwq, dwk [D] float32 (NULL = not wanted; only with weights), summed over rows and heads in a fixed order.
  * q and k are read with weights only.  Workspace: prism_rope_bwd_workspace_bytes, needed with dwq or dwk only. */
 size_t prism_rope_bwd_workspace_bytes(int B, int H, int G, int T, int D, int rot, prism_dtype dt);
@@ -647,7 +647,7 @@ prism_status prism_attn_fwd(const void* q, const prism_strides* q_strides, const
 
 /* Gradients of sum <d_o, o> for prism_attn_fwd with the same arguments, from its o and lse:
  *   dq [B, H, T, D], dk, dv [B, G, T, D] dtype dt, strided (dk, dv: summed over the group's heads in float32).
- * They share no memory with the inputs.  Workspace: prism_attn_bwd_workspace_bytes. */
+ * They share no memory with the inputs nor with each other.  Workspace: prism_attn_bwd_workspace_bytes. */
 size_t prism_attn_bwd_workspace_bytes(int B, int H, int G, int T, int D, prism_dtype dt);
 prism_status prism_attn_bwd(const void* q, const prism_strides* q_strides, const void* k, const prism_strides* k_strides,
                             const void* v, const prism_strides* v_strides, const void* o, const prism_strides* o_strides,

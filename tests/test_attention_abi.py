@@ -117,6 +117,25 @@ def test_attention_outputs_over_inputs(lib):
     assert attn_fwd(lib, k=Q) == INVALID and attn_fwd(lib, v=Q) == INVALID
 
 
+def test_outputs_apart(lib):
+    R, S = 1 << 22, 1 << 23
+    assert attn_fwd(lib, o=P) == INVALID                               # a query's buffer: its rows may still be read
+    assert attn_fwd(lib, q=Q) == INVALID
+    for two in (("dq", "dk"), ("dq", "dv"), ("dk", "dv")):
+        at = {"dq": Q, "dk": R, "dv": S}
+        at[two[1]] = at[two[0]]
+        assert attn_bwd(lib, **at) == INVALID, two
+    # rotation: an output over its own input has its strides; never over the other one
+    assert rope_fwd(lib, q=P, k=R, yq=Q, yk=Q) == INVALID
+    assert rope_fwd(lib, q=P, k=R, yq=R, yk=Q) == INVALID and rope_fwd(lib, q=P, k=R, yq=Q, yk=P) == INVALID
+    assert rope_fwd(lib, q=P, k=R, yq=P, ys=st(2048, 64, 128), yk=Q) == INVALID
+    assert rope_bwd(lib, dyq=P, dyk=R, dq=P, dqs=st(2048, 64, 128), dk=Q) == INVALID
+    assert rope_bwd(lib, dyq=P, dyk=R, dq=R, dk=Q) == INVALID and rope_bwd(lib, dyq=P, dyk=R, dq=Q, dk=Q) == INVALID
+    assert rope_bwd(lib, q=S, k=P, dyq=R, dyk=R, dq=S, dk=Q) == INVALID
+    assert cache_write(lib, ck=Q, cv=Q) == INVALID
+    assert cache_write(lib, ck=Q, cv=R, sk=S, sv=S) == INVALID
+
+
 def test_workspaces(lib):
     need = lib.prism_attn_bwd_workspace_bytes(1, 2, 1, 8, 64, 1)
     assert need > 0 and attn_bwd(lib, ws_bytes=need - 1) == WORKSPACE and attn_bwd(lib, ws=None) == WORKSPACE

@@ -5,10 +5,6 @@ namespace prism {
 namespace host {
 namespace {
 
-template <class K>
-bool room(K kernel, int bytes) {
-  return hipFuncSetAttribute(reinterpret_cast<const void*>(kernel), hipFuncAttributeMaxDynamicSharedMemorySize, bytes) == hipSuccess;
-}
 unsigned row_tiles(const AttnArgs& a, int rows) {
   return (unsigned)(a.starts != nullptr ? a.T / rows + a.S : (size_t)a.B * ((a.T + rows - 1) / rows));
 }
@@ -17,23 +13,16 @@ unsigned row_tiles(const AttnArgs& a, int rows) {
 template <class T, int D, int OW, int SW, int BN, bool AHEAD>
 prism_status by_queries(const AttnArgs& a, hipStream_t s) {
   using F = attn::Pass<T, D, OW, SW, BN, AHEAD>;
-  const auto kernel = attn::dq_kernel<T, D, OW, SW, BN, AHEAD>;
-  static const bool ok = room(kernel, F::kLds);
-  if (!ok) return PRISM_ERR_HIP;
-  kernel<<<dim3(row_tiles(a, F::kOwn) * a.H), F::kThreads, F::kLds, s>>>(a);
-  return hipGetLastError() == hipSuccess ? PRISM_OK : PRISM_ERR_HIP;
+  return launch_wide<attn::dq_kernel<T, D, OW, SW, BN, AHEAD>>(row_tiles(a, F::kOwn) * a.H, F::kThreads, F::kLds, a, s);
 }
 template <class T, int D, int OW, int SW, int BN, bool AHEAD>
 prism_status by_keys(const AttnArgs& a, hipStream_t s) {
   using F = attn::Pass<T, D, OW, SW, BN, AHEAD>;
-  const auto kernel = attn::dkv_kernel<T, D, OW, SW, BN, AHEAD>;
-  static const bool ok = room(kernel, F::kLds);
-  if (!ok) return PRISM_ERR_HIP;
-  kernel<<<dim3(row_tiles(a, F::kOwn) * a.G * a.splits), F::kThreads, F::kLds, s>>>(a);
-  if (a.splits > 1) {
-    const size_t rows = 2 * (size_t)a.B * a.G * a.T, per = 256 / (D / 4);
-    attn::sum_kernel<T, D><<<dim3((unsigned)((rows + per - 1) / per)), 256, 0, s>>>(a);
-  }
+  const prism_status st =
+      launch_wide<attn::dkv_kernel<T, D, OW, SW, BN, AHEAD>>(row_tiles(a, F::kOwn) * a.G * a.splits, F::kThreads, F::kLds, a, s);
+  if (st != PRISM_OK || a.splits == 1) return st;
+  const size_t rows = 2 * (size_t)a.B * a.G * a.T, per = 256 / (D / 4);
+  attn::sum_kernel<T, D><<<dim3((unsigned)((rows + per - 1) / per)), 256, 0, s>>>(a);
   return hipGetLastError() == hipSuccess ? PRISM_OK : PRISM_ERR_HIP;
 }
 

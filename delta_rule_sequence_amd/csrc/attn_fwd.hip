@@ -5,10 +5,6 @@ namespace prism {
 namespace host {
 namespace {
 
-template <class K>
-bool room(K kernel, int bytes) {
-  return hipFuncSetAttribute(reinterpret_cast<const void*>(kernel), hipFuncAttributeMaxDynamicSharedMemorySize, bytes) == hipSuccess;
-}
 size_t row_tiles(const AttnArgs& a, size_t rows, size_t each) {
   return a.starts != nullptr ? a.T * each / rows + a.S : a.B * ((a.T * each + rows - 1) / rows);
 }
@@ -16,27 +12,21 @@ size_t row_tiles(const AttnArgs& a, size_t rows, size_t each) {
 template <class T, int D, int NW, int BN>
 prism_status many(const AttnArgs& a, hipStream_t stream) {
   using F = attn::FwdTile<T, D, NW, BN, attn::kPrompt>;
-  const auto kernel = attn::fwd_kernel<T, D, NW, BN, 1, attn::kPrompt>;
-  static const bool ok = room(kernel, F::kLds);
-  if (!ok) return PRISM_ERR_HIP;
-  kernel<<<dim3((unsigned)(row_tiles(a, F::kRows, 1) * a.H)), F::kThreads, F::kLds, stream>>>(a);
-  return hipGetLastError() == hipSuccess ? PRISM_OK : PRISM_ERR_HIP;
+  return launch_wide<attn::fwd_kernel<T, D, NW, BN, attn::kPrompt>>((unsigned)(row_tiles(a, F::kRows, 1) * a.H), F::kThreads, F::kLds, a, stream);
 }
 template <class T, int D>
 prism_status few(const AttnArgs& a, hipStream_t stream) {
   using F = attn::FewTile<T, D, attn::kPrompt>;
-  const auto kernel = attn::few_kernel<T, D, attn::kPrompt>;
-  static const bool ok = room(kernel, F::kLds);
-  if (!ok) return PRISM_ERR_HIP;
-  kernel<<<dim3((unsigned)(row_tiles(a, 32, a.H / a.G) * a.G)), 256, F::kLds, stream>>>(a);
-  return hipGetLastError() == hipSuccess ? PRISM_OK : PRISM_ERR_HIP;
+  return launch_wide<attn::few_kernel<T, D, attn::kPrompt>>((unsigned)(row_tiles(a, 32, a.H / a.G) * a.G), 256, F::kLds, a, stream);
 }
 
 // Workgroups of 128 rows, or of 256 for wide heads of bfloat16 where there are many; else tiles of 32 rows whose keys four waves
 // share.  Measured at the sides of the borders, us, few rows / many rows: bfloat16 of 64: 1 x 16 x 2048 30 / 37, 1 x 32 x 2048
 // 50 / 40, 4 x 16 x 256 7.4 / 8.8, 4 x 16 x 512 14.7 / 13.1; float32 of 64: 1 x 32 x 2048 171 / 217, 8 x 12 x 2048 486 / 466,
 // 8 x 16 x 512 64 / 65, 32 x 16 x 256 86 / 74; of 128: 1 x 16 x 2048 192 / 303, 1 x 32 x 2048 379 / 337; 128 / 256 rows,
-// bfloat16 of 128: 2 x 32 x 2048 114 / 88, 1 x 32 x 2048 62 / 67.
+// bfloat16 of 128: 2 x 32 x 2048 114 / 88, 1 x 32 x 2048 62 / 67; of 64, four waves per SIMD each: 1 x 16 x 8192 204 / 226, 1 x 16 x
+// 16384 658 / 615, 4 x 16 x 4096 178 / 172, 64 x 16 x 512 86 / 87 (128 rows with tiles of 64 keys, two waves per SIMD: 2 x 16 x 8192
+// 349, where these take 337 / 315).
 template <class T, int D>
 prism_status run(const AttnArgs& a, hipStream_t s) {
   const size_t blocks = row_tiles(a, 128, 1) * a.H;
@@ -45,6 +35,8 @@ prism_status run(const AttnArgs& a, hipStream_t s) {
   if (blocks <= few_most) return few<T, D>(a, s);
   if constexpr (D == 128 && sizeof(T) == 2)
     if (blocks >= 1024) return many<T, D, 8, 64>(a, s);
+  if constexpr (D == 64 && sizeof(T) == 2)
+    return blocks >= 2048 && a.T >= 2048 ? many<T, D, 8, 64>(a, s) : many<T, D, 4, 32>(a, s);
   return many<T, D, 4, (sizeof(T) == 4 && D > 32 ? 32 : 64)>(a, s);
 }
 

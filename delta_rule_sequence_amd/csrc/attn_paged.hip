@@ -14,29 +14,16 @@ prism_status write(const AttnArgs& a, hipStream_t s) {
   return launched();
 }
 
-template <class K>
-bool room(K kernel, int bytes) {
-  return hipFuncSetAttribute(reinterpret_cast<const void*>(kernel), hipFuncAttributeMaxDynamicSharedMemorySize, bytes) == hipSuccess;
-}
-
 template <class T, int D, attn::Keys KEYS>
 prism_status few(const AttnArgs& a, hipStream_t s) {
   using F = attn::FewTile<T, D, KEYS>;
-  const auto kernel = attn::few_kernel<T, D, KEYS>;
-  static const bool ok = room(kernel, F::kLds);
-  if (!ok) return PRISM_ERR_HIP;
-  kernel<<<dim3((unsigned)(a.B * a.G * ((a.T * (a.H / a.G) + 31) / 32) * a.splits)), 256, F::kLds, s>>>(a);
-  return launched();
+  return launch_wide<attn::few_kernel<T, D, KEYS>>((unsigned)(a.B * a.G * ((a.T * (a.H / a.G) + 31) / 32) * a.splits), 256, F::kLds, a, s);
 }
 template <class T, int D, attn::Keys KEYS, int NW>
 prism_status many(const AttnArgs& a, hipStream_t s) {
   constexpr int BN = sizeof(T) == 2 || D == 32 ? 64 : 32;
   using F = attn::FwdTile<T, D, NW, BN, KEYS>;
-  const auto kernel = attn::fwd_kernel<T, D, NW, BN, 1, KEYS>;
-  static const bool ok = room(kernel, F::kLds);
-  if (!ok) return PRISM_ERR_HIP;
-  kernel<<<dim3((unsigned)(row_tiles(a, F::kRows) * a.H * a.splits)), F::kThreads, F::kLds, s>>>(a);
-  return launched();
+  return launch_wide<attn::fwd_kernel<T, D, NW, BN, KEYS>>((unsigned)(row_tiles(a, F::kRows) * a.H * a.splits), F::kThreads, F::kLds, a, s);
 }
 template <class T, int D, attn::Keys KEYS>
 prism_status paged(int rows, const AttnArgs& a, hipStream_t s) {

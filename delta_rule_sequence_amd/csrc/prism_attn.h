@@ -92,9 +92,9 @@ template <int PARTS> struct Operand<float, PARTS> {
   __device__ __forceinline__ void scale(float f) { x *= f; }
 };
 
-// acc[j][] += (32 rows of D values at `rows`, transposed) * x[j];  at: this lane's place, Rows::transposed.
-template <int D, int PARTS, int N>
-__device__ __forceinline__ void mul_transposed(f32x16 (&acc)[N][D / 32], const char* rows, const Operand<bf16_t, PARTS> (&x)[N]) {
+// acc += (32 rows of D values at `rows` + this lane's place, Rows::transposed) * x
+template <int D, int PARTS>
+__device__ __forceinline__ void mul_transposed(f32x16 (&acc)[D / 32], const char* rows, const Operand<bf16_t, PARTS>& x) {
   constexpr int S = Rows<bf16_t, D>::kStride;
 #pragma unroll
   for (int kb = 0; kb < 2; ++kb)
@@ -104,21 +104,18 @@ __device__ __forceinline__ void mul_transposed(f32x16 (&acc)[N][D / 32], const c
       const s16x4 lo = lds_column4(p), up = lds_column4(p + 8 * S);
       const bf16x8 a = __builtin_bit_cast(bf16x8, __builtin_shufflevector(lo, up, 0, 1, 2, 3, 4, 5, 6, 7));
 #pragma unroll
-      for (int j = 0; j < N; ++j)
-#pragma unroll
-        for (int q = 0; q < PARTS; ++q) acc[j][d] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(a, x[j].part[q][kb], acc[j][d], 0, 0, 0);
+      for (int q = 0; q < PARTS; ++q) acc[d] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(a, x.part[q][kb], acc[d], 0, 0, 0);
     }
 }
-template <int D, int PARTS, int N>
-__device__ __forceinline__ void mul_transposed(f32x16 (&acc)[N][D / 32], const char* rows, const Operand<float, PARTS> (&x)[N]) {
+template <int D, int PARTS>
+__device__ __forceinline__ void mul_transposed(f32x16 (&acc)[D / 32], const char* rows, const Operand<float, PARTS>& x) {
   constexpr int S = Rows<float, D>::kStride;
 #pragma unroll
   for (int i = 0; i < 16; ++i)
 #pragma unroll
     for (int d = 0; d < D / 32; ++d) {
       const float a = *reinterpret_cast<const float*>(rows + (8 * (i >> 2) + (i & 3)) * S + d * 128);
-#pragma unroll
-      for (int j = 0; j < N; ++j) acc[j][d] = __builtin_amdgcn_mfma_f32_32x32x2f32(a, x[j].x[i], acc[j][d], 0, 0, 0);
+      acc[d] = __builtin_amdgcn_mfma_f32_32x32x2f32(a, x.x[i], acc[d], 0, 0, 0);
     }
 }
 
@@ -472,8 +469,8 @@ __device__ __forceinline__ float* share_stats(const AttnArgs& a, int D, size_t r
   return a.part + (size_t)a.splits * a.B * a.H * a.T * D + 2 * row;
 }
 
-template <class T, int D, int NW, int BN, int PARTS, Keys KEYS>
-__global__ __launch_bounds__(64 * NW, D * (int)sizeof(T) > 256 ? 1 : 2) void fwd_kernel(AttnArgs a) {
+template <class T, int D, int NW, int BN, Keys KEYS>
+__global__ __launch_bounds__(64 * NW, D * (int)sizeof(T) > 256 ? 1 : D * (int)sizeof(T) <= 128 && KEYS == kPrompt ? 4 : 2) void fwd_kernel(AttnArgs a) {
   using F = FwdTile<T, D, NW, BN, KEYS>;
   using R = Rows<T, D>;
   extern __shared__ __align__(16) char lds[];
@@ -543,10 +540,10 @@ __global__ __launch_bounds__(64 * NW, D * (int)sizeof(T) > 256 ? 1 : 2) void fwd
   char* const v_tiles = lds + 3 * F::kTile;
   float* const scales = reinterpret_cast<float*>(lds + 6 * F::kTile + F::kZero);  // three of K, three of V
 
-  f32x16 o[1][D / 32];
+  f32x16 o[D / 32];
   float m = -kInf, sum = 0.f;
 #pragma unroll
-  for (int d = 0; d < D / 32; ++d) o[0][d] = zero16();
+  for (int d = 0; d < D / 32; ++d) o[d] = zero16();
   const float c = a.scale * kLog2e;
   const int rrow = R::by_rows(l), rcol = R::transposed(l), pw = past + qw;
   const int i = pw + (l & 31);                                        // this lane's position
@@ -561,8 +558,8 @@ __global__ __launch_bounds__(64 * NW, D * (int)sizeof(T) > 256 ? 1 : 2) void fwd
   // 32 keys after another: while the exponentials of some are formed, the matrix cores form the scores of the next and the
   // products of the ones before with their values.
   f32x16 x[2];                                                        // scores of these keys, and of the next
-  Operand<T, PARTS> p[1];                                             // p of the keys before
-  p[0].set(zero16());
+  Operand<T, 1> p;                                             // p of the keys before
+  p.set(zero16());
   // and their values: before the first ones and where p is empty, zeros (0 times an infinity would be NaN)
   char* const zeros = lds + 6 * F::kTile;
   for (int z = tid * 16; z < F::kZero; z += F::kThreads * 16) *reinterpret_cast<u32x4*>(zeros + z) = u32x4{0, 0, 0, 0};
@@ -589,8 +586,8 @@ __global__ __launch_bounds__(64 * NW, D * (int)sizeof(T) > 256 ? 1 : 2) void fwd
     if (t + 3 < t1) load_k(t + 3);
   };
   const int tw = min(t1, max(t0, wlast / BN + 1));                    // the wave's own tiles
-  int t = t0;
-  for (; t < tw; ++t) {
+  const auto tile = [&](int t, auto odd) {                            // odd: x[1] has the scores of the tile's first keys
+    constexpr int X = decltype(odd)::value;
     if (t > t0) __syncthreads();
     const int buf1 = buf == 2 ? 0 : buf + 1, buf2 = buf1 == 2 ? 0 : buf1 + 1;
     stage(t, buf1, buf2);
@@ -600,7 +597,7 @@ __global__ __launch_bounds__(64 * NW, D * (int)sizeof(T) > 256 ? 1 : 2) void fwd
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
       const int j0 = t * BN + 32 * n;
-      f32x16& y = x[n & 1];
+      f32x16& y = x[(n + X) & 1];
       if constexpr (KEYS == kCache8) {
 #pragma unroll
         for (int r = 0; r < 4; ++r) {
@@ -627,14 +624,14 @@ __global__ __launch_bounds__(64 * NW, D * (int)sizeof(T) > 256 ? 1 : 2) void fwd
         const float f = to == m ? 1.f : __builtin_amdgcn_exp2f((m - to) * c);
         m = to;
         sum *= f;
-        p[0].scale(f);                                                // rounded once more, at 2^-8 of what comes now
+        p.scale(f);                                                // rounded once more, at 2^-8 of what comes now
 #pragma unroll
-        for (int d = 0; d < D / 32; ++d) o[0][d] *= f;
+        for (int d = 0; d < D / 32; ++d) o[d] *= f;
       }
       const float shift = m == -kInf ? 0.f : m * c;
       // behind the last keys: scores of whatever lies there, unused
-      scores(x[(n + 1) & 1], n + 1 < NT ? kt + (n + 1) * 32 * R::kStride : kn);
-      mul_transposed<D, PARTS, 1>(o, pv, p);
+      scores(x[(n + X + 1) & 1], n + 1 < NT ? kt + (n + 1) * 32 * R::kStride : kn);
+      mul_transposed<D, 1>(o, pv, p);
       pv = vt + rcol + n * 32 * R::kStride;
       float part = 0.f;
 #pragma unroll
@@ -651,21 +648,18 @@ __global__ __launch_bounds__(64 * NW, D * (int)sizeof(T) > 256 ? 1 : 2) void fwd
           for (int u = 0; u < 4; ++u) y[4 * r + u] *= f[u];
         }
       }
-      p[0].set(y);
-#ifdef SGB
-      if constexpr (sizeof(T) == 2) {
-#pragma unroll
-        for (int k = 0; k < R::kSteps + PARTS * D / 16; ++k) {
-          __builtin_amdgcn_sched_group_barrier(0x100, 2, 0);
-          __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
-          __builtin_amdgcn_sched_group_barrier(0x002, SGB, 0);
-        }
-      }
-#endif
+      p.set(y);
     }
-    if constexpr (NT % 2 == 1) x[0] = x[1];
+  };
+  int t = t0;
+  if constexpr (NT % 2 == 1) {
+    for (; t + 1 < tw; t += 2) {
+      tile(t, std::integral_constant<int, 0>());
+      tile(t + 1, std::integral_constant<int, 1>());
+    }
   }
-  mul_transposed<D, PARTS, 1>(o, pv, p);
+  for (; t < tw; ++t) tile(t, std::integral_constant<int, 0>());
+  mul_transposed<D, 1>(o, pv, p);
   for (; t < t1; ++t) {                                               // those of the block's other waves
     if (t > t0) __syncthreads();
     const int buf1 = buf == 2 ? 0 : buf + 1, buf2 = buf1 == 2 ? 0 : buf1 + 1;
@@ -673,8 +667,8 @@ __global__ __launch_bounds__(64 * NW, D * (int)sizeof(T) > 256 ? 1 : 2) void fwd
     buf = buf1;
   }
   const int iq = qw + (l & 31);
-  if (__any(iq < s.n && (!finite(o[0]) || !(fabsf(m * c) <= kFar || m == -kInf)))) {
-    careful_rows<T, D, KEYS>(a, qf, kp, vp, kst, vst, table, group, t0 * NT, t1 * NT, 1, keys, first, iq < s.n ? last : -1, m, sum, o[0]);
+  if (__any(iq < s.n && (!finite(o) || !(fabsf(m * c) <= kFar || m == -kInf)))) {
+    careful_rows<T, D, KEYS>(a, qf, kp, vp, kst, vst, table, group, t0 * NT, t1 * NT, 1, keys, first, iq < s.n ? last : -1, m, sum, o);
   }
 
   const float total = both_sum(sum);
@@ -682,11 +676,11 @@ __global__ __launch_bounds__(64 * NW, D * (int)sizeof(T) > 256 ? 1 : 2) void fwd
   if (a.splits > 1) {
     const size_t row = share(a, split, s, head, iq);
     if (h == 0) share_stats(a, D, row)[0] = m, share_stats(a, D, row)[1] = total;
-    store_columns<float, D>(reinterpret_cast<char*>(a.part + row * D), o[0], 1.f, h);
+    store_columns<float, D>(reinterpret_cast<char*>(a.part + row * D), o, 1.f, h);
     return;
   }
   // a row without keys: zeros, and a logarithm of -infinity
-  store_columns<T, D>((char*)a.o + (s.b * a.os.b + head * a.os.h + (long long)(s.first + iq) * a.os.t) * e, o[0],
+  store_columns<T, D>((char*)a.o + (s.b * a.os.b + head * a.os.h + (long long)(s.first + iq) * a.os.t) * e, o,
                       total == 0.f ? 0.f : 1.f / total, h);
   if (a.lse != nullptr && h == 0) a.lse[((long long)s.b * a.H + head) * a.T + s.first + iq] = row_lse(m, total, a.scale);
 }
@@ -769,9 +763,9 @@ __global__ __launch_bounds__(256, D * (int)sizeof(T) > 256 ? 1 : 2) void few_ker
   };
   if (t0 + w < t1) load(t0 + w);
 
-  f32x16 o[1][D / 32];
+  f32x16 o[D / 32];
 #pragma unroll
-  for (int d = 0; d < D / 32; ++d) o[0][d] = zero16();
+  for (int d = 0; d < D / 32; ++d) o[d] = zero16();
   float m = -kInf, sum = 0.f;
   const float c = a.scale * kLog2e;
   const int rrow = R::by_rows(l), rcol = R::transposed(l);
@@ -806,7 +800,7 @@ __global__ __launch_bounds__(256, D * (int)sizeof(T) > 256 ? 1 : 2) void few_ker
       m = to;
       sum *= f;
 #pragma unroll
-      for (int d = 0; d < D / 32; ++d) o[0][d] *= f;
+      for (int d = 0; d < D / 32; ++d) o[d] *= f;
     }
     const float shift = m == -kInf ? 0.f : m * c;
 #pragma unroll
@@ -821,20 +815,20 @@ __global__ __launch_bounds__(256, D * (int)sizeof(T) > 256 ? 1 : 2) void few_ker
         if constexpr (KEYS == kCache8) x[k] *= f[u];
       }
     }
-    Operand<T, PARTS> p[1];
-    p[0].set(x);
-    mul_transposed<D, PARTS, 1>(o, vt + rcol, p);
+    Operand<T, PARTS> p;
+    p.set(x);
+    mul_transposed<D, PARTS>(o, vt + rcol, p);
     __builtin_amdgcn_wave_barrier();
   }
 
-  if (__any(tq < s.n && (!finite(o[0]) || !(fabsf(m * c) <= kFar || m == -kInf)))) {
+  if (__any(tq < s.n && (!finite(o) || !(fabsf(m * c) <= kFar || m == -kInf)))) {
     careful_rows<T, D, KEYS>(a, qf, kp, vp, kst, vst, table, group, t0 + w, t1, 4, keys, a.window > 0 ? i - a.window + 1 : 0,
-                          tq >= s.n ? -1 : a.causal ? min(i, keys - 1) : keys - 1, m, sum, o[0]);
+                          tq >= s.n ? -1 : a.causal ? min(i, keys - 1) : keys - 1, m, sum, o);
   }
 
   // the waves' shares through LDS
   const float total = both_sum(sum);
-  store_columns<float, D>(kt + (l & 31) * F::kOut, o[0], 1.f, h);
+  store_columns<float, D>(kt + (l & 31) * F::kOut, o, 1.f, h);
   float* const stats = reinterpret_cast<float*>(kt + 32 * F::kOut);
   if (h == 0) stats[2 * (l & 31)] = m, stats[2 * (l & 31) + 1] = total;
   __syncthreads();

@@ -3,6 +3,8 @@
 #pragma once
 #include <hip/hip_runtime.h>
 
+#include <atomic>
+
 #include "prism.h"
 
 namespace prism {
@@ -48,10 +50,26 @@ struct RopeArgs {
 };
 
 namespace host {
+// A launch with `lds` bytes of dynamic LDS, which may be more than a kernel has by default: each device is told once.
+template <auto KERNEL>
+prism_status launch_wide(unsigned blocks, unsigned threads, int lds, const AttnArgs& a, hipStream_t stream) {
+  static std::atomic<unsigned long long> told{0};                     // the devices, by bits
+  int dev = 0;
+  if (hipGetDevice(&dev) != hipSuccess) return PRISM_ERR_HIP;
+  const unsigned long long bit = dev < 64 ? 1ull << dev : 0;
+  if ((told.load(std::memory_order_relaxed) & bit) == 0) {
+    if (hipFuncSetAttribute(reinterpret_cast<const void*>(KERNEL), hipFuncAttributeMaxDynamicSharedMemorySize, lds) != hipSuccess)
+      return PRISM_ERR_HIP;
+    told.fetch_or(bit, std::memory_order_relaxed);
+  }
+  KERNEL<<<dim3(blocks), dim3(threads), lds, stream>>>(a);
+  return hipGetLastError() == hipSuccess ? PRISM_OK : PRISM_ERR_HIP;
+}
+
+// Each enqueues on `stream` and reports launch failures.
 prism_status launch_cache_write(prism_dtype dt, int D, bool bits8, const AttnArgs& a, hipStream_t stream);
 prism_status launch_attn_paged(prism_dtype dt, int D, bool bits8, int rows, const AttnArgs& a, hipStream_t stream);
 prism_status launch_rope(prism_dtype dt, bool bwd, const RopeArgs& a, hipStream_t stream);
-// Each enqueues on `stream` and reports launch failures.
 prism_status launch_attn_fwd(prism_dtype dt, int D, const AttnArgs& a, hipStream_t stream);
 prism_status launch_attn_bwd(prism_dtype dt, int D, const AttnArgs& a, hipStream_t stream);
 }  // namespace host

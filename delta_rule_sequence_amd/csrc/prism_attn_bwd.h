@@ -150,9 +150,9 @@ __global__ __launch_bounds__(64 * OW * SW, SW > 1 || D * (int)sizeof(T) > 256 ? 
     sv.store(v_tiles + place * F::kTile, tid);
   };
 
-  f32x16 dq[1][D / 32];
+  f32x16 dq[D / 32];
 #pragma unroll
-  for (int d = 0; d < D / 32; ++d) dq[0][d] = zero16();
+  for (int d = 0; d < D / 32; ++d) dq[d] = zero16();
   const int rrow = R::by_rows(l), rcol = R::transposed(l);
   const int last = a.causal ? min(i, s.n - 1) : s.n - 1, first = a.window > 0 ? i - a.window + 1 : 0;
   const int wlast = a.causal ? min(qw + 31, s.n - 1) : s.n - 1;
@@ -211,14 +211,14 @@ __global__ __launch_bounds__(64 * OW * SW, SW > 1 || D * (int)sizeof(T) > 256 ? 
         products(xs[(m + 1) & 1], gs[(m + 1) & 1], m + 1 < M ? here + SW * 32 * R::kStride : after + sw * 32 * R::kStride);
 #pragma unroll
       for (int r = 0; r < 16; ++r) x[r] = __builtin_amdgcn_exp2f(fmaf(x[r], c, -lse)) * (g[r] - delta);
-      Operand<T, 1> ds[1];
-      ds[0].set(x);
-      mul_transposed<D, 1, 1>(dq, lds + here + rcol, ds);
+      Operand<T, 1> ds;
+      ds.set(x);
+      mul_transposed<D, 1>(dq, lds + here + rcol, ds);
     }
   }
-  if constexpr (SW > 1) join_waves<D, OW, SW>(dq[0], lds, ow, sw);
+  if constexpr (SW > 1) join_waves<D, OW, SW>(dq, lds, ow, sw);
   if (i < s.n && sw == 0)
-    store_columns<T, D>((char*)a.dq + (s.b * a.dqs.b + head * a.dqs.h + (long long)(s.first + i) * a.dqs.t) * e, dq[0], a.scale, h);
+    store_columns<T, D>((char*)a.dq + (s.b * a.dqs.b + head * a.dqs.h + (long long)(s.first + i) * a.dqs.t) * e, dq, a.scale, h);
 }
 
 // dk and dv: KW waves of 32 keys, QW that take a tile's queries by turns; the heads of the group one after the other.
@@ -275,9 +275,9 @@ __global__ __launch_bounds__(64 * KW * QW, D * (int)sizeof(T) > 128 ? 1 : 2) voi
     if (tid < BN) rt[2 * BN + tid] = row;
   };
 
-  f32x16 dk[1][D / 32], dv[1][D / 32];
+  f32x16 dk[D / 32], dv[D / 32];
 #pragma unroll
-  for (int d = 0; d < D / 32; ++d) dk[0][d] = zero16(), dv[0][d] = zero16();
+  for (int d = 0; d < D / 32; ++d) dk[d] = zero16(), dv[d] = zero16();
   const float scale = a.scale * kLog2e;
   const int rrow = R::by_rows(l), rcol = R::transposed(l);
   f32x16 xs[F::kAhead ? 2 : 1], gs[F::kAhead ? 2 : 1];                // s and dp of these 32 queries, and of the next
@@ -290,6 +290,7 @@ __global__ __launch_bounds__(64 * KW * QW, D * (int)sizeof(T) > 128 ? 1 : 2) voi
   };
 
   constexpr int M = NT / QW;                                          // a tile's parts of a wave
+  static_assert(!F::kAhead || M % 2 == 0, "two halves by turns");
   int place = 0;                                                      // this step's tile in LDS
   if (steps > 0) load();
   if constexpr (F::kAhead) {
@@ -357,27 +358,26 @@ __global__ __launch_bounds__(64 * KW * QW, D * (int)sizeof(T) > 128 ? 1 : 2) voi
           g[r] = x[r] * (g[r] - delta[u]);
         }
       }
-      Operand<T, 1> p[1];
-      p[0].set(x);
-      mul_transposed<D, 1, 1>(dv, g_tiles + at + rcol, p);
-      p[0].set(g);
-      mul_transposed<D, 1, 1>(dk, lds + at + rcol, p);
+      Operand<T, 1> p;
+      p.set(x);
+      mul_transposed<D, 1>(dv, g_tiles + at + rcol, p);
+      p.set(g);
+      mul_transposed<D, 1>(dk, lds + at + rcol, p);
     }
-    if constexpr (F::kAhead && M % 2 == 1) xs[0] = xs[1], gs[0] = gs[1];
   }
   if constexpr (QW > 1) {
-    join_waves<D, KW, QW>(dk[0], lds, kw, qw);
-    join_waves<D, KW, QW>(dv[0], lds, kw, qw);
+    join_waves<D, KW, QW>(dk, lds, kw, qw);
+    join_waves<D, KW, QW>(dv, lds, kw, qw);
   }
   if (j >= s.n || qw > 0) return;
   if (a.splits > 1) {                                                 // [splits][dk, dv][B G T][D], added up by sum_kernel
     const size_t all = (size_t)a.B * a.G * a.T, at = ((size_t)s.b * a.G + group) * a.T + s.first + j;
-    store_columns<float, D>((char*)(a.part + ((2 * split) * all + at) * D), dk[0], a.scale, h);
-    store_columns<float, D>((char*)(a.part + ((2 * split + 1) * all + at) * D), dv[0], 1.f, h);
+    store_columns<float, D>((char*)(a.part + ((2 * split) * all + at) * D), dk, a.scale, h);
+    store_columns<float, D>((char*)(a.part + ((2 * split + 1) * all + at) * D), dv, 1.f, h);
     return;
   }
-  store_columns<T, D>((char*)a.dk + (s.b * a.dks.b + group * a.dks.h + (long long)(s.first + j) * a.dks.t) * e, dk[0], a.scale, h);
-  store_columns<T, D>((char*)a.dv + (s.b * a.dvs.b + group * a.dvs.h + (long long)(s.first + j) * a.dvs.t) * e, dv[0], 1.f, h);
+  store_columns<T, D>((char*)a.dk + (s.b * a.dks.b + group * a.dks.h + (long long)(s.first + j) * a.dks.t) * e, dk, a.scale, h);
+  store_columns<T, D>((char*)a.dv + (s.b * a.dvs.b + group * a.dvs.h + (long long)(s.first + j) * a.dvs.t) * e, dv, 1.f, h);
 }
 
 // dk and dv from the shares of the heads: D / 4 lanes per row of one of them, tokens of the sequences only.

@@ -33,11 +33,10 @@ prism_status run(const AttnArgs& a, hipStream_t s) {
   const bool f32 = sizeof(T) == 4;
   const size_t few_most = f32 && D < 128 ? (a.T >= 1024 ? 1024 : 512) : a.T >= (f32 ? 512 : 1024) ? 320 : 192;
   if (blocks <= few_most) return few<T, D>(a, s);
-  if constexpr (D == 128 && sizeof(T) == 2)
-    if (blocks >= 1024) return many<T, D, 8, 64>(a, s);
-  if constexpr (D == 64 && sizeof(T) == 2)
-    return blocks >= 2048 && a.T >= 2048 ? many<T, D, 8, 64>(a, s) : many<T, D, 4, 32>(a, s);
-  return many<T, D, 4, (sizeof(T) == 4 && D > 32 ? 32 : 64)>(a, s);
+  if constexpr (sizeof(T) == 4) return many<T, D, 4, (D > 32 ? 32 : 64)>(a, s);
+  else if constexpr (D == 128) return blocks >= 1024 ? many<T, D, 8, 64>(a, s) : many<T, D, 4, 64>(a, s);
+  else if constexpr (D == 64) return blocks >= 2048 && a.T >= 2048 ? many<T, D, 8, 64>(a, s) : many<T, D, 4, 32>(a, s);
+  else return many<T, D, 4, 64>(a, s);
 }
 
 }  // namespace

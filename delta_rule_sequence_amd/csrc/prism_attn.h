@@ -23,6 +23,11 @@ typedef unsigned u32x4 __attribute__((ext_vector_type(4)));
 constexpr float kLog2e = 1.44269504088896341f, kLn2 = 0.693147180559945309f;
 constexpr float kInf = __builtin_inff();
 
+// x, formed again at each place rather than held in a register from one to the next.
+__device__ __forceinline__ int anew(int x) {
+  asm volatile("" : "+v"(x));
+  return x;
+}
 __device__ __forceinline__ int uniform(int x) { return __builtin_amdgcn_readfirstlane(x); }
 
 // ---- 32 x 32 tiles ---------------------------------------------------------------------------------
@@ -546,8 +551,11 @@ __global__ __launch_bounds__(64 * NW, D * (int)sizeof(T) > 256 ? 1 : D * (int)si
   for (int d = 0; d < D / 32; ++d) o[d] = zero16();
   const float c = a.scale * kLog2e;
   const int rrow = R::by_rows(l), rcol = R::transposed(l), pw = past + qw;
-  const int i = pw + (l & 31);                                        // this lane's position
-  const int last = a.causal ? min(i, keys - 1) : keys - 1, first = a.window > 0 ? i - a.window + 1 : 0;
+  // the keys first .. last that this lane's position sees, formed where they are needed: registers are short
+  const auto seen = [&](int& first, int& last) {
+    const int i = pw + (anew(l) & 31);
+    last = a.causal ? min(i, keys - 1) : keys - 1, first = a.window > 0 ? i - a.window + 1 : 0;
+  };
   const int wlast = a.causal ? min(pw + 31, keys - 1) : keys - 1;     // of all of the wave's positions
   const auto scores = [&](f32x16& x, const char* tile) {
     x = zero16();
@@ -608,6 +616,8 @@ __global__ __launch_bounds__(64 * NW, D * (int)sizeof(T) > 256 ? 1 : D * (int)si
       }
       // keys that not all of the wave's queries see
       if (j0 + 31 > (a.causal ? min(pw, keys - 1) : keys - 1) || (a.window > 0 && j0 <= pw + 31 - a.window)) {
+        int first, last;
+        seen(first, last);
 #pragma unroll
         for (int r = 0; r < 16; ++r) {
           const int j = 8 * (r >> 2) + (r & 3) + j0 + 4 * h;
@@ -667,6 +677,8 @@ __global__ __launch_bounds__(64 * NW, D * (int)sizeof(T) > 256 ? 1 : D * (int)si
     buf = buf1;
   }
   const int iq = qw + (l & 31);
+  int first, last;
+  seen(first, last);
   if (__any(iq < s.n && (!finite(o) || !(fabsf(m * c) <= kFar || m == -kInf)))) {
     careful_rows<T, D, KEYS>(a, qf, kp, vp, kst, vst, table, group, t0 * NT, t1 * NT, 1, keys, first, iq < s.n ? last : -1, m, sum, o);
   }

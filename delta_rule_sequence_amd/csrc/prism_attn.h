@@ -49,9 +49,12 @@ __device__ __forceinline__ f32x16 zero16() {
   return z;
 }
 
-// Rows of D values in LDS.  32 bytes between rows spread both kinds of reads over the banks.
-template <class T, int D> struct Rows {
-  static constexpr int kBytes = D * (int)sizeof(T), kStride = kBytes + 32;
+// Rows of D values in LDS, PAD bytes between them.  A read by rows wants 16 rows' 16-byte pieces in different ones of
+// the 64 banks, a transposed one four rows' 64 bytes (float32: two rows' 128, four rows apart); kBoth is two-way for either.
+constexpr int kBoth = 32, kByRows = 16;
+template <class T, int D> constexpr int kTransposed = sizeof(T) == 4 ? 32 : D == 32 ? 0 : 64;
+template <class T, int D, int PAD = kBoth> struct Rows {
+  static constexpr int kBytes = D * (int)sizeof(T), kStride = kBytes + PAD;
   static constexpr int kPieces = kBytes / 16, kSteps = kPieces / 2;
   static constexpr int kPer = 16 / (int)sizeof(T);   // values of a piece
   // This lane's place in a tile of 32 rows, read by rows or transposed.
@@ -98,9 +101,9 @@ template <int PARTS> struct Operand<float, PARTS> {
 };
 
 // acc += (32 rows of D values at `rows` + this lane's place, Rows::transposed) * x
-template <int D, int PARTS>
+template <int D, int PARTS, int PAD = kBoth>
 __device__ __forceinline__ void mul_transposed(f32x16 (&acc)[D / 32], const char* rows, const Operand<bf16_t, PARTS>& x) {
-  constexpr int S = Rows<bf16_t, D>::kStride;
+  constexpr int S = Rows<bf16_t, D, PAD>::kStride;
 #pragma unroll
   for (int kb = 0; kb < 2; ++kb)
 #pragma unroll
@@ -112,9 +115,9 @@ __device__ __forceinline__ void mul_transposed(f32x16 (&acc)[D / 32], const char
       for (int q = 0; q < PARTS; ++q) acc[d] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(a, x.part[q][kb], acc[d], 0, 0, 0);
     }
 }
-template <int D, int PARTS>
+template <int D, int PARTS, int PAD = kBoth>
 __device__ __forceinline__ void mul_transposed(f32x16 (&acc)[D / 32], const char* rows, const Operand<float, PARTS>& x) {
-  constexpr int S = Rows<float, D>::kStride;
+  constexpr int S = Rows<float, D, PAD>::kStride;
 #pragma unroll
   for (int i = 0; i < 16; ++i)
 #pragma unroll
@@ -230,12 +233,14 @@ enum Keys { kPrompt, kCache, kCache8 };
 // tile t + 2 of K and t + 1 of V, and asks for the ones behind them.
 template <class T, int D, int NW, int BN, Keys KEYS>
 struct FwdTile {
-  using R = Rows<T, D>;
+  using K = Rows<T, D, kByRows>;
+  using V = Rows<T, D, kTransposed<T, D>>;
   static constexpr int kThreads = 64 * NW, kRows = 32 * NW;
-  static constexpr int kTile = BN * R::kStride;
+  static constexpr int kKeys = BN * K::kStride, kValues = BN * V::kStride;
   static constexpr int kScales = KEYS == kCache8 ? 6 * BN * 4 : 0;
-  static constexpr int kZero = 32 * R::kStride;                        // rows of zeros
-  static constexpr int kLds = 6 * kTile + kZero + kScales;
+  static constexpr int kZero = 32 * V::kStride;                        // rows of zeros
+  static constexpr int kValuesAt = 3 * kKeys, kZeroAt = kValuesAt + 3 * kValues, kScalesAt = kZeroAt + kZero;
+  static constexpr int kLds = kScalesAt + kScales;
 };
 
 // Eight e4m3 values as bfloat16, exactly.
@@ -321,12 +326,12 @@ template <class T, int D, int NT, int BN, Keys KEYS> struct KeyTile {
       if (tid < BN && j < n && (unsigned)p < (unsigned)a.pages) scale = scales[((size_t)p * a.G + group) * page + (j & (page - 1))];
     }
   }
-  __device__ __forceinline__ void store(char* tile, float* scales, int tid) const {
+  template <int STRIDE> __device__ __forceinline__ void store(char* tile, float* scales, int tid) const {
     const int row = tid / kPieces, at = tid % kPieces;
     if (!kPart || row < BN) {
 #pragma unroll
       for (int i = 0; i < kEach; ++i) {
-        char* const p = tile + (row + i * kStep) * R::kStride;
+        char* const p = tile + (row + i * kStep) * STRIDE;
         if constexpr (KEYS == kCache8) {
           *reinterpret_cast<u32x4*>(p + at * 32) = widen8(x[i][0], x[i][1]);
           *reinterpret_cast<u32x4*>(p + at * 32 + 16) = widen8(x[i][2], x[i][3]);
@@ -542,15 +547,15 @@ __global__ __launch_bounds__(64 * NW, D * (int)sizeof(T) > 256 ? 1 : D * (int)si
     if constexpr (KEYS == kPrompt) nv.load_prompt(vp + (long long)t * BN * vst, vst, keys - t * BN, tid);
     else nv.load_cache(a, a.cache_v, a.cache_vs, of_v, group, t * BN, keys, tid);
   };
-  char* const v_tiles = lds + 3 * F::kTile;
-  float* const scales = reinterpret_cast<float*>(lds + 6 * F::kTile + F::kZero);  // three of K, three of V
+  char* const v_tiles = lds + F::kValuesAt;
+  float* const scales = reinterpret_cast<float*>(lds + F::kScalesAt);  // three of K, three of V
 
   f32x16 o[D / 32];
   float m = -kInf, sum = 0.f;
 #pragma unroll
   for (int d = 0; d < D / 32; ++d) o[d] = zero16();
   const float c = a.scale * kLog2e;
-  const int rrow = R::by_rows(l), rcol = R::transposed(l), pw = past + qw;
+  const int rrow = F::K::by_rows(l), rcol = F::V::transposed(l), pw = past + qw;
   // the keys first .. last that this lane's position sees, formed where they are needed: registers are short
   const auto seen = [&](int& first, int& last) {
     const int i = pw + (anew(l) & 31);
@@ -569,18 +574,18 @@ __global__ __launch_bounds__(64 * NW, D * (int)sizeof(T) > 256 ? 1 : D * (int)si
   Operand<T, 1> p;                                             // p of the keys before
   p.set(zero16());
   // and their values: before the first ones and where p is empty, zeros (0 times an infinity would be NaN)
-  char* const zeros = lds + 6 * F::kTile;
+  char* const zeros = lds + F::kZeroAt;
   for (int z = tid * 16; z < F::kZero; z += F::kThreads * 16) *reinterpret_cast<u32x4*>(zeros + z) = u32x4{0, 0, 0, 0};
   const char* pv = zeros + rcol;
   int buf = 0;                                                        // tile t's place in LDS
   if (t0 < t1) {
     load_k(t0);
     load_v(t0);
-    nk.store(lds, scales, tid);
-    nv.store(v_tiles, scales + 3 * BN, tid);
+    nk.template store<F::K::kStride>(lds, scales, tid);
+    nv.template store<F::V::kStride>(v_tiles, scales + 3 * BN, tid);
     if (t0 + 1 < t1) {
       load_k(t0 + 1);
-      nk.store(lds + F::kTile, scales + BN, tid);
+      nk.template store<F::K::kStride>(lds + F::kKeys, scales + BN, tid);
       load_v(t0 + 1);
     }
     if (t0 + 2 < t1) load_k(t0 + 2);
@@ -588,8 +593,8 @@ __global__ __launch_bounds__(64 * NW, D * (int)sizeof(T) > 256 ? 1 : D * (int)si
   __syncthreads();
   if (t0 < t1) scores(x[0], lds);
   const auto stage = [&](int t, int buf1, int buf2) {
-    if (t + 2 < t1) nk.store(lds + buf2 * F::kTile, scales + buf2 * BN, tid);
-    if (t + 1 < t1) nv.store(v_tiles + buf1 * F::kTile, scales + (3 + buf1) * BN, tid);
+    if (t + 2 < t1) nk.template store<F::K::kStride>(lds + buf2 * F::kKeys, scales + buf2 * BN, tid);
+    if (t + 1 < t1) nv.template store<F::V::kStride>(v_tiles + buf1 * F::kValues, scales + (3 + buf1) * BN, tid);
     if (t + 2 < t1) load_v(t + 2);
     if (t + 3 < t1) load_k(t + 3);
   };
@@ -599,7 +604,7 @@ __global__ __launch_bounds__(64 * NW, D * (int)sizeof(T) > 256 ? 1 : D * (int)si
     if (t > t0) __syncthreads();
     const int buf1 = buf == 2 ? 0 : buf + 1, buf2 = buf1 == 2 ? 0 : buf1 + 1;
     stage(t, buf1, buf2);
-    const char *kt = lds + buf * F::kTile, *kn = lds + buf1 * F::kTile, *vt = v_tiles + buf * F::kTile;
+    const char *kt = lds + buf * F::kKeys, *kn = lds + buf1 * F::kKeys, *vt = v_tiles + buf * F::kValues;
     const float *ks = scales + buf * BN, *vs = scales + (3 + buf) * BN;
     buf = buf1;
 #pragma unroll
@@ -640,9 +645,9 @@ __global__ __launch_bounds__(64 * NW, D * (int)sizeof(T) > 256 ? 1 : D * (int)si
       }
       const float shift = m == -kInf ? 0.f : m * c;
       // behind the last keys: scores of whatever lies there, unused
-      scores(x[(n + X + 1) & 1], n + 1 < NT ? kt + (n + 1) * 32 * R::kStride : kn);
-      mul_transposed<D, 1>(o, pv, p);
-      pv = vt + rcol + n * 32 * R::kStride;
+      scores(x[(n + X + 1) & 1], n + 1 < NT ? kt + (n + 1) * 32 * F::K::kStride : kn);
+      mul_transposed<D, 1, kTransposed<T, D>>(o, pv, p);
+      pv = vt + rcol + n * 32 * F::V::kStride;
       float part = 0.f;
 #pragma unroll
       for (int r = 0; r < 16; ++r) {
@@ -669,7 +674,7 @@ __global__ __launch_bounds__(64 * NW, D * (int)sizeof(T) > 256 ? 1 : D * (int)si
     }
   }
   for (; t < tw; ++t) tile(t, std::integral_constant<int, 0>());
-  mul_transposed<D, 1>(o, pv, p);
+  mul_transposed<D, 1, kTransposed<T, D>>(o, pv, p);
   for (; t < t1; ++t) {                                               // those of the block's other waves
     if (t > t0) __syncthreads();
     const int buf1 = buf == 2 ? 0 : buf + 1, buf2 = buf1 == 2 ? 0 : buf1 + 1;
@@ -702,12 +707,12 @@ __global__ __launch_bounds__(64 * NW, D * (int)sizeof(T) > 256 ? 1 : D * (int)si
 // waves take every fourth tile of 32 keys each, in LDS of their own, with a maximum, a sum and an o of their own, and join them
 // at the end.  For single tokens, and for prompts that are too short to fill the device with a workgroup per 128 rows.
 template <class T, int D, Keys KEYS> struct FewTile {
-  using R = Rows<T, D>;
-  static constexpr int kTile = 32 * R::kStride;
-  static constexpr int kWave = 2 * kTile + (KEYS == kCache8 ? 64 * 4 : 0);   // keys, values, scales
-  static constexpr int kOut = (D + 4) * 4;                                    // a row of o on its way to the join
-  static constexpr int kLds = 4 * kWave;
-  static_assert(32 * kOut + 64 * 4 <= kWave, "the join fits");
+  using K = Rows<T, D, kByRows>;
+  using V = Rows<T, D, kTransposed<T, D>>;
+  static constexpr int kKeys = 32 * K::kStride, kTiles = kKeys + 32 * V::kStride;
+  static constexpr int kOut = (D + 4) * 4, kJoin = 32 * kOut + 64 * 4;        // a row of o on its way to the join; all, and m, l
+  static constexpr int kUsed = kTiles + (KEYS == kCache8 ? 64 * 4 : 0);       // keys, values, scales
+  static constexpr int kWave = kUsed > kJoin ? kUsed : kJoin, kLds = 4 * kWave;
 };
 
 template <class T, int D, Keys KEYS>
@@ -757,8 +762,8 @@ __global__ __launch_bounds__(256, D * (int)sizeof(T) > 256 ? 1 : 2) void few_ker
                                               (2 * k + h) * 16);
   }
   char* const kt = lds + w * F::kWave;
-  char* const vt = kt + F::kTile;
-  float* const scales = reinterpret_cast<float*>(kt + 2 * F::kTile);
+  char* const vt = kt + F::kKeys;
+  float* const scales = reinterpret_cast<float*>(kt + F::kTiles);
   KeyTile<T, D, 64, 32, KEYS> nk, nv;
   Pages<32> coming;
   if constexpr (KEYS != kPrompt) coming.ask(a, table, t0 + w, t1, keys);
@@ -780,11 +785,11 @@ __global__ __launch_bounds__(256, D * (int)sizeof(T) > 256 ? 1 : 2) void few_ker
   for (int d = 0; d < D / 32; ++d) o[d] = zero16();
   float m = -kInf, sum = 0.f;
   const float c = a.scale * kLog2e;
-  const int rrow = R::by_rows(l), rcol = R::transposed(l);
+  const int rrow = F::K::by_rows(l), rcol = F::V::transposed(l);
   const int i = tq < s.n ? past + tq : -1;                             // this lane's position
   for (int t = t0 + w; t < t1; t += 4) {
-    nk.store(kt, scales, l);
-    nv.store(vt, scales + 32, l);
+    nk.template store<F::K::kStride>(kt, scales, l);
+    nv.template store<F::V::kStride>(vt, scales + 32, l);
     __builtin_amdgcn_wave_barrier();
     if (t + 4 < t1) load(t + 4);
     f32x16 x = zero16();
@@ -829,7 +834,7 @@ __global__ __launch_bounds__(256, D * (int)sizeof(T) > 256 ? 1 : 2) void few_ker
     }
     Operand<T, PARTS> p;
     p.set(x);
-    mul_transposed<D, PARTS>(o, vt + rcol, p);
+    mul_transposed<D, PARTS, kTransposed<T, D>>(o, vt + rcol, p);
     __builtin_amdgcn_wave_barrier();
   }
 

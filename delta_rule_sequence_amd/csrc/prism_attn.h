@@ -7,6 +7,16 @@
 // so that m, l and the rescaling of o are single registers, and the tile's accumulators are, rounded, the second
 // operand of O^T = V^T P^T without leaving their lane.  Q stays in registers; tiles of K and V go through LDS, read by
 // rows (K) and transposed on the way (V).
+//
+// Rounding: q, k, v are exact operands; p passes as one bfloat16 part in the kernel of many rows, off by 2^-8 of a term at most:
+// o is then off by 0.0021 of its size where a float32 p would leave 0.0016, its own rounding.  Two parts (0.0017) take a second
+// product with V: 1 x 16 x 16384 of 128 1.50 ms for 1.09, 2 x 16 x 8192 of 64 534 us for 379, 4 x 16 x 4096 of 128 430 for 315.  The
+// kernel of few rows waits for bytes and passes two.
+//
+// Bounds, bfloat16: heads of 128 run at 0.89 of a large matrix product's rate (1 x 16 x 16384 causal, 1030 us: 1068 of 1200 TFLOP/s), the
+// matrix cores busy for 42 % of the cycles at 2.4 GHz (that product's: 48).  Heads of 64 (868 TFLOP/s at 2 x 16 x 8192) spend as many cycles on a tile's 62 to 90
+// vector instructions, 16 exponentials among them, as on its 8 matrix instructions, and the two overlap in part only.  64 queries to a wave (355
+// for 900 TFLOP/s at 128: registers), wave priorities and a fixed interleaving of the two kinds gained nothing or lost 5 to 10 %.
 #pragma once
 #include <climits>
 #include <type_traits>
@@ -230,7 +240,8 @@ __device__ __forceinline__ Seq find_tile(const AttnArgs& a, unsigned unit, int r
 enum Keys { kPrompt, kCache, kCache8 };
 
 // NW waves of 32 queries; keys in tiles of BN, three of K and three of V in LDS.  Step t computes on tile t, stores
-// tile t + 2 of K and t + 1 of V, and asks for the ones behind them.
+// tile t + 2 of K and t + 1 of V, and asks for the ones behind them.  (A spacing of 32 bytes for both kinds, two-way for either read,
+// takes 1 to 4 % longer: 1 x 16 x 16384 of 128 1053 us for 1030.)
 template <class T, int D, int NW, int BN, Keys KEYS>
 struct FwdTile {
   using K = Rows<T, D, kByRows>;
@@ -706,6 +717,7 @@ __global__ __launch_bounds__(64 * NW, D * (int)sizeof(T) > 256 ? 1 : D * (int)si
 // The rows of a group's heads, token by token, lie in tiles of 32 rows, so that keys are read once for all of them.  Four
 // waves take every fourth tile of 32 keys each, in LDS of their own, with a maximum, a sum and an o of their own, and join them
 // at the end.  For single tokens, and for prompts that are too short to fill the device with a workgroup per 128 rows.
+// Single tokens are bound by the cache's bytes (5.17 of the copy's 5.19 TB/s over 800 MB); a workgroup keeps 4 x 16 KB of loads in flight.
 template <class T, int D, Keys KEYS> struct FewTile {
   using K = Rows<T, D, kByRows>;
   using V = Rows<T, D, kTransposed<T, D>>;
@@ -889,7 +901,8 @@ __global__ __launch_bounds__(256, D * (int)sizeof(T) > 256 ? 1 : 2) void few_ker
 }
 
 // Joins the shares of the rows, at most 64 of each: a wave per row, whose lanes weigh a share each and then take D / 4 columns of
-// every (256 / D)-th share.
+// every (256 / D)-th share.  (Thread per four columns that walks the shares: 83 us for the two kernels where these take 39, 13 single
+// tokens over 11610 in 22 shares.)
 template <class T, int D>
 __global__ __launch_bounds__(256) void join_kernel(AttnArgs a) {
   constexpr int L = D / 4, N = 64 / L;

@@ -6,7 +6,8 @@
 //   backward: g = the rotation by -angle of dy;  with u = g w, xhat = x r:  dx = r (u - xhat mean(u xhat)),  dw = sum g xhat
 //
 // Bound by its bytes: a row is read once, by a group of lanes that holds V pairs (or 2 V of the other channels) each,
-// and a lane group takes several heads of one token, whose sines and cosines it forms once.
+// and a lane group takes several heads of one token, whose sines and cosines it forms once, four rows in flight.  The forward runs at 0.72
+// of a copy's rate (18 us for 13), the backward, which reads x and dy, at 0.7 without the weights' sum of 4 to 6 us.
 #pragma once
 #include "prism_attn_args.h"
 #include "prism_tile.h"

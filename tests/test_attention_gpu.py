@@ -334,6 +334,80 @@ def test_long_sequence(prism):
                    f64(lse[0, 1, t:t + 1]), past=t)
 
 
+# Enough rows for the workgroups of 128 and 256: each type and width on both sides of their borders.
+MANY = [("bf16", 4, 16, 8, 515, 64, 0), ("bf16", 2, 64, 32, 2050, 64, 0), ("bf16", 3, 24, 12, 400, 32, 70), ("bf16", 2, 32, 16, 450, 128, 0),
+        ("bf16", 8, 32, 16, 500, 128, 130), ("f32", 8, 24, 12, 333, 32, 0), ("f32", 8, 24, 12, 333, 64, 50), ("f32", 4, 24, 12, 300, 128, 0)]
+
+
+@pytest.mark.parametrize("case", MANY, ids=lambda c: "_".join(map(str, c)))
+def test_many_rows(prism, case):
+    """A padded batch whose padding holds NaN: the first and the last sequence's first and last group."""
+    import torch
+    dt, B, H, G, T, D, window = case
+    r = Rng(23, dt)
+    q, k, v = r.heads(B, T, H, G, G, D=D)
+    do = r.vec(B, H, T, D)
+    lens = [T] + [int(n) for n in r.r.integers(1, T, B - 2)] + [T - 67]
+    for b, n in enumerate(lens):
+        for t in (q, k, v, do):
+            t[b, :, n:] = float("nan")
+    out = (torch.full((B, H, T, D), 7.0, dtype=torch_dtype(dt), device="cuda"), torch.full((B, H, T), 7.0, device="cuda"))
+    o, lse = prism.attn_fwd(q, k, v, lens=i32(lens), window=window, out=out)
+    grads = prism.attn_bwd(q, k, v, o, lse, do, lens=i32(lens), window=window)
+    for b in (0, B - 1):
+        n = lens[b]
+        for g in (0, G - 1):
+            at = slice(2 * g, 2 * g + 2)                               # H = 2 G
+            check_prompt(dt, q[b:b + 1, at], k[b:b + 1, g:g + 1], v[b:b + 1, g:g + 1], o[b:b + 1, at], lse[b:b + 1, at], [(0, 0, n)],
+                         D ** -0.5, window=window, do=do[b:b + 1, at],
+                         grads={"dq": grads["dq"][b:b + 1, at], "dk": grads["dk"][b:b + 1, g:g + 1], "dv": grads["dv"][b:b + 1, g:g + 1]})
+    for b, n in enumerate(lens):
+        assert (o[b, :, n:] == 7).all() and (lse[b, :, n:] == 7).all()
+        assert all((grads[x][b, :, n:] == 0).all() for x in grads) and all(torch.isfinite(t[b, :, :n]).all() for t in grads.values())
+    again = prism.attn_fwd(q, k, v, lens=i32(lens), window=window)
+    assert all(torch.equal(again[0][b, :, :n], o[b, :, :n]) for b, n in enumerate(lens))
+
+
+@pytest.mark.parametrize("case", [MANY[0], MANY[2], MANY[4], MANY[6]], ids=lambda c: "_".join(map(str, c)))
+def test_many_rows_that_do_not_see_a_key(prism, case):
+    """Keys and values that are not finite reach the rows behind them and no others."""
+    import torch
+    dt, B, H, G, T, D, window = case
+    r = Rng(24, dt)
+    q, k, v = r.heads(B, T, H, G, G, D=D)
+    at = 301
+    k[0, 0, at] = float("nan")
+    v[B - 1, G - 1, at] = float("inf")
+    o, lse = prism.attn_fwd(q, k, v, window=window)
+    last = min(T, at + window) if window else T
+    for b, g in ((0, 0), (B - 1, G - 1)):
+        h = slice(2 * g, 2 * g + 2)
+        check_prompt(dt, q[b:b + 1, h, :at], k[b:b + 1, g:g + 1, :at], v[b:b + 1, g:g + 1, :at], o[b:b + 1, h, :at], lse[b:b + 1, h, :at],
+                     [(0, 0, at)], D ** -0.5, window=window)
+        assert not torch.isfinite(o[b, h, at:last]).any() and torch.isfinite(o[b, h, last:]).all()
+    assert torch.isfinite(o[1, 1:]).all() and torch.isfinite(o[0, 2:]).all()
+
+
+@pytest.mark.parametrize("dt,D", [("bf16", 64), ("bf16", 128), ("f32", 32)])
+def test_many_rows_packed(prism, dt, D):
+    import torch
+    r = Rng(25, dt)
+    H, G, lens = 48, 24, (700, 0, 1, 33, 1200)
+    starts = np.cumsum((11,) + lens)
+    T = int(starts[-1]) + 45
+    q, k, v = r.heads(1, T, H, G, G, D=D)
+    do = r.vec(1, H, T, D)
+    out = (torch.full((1, H, T, D), 7.0, dtype=torch_dtype(dt), device="cuda"), torch.full((1, H, T), 7.0, device="cuda"))
+    o, lse = prism.attn_fwd(q, k, v, starts=i32(starts), out=out)
+    grads = prism.attn_bwd(q, k, v, o, lse, do, starts=i32(starts))
+    for g in (0, G - 1):
+        at = slice(2 * g, 2 * g + 2)
+        check_prompt(dt, q[:, at], k[:, g:g + 1], v[:, g:g + 1], o[:, at], lse[:, at], [(0, int(a), n) for a, n in zip(starts, lens)],
+                     D ** -0.5, do=do[:, at], grads={"dq": grads["dq"][:, at], "dk": grads["dk"][:, g:g + 1], "dv": grads["dv"][:, g:g + 1]})
+    for lo, hi in ((0, 11), (int(starts[-1]), T)):
+        assert (o[:, :, lo:hi] == 7).all() and (lse[:, :, lo:hi] == 7).all() and all((t[:, :, lo:hi] == 0).all() for t in grads.values())
+
+
 # ---- norm and rotation --------------------------------------------------------------------------
 ROPE = [("bf16", 2, 3, 1, 5, 64, 64, True), ("bf16", 1, 4, 2, 7, 128, 32, True), ("f32", 1, 2, 1, 9, 96, 24, True), ("f32", 3, 1, 1, 1, 32, 8, False),
         ("bf16", 1, 5, 3, 33, 256, 256, True), ("f32", 1, 2, 2, 3, 512, 500, True), ("bf16", 1, 1, 1, 4, 10, 6, True), ("f32", 2, 3, 2, 2, 2, 2, True),

@@ -10,10 +10,11 @@
 // Rounding: p and ds pass as one bfloat16 part each, as in the forward: gradients are off by 0.0024 of their size where float32
 // products would leave 0.0018.  The tiles' scores and their lse come from the same products as the forward's.
 //
-// Bounds, bfloat16: 8 x 12 x 2048 of 64, causal, 234 us (dq 100, dk and dv 134): matrix instructions are busy for 0.31 of the
-// cycles, vector instructions for about 0.4, the tiles' reads from LDS (rows and transposed, from one copy of the tile with two-way
-// conflicts) for the rest.  4 x 16 x 4096 of 128: 1080 us, 636 TFLOP/s of the five products that are needed, 890 of the
-// seven formed.  dk and dv in two kernels: 1195 to 1545 us there; the next tile's products ahead in dkv of 128: 1137.
+// Bounds, bfloat16: 8 x 12 x 2048 of 64, causal, 234 us (dq 95, dk and dv 135): the matrix cores are busy for 0.31 of the cycles at
+// 2.4 GHz, the vector instructions of the exponentials, of ds and of the two roundings for about as many, and the two overlap in part only;
+// reads from LDS are not what bounds it (a spacing without conflicts for dq's values: equal).  4 x 16 x 4096 of 128: 1077 us, 638 TFLOP/s
+// of the five products that are needed, 890 of the seven formed.  dk and dv in two kernels: 1195 to 1545 us there; the next
+// tile's products ahead in dkv of 128: 1137.
 #pragma once
 #include "prism_attn.h"
 

@@ -20,13 +20,13 @@ prism_status few(const AttnArgs& a, hipStream_t stream) {
   return launch_wide<attn::few_kernel<T, D, attn::kPrompt>>((unsigned)(row_tiles(a, 32, a.H / a.G) * a.G), 256, F::kLds, a, stream);
 }
 
-// Workgroups of 128 rows, or of 256 for wide heads of bfloat16 where there are many; else tiles of 32 rows whose keys four waves
-// share.  Measured at the sides of the borders, us, few rows / many rows: bfloat16 of 64: 1 x 16 x 2048 30 / 37, 1 x 32 x 2048
-// 50 / 40, 4 x 16 x 256 7.4 / 8.8, 4 x 16 x 512 14.7 / 13.1; float32 of 64: 1 x 32 x 2048 171 / 217, 8 x 12 x 2048 486 / 466,
-// 8 x 16 x 512 64 / 65, 32 x 16 x 256 86 / 74; of 128: 1 x 16 x 2048 192 / 303, 1 x 32 x 2048 379 / 337; 128 / 256 rows,
-// bfloat16 of 128: 2 x 32 x 2048 114 / 88, 1 x 32 x 2048 62 / 67; of 64, four waves per SIMD each: 1 x 16 x 8192 204 / 226, 1 x 16 x
-// 16384 658 / 615, 4 x 16 x 4096 178 / 172, 64 x 16 x 512 86 / 87 (128 rows with tiles of 64 keys, two waves per SIMD: 2 x 16 x 8192
-// 349, where these take 337 / 315).
+// Workgroups of 128 rows, or of 256 for bfloat16 heads of 64 and 128 where there are many; else tiles of 32 rows whose keys four waves
+// share.  Measured at the sides of the borders, us, on rotating inputs, few rows / many rows: bfloat16 of 64: 1 x 16 x 2048 36 / 47,
+// 1 x 32 x 2048 63 / 50, 4 x 16 x 256 13.5 / 12.6, 4 x 16 x 512 17.5 / 16.8; of 32: 1 x 16 x 2048 22 / 32, 1 x 32 x 2048 36 / 32; of 128:
+// 1 x 16 x 2048 50 / 51, 1 x 32 x 2048 86 / 60; float32 of 64: 1 x 32 x 2048 184 / 212, 8 x 12 x 2048 485 / 447, 8 x 16 x 512 65 / 63,
+// 32 x 16 x 256 87 / 71; of 128: 1 x 16 x 2048 195 / 294, 1 x 32 x 2048 384 / 327.  128 / 256 rows, bfloat16 of 128: 2 x 32 x 2048
+// 114 / 88, 1 x 32 x 2048 62 / 67; of 64, four waves per SIMD each: 1 x 16 x 8192 204 / 226, 1 x 16 x 16384 658 / 615, 4 x 16 x 4096
+// 178 / 172, 64 x 16 x 512 86 / 87 (128 rows with tiles of 64 keys, two waves per SIMD: 2 x 16 x 8192 349, where these take 337 / 315).
 template <class T, int D>
 prism_status run(const AttnArgs& a, hipStream_t s) {
   const size_t blocks = row_tiles(a, 128, 1) * a.H;

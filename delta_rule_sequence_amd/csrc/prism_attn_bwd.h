@@ -186,12 +186,27 @@ __global__ __launch_bounds__(64 * OW * SW, SW > 1 || D * (int)sizeof(T) > 256 ? 
     __syncthreads();
     products(xs[0], gs[0], sw * 32 * R::kStride);
   }
-  for (int t = t0; t < t1; ++t) {
+  const auto stage = [&](int t, int next) {
+    if (t > t0) __syncthreads();
+    if (t + 2 < t1) store(next + 1 == F::kTiles ? 0 : next + 1);
+    if (t + 3 < t1) load(t + 3);
+  };
+  int t = t0;
+  if constexpr (F::kAhead) {
+    // Tiles in front of all of the wave's windows stay out of its sums: a key that is not finite, times a p of 0, would enter
+    // rows of the workgroup's last waves, up to 318 tokens behind the last one that sees it.
+    const int own = a.window > 0 ? min(max(qw - a.window + 1, 0) / BN, t1) : t0;
+    for (; t < own; ++t) {
+      const int next = place + 1 == F::kTiles ? 0 : place + 1;
+      stage(t, next);
+      place = next;
+      if (t + 1 == own && own < t1) products(xs[0], gs[0], place * F::kTile + sw * 32 * R::kStride);
+    }
+  }
+  for (; t < t1; ++t) {
     int next = place + 1 == F::kTiles ? 0 : place + 1;
     if constexpr (F::kAhead) {
-      if (t > t0) __syncthreads();
-      if (t + 2 < t1) store(next + 1 == F::kTiles ? 0 : next + 1);
-      if (t + 3 < t1) load(t + 3);
+      stage(t, next);
     } else {
       store(place);
       __syncthreads();

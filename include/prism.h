@@ -604,8 +604,8 @@ prism_status prism_norm_bwd(const void* h, long long h_stride, const float* weig
  * fixed order.  With PRISM_BF16 the probabilities enter their product with the values as bfloat16, and in the
  * gradients so do they and the gradients of the scores: each output is off by its own rounding and about one more of its
  * terms.  (Where few rows leave time, as for single tokens over a cache, they enter as two bfloat16 parts, which keep 16 bits.)
- * Non-finite inputs: a query's reach its own row of o and lse, a key's or value's the rows that see it; in the
- * gradients they may also reach tokens within 256 of those.  Scores past 45000 in magnitude, and results that are
+ * Non-finite inputs: a query's reach its own row of o and lse, a key's or value's the rows that see it; in the gradients
+ * these rows and the keys that they see, and they may also reach tokens within 256 of all these.  Scores past 45000 in magnitude, and results that are
  * not finite, are formed again key by key, which takes longer. */
 
 /* Norm (optional) and rotation of queries and keys, in one pass:

@@ -1,4 +1,6 @@
 // attn_paged.hip - launches of the paged cache's write and of the attention over it (prism_paged.h, prism_attn.h)
+#include <algorithm>
+
 #include "prism_paged.h"
 
 namespace prism {
@@ -10,8 +12,13 @@ int row_tiles(const AttnArgs& a, int rows) { return a.starts != nullptr ? a.T / 
 
 template <class T, int D, bool BITS8>
 prism_status write(const AttnArgs& a, hipStream_t s) {
-  attn::cache_write_kernel<T, D, BITS8><<<dim3(row_tiles(a, attn::kWriteTokens)), 256, 0, s>>>(a);
-  return launched();
+  // at most 2^24 tiles, 2^23 of them to a launch
+  const unsigned tiles = row_tiles(a, attn::kWriteTokens), most = 1u << 23;
+  for (unsigned first = 0; first < tiles; first += most) {
+    attn::cache_write_kernel<T, D, BITS8><<<dim3(std::min(tiles - first, most)), 256, 0, s>>>(a, first);
+    if (launched() != PRISM_OK) return PRISM_ERR_HIP;
+  }
+  return PRISM_OK;
 }
 
 template <class T, int D, attn::Keys KEYS>

@@ -16,12 +16,12 @@ namespace attn {
 constexpr int kWriteTokens = 16;
 
 template <class T, int D, bool BITS8>
-__global__ __launch_bounds__(256) void cache_write_kernel(AttnArgs a) {
+__global__ __launch_bounds__(256) void cache_write_kernel(AttnArgs a, unsigned first_tile) {
   const int G = a.G;
   constexpr int V = 16 / (int)sizeof(T), L = D / V;
   typedef T vec __attribute__((ext_vector_type(V)));
   a.G = 1;                                                            // tiles of all groups at once
-  const Seq s = find_tile(a, blockIdx.x, kWriteTokens, 1, false);
+  const Seq s = find_tile(a, first_tile + blockIdx.x, kWriteTokens, 1, false);
   if (s.id < 0) return;
   const int t0 = s.tile * kWriteTokens, n = min(kWriteTokens, s.n - t0), at = threadIdx.x % L;
   const long long past = max(a.past[s.id], 0);

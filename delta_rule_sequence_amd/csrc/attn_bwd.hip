@@ -35,7 +35,8 @@ template <class T, int D>
 prism_status run(const AttnArgs& a, hipStream_t s) {
   const bool f32 = sizeof(T) == 4, long_rows = a.T >= 1024;
   const size_t small_most = f32 ? (D == 128 ? 512 : long_rows ? 256 : 160) : D == 32 ? (long_rows ? 384 : 192) : long_rows ? 128 : 96;
-  const bool small = (size_t)row_tiles(a, 128) * a.H <= small_most;
+  const size_t blocks = (size_t)row_tiles(a, 128) * a.H;
+  const bool small = blocks <= small_most || (!f32 && blocks > kMostThreads / 512);   // or more than a launch of eight waves each holds
   prism_status st;
   if constexpr (sizeof(T) == 4) {
     constexpr int SW = D == 128 ? 2 : 4;                              // 128 rows of 128 float32 twice do not fit

@@ -33,9 +33,11 @@ prism_status run(const AttnArgs& a, hipStream_t s) {
   const bool f32 = sizeof(T) == 4;
   const size_t few_most = f32 && D < 128 ? (a.T >= 1024 ? 1024 : 512) : a.T >= (f32 ? 512 : 1024) ? 320 : 192;
   if (blocks <= few_most) return few<T, D>(a, s);
+  // 2^23 tiles of 32 rows, the most there are, may be as many of 256: a launch too large for eight waves each
+  const bool eight_fit = row_tiles(a, 256, 1) * a.H <= kMostThreads / 512;
   if constexpr (sizeof(T) == 4) return many<T, D, 4, (D > 32 ? 32 : 64)>(a, s);
-  else if constexpr (D == 128) return blocks >= 1024 ? many<T, D, 8, 64>(a, s) : many<T, D, 4, 64>(a, s);
-  else if constexpr (D == 64) return blocks >= 2048 && a.T >= 2048 ? many<T, D, 8, 64>(a, s) : many<T, D, 4, 32>(a, s);
+  else if constexpr (D == 128) return blocks >= 1024 && eight_fit ? many<T, D, 8, 64>(a, s) : many<T, D, 4, 64>(a, s);
+  else if constexpr (D == 64) return blocks >= 2048 && a.T >= 2048 && eight_fit ? many<T, D, 8, 64>(a, s) : many<T, D, 4, 32>(a, s);
   else return many<T, D, 4, 64>(a, s);
 }
 

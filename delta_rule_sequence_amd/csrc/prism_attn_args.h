@@ -50,6 +50,9 @@ struct RopeArgs {
 };
 
 namespace host {
+// A launch holds less than 2^32 threads.
+constexpr size_t kMostThreads = ((size_t)1 << 32) - 1;
+
 // A launch with `lds` bytes of dynamic LDS, which may be more than a kernel has by default: each device is told once.
 template <auto KERNEL>
 prism_status launch_wide(unsigned blocks, unsigned threads, int lds, const AttnArgs& a, hipStream_t stream) {

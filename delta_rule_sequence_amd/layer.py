@@ -71,8 +71,8 @@ def _tensor(name, t, shape, dtype, dev):
 
 def _sizes(*n):
     """Sizes as the C interface holds them (ctypes would cut them off)."""
-    if max(n) > 0x7fffffff:
-        raise PrismError(f"a size of {max(n)} is more than 2^31 - 1")
+    if max(n) > 0x7fffffff or min(n) < -0x80000000:
+        raise PrismError(f"a size of {max(n, key=abs)} is beyond 2^31 - 1")
 
 
 def _dense(name, t, shape, dtype, dev):

@@ -74,3 +74,31 @@ def test_rows_that_do_not_see_a_row_of_the_cache(prism, case, room):  # noqa: F8
                 check_head(f"[{s},{h}] from {run[0]}", dt, qh[run], kz, vz, scale, oh[run], window=window, past=past[s] + int(run[0]),
                            extra=4 * U if bits8 else 0.0)
     assert finite > 0 and torch.isfinite(o[2, heads - 1, :5]).all()
+
+
+@pytest.mark.parametrize("bits8", [False, True])
+def test_pages_beyond_32_bit_offsets(prism, bits8):  # noqa: F811
+    """Pages on both sides of 2^32 values of a cache hold what they hold in a small one, and are read alike."""
+    import torch
+    G, page, D, n, pages = 8, 64, 128, 450, 70000                      # 2^16 values to a page
+    r = Rng(84, "bf16")
+    k, v = r.heads(1, n, G, G, D=D)
+    ids = [pages - 1, 3, 65535, 65536, 40000, 32768, 16383, pages - 2]
+    near, far = i32([list(range(8))]), i32([ids])
+
+    def caches(count):
+        c = [torch.empty(count, G, page, D, dtype=torch.float8_e4m3fn if bits8 else torch.bfloat16, device="cuda") for _ in range(2)]
+        return c, [torch.empty(count, G, page, device="cuda") for _ in range(2)] if bits8 else None
+
+    (a, sa), (b, sb) = caches(8), caches(pages)
+    prism.cache_write(*a, k, v, near, i32([0]), scales=sa)
+    prism.cache_write(*b, k, v, far, i32([0]), scales=sb)
+    for x, y in zip(a + (sa or []), b + (sb or [])):
+        x, y = (t.view(torch.uint8) if t.dtype.itemsize == 1 else t for t in (x, y))
+        for i, j in enumerate(ids):
+            rows = min(page, max(0, n - i * page))
+            assert torch.equal(x[i, :, :rows], y[j, :, :rows])
+    for T, heads in ((1, 16), (40, 8), (200, 16), (300, 8)):           # one tile of rows, several, workgroups of 128 and of 256
+        q = r.vec(1, heads, T, D)
+        got = [prism.attn_paged(q, *c, t, i32([n - T]), scales=s) for c, t, s in ((a, near, sa), (b, far, sb))]
+        assert bool(torch.isfinite(got[0]).all()) and torch.equal(*got)

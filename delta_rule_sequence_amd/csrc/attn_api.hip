@@ -66,10 +66,12 @@ prism_status cache_check(int G, int D, int pages, int page, int max_pages, int T
 
 // How new tokens read the cache.  Few rows of a group's heads: tiles of 32 rows that share the cache's keys; else 128 rows of a head to a
 // workgroup, 256 of wide heads.  A sequence's keys are split until the device is full, into ranges of 512 keys or more (128 where
-// that leaves CUs without any).  Measured, us: 256 rows (8 x 16 heads x 32 tokens over 4096 of 128) 46 as few, 75 as many, 512 rows
-// (2 x 16 x 128 over 8192) 39 as many with one workgroup per CU, 48 with two (of 64 wide heads two fit a CU: 512 tokens 63
-// with two, 83 with one); 1 x 32 x 512 tokens over 4096: 88 with 128 rows, 62 with 256; single tokens of 13 x 2 over 11610: 38
-// with ranges of 512, 40 of 256; 4 x 8 over 500: 13.5 and 11.2 with 128.
+// that leaves CUs without any) of the max_pages * page keys that its table has room for: the host does not know how many a sequence
+// holds, nor is the window reckoned with, and a kernel deals out what a sequence has to all the ranges evenly.
+// Measured, us: 256 rows (8 x 16 heads x 32 tokens over 4096 of 128) 46 as few, 75 as many, 512 rows (2 x 16 x 128 over 8192) 39 as many
+// with one workgroup per CU, 48 with two (of 64 wide heads two fit a CU: 512 tokens 63 with two, 83 with one); 1 x 32 x 512 tokens over
+// 4096: 88 with 128 rows, 62 with 256; single tokens of 13 x 2 over 11610: 38 with ranges of 512, 40 of 256; 4 x 8 over 500: 13.5 and
+// 11.2 with 128.
 struct PagedPlan {
   int rows, splits;               // rows of a tile: 32 (few), 128 or 256
   size_t total;

@@ -21,7 +21,8 @@ prism_status few(const AttnArgs& a, hipStream_t stream) {
 }
 
 // Workgroups of 128 rows, or of 256 for bfloat16 heads of 64 and 128 where there are many; else tiles of 32 rows whose keys four waves
-// share.  Measured at the sides of the borders, us, on rotating inputs, few rows / many rows: bfloat16 of 64: 1 x 16 x 2048 36 / 47,
+// share.  Packed batches go by the tiles that all their tokens and sequences may take, whatever each holds: 1000 sequences of 16 tokens, 32 heads
+// of 64, take 553 us in workgroups with one live wave of four or eight.  Measured at the sides of the borders, us, on rotating inputs, one length for all sequences, few rows / many rows: bfloat16 of 64: 1 x 16 x 2048 36 / 47,
 // 1 x 32 x 2048 63 / 50, 4 x 16 x 256 13.5 / 12.6, 4 x 16 x 512 17.5 / 16.8; of 32: 1 x 16 x 2048 22 / 32, 1 x 32 x 2048 36 / 32; of 128:
 // 1 x 16 x 2048 50 / 51, 1 x 32 x 2048 86 / 60; float32 of 64: 1 x 32 x 2048 184 / 212, 8 x 12 x 2048 485 / 447, 8 x 16 x 512 65 / 63,
 // 32 x 16 x 256 87 / 71; of 128: 1 x 16 x 2048 195 / 294, 1 x 32 x 2048 384 / 327.  128 / 256 rows, bfloat16 of 128: 2 x 32 x 2048

@@ -10,11 +10,11 @@
 //
 // Rounding: q, k, v are exact operands; p passes as one bfloat16 part in the kernel of many rows, off by 2^-8 of a term at most:
 // o is then off by 0.0021 of its size where a float32 p would leave 0.0016, its own rounding.  Two parts (0.0017) take a second
-// product with V: 1 x 16 x 16384 of 128 1.50 ms for 1.09, 2 x 16 x 8192 of 64 534 us for 379, 4 x 16 x 4096 of 128 430 for 315.  The
-// kernel of few rows waits for bytes and passes two.
+// product with V: 1 x 16 x 16384 of 128 1.46 ms for 1.06, 2 x 16 x 8192 of 64 509 us for 320 (15 registers go to scratch), 4 x 16 x 4096
+// of 128 399 for 294.  The kernel of few rows waits for bytes and passes two.
 //
-// Bounds, bfloat16: heads of 128 run at 0.89 of a large matrix product's rate (1 x 16 x 16384 causal, 1030 us: 1068 of 1200 TFLOP/s), the
-// matrix cores busy for 42 % of the cycles at 2.4 GHz (that product's: 48).  Heads of 64 (868 TFLOP/s at 2 x 16 x 8192) spend as many cycles on a tile's 62 to 90
+// Bounds, bfloat16: heads of 128 run at 0.87 of a large matrix product's rate (1 x 16 x 16384 causal, 1050 us: 1047 of 1200 TFLOP/s), the
+// matrix cores busy for 42 % of the cycles at 2.4 GHz (that product's: 48).  Heads of 64 (860 TFLOP/s at 2 x 16 x 8192) spend as many cycles on a tile's 62 to 90
 // vector instructions, 16 exponentials among them, as on its 8 matrix instructions, and the two overlap in part only.  64 queries to a wave (355
 // for 900 TFLOP/s at 128: registers), wave priorities and a fixed interleaving of the two kinds gained nothing or lost 5 to 10 %.
 #pragma once
@@ -66,7 +66,6 @@ template <class T, int D> constexpr int kTransposed = sizeof(T) == 4 ? 32 : D ==
 template <class T, int D, int PAD = kBoth> struct Rows {
   static constexpr int kBytes = D * (int)sizeof(T), kStride = kBytes + PAD;
   static constexpr int kPieces = kBytes / 16, kSteps = kPieces / 2;
-  static constexpr int kPer = 16 / (int)sizeof(T);   // values of a piece
   // This lane's place in a tile of 32 rows, read by rows or transposed.
   static __device__ __forceinline__ int by_rows(int l) { return (l & 31) * kStride + (l >> 5) * 16; }
   static __device__ __forceinline__ int transposed(int l) {
@@ -241,7 +240,7 @@ enum Keys { kPrompt, kCache, kCache8 };
 
 // NW waves of 32 queries; keys in tiles of BN, three of K and three of V in LDS.  Step t computes on tile t, stores
 // tile t + 2 of K and t + 1 of V, and asks for the ones behind them.  (A spacing of 32 bytes for both kinds, two-way for either read,
-// takes 1 to 4 % longer: 1 x 16 x 16384 of 128 1053 us for 1030.)
+// took 1 to 4 % longer: 1 x 16 x 16384 of 128 2 %.)
 template <class T, int D, int NW, int BN, Keys KEYS>
 struct FwdTile {
   using K = Rows<T, D, kByRows>;

@@ -11,8 +11,9 @@ namespace attn {
 
 // ---- write ----------------------------------------------------------------------------------------------
 // A workgroup takes kWriteTokens tokens of a sequence, all groups, keys and values; a row lies in D / 8 or D / 4 lanes, and 8 rows are
-// in flight.  Bound by its bytes and, with 8 bits, the latency of the row maximum's exchange: 16 us where a copy of the bytes of
-// 8 x 2048 tokens of 4 groups of 128 takes 7.4; a token's step is a launch (3.4 us).
+// in flight.  With 8 bits bound by instructions (1100 vector instructions per wave, addresses and the divisions by the group count
+// among them: 7 us of issue) and the latency of the row maximum's exchange: 16 us where a copy of the bytes of 8 x 2048 tokens of
+// 4 groups of 128 takes 7.4; a token's step is a launch (3.4 us).
 constexpr int kWriteTokens = 16;
 
 template <class T, int D, bool BITS8>

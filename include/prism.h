@@ -605,8 +605,8 @@ prism_status prism_norm_bwd(const void* h, long long h_stride, const float* weig
  * gradients so do they and the gradients of the scores: each output is off by its own rounding and about one more of its
  * terms.  (Where few rows leave time, as for single tokens over a cache, they enter as two bfloat16 parts, which keep 16 bits.)
  * Non-finite inputs: a query's reach its own row of o and lse, a key's or value's the rows that see it; in the gradients
- * these rows and the keys that they see, and they may also reach tokens within 256 of all these.  Scores past 45000 in magnitude, and results that are
- * not finite, are formed again key by key, which takes longer. */
+ * these rows and the keys that they see, and they may also reach tokens within 256 of all these.  Scores past 45000 in
+ * magnitude, and results that are not finite, are formed again key by key, which takes longer. */
 
 /* Norm (optional) and rotation of queries and keys, in one pass:
  *   h = w x / sqrt(mean(x^2) + eps) over a head's D channels where wq and wk [D] float32 are given (both or neither); else h = x
@@ -663,9 +663,10 @@ prism_status prism_attn_bwd(const void* q, const prism_strides* q_strides, const
  * positions of the sequence in front of this call's tokens (S = B without starts).  max_pages * page + T < 2^31 - 8192.
  *
  * prism_cache_write writes rows k, v [B, G, T, D] (strided): token t of sequence s at position past[s] + t.  With 8 bits
- * scale = (the largest |x| of the row) / 448, or 1 and bytes of 0 where all are below 2^-100; a row with a non-finite
- * value has a scale of infinity or NaN and bytes of NaN.  Positions past max_pages * page and pages outside
- * 0 .. pages - 1 are not written; two positions that share a row leave either's. */
+ * scale = (the largest |x| of the row) / 448, or 1 and zeros of x's signs where all are below 2^-100; a row with a
+ * non-finite value has a scale of infinity or NaN and bytes of NaN.  Positions past max_pages * page and pages outside
+ * 0 .. pages - 1 are not written.  A row that a call writes for two tokens (a page that its tables hold twice) may hold
+ * parts of both. */
 prism_status prism_cache_write(const void* k, const prism_strides* k_strides, const void* v, const prism_strides* v_strides,
                                const int* table, const int* past, const int* lens, const int* starts, int S,
                                int B, int G, int T, int D, int pages, int page, int max_pages, prism_dtype dt,
